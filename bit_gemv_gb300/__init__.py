@@ -3,8 +3,8 @@ projection). Argument marshalling only: every step of the computation runs in
 the library's CUDA kernels or its host C++ code. There is no fallback: if the
 shared library is missing, importing this package raises ImportError.
 
-Names match the C entry points of include/ninfer_ternary.h. Host entry points
-take and return numpy arrays; device entry points take torch CUDA tensors and
+Names match the C entry points of include/ninfer_ternary.h and
+include/ninfer_decode.h. Host entry points take and return numpy arrays; device entry points take torch CUDA tensors and
 run on the current torch CUDA stream.
 """
 from __future__ import annotations
@@ -26,7 +26,9 @@ _lib = C.CDLL(LIBRARY_PATH)
 PQ2_0_G128 = 142
 PTQ1_0_G128 = 143
 FORMATS = {"PQ2_0_G128": PQ2_0_G128, "PTQ1_0_G128": PTQ1_0_G128}
-F32, BF16, F16 = 0, 1, 2
+F32, BF16, F16, E4M3 = 0, 1, 2, 3
+# bits of the status words of the decode-step operators
+KV_OUT_OF_PAGES, KV_ROW_TOO_SHORT, KV_OUT_OF_SLOTS, KV_BAD_LENGTH, KV_BAD_SLOT, LOGITS_BAD_TOKEN = 1, 2, 4, 8, 16, 32
 
 GEOMETRY_FIELDS = ("n", "k", "k_pad", "groups_per_row", "base_bytes_per_group",
                    "high_bytes_per_group", "base_row_bytes", "high_row_bytes",
@@ -37,6 +39,21 @@ RowSplitGeometry = namedtuple("RowSplitGeometry", GEOMETRY_FIELDS)
 
 class _Geom(C.Structure):
     _fields_ = [(f, C.c_uint64) for f in GEOMETRY_FIELDS]
+
+
+class _KvCacheStruct(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("pages", C.c_uint64), ("page_size", C.c_uint64),
+                ("kv_heads", C.c_uint64), ("head_dim", C.c_uint64), ("page_stride", C.c_uint64),
+                ("token_stride", C.c_uint64), ("head_stride", C.c_uint64), ("k_scale", C.c_float),
+                ("v_scale", C.c_float), ("dtype", C.c_int), ("reserved", C.c_int)]
+
+
+class _LogitsControls(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("history_lengths", C.c_void_p), ("prompt_lengths", C.c_void_p),
+                ("history_stride", C.c_uint64), ("repetition", C.c_void_p), ("presence", C.c_void_p),
+                ("frequency", C.c_void_p), ("bias_offsets", C.c_void_p), ("bias_ids", C.c_void_p),
+                ("bias_values", C.c_void_p), ("bias_count", C.c_uint64), ("mask", C.c_void_p),
+                ("mask_rows", C.c_void_p), ("mask_row_count", C.c_uint64), ("mask_stride", C.c_uint64)]
 
 
 class NinferError(RuntimeError):
@@ -71,6 +88,13 @@ _sig = {
     "ninfer_ternary_gate_up_workspace": (_int, [_int, _u64, _u64, _u64, _int, _int, C.POINTER(_u64)]),
     "ninfer_ternary_gate_up": (_int, [_int, _vp, _vp, _u64, _u64, _u64, _vp, _int, _vp, _vp, _vp, _int, _u64, _vp,
                                       _u64, _vp]),
+    "ninfer_kv_tables": (_int, [_vp, _vp, _u64, _u64, _vp, _u64, _vp, _u64, _u64, _vp, _vp, _vp, _u64, _vp, _vp, _vp,
+                                _vp, _vp]),
+    "ninfer_kv_append": (_int, [_vp, _vp, _int, _u64, _u64, _u64, _u64, _u64, _vp, C.POINTER(_KvCacheStruct), _vp, _vp]),
+    "ninfer_kv_attention_workspace": (_int, [C.POINTER(_KvCacheStruct), _u64, _u64, C.POINTER(_u64)]),
+    "ninfer_kv_attention": (_int, [_vp, _int, _u64, _u64, _u64, _u64, C.POINTER(_KvCacheStruct), _vp, _u64, _u64, _vp,
+                                   C.c_float, _u64, _vp, _int, _vp, _vp, _u64, _vp]),
+    "ninfer_logits_process": (_int, [_vp, _u64, _vp, _u64, _int, _u64, _u64, C.POINTER(_LogitsControls), _vp, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024
 for _name, (_res, _args) in _sig.items():
@@ -311,4 +335,193 @@ def ninfer_ternary_embed(fmt, payload, n: int, k: int, ids, signs=None, out=None
         _fmt(fmt), _dev(payload, "payload"), payload.numel(), n, k, _dev(ids, "ids"), count,
         _dev(signs, "signs") if signs is not None else None, _dev(out, "out"), _dt(out.dtype),
         _dev(status, "status") if status is not None else None, _stream(ids)))
+    return out
+
+
+# ------------------------------------------------------------ decode step ---
+_TYPES: dict = {}       # torch dtype -> library dtype, filled on first use (torch is imported lazily)
+
+
+def _types():
+    if not _TYPES:
+        torch = _torch()
+        _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3})
+    return _TYPES
+
+
+def _raw_stream(t) -> int:
+    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
+
+
+def _arg(t, name, dtype, shape=None):
+    """Address of a contiguous CUDA tensor of one dtype (and shape); None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dims, dtypes):
+    """Checks a CUDA tensor whose last dimension is contiguous and whose other
+    strides are free; returns its library dtype."""
+    code = _types().get(t.dtype, -1)
+    if not t.is_cuda or t.dim() != dims or code not in dtypes or (t.stride(-1) != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions, the last one contiguous, of a supported dtype")
+    return code
+
+
+class KvCache:
+    """A paged key/value cache over two pools indexed [page][token][head][element]
+    (any strides, the last dimension contiguous; bfloat16, float16 or
+    float8_e4m3fn). A stored value stands for itself times k_scale (v_scale)."""
+
+    def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+        code = _rows(k, "k", 4, (BF16, F16, E4M3))
+        if _rows(v, "v", 4, (BF16, F16, E4M3)) != code or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+            raise ValueError("k and v must have the same dtype, shape, strides and device")
+        self.k, self.v = k, v
+        pages, page_size, heads, dim = k.shape
+        self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
+        strides = [s if n > 1 else 0 for s, n in zip(k.stride(), k.shape)]
+        self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dim, strides[0], strides[1],
+                                      strides[2], k_scale, v_scale, code, 0)
+        self._ref = C.byref(self._struct)
+
+
+KvTablesFields = ("block_table", "slots", "positions", "token_rows", "offsets", "lengths", "counts")
+
+
+class KvTables(namedtuple("KvTables", KvTablesFields)):
+    """What ninfer_kv_tables writes; give one back as `out` to reuse its buffers."""
+    __slots__ = ()
+
+    @classmethod
+    def empty(cls, block_table, capacity: int):
+        """Buffers for the requests of block_table (requests, table_pages) and `capacity` new tokens."""
+        torch = _torch()
+        new = lambda n, t: torch.empty(n, dtype=t, device=block_table.device)  # noqa: E731
+        n, i32 = block_table.shape[0], torch.int32
+        return cls(block_table, new(capacity, torch.int64), new(capacity, i32), new(capacity, i32), new(n + 1, i32),
+                   new(n, i32), new(2, i32))
+
+
+def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_table, capacity: int, out=None, status=None):
+    """Block tables and slot maps of a step's new tokens from the requests'
+    lengths: fills the fresh entries of block_table in place and returns a
+    KvTables. new_tokens None: one a request; free_pages None: no free page."""
+    i32 = _torch().int32
+    if not block_table.is_cuda or block_table.dtype != i32 or block_table.dim() != 2 or block_table.stride(1) != 1:
+        raise ValueError("block_table must be an int32 CUDA tensor (requests, table_pages) with contiguous rows")
+    n, width = block_table.shape
+    if out is None:
+        out = KvTables.empty(block_table, capacity)
+    _check(_lib.ninfer_kv_tables(
+        _arg(lengths, "lengths", i32, (n,)), _arg(new_tokens, "new_tokens", i32, (n,)), n, page_size,
+        _arg(free_pages, "free_pages", i32), free_pages.numel() if free_pages is not None else 0,
+        block_table.data_ptr(), width, block_table.stride(0) if n > 1 else width,
+        _arg(out.slots, "slots", _torch().int64, (capacity,)), _arg(out.positions, "positions", i32, (capacity,)),
+        _arg(out.token_rows, "token_rows", i32, (capacity,)), capacity, _arg(out.offsets, "offsets", i32, (n + 1,)),
+        _arg(out.lengths, "lengths", i32, (n,)), _arg(out.counts, "counts", i32, (2,)), _arg(status, "status", i32),
+        _raw_stream(lengths)))
+    return out if out.block_table is block_table else out._replace(block_table=block_table)
+
+
+def ninfer_kv_append(cache: KvCache, k, v, slots, status=None) -> None:
+    """Writes the new keys and values k, v (tokens, kv_heads, head_dim) into the cache's slots."""
+    code = _rows(k, "k", 3, (F32, BF16, F16))
+    if k.shape != v.shape or k.dtype != v.dtype or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+        raise ValueError("k and v must be (tokens, kv_heads, head_dim) of the cache and of one dtype")
+    _rows(v, "v", 3, (F32, BF16, F16))
+    torch = _torch()
+    tokens = k.shape[0]
+    ks, vs = k.stride(), v.stride()
+    _check(_lib.ninfer_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1],
+                                 _arg(slots, "slots", torch.int64, (tokens,)), cache._ref,
+                                 _arg(status, "status", torch.int32), _raw_stream(k)))
+
+
+def ninfer_kv_attention_workspace(cache: KvCache, requests: int, q_heads: int) -> int:
+    b = C.c_uint64()
+    _check(_lib.ninfer_kv_attention_workspace(cache._ref, requests, q_heads, C.byref(b)))
+    return b.value
+
+
+def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, window: int = 0, out=None, out_dtype=None,
+                        lse=None, workspace=None):
+    """Attention of one new token per request, q (requests, q_heads, head_dim),
+    over the cache's pages in block_table (requests, table_pages); lengths count
+    the new token. scale: head_dim ** -0.5 unless given; window 0: every key.
+    lse: a float32 (requests, q_heads) tensor to be written, or None."""
+    torch = _torch()
+    code = _rows(q, "q", 3, (F32, BF16, F16))
+    requests, heads, dim = q.shape
+    if dim != cache.head_dim:
+        raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
+    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
+            block_table.shape[0] != requests or block_table.stride(1) != 1:
+        raise ValueError("block_table must be an int32 CUDA tensor (requests, table_pages) with contiguous rows")
+    if out is None:
+        out = torch.empty((requests, heads, dim), dtype=out_dtype or q.dtype, device=q.device)
+    elif tuple(out.shape) != (requests, heads, dim) or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("out must be a contiguous CUDA tensor (requests, q_heads, head_dim)")
+    if workspace is None:
+        workspace = torch.empty(ninfer_kv_attention_workspace(cache, requests, heads), dtype=torch.uint8, device=q.device)
+    width = block_table.shape[1]
+    qs = q.stride()
+    _check(_lib.ninfer_kv_attention(
+        q.data_ptr(), code, requests, heads, qs[0], qs[1], cache._ref, block_table.data_ptr(), width,
+        block_table.stride(0) if requests > 1 else width, _arg(lengths, "lengths", torch.int32, (requests,)),
+        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), _types().get(out.dtype, -1),
+        _arg(lse, "lse", torch.float32, (requests, heads)), _dev_bytes(workspace), workspace.numel() * workspace.element_size(),
+        _raw_stream(q)))
+    return out
+
+
+def _dev_bytes(t):
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, prompt_lengths=None, repetition=None,
+                          presence=None, frequency=None, bias_offsets=None, bias_ids=None, bias_values=None, mask=None,
+                          mask_rows=None, status=None):
+    """Penalties, biases and grammar masks on logits (rows, vocab); out may be
+    logits itself. history: int32 (rows, longest); mask: int32 words (mask rows,
+    ceil(vocab / 32)), bit set where a token is allowed."""
+    torch = _torch()
+    f32, i32 = torch.float32, torch.int32
+    code = _rows(logits, "logits", 2, (F32, BF16, F16))
+    rows, vocab = logits.shape
+    if out is None:
+        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    elif _rows(out, "out", 2, (code,)) != code or out.shape != logits.shape:
+        raise ValueError("out must have the shape and dtype of logits")
+    c = _LogitsControls()
+    if history is not None:
+        c.history = _arg(history, "history", i32)
+        if history.dim() != 2 or history.shape[0] != rows:
+            raise ValueError("history must be (rows, longest)")
+        c.history_stride = history.shape[1]
+        c.history_lengths = _arg(history_lengths, "history_lengths", i32, (rows,))
+        c.prompt_lengths = _arg(prompt_lengths, "prompt_lengths", i32, (rows,))
+    c.repetition = _arg(repetition, "repetition", f32, (rows,))
+    c.presence = _arg(presence, "presence", f32, (rows,))
+    c.frequency = _arg(frequency, "frequency", f32, (rows,))
+    if bias_ids is not None and bias_ids.numel():
+        c.bias_offsets = _arg(bias_offsets, "bias_offsets", i32, (rows + 1,))
+        c.bias_count = bias_ids.numel()
+        c.bias_ids = _arg(bias_ids, "bias_ids", i32)
+        c.bias_values = _arg(bias_values, "bias_values", f32, (c.bias_count,))
+    if mask is not None:
+        if not mask.is_cuda or mask.dim() != 2 or mask.dtype != i32 or mask.stride(1) != 1 or mask.shape[1] * 32 < vocab:
+            raise ValueError("mask must be an int32 CUDA tensor (mask rows, at least vocab / 32 words)")
+        c.mask, c.mask_row_count, c.mask_stride = mask.data_ptr(), mask.shape[0], mask.stride(0)
+        c.mask_rows = _arg(mask_rows, "mask_rows", i32, (rows,))
+    _check(_lib.ninfer_logits_process(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, out.data_ptr(),
+                                      out.stride(0) if rows > 1 else vocab, code, rows, vocab, C.byref(c),
+                                      _arg(status, "status", i32), _raw_stream(logits)))
     return out

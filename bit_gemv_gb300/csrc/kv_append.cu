@@ -1,0 +1,158 @@
+// ninfer_kv_append: new keys and values into the slots of a paged cache, and the
+// rules of the cache description.
+//
+// Pure data movement: each source element is read once and each stored element
+// written once, so HBM bounds it (latency, for the few rows of a decode step).
+// One thread moves one 16-byte unit of the stored row (8 or 16 elements), K and V
+// in the same launch.
+#include "decode.cuh"
+
+namespace ninfer {
+
+int check_cache(const ninfer_kv_cache *c, const char *who) {
+    if (!c || !c->k || !c->v) return fail(NINFER_ERR_INVALID_ARGUMENT, "%s: NULL cache, k or v", who);
+    if (!cache_dtype_valid(c->dtype)) return fail(NINFER_ERR_INVALID_ARGUMENT, "%s: cache dtype %d unsupported", who, c->dtype);
+    if (!(c->k_scale > 0) || !(c->v_scale > 0) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+        return fail(NINFER_ERR_INVALID_ARGUMENT, "%s: cache scales must be finite and positive", who);
+    if (c->reserved) return fail(NINFER_ERR_INVALID_ARGUMENT, "%s: cache.reserved must be 0", who);
+    const uint64_t es = cache_dtype_size(c->dtype), unit = 16 / es, most = 0x7fffffffull;
+    if (!c->pages || !c->page_size || !c->kv_heads || c->pages > most || c->page_size > most || c->kv_heads > 65535)
+        return fail(NINFER_ERR_SHAPE, "%s: cache of %llu pages of %llu tokens, %llu heads", who,
+                    (unsigned long long)c->pages, (unsigned long long)c->page_size, (unsigned long long)c->kv_heads);
+    if (!c->head_dim || c->head_dim > 256 || c->head_dim % unit)
+        return fail(NINFER_ERR_SHAPE, "%s: head_dim %llu is not a multiple of %llu up to 256", who,
+                    (unsigned long long)c->head_dim, (unsigned long long)unit);
+    const uint64_t strides[3] = {c->pages > 1 ? c->page_stride : 0, c->page_size > 1 ? c->token_stride : 0,
+                                 c->kv_heads > 1 ? c->head_stride : 0};
+    for (uint64_t s : strides) {
+        if (s % unit) return fail(NINFER_ERR_ALIGNMENT, "%s: cache strides must be multiples of 16 bytes", who);
+        if (s >= (1ull << 40) / es) return fail(NINFER_ERR_OVERFLOW, "%s: cache stride of 2^40 bytes or more", who);
+    }
+    if (!aligned(c->k, 16) || !aligned(c->v, 16)) return fail(NINFER_ERR_ALIGNMENT, "%s: k and v must be 16-byte aligned", who);
+    return NINFER_OK;
+}
+
+namespace {
+
+struct AppendParams {
+    const uint8_t *src[2];              // k_new, v_new
+    uint8_t *dst[2];                    // cache.k, cache.v
+    uint64_t src_token[2], src_head[2]; // source strides, elements
+    uint64_t page_stride, token_stride, head_stride;
+    float scale[2];
+    const int64_t *slots;
+    uint64_t slot_count;                // of the cache
+    uint64_t total;                     // 16-byte units of one of the two
+    FastDiv units, heads;               // units a head, heads
+    uint32_t page_size;
+    int src_dtype;
+    int32_t *status;
+};
+
+// Eight floats, each divided by its scale, as 16 bytes of bf16 or f16 (kEs 2) or 8 bytes of e4m3 (kEs 1).
+template <int kDtype>
+__device__ __forceinline__ void pack8(const float (&x)[8], uint32_t *out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (kDtype == NINFER_BF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+            out[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else if (kDtype == NINFER_F16) {
+            const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+            out[i] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const uint32_t q = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i], x[2 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+            out[i / 2] = i & 1 ? out[i / 2] | (q << 16) : q;
+        }
+    }
+}
+
+template <int kDtype>
+__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+    constexpr uint32_t kEs = kDtype == NINFER_E4M3 ? 1 : 2, kUnit = 16 / kEs;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= p.total) return;
+    const int which = blockIdx.y;
+    // total < 2^32: the host splits longer calls
+    const uint32_t head_row = p.units.div((uint32_t)i), unit = (uint32_t)i - head_row * p.units.d;
+    const uint32_t token = p.heads.div(head_row), head = head_row - token * p.heads.d;
+    const int64_t slot = p.slots[token];
+    if (slot < 0) return;
+    if ((uint64_t)slot >= p.slot_count) {
+        if (p.status && unit == 0 && head == 0) atomicOr(p.status, NINFER_KV_BAD_SLOT);
+        return;
+    }
+    float x[kUnit];
+    const uint64_t from = token * p.src_token[which] + head * p.src_head[which] + unit * kUnit;
+#pragma unroll
+    for (uint32_t j = 0; j < kUnit; j += 8) load8(p.src[which], from + j, p.src_dtype, *reinterpret_cast<float(*)[8]>(x + j));
+    const float scale = p.scale[which];
+    if (scale != 1.f)
+#pragma unroll
+        for (uint32_t j = 0; j < kUnit; ++j) x[j] = __fdiv_rn(x[j], scale);
+    uint32_t o[4];
+#pragma unroll
+    for (uint32_t j = 0; j < kUnit; j += 8) pack8<kDtype>(*reinterpret_cast<float(*)[8]>(x + j), o + j / 4);
+    const uint64_t page = (uint64_t)slot / p.page_size, at = (uint64_t)slot % p.page_size;
+    uint8_t *to = p.dst[which] + (page * p.page_stride + at * p.token_stride + head * p.head_stride + unit * kUnit) * kEs;
+    *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+}  // namespace
+}  // namespace ninfer
+
+using namespace ninfer;
+
+extern "C" int ninfer_kv_append(const void *k_new, const void *v_new, int src_dtype, uint64_t tokens,
+                                uint64_t k_token_stride, uint64_t k_head_stride, uint64_t v_token_stride,
+                                uint64_t v_head_stride, const int64_t *slots, const ninfer_kv_cache *cache,
+                                int32_t *status, ninfer_stream stream) {
+    int st = check_cache(cache, "append");
+    if (st) return st;
+    if (!k_new || !v_new || !slots) return fail(NINFER_ERR_INVALID_ARGUMENT, "append: NULL k_new, v_new or slots");
+    if (!dtype_valid(src_dtype)) return fail(NINFER_ERR_INVALID_ARGUMENT, "append: source dtype %d unsupported", src_dtype);
+    const uint64_t es = cache_dtype_size(cache->dtype), unit = 16 / es, aligned_elems = 16 / dtype_size(src_dtype);
+    if (tokens == 0 || tokens > 0x7fffffffull) return fail(NINFER_ERR_SHAPE, "append: tokens must be 1 to 2^31 - 1");
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(slots, 8) || (status && !aligned(status, 4)))
+        return fail(NINFER_ERR_ALIGNMENT, "append: k_new and v_new must be 16-byte, slots 8-byte aligned");
+    if ((tokens > 1 && (k_token_stride % aligned_elems || v_token_stride % aligned_elems)) ||
+        (cache->kv_heads > 1 && (k_head_stride % aligned_elems || v_head_stride % aligned_elems)))
+        return fail(NINFER_ERR_ALIGNMENT, "append: source strides must be multiples of 16 bytes");
+    AppendParams p;
+    const uint64_t units = cache->head_dim / unit, per_token = units * cache->kv_heads;
+    p.dst[0] = static_cast<uint8_t *>(cache->k);
+    p.dst[1] = static_cast<uint8_t *>(cache->v);
+    p.src_token[0] = k_token_stride;
+    p.src_token[1] = v_token_stride;
+    p.src_head[0] = k_head_stride;
+    p.src_head[1] = v_head_stride;
+    p.page_stride = cache->page_stride;
+    p.token_stride = cache->token_stride;
+    p.head_stride = cache->head_stride;
+    p.scale[0] = cache->k_scale;
+    p.scale[1] = cache->v_scale;
+    p.slot_count = cache->pages * cache->page_size;
+    p.units = FastDiv((uint32_t)units);
+    p.heads = FastDiv((uint32_t)cache->kv_heads);
+    p.page_size = (uint32_t)cache->page_size;
+    p.src_dtype = src_dtype;
+    p.status = status;
+    const auto kernel = cache->dtype == NINFER_BF16  ? append_kernel<NINFER_BF16>
+                        : cache->dtype == NINFER_F16 ? append_kernel<NINFER_F16>
+                                                     : append_kernel<NINFER_E4M3>;
+    // at most 2^31 units a launch: the kernel indexes units with 32 bits
+    const uint64_t step = (1ull << 31) / per_token ? (1ull << 31) / per_token : 1;
+    for (uint64_t t = 0; t < tokens; t += step) {
+        const uint64_t n = tokens - t < step ? tokens - t : step;
+        p.src[0] = static_cast<const uint8_t *>(k_new) + t * k_token_stride * dtype_size(src_dtype);
+        p.src[1] = static_cast<const uint8_t *>(v_new) + t * v_token_stride * dtype_size(src_dtype);
+        p.slots = slots + t;
+        p.total = n * per_token;
+        st = launch_dependent("append", kernel, dim3((unsigned)((p.total + 255) / 256), 2), dim3(256), 0,
+                              (cudaStream_t)stream, p);
+        if (st) return st;
+    }
+    return NINFER_OK;
+}

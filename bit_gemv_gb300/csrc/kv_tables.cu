@@ -1,0 +1,208 @@
+// ninfer_kv_tables: block tables, slots and positions of a step's new tokens from
+// the requests' lengths, in one launch.
+//
+// Two prefix sums over the requests (new tokens, pages to take) and one lookup
+// a token. Latency bounds a decode step and the 16 bytes written a token a large
+// admission, so every CTA recomputes the sums instead of waiting for another one:
+// thread i of the block sums a contiguous run of requests, the block scans the
+// threads' sums, and a token then finds its run by binary search among them in
+// shared memory and its request by walking the run.
+#include "decode.cuh"
+
+namespace ninfer {
+namespace {
+
+constexpr int kThreads = 1024;
+
+struct TablesParams {
+    const int32_t *lengths, *fresh, *free_pages;
+    int32_t *table;
+    int64_t *slots;
+    int32_t *positions, *rows, *offsets, *lengths_out, *counts, *status;
+    uint64_t table_stride;
+    uint32_t requests, run, table_pages, free_count, capacity;
+    FastDiv page;
+};
+
+__device__ __forceinline__ int32_t clamp31(uint64_t v) { return v > 0x7fffffffull ? 0x7fffffff : (int32_t)v; }
+
+struct Request {
+    uint32_t length, fresh;     // tokens held, new ones (both < 2^31)
+    uint32_t held, pages;       // pages held, pages to take
+};
+
+__device__ __forceinline__ Request request(const TablesParams &p, uint32_t i) {
+    Request r;
+    const int32_t l = p.lengths[i], n = p.fresh ? p.fresh[i] : 1;
+    r.length = l > 0 ? l : 0;
+    r.fresh = n > 0 ? n : 0;
+    const uint32_t q = p.page.div(r.length);
+    r.held = q + (q * p.page.d != r.length);
+    const uint32_t end = r.length + r.fresh, qe = p.page.div(end);   // < 2^32
+    r.pages = qe + (qe * p.page.d != end) - r.held;
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) {
+    __shared__ uint64_t s_tokens[kThreads], s_pages[kThreads];      // sums before thread i's run
+    __shared__ uint64_t s_warp[2][33];
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint64_t first = (uint64_t)tid * p.run, last = min(first + p.run, (uint64_t)p.requests);
+    uint64_t tokens = 0, pages = 0;
+    int bad = 0;
+    for (uint64_t i = first; i < last; ++i) {
+        const Request r = request(p, (uint32_t)i);
+        tokens += r.fresh;
+        pages += r.pages;
+        if (blockIdx.x == 0) {
+            if (p.lengths[i] < 0 || (p.fresh && p.fresh[i] < 0) || r.length + r.fresh > 0x7fffffffu) bad |= NINFER_KV_BAD_LENGTH;
+            if (r.pages && r.held + r.pages > p.table_pages) bad |= NINFER_KV_ROW_TOO_SHORT;
+        }
+    }
+    uint64_t t = tokens, g = pages;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint64_t a = __shfl_up_sync(~0u, t, s), b = __shfl_up_sync(~0u, g, s);
+        if (lane >= s) {
+            t += a;
+            g += b;
+        }
+    }
+    if (lane == 31) {
+        s_warp[0][warp] = t;
+        s_warp[1][warp] = g;
+    }
+    __syncthreads();
+    if (warp < 2) {
+        uint64_t w = s_warp[warp][lane];
+        const uint64_t own = w;
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint64_t a = __shfl_up_sync(~0u, w, s);
+            if (lane >= s) w += a;
+        }
+        s_warp[warp][lane] = w - own;
+        if (lane == 31) s_warp[warp][32] = w;
+    }
+    __syncthreads();
+    t += s_warp[0][warp] - tokens;
+    g += s_warp[1][warp] - pages;
+    s_tokens[tid] = t;
+    s_pages[tid] = g;
+    const uint64_t total = s_warp[0][32], taken = s_warp[1][32];
+    __syncthreads();
+
+    // outputs by request: the runs are dealt out to the CTAs
+    if (tid % gridDim.x == blockIdx.x) {
+        uint64_t at = t;
+        for (uint64_t i = first; i < last; ++i) {
+            const Request r = request(p, (uint32_t)i);
+            if (p.offsets) p.offsets[i] = clamp31(at);
+            if (p.lengths_out) p.lengths_out[i] = clamp31((uint64_t)r.length + r.fresh);
+            at += r.fresh;
+        }
+    }
+    if (blockIdx.x == 0) {
+        if (tid == 0) {
+            if (p.offsets) p.offsets[p.requests] = clamp31(total);
+            if (p.counts) {
+                p.counts[0] = clamp31(total);
+                p.counts[1] = clamp31(taken);
+            }
+            if (taken > p.free_count) bad |= NINFER_KV_OUT_OF_PAGES;
+            if (total > p.capacity) bad |= NINFER_KV_OUT_OF_SLOTS;
+        }
+        if (bad && p.status) atomicOr(p.status, bad);
+    }
+
+    // outputs by token; the first new token of a fresh page also enters the page
+    const uint64_t all = max(total, (uint64_t)p.capacity);
+    for (uint64_t k = (uint64_t)blockIdx.x * kThreads + tid; k < all; k += (uint64_t)gridDim.x * kThreads) {
+        if (k >= total) {
+            if (p.slots) p.slots[k] = -1;
+            if (p.positions) p.positions[k] = -1;
+            if (p.rows) p.rows[k] = -1;
+            continue;
+        }
+        uint32_t lo = 0;                     // last thread whose run starts at or before k
+#pragma unroll
+        for (uint32_t s = kThreads / 2; s; s >>= 1)
+            if (s_tokens[lo + s] <= k) lo += s;
+        uint64_t at = s_tokens[lo], base = s_pages[lo];
+        uint32_t i = lo * p.run;
+        Request r = request(p, i);
+        while (k >= at + r.fresh) {          // ends: k < total
+            at += r.fresh;
+            base += r.pages;
+            r = request(p, ++i);
+        }
+        const uint32_t pos = r.length + (uint32_t)(k - at), pi = p.page.div(pos), in = pos - pi * p.page.d;
+        int32_t *entry = p.table + i * p.table_stride + pi;
+        int32_t page = -1;
+        if (pi < p.table_pages) {
+            if (pi < r.held) page = *entry;
+            else {
+                const uint64_t q = base + (pi - r.held);
+                if (q < p.free_count) page = p.free_pages[q];
+                if (in == 0) *entry = page;
+            }
+        }
+        if (k < p.capacity) {
+            if (p.slots) p.slots[k] = page < 0 ? -1 : (int64_t)page * p.page.d + in;
+            if (p.positions) p.positions[k] = clamp31(pos);
+            if (p.rows) p.rows[k] = (int32_t)i;
+        }
+    }
+}
+
+}  // namespace
+}  // namespace ninfer
+
+using namespace ninfer;
+
+extern "C" int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_tokens, uint64_t requests,
+                                uint64_t page_size, const int32_t *free_pages, uint64_t free_count,
+                                int32_t *block_table, uint64_t table_pages, uint64_t table_stride, int64_t *slots,
+                                int32_t *positions, int32_t *token_rows, uint64_t capacity, int32_t *offsets,
+                                int32_t *lengths_out, int32_t *counts, int32_t *status, ninfer_stream stream) {
+    if (!lengths || !block_table) return fail(NINFER_ERR_INVALID_ARGUMENT, "tables: NULL lengths or block_table");
+    if (free_count && !free_pages) return fail(NINFER_ERR_INVALID_ARGUMENT, "tables: NULL free_pages with a count");
+    const uint64_t most = 0x7fffffffull;
+    if (!requests || !page_size || !table_pages || requests > most || page_size > most || table_pages > most ||
+        capacity > most || free_count > most)
+        return fail(NINFER_ERR_SHAPE, "tables: %llu requests, pages of %llu tokens, %llu pages a row (each 1 to 2^31 - 1; "
+                    "capacity and free_count up to 2^31 - 1)", (unsigned long long)requests,
+                    (unsigned long long)page_size, (unsigned long long)table_pages);
+    if (table_stride < table_pages && requests > 1) return fail(NINFER_ERR_SHAPE, "tables: table_stride < table_pages");
+    if (table_stride > (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "tables: table_stride over 2^40");
+    for (const void *a : {(const void *)lengths, (const void *)new_tokens, (const void *)free_pages,
+                          (const void *)block_table, (const void *)positions, (const void *)token_rows,
+                          (const void *)offsets, (const void *)lengths_out, (const void *)counts, (const void *)status})
+        if (!aligned(a, 4)) return fail(NINFER_ERR_ALIGNMENT, "tables: int32 buffers must be 4-byte aligned");
+    if (!aligned(slots, 8)) return fail(NINFER_ERR_ALIGNMENT, "tables: slots must be 8-byte aligned");
+    TablesParams p;
+    p.lengths = lengths;
+    p.fresh = new_tokens;
+    p.free_pages = free_pages;
+    p.table = block_table;
+    p.slots = slots;
+    p.positions = positions;
+    p.rows = token_rows;
+    p.offsets = offsets;
+    p.lengths_out = lengths_out;
+    p.counts = counts;
+    p.status = status;
+    p.table_stride = table_stride;
+    p.requests = (uint32_t)requests;
+    p.run = (uint32_t)((requests + kThreads - 1) / kThreads);
+    p.table_pages = (uint32_t)table_pages;
+    p.free_count = (uint32_t)free_count;
+    p.capacity = (uint32_t)capacity;
+    p.page = FastDiv((uint32_t)page_size);
+    const uint64_t work = capacity > requests ? capacity : requests;
+    const uint64_t want = (work + kThreads - 1) / kThreads;
+    return launch_dependent("tables", tables_kernel, dim3((unsigned)(want < 304 ? want : 304)), dim3(kThreads), 0,
+                            (cudaStream_t)stream, p);
+}
