@@ -1,101 +1,762 @@
 // ninfer_kv_attention: attention of one new token per request over a paged cache.
 //
-// One pass over the keys with a running maximum m and sum l: a new score s
-// rescales what was summed by e^{m - max(m, s)}. One CTA per (request, query
-// head); its warps take every eighth key, each lane eight elements of the row,
-// and join their (m, l, sum) at the end.
+// Mathematics. One pass over the keys with a running maximum m and sum l per
+// query head: scores above m rescale what was summed by 2^{m_old - m_new} (scores are
+// kept in units of log2). Parts of a row that different warps or CTAs
+// summed are joined the same way, with M = max m_i: l = sum 2^{m_i - M} l_i.
+//
+// What bounds it. Every key and value is used by the few query heads of its
+// group (4 * group flops an element), so HBM does; the tensor cores only have
+// to keep up. mma.sync.m16n8k16 serves: 16 keys of 128 elements take 24 to 32 of them.
+//   scores   A = queries (16 rows: 8 heads' 16-bit values, then their 16-bit
+//            remainders), B = keys: the remainders ride in rows that would be empty.
+//   values   A = values transposed (ldmatrix.trans), B = weights: a score tile's accumulator
+//            registers are the weights' B fragment as they are, and value and
+//            remainder of a weight add up in one accumulator.
+//
+// Split. The keys of every (request, key head, 8 query heads) are cut into
+// units of 8 KB of keys and 8 KB of values; all units of the call form one
+// line, of which each CTA (one an SM) and in it each warp takes an equal,
+// contiguous part, so that any mix of lengths keeps every SM busy to the end.
+// A warp writes a row that lies in its part whole; cut rows are joined in the CTA,
+// and rows cut between CTAs by a second, small kernel.
+//
+// Loads. Each warp has a ring of three 8 KB items in shared memory, keys and
+// values of its units in turn, filled by tensor-map copies of whole page
+// pieces (128-byte swizzle, so that ldmatrix is free of bank conflicts); no warp
+// waits for another one until its part is done. Up to 192 KB an SM are in
+// flight. Pieces past the row's end are not fetched.
 #include <cmath>
+#include <cstring>
+#include <mutex>
+
+#include <cuda.h>
 
 #include "decode.cuh"
+#include "gemv.h"
 
 namespace ninfer {
 namespace {
 
+constexpr int kWarps = 8, kThreads = 32 * kWarps, kItems = 3;
+constexpr uint32_t kItemBytes = 8192;
+constexpr uint32_t kRingBytes = kWarps * kItems * kItemBytes;
+constexpr uint32_t kNone = 0xffffffffu;
+
 struct AttentionParams {
+    CUtensorMap k, v;                   // {element, token, head, page}
     const void *q;
-    const uint8_t *k, *v;
     const int32_t *table, *lengths;
     void *out;
     float *lse;
-    uint64_t q_request, q_head, table_stride, page_stride, token_stride, head_stride, window;
-    float scale, v_scale;       // scores: scale * k_scale
-    uint32_t q_heads, group, head_dim, table_pages, pages;
-    FastDiv page;
-    int q_dtype, out_dtype, dtype;
+    uint4 *meta;                        // per CTA: row of its tail, whether its head part ends a row, and has one
+    float2 *cta_ml;                     // [CTA][2][8]: m, l
+    float4 *cta_o, *warp_o;             // [CTA][2] and [CTA][warp][2] sums, in fragment order
+    int64_t q_request, q_head, table_stride;
+    uint32_t *err;
+    float scale, v_scale;               // scale: of scores, in log2
+    uint32_t requests, run, q_heads, group, head_dim, head_rows, box, window, most, min_units;
+    FastDiv page, tiles, heads;         // tokens a page, 8-head tiles a key head, rows a request
+    int q_dtype, out_dtype;
 };
 
-__device__ __forceinline__ void load_cache8(const uint8_t *base, uint64_t idx, int dtype, float (&x)[8]) {
-    if (dtype != NINFER_E4M3) {
-        load8(base, idx, dtype, x);
-        return;
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Two 8-bit floats as two binary16 values (exact).
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)two));
+    return h;
+}
+
+// What depends on the cache's type and the padded head width. Operands of the
+// tensor cores are bfloat16 for a bfloat16 cache and binary16 for the other two.
+template <int kDtype, int kWidth>
+struct Shape {
+    static constexpr bool kBf16 = kDtype == NINFER_BF16, kBytes8 = kDtype == NINFER_E4M3;
+    static constexpr int kEs = kBytes8 ? 1 : 2;
+    static constexpr int kKeys = kItemBytes / (kWidth * kEs);   // of a unit: 16, 32 or 64
+    static constexpr int kChunks = kWidth * kEs / 128;          // 128-byte columns of an item
+    static constexpr int kSteps = kWidth / 16;                  // 16-element steps of a row
+    static constexpr int kScoreTiles = kKeys / 8;
+    // binary16 weights carry a factor 2^14: weights down to 2^-38 of the largest one keep a value
+    static constexpr float kBias = kBf16 ? 0.f : 14.f;
+
+    static __device__ __forceinline__ uint32_t pack(float a, float b) {
+        if (kBf16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+            return *reinterpret_cast<const uint32_t *>(&h);
+        }
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
     }
-    const uint2 u = *reinterpret_cast<const uint2 *>(base + idx);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint32_t w = ((j & 2) ? u.y : u.x) >> (16 * (j & 1));
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w & 0xffff), __NV_E4M3);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-        x[2 * j] = f.x;
-        x[2 * j + 1] = f.y;
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        if (kBf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+        return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    }
+    // x as a 16-bit value and the 16-bit remainder
+    static __device__ __forceinline__ void split(float a, float b, uint32_t &value, uint32_t &rest) {
+        value = pack(a, b);
+        const float2 f = unpack(value);
+        rest = pack(a - f.x, b - f.y);
+    }
+    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        if (kBf16)
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        else
+            asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    // Element of a row that accumulator row g (+ 8 * half) of value tile `tile` stands for.
+    // 8-bit values leave ldmatrix.trans in pairs, so that rows g and g + 8 are neighbours.
+    static __device__ __forceinline__ int element(int tile, int g, int half) {
+        return 16 * tile + (kBytes8 ? 2 * g + half : g + 8 * half);
+    }
+};
+
+// Keys of a request, and how many units they take.
+struct Row {
+    uint32_t from, end, units;
+};
+
+template <int kKeys>
+__device__ __forceinline__ Row row_of(const AttentionParams &p, uint32_t request) {
+    Row r;
+    const int32_t n = p.lengths[request];
+    r.end = n <= 0 ? 0u : min((uint32_t)n, p.most);
+    r.from = p.window && r.end > p.window ? r.end - p.window : 0u;
+    r.units = r.end ? (r.end + kKeys - 1) / kKeys - r.from / kKeys : 0u;
+    return r;
+}
+
+// A place on the line of units.
+struct Cursor {
+    uint32_t request, head, unit;       // head: of the request's rows
+    Row row;
+};
+
+template <int kKeys>
+__device__ __forceinline__ void advance(const AttentionParams &p, Cursor &c) {
+    if (++c.unit < c.row.units) return;
+    c.unit = 0;
+    if (++c.head < p.head_rows) return;
+    c.head = 0;
+    while (++c.request < p.requests) {
+        c.row = row_of<kKeys>(p, c.request);
+        if (c.row.units) return;
     }
 }
 
-__global__ void __launch_bounds__(256) attention_kernel(const AttentionParams p) {
-    __shared__ float s_m[8], s_l[8], s_o[8][256];
+__device__ __forceinline__ float2 load2(const void *base, int64_t idx, int dtype) {
+    if (dtype == NINFER_F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + idx);
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + idx);
+    if (dtype == NINFER_BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+}
+
+// One value tile of a finished row: o / l in the output's type, for heads 2 t and 2 t + 1.
+template <class S>
+__device__ __forceinline__ void store_tile(const AttentionParams &p, uint32_t row, int tile, int lane, const float4 &o, float l0,
+                                           float l1) {
+    const uint32_t request = p.heads.div(row), hr = row - request * p.head_rows, kvh = p.tiles.div(hr);
+    const uint32_t first = (hr - kvh * p.tiles.d) * 8, g = lane >> 2, h = first + 2 * (lane & 3);
+    const uint64_t head = (uint64_t)request * p.q_heads + kvh * p.group + h;
+    const float r0 = l0 == 0.f ? 0.f : p.v_scale / l0, r1 = l1 == 0.f ? 0.f : p.v_scale / l1;
+    const float v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const uint32_t e = S::element(tile, g, half);
+        if (e >= p.head_dim) continue;
+        if (h < p.group) store1(p.out, head * p.head_dim + e, p.out_dtype, l0 == 0.f ? 0.f : v[2 * half] * r0);
+        if (h + 1 < p.group) store1(p.out, (head + 1) * p.head_dim + e, p.out_dtype, l1 == 0.f ? 0.f : v[2 * half + 1] * r1);
+    }
+}
+
+// ln of the sum of e^score for head `h` of the row's tile.
+template <class S>
+__device__ __forceinline__ void store_lse(const AttentionParams &p, uint32_t row, uint32_t h, float m, float l) {
+    const uint32_t request = p.heads.div(row), hr = row - request * p.head_rows, kvh = p.tiles.div(hr);
+    h += (hr - kvh * p.tiles.d) * 8;
+    if (p.lse && h < p.group)
+        p.lse[(uint64_t)request * p.q_heads + kvh * p.group + h] =
+            l == 0.f ? -INFINITY : (m - S::kBias) * 0.693147180559945f + logf(l);
+}
+
+template <int kDtype, int kWidth>
+__global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttentionParams p) {
+    using S = Shape<kDtype, kWidth>;
+    constexpr int kKeys = S::kKeys, kSteps = S::kSteps, kTiles = kWidth / 16, kPart = kTiles * 32;
+    extern __shared__ uint8_t ring_raw[];
+    __shared__ __align__(8) uint64_t s_bar[kWarps][kItems];
+    __shared__ uint64_t s_sum[kWarps];
+    __shared__ uint32_t s_start[kWarps][3];                 // request, row of it, unit
+    __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
+    __shared__ float2 s_ml[2 * kWarps][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const uint32_t ring = ((smem_u32(ring_raw) + 1023) & ~1023u) + warp * (kItems * kItemBytes);
+    const uint32_t bar = smem_u32(&s_bar[warp][0]);
+    if (lane == 0)
+        for (int i = 0; i < kItems; ++i) mbar_init(bar + 8 * i, 1);
+    if (threadIdx.x == 0) {
+        prefetch_tmap(&p.k);
+        prefetch_tmap(&p.v);
+    }
+    if (lane < 2) s_row[2 * warp + lane] = kNone;
+    fence_mbar_init();
     pdl_launch_dependents();
     pdl_wait();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint64_t r = blockIdx.x / p.q_heads;
-    const uint32_t h = blockIdx.x % p.q_heads, kvh = h / p.group, e = lane * 8;
-    const bool on = e < p.head_dim;
-    int64_t n = p.lengths[r];
-    const int64_t most = (int64_t)p.table_pages * p.page.d;
-    n = n < 0 ? 0 : n > most ? most : n;
-    const int64_t from = p.window && (uint64_t)n > p.window ? n - (int64_t)p.window : 0;
-    float q[8] = {}, o[8] = {}, m = -INFINITY, l = 0.f;
-    if (on) load8(p.q, r * p.q_request + h * p.q_head + e, p.q_dtype, q);
-    for (int64_t j = from + warp; j < n; j += 8) {
-        const uint32_t pg = p.page.div((uint32_t)j);
-        const int32_t page = p.table[r * p.table_stride + pg];
-        const bool held = on && page >= 0 && (uint32_t)page < p.pages;
-        const uint64_t at = (uint64_t)(held ? page : 0) * p.page_stride + (uint64_t)((uint32_t)j - pg * p.page.d) * p.token_stride +
-                            kvh * p.head_stride + e;
-        float k[8] = {}, v[8] = {}, s = 0.f;
-        if (held) {
-            load_cache8(p.k, at, p.dtype, k);
-            load_cache8(p.v, at, p.dtype, v);
-        }
+
+    // ---- this warp's part of the line ----
+    const uint32_t r0 = min(threadIdx.x * p.run, p.requests), r1 = min(r0 + p.run, p.requests);
+    uint64_t mine = 0;
+    for (uint32_t r = r0; r < r1; ++r) mine += row_of<kKeys>(p, r).units;
+    mine *= p.head_rows;
+    uint64_t upto = mine;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s = fmaf(q[i], k[i], s);
-#pragma unroll
-        for (int b = 16; b; b >>= 1) s += __shfl_xor_sync(~0u, s, b);
-        s *= p.scale;
-        const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-        const float f = expf(m - mu), w = expf(s - mu);
-        l = fmaf(l, f, w);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] = fmaf(o[i], f, w * v[i]);
-        m = mn;
+    for (int s = 1; s < 32; s <<= 1) {
+        const uint64_t a = __shfl_up_sync(~0u, upto, s);
+        if (lane >= s) upto += a;
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
-    }
-    if (on)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s_o[warp][e + i] = o[i];
+    if (lane == 31) s_sum[warp] = upto;
     __syncthreads();
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < 8; ++w) top = fmaxf(top, s_m[w]);
-    const float mu = top == -INFINITY ? 0.f : top;
-    for (int w = 0; w < 8; ++w) sum += s_l[w] * expf(s_m[w] - mu);
-    const uint64_t row = r * p.q_heads + h;
-    if (threadIdx.x == 0 && p.lse) p.lse[row] = top + logf(sum);
-    if (threadIdx.x < p.head_dim) {
-        float acc = 0.f;
-        for (int w = 0; w < 8; ++w) acc += s_o[w][threadIdx.x] * expf(s_m[w] - mu);
-        store1(p.out, row * p.head_dim + threadIdx.x, p.out_dtype, sum == 0.f ? 0.f : acc / sum * p.v_scale);
+    uint64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) upto += s_sum[w];
+        total += s_sum[w];
     }
+    const uint64_t before = upto - mine;
+    const uint64_t ctas = min((uint64_t)gridDim.x, (total + p.min_units - 1) / p.min_units);
+    const bool active = blockIdx.x < ctas;
+    const uint64_t c0 = active ? blockIdx.x * total / ctas : 0, c1 = active ? (blockIdx.x + 1) * total / ctas : 0;
+    if (before < c1 && upto > c0) {
+#pragma unroll 1
+        for (int w = 0; w < kWarps; ++w) {
+            uint64_t at = c0 + w * (c1 - c0) / kWarps;
+            if (at < before || at >= upto) continue;
+            at -= before;
+            for (uint32_t r = r0; r < r1; ++r) {
+                const Row row = row_of<kKeys>(p, r);
+                const uint64_t n = (uint64_t)row.units * p.head_rows;
+                if (at < n) {
+                    s_start[w][0] = r;
+                    s_start[w][1] = (uint32_t)(at / row.units);
+                    s_start[w][2] = (uint32_t)(at % row.units);
+                    break;
+                }
+                at -= n;
+            }
+        }
+    }
+    __syncthreads();
+    uint32_t left = (uint32_t)((warp + 1) * (c1 - c0) / kWarps - warp * (c1 - c0) / kWarps);
+
+    // ---- the ring ----
+    Cursor ld, cp;
+    ld.request = s_start[warp][0];
+    ld.head = s_start[warp][1];
+    ld.unit = s_start[warp][2];
+    if (left) ld.row = row_of<kKeys>(p, ld.request);
+    cp = ld;
+    uint32_t to_load = 2 * left, loaded = 0, taken = 0;     // items
+    uint32_t slot_in = 0, slot_out = 0, phase = 0;
+    int32_t page[2], token[2];                              // of this lane's pieces of the unit being loaded
+    const uint32_t pieces = kKeys / p.box;
+    auto load_item = [&] {
+        const bool values = loaded & 1;
+        const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys;
+        const uint32_t lo = ld.row.from > base ? (ld.row.from - base) / p.box : 0u;
+        const uint32_t hi = min(pieces, (ld.row.end - base + p.box - 1) / p.box);
+        if (!values) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t b = lane + 32 * i;
+                if (b < lo || b >= hi) continue;
+                const uint32_t key = base + b * p.box, pg = p.page.div(key);
+                token[i] = (int32_t)(key - pg * p.page.d);
+                page[i] = p.table[(int64_t)ld.request * p.table_stride + pg];
+            }
+        }
+        const uint32_t b = bar + 8 * slot_in;
+        if (lane == 0) mbar_arrive_expect_tx(b, (hi - lo) * p.box * (kWidth * S::kEs));
+        __syncwarp();
+        const int head = (int)p.tiles.div(ld.head);
+        const CUtensorMap *map = values ? &p.v : &p.k;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t q = lane + 32 * i;
+            if (q < lo || q >= hi) continue;
+#pragma unroll
+            for (int c = 0; c < S::kChunks; ++c)
+                tma_load_4d(ring + slot_in * kItemBytes + c * (kKeys * 128) + q * p.box * 128, map, c * (128 / S::kEs), token[i],
+                            head, page[i], b);
+        }
+        if (values) advance<kKeys>(p, ld);
+        ++loaded;
+        slot_in = slot_in == kItems - 1 ? 0 : slot_in + 1;
+    };
+    for (int i = 0; i < kItems && loaded < to_load; ++i) load_item();
+
+    bool alive = true;
+    auto wait_item = [&] {
+        const bool ok = mbar_wait(bar + 8 * slot_out, phase, p.err);
+        alive = __all_sync(~0u, ok);
+    };
+    auto release_item = [&] {
+        __syncwarp();
+        ++taken;
+        if (++slot_out == kItems) {
+            slot_out = 0;
+            phase ^= 1;
+        }
+        if (loaded < to_load) load_item();
+    };
+
+    // ---- the units ----
+    uint32_t qa[kSteps][4];
+    float o[kTiles][4], m = -INFINITY, l = 0.f, sc = 0.f;
+    bool fresh = true, begun = false;       // a new row's queries are due; the row began in this part
+    const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
+    while (left && alive) {
+        --left;
+        if (fresh) {
+            fresh = false;
+            begun = cp.unit == 0;
+            m = -INFINITY;
+            l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+            const uint32_t kvh = p.tiles.div(cp.head), h = (cp.head - kvh * p.tiles.d) * 8 + g;
+            const int64_t at = (int64_t)cp.request * p.q_request + (int64_t)(kvh * p.group + h) * p.q_head;
+            float2 x[kSteps][2];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t e = 16 * i + (S::kBytes8 ? 4 * t + 2 * j : 2 * t + 8 * j);
+                    x[i][j] = h < p.group && e < p.head_dim ? load2(p.q, at + e, p.q_dtype) : make_float2(0.f, 0.f);
+                    top = fmaxf(top, fmaxf(fabsf(x[i][j].x), fabsf(x[i][j].y)));
+                }
+            sc = p.scale;
+            float down = 1.f;
+            if (!S::kBf16) {
+                // binary16 operands: a power of two brings the head's largest element to [1, 2)
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+                const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -100) : 0;
+                down = ldexpf(1.f, -e);
+                sc = ldexpf(sc, e);
+            }
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = x[i][j].x * down, b = x[i][j].y * down;
+                    S::split(a, b, qa[i][2 * j], qa[i][2 * j + 1]);
+                    if (isinf(a) || isinf(b)) qa[i][2 * j + 1] = 0;     // no remainder: inf - inf
+                }
+        }
+        const uint32_t base = (cp.row.from / kKeys + cp.unit) * kKeys;
+        const bool edge = base < cp.row.from || base + kKeys > cp.row.end;
+
+        // scores: rows g (values of q) and g + 8 (remainders) of the tile add up
+        wait_item();
+        float s[S::kScoreTiles][4];
+#pragma unroll
+        for (int i = 0; i < S::kScoreTiles; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        uint32_t item = ring + slot_out * kItemBytes;
+        {
+            const uint32_t lane_at = item + ((lane_mat >> 1) * 8 + lane_row) * 128;
+            if constexpr (!S::kBytes8) {
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i) {
+                    const uint32_t unit = 2 * i, col = (((unit & 7) + (lane_mat & 1)) ^ lane_row) << 4;
+#pragma unroll
+                    for (int n = 0; n < S::kScoreTiles / 2; ++n) {
+                        uint32_t b[4];
+                        ldmatrix4(b, lane_at + (unit >> 3) * (kKeys * 128) + n * 2048 + col);
+                        S::mma(s[2 * n], qa[i], b[0], b[1]);
+                        S::mma(s[2 * n + 1], qa[i], b[2], b[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSteps; i += 2) {
+                    const uint32_t col = (((i & 7) + (lane_mat & 1)) ^ lane_row) << 4;
+#pragma unroll
+                    for (int n = 0; n < S::kScoreTiles / 2; ++n) {
+                        uint32_t b[4];
+                        ldmatrix4(b, lane_at + (i >> 3) * (kKeys * 128) + n * 2048 + col);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            S::mma(s[2 * n + (j >> 1)], qa[i + (j & 1)], e4m3x2_to_f16x2(b[j]), e4m3x2_to_f16x2(b[j] >> 16));
+                    }
+                }
+            }
+        }
+        release_item();
+        float top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < S::kScoreTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // an infinite score stands: a remainder of 0 times an infinite key is NaN
+                s[i][j] = (isinf(s[i][j]) ? s[i][j] : s[i][j] + s[i][j + 2]) * sc;
+                if (edge) {
+                    const uint32_t key = base + 8 * i + 2 * t + j;
+                    if (key < cp.row.from || key >= cp.row.end) s[i][j] = -INFINITY;
+                }
+                top = fmaxf(top, s[i][j]);
+            }
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        const float mn = fmaxf(m, top);
+        if (__any_sync(~0u, mn != m)) {
+            const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
+            const float f0 = __shfl_sync(~0u, f, 8 * t), f1 = __shfl_sync(~0u, f, 8 * t + 4);
+            l *= f;
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            }
+            m = mn;
+        }
+        const float shift = (mn == -INFINITY ? 0.f : mn) - S::kBias;
+        uint32_t w[S::kScoreTiles][2];          // weights of keys 2 t and 2 t + 1: value and remainder
+#pragma unroll
+        for (int i = 0; i < S::kScoreTiles; ++i) {
+            const float a = exp2_approx(s[i][0] - shift), b = exp2_approx(s[i][1] - shift);
+            l += a + b;
+            S::split(a, b, w[i][0], w[i][1]);
+        }
+
+        wait_item();
+        item = ring + slot_out * kItemBytes;
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk) {
+            uint32_t keep[2] = {~0u, ~0u};      // rows outside the request hold anything, NaN too: zeros instead
+            if (edge) {
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t key = base + 16 * kk + 8 * j + 2 * t;
+                    keep[j] = (key >= cp.row.from && key < cp.row.end ? 0xffffu : 0u) |
+                              (key + 1 >= cp.row.from && key + 1 < cp.row.end ? 0xffff0000u : 0u);
+                }
+            }
+            if constexpr (!S::kBytes8) {
+                const uint32_t lane_at = item + (16 * kk + (lane_mat >> 1) * 8 + lane_row) * 128;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    uint32_t a[4];
+                    ldmatrix4_trans(a, lane_at + (i >> 2) * (kKeys * 128) + (((2 * (i & 3) + (lane_mat & 1)) ^ lane_row) << 4));
+                    a[0] &= keep[0];
+                    a[1] &= keep[0];
+                    a[2] &= keep[1];
+                    a[3] &= keep[1];
+                    S::mma(o[i], a, w[2 * kk][0], w[2 * kk + 1][0]);
+                    S::mma(o[i], a, w[2 * kk][1], w[2 * kk + 1][1]);
+                }
+            } else {
+                const uint32_t lane_at = item + (16 * kk + (lane_mat & 1) * 8 + lane_row) * 128;
+#pragma unroll
+                for (int i = 0; i < kTiles; i += 2) {
+                    uint32_t r[4];
+                    ldmatrix4_trans(r, lane_at + (i >> 3) * (kKeys * 128) + ((((i & 7) + (lane_mat >> 1)) ^ lane_row) << 4));
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t x = __byte_perm(r[2 * j] & keep[0], 0, 0x3120), y = __byte_perm(r[2 * j + 1] & keep[1], 0, 0x3120);
+                        const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y),
+                                               e4m3x2_to_f16x2(y >> 16)};
+                        S::mma(o[i + j], a, w[2 * kk][0], w[2 * kk + 1][0]);
+                        S::mma(o[i + j], a, w[2 * kk][1], w[2 * kk + 1][1]);
+                    }
+                }
+            }
+        }
+        release_item();
+
+        const bool ends = cp.unit + 1 == cp.row.units;
+        if (ends || !left) {
+            const uint32_t row = cp.request * p.head_rows + cp.head;
+            l += __shfl_xor_sync(~0u, l, 1);
+            l += __shfl_xor_sync(~0u, l, 2);
+            if (begun && ends) {
+                const float l0 = __shfl_sync(~0u, l, 8 * t), l1 = __shfl_sync(~0u, l, 8 * t + 4);
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i)
+                    store_tile<S>(p, row, i, lane, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]), l0, l1);
+                if (t == 0) store_lse<S>(p, row, g, m, l);
+            } else {
+                const int slot = 2 * warp + (begun ? 1 : 0);
+                float4 *to = p.warp_o + ((uint64_t)blockIdx.x * 2 * kWarps + slot) * kPart + lane;
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) to[32 * i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+                if (t == 0) s_ml[slot][g] = make_float2(m, l);
+                if (lane == 0) {
+                    s_row[slot] = row;
+                    s_flags[slot] = (begun ? 1u : 0u) | (ends ? 2u : 0u);
+                }
+            }
+            fresh = true;
+        }
+        advance<kKeys>(p, cp);
+    }
+    if (!alive) {
+        // a copy never arrived (reported in the error word): let the others land, bounded, before the CTA goes
+        while (taken < loaded) {
+            mbar_wait(bar + 8 * slot_out, phase, p.err, 200000000ll);
+            ++taken;
+            if (++slot_out == kItems) {
+                slot_out = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    // requests without keys
+    for (uint32_t r = blockIdx.x; r < p.requests; r += gridDim.x) {
+        if (row_of<kKeys>(p, r).units) continue;
+        for (uint32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kThreads)
+            store1(p.out, (uint64_t)r * p.q_heads * p.head_dim + i, p.out_dtype, 0.f);
+        if (p.lse)
+            for (uint32_t i = threadIdx.x; i < p.q_heads; i += kThreads) p.lse[(uint64_t)r * p.q_heads + i] = -INFINITY;
+    }
+    __syncthreads();
+
+    // ---- rows cut between warps, joined in order; what is still cut goes to the second kernel ----
+    uint4 meta = make_uint4(kNone, 0, 0, 0);
+    for (int i = 0; i < 2 * kWarps;) {
+        const uint32_t row = s_row[i];
+        if (row == kNone) {
+            ++i;
+            continue;
+        }
+        int end = i, last = i;
+        for (; end < 2 * kWarps && (s_row[end] == row || s_row[end] == kNone); ++end)
+            if (s_row[end] == row) last = end;
+        const bool begins = s_flags[i] & 1, ends = s_flags[last] & 2;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        for (int j = i; j <= last; ++j) {
+            if (s_row[j] != row) continue;
+            m0 = fmaxf(m0, s_ml[j][2 * t].x);
+            m1 = fmaxf(m1, s_ml[j][2 * t + 1].x);
+        }
+        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
+        for (int j = i; j <= last; ++j) {
+            if (s_row[j] != row) continue;
+            l0 = fmaf(s_ml[j][2 * t].y, exp2_approx(s_ml[j][2 * t].x - u0), l0);
+            l1 = fmaf(s_ml[j][2 * t + 1].y, exp2_approx(s_ml[j][2 * t + 1].x - u1), l1);
+        }
+        const int part = begins ? 1 : 0;
+        for (int tile = warp; tile < kTiles; tile += kWarps) {
+            float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j = i; j <= last; ++j) {
+                if (s_row[j] != row) continue;
+                const float4 x = p.warp_o[((uint64_t)blockIdx.x * 2 * kWarps + j) * kPart + 32 * tile + lane];
+                const float f0 = exp2_approx(s_ml[j][2 * t].x - u0), f1 = exp2_approx(s_ml[j][2 * t + 1].x - u1);
+                a.x = fmaf(x.x, f0, a.x);
+                a.y = fmaf(x.y, f1, a.y);
+                a.z = fmaf(x.z, f0, a.z);
+                a.w = fmaf(x.w, f1, a.w);
+            }
+            if (begins && ends) store_tile<S>(p, row, tile, lane, a, l0, l1);
+            else p.cta_o[((uint64_t)blockIdx.x * 2 + part) * kPart + 32 * tile + lane] = a;
+        }
+        if (warp == 0 && g == 0) {
+            if (begins && ends) {
+                store_lse<S>(p, row, 2 * t, m0, l0);
+                store_lse<S>(p, row, 2 * t + 1, m1, l1);
+            } else {
+                p.cta_ml[(blockIdx.x * 2 + part) * 8 + 2 * t] = make_float2(m0, l0);
+                p.cta_ml[(blockIdx.x * 2 + part) * 8 + 2 * t + 1] = make_float2(m1, l1);
+            }
+        }
+        if (!(begins && ends)) {
+            if (begins) meta.x = row;
+            else {
+                meta.y = ends ? 1u : 0u;
+                meta.z = 1u;
+            }
+        }
+        i = end;
+    }
+    if (threadIdx.x == 0) p.meta[blockIdx.x] = meta;
+}
+
+// Joins the rows that were cut between CTAs: block (c, tile) takes the row whose
+// first part is CTA c's tail, if there is one, through the head parts of the
+// following CTAs up to the one that ends it.
+template <int kDtype, int kWidth>
+__global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionParams p, uint32_t ctas) {
+    using S = Shape<kDtype, kWidth>;
+    constexpr int kTiles = kWidth / 16, kPart = kTiles * 32;
+    __shared__ uint32_t s_last;
+    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+    __shared__ float4 s_o[kWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
+    const uint32_t c = blockIdx.x, tile = blockIdx.y;
+    if (threadIdx.x == 0) s_last = kNone;
+    pdl_launch_dependents();
+    pdl_wait();
+    const uint32_t row = p.meta[c].x;
+    if (row == kNone) return;
+    __syncthreads();
+    for (uint32_t i = c + 1 + threadIdx.x; i < ctas; i += kThreads)
+        if (p.meta[i].z && p.meta[i].y) {
+            atomicMin(&s_last, i);
+            break;
+        }
+    __syncthreads();
+    const uint32_t last = min(s_last, ctas - 1), parts = last - c + 1;
+    // part 0 is CTA c's tail, part i the head of CTA c + i
+    auto at = [&](uint32_t i) { return (uint64_t)(c + i) * 2 + (i ? 0 : 1); };
+    float m = -INFINITY;
+    for (uint32_t i = threadIdx.x >> 3; i < parts; i += kThreads / 8) m = fmaxf(m, p.cta_ml[at(i) * 8 + (lane & 7)].x);
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
+    if (lane < 8) s_m[warp][lane] = m;
+    __syncthreads();
+    m = -INFINITY;
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][lane & 7]);
+    const float u = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    for (uint32_t i = threadIdx.x >> 3; i < parts; i += kThreads / 8) {
+        const float2 ml = p.cta_ml[at(i) * 8 + (lane & 7)];
+        l = fmaf(ml.y, exp2_approx(ml.x - u), l);
+    }
+    l += __shfl_xor_sync(~0u, l, 8);
+    l += __shfl_xor_sync(~0u, l, 16);
+    if (lane < 8) s_l[warp][lane] = l;
+    const float u0 = __shfl_sync(~0u, u, 2 * t), u1 = __shfl_sync(~0u, u, 2 * t + 1);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (uint32_t i = warp; i < parts; i += kWarps) {
+        const float4 x = p.cta_o[at(i) * kPart + 32 * tile + lane];
+        const float f0 = exp2_approx(p.cta_ml[at(i) * 8 + 2 * t].x - u0), f1 = exp2_approx(p.cta_ml[at(i) * 8 + 2 * t + 1].x - u1);
+        a.x = fmaf(x.x, f0, a.x);
+        a.y = fmaf(x.y, f1, a.y);
+        a.z = fmaf(x.z, f0, a.z);
+        a.w = fmaf(x.w, f1, a.w);
+    }
+    s_o[warp][lane] = a;
+    __syncthreads();
+    if (warp) return;
+    l = 0.f;
+    for (int w = 0; w < kWarps; ++w) l += s_l[w][lane & 7];
+    for (int w = 1; w < kWarps; ++w) {
+        a.x += s_o[w][lane].x;
+        a.y += s_o[w][lane].y;
+        a.z += s_o[w][lane].z;
+        a.w += s_o[w][lane].w;
+    }
+    store_tile<S>(p, row, tile, lane, a, __shfl_sync(~0u, l, 2 * t), __shfl_sync(~0u, l, 2 * t + 1));
+    if (tile == 0 && lane < 8) store_lse<S>(p, row, lane, m, l);
+}
+
+// ------------------------------------------------------------------ host ---
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+int encode_fn(EncodeFn *out) {
+    static EncodeFn fn = nullptr;
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!fn) {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
+        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr)
+            return fail(NINFER_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(e));
+        fn = reinterpret_cast<EncodeFn>(ptr);
+    }
+    *out = fn;
+    return NINFER_OK;
+}
+
+// The pool as {element, token, head, page}; boxes of 128 bytes x `box` tokens of
+// one head. Elements past head_dim, and pages outside the pool, read as zeros.
+int encode_pool(CUtensorMap *map, const ninfer_kv_cache *c, void *base, uint32_t box) {
+    EncodeFn fn;
+    const int st = encode_fn(&fn);
+    if (st) return st;
+    const uint64_t es = cache_dtype_size(c->dtype), row = (c->head_dim * es + 15) / 16 * 16;
+    const cuuint64_t dims[4] = {c->head_dim, c->page_size, c->kv_heads, c->pages};
+    const cuuint64_t strides[3] = {c->page_size > 1 ? c->token_stride * es : row, c->kv_heads > 1 ? c->head_stride * es : row,
+                                   c->pages > 1 ? c->page_stride * es : row};
+    const cuuint32_t boxes[4] = {(cuuint32_t)(128 / es), box, 1, 1}, ones[4] = {1, 1, 1, 1};
+    const CUtensorMapDataType type = c->dtype == NINFER_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                     : c->dtype == NINFER_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = fn(map, type, 4, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(NINFER_ERR_CUDA, "attention: tensor map encode failed (CUresult %d)", (int)r);
+    return NINFER_OK;
+}
+
+struct Instance {
+    void (*attention)(const AttentionParams), (*join)(const AttentionParams, uint32_t);
+    uint32_t width, keys;
+};
+
+template <int kDtype, int kWidth>
+Instance instance() {
+    return Instance{attention_kernel<kDtype, kWidth>, join_kernel<kDtype, kWidth>, kWidth, (uint32_t)Shape<kDtype, kWidth>::kKeys};
+}
+
+// Head widths are padded to 64, 128 or 256 elements, 8-bit ones to a whole 128-byte row (128 or 256).
+Instance instance_of(const ninfer_kv_cache *c) {
+    const bool narrow = c->head_dim <= 64, half = c->head_dim <= 128;
+    if (c->dtype == NINFER_E4M3) return half ? instance<NINFER_E4M3, 128>() : instance<NINFER_E4M3, 256>();
+    if (c->dtype == NINFER_F16)
+        return narrow ? instance<NINFER_F16, 64>() : half ? instance<NINFER_F16, 128>() : instance<NINFER_F16, 256>();
+    return narrow ? instance<NINFER_BF16, 64>() : half ? instance<NINFER_BF16, 128>() : instance<NINFER_BF16, 256>();
+}
+
+struct Layout {
+    uint64_t ml, cta_o, warp_o, bytes;      // offsets in the workspace
+};
+
+Layout layout(uint32_t ctas, uint32_t width) {
+    const uint64_t part = (uint64_t)width * 8 * sizeof(float);
+    Layout w;
+    w.ml = (uint64_t)ctas * sizeof(uint4);
+    w.cta_o = (w.ml + (uint64_t)ctas * 2 * 8 * sizeof(float2) + 255) / 256 * 256;
+    w.warp_o = w.cta_o + ctas * 2 * part;
+    w.bytes = w.warp_o + (uint64_t)ctas * 2 * kWarps * part;
+    return w;
 }
 
 int check_heads(const ninfer_kv_cache *cache, uint64_t requests, uint64_t q_heads) {
@@ -120,7 +781,10 @@ extern "C" int ninfer_kv_attention_workspace(const ninfer_kv_cache *cache, uint6
     if (!st) st = check_heads(cache, requests, q_heads);
     if (st) return st;
     if (!bytes) return fail(NINFER_ERR_INVALID_ARGUMENT, "attention workspace: NULL output");
-    *bytes = 0;
+    DeviceInfo d;
+    st = device_info(&d);
+    if (st) return st;
+    *bytes = layout(d.sms, instance_of(cache).width).bytes;
     return NINFER_OK;
 }
 
@@ -129,8 +793,8 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
                                    const int32_t *block_table, uint64_t table_pages, uint64_t table_stride,
                                    const int32_t *lengths, float scale, uint64_t window, void *out, int out_dtype,
                                    float *lse, void *workspace, uint64_t workspace_bytes, ninfer_stream stream) {
-    uint64_t need = 0;
-    int st = ninfer_kv_attention_workspace(cache, requests, q_heads, &need);
+    int st = check_cache(cache, "attention");
+    if (!st) st = check_heads(cache, requests, q_heads);
     if (st) return st;
     if (!q || !block_table || !lengths || !out)
         return fail(NINFER_ERR_INVALID_ARGUMENT, "attention: NULL q, block_table, lengths or out");
@@ -147,36 +811,57 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
         return fail(NINFER_ERR_ALIGNMENT, "attention: q, out and the strides of q must be 16-byte aligned");
     if (!aligned(block_table, 4) || !aligned(lengths, 4) || !aligned(lse, 4))
         return fail(NINFER_ERR_ALIGNMENT, "attention: block_table, lengths and lse must be 4-byte aligned");
-    if (need && (!workspace || workspace_bytes < need))
+    DeviceInfo d;
+    st = device_info(&d);
+    if (st) return st;
+    const Instance in = instance_of(cache);
+    const Layout w = layout(d.sms, in.width);
+    if (!workspace || workspace_bytes < w.bytes)
         return fail(NINFER_ERR_SIZE_MISMATCH, "attention: workspace of %llu bytes needed, %llu given",
-                    (unsigned long long)need, (unsigned long long)workspace_bytes);
-    if (need && !aligned(workspace, 256)) return fail(NINFER_ERR_ALIGNMENT, "attention: workspace must be 256-byte aligned");
+                    (unsigned long long)w.bytes, (unsigned long long)(workspace ? workspace_bytes : 0));
+    if (!aligned(workspace, 256)) return fail(NINFER_ERR_ALIGNMENT, "attention: workspace must be 256-byte aligned");
     AttentionParams p;
+    // a box lies in one page: the largest power of two that divides page_size, up to a unit's keys
+    uint32_t box = in.keys;
+    while (cache->page_size % box) box /= 2;
+    st = encode_pool(&p.k, cache, cache->k, box);
+    if (!st) st = encode_pool(&p.v, cache, cache->v, box);
+    if (!st) st = device_error_word(&p.err);
+    constexpr int kSmem = kRingBytes + 1024;
+    if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(in.attention), kSmem);
+    if (st) return st;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = q;
-    p.k = static_cast<const uint8_t *>(cache->k);
-    p.v = static_cast<const uint8_t *>(cache->v);
     p.table = block_table;
     p.lengths = lengths;
     p.out = out;
     p.lse = lse;
-    p.q_request = q_request_stride;
-    p.q_head = q_head_stride;
-    p.table_stride = table_stride;
-    p.page_stride = cache->page_stride;
-    p.token_stride = cache->token_stride;
-    p.head_stride = cache->head_stride;
-    p.window = window;
-    p.scale = scale * cache->k_scale;
+    p.meta = reinterpret_cast<uint4 *>(ws);
+    p.cta_ml = reinterpret_cast<float2 *>(ws + w.ml);
+    p.cta_o = reinterpret_cast<float4 *>(ws + w.cta_o);
+    p.warp_o = reinterpret_cast<float4 *>(ws + w.warp_o);
+    p.q_request = (int64_t)q_request_stride;
+    p.q_head = (int64_t)q_head_stride;
+    p.table_stride = (int64_t)table_stride;
+    p.scale = scale * cache->k_scale * 1.44269504088896f;
     p.v_scale = cache->v_scale;
+    p.requests = (uint32_t)requests;
+    p.run = (uint32_t)((requests + kThreads - 1) / kThreads);
     p.q_heads = (uint32_t)q_heads;
     p.group = (uint32_t)(q_heads / cache->kv_heads);
     p.head_dim = (uint32_t)cache->head_dim;
-    p.table_pages = (uint32_t)table_pages;
-    p.pages = (uint32_t)cache->pages;
+    p.tiles = FastDiv((p.group + 7) / 8);
+    p.head_rows = (uint32_t)cache->kv_heads * p.tiles.d;
+    p.heads = FastDiv(p.head_rows);
+    p.box = box;
+    p.most = (uint32_t)(table_pages * cache->page_size);
+    p.window = window < p.most ? (uint32_t)window : 0;
+    p.min_units = kWarps;
     p.page = FastDiv((uint32_t)cache->page_size);
     p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
-    p.dtype = cache->dtype;
-    return launch_dependent("attention", attention_kernel, dim3((unsigned)(requests * q_heads)), dim3(256), 0,
-                            (cudaStream_t)stream, p);
+    st = launch_dependent("attention", in.attention, dim3(d.sms), dim3(kThreads), kSmem, (cudaStream_t)stream, p);
+    if (st) return st;
+    return launch_dependent("attention join", in.join, dim3(d.sms, in.width / 16), dim3(kThreads), 0, (cudaStream_t)stream, p,
+                            (uint32_t)d.sms);
 }

@@ -122,7 +122,8 @@ int ninfer_kv_append(const void *k_new, const void *v_new, int src_dtype, uint64
  *   over the keys j of request r with max(0, n - window) <= j < n (window 0: all of them),
  *   n = lengths[r], the new token included (append it first), key j in page
  *   block_table[r][j / page_size]. A request without keys (n <= 0), or whose scores are
- *   all -infinity, gives zeros and lse -infinity. Cache entries outside the range are
+ *   all -infinity, gives zeros and lse -infinity. An infinite value among the keys' values
+ *   makes its element of the result infinite or NaN. Cache entries outside the range are
  *   never part of the result, whatever they hold. Lengths past table_pages * page_size are
  *   cut to it; table entries outside [0, pages) stand for a page of zeros.
  *   q: device, q_dtype f32, bf16 or f16, element e of head h of request r at
