@@ -41,7 +41,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kItems = 3;
 constexpr uint32_t kItemBytes = 8192;
 constexpr uint32_t kRingBytes = kWarps * kItems * kItemBytes;
-constexpr uint32_t kNone = 0xffffffffu;
+constexpr uint32_t kNone = 0xffffffffu, kRowKeys = 1024;
 
 struct AttentionParams {
     CUtensorMap k, v;                   // {element, token, head, page}
@@ -51,11 +51,12 @@ struct AttentionParams {
     float *lse;
     uint4 *meta;                        // per CTA: row of its tail, whether its head part ends a row, and has one
     float2 *cta_ml;                     // [CTA][2][8]: m, l
-    float4 *cta_o, *warp_o;             // [CTA][2] and [CTA][warp][2] sums, in fragment order
+    float4 *cta_o, *warp_o;             // [CTA][2] and [CTA][warp] sums, in fragment order
     int64_t q_request, q_head, table_stride;
     uint32_t *err;
     float scale, v_scale;               // scale: of scores, in log2
-    uint32_t requests, run, q_heads, group, head_dim, head_rows, box, window, most, min_units;
+    uint32_t requests, run, q_heads, group, head_dim, head_rows, box, window, most;
+    uint32_t by_row;                    // CTA c has row c, and no other: nothing is cut between CTAs
     FastDiv page, tiles, heads;         // tokens a page, 8-head tiles a key head, rows a request
     int q_dtype, out_dtype;
 };
@@ -176,13 +177,6 @@ __device__ __forceinline__ void advance(const AttentionParams &p, Cursor &c) {
     }
 }
 
-__device__ __forceinline__ float2 load2(const void *base, int64_t idx, int dtype) {
-    if (dtype == NINFER_F32) return *reinterpret_cast<const float2 *>(static_cast<const float *>(base) + idx);
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(base) + idx);
-    if (dtype == NINFER_BF16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&u));
-}
-
 // One value tile of a finished row: o / l in the output's type, for heads 2 t and 2 t + 1.
 template <class S>
 __device__ __forceinline__ void store_tile(const AttentionParams &p, uint32_t row, int tile, int lane, const float4 &o, float l0,
@@ -217,12 +211,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     constexpr int kKeys = S::kKeys, kSteps = S::kSteps, kTiles = kWidth / 16, kPart = kTiles * 32;
     extern __shared__ uint8_t ring_raw[];
     __shared__ __align__(8) uint64_t s_bar[kWarps][kItems];
-    __shared__ uint64_t s_sum[kWarps];
-    __shared__ uint32_t s_start[kWarps][3];                 // request, row of it, unit
+    __shared__ uint64_t s_sum[kWarps], s_upto[kThreads];
     __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
-    __shared__ float2 s_ml[2 * kWarps][8];
+    __shared__ float2 s_ml[2 * kWarps][8], s_total[2 * kWarps][8];
+    __shared__ float s_factor[2 * kWarps][8];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const uint32_t ring = ((smem_u32(ring_raw) + 1023) & ~1023u) + warp * (kItems * kItemBytes);
+    const uint32_t ring_skip = (1024 - (smem_u32(ring_raw) & 1023)) & 1023;
+    const uint32_t ring = smem_u32(ring_raw) + ring_skip + warp * (kItems * kItemBytes);
     const uint32_t bar = smem_u32(&s_bar[warp][0]);
     if (lane == 0)
         for (int i = 0; i < kItems; ++i) mbar_init(bar + 8 * i, 1);
@@ -236,95 +231,120 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     pdl_wait();
 
     // ---- this warp's part of the line ----
-    const uint32_t r0 = min(threadIdx.x * p.run, p.requests), r1 = min(r0 + p.run, p.requests);
-    uint64_t mine = 0;
-    for (uint32_t r = r0; r < r1; ++r) mine += row_of<kKeys>(p, r).units;
-    mine *= p.head_rows;
-    uint64_t upto = mine;
+    Cursor ld;
+    uint32_t left = 0;          // units of this warp
+    bool empties = false;       // whether any request has no keys
+    if (p.by_row) {
+        ld.request = p.heads.div(blockIdx.x);
+        ld.head = blockIdx.x - ld.request * p.head_rows;
+        ld.row = row_of<kKeys>(p, ld.request);
+        const uint32_t share = ld.row.units / kWarps, more = ld.row.units % kWarps;
+        ld.unit = warp * share + min((uint32_t)warp, more);
+        left = share + (warp < more);
+        empties = ld.row.units == 0 && ld.head == 0;
+    } else {
+        const uint32_t r0 = min(threadIdx.x * p.run, p.requests), r1 = min(r0 + p.run, p.requests);
+        uint64_t mine = 0;
+        for (uint32_t r = r0; r < r1; ++r) {
+            const uint32_t units = row_of<kKeys>(p, r).units;
+            mine += units;
+            empties |= units == 0;
+        }
+        mine *= p.head_rows;
+        uint64_t upto = mine;
 #pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        const uint64_t a = __shfl_up_sync(~0u, upto, s);
-        if (lane >= s) upto += a;
-    }
-    if (lane == 31) s_sum[warp] = upto;
-    __syncthreads();
-    uint64_t total = 0;
+        for (int s = 1; s < 32; s <<= 1) {
+            const uint64_t a = __shfl_up_sync(~0u, upto, s);
+            if (lane >= s) upto += a;
+        }
+        if (lane == 31) s_sum[warp] = upto;
+        empties = __syncthreads_or(empties);
+        uint64_t total = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) upto += s_sum[w];
-        total += s_sum[w];
-    }
-    const uint64_t before = upto - mine;
-    const uint64_t ctas = min((uint64_t)gridDim.x, (total + p.min_units - 1) / p.min_units);
-    const bool active = blockIdx.x < ctas;
-    const uint64_t c0 = active ? blockIdx.x * total / ctas : 0, c1 = active ? (blockIdx.x + 1) * total / ctas : 0;
-    if (before < c1 && upto > c0) {
-#pragma unroll 1
         for (int w = 0; w < kWarps; ++w) {
-            uint64_t at = c0 + w * (c1 - c0) / kWarps;
-            if (at < before || at >= upto) continue;
-            at -= before;
-            for (uint32_t r = r0; r < r1; ++r) {
-                const Row row = row_of<kKeys>(p, r);
-                const uint64_t n = (uint64_t)row.units * p.head_rows;
-                if (at < n) {
-                    s_start[w][0] = r;
-                    s_start[w][1] = (uint32_t)(at / row.units);
-                    s_start[w][2] = (uint32_t)(at % row.units);
-                    break;
-                }
-                at -= n;
+            if (w < warp) upto += s_sum[w];
+            total += s_sum[w];
+        }
+        s_upto[threadIdx.x] = upto;
+        // equal parts for the CTAs, of at least a unit a warp, and in them for the warps
+        const uint32_t ctas = (uint32_t)min((uint64_t)gridDim.x, (total + kWarps - 1) / kWarps);
+        uint64_t at = 0, n = 0;
+        if (blockIdx.x < ctas) {
+            const uint64_t share = total >> 32 ? total / ctas : (uint32_t)total / ctas;
+            const uint32_t more = (uint32_t)(total - share * ctas);
+            n = share + (blockIdx.x < more);
+            at = blockIdx.x * share + min(blockIdx.x, more);
+        }
+        const uint32_t more = (uint32_t)n % kWarps;
+        left = (uint32_t)(n / kWarps) + (warp < more);
+        at += warp * (n / kWarps) + min((uint32_t)warp, more);
+        __syncthreads();
+        if (left) {
+            // the first run of requests that ends past `at`, then the request in it
+            uint32_t run = 0;
+#pragma unroll
+            for (int k = kWarps - 1; k >= 0; --k) {
+                const uint32_t past = __ballot_sync(~0u, s_upto[32 * k + lane] > at);
+                if (past) run = 32 * k + __ffs(past) - 1;
             }
+            if (run) at -= s_upto[run - 1];
+            ld.request = run * p.run;
+            ld.row = row_of<kKeys>(p, ld.request);
+            for (uint64_t size; at >= (size = (uint64_t)ld.row.units * p.head_rows); ld.row = row_of<kKeys>(p, ++ld.request)) at -= size;
+            ld.head = at >> 32 ? (uint32_t)(at / ld.row.units) : (uint32_t)at / ld.row.units;
+            ld.unit = (uint32_t)(at - (uint64_t)ld.head * ld.row.units);
         }
     }
-    __syncthreads();
-    uint32_t left = (uint32_t)((warp + 1) * (c1 - c0) / kWarps - warp * (c1 - c0) / kWarps);
 
-    // ---- the ring ----
-    Cursor ld, cp;
-    ld.request = s_start[warp][0];
-    ld.head = s_start[warp][1];
-    ld.unit = s_start[warp][2];
-    if (left) ld.row = row_of<kKeys>(p, ld.request);
-    cp = ld;
-    uint32_t to_load = 2 * left, loaded = 0, taken = 0;     // items
-    uint32_t slot_in = 0, slot_out = 0, phase = 0;
-    int32_t page[2], token[2];                              // of this lane's pieces of the unit being loaded
+    // ---- the ring: keys and values of the units in turn ----
+    Cursor cp = ld;
+    uint32_t keys_due = left, values_due = left, slot_in = 0, slot_out = 0, phase = 0, in_flight = 0;
+    int32_t page[2], token[2];              // of this lane's pieces of the unit that is loaded next
     const uint32_t pieces = kKeys / p.box;
-    auto load_item = [&] {
-        const bool values = loaded & 1;
+    uint32_t piece_lo = 0, piece_hi = 0;    // its pieces that hold keys of the request
+    auto find_pages = [&] {
         const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys;
-        const uint32_t lo = ld.row.from > base ? (ld.row.from - base) / p.box : 0u;
-        const uint32_t hi = min(pieces, (ld.row.end - base + p.box - 1) / p.box);
-        if (!values) {
+        piece_lo = ld.row.from > base ? (ld.row.from - base) / p.box : 0u;
+        piece_hi = min(pieces, (ld.row.end - base + p.box - 1) / p.box);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const uint32_t b = lane + 32 * i;
-                if (b < lo || b >= hi) continue;
-                const uint32_t key = base + b * p.box, pg = p.page.div(key);
-                token[i] = (int32_t)(key - pg * p.page.d);
-                page[i] = p.table[(int64_t)ld.request * p.table_stride + pg];
-            }
+        for (int i = 0; i < 2; ++i) {
+            const uint32_t b = lane + 32 * i;
+            if (b < piece_lo || b >= piece_hi) continue;
+            const uint32_t key = base + b * p.box, pg = p.page.div(key);
+            token[i] = (int32_t)(key - pg * p.page.d);
+            page[i] = p.table[(int64_t)ld.request * p.table_stride + pg];
         }
-        const uint32_t b = bar + 8 * slot_in;
-        if (lane == 0) mbar_arrive_expect_tx(b, (hi - lo) * p.box * (kWidth * S::kEs));
+    };
+    auto load_item = [&](const CUtensorMap *map) {
+        const uint32_t b = bar + 8 * slot_in, to = ring + slot_in * kItemBytes;
+        if (lane == 0) mbar_arrive_expect_tx(b, (piece_hi - piece_lo) * p.box * (kWidth * S::kEs));
         __syncwarp();
         const int head = (int)p.tiles.div(ld.head);
-        const CUtensorMap *map = values ? &p.v : &p.k;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const uint32_t q = lane + 32 * i;
-            if (q < lo || q >= hi) continue;
+            if (q < piece_lo || q >= piece_hi) continue;
 #pragma unroll
             for (int c = 0; c < S::kChunks; ++c)
-                tma_load_4d(ring + slot_in * kItemBytes + c * (kKeys * 128) + q * p.box * 128, map, c * (128 / S::kEs), token[i],
-                            head, page[i], b);
+                tma_load_4d(to + c * (kKeys * 128) + q * p.box * 128, map, c * (128 / S::kEs), token[i], head, page[i], b);
         }
-        if (values) advance<kKeys>(p, ld);
-        ++loaded;
+        ++in_flight;
         slot_in = slot_in == kItems - 1 ? 0 : slot_in + 1;
     };
-    for (int i = 0; i < kItems && loaded < to_load; ++i) load_item();
+    auto load_keys = [&] {
+        if (!keys_due) return;
+        --keys_due;
+        load_item(&p.k);
+    };
+    auto load_values = [&] {
+        if (!values_due) return;
+        load_item(&p.v);
+        if (--values_due) {
+            advance<kKeys>(p, ld);
+            find_pages();       // read early: the next unit's keys are asked for half a unit later
+        }
+    };
+    if (left) find_pages();
 
     bool alive = true;
     auto wait_item = [&] {
@@ -333,18 +353,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     auto release_item = [&] {
         __syncwarp();
-        ++taken;
+        --in_flight;
         if (++slot_out == kItems) {
             slot_out = 0;
             phase ^= 1;
         }
-        if (loaded < to_load) load_item();
     };
 
     // ---- the units ----
     uint32_t qa[kSteps][4];
     float o[kTiles][4], m = -INFINITY, l = 0.f, sc = 0.f;
-    bool fresh = true, begun = false;       // a new row's queries are due; the row began in this part
+    bool fresh = true, begun = false, primed = false;   // a new row's queries are due; it began in this part; loads run
     const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
     while (left && alive) {
         --left;
@@ -357,25 +376,45 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             const uint32_t kvh = p.tiles.div(cp.head), h = (cp.head - kvh * p.tiles.d) * 8 + g;
             const int64_t at = (int64_t)cp.request * p.q_request + (int64_t)(kvh * p.group + h) * p.q_head;
+            // all of a lane's loads first, then the first unit's copies, then the conversions
             float2 x[kSteps][2];
-            float top = 0.f;
+            const bool wide = p.q_dtype == NINFER_F32;
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const uint32_t e = 16 * i + (S::kBytes8 ? 4 * t + 2 * j : 2 * t + 8 * j);
-                    x[i][j] = h < p.group && e < p.head_dim ? load2(p.q, at + e, p.q_dtype) : make_float2(0.f, 0.f);
+                    const bool on = h < p.group && e < p.head_dim;
+                    x[i][j] = make_float2(0.f, 0.f);
+                    if (on && wide) x[i][j] = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.q) + at + e);
+                    if (on && !wide)
+                        x[i][j].x = __uint_as_float(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) + at + e));
+                }
+            if (!primed) {
+                load_keys();
+                load_values();
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    if (!wide) {
+                        const uint32_t u = __float_as_uint(x[i][j].x);
+                        x[i][j] = p.q_dtype == NINFER_BF16 ? make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u))
+                                                           : __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                    }
                     top = fmaxf(top, fmaxf(fabsf(x[i][j].x), fabsf(x[i][j].y)));
                 }
             sc = p.scale;
             float down = 1.f;
             if (!S::kBf16) {
-                // binary16 operands: a power of two brings the head's largest element to [1, 2)
+                // binary16 operands: a power of two brings the head's largest element to about 1
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                const int e = top > 0.f && top < INFINITY ? max(ilogbf(top), -100) : 0;
-                down = ldexpf(1.f, -e);
-                sc = ldexpf(sc, e);
+                const int e = top > 0.f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 27), 253) : 127;
+                down = __uint_as_float((uint32_t)(254 - e) << 23);
+                sc *= __uint_as_float((uint32_t)e << 23);
             }
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
@@ -385,6 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     S::split(a, b, qa[i][2 * j], qa[i][2 * j + 1]);
                     if (isinf(a) || isinf(b)) qa[i][2 * j + 1] = 0;     // no remainder: inf - inf
                 }
+            if (!primed) load_keys();
+            primed = true;
         }
         const uint32_t base = (cp.row.from / kKeys + cp.unit) * kKeys;
         const bool edge = base < cp.row.from || base + kKeys > cp.row.end;
@@ -425,6 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
         }
         release_item();
+        load_values();      // of the next unit
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < S::kScoreTiles; ++i)
@@ -507,6 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
         }
         release_item();
+        load_keys();        // of the unit after that
 
         const bool ends = cp.unit + 1 == cp.row.units;
         if (ends || !left) {
@@ -521,13 +564,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 if (t == 0) store_lse<S>(p, row, g, m, l);
             } else {
                 const int slot = 2 * warp + (begun ? 1 : 0);
-                float4 *to = p.warp_o + ((uint64_t)blockIdx.x * 2 * kWarps + slot) * kPart + lane;
+                // at the end of the warp's part its ring is free, and holds the sums until they are joined
+                float4 *to = left ? p.warp_o + ((uint64_t)blockIdx.x * kWarps + warp) * kPart
+                                  : reinterpret_cast<float4 *>(ring_raw + ring_skip + warp * (kItems * kItemBytes)) + (slot & 1) * kPart;
+                to += lane;
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) to[32 * i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
                 if (t == 0) s_ml[slot][g] = make_float2(m, l);
                 if (lane == 0) {
                     s_row[slot] = row;
-                    s_flags[slot] = (begun ? 1u : 0u) | (ends ? 2u : 0u);
+                    s_flags[slot] = (begun ? 1u : 0u) | (ends ? 2u : 0u) | (left ? 4u : 0u);
                 }
             }
             fresh = true;
@@ -536,26 +582,44 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     if (!alive) {
         // a copy never arrived (reported in the error word): let the others land, bounded, before the CTA goes
-        while (taken < loaded) {
+        for (; in_flight; --in_flight) {
             mbar_wait(bar + 8 * slot_out, phase, p.err, 200000000ll);
-            ++taken;
             if (++slot_out == kItems) {
                 slot_out = 0;
                 phase ^= 1;
             }
         }
     }
-    // requests without keys
-    for (uint32_t r = blockIdx.x; r < p.requests; r += gridDim.x) {
-        if (row_of<kKeys>(p, r).units) continue;
-        for (uint32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kThreads)
-            store1(p.out, (uint64_t)r * p.q_heads * p.head_dim + i, p.out_dtype, 0.f);
-        if (p.lse)
-            for (uint32_t i = threadIdx.x; i < p.q_heads; i += kThreads) p.lse[(uint64_t)r * p.q_heads + i] = -INFINITY;
+    if (empties) {
+        // requests without keys: by_row CTAs look at their own, others share them out
+        const uint32_t step = p.by_row ? p.requests : gridDim.x;
+        for (uint32_t r = p.by_row ? p.heads.div(blockIdx.x) : blockIdx.x; r < p.requests; r += step) {
+            if (row_of<kKeys>(p, r).units) continue;
+            for (uint32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kThreads)
+                store1(p.out, (uint64_t)r * p.q_heads * p.head_dim + i, p.out_dtype, 0.f);
+            if (p.lse)
+                for (uint32_t i = threadIdx.x; i < p.q_heads; i += kThreads) p.lse[(uint64_t)r * p.q_heads + i] = -INFINITY;
+        }
     }
     __syncthreads();
 
     // ---- rows cut between warps, joined in order; what is still cut goes to the second kernel ----
+    if (threadIdx.x < 16 * kWarps) {
+        const uint32_t j = threadIdx.x >> 3, h = threadIdx.x & 7, row = s_row[j];
+        if (row != kNone) {
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * kWarps; ++i)
+                if (s_row[i] == row) top = fmaxf(top, s_ml[i][h].x);
+            const float u = top == -INFINITY ? 0.f : top;
+#pragma unroll
+            for (int i = 0; i < 2 * kWarps; ++i)
+                if (s_row[i] == row) sum = fmaf(s_ml[i][h].y, exp2_approx(s_ml[i][h].x - u), sum);
+            s_total[j][h] = make_float2(top, sum);
+            s_factor[j][h] = exp2_approx(s_ml[j][h].x - u);
+        }
+    }
+    __syncthreads();
     uint4 meta = make_uint4(kNone, 0, 0, 0);
     for (int i = 0; i < 2 * kWarps;) {
         const uint32_t row = s_row[i];
@@ -566,44 +630,30 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         int end = i, last = i;
         for (; end < 2 * kWarps && (s_row[end] == row || s_row[end] == kNone); ++end)
             if (s_row[end] == row) last = end;
-        const bool begins = s_flags[i] & 1, ends = s_flags[last] & 2;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-        for (int j = i; j <= last; ++j) {
-            if (s_row[j] != row) continue;
-            m0 = fmaxf(m0, s_ml[j][2 * t].x);
-            m1 = fmaxf(m1, s_ml[j][2 * t + 1].x);
-        }
-        const float u0 = m0 == -INFINITY ? 0.f : m0, u1 = m1 == -INFINITY ? 0.f : m1;
-        for (int j = i; j <= last; ++j) {
-            if (s_row[j] != row) continue;
-            l0 = fmaf(s_ml[j][2 * t].y, exp2_approx(s_ml[j][2 * t].x - u0), l0);
-            l1 = fmaf(s_ml[j][2 * t + 1].y, exp2_approx(s_ml[j][2 * t + 1].x - u1), l1);
-        }
-        const int part = begins ? 1 : 0;
+        const bool begins = s_flags[i] & 1, ends = s_flags[last] & 2, whole = begins && ends;
+        const uint64_t part = (uint64_t)blockIdx.x * 2 + (begins ? 1 : 0);
         for (int tile = warp; tile < kTiles; tile += kWarps) {
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int j = i; j <= last; ++j) {
                 if (s_row[j] != row) continue;
-                const float4 x = p.warp_o[((uint64_t)blockIdx.x * 2 * kWarps + j) * kPart + 32 * tile + lane];
-                const float f0 = exp2_approx(s_ml[j][2 * t].x - u0), f1 = exp2_approx(s_ml[j][2 * t + 1].x - u1);
+                const float4 *from = s_flags[j] & 4 ? p.warp_o + ((uint64_t)blockIdx.x * kWarps + (j >> 1)) * kPart
+                                                    : reinterpret_cast<const float4 *>(ring_raw + ring_skip + (j >> 1) * (kItems * kItemBytes)) + (j & 1) * kPart;
+                const float4 x = from[32 * tile + lane];
+                const float f0 = s_factor[j][2 * t], f1 = s_factor[j][2 * t + 1];
                 a.x = fmaf(x.x, f0, a.x);
                 a.y = fmaf(x.y, f1, a.y);
                 a.z = fmaf(x.z, f0, a.z);
                 a.w = fmaf(x.w, f1, a.w);
             }
-            if (begins && ends) store_tile<S>(p, row, tile, lane, a, l0, l1);
-            else p.cta_o[((uint64_t)blockIdx.x * 2 + part) * kPart + 32 * tile + lane] = a;
+            if (whole) store_tile<S>(p, row, tile, lane, a, s_total[i][2 * t].y, s_total[i][2 * t + 1].y);
+            else p.cta_o[part * kPart + 32 * tile + lane] = a;
         }
-        if (warp == 0 && g == 0) {
-            if (begins && ends) {
-                store_lse<S>(p, row, 2 * t, m0, l0);
-                store_lse<S>(p, row, 2 * t + 1, m1, l1);
-            } else {
-                p.cta_ml[(blockIdx.x * 2 + part) * 8 + 2 * t] = make_float2(m0, l0);
-                p.cta_ml[(blockIdx.x * 2 + part) * 8 + 2 * t + 1] = make_float2(m1, l1);
-            }
+        if (warp == 0 && lane < 8) {
+            const float2 ml = s_total[i][lane];
+            if (whole) store_lse<S>(p, row, lane, ml.x, ml.y);
+            else p.cta_ml[part * 8 + lane] = ml;
         }
-        if (!(begins && ends)) {
+        if (!whole) {
             if (begins) meta.x = row;
             else {
                 meta.y = ends ? 1u : 0u;
@@ -612,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         i = end;
     }
-    if (threadIdx.x == 0) p.meta[blockIdx.x] = meta;
+    if (threadIdx.x == 0 && !p.by_row) p.meta[blockIdx.x] = meta;
 }
 
 // Joins the rows that were cut between CTAs: block (c, tile) takes the row whose
@@ -623,66 +673,55 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     using S = Shape<kDtype, kWidth>;
     constexpr int kTiles = kWidth / 16, kPart = kTiles * 32;
     __shared__ uint32_t s_last;
-    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
-    __shared__ float4 s_o[kWarps][32];
+    __shared__ float4 s_ml[kWarps][4], s_o[kWarps][32];     // m and l of heads 2 t and 2 t + 1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
     const uint32_t c = blockIdx.x, tile = blockIdx.y;
-    if (threadIdx.x == 0) s_last = kNone;
+    if (threadIdx.x == 0) s_last = ctas - 1;
     pdl_launch_dependents();
     pdl_wait();
     const uint32_t row = p.meta[c].x;
-    if (row == kNone) return;
     __syncthreads();
-    for (uint32_t i = c + 1 + threadIdx.x; i < ctas; i += kThreads)
-        if (p.meta[i].z && p.meta[i].y) {
+    for (uint32_t i = c + 1 + threadIdx.x; i < ctas; i += kThreads) {
+        const uint4 meta = p.meta[i];
+        if (meta.z && meta.y) {
             atomicMin(&s_last, i);
             break;
         }
-    __syncthreads();
-    const uint32_t last = min(s_last, ctas - 1), parts = last - c + 1;
-    // part 0 is CTA c's tail, part i the head of CTA c + i
-    auto at = [&](uint32_t i) { return (uint64_t)(c + i) * 2 + (i ? 0 : 1); };
-    float m = -INFINITY;
-    for (uint32_t i = threadIdx.x >> 3; i < parts; i += kThreads / 8) m = fmaxf(m, p.cta_ml[at(i) * 8 + (lane & 7)].x);
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, 16));
-    if (lane < 8) s_m[warp][lane] = m;
-    __syncthreads();
-    m = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, s_m[w][lane & 7]);
-    const float u = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (uint32_t i = threadIdx.x >> 3; i < parts; i += kThreads / 8) {
-        const float2 ml = p.cta_ml[at(i) * 8 + (lane & 7)];
-        l = fmaf(ml.y, exp2_approx(ml.x - u), l);
     }
-    l += __shfl_xor_sync(~0u, l, 8);
-    l += __shfl_xor_sync(~0u, l, 16);
-    if (lane < 8) s_l[warp][lane] = l;
-    const float u0 = __shfl_sync(~0u, u, 2 * t), u1 = __shfl_sync(~0u, u, 2 * t + 1);
+    if (row == kNone) return;
+    __syncthreads();
+    // part 0 is CTA c's tail, part i the head of CTA c + i; each warp joins every eighth, then the warps
+    const uint32_t parts = s_last - c + 1;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto join = [&](float4 ml, float4 x) {          // ml: m and l of the two heads
+        const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.z);
+        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+        const float f0 = exp2_approx(m0 - u0), f1 = exp2_approx(m1 - u1), g0 = exp2_approx(ml.x - u0), g1 = exp2_approx(ml.z - u1);
+        l0 = l0 * f0 + ml.y * g0;
+        l1 = l1 * f1 + ml.w * g1;
+        a.x = a.x * f0 + x.x * g0;
+        a.y = a.y * f1 + x.y * g1;
+        a.z = a.z * f0 + x.z * g0;
+        a.w = a.w * f1 + x.w * g1;
+        m0 = n0;
+        m1 = n1;
+    };
 #pragma unroll 4
     for (uint32_t i = warp; i < parts; i += kWarps) {
-        const float4 x = p.cta_o[at(i) * kPart + 32 * tile + lane];
-        const float f0 = exp2_approx(p.cta_ml[at(i) * 8 + 2 * t].x - u0), f1 = exp2_approx(p.cta_ml[at(i) * 8 + 2 * t + 1].x - u1);
-        a.x = fmaf(x.x, f0, a.x);
-        a.y = fmaf(x.y, f1, a.y);
-        a.z = fmaf(x.z, f0, a.z);
-        a.w = fmaf(x.w, f1, a.w);
+        const uint64_t at = (uint64_t)(c + i) * 2 + (i ? 0 : 1);
+        join(reinterpret_cast<const float4 *>(p.cta_ml)[at * 4 + t], p.cta_o[at * kPart + 32 * tile + lane]);
     }
+    if (lane < 4) s_ml[warp][lane] = make_float4(m0, l0, m1, l1);
     s_o[warp][lane] = a;
     __syncthreads();
     if (warp) return;
-    l = 0.f;
-    for (int w = 0; w < kWarps; ++w) l += s_l[w][lane & 7];
-    for (int w = 1; w < kWarps; ++w) {
-        a.x += s_o[w][lane].x;
-        a.y += s_o[w][lane].y;
-        a.z += s_o[w][lane].z;
-        a.w += s_o[w][lane].w;
+    for (uint32_t w = 1; w < min(parts, (uint32_t)kWarps); ++w) join(s_ml[w][t], s_o[w][lane]);
+    store_tile<S>(p, row, tile, lane, a, l0, l1);
+    if (tile == 0 && lane < 4) {
+        store_lse<S>(p, row, 2 * t, m0, l0);
+        store_lse<S>(p, row, 2 * t + 1, m1, l1);
     }
-    store_tile<S>(p, row, tile, lane, a, __shfl_sync(~0u, l, 2 * t), __shfl_sync(~0u, l, 2 * t + 1));
-    if (tile == 0 && lane < 8) store_lse<S>(p, row, lane, m, l);
 }
 
 // ------------------------------------------------------------------ host ---
@@ -755,7 +794,7 @@ Layout layout(uint32_t ctas, uint32_t width) {
     w.ml = (uint64_t)ctas * sizeof(uint4);
     w.cta_o = (w.ml + (uint64_t)ctas * 2 * 8 * sizeof(float2) + 255) / 256 * 256;
     w.warp_o = w.cta_o + ctas * 2 * part;
-    w.bytes = w.warp_o + (uint64_t)ctas * 2 * kWarps * part;
+    w.bytes = w.warp_o + (uint64_t)ctas * kWarps * part;
     return w;
 }
 
@@ -856,12 +895,15 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     p.box = box;
     p.most = (uint32_t)(table_pages * cache->page_size);
     p.window = window < p.most ? (uint32_t)window : 0;
-    p.min_units = kWarps;
     p.page = FastDiv((uint32_t)cache->page_size);
     p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
-    st = launch_dependent("attention", in.attention, dim3(d.sms), dim3(kThreads), kSmem, (cudaStream_t)stream, p);
-    if (st) return st;
+    // Few and short rows: a CTA each, no schedule and no second kernel.
+    const uint64_t rows = requests * p.head_rows;
+    p.by_row = rows <= (uint64_t)d.sms && p.most <= kRowKeys;
+    st = launch_dependent("attention", in.attention, dim3(p.by_row ? (unsigned)rows : d.sms), dim3(kThreads), kSmem,
+                          (cudaStream_t)stream, p);
+    if (st || p.by_row) return st;
     return launch_dependent("attention join", in.join, dim3(d.sms, in.width / 16), dim3(kThreads), 0, (cudaStream_t)stream, p,
                             (uint32_t)d.sms);
 }
