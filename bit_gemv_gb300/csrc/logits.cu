@@ -2,10 +2,17 @@
 // on the logits of the output head.
 //
 // One pass over the logits (read once, written once): HBM bounds a batch,
-// latency a single row. A CTA owns a slice of one row's tokens. It first
-// enters the row's history into a table of counts in shared memory, one word a
-// token of its slice (bit 31: seen at all, the rest: how often after the
-// prompt), and the biases into a second table, then streams the slice through.
+// latency a single row. A CTA owns a slice of one row's tokens and keeps a
+// table of them in shared memory, one entry a token: how often it was answered,
+// whether it was seen in the prompt, whether it has a bias; the slice's mask words
+// stand behind it. It asks for its first logits, enters the row's history, biases and
+// mask while they are under way, and streams the slice through: four tokens with empty entries pass as they
+// are. Tokens with a bias are left out there and done one by one from the list,
+// so that the biases need no table of their own.
+//
+// Slices. Every CTA of a row reads the row's whole history, so slices are as large
+// as the table of a third of an SM allows, and as many as fill the SMs once: 64
+// rows are 7 slices of about 35,500 tokens each.
 #include <cmath>
 
 #include "decode.cuh"
@@ -14,9 +21,10 @@
 namespace ninfer {
 namespace {
 
-constexpr uint32_t kSlice = 8192;       // tokens of a CTA: 64 KB of tables
-constexpr int kThreads = 512;
-constexpr uint32_t kSeen = 0x80000000u;
+constexpr int kThreads = 384, kResident = 3;        // CTAs an SM
+constexpr uint32_t kSmemBytes = 76800;              // of a CTA: three fit an SM
+constexpr uint32_t kMostNarrow = 36096, kMostWide = 18560;      // tokens of a slice: (16 or 32) + 1 bits each
+constexpr uint32_t kLeast = 2048;                   // tokens of a slice: a 16-byte load a thread
 
 struct LogitsParams {
     const void *x;
@@ -24,67 +32,186 @@ struct LogitsParams {
     uint64_t x_stride, out_stride;
     ninfer_logits_controls c;
     int32_t *status;
-    uint32_t vocab, slices;
+    uint32_t vocab, slices, slice, mask_at;     // mask_at: word of shared memory where the mask words begin
     int dtype;
 };
 
-__global__ void __launch_bounds__(kThreads) logits_kernel(const LogitsParams p) {
-    extern __shared__ __align__(16) uint32_t tables[];
-    uint32_t *count = tables;
-    float *bias = reinterpret_cast<float *>(tables + kSlice);
+// Table entries. Histories below 2^14 tokens take 16 bits a token, longer ones 32.
+template <bool kWide>
+struct Entry;
+template <>
+struct Entry<false> {
+    using Word = uint16_t;
+    static constexpr uint32_t kPrompt = 0x8000u, kBias = 0x4000u, kCount = 0x3fffu;
+    static __device__ __forceinline__ void set(uint32_t *table, uint32_t i, uint32_t flag) { atomicOr(table + (i >> 1), flag << (16 * (i & 1))); }
+    static __device__ __forceinline__ void add(uint32_t *table, uint32_t i) { atomicAdd(table + (i >> 1), 1u << (16 * (i & 1))); }
+};
+template <>
+struct Entry<true> {
+    using Word = uint32_t;
+    static constexpr uint32_t kPrompt = 0x80000000u, kBias = 0x40000000u, kCount = 0x3fffffffu;
+    static __device__ __forceinline__ void set(uint32_t *table, uint32_t i, uint32_t flag) { atomicOr(table + i, flag); }
+    static __device__ __forceinline__ void add(uint32_t *table, uint32_t i) { atomicAdd(table + i, 1u); }
+};
+
+template <int kDtype>
+__device__ __forceinline__ float value(uint32_t w, int half) {
+    if (kDtype == NINFER_F32) return __uint_as_float(w);
+    if (kDtype == NINFER_BF16) return __uint_as_float(half ? w & 0xffff0000u : w << 16);
+    return __half2float(__ushort_as_half((uint16_t)(half ? w >> 16 : w & 0xffff)));
+}
+
+template <int kDtype, bool kWide>
+__global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __grid_constant__ LogitsParams p) {
+    using E = Entry<kWide>;
+    constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs, kAhead = 4;
+    extern __shared__ __align__(16) uint32_t table[];
+    const uint32_t tid = threadIdx.x, row = blockIdx.x / p.slices, first = blockIdx.x % p.slices * p.slice;
+    const uint32_t size = min(p.slice, p.vocab - first);
+    for (uint32_t i = tid; i * 16 < size * (uint32_t)sizeof(typename E::Word); i += kThreads)
+        reinterpret_cast<uint4 *>(table)[i] = make_uint4(0, 0, 0, 0);
     pdl_launch_dependents();
     pdl_wait();
-    const uint32_t tid = threadIdx.x, row = blockIdx.x / p.slices;
-    const uint32_t first = blockIdx.x % p.slices * kSlice, size = min(kSlice, p.vocab - first);
-    for (uint32_t i = tid; i < kSlice; i += kThreads) {
-        count[i] = 0;
-        bias[i] = 0.f;
-    }
-    __syncthreads();
-    int bad = 0;
-    if (p.c.history) {
-        const int64_t most = (int64_t)p.c.history_stride;
-        const int64_t n = min((int64_t)max(p.c.history_lengths[row], 0), most);
-        const int64_t told = p.c.prompt_lengths ? p.c.prompt_lengths[row] : 0;
-        const int32_t *h = p.c.history + row * p.c.history_stride;
-        for (int64_t i = tid; i < n; i += kThreads) {
-            const uint32_t v = (uint32_t)h[i];
-            if (v >= p.vocab) bad |= NINFER_LOGITS_BAD_TOKEN;
-            if (v - first < size) {
-                atomicOr(count + (v - first), kSeen);
-                if (i >= told) atomicAdd(count + (v - first), 1u);
-            }
-        }
-    }
+    const uint8_t *x = static_cast<const uint8_t *>(p.x) + (row * p.x_stride + first) * kEs;
+    uint8_t *out = static_cast<uint8_t *>(p.out) + (row * p.out_stride + first) * kEs;
+    // the row's numbers, all asked for at once
+    int32_t n = 0, told = 0, b0 = 0, b1 = 0, mask_row = -1;
+    float rep = 1.f, pres = 0.f, freq = 0.f;
+    if (p.c.history) n = p.c.history_lengths[row];
+    if (p.c.prompt_lengths) told = p.c.prompt_lengths[row];
     if (p.c.bias_ids) {
-        const int64_t all = (int64_t)p.c.bias_count;
-        const int64_t b0 = max((int64_t)p.c.bias_offsets[row], (int64_t)0), b1 = min((int64_t)p.c.bias_offsets[row + 1], all);
-        for (int64_t i = b0 + tid; i < b1; i += kThreads) {
-            const uint32_t v = (uint32_t)p.c.bias_ids[i];
-            if (v >= p.vocab) bad |= NINFER_LOGITS_BAD_TOKEN;
-            if (v - first < size) bias[v - first] = p.c.bias_values[i];
+        b0 = p.c.bias_offsets[row];
+        b1 = p.c.bias_offsets[row + 1];
+    }
+    if (p.c.mask) mask_row = p.c.mask_rows ? p.c.mask_rows[row] : (int32_t)row;
+    if (p.c.repetition) rep = p.c.repetition[row];
+    if (p.c.presence) pres = p.c.presence[row];
+    if (p.c.frequency) freq = p.c.frequency[row];
+    // rows on 16-byte boundaries go in vectors, others (and the last few tokens) one by one
+    const uint32_t vecs = (p.x_stride * kEs) % 16 == 0 && (p.out_stride * kEs) % 16 == 0 ? size / kVec : 0;
+    uint4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (tid + k * kThreads < vecs) ahead[k] = reinterpret_cast<const uint4 *>(x)[tid + k * kThreads];
+    __syncthreads();            // the table is empty
+    int bad = 0;
+    n = min(max(n, 0), (int32_t)p.c.history_stride);
+    b0 = max(b0, 0);
+    b1 = min(b1, (int32_t)p.c.bias_count);
+    if (mask_row >= 0 && (uint64_t)mask_row >= p.c.mask_row_count) {
+        bad = NINFER_LOGITS_BAD_TOKEN;
+        mask_row = -1;
+    }
+    const int32_t *h = p.c.history + row * p.c.history_stride;
+    for (int32_t i0 = tid; i0 < n; i0 += 8 * kThreads) {
+        uint32_t v[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kThreads < n) v[k] = (uint32_t)h[i0 + k * kThreads];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int32_t i = i0 + k * kThreads;
+            if (i >= n) continue;
+            if (v[k] >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
+            const uint32_t at = v[k] - first;
+            if (at >= size) continue;
+            if (i < told) E::set(table, at, E::kPrompt);
+            else E::add(table, at);
         }
     }
-    __syncthreads();
-    const float rep = p.c.repetition ? p.c.repetition[row] : 1.f, pres = p.c.presence ? p.c.presence[row] : 0.f;
-    const float freq = p.c.frequency ? p.c.frequency[row] : 0.f;
-    const uint32_t *mask = nullptr;
-    if (p.c.mask) {
-        const int64_t m = p.c.mask_rows ? (int64_t)p.c.mask_rows[row] : (int64_t)row;
-        if (m >= (int64_t)p.c.mask_row_count) bad |= NINFER_LOGITS_BAD_TOKEN;
-        else if (m >= 0) mask = p.c.mask + m * p.c.mask_stride;
+    for (int32_t i = b0 + tid; i < b1; i += kThreads) {
+        const uint32_t v = (uint32_t)p.c.bias_ids[i];
+        if (v >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
+        if (v - first < size) E::set(table, v - first, E::kBias);
     }
-    for (uint32_t i = tid; i < size; i += kThreads) {
-        float x = load1(p.x, row * p.x_stride + first + i, p.dtype);
-        const uint32_t c = count[i];
-        if (c) x = x > 0.f ? __fdiv_rn(x, rep) : x * rep;
-        if (c & ~kSeen) x -= freq * (float)(c & ~kSeen) + pres;
-        x += bias[i];
-        const uint32_t v = first + i;
-        if (mask && !(mask[v >> 5] >> (v & 31) & 1)) x = -INFINITY;
-        store1(p.out, row * p.out_stride + v, p.dtype, x);
+    uint32_t *mask = table + p.mask_at;
+    if (mask_row >= 0) {
+        const uint32_t *from = p.c.mask + mask_row * p.c.mask_stride + (first >> 5);
+        for (uint32_t i = tid; i * 32 < size; i += kThreads) mask[i] = from[i];
+    }
+    __syncthreads();
+
+    const typename E::Word *entries = reinterpret_cast<const typename E::Word *>(table);
+    auto penalised = [&](float v, uint32_t e) {
+        v = v > 0.f ? __fdiv_rn(v, rep) : v * rep;
+        return e & E::kCount ? v - fmaf(freq, (float)(e & E::kCount), pres) : v;
+    };
+    auto one = [&](uint32_t i, float bias) {        // token `i` of the slice
+        float v = load1(x, i, kDtype);
+        if (entries[i] & (E::kPrompt | E::kCount)) v = penalised(v, entries[i]);
+        v += bias;
+        if (mask_row >= 0 && !(mask[i >> 5] >> (i & 31) & 1)) v = -INFINITY;
+        store1(out, i, kDtype, v);
+    };
+    constexpr uint32_t kLowest = kDtype == NINFER_F32 ? 0xff800000u : kDtype == NINFER_BF16 ? 0xff80ff80u : 0xfc00fc00u;  // -infinity
+    for (uint32_t g0 = tid; g0 < vecs; g0 += kAhead * kThreads) {
+        uint4 now[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            now[k] = ahead[k];
+            const uint32_t g = g0 + (kAhead + k) * kThreads;
+            if (g < vecs) ahead[k] = reinterpret_cast<const uint4 *>(x)[g];
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const uint32_t g = g0 + k * kThreads;
+            if (g >= vecs) break;
+            uint32_t w[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
+            // the vector's entries: kVec of them, 8 to 32 bytes
+            uint32_t e[kVec * sizeof(typename E::Word) / 4], any = 0;
+#pragma unroll
+            for (int j = 0; j < (int)(sizeof e / 4); ++j) {
+                e[j] = table[g * (sizeof e / 4) + j];
+                any |= e[j];
+            }
+            uint32_t bits = ~0u;
+            if (mask_row >= 0) bits = mask[g * kVec >> 5] >> (g * kVec & 31);
+            if (any & (kWide ? E::kBias : E::kBias * 0x10001u)) {
+                // a token with a bias is among them: the others alone
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (!(entries[g * kVec + j] & E::kBias)) one(g * kVec + j, 0.f);
+                continue;
+            }
+            if (any) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) {
+                    const uint32_t ej = kWide ? e[j] : e[j / 2] >> (16 * (j & 1)) & 0xffffu;
+                    if (!ej) continue;
+                    const float v = penalised(value<kDtype>(w[j * kEs / 4], j & 1), ej);
+                    if (kDtype == NINFER_F32) w[j] = __float_as_uint(v);
+                    else {
+                        const uint32_t r = kDtype == NINFER_BF16 ? (uint32_t)__bfloat16_as_ushort(__float2bfloat16_rn(v))
+                                                                 : (uint32_t)__half_as_ushort(__float2half_rn(v));
+                        w[j / 2] = j & 1 ? (w[j / 2] & 0xffffu) | r << 16 : (w[j / 2] & 0xffff0000u) | r;
+                    }
+                }
+            }
+            if (~bits & ((1u << kVec) - 1)) {
+#pragma unroll
+                for (int j = 0; j < kVec; ++j)
+                    if (!(bits >> j & 1)) {
+                        if (kDtype == NINFER_F32) w[j] = kLowest;
+                        else w[j / 2] = j & 1 ? (w[j / 2] & 0xffffu) | (kLowest & 0xffff0000u) : (w[j / 2] & 0xffff0000u) | (kLowest & 0xffffu);
+                    }
+            }
+            reinterpret_cast<uint4 *>(out)[g] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    for (uint32_t i = vecs * kVec + tid; i < size; i += kThreads)
+        if (!(entries[i] & E::kBias)) one(i, 0.f);
+    for (int32_t i = b0 + tid; i < b1; i += kThreads) {
+        const uint32_t at = (uint32_t)p.c.bias_ids[i] - first;
+        if (at < size) one(at, p.c.bias_values[i]);
     }
     if (bad && p.status) atomicOr(p.status, bad);
+}
+
+template <bool kWide>
+auto kernel_of(int dtype) {
+    return dtype == NINFER_F32    ? logits_kernel<NINFER_F32, kWide>
+           : dtype == NINFER_BF16 ? logits_kernel<NINFER_BF16, kWide>
+                                  : logits_kernel<NINFER_F16, kWide>;
 }
 
 }  // namespace
@@ -119,7 +246,17 @@ extern "C" int ninfer_logits_process(const void *logits, uint64_t logits_stride,
                           (const void *)c.bias_offsets, (const void *)c.bias_ids, (const void *)c.bias_values,
                           (const void *)c.mask, (const void *)c.mask_rows, (const void *)status})
         if (!aligned(a, 4)) return fail(NINFER_ERR_ALIGNMENT, "logits: control buffers must be 4-byte aligned");
+    DeviceInfo d;
+    int st = device_info(&d);
+    if (st) return st;
+    const bool wide = c.history && c.history_stride > Entry<false>::kCount;
+    // a slice: at most a table, at least kLeast tokens, and as many as fill the SMs once
+    const uint64_t most = wide ? kMostWide : kMostNarrow, slots = (uint64_t)d.sms * kResident;
+    uint64_t slices = slots / rows;
+    slices = std::min(std::max(slices, (vocab + most - 1) / most), std::max((vocab + kLeast - 1) / kLeast, (vocab + most - 1) / most));
     LogitsParams p;
+    p.slice = (uint32_t)std::min<uint64_t>(((vocab + slices - 1) / slices + 127) / 128 * 128, most);
+    slices = (vocab + p.slice - 1) / p.slice;
     p.x = logits;
     p.out = out;
     p.x_stride = logits_stride;
@@ -127,12 +264,13 @@ extern "C" int ninfer_logits_process(const void *logits, uint64_t logits_stride,
     p.c = c;
     p.status = status;
     p.vocab = (uint32_t)vocab;
-    p.slices = (uint32_t)((vocab + kSlice - 1) / kSlice);
+    p.slices = (uint32_t)slices;
     p.dtype = dtype;
-    if (rows * p.slices > 0x7fffffffull) return fail(NINFER_ERR_OVERFLOW, "logits: rows * vocab too large");
-    constexpr int kBytes = kSlice * 8;
-    const int st = ninfer::set_smem_attribute(reinterpret_cast<const void *>(logits_kernel), kBytes);
+    if (rows * slices > 0x7fffffffull) return fail(NINFER_ERR_OVERFLOW, "logits: rows * vocab too large");
+    const auto kernel = wide ? kernel_of<true>(dtype) : kernel_of<false>(dtype);
+    st = set_smem_attribute(reinterpret_cast<const void *>(kernel), kSmemBytes);
     if (st) return st;
-    return launch_dependent("logits", logits_kernel, dim3((unsigned)(rows * p.slices)), dim3(kThreads), kBytes,
-                            (cudaStream_t)stream, p);
+    p.mask_at = p.slice * (wide ? 4 : 2) / 4;
+    const size_t smem = p.mask_at * 4 + p.slice / 8;
+    return launch_dependent("logits", kernel, dim3((unsigned)(rows * slices)), dim3(kThreads), smem, (cudaStream_t)stream, p);
 }
