@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 from collections import namedtuple
 
 import numpy as np
@@ -94,7 +95,7 @@ _sig = {
     "ninfer_kv_attention_workspace": (_int, [C.POINTER(_KvCacheStruct), _u64, _u64, C.POINTER(_u64)]),
     "ninfer_kv_attention": (_int, [_vp, _int, _u64, _u64, _u64, _u64, C.POINTER(_KvCacheStruct), _vp, _u64, _u64, _vp,
                                    C.c_float, _u64, _vp, _int, _vp, _vp, _u64, _vp]),
-    "ninfer_logits_process": (_int, [_vp, _u64, _vp, _u64, _int, _u64, _u64, C.POINTER(_LogitsControls), _vp, _vp]),
+    "ninfer_logits_process": (_int, [_vp, _u64, _vp, _u64, _int, _u64, _u64, _vp, _vp, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024
 for _name, (_res, _args) in _sig.items():
@@ -339,38 +340,50 @@ def ninfer_ternary_embed(fmt, payload, n: int, k: int, ids, signs=None, out=None
 
 
 # ------------------------------------------------------------ decode step ---
-_TYPES: dict = {}       # torch dtype -> library dtype, filled on first use (torch is imported lazily)
+# A decode step's calls are short, so that their checks are written for speed:
+# torch's types and the stream query are looked up once, addresses and strides
+# go to the library as plain integers, the controls of the logits as packed bytes.
+_TYPES: dict = {}       # torch dtype -> library dtype
+_I32 = _I64 = _F32 = _raw_stream = None
+_CONTROLS = struct.Struct("=15Q")
 
 
 def _types():
+    global _I32, _I64, _F32, _raw_stream
     if not _TYPES:
         torch = _torch()
+        _I32, _I64, _F32, _raw_stream = torch.int32, torch.int64, torch.float32, torch._C._cuda_getCurrentRawStream
         _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3})
     return _TYPES
 
 
-def _raw_stream(t) -> int:
-    return _torch()._C._cuda_getCurrentRawStream(t.device.index)
-
-
-def _arg(t, name, dtype, shape=None):
-    """Address of a contiguous CUDA tensor of one dtype (and shape); None stays None."""
+def _arg(t, name, dtype, count):
+    """Address of a contiguous CUDA tensor of one dtype and `count` elements; None is 0."""
     if t is None:
-        return None
-    if not t.is_cuda or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, not {tuple(t.shape)}")
+        return 0
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {count} elements of {dtype}, "
+                         f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
 def _rows(t, name, dims, dtypes):
     """Checks a CUDA tensor whose last dimension is contiguous and whose other
-    strides are free; returns its library dtype."""
-    code = _types().get(t.dtype, -1)
-    if not t.is_cuda or t.dim() != dims or code not in dtypes or (t.stride(-1) != 1 and t.shape[-1] > 1):
+    strides are free; returns its library dtype and its strides."""
+    code = (_TYPES or _types()).get(t.dtype, -1)
+    strides = t.stride()
+    if not t.is_cuda or len(strides) != dims or code not in dtypes or (strides[-1] != 1 and t.shape[-1] > 1):
         raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions, the last one contiguous, of a supported dtype")
-    return code
+    return code, strides
+
+
+def _table(t, name):
+    """Address, width and row stride of an int32 table with contiguous rows."""
+    strides = t.stride()
+    if t.dtype is not _I32 or not t.is_cuda or len(strides) != 2 or (strides[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a two-dimensional int32 CUDA tensor with contiguous rows")
+    n, width = t.shape
+    return t.data_ptr(), n, width, strides[0] if n > 1 else width
 
 
 class KvCache:
@@ -379,24 +392,21 @@ class KvCache:
     float8_e4m3fn). A stored value stands for itself times k_scale (v_scale)."""
 
     def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
-        code = _rows(k, "k", 4, (BF16, F16, E4M3))
-        if _rows(v, "v", 4, (BF16, F16, E4M3)) != code or v.shape != k.shape or v.stride() != k.stride() or v.device != k.device:
+        code, strides = _rows(k, "k", 4, (BF16, F16, E4M3))
+        if _rows(v, "v", 4, (BF16, F16, E4M3)) != (code, strides) or v.shape != k.shape or v.device != k.device:
             raise ValueError("k and v must have the same dtype, shape, strides and device")
         self.k, self.v = k, v
         pages, page_size, heads, dim = k.shape
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
-        strides = [s if n > 1 else 0 for s, n in zip(k.stride(), k.shape)]
+        strides = [s if n > 1 else 0 for s, n in zip(strides, k.shape)]
         self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dim, strides[0], strides[1],
                                       strides[2], k_scale, v_scale, code, 0)
         self._ref = C.byref(self._struct)
 
 
-KvTablesFields = ("block_table", "slots", "positions", "token_rows", "offsets", "lengths", "counts")
-
-
-class KvTables(namedtuple("KvTables", KvTablesFields)):
-    """What ninfer_kv_tables writes; give one back as `out` to reuse its buffers."""
-    __slots__ = ()
+class KvTables(namedtuple("KvTables", ("block_table", "slots", "positions", "token_rows", "offsets", "lengths", "counts"))):
+    """What ninfer_kv_tables writes; give one back as `out` to reuse its buffers,
+    which are checked when it is first used."""
 
     @classmethod
     def empty(cls, block_table, capacity: int):
@@ -407,40 +417,49 @@ class KvTables(namedtuple("KvTables", KvTablesFields)):
         return cls(block_table, new(capacity, torch.int64), new(capacity, i32), new(capacity, i32), new(n + 1, i32),
                    new(n, i32), new(2, i32))
 
+    def _addresses(self, capacity: int):
+        known = self.__dict__.get("_known")
+        if known is None or known[0] != capacity:
+            table = _table(self.block_table, "block_table")
+            n = table[1]
+            known = self.__dict__["_known"] = (
+                capacity, table,
+                (_arg(self.slots, "slots", _I64, capacity), _arg(self.positions, "positions", _I32, capacity),
+                 _arg(self.token_rows, "token_rows", _I32, capacity)),
+                (_arg(self.offsets, "offsets", _I32, n + 1), _arg(self.lengths, "lengths", _I32, n),
+                 _arg(self.counts, "counts", _I32, 2)))
+        return known
+
 
 def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_table, capacity: int, out=None, status=None):
     """Block tables and slot maps of a step's new tokens from the requests'
     lengths: fills the fresh entries of block_table in place and returns a
     KvTables. new_tokens None: one a request; free_pages None: no free page."""
-    i32 = _torch().int32
-    if not block_table.is_cuda or block_table.dtype != i32 or block_table.dim() != 2 or block_table.stride(1) != 1:
-        raise ValueError("block_table must be an int32 CUDA tensor (requests, table_pages) with contiguous rows")
-    n, width = block_table.shape
+    _TYPES or _types()
     if out is None:
         out = KvTables.empty(block_table, capacity)
+    elif out.block_table is not block_table:
+        out = out._replace(block_table=block_table)
+    _, (table, n, width, stride), tokens, requests = out._addresses(capacity)
+    free = free_pages.numel() if free_pages is not None else 0
     _check(_lib.ninfer_kv_tables(
-        _arg(lengths, "lengths", i32, (n,)), _arg(new_tokens, "new_tokens", i32, (n,)), n, page_size,
-        _arg(free_pages, "free_pages", i32), free_pages.numel() if free_pages is not None else 0,
-        block_table.data_ptr(), width, block_table.stride(0) if n > 1 else width,
-        _arg(out.slots, "slots", _torch().int64, (capacity,)), _arg(out.positions, "positions", i32, (capacity,)),
-        _arg(out.token_rows, "token_rows", i32, (capacity,)), capacity, _arg(out.offsets, "offsets", i32, (n + 1,)),
-        _arg(out.lengths, "lengths", i32, (n,)), _arg(out.counts, "counts", i32, (2,)), _arg(status, "status", i32),
-        _raw_stream(lengths)))
-    return out if out.block_table is block_table else out._replace(block_table=block_table)
+        _arg(lengths, "lengths", _I32, n), _arg(new_tokens, "new_tokens", _I32, n), n, page_size,
+        _arg(free_pages, "free_pages", _I32, free), free, table, width, stride, *tokens, capacity, *requests,
+        _arg(status, "status", _I32, 1), _raw_stream(lengths.get_device())))
+    return out
 
 
 def ninfer_kv_append(cache: KvCache, k, v, slots, status=None) -> None:
     """Writes the new keys and values k, v (tokens, kv_heads, head_dim) into the cache's slots."""
-    code = _rows(k, "k", 3, (F32, BF16, F16))
-    if k.shape != v.shape or k.dtype != v.dtype or k.shape[1] != cache.kv_heads or k.shape[2] != cache.head_dim:
+    code, ks = _rows(k, "k", 3, (F32, BF16, F16))
+    code_v, vs = _rows(v, "v", 3, (F32, BF16, F16))
+    shape = k.shape
+    if code != code_v or shape != v.shape or shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
         raise ValueError("k and v must be (tokens, kv_heads, head_dim) of the cache and of one dtype")
-    _rows(v, "v", 3, (F32, BF16, F16))
-    torch = _torch()
-    tokens = k.shape[0]
-    ks, vs = k.stride(), v.stride()
+    tokens = shape[0]
     _check(_lib.ninfer_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1],
-                                 _arg(slots, "slots", torch.int64, (tokens,)), cache._ref,
-                                 _arg(status, "status", torch.int32), _raw_stream(k)))
+                                 _arg(slots, "slots", _I64, tokens), cache._ref, _arg(status, "status", _I32, 1),
+                                 _raw_stream(k.get_device())))
 
 
 def ninfer_kv_attention_workspace(cache: KvCache, requests: int, q_heads: int) -> int:
@@ -455,35 +474,27 @@ def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, win
     over the cache's pages in block_table (requests, table_pages); lengths count
     the new token. scale: head_dim ** -0.5 unless given; window 0: every key.
     lse: a float32 (requests, q_heads) tensor to be written, or None."""
-    torch = _torch()
-    code = _rows(q, "q", 3, (F32, BF16, F16))
+    code, strides = _rows(q, "q", 3, (F32, BF16, F16))
     requests, heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
-    if not block_table.is_cuda or block_table.dtype != torch.int32 or block_table.dim() != 2 or \
-            block_table.shape[0] != requests or block_table.stride(1) != 1:
-        raise ValueError("block_table must be an int32 CUDA tensor (requests, table_pages) with contiguous rows")
+    table, n, width, stride = _table(block_table, "block_table")
+    if n != requests:
+        raise ValueError(f"block_table has {n} rows for {requests} requests")
     if out is None:
-        out = torch.empty((requests, heads, dim), dtype=out_dtype or q.dtype, device=q.device)
-    elif tuple(out.shape) != (requests, heads, dim) or not out.is_contiguous() or not out.is_cuda:
-        raise ValueError("out must be a contiguous CUDA tensor (requests, q_heads, head_dim)")
+        out = _torch().empty((requests, heads, dim), dtype=out_dtype or q.dtype, device=q.device)
     if workspace is None:
-        workspace = torch.empty(ninfer_kv_attention_workspace(cache, requests, heads), dtype=torch.uint8, device=q.device)
-    width = block_table.shape[1]
-    qs = q.stride()
-    _check(_lib.ninfer_kv_attention(
-        q.data_ptr(), code, requests, heads, qs[0], qs[1], cache._ref, block_table.data_ptr(), width,
-        block_table.stride(0) if requests > 1 else width, _arg(lengths, "lengths", torch.int32, (requests,)),
-        dim ** -0.5 if scale is None else scale, window, out.data_ptr(), _types().get(out.dtype, -1),
-        _arg(lse, "lse", torch.float32, (requests, heads)), _dev_bytes(workspace), workspace.numel() * workspace.element_size(),
-        _raw_stream(q)))
-    return out
-
-
-def _dev_bytes(t):
-    if not t.is_cuda or not t.is_contiguous():
+        need = ninfer_kv_attention_workspace(cache, requests, heads)
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=q.device)
+    elif not workspace.is_cuda or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor")
-    return t.data_ptr()
+    dtype = out.dtype
+    _check(_lib.ninfer_kv_attention(
+        q.data_ptr(), code, requests, heads, strides[0], strides[1], cache._ref, table, width, stride,
+        _arg(lengths, "lengths", _I32, requests), dim ** -0.5 if scale is None else scale, window,
+        _arg(out, "out", dtype, requests * heads * dim), _TYPES.get(dtype, -1), _arg(lse, "lse", _F32, requests * heads),
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(q.get_device())))
+    return out
 
 
 def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, prompt_lengths=None, repetition=None,
@@ -492,36 +503,34 @@ def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, 
     """Penalties, biases and grammar masks on logits (rows, vocab); out may be
     logits itself. history: int32 (rows, longest); mask: int32 words (mask rows,
     ceil(vocab / 32)), bit set where a token is allowed."""
-    torch = _torch()
-    f32, i32 = torch.float32, torch.int32
-    code = _rows(logits, "logits", 2, (F32, BF16, F16))
+    code, strides = _rows(logits, "logits", 2, (F32, BF16, F16))
     rows, vocab = logits.shape
     if out is None:
-        out = torch.empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    elif _rows(out, "out", 2, (code,)) != code or out.shape != logits.shape:
+        out = _torch().empty((rows, vocab), dtype=logits.dtype, device=logits.device)
+    code_out, out_strides = _rows(out, "out", 2, (code,))
+    if out is not logits and out.shape != (rows, vocab):
         raise ValueError("out must have the shape and dtype of logits")
-    c = _LogitsControls()
+    h = n = p = longest = offsets = ids = values = count = m = m_rows = m_count = m_stride = 0
     if history is not None:
-        c.history = _arg(history, "history", i32)
-        if history.dim() != 2 or history.shape[0] != rows:
+        if history.dim() != 2:
             raise ValueError("history must be (rows, longest)")
-        c.history_stride = history.shape[1]
-        c.history_lengths = _arg(history_lengths, "history_lengths", i32, (rows,))
-        c.prompt_lengths = _arg(prompt_lengths, "prompt_lengths", i32, (rows,))
-    c.repetition = _arg(repetition, "repetition", f32, (rows,))
-    c.presence = _arg(presence, "presence", f32, (rows,))
-    c.frequency = _arg(frequency, "frequency", f32, (rows,))
-    if bias_ids is not None and bias_ids.numel():
-        c.bias_offsets = _arg(bias_offsets, "bias_offsets", i32, (rows + 1,))
-        c.bias_count = bias_ids.numel()
-        c.bias_ids = _arg(bias_ids, "bias_ids", i32)
-        c.bias_values = _arg(bias_values, "bias_values", f32, (c.bias_count,))
+        longest = history.shape[1]
+        h = _arg(history, "history", _I32, rows * longest)
+        n = _arg(history_lengths, "history_lengths", _I32, rows)
+        p = _arg(prompt_lengths, "prompt_lengths", _I32, rows)
+    if bias_ids is not None and (count := bias_ids.numel()):
+        offsets = _arg(bias_offsets, "bias_offsets", _I32, rows + 1)
+        ids = _arg(bias_ids, "bias_ids", _I32, count)
+        values = _arg(bias_values, "bias_values", _F32, count)
     if mask is not None:
-        if not mask.is_cuda or mask.dim() != 2 or mask.dtype != i32 or mask.stride(1) != 1 or mask.shape[1] * 32 < vocab:
-            raise ValueError("mask must be an int32 CUDA tensor (mask rows, at least vocab / 32 words)")
-        c.mask, c.mask_row_count, c.mask_stride = mask.data_ptr(), mask.shape[0], mask.stride(0)
-        c.mask_rows = _arg(mask_rows, "mask_rows", i32, (rows,))
-    _check(_lib.ninfer_logits_process(logits.data_ptr(), logits.stride(0) if rows > 1 else vocab, out.data_ptr(),
-                                      out.stride(0) if rows > 1 else vocab, code, rows, vocab, C.byref(c),
-                                      _arg(status, "status", i32), _raw_stream(logits)))
+        m, m_count, width, m_stride = _table(mask, "mask")
+        if width * 32 < vocab:
+            raise ValueError(f"mask has {width} words a row for {vocab} tokens")
+        m_rows = _arg(mask_rows, "mask_rows", _I32, rows)
+    controls = _CONTROLS.pack(
+        h, n, p, longest, _arg(repetition, "repetition", _F32, rows), _arg(presence, "presence", _F32, rows),
+        _arg(frequency, "frequency", _F32, rows), offsets, ids, values, count, m, m_rows, m_count, m_stride)
+    _check(_lib.ninfer_logits_process(
+        logits.data_ptr(), strides[0] if rows > 1 else vocab, out.data_ptr(), out_strides[0] if rows > 1 else vocab, code,
+        rows, vocab, controls, _arg(status, "status", _I32, 1), _raw_stream(logits.get_device())))
     return out

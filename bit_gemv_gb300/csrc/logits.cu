@@ -64,7 +64,8 @@ __device__ __forceinline__ float value(uint32_t w, int half) {
 template <int kDtype, bool kWide>
 __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __grid_constant__ LogitsParams p) {
     using E = Entry<kWide>;
-    constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs, kAhead = 4;
+    constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs, kAhead = 2, kQuads = 4;
+    constexpr int kMaskWords = ((kWide ? kMostWide : kMostNarrow) / 32 + kThreads - 1) / kThreads;
     extern __shared__ __align__(16) uint32_t table[];
     const uint32_t tid = threadIdx.x, row = blockIdx.x / p.slices, first = blockIdx.x % p.slices * p.slice;
     const uint32_t size = min(p.slice, p.vocab - first);
@@ -89,60 +90,101 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
     if (p.c.frequency) freq = p.c.frequency[row];
     // rows on 16-byte boundaries go in vectors, others (and the last few tokens) one by one
     const uint32_t vecs = (p.x_stride * kEs) % 16 == 0 && (p.out_stride * kEs) % 16 == 0 ? size / kVec : 0;
-    uint4 ahead[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k)
-        if (tid + k * kThreads < vecs) ahead[k] = reinterpret_cast<const uint4 *>(x)[tid + k * kThreads];
-    __syncthreads();            // the table is empty
     int bad = 0;
     n = min(max(n, 0), (int32_t)p.c.history_stride);
+    const int32_t *h = p.c.history + row * p.c.history_stride;
+    const bool quads = p.c.history_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(p.c.history) & 15) == 0;
+    // the history before the logits, which would hold it up
+    uint4 v[kQuads], ahead[kAhead];
+    auto read_history = [&](int32_t i0) {
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const int32_t i = i0 + 4 * kThreads * k;
+            v[k] = make_uint4(~0u, ~0u, ~0u, ~0u);
+            if (i >= n) continue;
+            if (quads) v[k] = *reinterpret_cast<const uint4 *>(h + i);      // rows are whole quads long
+            else {
+                v[k].x = h[i];
+                if (i + 1 < n) v[k].y = h[i + 1];
+                if (i + 2 < n) v[k].z = h[i + 2];
+                if (i + 3 < n) v[k].w = h[i + 3];
+            }
+        }
+    };
+    read_history(4 * tid);
+    // a thread's first bias and its mask words
     b0 = max(b0, 0);
     b1 = min(b1, (int32_t)p.c.bias_count);
+    const bool biased = b0 + (int32_t)tid < b1;
+    uint32_t bias_token = ~0u;
+    float bias_value = 0.f;
+    if (biased) {
+        bias_token = (uint32_t)p.c.bias_ids[b0 + tid];
+        bias_value = p.c.bias_values[b0 + tid];
+    }
     if (mask_row >= 0 && (uint64_t)mask_row >= p.c.mask_row_count) {
         bad = NINFER_LOGITS_BAD_TOKEN;
         mask_row = -1;
     }
-    const int32_t *h = p.c.history + row * p.c.history_stride;
-    for (int32_t i0 = tid; i0 < n; i0 += 8 * kThreads) {
-        uint32_t v[8];
+    uint32_t *mask = table + p.mask_at, words[kMaskWords];
+    if (mask_row >= 0) {
+        const uint32_t *from = p.c.mask + mask_row * p.c.mask_stride + (first >> 5);
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            if (i0 + k * kThreads < n) v[k] = (uint32_t)h[i0 + k * kThreads];
+        for (int k = 0; k < kMaskWords; ++k)
+            if ((tid + k * kThreads) * 32 < size) words[k] = from[tid + k * kThreads];
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int32_t i = i0 + k * kThreads;
-            if (i >= n) continue;
-            if (v[k] >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
-            const uint32_t at = v[k] - first;
-            if (at >= size) continue;
-            if (i < told) E::set(table, at, E::kPrompt);
-            else E::add(table, at);
+    for (int k = 0; k < kAhead; ++k)
+        if (tid + k * kThreads < vecs) ahead[k] = reinterpret_cast<const uint4 *>(x)[tid + k * kThreads];
+    __syncthreads();            // the table is empty
+    for (int32_t i0 = 4 * tid; i0 < n; i0 += 4 * kThreads * kQuads) {
+        if (i0 != 4 * (int32_t)tid) read_history(i0);
+#pragma unroll
+        for (int k = 0; k < kQuads; ++k) {
+            const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int32_t i = i0 + 4 * kThreads * k + j;
+                if (i >= n) break;
+                if (w[j] >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
+                const uint32_t at = w[j] - first;
+                if (at >= size) continue;
+                if (i < told) E::set(table, at, E::kPrompt);
+                else E::add(table, at);
+            }
         }
     }
-    for (int32_t i = b0 + tid; i < b1; i += kThreads) {
+    if (biased && bias_token >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
+    float bias_logit = 0.f;                 // of this thread's first bias, if it lies in the slice
+    bias_token -= first;
+    if (bias_token < size) {
+        E::set(table, bias_token, E::kBias);
+        bias_logit = load1(x, bias_token, kDtype);
+    }
+    for (int32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
         const uint32_t v = (uint32_t)p.c.bias_ids[i];
         if (v >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
         if (v - first < size) E::set(table, v - first, E::kBias);
     }
-    uint32_t *mask = table + p.mask_at;
     if (mask_row >= 0) {
-        const uint32_t *from = p.c.mask + mask_row * p.c.mask_stride + (first >> 5);
-        for (uint32_t i = tid; i * 32 < size; i += kThreads) mask[i] = from[i];
+#pragma unroll
+        for (int k = 0; k < kMaskWords; ++k)
+            if ((tid + k * kThreads) * 32 < size) mask[tid + k * kThreads] = words[k];
     }
     __syncthreads();
 
     const typename E::Word *entries = reinterpret_cast<const typename E::Word *>(table);
-    auto penalised = [&](float v, uint32_t e) {
-        v = v > 0.f ? __fdiv_rn(v, rep) : v * rep;
-        return e & E::kCount ? v - fmaf(freq, (float)(e & E::kCount), pres) : v;
+    const float less = 1.f / rep;
+    auto penalised = [&](float v, uint32_t e) {         // an empty entry leaves v as it is
+        v *= e ? v > 0.f ? less : rep : 1.f;
+        return v - (e & E::kCount ? fmaf(freq, (float)(e & E::kCount), pres) : 0.f);
     };
-    auto one = [&](uint32_t i, float bias) {        // token `i` of the slice
-        float v = load1(x, i, kDtype);
-        if (entries[i] & (E::kPrompt | E::kCount)) v = penalised(v, entries[i]);
-        v += bias;
+    auto one = [&](uint32_t i, float v, float bias) {       // token `i` of the slice, whose logit is v
+        v = penalised(v, entries[i] & (E::kPrompt | E::kCount)) + bias;
         if (mask_row >= 0 && !(mask[i >> 5] >> (i & 31) & 1)) v = -INFINITY;
         store1(out, i, kDtype, v);
     };
+    if (bias_token < size) one(bias_token, bias_logit, bias_value);
     constexpr uint32_t kLowest = kDtype == NINFER_F32 ? 0xff800000u : kDtype == NINFER_BF16 ? 0xff80ff80u : 0xfc00fc00u;  // -infinity
     for (uint32_t g0 = tid; g0 < vecs; g0 += kAhead * kThreads) {
         uint4 now[kAhead];
@@ -170,14 +212,13 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
                 // a token with a bias is among them: the others alone
 #pragma unroll
                 for (int j = 0; j < kVec; ++j)
-                    if (!(entries[g * kVec + j] & E::kBias)) one(g * kVec + j, 0.f);
+                    if (!(entries[g * kVec + j] & E::kBias)) one(g * kVec + j, value<kDtype>(w[j * kEs / 4], j & 1), 0.f);
                 continue;
             }
             if (any) {
 #pragma unroll
                 for (int j = 0; j < kVec; ++j) {
                     const uint32_t ej = kWide ? e[j] : e[j / 2] >> (16 * (j & 1)) & 0xffffu;
-                    if (!ej) continue;
                     const float v = penalised(value<kDtype>(w[j * kEs / 4], j & 1), ej);
                     if (kDtype == NINFER_F32) w[j] = __float_as_uint(v);
                     else {
@@ -199,10 +240,10 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
         }
     }
     for (uint32_t i = vecs * kVec + tid; i < size; i += kThreads)
-        if (!(entries[i] & E::kBias)) one(i, 0.f);
-    for (int32_t i = b0 + tid; i < b1; i += kThreads) {
+        if (!(entries[i] & E::kBias)) one(i, load1(x, i, kDtype), 0.f);
+    for (int32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
         const uint32_t at = (uint32_t)p.c.bias_ids[i] - first;
-        if (at < size) one(at, p.c.bias_values[i]);
+        if (at < size) one(at, load1(x, at, kDtype), p.c.bias_values[i]);
     }
     if (bad && p.status) atomicOr(p.status, bad);
 }
