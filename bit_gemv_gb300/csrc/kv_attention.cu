@@ -27,10 +27,6 @@
 // waits for another one until its part is done. Up to 192 KB an SM are in
 // flight. Pieces past the row's end are not fetched.
 #include <cmath>
-#include <cstring>
-#include <mutex>
-
-#include <cuda.h>
 
 #include "decode.cuh"
 #include "gemv.h"
@@ -44,7 +40,7 @@ constexpr uint32_t kRingBytes = kWarps * kItems * kItemBytes;
 constexpr uint32_t kNone = 0xffffffffu, kRowKeys = 1024;
 
 struct AttentionParams {
-    CUtensorMap k, v;                   // {element, token, head, page}
+    const uint8_t *k, *v;
     const void *q;
     const int32_t *table, *lengths;
     void *out;
@@ -53,20 +49,23 @@ struct AttentionParams {
     float2 *cta_ml;                     // [CTA][2][8]: m, l
     float4 *cta_o, *warp_o;             // [CTA][2] and [CTA][warp] sums, in fragment order
     int64_t q_request, q_head, table_stride;
-    uint32_t *err;
+    uint64_t page_bytes, token_bytes, head_bytes;       // strides of the pools
     float scale, v_scale;               // scale: of scores, in log2
-    uint32_t requests, run, q_heads, group, head_dim, head_rows, box, window, most;
+    uint32_t requests, run, q_heads, group, head_dim, head_rows, pages, piece_log, window, most;
     uint32_t by_row;                    // CTA c has row c, and no other: nothing is cut between CTAs
     FastDiv page, tiles, heads;         // tokens a page, 8-head tiles a key head, rows a request
     int q_dtype, out_dtype;
 };
 
-__device__ __forceinline__ void tma_load_4d(uint32_t dst, const void *tmap, int x, int y, int z, int w, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
-        : "memory");
+// 16 bytes into shared memory, or zeros where `bytes` is 0 (nothing is read then).
+__device__ __forceinline__ void copy16(uint32_t dst, const uint8_t *src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until all but the last n groups of this thread's copies have landed.
+template <int n>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(n) : "memory");
 }
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -251,7 +250,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     using S = Shape<kDtype, kWidth>;
     constexpr int kKeys = S::kKeys, kSteps = S::kSteps, kTiles = kWidth / 16, kPart = kTiles * 32;
     extern __shared__ uint8_t ring_raw[];
-    __shared__ __align__(8) uint64_t s_bar[kWarps][kItems];
     __shared__ uint64_t s_sum[kWarps], s_upto[kThreads];
     __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
     __shared__ float2 s_ml[2 * kWarps][8], s_total[2 * kWarps][8];
@@ -259,15 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring_skip = (1024 - (smem_u32(ring_raw) & 1023)) & 1023;
     const uint32_t ring = smem_u32(ring_raw) + ring_skip + warp * (kItems * kItemBytes);
-    const uint32_t bar = smem_u32(&s_bar[warp][0]);
-    if (lane == 0)
-        for (int i = 0; i < kItems; ++i) mbar_init(bar + 8 * i, 1);
-    if (threadIdx.x == 0) {
-        prefetch_tmap(&p.k);
-        prefetch_tmap(&p.v);
-    }
     if (lane < 2) s_row[2 * warp + lane] = kNone;
-    fence_mbar_init();
     pdl_launch_dependents();
     pdl_wait();
 
@@ -333,66 +323,75 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
     // ---- the ring: keys and values of the units in turn ----
     Cursor cp = ld;
-    uint32_t keys_due = left, values_due = left, slot_in = 0, slot_out = 0, phase = 0, in_flight = 0;
-    int32_t page[2], token[2];              // of this lane's pieces of the unit that is loaded next
-    const uint32_t pieces = kKeys / p.box;
-    uint32_t piece_lo = 0, piece_hi = 0;    // its pieces that hold keys of the request
+    uint32_t keys_due = left, values_due = left, slot_in = 0, slot_out = 0;
+    constexpr int kRowUnits = kWidth * S::kEs / 16, kRowsAtOnce = 32 / kRowUnits;   // 16-byte units a row, rows a copy of the warp
+    constexpr int kPieces = (kKeys + 31) / 32;
+    // The unit that is loaded next is in pieces of 2^piece_log keys, each within one page; lane q has pieces q and q + 32.
+    int32_t page[kPieces];
+    uint32_t token[kPieces];
+    const uint32_t pieces = kKeys >> p.piece_log;
     auto find_pages = [&] {
         const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys;
-        piece_lo = ld.row.from > base ? (ld.row.from - base) / p.box : 0u;
-        piece_hi = min(pieces, (ld.row.end - base + p.box - 1) / p.box);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t b = lane + 32 * i;
-            if (b < piece_lo || b >= piece_hi) continue;
-            const uint32_t key = base + b * p.box, pg = p.page.div(key);
-            token[i] = (int32_t)(key - pg * p.page.d);
-            page[i] = p.table[(int64_t)ld.request * p.table_stride + pg];
+        for (int i = 0; i < kPieces; ++i) {
+            const uint32_t key = base + ((lane + 32 * i) << p.piece_log);
+            page[i] = -1;
+            if (lane + 32u * i < pieces && key < ld.row.end) {
+                const uint32_t pg = p.page.div(key);
+                token[i] = key - pg * p.page.d;
+                page[i] = p.table[(int64_t)ld.request * p.table_stride + pg];
+            }
         }
     };
-    auto load_item = [&](const CUtensorMap *map) {
-        const uint32_t b = bar + 8 * slot_in, to = ring + slot_in * kItemBytes;
-        if (lane == 0) mbar_arrive_expect_tx(b, (piece_hi - piece_lo) * p.box * (kWidth * S::kEs));
-        __syncwarp();
-        const int head = (int)p.tiles.div(ld.head);
+    const uint32_t unit = lane & (kRowUnits - 1), unit_row = lane / kRowUnits;
+    auto load_item = [&](const uint8_t *pool) {
+        const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys;
+        const uint32_t to = ring + slot_in * kItemBytes + (unit >> 3) * (kKeys * 128);
+        const uint64_t head = p.tiles.div(ld.head) * p.head_bytes;
+        const uint8_t *at[kPieces];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const uint32_t q = lane + 32 * i;
-            if (q < piece_lo || q >= piece_hi) continue;
+        for (int i = 0; i < kPieces; ++i)
+            at[i] = (uint32_t)page[i] < p.pages ? pool + (uint32_t)page[i] * p.page_bytes + token[i] * p.token_bytes + head : nullptr;
 #pragma unroll
-            for (int c = 0; c < S::kChunks; ++c)
-                tma_load_4d(to + c * (kKeys * 128) + q * p.box * 128, map, c * (128 / S::kEs), token[i], head, page[i], b);
+        for (int k = 0; k < kKeys / kRowsAtOnce; ++k) {
+            const uint32_t r = k * kRowsAtOnce + unit_row, q = r >> p.piece_log;
+            uint64_t from = __shfl_sync(~0u, reinterpret_cast<uint64_t>(at[0]), q & 31);
+            if (kPieces > 1) {
+                const uint64_t more = __shfl_sync(~0u, reinterpret_cast<uint64_t>(at[kPieces - 1]), q & 31);
+                if (q >= 32) from = more;
+            }
+            const bool on = from && base + r >= ld.row.from && base + r < ld.row.end && unit * (16 / S::kEs) < p.head_dim;
+            from += (r & ((1u << p.piece_log) - 1)) * p.token_bytes + unit * 16;
+            copy16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), on ? reinterpret_cast<const uint8_t *>(from) : pool, on ? 16 : 0);
         }
-        ++in_flight;
         slot_in = slot_in == kItems - 1 ? 0 : slot_in + 1;
     };
+    // one group an item, empty ones at the end, so that the oldest of three is always the one waited for
     auto load_keys = [&] {
-        if (!keys_due) return;
-        --keys_due;
-        load_item(&p.k);
+        if (keys_due) {
+            --keys_due;
+            load_item(p.k);
+        }
+        copies_commit();
     };
     auto load_values = [&] {
-        if (!values_due) return;
-        load_item(&p.v);
-        if (--values_due) {
-            advance<kKeys>(p, ld);
-            find_pages();       // read early: the next unit's keys are asked for half a unit later
+        if (values_due) {
+            load_item(p.v);
+            if (--values_due) {
+                advance<kKeys>(p, ld);
+                find_pages();       // read early: the next unit's keys are asked for half a unit later
+            }
         }
+        copies_commit();
     };
     if (left) find_pages();
-
-    bool alive = true;
     auto wait_item = [&] {
-        const bool ok = mbar_wait(bar + 8 * slot_out, phase, p.err);
-        alive = __all_sync(~0u, ok);
+        copies_wait<kItems - 1>();
+        __syncwarp();
     };
     auto release_item = [&] {
         __syncwarp();
-        --in_flight;
-        if (++slot_out == kItems) {
-            slot_out = 0;
-            phase ^= 1;
-        }
+        slot_out = slot_out == kItems - 1 ? 0 : slot_out + 1;
     };
 
     // ---- the units ----
@@ -400,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     float o[kTiles][4], m = -INFINITY, l = 0.f, sc = 0.f;
     bool fresh = true, begun = false, primed = false;   // a new row's queries are due; it began in this part; loads run
     const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
-    while (left && alive) {
+    while (left) {
         --left;
         if (fresh) {
             fresh = false;
@@ -544,25 +543,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         item = ring + slot_out * kItemBytes;
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk) {
-            uint32_t keep[2] = {~0u, ~0u};      // rows outside the request hold anything, NaN too: zeros instead
-            if (edge) {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t key = base + 16 * kk + 8 * j + 2 * t;
-                    keep[j] = (key >= cp.row.from && key < cp.row.end ? 0xffffu : 0u) |
-                              (key + 1 >= cp.row.from && key + 1 < cp.row.end ? 0xffff0000u : 0u);
-                }
-            }
             if constexpr (!S::kBytes8) {
                 const uint32_t lane_at = item + (16 * kk + (lane_mat >> 1) * 8 + lane_row) * 128;
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
                     uint32_t a[4];
                     ldmatrix4_trans(a, lane_at + (i >> 2) * (kKeys * 128) + (((2 * (i & 3) + (lane_mat & 1)) ^ lane_row) << 4));
-                    a[0] &= keep[0];
-                    a[1] &= keep[0];
-                    a[2] &= keep[1];
-                    a[3] &= keep[1];
                     S::mma(o[i], a, w[2 * kk][0], w[2 * kk + 1][0]);
                     S::mma(o[i], a, w[2 * kk][1], w[2 * kk + 1][1]);
                 }
@@ -574,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     ldmatrix4_trans(r, lane_at + (i >> 3) * (kKeys * 128) + ((((i & 7) + (lane_mat >> 1)) ^ lane_row) << 4));
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const uint32_t x = __byte_perm(r[2 * j] & keep[0], 0, 0x3120), y = __byte_perm(r[2 * j + 1] & keep[1], 0, 0x3120);
+                        const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
                         const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y),
                                                e4m3x2_to_f16x2(y >> 16)};
                         S::mma(o[i + j], a, w[2 * kk][0], w[2 * kk + 1][0]);
@@ -614,16 +600,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             fresh = true;
         }
         advance<kKeys>(p, cp);
-    }
-    if (!alive) {
-        // a copy never arrived (reported in the error word): let the others land, bounded, before the CTA goes
-        for (; in_flight; --in_flight) {
-            mbar_wait(bar + 8 * slot_out, phase, p.err, 200000000ll);
-            if (++slot_out == kItems) {
-                slot_out = 0;
-                phase ^= 1;
-            }
-        }
     }
     if (empties) {
         // requests without keys: by_row CTAs look at their own, others share them out
@@ -774,53 +750,6 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 }
 
 // ------------------------------------------------------------------ host ---
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
-                              const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-int encode_fn(EncodeFn *out) {
-    static EncodeFn fn = nullptr;
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
-    if (!fn) {
-        void *ptr = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q);
-        if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || !ptr)
-            return fail(NINFER_ERR_CUDA, "cuTensorMapEncodeTiled unavailable (%s)", cudaGetErrorString(e));
-        fn = reinterpret_cast<EncodeFn>(ptr);
-    }
-    *out = fn;
-    return NINFER_OK;
-}
-
-// The pool as {element, token, head, page}; boxes of 128 bytes x `box` tokens of
-// one head. Elements past head_dim, and pages outside the pool, read as zeros.
-int encode_pool(CUtensorMap *map, const ninfer_kv_cache *c, void *base, uint32_t box) {
-    EncodeFn fn;
-    const int st = encode_fn(&fn);
-    if (st) return st;
-    const uint64_t es = cache_dtype_size(c->dtype), row = (c->head_dim * es + 15) / 16 * 16;
-    const cuuint64_t dims[4] = {c->head_dim, c->page_size, c->kv_heads, c->pages};
-    const cuuint64_t strides[3] = {c->page_size > 1 ? c->token_stride * es : row, c->kv_heads > 1 ? c->head_stride * es : row,
-                                   c->pages > 1 ? c->page_stride * es : row};
-    const cuuint32_t boxes[4] = {(cuuint32_t)(128 / es), box, 1, 1}, ones[4] = {1, 1, 1, 1};
-    const CUtensorMapDataType type = c->dtype == NINFER_E4M3  ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                     : c->dtype == NINFER_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                              : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    // A miss fetches 256 bytes where those belong to the same head; where a head's
-    // row is shorter and other heads lie between its tokens, half of them would be
-    // thrown away (8-bit rows of 128 bytes, 1.2 GB: 282 us with 256, 230 us with
-    // 128; 16-bit rows of 256 bytes, 184 MB: 47.3 us with 256, 48.2 us with 128).
-    const bool runs_on = strides[0] == c->head_dim * es || c->head_dim * es >= 256;
-    const CUresult r = fn(map, type, 4, base, dims, strides, boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B,
-                          runs_on ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(NINFER_ERR_CUDA, "attention: tensor map encode failed (CUresult %d)", (int)r);
-    return NINFER_OK;
-}
-
 struct Instance {
     void (*attention)(const AttentionParams), (*join)(const AttentionParams, uint32_t);
     uint32_t width, keys;
@@ -916,14 +845,11 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
                     (unsigned long long)w.bytes, (unsigned long long)(workspace ? workspace_bytes : 0));
     if (!aligned(workspace, 256)) return fail(NINFER_ERR_ALIGNMENT, "attention: workspace must be 256-byte aligned");
     AttentionParams p;
-    // a box lies in one page: the largest power of two that divides page_size, up to a unit's keys
-    uint32_t box = in.keys;
-    while (cache->page_size % box) box /= 2;
-    st = encode_pool(&p.k, cache, cache->k, box);
-    if (!st) st = encode_pool(&p.v, cache, cache->v, box);
-    if (!st) st = device_error_word(&p.err);
+    // a piece of a unit lies in one page: the largest power of two that divides page_size, up to a unit's keys
+    uint32_t piece = in.keys;
+    while (cache->page_size % piece) piece /= 2;
     constexpr int kSmem = kRingBytes + 1024;
-    if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(in.attention), kSmem);
+    st = set_smem_attribute(reinterpret_cast<const void *>(in.attention), kSmem);
     if (st) return st;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.q = q;
@@ -948,7 +874,14 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     p.tiles = FastDiv((p.group + 7) / 8);
     p.head_rows = (uint32_t)cache->kv_heads * p.tiles.d;
     p.heads = FastDiv(p.head_rows);
-    p.box = box;
+    p.pages = (uint32_t)cache->pages;
+    p.piece_log = (uint32_t)__builtin_ctz(piece);
+    const uint64_t es = cache_dtype_size(cache->dtype);
+    p.k = static_cast<const uint8_t *>(cache->k);
+    p.v = static_cast<const uint8_t *>(cache->v);
+    p.page_bytes = cache->page_stride * es;
+    p.token_bytes = cache->token_stride * es;
+    p.head_bytes = cache->head_stride * es;
     p.most = (uint32_t)(table_pages * cache->page_size);
     p.window = window < p.most ? (uint32_t)window : 0;
     p.page = FastDiv((uint32_t)cache->page_size);
