@@ -8,11 +8,12 @@
 // What bounds it. Every key and value is used by the few query heads of its
 // group (4 * group flops an element), so HBM does; the tensor cores only have
 // to keep up. mma.sync.m16n8k16 serves: 16 keys of 128 elements take 24 to 32 of them.
-//   scores   A = queries (16 rows: 8 heads' 16-bit values, then their 16-bit
-//            remainders), B = keys: the remainders ride in rows that would be empty.
-//   values   A = values transposed (ldmatrix.trans), B = weights: a score tile's accumulator
-//            registers are the weights' B fragment as they are, and value and
-//            remainder of a weight add up in one accumulator.
+//   scores   A = 16 keys, B = 8 heads' queries;
+//   values   A = 16 elements of the values transposed (ldmatrix.trans), B = 8 heads' weights,
+//            transposed from the scores' accumulators in the registers (movmatrix).
+// The 8 heads of a row are the narrow side of both, so that a group of eight wastes
+// nothing. 32-bit operands enter as a 16-bit value and the 16-bit remainder, one
+// mma each.
 //
 // Split. The keys of every (request, key head, 8 query heads) are cut into
 // units of 8 KB of keys and 8 KB of values; all units of the call form one
@@ -104,7 +105,7 @@ struct Shape {
     static constexpr int kKeys = kItemBytes / (kWidth * kEs);   // of a unit: 16, 32 or 64
     static constexpr int kChunks = kWidth * kEs / 128;          // 128-byte columns of an item
     static constexpr int kSteps = kWidth / 16;                  // 16-element steps of a row
-    static constexpr int kScoreTiles = kKeys / 8;
+    static constexpr int kKeyTiles = kKeys / 16;
     // binary16 weights carry a factor 2^14: weights down to 2^-38 of the largest one keep a value
     static constexpr float kBias = kBf16 ? 0.f : 14.f;
 
@@ -245,7 +246,11 @@ __device__ __forceinline__ void store_lse(const AttentionParams &p, const Place 
 // What the sums of a row are multiplied by in the end; a row without weights gives zeros.
 __device__ __forceinline__ float scale_of(const AttentionParams &p, float l) { return l == 0.f ? 0.f : p.v_scale / l; }
 
-template <int kDtype, int kWidth>
+// kRests: whether remainders take part. They do not where they are zeros (a 16-bit q that
+// the operand type holds) and the output is rounded far more coarsely than the
+// weights: binary16 weights (2^-12) and a bfloat16 result (2^-9), whose error grows by
+// less than 1 %. bfloat16 weights always have theirs.
+template <int kDtype, int kWidth, bool kRests>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttentionParams p) {
     using S = Shape<kDtype, kWidth>;
     constexpr int kKeys = S::kKeys, kSteps = S::kSteps, kTiles = kWidth / 16, kPart = kTiles * 32;
@@ -395,17 +400,20 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
 
     // ---- the units ----
-    uint32_t qa[kSteps][4];
-    float o[kTiles][4], m = -INFINITY, l = 0.f, sc = 0.f;
+    // q[i]: elements 16 i .. 16 i + 15 of head g, value and remainder of the two halves of a B operand.
+    // m, l, sc, o: of heads 2 t and 2 t + 1, as an accumulator has them.
+    uint32_t q[kSteps][4];
+    float o[kTiles][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, sc0 = 0.f, sc1 = 0.f;
     bool fresh = true, begun = false, primed = false;   // a new row's queries are due; it began in this part; loads run
     const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
+    constexpr bool kWeightRests = S::kBf16 || kRests;
     while (left) {
         --left;
         if (fresh) {
             fresh = false;
             begun = cp.unit == 0;
-            m = -INFINITY;
-            l = 0.f;
+            m0 = m1 = -INFINITY;
+            l0 = l1 = 0.f;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
             const uint32_t kvh = p.tiles.div(cp.head), h = (cp.head - kvh * p.tiles.d) * 8 + g;
@@ -440,8 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     }
                     top = fmaxf(top, fmaxf(fabsf(x[i][j].x), fabsf(x[i][j].y)));
                 }
-            sc = p.scale;
-            float down = 1.f;
+            float sc = p.scale, down = 1.f;
             if (!S::kBf16) {
                 // binary16 operands: a power of two brings the head's largest element to about 1
                 top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -450,13 +457,15 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 down = __uint_as_float((uint32_t)(254 - e) << 23);
                 sc *= __uint_as_float((uint32_t)e << 23);
             }
+            sc0 = __shfl_sync(~0u, sc, 8 * t);
+            sc1 = __shfl_sync(~0u, sc, 8 * t + 4);
 #pragma unroll
             for (int i = 0; i < kSteps; ++i)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float a = x[i][j].x * down, b = x[i][j].y * down;
-                    S::split(a, b, qa[i][2 * j], qa[i][2 * j + 1]);
-                    if (isinf(a) || isinf(b)) qa[i][2 * j + 1] = 0;     // no remainder: inf - inf
+                    S::split(a, b, q[i][2 * j], q[i][2 * j + 1]);
+                    if (isinf(a) || isinf(b)) q[i][2 * j + 1] = 0;      // no remainder: inf - inf
                 }
             if (!primed) load_keys();
             primed = true;
@@ -464,63 +473,67 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         const uint32_t base = (cp.row.from / kKeys + cp.unit) * kKeys;
         const bool edge = base < cp.row.from || base + kKeys > cp.row.end;
 
-        // scores: rows g (values of q) and g + 8 (remainders) of the tile add up
+        // scores: keys g and g + 8 of each 16, heads 2 t and 2 t + 1
         wait_item();
-        float s[S::kScoreTiles][4];
+        float s[S::kKeyTiles][4], r[S::kKeyTiles][4];        // of the queries' values, of their remainders
 #pragma unroll
-        for (int i = 0; i < S::kScoreTiles; ++i) s[i][0] = s[i][1] = s[i][2] = s[i][3] = 0.f;
+        for (int i = 0; i < S::kKeyTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[i][j] = r[i][j] = 0.f;
         uint32_t item = ring + slot_out * kItemBytes;
         {
-            const uint32_t lane_at = item + ((lane_mat >> 1) * 8 + lane_row) * 128;
-            if constexpr (!S::kBytes8) {
+            const uint32_t lane_at = item + ((lane_mat & 1) * 8 + lane_row) * 128;
+            constexpr int kUnits = S::kBytes8 ? 1 : 2;      // 16-byte units a step
 #pragma unroll
-                for (int i = 0; i < kSteps; ++i) {
-                    const uint32_t unit = 2 * i, col = (((unit & 7) + (lane_mat & 1)) ^ lane_row) << 4;
+            for (int i = 0; i < kSteps; i += 2 / kUnits) {
+                const uint32_t unit = kUnits * i, at = lane_at + (unit >> 3) * (kKeys * 128) + ((((unit & 7) + (lane_mat >> 1)) ^ lane_row) << 4);
 #pragma unroll
-                    for (int n = 0; n < S::kScoreTiles / 2; ++n) {
-                        uint32_t b[4];
-                        ldmatrix4(b, lane_at + (unit >> 3) * (kKeys * 128) + n * 2048 + col);
-                        S::mma(s[2 * n], qa[i], b[0], b[1]);
-                        S::mma(s[2 * n + 1], qa[i], b[2], b[3]);
-                    }
-                }
-            } else {
+                for (int n = 0; n < S::kKeyTiles; ++n) {
+                    uint32_t k[4];
+                    ldmatrix4(k, at + n * 2048);
+                    if constexpr (!S::kBytes8) {
+                        S::mma(s[n], k, q[i][0], q[i][2]);
+                        if constexpr (kRests) S::mma(r[n], k, q[i][1], q[i][3]);
+                    } else {
 #pragma unroll
-                for (int i = 0; i < kSteps; i += 2) {
-                    const uint32_t col = (((i & 7) + (lane_mat & 1)) ^ lane_row) << 4;
-#pragma unroll
-                    for (int n = 0; n < S::kScoreTiles / 2; ++n) {
-                        uint32_t b[4];
-                        ldmatrix4(b, lane_at + (i >> 3) * (kKeys * 128) + n * 2048 + col);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            S::mma(s[2 * n + (j >> 1)], qa[i + (j & 1)], e4m3x2_to_f16x2(b[j]), e4m3x2_to_f16x2(b[j] >> 16));
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t a[4] = {e4m3x2_to_f16x2(k[2 * j]), e4m3x2_to_f16x2(k[2 * j + 1]),
+                                                   e4m3x2_to_f16x2(k[2 * j] >> 16), e4m3x2_to_f16x2(k[2 * j + 1] >> 16)};
+                            S::mma(s[n], a, q[i + j][0], q[i + j][2]);
+                            if constexpr (kRests) S::mma(r[n], a, q[i + j][1], q[i + j][3]);
+                        }
                     }
                 }
             }
         }
         release_item();
         load_values();      // of the next unit
-        float top = -INFINITY;
+        float top0 = -INFINITY, top1 = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < S::kScoreTiles; ++i)
+        for (int i = 0; i < S::kKeyTiles; ++i)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 4; ++j) {
                 // an infinite score stands: a remainder of 0 times an infinite key is NaN
-                s[i][j] = (isinf(s[i][j]) ? s[i][j] : s[i][j] + s[i][j + 2]) * sc;
+                if constexpr (kRests) s[i][j] = isinf(s[i][j]) ? s[i][j] : s[i][j] + r[i][j];
+                s[i][j] *= j & 1 ? sc1 : sc0;
                 if (edge) {
-                    const uint32_t key = base + 8 * i + 2 * t + j;
+                    const uint32_t key = base + 16 * i + g + (j & 2 ? 8 : 0);
                     if (key < cp.row.from || key >= cp.row.end) s[i][j] = -INFINITY;
                 }
-                top = fmaxf(top, s[i][j]);
+                if (j & 1) top1 = fmaxf(top1, s[i][j]);
+                else top0 = fmaxf(top0, s[i][j]);
             }
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        const float mn = fmaxf(m, top);
-        if (__any_sync(~0u, mn != m)) {
-            const float f = mn == -INFINITY ? 1.f : exp2_approx(m - mn);
-            const float f0 = __shfl_sync(~0u, f, 8 * t), f1 = __shfl_sync(~0u, f, 8 * t + 4);
-            l *= f;
+#pragma unroll
+        for (int b = 4; b <= 16; b <<= 1) {
+            top0 = fmaxf(top0, __shfl_xor_sync(~0u, top0, b));
+            top1 = fmaxf(top1, __shfl_xor_sync(~0u, top1, b));
+        }
+        top0 = fmaxf(m0, top0);
+        top1 = fmaxf(m1, top1);
+        if (__any_sync(~0u, top0 != m0 || top1 != m1)) {
+            const float f0 = top0 == -INFINITY ? 1.f : exp2_approx(m0 - top0), f1 = top1 == -INFINITY ? 1.f : exp2_approx(m1 - top1);
+            l0 *= f0;
+            l1 *= f1;
 #pragma unroll
             for (int i = 0; i < kTiles; ++i) {
                 o[i][0] *= f0;
@@ -528,16 +541,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 o[i][2] *= f0;
                 o[i][3] *= f1;
             }
-            m = mn;
+            m0 = top0;
+            m1 = top1;
         }
-        const float shift = (mn == -INFINITY ? 0.f : mn) - S::kBias;
-        uint32_t w[S::kScoreTiles][2];          // weights of keys 2 t and 2 t + 1: value and remainder
+        const float shift0 = (m0 == -INFINITY ? 0.f : m0) - S::kBias, shift1 = (m1 == -INFINITY ? 0.f : m1) - S::kBias;
+        // weights, transposed to a B operand: head g, keys 2 t and 2 t + 1 of each eight
+        uint32_t w[S::kKeyTiles][2], w_rest[S::kKeyTiles][2];
 #pragma unroll
-        for (int i = 0; i < S::kScoreTiles; ++i) {
-            const float a = exp2_approx(s[i][0] - shift), b = exp2_approx(s[i][1] - shift);
-            l += a + b;
-            S::split(a, b, w[i][0], w[i][1]);
-        }
+        for (int i = 0; i < S::kKeyTiles; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float a = exp2_approx(s[i][2 * j] - shift0), b = exp2_approx(s[i][2 * j + 1] - shift1);
+                l0 += a;
+                l1 += b;
+                uint32_t value, rest;
+                S::split(a, b, value, rest);
+                w[i][j] = movmatrix(value);
+                if constexpr (kWeightRests) w_rest[i][j] = movmatrix(rest);
+            }
 
         wait_item();
         item = ring + slot_out * kItemBytes;
@@ -549,8 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int i = 0; i < kTiles; ++i) {
                     uint32_t a[4];
                     ldmatrix4_trans(a, lane_at + (i >> 2) * (kKeys * 128) + (((2 * (i & 3) + (lane_mat & 1)) ^ lane_row) << 4));
-                    S::mma(o[i], a, w[2 * kk][0], w[2 * kk + 1][0]);
-                    S::mma(o[i], a, w[2 * kk][1], w[2 * kk + 1][1]);
+                    S::mma(o[i], a, w[kk][0], w[kk][1]);
+                    if constexpr (kWeightRests) S::mma(o[i], a, w_rest[kk][0], w_rest[kk][1]);
                 }
             } else {
                 const uint32_t lane_at = item + (16 * kk + (lane_mat & 1) * 8 + lane_row) * 128;
@@ -563,8 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
                         const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y),
                                                e4m3x2_to_f16x2(y >> 16)};
-                        S::mma(o[i + j], a, w[2 * kk][0], w[2 * kk + 1][0]);
-                        S::mma(o[i + j], a, w[2 * kk][1], w[2 * kk + 1][1]);
+                        S::mma(o[i + j], a, w[kk][0], w[kk][1]);
+                        if constexpr (kWeightRests) S::mma(o[i + j], a, w_rest[kk][0], w_rest[kk][1]);
                     }
                 }
             }
@@ -574,15 +595,21 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
         const bool ends = cp.unit + 1 == cp.row.units;
         if (ends || !left) {
-            l += __shfl_xor_sync(~0u, l, 1);
-            l += __shfl_xor_sync(~0u, l, 2);
+#pragma unroll
+            for (int b = 4; b <= 16; b <<= 1) {
+                l0 += __shfl_xor_sync(~0u, l0, b);
+                l1 += __shfl_xor_sync(~0u, l1, b);
+            }
             if (begun && ends) {
                 const Place at = place_of(p, cp.request, cp.head);
-                const float r = scale_of(p, l), r0 = __shfl_sync(~0u, r, 8 * t), r1 = __shfl_sync(~0u, r, 8 * t + 4);
+                const float r0 = scale_of(p, l0), r1 = scale_of(p, l1);
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i)
                     store_tile<S>(p, at, i, lane, make_float4(o[i][0], o[i][1], o[i][2], o[i][3]), r0, r1);
-                if (t == 0) store_lse<S>(p, at, g, m, l);
+                if (g == 0) {
+                    store_lse<S>(p, at, 2 * t, m0, l0);
+                    store_lse<S>(p, at, 2 * t + 1, m1, l1);
+                }
             } else {
                 const int slot = 2 * warp + (begun ? 1 : 0);
                 // at the end of the warp's part its ring is free, and holds the sums until they are joined
@@ -591,7 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 to += lane;
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) to[32 * i] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-                if (t == 0) s_ml[slot][g] = make_float2(m, l);
+                if (g == 0) {
+                    s_ml[slot][2 * t] = make_float2(m0, l0);
+                    s_ml[slot][2 * t + 1] = make_float2(m1, l1);
+                }
                 if (lane == 0) {
                     s_row[slot] = cp.request * p.head_rows + cp.head;
                     s_flags[slot] = (begun ? 1u : 0u) | (ends ? 2u : 0u) | (left ? 4u : 0u);
@@ -756,17 +786,19 @@ struct Instance {
 };
 
 template <int kDtype, int kWidth>
-Instance instance() {
-    return Instance{attention_kernel<kDtype, kWidth>, join_kernel<kDtype, kWidth>, kWidth, (uint32_t)Shape<kDtype, kWidth>::kKeys};
+Instance instance(bool rests) {
+    return Instance{rests ? attention_kernel<kDtype, kWidth, true> : attention_kernel<kDtype, kWidth, false>,
+                    join_kernel<kDtype, kWidth>, kWidth, (uint32_t)Shape<kDtype, kWidth>::kKeys};
 }
 
 // Head widths are padded to 64, 128 or 256 elements, 8-bit ones to a whole 128-byte row (128 or 256).
-Instance instance_of(const ninfer_kv_cache *c) {
-    const bool narrow = c->head_dim <= 64, half = c->head_dim <= 128;
-    if (c->dtype == NINFER_E4M3) return half ? instance<NINFER_E4M3, 128>() : instance<NINFER_E4M3, 256>();
+Instance instance_of(const ninfer_kv_cache *c, int q_dtype, int out_dtype) {
+    const bool narrow = c->head_dim <= 64, half = c->head_dim <= 128, bf = c->dtype == NINFER_BF16;
+    const bool rests = bf ? q_dtype != NINFER_BF16 : q_dtype == NINFER_F32 || out_dtype != NINFER_BF16;
+    if (c->dtype == NINFER_E4M3) return half ? instance<NINFER_E4M3, 128>(rests) : instance<NINFER_E4M3, 256>(rests);
     if (c->dtype == NINFER_F16)
-        return narrow ? instance<NINFER_F16, 64>() : half ? instance<NINFER_F16, 128>() : instance<NINFER_F16, 256>();
-    return narrow ? instance<NINFER_BF16, 64>() : half ? instance<NINFER_BF16, 128>() : instance<NINFER_BF16, 256>();
+        return narrow ? instance<NINFER_F16, 64>(rests) : half ? instance<NINFER_F16, 128>(rests) : instance<NINFER_F16, 256>(rests);
+    return narrow ? instance<NINFER_BF16, 64>(rests) : half ? instance<NINFER_BF16, 128>(rests) : instance<NINFER_BF16, 256>(rests);
 }
 
 struct Layout {
@@ -808,7 +840,7 @@ extern "C" int ninfer_kv_attention_workspace(const ninfer_kv_cache *cache, uint6
     DeviceInfo d;
     st = device_info(&d);
     if (st) return st;
-    *bytes = layout(d.sms, instance_of(cache).width).bytes;
+    *bytes = layout(d.sms, instance_of(cache, NINFER_F32, NINFER_F32).width).bytes;
     return NINFER_OK;
 }
 
@@ -838,7 +870,7 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     DeviceInfo d;
     st = device_info(&d);
     if (st) return st;
-    const Instance in = instance_of(cache);
+    const Instance in = instance_of(cache, q_dtype, out_dtype);
     const Layout w = layout(d.sms, in.width);
     if (!workspace || workspace_bytes < w.bytes)
         return fail(NINFER_ERR_SIZE_MISMATCH, "attention: workspace of %llu bytes needed, %llu given",
