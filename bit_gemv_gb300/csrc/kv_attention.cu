@@ -98,13 +98,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
 
 // What depends on the cache's type and the padded head width. Operands of the
 // tensor cores are bfloat16 for a bfloat16 cache and binary16 for the other two.
-template <int kDtype, int kWidth>
+template <int kDtype, int kWidth_, int kUsed>
 struct Shape {
+    static constexpr int kWidth = kWidth_;                      // elements of a row in shared memory
     static constexpr bool kBf16 = kDtype == NINFER_BF16, kBytes8 = kDtype == NINFER_E4M3;
     static constexpr int kEs = kBytes8 ? 1 : 2;
     static constexpr int kKeys = kItemBytes / (kWidth * kEs);   // of a unit: 16, 32 or 64
-    static constexpr int kChunks = kWidth * kEs / 128;          // 128-byte columns of an item
-    static constexpr int kSteps = kWidth / 16;                  // 16-element steps of a row
+    static constexpr int kSteps = kUsed / 16;                   // 16-element steps of a row that are computed
     static constexpr int kKeyTiles = kKeys / 16;
     // binary16 weights carry a factor 2^14: weights down to 2^-38 of the largest one keep a value
     static constexpr float kBias = kBf16 ? 0.f : 14.f;
@@ -250,10 +250,9 @@ __device__ __forceinline__ float scale_of(const AttentionParams &p, float l) { r
 // the operand type holds) and the output is rounded far more coarsely than the
 // weights: binary16 weights (2^-12) and a bfloat16 result (2^-9), whose error grows by
 // less than 1 %. bfloat16 weights always have theirs.
-template <int kDtype, int kWidth, bool kRests>
+template <class S, bool kRests>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttentionParams p) {
-    using S = Shape<kDtype, kWidth>;
-    constexpr int kKeys = S::kKeys, kSteps = S::kSteps, kTiles = kWidth / 16, kPart = kTiles * 32;
+    constexpr int kKeys = S::kKeys, kWidth = S::kWidth, kSteps = S::kSteps, kTiles = kSteps, kPart = kTiles * 32;
     extern __shared__ uint8_t ring_raw[];
     __shared__ uint64_t s_sum[kWarps], s_upto[kThreads];
     __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
@@ -722,10 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 // Joins the rows that were cut between CTAs: block (c, tile) takes the row whose
 // first part is CTA c's tail, if there is one, through the head parts of the
 // following CTAs up to the one that ends it.
-template <int kDtype, int kWidth>
+template <class S>
 __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ AttentionParams p, uint32_t ctas) {
-    using S = Shape<kDtype, kWidth>;
-    constexpr int kTiles = kWidth / 16, kPart = kTiles * 32;
+    constexpr int kPart = S::kSteps * 32;
     __shared__ uint32_t s_last;
     __shared__ float4 s_ml[kWarps][4], s_o[kWarps][32];     // m and l of heads 2 t and 2 t + 1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, t = lane & 3;
@@ -782,23 +780,34 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
 // ------------------------------------------------------------------ host ---
 struct Instance {
     void (*attention)(const AttentionParams), (*join)(const AttentionParams, uint32_t);
-    uint32_t width, keys;
+    uint32_t used, keys;
 };
 
-template <int kDtype, int kWidth>
+template <int kDtype, int kWidth, int kUsed>
 Instance instance(bool rests) {
-    return Instance{rests ? attention_kernel<kDtype, kWidth, true> : attention_kernel<kDtype, kWidth, false>,
-                    join_kernel<kDtype, kWidth>, kWidth, (uint32_t)Shape<kDtype, kWidth>::kKeys};
+    using S = Shape<kDtype, kWidth, kUsed>;
+    return Instance{rests ? attention_kernel<S, true> : attention_kernel<S, false>, join_kernel<S>, kUsed, (uint32_t)S::kKeys};
 }
 
-// Head widths are padded to 64, 128 or 256 elements, 8-bit ones to a whole 128-byte row (128 or 256).
+// Rows are 128, 256 or 512 bytes in shared memory (64, 128 or 256 elements, of 8 bits 128 or 256).
+// HBM bounds 16-bit caches whatever is computed of the padding; the 8-bit ones, whose
+// conversions and products nearly fill the time of their copies, compute no more than needed.
 Instance instance_of(const ninfer_kv_cache *c, int q_dtype, int out_dtype) {
-    const bool narrow = c->head_dim <= 64, half = c->head_dim <= 128, bf = c->dtype == NINFER_BF16;
-    const bool rests = bf ? q_dtype != NINFER_BF16 : q_dtype == NINFER_F32 || out_dtype != NINFER_BF16;
-    if (c->dtype == NINFER_E4M3) return half ? instance<NINFER_E4M3, 128>(rests) : instance<NINFER_E4M3, 256>(rests);
+    const uint64_t dim = c->head_dim;
+    const bool bf = c->dtype == NINFER_BF16, rests = bf ? q_dtype != NINFER_BF16 : q_dtype == NINFER_F32 || out_dtype != NINFER_BF16;
+    if (c->dtype == NINFER_E4M3)
+        return dim <= 64    ? instance<NINFER_E4M3, 128, 64>(rests)
+               : dim <= 96  ? instance<NINFER_E4M3, 128, 96>(rests)
+               : dim <= 128 ? instance<NINFER_E4M3, 128, 128>(rests)
+               : dim <= 192 ? instance<NINFER_E4M3, 256, 192>(rests)
+                            : instance<NINFER_E4M3, 256, 256>(rests);
     if (c->dtype == NINFER_F16)
-        return narrow ? instance<NINFER_F16, 64>(rests) : half ? instance<NINFER_F16, 128>(rests) : instance<NINFER_F16, 256>(rests);
-    return narrow ? instance<NINFER_BF16, 64>(rests) : half ? instance<NINFER_BF16, 128>(rests) : instance<NINFER_BF16, 256>(rests);
+        return dim <= 64    ? instance<NINFER_F16, 64, 64>(rests)
+               : dim <= 128 ? instance<NINFER_F16, 128, 128>(rests)
+                            : instance<NINFER_F16, 256, 256>(rests);
+    return dim <= 64    ? instance<NINFER_BF16, 64, 64>(rests)
+           : dim <= 128 ? instance<NINFER_BF16, 128, 128>(rests)
+                        : instance<NINFER_BF16, 256, 256>(rests);
 }
 
 struct Layout {
@@ -840,7 +849,7 @@ extern "C" int ninfer_kv_attention_workspace(const ninfer_kv_cache *cache, uint6
     DeviceInfo d;
     st = device_info(&d);
     if (st) return st;
-    *bytes = layout(d.sms, instance_of(cache, NINFER_F32, NINFER_F32).width).bytes;
+    *bytes = layout(d.sms, instance_of(cache, NINFER_F32, NINFER_F32).used).bytes;
     return NINFER_OK;
 }
 
@@ -871,7 +880,7 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     st = device_info(&d);
     if (st) return st;
     const Instance in = instance_of(cache, q_dtype, out_dtype);
-    const Layout w = layout(d.sms, in.width);
+    const Layout w = layout(d.sms, in.used);
     if (!workspace || workspace_bytes < w.bytes)
         return fail(NINFER_ERR_SIZE_MISMATCH, "attention: workspace of %llu bytes needed, %llu given",
                     (unsigned long long)w.bytes, (unsigned long long)(workspace ? workspace_bytes : 0));
@@ -925,6 +934,6 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     st = launch_dependent("attention", in.attention, dim3(p.by_row ? (unsigned)rows : d.sms), dim3(kThreads), kSmem,
                           (cudaStream_t)stream, p);
     if (st || p.by_row) return st;
-    return launch_dependent("attention join", in.join, dim3(d.sms, in.width / 16), dim3(kThreads), 0, (cudaStream_t)stream, p,
+    return launch_dependent("attention join", in.join, dim3(d.sms, in.used / 16), dim3(kThreads), 0, (cudaStream_t)stream, p,
                             (uint32_t)d.sms);
 }
