@@ -348,25 +348,31 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
     };
     const uint32_t unit = lane & (kRowUnits - 1), unit_row = lane / kRowUnits;
+    const uint32_t column = (unit >> 3) * (kKeys * 128) + unit_row * 128, turn = ((unit & 7) ^ (unit_row & 7)) << 4;
+    const uint32_t in_piece = (1u << p.piece_log) - 1;
     auto load_item = [&](const uint8_t *pool) {
-        const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys;
-        const uint32_t to = ring + slot_in * kItemBytes + (unit >> 3) * (kKeys * 128);
+        // keys before `lo` or from `hi` on, and all of a unit past the head, are filled with zeros
+        const uint32_t base = (ld.row.from / kKeys + ld.unit) * kKeys + unit_row;
+        const uint32_t lo = ld.row.from > base ? ld.row.from - base : 0u;
+        const uint32_t hi = unit * (16 / S::kEs) < p.head_dim && ld.row.end > base ? ld.row.end - base : 0u;
+        const uint32_t to = ring + slot_in * kItemBytes + column;
         const uint64_t head = p.tiles.div(ld.head) * p.head_bytes;
-        const uint8_t *at[kPieces];
+        uint64_t at[kPieces];
 #pragma unroll
         for (int i = 0; i < kPieces; ++i)
-            at[i] = (uint32_t)page[i] < p.pages ? pool + (uint32_t)page[i] * p.page_bytes + token[i] * p.token_bytes + head : nullptr;
+            at[i] = (uint32_t)page[i] < p.pages ? reinterpret_cast<uint64_t>(pool) + (uint32_t)page[i] * p.page_bytes + token[i] * p.token_bytes + head : 0u;
+        const uint64_t none = reinterpret_cast<uint64_t>(pool), own = unit * 16;
 #pragma unroll
         for (int k = 0; k < kKeys / kRowsAtOnce; ++k) {
-            const uint32_t r = k * kRowsAtOnce + unit_row, q = r >> p.piece_log;
-            uint64_t from = __shfl_sync(~0u, reinterpret_cast<uint64_t>(at[0]), q & 31);
+            const uint32_t r = k * kRowsAtOnce, q = (r + unit_row) >> p.piece_log;
+            uint64_t from = __shfl_sync(~0u, at[0], q & 31);
             if (kPieces > 1) {
-                const uint64_t more = __shfl_sync(~0u, reinterpret_cast<uint64_t>(at[kPieces - 1]), q & 31);
+                const uint64_t more = __shfl_sync(~0u, at[kPieces - 1], q & 31);
                 if (q >= 32) from = more;
             }
-            const bool on = from && base + r >= ld.row.from && base + r < ld.row.end && unit * (16 / S::kEs) < p.head_dim;
-            from += (r & ((1u << p.piece_log) - 1)) * p.token_bytes + unit * 16;
-            copy16(to + r * 128 + (((unit & 7) ^ (r & 7)) << 4), on ? reinterpret_cast<const uint8_t *>(from) : pool, on ? 16 : 0);
+            const bool on = from && r >= lo && r < hi;
+            from += ((r + unit_row) & in_piece) * p.token_bytes + own;
+            copy16(to + r * 128 + (turn ^ (r & 7) << 4), reinterpret_cast<const uint8_t *>(on ? from : none), on ? 16 : 0);
         }
         slot_in = slot_in == kItems - 1 ? 0 : slot_in + 1;
     };
@@ -421,16 +427,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             float2 x[kSteps][2];
             const bool wide = p.q_dtype == NINFER_F32;
 #pragma unroll
-            for (int i = 0; i < kSteps; ++i)
+            for (int i = 0; i < kSteps; ++i) x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+            // head_dim ends on a multiple of 8 (8-bit caches: 16), so that the lanes of a load stop together
+            if (wide && h < p.group) {
+                const float2 *from = reinterpret_cast<const float2 *>(static_cast<const float *>(p.q) + at + (S::kBytes8 ? 4 : 2) * t);
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const uint32_t e = 16 * i + (S::kBytes8 ? 4 * t + 2 * j : 2 * t + 8 * j);
-                    const bool on = h < p.group && e < p.head_dim;
-                    x[i][j] = make_float2(0.f, 0.f);
-                    if (on && wide) x[i][j] = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.q) + at + e);
-                    if (on && !wide)
-                        x[i][j].x = __uint_as_float(*reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) + at + e));
-                }
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (16 * i + (S::kBytes8 ? 0 : 8 * j) < (int)p.head_dim) x[i][j] = from[8 * i + (S::kBytes8 ? j : 4 * j)];
+            } else if (h < p.group) {
+                const uint32_t *from = reinterpret_cast<const uint32_t *>(static_cast<const uint16_t *>(p.q) + at + (S::kBytes8 ? 4 : 2) * t);
+#pragma unroll
+                for (int i = 0; i < kSteps; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (16 * i + (S::kBytes8 ? 0 : 8 * j) < (int)p.head_dim)
+                            x[i][j].x = __uint_as_float(from[8 * i + (S::kBytes8 ? j : 4 * j)]);
+            }
             if (!primed) {
                 load_keys();
                 load_values();
