@@ -17,8 +17,8 @@
 //
 // Split. The keys of every (request, key head, 8 query heads) are cut into
 // units of 8 KB of keys and 8 KB of values; all units of the call form one
-// line, of which each CTA (one an SM) and in it each warp takes an equal,
-// contiguous part, so that any mix of lengths keeps every SM busy to the end.
+// line, on which a row's beginning counts as some units more, and of which each CTA (one
+// an SM) and in it each warp takes an equal, contiguous part, so that any mix of lengths keeps every SM busy to the end.
 // A warp writes a row that lies in its part whole; cut rows are joined in the CTA,
 // and rows cut between CTAs by a second, small kernel.
 //
@@ -39,6 +39,10 @@ constexpr int kWarps = 8, kThreads = 32 * kWarps, kItems = 3;
 constexpr uint32_t kItemBytes = 8192;
 constexpr uint32_t kRingBytes = kWarps * kItems * kItemBytes;
 constexpr uint32_t kNone = 0xffffffffu, kRowKeys = 1024;
+// What beginning a row costs, in units: its queries, its first copies, its output. 0, 1, 2, 3 and 4
+// measured 42.7, 41.4, 40.5, 39.5 and 39.6 us for 32 requests of 200 to 4500 keys and 24.2, 21.7, 20.2,
+// 20.2 and 21.5 us for 24 of 1 to 3001 with 16 key heads each; no change for long rows.
+constexpr uint32_t kRowCost = 3;
 
 struct AttentionParams {
     const uint8_t *k, *v;
@@ -267,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
     // ---- this warp's part of the line ----
     Cursor ld;
-    uint32_t left = 0;          // units of this warp
+    uint32_t left = 0;          // of this warp's part: units, and kRowCost for each row that begins after the first
     bool empties = false;       // whether any request has no keys
     if (p.by_row) {
         ld.request = p.heads.div(blockIdx.x);
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         uint64_t mine = 0;
         for (uint32_t r = r0; r < r1; ++r) {
             const uint32_t units = row_of<kKeys>(p, r).units;
-            mine += units;
+            mine += units ? units + kRowCost : 0u;
             empties |= units == 0;
         }
         mine *= p.head_rows;
@@ -319,15 +323,24 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             const uint32_t run = 32 * w + k;
             ld.request = run * p.run;
             ld.row = row_of<kKeys>(p, ld.request);
-            for (uint64_t size; at >= (size = (uint64_t)ld.row.units * p.head_rows); ld.row = row_of<kKeys>(p, ++ld.request)) at -= size;
-            ld.head = at >> 32 ? (uint32_t)(at / ld.row.units) : (uint32_t)at / ld.row.units;
-            ld.unit = (uint32_t)(at - (uint64_t)ld.head * ld.row.units);
+            uint32_t size = ld.row.units ? ld.row.units + kRowCost : 0u;        // of one of the request's rows
+            while (at >= (uint64_t)size * p.head_rows) {
+                at -= (uint64_t)size * p.head_rows;
+                ld.row = row_of<kKeys>(p, ++ld.request);
+                size = ld.row.units ? ld.row.units + kRowCost : 0u;
+            }
+            ld.head = at >> 32 ? (uint32_t)(at / size) : (uint32_t)at / size;
+            const uint32_t in_row = (uint32_t)(at - (uint64_t)ld.head * size), paid = min(in_row, kRowCost);
+            ld.unit = in_row - paid;
+            left -= min(left, kRowCost - paid);
         }
     }
 
     // ---- the ring: keys and values of the units in turn ----
     Cursor cp = ld;
-    uint32_t keys_due = left, values_due = left, slot_in = 0, slot_out = 0;
+    // A part that ends within the cost of a row's beginning leaves that row to the next part.
+    auto spend = [](uint32_t left, bool row_ends) { return --left, row_ends ? left - min(left, kRowCost) : left; };
+    uint32_t due = left, slot_in = 0, slot_out = 0;         // due: of what is not loaded yet
     constexpr int kRowUnits = kWidth * S::kEs / 16, kRowsAtOnce = 32 / kRowUnits;   // 16-byte units a row, rows a copy of the warp
     constexpr int kPieces = (kKeys + 31) / 32;
     // The unit that is loaded next is in pieces of 2^piece_log keys, each within one page; lane q has pieces q and q + 32.
@@ -378,16 +391,14 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
     // one group an item, empty ones at the end, so that the oldest of three is always the one waited for
     auto load_keys = [&] {
-        if (keys_due) {
-            --keys_due;
-            load_item(p.k);
-        }
+        if (due) load_item(p.k);
         copies_commit();
     };
     auto load_values = [&] {
-        if (values_due) {
+        if (due) {
             load_item(p.v);
-            if (--values_due) {
+            due = spend(due, ld.unit + 1 == ld.row.units);
+            if (due) {
                 advance<kKeys>(p, ld);
                 find_pages();       // read early: the next unit's keys are asked for half a unit later
             }
@@ -413,7 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
     constexpr bool kWeightRests = S::kBf16 || kRests;
     while (left) {
-        --left;
+        const bool ends = cp.unit + 1 == cp.row.units;
+        left = spend(left, ends);
         if (fresh) {
             fresh = false;
             begun = cp.unit == 0;
@@ -606,7 +618,6 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         release_item();
         load_keys();        // of the unit after that
 
-        const bool ends = cp.unit + 1 == cp.row.units;
         if (ends || !left) {
 #pragma unroll
             for (int b = 4; b <= 16; b <<= 1) {

@@ -20,7 +20,7 @@ struct TablesParams {
     int64_t *slots;
     int32_t *positions, *rows, *offsets, *lengths_out, *counts, *status;
     uint64_t table_stride;
-    uint32_t requests, run, table_pages, free_count, capacity;
+    uint32_t requests, run, table_pages, free_count, capacity, vectors;
     FastDiv page;
 };
 
@@ -117,42 +117,60 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
         if (bad && p.status) atomicOr(p.status, bad);
     }
 
-    // outputs by token; the first new token of a fresh page also enters the page
+    // outputs by token, four neighbours a thread (of one request, mostly: one search); the first new
+    // token of a fresh page also enters the page
     const uint64_t all = max(total, (uint64_t)p.capacity);
-    for (uint64_t k = (uint64_t)blockIdx.x * kThreads + tid; k < all; k += (uint64_t)gridDim.x * kThreads) {
-        if (k >= total) {
-            if (p.slots) p.slots[k] = -1;
-            if (p.positions) p.positions[k] = -1;
-            if (p.rows) p.rows[k] = -1;
-            continue;
-        }
-        uint32_t lo = 0;                     // last thread whose run starts at or before k
+    for (uint64_t k0 = 4 * ((uint64_t)blockIdx.x * kThreads + tid); k0 < all; k0 += 4ull * gridDim.x * kThreads) {
+        uint32_t lo = 0;                     // last thread whose run starts at or before k0
 #pragma unroll
         for (uint32_t s = kThreads / 2; s; s >>= 1)
-            if (s_tokens[lo + s] <= k) lo += s;
+            if (s_tokens[lo + s] <= k0) lo += s;
         uint64_t at = s_tokens[lo], base = s_pages[lo];
         uint32_t i = lo * p.run;
-        Request r = request(p, i);
-        while (k >= at + r.fresh) {          // ends: k < total
-            at += r.fresh;
-            base += r.pages;
-            r = request(p, ++i);
-        }
-        const uint32_t pos = r.length + (uint32_t)(k - at), pi = p.page.div(pos), in = pos - pi * p.page.d;
-        int32_t *entry = p.table + i * p.table_stride + pi;
-        int32_t page = -1;
-        if (pi < p.table_pages) {
-            if (pi < r.held) page = *entry;
-            else {
-                const uint64_t q = base + (pi - r.held);
-                if (q < p.free_count) page = p.free_pages[q];
-                if (in == 0) *entry = page;
+        Request r = {};
+        if (k0 < total) r = request(p, i);
+        int64_t slot[4];
+        int32_t position[4], row[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t k = k0 + j;
+            slot[j] = position[j] = row[j] = -1;
+            if (k >= total) continue;
+            while (k >= at + r.fresh) {      // ends: k < total
+                at += r.fresh;
+                base += r.pages;
+                r = request(p, ++i);
             }
+            const uint32_t pos = r.length + (uint32_t)(k - at), pi = p.page.div(pos), in = pos - pi * p.page.d;
+            int32_t page = -1;
+            if (pi < p.table_pages) {
+                int32_t *entry = p.table + i * p.table_stride + pi;
+                if (pi < r.held) page = *entry;
+                else {
+                    const uint64_t q = base + (pi - r.held);
+                    if (q < p.free_count) page = p.free_pages[q];
+                    if (in == 0) *entry = page;
+                }
+            }
+            slot[j] = page < 0 ? -1 : (int64_t)page * p.page.d + in;
+            position[j] = clamp31(pos);
+            row[j] = (int32_t)i;
         }
-        if (k < p.capacity) {
-            if (p.slots) p.slots[k] = page < 0 ? -1 : (int64_t)page * p.page.d + in;
-            if (p.positions) p.positions[k] = clamp31(pos);
-            if (p.rows) p.rows[k] = (int32_t)i;
+        if (p.vectors && k0 + 4 <= p.capacity) {
+            if (p.slots) {
+                reinterpret_cast<longlong2 *>(p.slots + k0)[0] = make_longlong2(slot[0], slot[1]);
+                reinterpret_cast<longlong2 *>(p.slots + k0)[1] = make_longlong2(slot[2], slot[3]);
+            }
+            if (p.positions) *reinterpret_cast<int4 *>(p.positions + k0) = make_int4(position[0], position[1], position[2], position[3]);
+            if (p.rows) *reinterpret_cast<int4 *>(p.rows + k0) = make_int4(row[0], row[1], row[2], row[3]);
+            continue;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (k0 + j >= p.capacity) break;
+            if (p.slots) p.slots[k0 + j] = slot[j];
+            if (p.positions) p.positions[k0 + j] = position[j];
+            if (p.rows) p.rows[k0 + j] = row[j];
         }
     }
 }
@@ -200,8 +218,9 @@ extern "C" int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_token
     p.table_pages = (uint32_t)table_pages;
     p.free_count = (uint32_t)free_count;
     p.capacity = (uint32_t)capacity;
+    p.vectors = aligned(slots, 16) && aligned(positions, 16) && aligned(token_rows, 16);
     p.page = FastDiv((uint32_t)page_size);
-    const uint64_t work = capacity > requests ? capacity : requests;
+    const uint64_t work = capacity / 4 > requests ? capacity / 4 : requests;
     const uint64_t want = (work + kThreads - 1) / kThreads;
     return launch_dependent("tables", tables_kernel, dim3((unsigned)(want < 304 ? want : 304)), dim3(kThreads), 0,
                             (cudaStream_t)stream, p);
