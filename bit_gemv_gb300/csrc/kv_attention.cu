@@ -12,8 +12,7 @@
 //   values   A = 16 elements of the values transposed (ldmatrix.trans), B = 8 heads' weights,
 //            transposed from the scores' accumulators in the registers (movmatrix).
 // The 8 heads of a row are the narrow side of both, so that a group of eight wastes
-// nothing. 32-bit operands enter as a 16-bit value and the 16-bit remainder, one
-// mma each.
+// nothing. 32-bit operands enter as sums of 16-bit terms, one mma each.
 //
 // Split. The keys of every (request, key head, 8 query heads) are cut into
 // units of 8 KB of keys and 8 KB of values; all units of the call form one
@@ -125,11 +124,16 @@ struct Shape {
         if (kBf16) return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
         return __half22float2(*reinterpret_cast<const __half2 *>(&u));
     }
-    // x as a 16-bit value and the 16-bit remainder
-    static __device__ __forceinline__ void split(float a, float b, uint32_t &value, uint32_t &rest) {
-        value = pack(a, b);
-        const float2 f = unpack(value);
-        rest = pack(a - f.x, b - f.y);
+    // x as a sum of 16-bit values: the nearest one, the nearest to what remains, and so on
+    template <int kTerms>
+    static __device__ __forceinline__ void split(float a, float b, uint32_t (&term)[kTerms]) {
+#pragma unroll
+        for (int i = 0; i < kTerms; ++i) {
+            term[i] = pack(a, b);
+            const float2 f = unpack(term[i]);
+            a -= f.x;
+            b -= f.y;
+        }
     }
     static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
         if (kBf16)
@@ -250,13 +254,15 @@ __device__ __forceinline__ void store_lse(const AttentionParams &p, const Place 
 // What the sums of a row are multiplied by in the end; a row without weights gives zeros.
 __device__ __forceinline__ float scale_of(const AttentionParams &p, float l) { return l == 0.f ? 0.f : p.v_scale / l; }
 
-// kRests: whether remainders take part. They do not where they are zeros (a 16-bit q that
-// the operand type holds) and the output is rounded far more coarsely than the
-// weights: binary16 weights (2^-12) and a bfloat16 result (2^-9), whose error grows by
-// less than 1 %. bfloat16 weights always have theirs.
-template <class S, bool kRests>
+// kFull: as exact as fp32 operands. Queries and weights then enter as three bfloat16
+// or two binary16 terms (24 and 22 bits). Otherwise the queries are of a 16-bit type
+// that one term holds, and the output is rounded to 16 bits: weights have two
+// bfloat16 terms (one would add as much error as that rounding), and one binary16
+// term where the output is bfloat16 (2^-12 against 2^-9: the error grows by less than 1 %).
+template <class S, bool kFull>
 __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_constant__ AttentionParams p) {
     constexpr int kKeys = S::kKeys, kWidth = S::kWidth, kSteps = S::kSteps, kTiles = kSteps, kPart = kTiles * 32;
+    constexpr int kQueryTerms = kFull ? S::kBf16 ? 3 : 2 : 1, kWeightTerms = S::kBf16 ? kFull ? 3 : 2 : kFull ? 2 : 1;
     extern __shared__ uint8_t ring_raw[];
     __shared__ uint64_t s_sum[kWarps], s_upto[kThreads];
     __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
@@ -416,13 +422,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     };
 
     // ---- the units ----
-    // q[i]: elements 16 i .. 16 i + 15 of head g, value and remainder of the two halves of a B operand.
+    // q[i][j]: elements 16 i .. 16 i + 15 of head g, the terms of the half j of a B operand.
     // m, l, sc, o: of heads 2 t and 2 t + 1, as an accumulator has them.
-    uint32_t q[kSteps][4];
+    uint32_t q[kSteps][2][kQueryTerms];
     float o[kTiles][4], m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f, sc0 = 0.f, sc1 = 0.f;
     bool fresh = true, begun = false, primed = false;   // a new row's queries are due; it began in this part; loads run
     const uint32_t lane_row = lane & 7, lane_mat = lane >> 3;
-    constexpr bool kWeightRests = S::kBf16 || kRests;
     while (left) {
         const bool ends = cp.unit + 1 == cp.row.units;
         left = spend(left, ends);
@@ -489,8 +494,10 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const float a = x[i][j].x * down, b = x[i][j].y * down;
-                    S::split(a, b, q[i][2 * j], q[i][2 * j + 1]);
-                    if (isinf(a) || isinf(b)) q[i][2 * j + 1] = 0;      // no remainder: inf - inf
+                    S::split(a, b, q[i][j]);
+                    if (isinf(a) || isinf(b))                           // nothing remains: inf - inf
+#pragma unroll
+                        for (int k = 1; k < kQueryTerms; ++k) q[i][j][k] = 0;
                 }
             if (!primed) load_keys();
             primed = true;
@@ -500,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
 
         // scores: keys g and g + 8 of each 16, heads 2 t and 2 t + 1
         wait_item();
-        float s[S::kKeyTiles][4], r[S::kKeyTiles][4];        // of the queries' values, of their remainders
+        float s[S::kKeyTiles][4], r[S::kKeyTiles][4];        // of the queries' first terms, of the others
 #pragma unroll
         for (int i = 0; i < S::kKeyTiles; ++i)
 #pragma unroll
@@ -517,15 +524,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     uint32_t k[4];
                     ldmatrix4(k, at + n * 2048);
                     if constexpr (!S::kBytes8) {
-                        S::mma(s[n], k, q[i][0], q[i][2]);
-                        if constexpr (kRests) S::mma(r[n], k, q[i][1], q[i][3]);
+                        S::mma(s[n], k, q[i][0][0], q[i][1][0]);
+#pragma unroll
+                        for (int m = 1; m < kQueryTerms; ++m) S::mma(r[n], k, q[i][0][m], q[i][1][m]);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint32_t a[4] = {e4m3x2_to_f16x2(k[2 * j]), e4m3x2_to_f16x2(k[2 * j + 1]),
                                                    e4m3x2_to_f16x2(k[2 * j] >> 16), e4m3x2_to_f16x2(k[2 * j + 1] >> 16)};
-                            S::mma(s[n], a, q[i + j][0], q[i + j][2]);
-                            if constexpr (kRests) S::mma(r[n], a, q[i + j][1], q[i + j][3]);
+                            S::mma(s[n], a, q[i + j][0][0], q[i + j][1][0]);
+#pragma unroll
+                            for (int m = 1; m < kQueryTerms; ++m) S::mma(r[n], a, q[i + j][0][m], q[i + j][1][m]);
                         }
                     }
                 }
@@ -538,8 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int i = 0; i < S::kKeyTiles; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                // an infinite score stands: a remainder of 0 times an infinite key is NaN
-                if constexpr (kRests) s[i][j] = isinf(s[i][j]) ? s[i][j] : s[i][j] + r[i][j];
+                // an infinite score stands: a term of 0 times an infinite key is NaN
+                if constexpr (kFull) s[i][j] = isinf(s[i][j]) ? s[i][j] : s[i][j] + r[i][j];
                 s[i][j] *= j & 1 ? sc1 : sc0;
                 if (edge) {
                     const uint32_t key = base + 16 * i + g + (j & 2 ? 8 : 0);
@@ -571,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         }
         const float shift0 = (m0 == -INFINITY ? 0.f : m0) - S::kBias, shift1 = (m1 == -INFINITY ? 0.f : m1) - S::kBias;
         // weights, transposed to a B operand: head g, keys 2 t and 2 t + 1 of each eight
-        uint32_t w[S::kKeyTiles][2], w_rest[S::kKeyTiles][2];
+        uint32_t w[S::kKeyTiles][2][kWeightTerms];
 #pragma unroll
         for (int i = 0; i < S::kKeyTiles; ++i)
 #pragma unroll
@@ -579,10 +588,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 const float a = exp2_approx(s[i][2 * j] - shift0), b = exp2_approx(s[i][2 * j + 1] - shift1);
                 l0 += a;
                 l1 += b;
-                uint32_t value, rest;
-                S::split(a, b, value, rest);
-                w[i][j] = movmatrix(value);
-                if constexpr (kWeightRests) w_rest[i][j] = movmatrix(rest);
+                S::split(a, b, w[i][j]);
+#pragma unroll
+                for (int m = 0; m < kWeightTerms; ++m) w[i][j][m] = movmatrix(w[i][j][m]);
             }
 
         wait_item();
@@ -595,8 +603,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                 for (int i = 0; i < kTiles; ++i) {
                     uint32_t a[4];
                     ldmatrix4_trans(a, lane_at + (i >> 2) * (kKeys * 128) + (((2 * (i & 3) + (lane_mat & 1)) ^ lane_row) << 4));
-                    S::mma(o[i], a, w[kk][0], w[kk][1]);
-                    if constexpr (kWeightRests) S::mma(o[i], a, w_rest[kk][0], w_rest[kk][1]);
+#pragma unroll
+                    for (int m = 0; m < kWeightTerms; ++m) S::mma(o[i], a, w[kk][0][m], w[kk][1][m]);
                 }
             } else {
                 const uint32_t lane_at = item + (16 * kk + (lane_mat & 1) * 8 + lane_row) * 128;
@@ -609,8 +617,8 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                         const uint32_t x = __byte_perm(r[2 * j], 0, 0x3120), y = __byte_perm(r[2 * j + 1], 0, 0x3120);
                         const uint32_t a[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y),
                                                e4m3x2_to_f16x2(y >> 16)};
-                        S::mma(o[i + j], a, w[kk][0], w[kk][1]);
-                        if constexpr (kWeightRests) S::mma(o[i + j], a, w_rest[kk][0], w_rest[kk][1]);
+#pragma unroll
+                        for (int m = 0; m < kWeightTerms; ++m) S::mma(o[i + j], a, w[kk][0][m], w[kk][1][m]);
                     }
                 }
             }
@@ -809,9 +817,9 @@ struct Instance {
 };
 
 template <int kDtype, int kWidth, int kUsed>
-Instance instance(bool rests) {
+Instance instance(bool full) {
     using S = Shape<kDtype, kWidth, kUsed>;
-    return Instance{rests ? attention_kernel<S, true> : attention_kernel<S, false>, join_kernel<S>, kUsed, (uint32_t)S::kKeys};
+    return Instance{full ? attention_kernel<S, true> : attention_kernel<S, false>, join_kernel<S>, kUsed, (uint32_t)S::kKeys};
 }
 
 // Rows are 128, 256 or 512 bytes in shared memory (64, 128 or 256 elements, of 8 bits 128 or 256).
@@ -819,20 +827,20 @@ Instance instance(bool rests) {
 // conversions and products nearly fill the time of their copies, compute no more than needed.
 Instance instance_of(const ninfer_kv_cache *c, int q_dtype, int out_dtype) {
     const uint64_t dim = c->head_dim;
-    const bool bf = c->dtype == NINFER_BF16, rests = bf ? q_dtype != NINFER_BF16 : q_dtype == NINFER_F32 || out_dtype != NINFER_BF16;
+    const bool bf = c->dtype == NINFER_BF16, full = bf ? q_dtype != NINFER_BF16 || out_dtype == NINFER_F32 : q_dtype == NINFER_F32 || out_dtype != NINFER_BF16;
     if (c->dtype == NINFER_E4M3)
-        return dim <= 64    ? instance<NINFER_E4M3, 128, 64>(rests)
-               : dim <= 96  ? instance<NINFER_E4M3, 128, 96>(rests)
-               : dim <= 128 ? instance<NINFER_E4M3, 128, 128>(rests)
-               : dim <= 192 ? instance<NINFER_E4M3, 256, 192>(rests)
-                            : instance<NINFER_E4M3, 256, 256>(rests);
+        return dim <= 64    ? instance<NINFER_E4M3, 128, 64>(full)
+               : dim <= 96  ? instance<NINFER_E4M3, 128, 96>(full)
+               : dim <= 128 ? instance<NINFER_E4M3, 128, 128>(full)
+               : dim <= 192 ? instance<NINFER_E4M3, 256, 192>(full)
+                            : instance<NINFER_E4M3, 256, 256>(full);
     if (c->dtype == NINFER_F16)
-        return dim <= 64    ? instance<NINFER_F16, 64, 64>(rests)
-               : dim <= 128 ? instance<NINFER_F16, 128, 128>(rests)
-                            : instance<NINFER_F16, 256, 256>(rests);
-    return dim <= 64    ? instance<NINFER_BF16, 64, 64>(rests)
-           : dim <= 128 ? instance<NINFER_BF16, 128, 128>(rests)
-                        : instance<NINFER_BF16, 256, 256>(rests);
+        return dim <= 64    ? instance<NINFER_F16, 64, 64>(full)
+               : dim <= 128 ? instance<NINFER_F16, 128, 128>(full)
+                            : instance<NINFER_F16, 256, 256>(full);
+    return dim <= 64    ? instance<NINFER_BF16, 64, 64>(full)
+           : dim <= 128 ? instance<NINFER_BF16, 128, 128>(full)
+                        : instance<NINFER_BF16, 256, 256>(full);
 }
 
 struct Layout {

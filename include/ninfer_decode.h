@@ -134,9 +134,10 @@ int ninfer_kv_append(const void *k_new, const void *v_new, int src_dtype, uint64
  *   lse: device float[requests][q_heads] or NULL.
  *   workspace: device, at least ninfer_kv_attention_workspace() bytes, 256-byte aligned;
  *     its contents are not preserved.
- * Arithmetic: products of 16-bit operands with fp32 sums on the tensor cores. q and the
- * weights e^{s - m} enter as a 16-bit value and the 16-bit remainder, so that the result is
- * that of fp32 operands to about 2^-17; running maxima and sums are fp32.
+ * Arithmetic: products of 16-bit operands with fp32 sums on the tensor cores. fp32 queries,
+ * and the weights e^{s - m} of fp32 results, enter as sums of 16-bit terms that hold 22 bits
+ * (NINFER_F16 and NINFER_E4M3 caches) or 24; other weights have 16 bits (NINFER_BF16) or 11
+ * and more. Running maxima and sums are fp32.
  * ninfer_kv_attention_workspace: bytes for these arguments and any lengths; host only.
  * Errors: INVALID_ARGUMENT, SHAPE, SIZE_MISMATCH (workspace), ALIGNMENT, OVERFLOW, CUDA.
  */
