@@ -37,7 +37,7 @@ namespace {
 constexpr int kWarps = 8, kThreads = 32 * kWarps, kItems = 3;
 constexpr uint32_t kItemBytes = 8192;
 constexpr uint32_t kRingBytes = kWarps * kItems * kItemBytes;
-constexpr uint32_t kNone = 0xffffffffu, kRowKeys = 1024;
+constexpr uint32_t kNone = 0xffffffffu;
 // What beginning a row costs, in units: its queries, its first copies, its output. 0, 1, 2, 3 and 4
 // measured 42.7, 41.4, 40.5, 39.5 and 39.6 us for 32 requests of 200 to 4500 keys and 24.2, 21.7, 20.2,
 // 20.2 and 21.5 us for 24 of 1 to 3001 with 16 key heads each; no change for long rows.
@@ -961,10 +961,16 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     p.page = FastDiv((uint32_t)cache->page_size);
     p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
-    // Few and short rows: a CTA each, no schedule and no second kernel.
-    const uint64_t rows = requests * p.head_rows;
-    p.by_row = rows <= (uint64_t)d.sms && p.most <= kRowKeys;
-    st = launch_dependent("attention", in.attention, dim3(p.by_row ? (unsigned)rows : d.sms), dim3(kThreads), kSmem,
+    // Few and short rows: a CTA each, no schedule and no second kernel. That costs about 5 us and
+    // 1.8 us for every 8 units of the longest row, the division of the line about 9.3 us and
+    // 1.8 us for every unit a warp: it pays up to about 20 units where rows are few (16 units,
+    // 4 rows: 8.1 against 9.4 us; 32 units: 11.9 against 9.8), and up to 32, past which
+    // rows of different lengths would leave most of the SMs waiting, where there is a row for
+    // every SM (32 units, 144 rows: 12.3 against 16.1 us).
+    const uint64_t rows = requests * p.head_rows, sms = d.sms;
+    const uint64_t longest = p.window ? std::min<uint64_t>(p.window, p.most) : p.most, units = (longest + in.keys - 1) / in.keys;
+    p.by_row = rows <= sms && units <= 32 && units * (sms - rows) <= 20 * sms;
+    st = launch_dependent("attention", in.attention, dim3((unsigned)(p.by_row ? rows : sms)), dim3(kThreads), kSmem,
                           (cudaStream_t)stream, p);
     if (st || p.by_row) return st;
     return launch_dependent("attention join", in.join, dim3(d.sms, in.used / 16), dim3(kThreads), 0, (cudaStream_t)stream, p,
