@@ -3,8 +3,8 @@
 //
 // Pure data movement: each source element is read once and each stored element
 // written once, so HBM bounds it (latency, for the few rows of a decode step).
-// One thread moves one 16-byte unit of the stored row (8 or 16 elements), K and V
-// in the same launch.
+// One thread moves one 16-byte unit of the stored row (8 or 16 elements) of K and of V,
+// all of its loads under way at once.
 #include "decode.cuh"
 
 namespace ninfer {
@@ -42,9 +42,8 @@ struct AppendParams {
     float scale[2];
     const int64_t *slots;
     uint64_t slot_count;                // of the cache
-    uint64_t total;                     // 16-byte units of one of the two
-    FastDiv units, heads;               // units a head, heads
-    uint32_t page_size;
+    uint32_t total;                     // 16-byte units of one of the two
+    FastDiv units, heads, page;         // units a head, heads, tokens a page
     int src_dtype;
     int32_t *status;
 };
@@ -68,36 +67,47 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t *out) {
 }
 
 template <int kDtype>
-__global__ void __launch_bounds__(256) append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr uint32_t kEs = kDtype == NINFER_E4M3 ? 1 : 2, kUnit = 16 / kEs;
     pdl_launch_dependents();
     pdl_wait();
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
+    const uint32_t i = blockIdx.x * 256 + threadIdx.x;      // total < 2^31: the host splits longer calls
     if (i >= p.total) return;
-    const int which = blockIdx.y;
-    // total < 2^32: the host splits longer calls
-    const uint32_t head_row = p.units.div((uint32_t)i), unit = (uint32_t)i - head_row * p.units.d;
+    const uint32_t head_row = p.units.div(i), unit = i - head_row * p.units.d;
     const uint32_t token = p.heads.div(head_row), head = head_row - token * p.heads.d;
     const int64_t slot = p.slots[token];
+    float x[2][kUnit];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        const uint64_t from = token * p.src_token[w] + head * p.src_head[w] + unit * kUnit;
+#pragma unroll
+        for (uint32_t j = 0; j < kUnit; j += 8) load8(p.src[w], from + j, p.src_dtype, *reinterpret_cast<float(*)[8]>(x[w] + j));
+    }
     if (slot < 0) return;
     if ((uint64_t)slot >= p.slot_count) {
         if (p.status && unit == 0 && head == 0) atomicOr(p.status, NINFER_KV_BAD_SLOT);
         return;
     }
-    float x[kUnit];
-    const uint64_t from = token * p.src_token[which] + head * p.src_head[which] + unit * kUnit;
+    uint64_t page, in;
+    if (p.slot_count >> 32) {
+        page = (uint64_t)slot / p.page.d;
+        in = (uint64_t)slot % p.page.d;
+    } else {
+        page = p.page.div((uint32_t)slot);
+        in = (uint32_t)slot - (uint32_t)page * p.page.d;
+    }
+    const uint64_t to = (page * p.page_stride + in * p.token_stride + head * p.head_stride + unit * kUnit) * kEs;
 #pragma unroll
-    for (uint32_t j = 0; j < kUnit; j += 8) load8(p.src[which], from + j, p.src_dtype, *reinterpret_cast<float(*)[8]>(x + j));
-    const float scale = p.scale[which];
-    if (scale != 1.f)
+    for (int w = 0; w < 2; ++w) {
+        const float scale = p.scale[w];
+        if (scale != 1.f)
 #pragma unroll
-        for (uint32_t j = 0; j < kUnit; ++j) x[j] = __fdiv_rn(x[j], scale);
-    uint32_t o[4];
+            for (uint32_t j = 0; j < kUnit; ++j) x[w][j] = __fdiv_rn(x[w][j], scale);
+        uint32_t o[4];
 #pragma unroll
-    for (uint32_t j = 0; j < kUnit; j += 8) pack8<kDtype>(*reinterpret_cast<float(*)[8]>(x + j), o + j / 4);
-    const uint64_t page = (uint64_t)slot / p.page_size, at = (uint64_t)slot % p.page_size;
-    uint8_t *to = p.dst[which] + (page * p.page_stride + at * p.token_stride + head * p.head_stride + unit * kUnit) * kEs;
-    *reinterpret_cast<uint4 *>(to) = make_uint4(o[0], o[1], o[2], o[3]);
+        for (uint32_t j = 0; j < kUnit; j += 8) pack8<kDtype>(*reinterpret_cast<float(*)[8]>(x[w] + j), o + j / 4);
+        *reinterpret_cast<uint4 *>(p.dst[w] + to) = make_uint4(o[0], o[1], o[2], o[3]);
+    }
 }
 
 }  // namespace
@@ -136,21 +146,21 @@ extern "C" int ninfer_kv_append(const void *k_new, const void *v_new, int src_dt
     p.slot_count = cache->pages * cache->page_size;
     p.units = FastDiv((uint32_t)units);
     p.heads = FastDiv((uint32_t)cache->kv_heads);
-    p.page_size = (uint32_t)cache->page_size;
+    p.page = FastDiv((uint32_t)cache->page_size);
     p.src_dtype = src_dtype;
     p.status = status;
     const auto kernel = cache->dtype == NINFER_BF16  ? append_kernel<NINFER_BF16>
                         : cache->dtype == NINFER_F16 ? append_kernel<NINFER_F16>
                                                      : append_kernel<NINFER_E4M3>;
-    // at most 2^31 units a launch: the kernel indexes units with 32 bits
-    const uint64_t step = (1ull << 31) / per_token ? (1ull << 31) / per_token : 1;
+    // fewer than 2^31 units a launch: the kernel counts them in 32 bits
+    const uint64_t step = ((1ull << 31) - 1) / per_token;
     for (uint64_t t = 0; t < tokens; t += step) {
         const uint64_t n = tokens - t < step ? tokens - t : step;
         p.src[0] = static_cast<const uint8_t *>(k_new) + t * k_token_stride * dtype_size(src_dtype);
         p.src[1] = static_cast<const uint8_t *>(v_new) + t * v_token_stride * dtype_size(src_dtype);
         p.slots = slots + t;
-        p.total = n * per_token;
-        st = launch_dependent("append", kernel, dim3((unsigned)((p.total + 255) / 256), 2), dim3(256), 0,
+        p.total = (uint32_t)(n * per_token);
+        st = launch_dependent("append", kernel, dim3((p.total + 255) / 256), dim3(256), 0,
                               (cudaStream_t)stream, p);
         if (st) return st;
     }
