@@ -64,7 +64,7 @@ __device__ __forceinline__ float value(uint32_t w, int half) {
 template <int kDtype, bool kWide>
 __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __grid_constant__ LogitsParams p) {
     using E = Entry<kWide>;
-    constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs, kAhead = 2, kQuads = 4;
+    constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs, kAhead = 2, kQuads = 6;
     constexpr int kMaskWords = ((kWide ? kMostWide : kMostNarrow) / 32 + kThreads - 1) / kThreads;
     extern __shared__ __align__(16) uint32_t table[];
     const uint32_t tid = threadIdx.x, row = blockIdx.x / p.slices, first = blockIdx.x % p.slices * p.slice;
