@@ -7,25 +7,39 @@
 //
 // What bounds it. Every key and value is used by the few query heads of its
 // group (4 * group flops an element), so HBM does; the tensor cores only have
-// to keep up. mma.sync.m16n8k16 serves: 16 keys of 128 elements take 24 to 32 of them.
+// to keep up, and mma.sync.m16n8k16 serves (11 % of the tensor pipe's cycles on a
+// 16-bit cache, 17 % on an 8-bit one).
 //   scores   A = 16 keys, B = 8 heads' queries;
 //   values   A = 16 elements of the values transposed (ldmatrix.trans), B = 8 heads' weights,
 //            transposed from the scores' accumulators in the registers (movmatrix).
 // The 8 heads of a row are the narrow side of both, so that a group of eight wastes
-// nothing. 32-bit operands enter as sums of 16-bit terms, one mma each.
+// nothing. Queries as the A operand, with their remainders in the rows that a group
+// of eight leaves empty, took twice the mmas: 231 against 203 us for 1.2 GB of 8-bit
+// keys and values. 32-bit operands enter as sums of 16-bit terms, one mma each.
 //
 // Split. The keys of every (request, key head, 8 query heads) are cut into
 // units of 8 KB of keys and 8 KB of values; all units of the call form one
-// line, on which a row's beginning counts as some units more, and of which each CTA (one
-// an SM) and in it each warp takes an equal, contiguous part, so that any mix of lengths keeps every SM busy to the end.
-// A warp writes a row that lies in its part whole; cut rows are joined in the CTA,
-// and rows cut between CTAs by a second, small kernel.
+// line, on which a row's beginning counts as some units more, and of which each CTA
+// (one an SM) and in it each warp takes an equal, contiguous part, so that any mix of
+// lengths keeps every SM busy. A warp writes a row that lies in its part whole; cut
+// rows are joined in the CTA, and rows cut between CTAs by a second, small kernel. Few
+// short rows go without all that, a CTA each. Groups of more than eight heads are rows
+// of their own for every eight; they pass over the same keys at about the same time.
 //
 // Loads. Each warp has a ring of three 8 KB items in shared memory, keys and
-// values of its units in turn, filled by tensor-map copies of whole page
-// pieces (128-byte swizzle, so that ldmatrix is free of bank conflicts); no warp
-// waits for another one until its part is done. Up to 192 KB an SM are in
-// flight. Pieces past the row's end are not fetched.
+// values of its units in turn, filled by 16-byte asynchronous copies of all lanes
+// (swizzled, so that ldmatrix is free of bank conflicts); no warp waits for
+// another one until its part is done. Up to 192 KB an SM are in flight, and a warp
+// hardly ever waits for a copy to land (under 1 % of a long row's time). Tensor-map boxes in
+// their place cost 105 to 185 cycles each to issue, a box a page and 128 bytes: 94.5 against
+// 88.4 us for one row of 131071 keys in pages of 64, 132 against 119 us for 8-bit rows of
+// 80 elements in pages of 24. Keys outside a request are filled with zeros in shared
+// memory, so that nothing a page holds behind them reaches a product.
+//
+// Measured (a plain copy runs at 6791 GB/s): 128 requests of 1000 to 16000 keys, 2.85 GB, 438 us (6.51 TB/s);
+// one of 131071, 537 MB, 87.8 us (6.11 TB/s); 16 of 20000 to 60000 on an 8-bit cache, 1.2 GB,
+// 188 us (6.39 TB/s); 32 of 200 to 4500, 184 MB, 39.3 us, of which about 12 are the beginning and
+// the joins.
 #include <cmath>
 
 #include "decode.cuh"
@@ -381,17 +395,47 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         for (int i = 0; i < kPieces; ++i)
             at[i] = (uint32_t)page[i] < p.pages ? reinterpret_cast<uint64_t>(pool) + (uint32_t)page[i] * p.page_bytes + token[i] * p.token_bytes + head : 0u;
         const uint64_t none = reinterpret_cast<uint64_t>(pool), own = unit * 16;
-#pragma unroll
-        for (int k = 0; k < kKeys / kRowsAtOnce; ++k) {
-            const uint32_t r = k * kRowsAtOnce, q = (r + unit_row) >> p.piece_log;
+        // where lane `unit_row`'s row of copy k comes from, or 0
+        auto row_at = [&](int k) {
+            const uint32_t r = k * kRowsAtOnce + unit_row, q = r >> p.piece_log;
             uint64_t from = __shfl_sync(~0u, at[0], q & 31);
             if (kPieces > 1) {
                 const uint64_t more = __shfl_sync(~0u, at[kPieces - 1], q & 31);
                 if (q >= 32) from = more;
             }
-            const bool on = from && r >= lo && r < hi;
+            return from;
+        };
+        auto copy = [&](int k, uint64_t from, bool on) {
+            const uint32_t r = k * kRowsAtOnce;
             from += ((r + unit_row) & in_piece) * p.token_bytes + own;
             copy16(to + r * 128 + (turn ^ (r & 7) << 4), reinterpret_cast<const uint8_t *>(on ? from : none), on ? 16 : 0);
+        };
+        constexpr int kCopies = kKeys / kRowsAtOnce;
+        if constexpr (S::kBytes8) {
+#pragma unroll
+            for (int k = 0; k < kCopies; ++k) {
+                const uint64_t from = row_at(k);
+                copy(k, from, from && k * kRowsAtOnce >= lo && k * kRowsAtOnce < hi);
+            }
+        } else {
+            // 16-bit rows: units that lie in the request and in pages whole go without a test a copy (2.85 GB: 446
+            // against 451 us); 8-bit rows took 2 to 5 % longer that way
+            const bool whole = base >= ld.row.from + unit_row && base - unit_row + kKeys <= ld.row.end && pieces <= 32 && (at[0] || lane >= pieces);
+            if (__all_sync(~0u, whole)) {
+                const bool on = unit * (16 / S::kEs) < p.head_dim;
+#pragma unroll
+                for (int k = 0; k < kCopies; ++k) {
+                    const uint32_t r = k * kRowsAtOnce + unit_row;
+                    const uint64_t from = __shfl_sync(~0u, at[0], r >> p.piece_log) + ((r & in_piece) * (uint32_t)p.token_bytes + unit * 16);
+                    copy16(to + k * kRowsAtOnce * 128 + (turn ^ (k * kRowsAtOnce & 7) << 4), reinterpret_cast<const uint8_t *>(from), on ? 16 : 0);
+                }
+            } else {
+#pragma unroll 4
+                for (int k = 0; k < kCopies; ++k) {
+                    const uint64_t from = row_at(k);
+                    copy(k, from, from && k * kRowsAtOnce >= lo && k * kRowsAtOnce < hi);
+                }
+            }
         }
         slot_in = slot_in == kItems - 1 ? 0 : slot_in + 1;
     };

@@ -5,14 +5,20 @@
 // latency a single row. A CTA owns a slice of one row's tokens and keeps a
 // table of them in shared memory, one entry a token: how often it was answered,
 // whether it was seen in the prompt, whether it has a bias; the slice's mask words
-// stand behind it. It asks for its first logits, enters the row's history, biases and
-// mask while they are under way, and streams the slice through: four tokens with empty entries pass as they
-// are. Tokens with a bias are left out there and done one by one from the list,
-// so that the biases need no table of their own.
+// stand behind it. It asks for the row's history, its mask words, its biases and its first
+// logits at once, enters them into the table, and streams the slice through. Tokens
+// with a bias are left out there and done one by one from the list, so that the
+// biases need no table of their own.
 //
 // Slices. Every CTA of a row reads the row's whole history, so slices are as large
 // as the table of a third of an SM allows, and as many as fill the SMs once: 64
-// rows are 7 slices of about 35,500 tokens each.
+// rows are 7 slices of about 35,500 tokens each. Twice as many measured 2 us less for
+// 64 rows and 2 to 4 us more for 11 to 47.
+//
+// Measured: 64 rows of 248320 fp32 logits with histories of 16 to 8000 tokens, 28.1 us for
+// 128 MB (18.8 us at the rate of a copy): 3.7 us until the table stands, 18 us of streaming, and the
+// launch. Copying the untouched tokens at once, and doing the touched ones after the
+// table, took 52 us (a dependent read for each of them). One row takes 2.3 us on the GPU.
 #include <cmath>
 
 #include "decode.cuh"

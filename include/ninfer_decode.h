@@ -39,8 +39,8 @@ typedef enum { NINFER_E4M3 = 3 } ninfer_cache_dtype;
  *   dtype: NINFER_BF16, NINFER_F16 or NINFER_E4M3.
  *   pages, page_size, kv_heads > 0, pages < 2^31, page_size < 2^31;
  *   head_dim: 1..256, a multiple of 8 (NINFER_E4M3: of 16).
- *   strides: multiples of 16 bytes (token_stride unread for page_size 1,
- *     head_stride for kv_heads 1, page_stride for pages 1).
+ *   strides: multiples of 16 bytes, token_stride below 2^25 bytes, the others below 2^40
+ *     (token_stride unread for page_size 1, head_stride for kv_heads 1, page_stride for pages 1).
  *   k, v: device, 16-byte aligned. k_scale, v_scale: finite, > 0.
  */
 typedef struct {

@@ -75,7 +75,7 @@ BAD_CACHES = [(dict(k=None), INVALID), (dict(v=None), INVALID), (dict(dtype=nt.F
               (dict(kv_heads=0), SHAPE), (dict(pages=2 ** 31), SHAPE), (dict(head_dim=0), SHAPE), (dict(head_dim=264), SHAPE),
               (dict(head_dim=60), SHAPE), (dict(head_dim=72, dtype=nt.E4M3), SHAPE), (dict(token_stride=100), ALIGN),
               (dict(page_stride=2052), ALIGN), (dict(head_stride=60), ALIGN), (dict(k=FAKE + 8), ALIGN),
-              (dict(v=FAKE + 2), ALIGN), (dict(page_stride=2 ** 40), OVERFLOW)]
+              (dict(v=FAKE + 2), ALIGN), (dict(page_stride=2 ** 40), OVERFLOW), (dict(token_stride=2 ** 24), OVERFLOW)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_CACHES)
