@@ -4,11 +4,13 @@ Bounds, fixed from the number formats:
 - tables: whole numbers, equal; append: the stored value is the fp64 quotient
   rounded once, equal (for scale 1 and powers of two; an fp32 quotient that is
   not exact may round a tie the other way: one step there).
-- attention: q and the softmax weights enter the tensor cores as a 16-bit value
-  and a 16-bit remainder (2^-16 relative at worst), everything else is fp32. A
+- attention: fp32 queries, and the weights of fp32 results, hold 22 bits or more
+  in the tensor cores, other weights 16 (bfloat16 caches), and 11 where a
+  bfloat16 result comes of a binary16 or 8-bit cache; everything else is fp32. A
   score is then off by at most S 2^-15 with S = scale * sum |q_d k_d| of the row,
-  a weight by twice that, and the result by (2 S + 1) 2^-15 sum_j p_j |v_j|,
-  plus half a step of the output's format. lse: (S + |lse| + 1) 2^-15.
+  a weight by twice that and its own rounding, W = 2^-15 or 2^-12, and the result by
+  (2 S 2^-15 + W) sum_j p_j |v_j|, plus half a step of the output's format.
+  lse: (S + |lse| + 1) 2^-15.
 - logits: three fp32 roundings of values up to the largest one that a token's
   chain holds, then one of the output's format.
 """
@@ -188,7 +190,8 @@ def check_attention(q, k, v, table, lengths, scale=None, window=0, out="bf16", s
     assert nt.ninfer_device_errors() == 0
     want, wlse, mag, big = od.kv_attention(f64(q), f64(k), f64(v), table, lengths, scale, window, *scales)
     got, glse = f64(y), f64(lse)
-    bound = (2 * big[..., None] + 1) * 2.0 ** -15 * mag + STEP[out] * np.abs(want) + (2.0 ** -25 if out == "f16" else 0)
+    weight = 2.0 ** -12 if out == "bf16" and k.dtype != torch.bfloat16 else 2.0 ** -15
+    bound = (2 * big[..., None] * 2.0 ** -15 + weight) * mag + STEP[out] * np.abs(want) + (2.0 ** -25 if out == "f16" else 0)
     bad = ~(np.abs(got - want) <= bound)
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5])
     empty = wlse == -np.inf
@@ -231,6 +234,16 @@ def test_attention_head_dims(dim):
 def test_attention_groups(heads, kvh):
     rng = np.random.default_rng(heads)
     check_attention(*attention_case(rng, [5, 90, 257], heads, kvh, 64, 16, "bf16", "bf16"))
+
+
+@pytest.mark.parametrize("heads,kvh,dim", [(9, 1, 128), (24, 2, 64), (16, 1, 104), (33, 1, 128), (16, 1, 136), (44, 2, 256)])
+@pytest.mark.parametrize("cache,q,out", [("bf16", "bf16", "bf16"), ("bf16", "f32", "f32"), ("f16", "f16", "bf16"),
+                                         ("e4m3", "bf16", "bf16"), ("e4m3", "f32", "f32")])
+def test_attention_wide_groups_split_and_joined(heads, kvh, dim, cache, q, out):
+    """Sixteen heads to a row, a last row of fewer, in rows that are cut between warps and CTAs."""
+    rng = np.random.default_rng(heads + dim)
+    dim = dim // 16 * 16 if cache == "e4m3" else dim
+    check_attention(*attention_case(rng, [6001, 3, 0, 777], heads, kvh, dim, 16, cache, q, "heads"), out=out)
 
 
 @pytest.mark.parametrize("lengths,heads,kvh,dim,page,cache", [
