@@ -42,24 +42,33 @@ inline uint32_t cache_dtype_size(int dt) { return dt == NINFER_E4M3 ? 1 : 2; }
 // The rules of ninfer_kv_cache; `who` begins the error message.
 int check_cache(const ninfer_kv_cache *c, const char *who);
 
-// Launch with programmatic dependent launch: the kernel calls pdl_wait() before
-// it touches memory.
+// Launch with programmatic dependent launch, in clusters of `cluster` CTAs: the
+// kernel calls pdl_wait() before it touches memory.
 template <class... P, class... A>
-int launch_dependent(const char *who, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
-                     A... args) {
+int launch_clusters(const char *who, unsigned cluster, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
+                    cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess) return fail(NINFER_ERR_CUDA, "%s launch: %s", who, cudaGetErrorString(e));
     return NINFER_OK;
+}
+
+template <class... P, class... A>
+int launch_dependent(const char *who, void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                     A... args) {
+    return launch_clusters(who, 1, kernel, grid, block, smem, stream, args...);
 }
 
 }  // namespace ninfer

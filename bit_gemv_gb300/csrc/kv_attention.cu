@@ -132,17 +132,28 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     p.page = FastDiv((uint32_t)cache->page_size);
     p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
-    // Few and short rows: a CTA each, no schedule and no second kernel. That costs about 5 us and
-    // 1.8 us for every 8 units of the longest row, the division of the line about 9.3 us and
-    // 1.8 us for every unit a warp: it pays up to about 20 units where rows are few (16 units,
-    // 4 rows: 8.1 against 9.4 us; 32 units: 11.9 against 9.8), and up to 32, past which
-    // rows of different lengths would leave most of the SMs waiting, where there is a row for
-    // every SM (32 units, 144 rows: 12.3 against 16.1 us).
+    // Few and short rows: a CTA, or a cluster of two, four or eight, for each, without a schedule and
+    // a second kernel. On the GPU that costs 5 us (clusters: 7) and 1.8 us for every 8 units of a
+    // CTA's part of the longest row; the division of the line costs 9 us (256 elements: 11) and
+    // 1.8 us for every unit a warp. Measured, rows of 128 elements in 16 bits, clusters against the line:
+    //   4 rows of 64 units 9.1 / 9.6 us, of 96 10.4 / 9.7;  16 of 32 8.0 / 9.4, of 96 11.3 / 10.2;
+    //   32 of 64 9.8 / 11.8, of 256 20.0 / 17.9;  64 of 64 12.3 / 13.4;  144 (a CTA each) of 32 11.0 / 15.3.
+    // Past 32 units a CTA, rows of different lengths would leave most of the SMs waiting. Clusters of
+    // eight and four do not fill every SM (their SMs are neighbours): 5/6 and 9/10 are counted on.
     const uint64_t rows = requests * p.head_rows, sms = d.sms;
     const uint64_t longest = p.window ? std::min<uint64_t>(p.window, p.most) : p.most, units = (longest + in.keys - 1) / in.keys;
-    p.by_row = rows <= sms && units <= 32 && units * (sms - rows) <= 20 * sms;
-    st = launch_dependent("attention", in.attention, dim3((unsigned)(p.by_row ? rows : sms)), dim3(kThreads), kSmem,
-                          (cudaStream_t)stream, p);
+    const uint64_t room[4] = {sms, sms, sms * 9 / 10, sms * 5 / 6};
+    p.by_row = 0;
+    for (p.cluster_log = 4; p.cluster_log-- > 0;) {
+        const uint64_t size = 1ull << p.cluster_log, ctas = rows * size;
+        p.by_row = ctas <= room[p.cluster_log] && (size == 1 || units > 4 * size) && units <= 32 * size &&
+                   units * (sms - ctas) <= (size == 1 ? 20 : 8 * size) * sms;
+        if (p.by_row) break;
+    }
+    if (!p.by_row) p.cluster_log = 0;
+    const unsigned cluster = 1u << p.cluster_log;
+    st = launch_clusters("attention", cluster, in.attention, dim3((unsigned)(p.by_row ? rows * cluster : sms)), dim3(kThreads), kSmem,
+                         (cudaStream_t)stream, p);
     if (st || p.by_row) return st;
     return launch_dependent("attention join", in.join, dim3(d.sms, in.used / 16 * in.heads / 8), dim3(kThreads), 0, (cudaStream_t)stream, p,
                             (uint32_t)d.sms);

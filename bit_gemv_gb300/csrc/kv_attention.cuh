@@ -24,9 +24,11 @@
 // (one an SM) and in it each warp takes an equal, contiguous part, so that any mix of
 // lengths keeps every SM busy. A warp writes a row that lies in its part whole; cut
 // rows are joined in the CTA, and rows cut between CTAs by a second, small kernel. Few
-// short rows go without all that, a CTA each. Groups of more than eight heads take sixteen
-// to a row up to 128 elements (8 key heads, 16 requests of 8000 to 24000 keys: groups of 16 162 us, with two rows
-// of eight 273 us, groups of 8 155 us); what is past that makes further rows of the same keys.
+// short rows go without all that: a CTA or a cluster of CTAs for each, which joins its
+// parts through distributed shared memory. Groups of more than eight heads take
+// sixteen to a row up to 128 elements (8 key heads, 16 requests of 8000 to 24000 keys:
+// groups of 16 162 us, with two rows of eight 273 us, groups of 8 155 us); what is
+// past that makes further rows of the same keys.
 //
 // Loads. Each warp has a ring of three 8 KB items in shared memory, keys and
 // values of its units in turn, filled by 16-byte asynchronous copies of all lanes
@@ -74,7 +76,7 @@ struct AttentionParams {
     uint64_t page_bytes, token_bytes, head_bytes;       // strides of the pools
     float scale, v_scale;               // scale: of scores, in log2
     uint32_t requests, run, q_heads, group, head_dim, head_rows, pages, piece_log, window, most;
-    uint32_t by_row;                    // CTA c has row c, and no other: nothing is cut between CTAs
+    uint32_t by_row, cluster_log;       // whether each cluster of 2^cluster_log CTAs has one row, and no other
     FastDiv page, tiles, heads;         // tokens a page, rows a key head, rows a request
     int q_dtype, out_dtype;
 };
@@ -278,6 +280,40 @@ __device__ __forceinline__ void store_lse(const AttentionParams &p, const Place 
 // What the sums of a row are multiplied by in the end; a row without weights gives zeros.
 __device__ __forceinline__ float scale_of(const AttentionParams &p, float l) { return l == 0.f ? 0.f : p.v_scale / l; }
 
+__device__ __forceinline__ float4 load_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
+    return v;
+}
+
+// Parts of one value tile for heads 2 t and 2 t + 1, joined one by one.
+struct Joined {
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float4 ml, float4 x) {      // ml: m and l of the two heads
+        const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.z);
+        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
+        const float f0 = exp2_approx(m0 - u0), f1 = exp2_approx(m1 - u1), g0 = exp2_approx(ml.x - u0), g1 = exp2_approx(ml.z - u1);
+        l0 = l0 * f0 + ml.y * g0;
+        l1 = l1 * f1 + ml.w * g1;
+        a.x = a.x * f0 + x.x * g0;
+        a.y = a.y * f1 + x.y * g1;
+        a.z = a.z * f0 + x.z * g0;
+        a.w = a.w * f1 + x.w * g1;
+        m0 = n0;
+        m1 = n1;
+    }
+};
+
+template <class S>
+__device__ __forceinline__ void store_joined(const AttentionParams &p, const Place &at, int tile, int lane, const Joined &s) {
+    store_tile<S>(p, at, tile, lane, s.a, scale_of(p, s.l0), scale_of(p, s.l1));
+    if (tile == 0 && lane < 4) {
+        store_lse<S>(p, at, 2 * lane, s.m0, s.l0);
+        store_lse<S>(p, at, 2 * lane + 1, s.m1, s.l1);
+    }
+}
+
 // kFull: as exact as fp32 operands. Queries and weights then enter as three bfloat16
 // or two binary16 terms (24 and 22 bits). Otherwise the queries are of a 16-bit type
 // that one term holds, and the output is rounded to 16 bits: weights have two
@@ -292,10 +328,12 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     __shared__ uint32_t s_row[2 * kWarps], s_flags[2 * kWarps];
     __shared__ float2 s_ml[2 * kWarps][S::kHeads], s_total[2 * kWarps][S::kHeads];
     __shared__ float s_factor[2 * kWarps][S::kHeads];
+    __shared__ __align__(16) float2 s_cta_ml[S::kHeads];     // of this CTA's part of the cluster's row
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const uint32_t ring_skip = (1024 - (smem_u32(ring_raw) & 1023)) & 1023;
     const uint32_t ring = smem_u32(ring_raw) + ring_skip + warp * (kItems * kItemBytes);
     if (lane < 2) s_row[2 * warp + lane] = kNone;
+    if (threadIdx.x < S::kHeads) s_cta_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
     pdl_launch_dependents();
     pdl_wait();
 
@@ -304,13 +342,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     uint32_t left = 0;          // of this warp's part: units, and kRowCost for each row that begins after the first
     bool empties = false;       // whether any request has no keys
     if (p.by_row) {
-        ld.request = p.heads.div(blockIdx.x);
-        ld.head = blockIdx.x - ld.request * p.head_rows;
+        const uint32_t row = blockIdx.x >> p.cluster_log, rank = blockIdx.x - (row << p.cluster_log);
+        ld.request = p.heads.div(row);
+        ld.head = row - ld.request * p.head_rows;
         ld.row = row_of<kKeys>(p, ld.request);
-        const uint32_t share = ld.row.units / kWarps, more = ld.row.units % kWarps;
-        ld.unit = warp * share + min((uint32_t)warp, more);
-        left = share + (warp < more);
-        empties = ld.row.units == 0 && ld.head == 0;
+        // equal parts for the cluster's CTAs, and in them for the warps
+        const uint32_t share = ld.row.units >> p.cluster_log, more = ld.row.units - (share << p.cluster_log);
+        const uint32_t n = share + (rank < more), warp_share = n / kWarps, warp_more = n % kWarps;
+        ld.unit = rank * share + min(rank, more) + warp * warp_share + min((uint32_t)warp, warp_more);
+        left = warp_share + (warp < warp_more);
+        empties = ld.row.units == 0 && ld.head == 0 && rank == 0;
     } else {
         const uint32_t r0 = min(threadIdx.x * p.run, p.requests), r1 = min(r0 + p.run, p.requests);
         uint64_t mine = 0;
@@ -700,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         load_keys();        // of the unit after that
 
         if (ends || !left) {
-            const bool whole = begun && ends;
+            const bool whole = begun && ends && !p.cluster_log;
             const int slot = 2 * warp + (begun ? 1 : 0);
             // at the end of the warp's part its ring is free, and holds the sums until they are joined
             float4 *to = left ? p.warp_o + ((uint64_t)blockIdx.x * kWarps + warp) * kPart
@@ -744,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     if (empties) {
         // requests without keys: by_row CTAs look at their own, others share them out
         const uint32_t step = p.by_row ? p.requests : gridDim.x;
-        for (uint32_t r = p.by_row ? p.heads.div(blockIdx.x) : blockIdx.x; r < p.requests; r += step) {
+        for (uint32_t r = p.by_row ? p.heads.div(blockIdx.x >> p.cluster_log) : blockIdx.x; r < p.requests; r += step) {
             if (row_of<kKeys>(p, r).units) continue;
             for (uint32_t i = threadIdx.x; i < p.q_heads * p.head_dim; i += kThreads)
                 store1(p.out, (uint64_t)r * p.q_heads * p.head_dim + i, p.out_dtype, 0.f);
@@ -754,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     }
     __syncthreads();
 
-    // ---- rows cut between warps, joined in order; what is still cut goes to the second kernel ----
+    // ---- rows cut between warps, joined in order; what is still cut goes to the cluster or the second kernel ----
     // slot j of a warp's parts: row, flags, and the slots that hold parts of the same row
     const int mine = lane & (2 * kWarps - 1);
     const uint32_t slot_row = s_row[mine], slot_flags = s_flags[mine];
@@ -776,12 +817,16 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         s_factor[j][h] = mask >> j & 1 ? exp2_approx(s_ml[j][h].x - u) : 0.f;
     }
     __syncthreads();
+    // behind the two parts that warp 0's ring may hold, room for what the cluster's other CTAs read
+    static_assert(3 * kPart * sizeof(float4) <= kItems * kItemBytes, "three parts fit a warp's ring");
+    float4 *cta_o = reinterpret_cast<float4 *>(ring_raw + ring_skip) + 2 * kPart;
     uint4 meta = make_uint4(kNone, 0, 0, 0);
     uint32_t starts = __ballot_sync(~0u, lane < 2 * kWarps && (slot_mask & ((2u << lane) - 1)) == 1u << lane);
     for (; starts; starts &= starts - 1) {
         const int i = __ffs(starts) - 1;
         const uint32_t row = __shfl_sync(~0u, slot_row, i), mask = __shfl_sync(~0u, slot_mask, i);
         const bool begins = __shfl_sync(~0u, slot_flags, i) & 1, ends = __shfl_sync(~0u, slot_flags, 31 - __clz(mask)) & 2;
+        const bool whole = begins && ends && !p.cluster_log;
         const uint32_t outside = __ballot_sync(~0u, slot_flags & 4);        // slots whose sums lie in the workspace
         const uint64_t part = (uint64_t)blockIdx.x * 2 + (begins ? 1 : 0);
         const Place place = place_of<S>(p, row);
@@ -810,16 +855,17 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     a.w = fmaf(x[n].w, f1, a.w);
                 }
             }
-            if (begins && ends)
-                store_tile<S>(p, place.eight(ht), tile, lane, a, scale_of(p, s_total[i][h0].y), scale_of(p, s_total[i][h0 + 1].y));
+            if (whole) store_tile<S>(p, place.eight(ht), tile, lane, a, scale_of(p, s_total[i][h0].y), scale_of(p, s_total[i][h0 + 1].y));
+            else if (p.cluster_log) cta_o[32 * job + lane] = a;
             else p.cta_o[part * kPart + 32 * job + lane] = a;
         }
         if (warp == 0 && lane < S::kHeads) {
             const float2 ml = s_total[i][lane];
-            if (begins && ends) store_lse<S>(p, place, lane, ml.x, ml.y);
+            if (whole) store_lse<S>(p, place, lane, ml.x, ml.y);
+            else if (p.cluster_log) s_cta_ml[lane] = ml;
             else p.cta_ml[part * S::kHeads + lane] = ml;
         }
-        if (!(begins && ends)) {
+        if (!whole) {
             if (begins) meta.x = row;
             else {
                 meta.y = ends ? 1u : 0u;
@@ -827,7 +873,28 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
             }
         }
     }
-    if (threadIdx.x == 0 && !p.by_row) p.meta[blockIdx.x] = meta;
+    if (!p.by_row) {
+        if (threadIdx.x == 0) p.meta[blockIdx.x] = meta;
+        return;
+    }
+    if (!p.cluster_log) return;
+
+    // ---- the cluster's row: each CTA joins some of its value tiles, from all CTAs' shared memory ----
+    const uint32_t row = blockIdx.x >> p.cluster_log, ctas = 1u << p.cluster_log, rank = blockIdx.x - (row << p.cluster_log);
+    cluster_sync();
+    const Place place = place_of<S>(p, row);
+    for (int job = rank * kWarps + warp; job < kHeadTiles * kTiles; job += kWarps << p.cluster_log) {
+        const int ht = kHeadTiles == 1 ? 0 : job / kTiles;
+        Joined sum;
+        for (uint32_t c = 0; c < ctas; ++c) {
+            const float4 ml = load_cluster(mapa_shared(smem_u32(&s_cta_ml[8 * ht + 2 * t]), c));
+            // a CTA without keys has written no sums
+            if (__any_sync(~0u, ml.x != -INFINITY || ml.z != -INFINITY))
+                sum.add(ml, load_cluster(mapa_shared(smem_u32(cta_o + 32 * job + lane), c)));
+        }
+        store_joined<S>(p, place.eight(ht), job - ht * kTiles, lane, sum);
+    }
+    cluster_sync();             // no CTA goes while another reads its shared memory
 }
 
 // Joins the rows that were cut between CTAs: block (c, value tile of eight heads) takes the row whose
@@ -856,37 +923,19 @@ __global__ void __launch_bounds__(kThreads) join_kernel(const __grid_constant__ 
     __syncthreads();
     // part 0 is CTA c's tail, part i the head of CTA c + i; each warp joins every eighth, then the warps
     const uint32_t parts = s_last - c + 1;
-    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto join = [&](float4 ml, float4 x) {          // ml: m and l of the two heads
-        const float n0 = fmaxf(m0, ml.x), n1 = fmaxf(m1, ml.z);
-        const float u0 = n0 == -INFINITY ? 0.f : n0, u1 = n1 == -INFINITY ? 0.f : n1;
-        const float f0 = exp2_approx(m0 - u0), f1 = exp2_approx(m1 - u1), g0 = exp2_approx(ml.x - u0), g1 = exp2_approx(ml.z - u1);
-        l0 = l0 * f0 + ml.y * g0;
-        l1 = l1 * f1 + ml.w * g1;
-        a.x = a.x * f0 + x.x * g0;
-        a.y = a.y * f1 + x.y * g1;
-        a.z = a.z * f0 + x.z * g0;
-        a.w = a.w * f1 + x.w * g1;
-        m0 = n0;
-        m1 = n1;
-    };
+    Joined sum;
 #pragma unroll 4
     for (uint32_t i = warp; i < parts; i += kWarps) {
         const uint64_t at = (uint64_t)(c + i) * 2 + (i ? 0 : 1);
-        join(reinterpret_cast<const float4 *>(p.cta_ml)[(at * S::kHeadTiles + ht) * 4 + t], p.cta_o[at * kPart + 32 * job + lane]);
+        sum.add(reinterpret_cast<const float4 *>(p.cta_ml)[(at * S::kHeadTiles + ht) * 4 + t], p.cta_o[at * kPart + 32 * job + lane]);
     }
-    if (lane < 4) s_ml[warp][lane] = make_float4(m0, l0, m1, l1);
-    s_o[warp][lane] = a;
+    if (lane < 4) s_ml[warp][lane] = make_float4(sum.m0, sum.l0, sum.m1, sum.l1);
+    s_o[warp][lane] = sum.a;
     __syncthreads();
     if (warp) return;
-    for (uint32_t w = 1; w < min(parts, (uint32_t)kWarps); ++w) join(s_ml[w][t], s_o[w][lane]);
+    for (uint32_t w = 1; w < min(parts, (uint32_t)kWarps); ++w) sum.add(s_ml[w][t], s_o[w][lane]);
     const Place place = place_of<S>(p, row).eight(ht);
-    store_tile<S>(p, place, tile, lane, a, scale_of(p, l0), scale_of(p, l1));
-    if (tile == 0 && lane < 4) {
-        store_lse<S>(p, place, 2 * t, m0, l0);
-        store_lse<S>(p, place, 2 * t + 1, m1, l1);
-    }
+    store_joined<S>(p, place, tile, lane, sum);
 }
 
 struct Instance {

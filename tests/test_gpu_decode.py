@@ -564,3 +564,18 @@ def test_c_entry_points_by_ctypes():
                                    vp(ws.data_ptr()), u64(ws.numel()), s) == 0
     torch.cuda.synchronize()
     assert torch.allclose(out, torch.ones_like(out))       # two keys of equal weight, values 0 and 2
+
+
+@pytest.mark.parametrize("rows", [(1, 1), (1, 4), (2, 8), (4, 9), (9, 8)])
+@pytest.mark.parametrize("longest", [130, 520, 1300, 2500, 4000])
+@pytest.mark.parametrize("cache,dim", [("bf16", 128), ("f16", 256), ("e4m3", 96)])
+def test_attention_few_rows(rows, longest, cache, dim):
+    """Few rows of up to a few units a warp: a CTA or a cluster for each, or the line, by the table's width;
+    shorter and empty rows among them, which leave CTAs of a cluster without keys."""
+    requests, kvh = rows
+    rng = np.random.default_rng(longest + dim)
+    lengths = ([longest, 1, 0, longest // 2, 33, longest - 1, 17, longest // 3, 5] * 2)[:requests]
+    for out in ("bf16", "f32"):
+        check_attention(*attention_case(rng, lengths, 3 * kvh, kvh, dim, 16, cache, "bf16", "heads"), out=out,
+                        window=0 if out == "bf16" else longest // 2 + 1)
+    check_attention(*attention_case(rng, lengths[:2], 12 * kvh, kvh, dim, 16, cache, "f32"), out="f32")
