@@ -579,3 +579,25 @@ def test_attention_few_rows(rows, longest, cache, dim):
         check_attention(*attention_case(rng, lengths, 3 * kvh, kvh, dim, 16, cache, "bf16", "heads"), out=out,
                         window=0 if out == "bf16" else longest // 2 + 1)
     check_attention(*attention_case(rng, lengths[:2], 12 * kvh, kvh, dim, 16, cache, "f32"), out="f32")
+
+
+@pytest.mark.parametrize("cache", ["f16", "bf16", "e4m3"])
+def test_attention_long_parts_stay_exact(cache):
+    """float32 results over 2.6 million keys, 2100 of them in each warp's part, against float64.
+
+    Relative error of the whole result, keys and queries of unit variance, 64 elements: weights 2^-22 from the
+    operands' terms and 2^-22 from the exponential, scores about 2^-21 (four cut sums of a score of about one),
+    each 16 keys' sum 2^-22 (cut), and their 131 rounded additions 2^-22: 8e-7 in quadrature, 2^-19 allowed. Sums
+    that are cut at every one of the additions would be 131 * 2^-25 = 4e-6 off, all towards zero."""
+    heads, dim, page, n = 16, 64, 32, 160000
+    g = torch.Generator(device="cuda").manual_seed(17)
+    dtype = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[cache]
+    k, v = (torch.randn(n // page, page, heads, dim, generator=g, device="cuda").to(dtype) for _ in range(2))
+    q = torch.randn(1, heads, dim, generator=g, device="cuda")
+    table = torch.arange(n // page, dtype=torch.int32, device="cuda").view(1, -1)
+    lengths = torch.tensor([n], dtype=torch.int32, device="cuda")
+    out = nt.ninfer_kv_attention(q, nt.KvCache(k, v), table, lengths, out_dtype=torch.float32)
+    for h in range(heads):
+        keys, values = (x[:, :, h].reshape(n, dim).to(torch.float64) for x in (k, v))
+        want = torch.softmax(keys @ q[0, h].double() * dim ** -0.5, 0) @ values
+        assert (out[0, h].double() - want).norm() <= 2.0 ** -19 * want.norm(), (cache, h)
