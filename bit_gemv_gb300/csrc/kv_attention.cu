@@ -136,8 +136,8 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     // a second kernel. On the GPU that costs 5 us (clusters: 7) and 1.8 us for every 8 units of a
     // CTA's part of the longest row; the division of the line costs 9 us (256 elements: 11) and
     // 1.8 us for every unit a warp. Measured, rows of 128 elements in 16 bits, clusters against the line:
-    //   4 rows of 64 units 9.1 / 9.6 us, of 96 10.4 / 9.7;  16 of 32 8.0 / 9.4, of 96 11.3 / 10.2;
-    //   32 of 64 9.8 / 11.8, of 256 20.0 / 17.9;  64 of 64 12.3 / 13.4;  144 (a CTA each) of 32 11.0 / 15.3.
+    //   4 rows of 64 units 9.1 / 9.7 us, of 80 10.2 / 9.9;  16 of 32 8.0 / 9.5, of 80 10.9 / 10.2;  32 of 64
+    //   9.8 / 11.8, of 128 13.1 / 13.4;  64 of 64 12.3 / 13.4, of 80 15.0 / 15.0;  144 (a CTA each) of 32 11.0 / 15.3.
     // Past 32 units a CTA, rows of different lengths would leave most of the SMs waiting. Clusters of
     // eight and four do not fill every SM (their SMs are neighbours): 5/6 and 9/10 are counted on.
     const uint64_t rows = requests * p.head_rows, sms = d.sms;
