@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
     const uint32_t ring_skip = (1024 - (smem_u32(ring_raw) & 1023)) & 1023;
     const uint32_t ring = smem_u32(ring_raw) + ring_skip + warp * (kItems * kItemBytes);
     if (lane < 2) s_row[2 * warp + lane] = kNone;
-    if (threadIdx.x < S::kHeads) s_cta_ml[threadIdx.x] = make_float2(-INFINITY, 0.f);
+    if (threadIdx.x < S::kHeads) s_cta_ml[threadIdx.x] = make_float2(-INFINITY, -1.f);      // no sums (they are never negative)
     pdl_launch_dependents();
     pdl_wait();
 
@@ -906,9 +906,9 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
         Joined sum;
         for (uint32_t c = 0; c < ctas; ++c) {
             const float4 ml = load_cluster(mapa_shared(smem_u32(&s_cta_ml[8 * ht + 2 * t]), c));
-            // a CTA without keys has written no sums
-            if (__any_sync(~0u, ml.x != -INFINITY || ml.z != -INFINITY))
-                sum.add(ml, load_cluster(mapa_shared(smem_u32(cta_o + 32 * job + lane), c)));
+            // a CTA without keys has written no sums; one whose scores are all NaN or -infinity has
+            if (ml.y < 0.f) continue;
+            sum.add(ml, load_cluster(mapa_shared(smem_u32(cta_o + 32 * job + lane), c)));
         }
         store_joined<S>(p, place.eight(ht), job - ht * kTiles, lane, sum);
     }

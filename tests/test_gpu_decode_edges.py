@@ -1,0 +1,84 @@
+"""Decode-step operators on the GPU where results are easily lost: NaN and infinities on
+every path of the attention, and sums and roundings held to the arithmetic that the header states.
+
+The attention has three paths, chosen from the block table's width: a CTA a row, a cluster
+of CTAs a row, and the division of all keys with a second kernel. Only the last one writes to
+its workspace, which is how a test sees that it reached the path that it is about."""
+import numpy as np
+import pytest
+import torch
+
+import bit_gemv_gb300 as nt
+from oracle import decode as od
+
+pytestmark = pytest.mark.gpu
+DEV = torch.device("cuda:0")
+TORCH = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16, "e4m3": torch.float8_e4m3fn}
+
+
+def f64(t):
+    return t.float().cpu().numpy().astype(np.float64)
+
+
+def i32(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.int32)).to(DEV)
+
+
+def attend(q, k, v, table, lengths, width, **kw):
+    """Attention under a block table of `width` pages a row; returns out, lse and whether the keys were divided."""
+    wide = np.full((len(lengths), width), -1, np.int64)
+    wide[:, :np.shape(table)[1]] = table
+    cache = nt.KvCache(k, v)
+    ws = torch.full((nt.ninfer_kv_attention_workspace(cache, *q.shape[:2]),), 0xa5, dtype=torch.uint8, device=DEV)
+    lse = torch.zeros(q.shape[:2], device=DEV)
+    out = nt.ninfer_kv_attention(q, cache, i32(wide), i32(lengths), scale=q.shape[2] ** -0.5, lse=lse, workspace=ws, **kw)
+    return out, lse, bool((ws != 0xa5).any())
+
+
+# 200 keys in 13 pages of 16; tables this wide lead to one CTA, clusters of 2, 4 and 8, and the division
+# (rows of 128 elements in 16 bits are 32 keys a unit: 7, 15, 30, 60 and 200 units)
+WIDTHS = {13: False, 30: False, 60: False, 120: False, 400: True}
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+@pytest.mark.parametrize("group", [1, 8, 16])
+@pytest.mark.parametrize("what", ["query", "one head's query", "keys", "last key", "values", "-inf keys", "-inf keys of infinite values"])
+def test_attention_nan_and_infinity_on_every_path(what, group, width):
+    rng = np.random.default_rng(group)
+    q, k, v = (torch.from_numpy(rng.standard_normal(s).astype(np.float32)).to(DEV).bfloat16()
+               for s in ((1, 2 * group, 128), (13, 16, 2, 128), (13, 16, 2, 128)))
+    # what is spoilt lies in key head 0 (query heads below `group`); key head 1 stays clean
+    if what == "query":
+        q[0, :group] = float("nan")
+    elif what == "one head's query":
+        q[0, 0, 5] = float("nan")
+    elif what == "keys":
+        k[4:6, :, 0] = float("nan")            # one unit of 32 keys, all that a CTA of eight has
+    elif what == "last key":
+        k[12, 7, 0, 127] = float("nan")
+    elif what == "values":
+        v[4:6, :, 0, 3] = float("nan")
+    else:
+        q[0, :group, 0], k[4:6, :, 0, 0] = 1.0, -float("inf")
+        if "values" in what:
+            v[4, 0, 0, 9] = float("inf")
+    out, lse, divided = attend(q, k, v, [list(range(13))], [200], width)
+    assert divided == WIDTHS[width]
+    with np.errstate(invalid="ignore"):
+        want, wlse, _, _ = od.kv_attention(f64(q), f64(k), f64(v), np.arange(13)[None], [200], 128 ** -0.5)
+    if "values" in what and "inf" in what:
+        want[0, :group, 9] = np.nan            # a weight of 0 times an infinite value
+    got, glse = f64(out), f64(lse)
+    assert np.array_equal(np.isnan(got), np.isnan(want)) and np.array_equal(np.isnan(glse), np.isnan(wlse))
+    fine, lfine = np.isfinite(want), np.isfinite(wlse)
+    # scores of deviation one, averages of standard normal values: 2^-6 is eight steps of a bfloat16 result near one
+    assert np.abs(got - want)[fine].max(initial=0) < 2.0 ** -6 and np.abs(glse - wlse)[lfine].max(initial=0) < 2.0 ** -10
+
+
+@pytest.mark.parametrize("width", WIDTHS)
+def test_attention_rows_of_minus_infinity_on_every_path(width):
+    q = torch.ones(1, 8, 128, dtype=torch.bfloat16, device=DEV)
+    k, v = torch.zeros(13, 16, 1, 128, dtype=torch.bfloat16, device=DEV), torch.ones(13, 16, 1, 128, dtype=torch.bfloat16, device=DEV)
+    k[..., 0] = -float("inf")
+    out, lse, _ = attend(q, k, v, [list(range(13))], [200], width)
+    assert (out == 0).all() and (lse == -float("inf")).all()
