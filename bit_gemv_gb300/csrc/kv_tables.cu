@@ -60,7 +60,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
         pages += r.pages;
         if (blockIdx.x == 0) {
             if (p.lengths[i] < 0 || (p.fresh && p.fresh[i] < 0) || r.length + r.fresh > 0x7fffffffu) bad |= NINFER_KV_BAD_LENGTH;
-            if (r.pages && r.held + r.pages > p.table_pages) bad |= NINFER_KV_ROW_TOO_SHORT;
+            if (r.fresh && r.held + r.pages > p.table_pages) bad |= NINFER_KV_ROW_TOO_SHORT;     // fresh pages among them or not
         }
     }
     uint64_t t = tokens, g = pages;

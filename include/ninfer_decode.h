@@ -55,7 +55,7 @@ typedef struct {
 /* Bits of *status. */
 enum {
     NINFER_KV_OUT_OF_PAGES = 1,   /* tables: the free list is shorter than the pages needed */
-    NINFER_KV_ROW_TOO_SHORT = 2,  /* tables: a request needs more than table_pages pages */
+    NINFER_KV_ROW_TOO_SHORT = 2,  /* tables: a request with new tokens needs more than table_pages pages */
     NINFER_KV_OUT_OF_SLOTS = 4,   /* tables: more new tokens than `capacity` (whether or not slots is given) */
     NINFER_KV_BAD_LENGTH = 8,     /* tables: a negative length, or one past 2^31 - 1 */
     NINFER_KV_BAD_SLOT = 16,      /* append: a slot at or past pages * page_size */

@@ -43,8 +43,8 @@ def kv_tables(lengths, new, page, free, table, capacity):
             taken += 1
             if j < width:
                 table[i, j] = fresh[j]
-            else:
-                status |= 2
+        if m and last > width:
+            status |= 2
         for pos in range(n, n + m):
             j = pos // page
             p = -1 if j >= width else fresh.get(j, table[i, j] if j < held else -1)

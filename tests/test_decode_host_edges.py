@@ -1,0 +1,19 @@
+"""Decode-step operators where results or memory are easily lost, the part that needs no
+GPU: the oracle at such inputs, and calls that are refused before any device work (fake aligned
+addresses stand in for device buffers)."""
+import ctypes as C
+
+import bit_gemv_gb300 as nt
+from oracle import decode as od
+
+OK, INVALID, SHAPE = 0, 1, 3
+FAKE = 1 << 20
+lib = nt._lib
+
+
+def test_oracle_reports_rows_too_short_for_tokens_in_held_pages():
+    # 40 tokens need three pages of 16 and so does the 41st; the row has two, and no page is taken
+    _, slots, *_, counts, status = od.kv_tables([40], [1], 16, [5, 6], [[1, 2]], 1)
+    assert slots.tolist() == [-1] and counts.tolist() == [1, 0] and status == 2
+    assert od.kv_tables([40], [0], 16, [5, 6], [[1, 2]], 1)[-1] == 0        # no new token: nothing is lost
+    assert od.kv_tables([31], [1], 16, [5, 6], [[1, 2]], 1)[-1] == 0

@@ -82,3 +82,19 @@ def test_attention_rows_of_minus_infinity_on_every_path(width):
     k[..., 0] = -float("inf")
     out, lse, _ = attend(q, k, v, [list(range(13))], [200], width)
     assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+# ----------------------------------------------------------------- tables ---
+@pytest.mark.parametrize("lengths,new,page,table,status", [
+    ([40], None, 16, [[1, 2]], nt.KV_ROW_TOO_SHORT),                       # in a page that the row has no entry for, taking none
+    ([16, 33], [0, 15], 16, [[3], [4]], nt.KV_ROW_TOO_SHORT),              # 48 tokens: the row's third page is full, none taken
+    ([40], [0], 16, [[1, 2]], 0),                                          # no new token, nothing lost
+    ([31], None, 16, [[1, 2]], 0), ([32], None, 16, [[1, 2]], nt.KV_ROW_TOO_SHORT), ([32], [0], 16, [[1, 2]], 0)])
+def test_tables_rows_too_short(lengths, new, page, table, status):
+    word = torch.zeros(1, dtype=torch.int32, device=DEV)
+    t = nt.ninfer_kv_tables(i32(lengths), None if new is None else i32(new), page, i32([9, 8, 7]), i32(table), 20, status=word)
+    want = od.kv_tables(lengths, [1] * len(lengths) if new is None else new, page, [9, 8, 7], table, 20)
+    for a, b in zip(t, want):
+        assert np.array_equal(a.cpu().numpy(), b)
+    assert int(word) == want[-1] == status
+    assert not status or -1 in t.slots[:int(t.counts[0])].tolist()
