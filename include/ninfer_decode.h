@@ -101,7 +101,7 @@ int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_tokens, uint64_t
 /*
  * ninfer_kv_append -- new keys and values into the cache:
  *   cache.k[slots[t]][h][e] = round(k_new[t][h][e] / k_scale), the same for v,
- *   rounded to nearest-even; NINFER_E4M3 saturates at +-448 and keeps NaN.
+ *   the exact quotient rounded once to nearest-even; NINFER_E4M3 saturates at +-448 and keeps NaN.
  *   k_new, v_new: device, src_dtype f32, bf16 or f16; element e of head h of token t at
  *     t * token_stride + h * head_stride + e (its own strides for each of the two; multiples
  *     of 16 bytes, so that slices of a fused projection's rows can be given as they are).

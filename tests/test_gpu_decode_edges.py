@@ -98,3 +98,33 @@ def test_tables_rows_too_short(lengths, new, page, table, status):
         assert np.array_equal(a.cpu().numpy(), b)
     assert int(word) == want[-1] == status
     assert not status or -1 in t.slots[:int(t.counts[0])].tolist()
+
+
+# ----------------------------------------------------------------- append ---
+@pytest.mark.parametrize("scale", [0.0137, 0.0625, 0.31, 1.7, 3.0, 2.0 ** -130, 1e30])
+@pytest.mark.parametrize("src", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("cache", ["bf16", "f16", "e4m3"])
+def test_append_rounds_the_quotient_once(cache, src, scale):
+    """Sources whose quotients lie at, just below and just above the points halfway between two values of the cache's type.
+
+    The quotient in 64 bits decides: a quotient of two 24-bit numbers that is not halfway between two values
+    of at most 8 bits (11 of f16) differs from that point by more than 2^-24 * 2^-12 of itself, which 53 bits show."""
+    rng = np.random.default_rng(7)
+    scale = float(np.float32(scale))
+    bits = {"bf16": 8, "f16": 11, "e4m3": 4}[cache]
+    halfway = (2 * rng.integers(2 ** (bits - 1), 2 ** bits, 6000) + 1) * 2.0 ** rng.integers(-24, 4, 6000) * rng.choice([-1, 1], 6000)
+    halfway[::7] = rng.standard_normal(halfway[::7].size) * 30
+    with np.errstate(over="ignore"):
+        x = torch.from_numpy((halfway * scale).astype(np.float32)).to(TORCH[src])
+    x[:16] = torch.tensor([0.0, -0.0, float("inf"), -float("inf"), float("nan"), 3e38, -3e38, 1e-45, -1e-45, 1e-38, 65504.0, 1.0,
+                           448.0, 464.0, 1e-4, -6e-8]).to(TORCH[src])
+    x = x.view(375, 1, 16)
+    k, v = (torch.zeros(24, 16, 1, 16, device=DEV).to(TORCH[cache]) for _ in range(2))
+    nt.ninfer_kv_append(nt.KvCache(k, v, scale, 1.0), x.to(DEV), x.to(DEV), torch.arange(375, device=DEV))
+    for pool, by in ((k, scale), (v, 1.0)):
+        want = od.round_to(f64(x) / by, cache, cache == "e4m3").reshape(-1)
+        if cache == "e4m3":
+            want = np.where(np.isinf(f64(x).reshape(-1)), np.sign(f64(x).reshape(-1)) * 448.0, want)
+        got = f64(pool).reshape(-1)[:want.size]
+        assert np.array_equal(got, want, equal_nan=True), np.argwhere(got != want)[:5]
+        assert np.array_equal(np.signbit(got[got == 0]), np.signbit(want[got == 0]))
