@@ -285,7 +285,8 @@ extern "C" int ninfer_logits_process(const void *logits, uint64_t logits_stride,
     if (c.mask && (!c.mask_row_count || (!c.mask_rows && c.mask_row_count < rows)))
         return fail(NINFER_ERR_SHAPE, "logits: %llu mask rows for %llu rows", (unsigned long long)c.mask_row_count,
                     (unsigned long long)rows);
-    if (c.history && c.history_stride > 0x7fffffffull) return fail(NINFER_ERR_SHAPE, "logits: history_stride over 2^31 - 1");
+    // what a table entry counts to; the kernel's 32-bit history indices pass it by less than 2^14
+    if (c.history && c.history_stride > Entry<true>::kCount) return fail(NINFER_ERR_SHAPE, "logits: history_stride over 2^30 - 1");
     if (c.bias_ids && c.bias_count > 0x7fffffffull) return fail(NINFER_ERR_SHAPE, "logits: bias_count over 2^31 - 1");
     if (!aligned(logits, 16) || !aligned(out, 16)) return fail(NINFER_ERR_ALIGNMENT, "logits: logits and out must be 16-byte aligned");
     for (const void *a : {(const void *)c.history, (const void *)c.history_lengths, (const void *)c.prompt_lengths,

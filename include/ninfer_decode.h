@@ -161,7 +161,7 @@ int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests, uint64_t 
  * Computed in fp32, rounded once to dtype.
  *   logits, out: device, dtype f32, bf16 or f16, row b at b * stride elements; out may be
  *     logits itself (same stride).
- *   history: device int32, row b at b * history_stride (tokens outside [0, vocab) are ignored and
+ *   history: device int32, row b at b * history_stride, below 2^30 (tokens outside [0, vocab) are ignored and
  *     set NINFER_LOGITS_BAD_TOKEN); NULL: no history. history_lengths: device
  *     int32[rows] (needed with a history; cut to [0, history_stride]).
  *     prompt_lengths: device int32[rows] or NULL (0).

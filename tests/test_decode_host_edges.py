@@ -17,3 +17,14 @@ def test_oracle_reports_rows_too_short_for_tokens_in_held_pages():
     assert slots.tolist() == [-1] and counts.tolist() == [1, 0] and status == 2
     assert od.kv_tables([40], [0], 16, [5, 6], [[1, 2]], 1)[-1] == 0        # no new token: nothing is lost
     assert od.kv_tables([31], [1], 16, [5, 6], [[1, 2]], 1)[-1] == 0
+
+
+def logits(x=FAKE, out=2 * FAKE, rows=2, vocab=100, stride=100, **kw):
+    return lib.ninfer_logits_process(x, stride, out, stride, nt.F32, rows, vocab, C.byref(nt._LogitsControls(**kw)), None, None)
+
+
+def test_logits_histories_are_shorter_than_a_table_entry_counts():
+    # an entry counts to 2^30 - 1; within 9216 of 2^31 the kernel's index would pass 31 bits
+    for stride in (2 ** 30, 2 ** 31 - 9000, 2 ** 31 - 1):
+        assert logits(history=FAKE, history_lengths=FAKE, history_stride=stride) == SHAPE
+    assert b"history_stride" in lib.ninfer_last_error()
