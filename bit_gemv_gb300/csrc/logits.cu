@@ -82,13 +82,13 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
     const uint8_t *x = static_cast<const uint8_t *>(p.x) + (row * p.x_stride + first) * kEs;
     uint8_t *out = static_cast<uint8_t *>(p.out) + (row * p.out_stride + first) * kEs;
     // the row's numbers, all asked for at once
-    int32_t n = 0, told = 0, b0 = 0, b1 = 0, mask_row = -1;
+    int32_t n = 0, told = 0, bias_from = 0, bias_to = 0, mask_row = -1;
     float rep = 1.f, pres = 0.f, freq = 0.f;
     if (p.c.history) n = p.c.history_lengths[row];
     if (p.c.prompt_lengths) told = p.c.prompt_lengths[row];
     if (p.c.bias_ids) {
-        b0 = p.c.bias_offsets[row];
-        b1 = p.c.bias_offsets[row + 1];
+        bias_from = p.c.bias_offsets[row];
+        bias_to = p.c.bias_offsets[row + 1];
     }
     if (p.c.mask) mask_row = p.c.mask_rows ? p.c.mask_rows[row] : (int32_t)row;
     if (p.c.repetition) rep = p.c.repetition[row];
@@ -118,10 +118,9 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
         }
     };
     read_history(4 * tid);
-    // a thread's first bias and its mask words
-    b0 = max(b0, 0);
-    b1 = min(b1, (int32_t)p.c.bias_count);
-    const bool biased = b0 + (int32_t)tid < b1;
+    // a thread's first bias and its mask words; unsigned, so that an offset near 2^31 - 1 stays past the last entry
+    const uint32_t b0 = min(max(bias_from, 0), (int32_t)p.c.bias_count), b1 = min(max(bias_to, 0), (int32_t)p.c.bias_count);
+    const bool biased = b0 + tid < b1;
     uint32_t bias_token = ~0u;
     float bias_value = 0.f;
     if (biased) {
@@ -167,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
         E::set(table, bias_token, E::kBias);
         bias_logit = load1(x, bias_token, kDtype);
     }
-    for (int32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
+    for (uint32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
         const uint32_t v = (uint32_t)p.c.bias_ids[i];
         if (v >= p.vocab) bad = NINFER_LOGITS_BAD_TOKEN;
         if (v - first < size) E::set(table, v - first, E::kBias);
@@ -247,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
     }
     for (uint32_t i = vecs * kVec + tid; i < size; i += kThreads)
         if (!(entries[i] & E::kBias)) one(i, load1(x, i, kDtype), 0.f);
-    for (int32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
+    for (uint32_t i = b0 + tid + kThreads; i < b1; i += kThreads) {
         const uint32_t at = (uint32_t)p.c.bias_ids[i] - first;
         if (at < size) one(at, load1(x, at, kDtype), p.c.bias_values[i]);
     }

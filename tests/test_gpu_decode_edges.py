@@ -128,3 +128,18 @@ def test_append_rounds_the_quotient_once(cache, src, scale):
         got = f64(pool).reshape(-1)[:want.size]
         assert np.array_equal(got, want, equal_nan=True), np.argwhere(got != want)[:5]
         assert np.array_equal(np.signbit(got[got == 0]), np.signbit(want[got == 0]))
+
+
+# ----------------------------------------------------------------- logits ---
+def test_logits_bias_offsets_are_cut_at_both_ends():
+    """Offsets past bias_count, up to the largest int32, and negative ones: nothing is read there."""
+    x = torch.randn(6, 700, device=DEV)
+    offsets = i32([2 ** 31 - 1, 2 ** 31 - 1, 2 ** 31 - 200, -2 ** 31, 2, 2 ** 31 - 1, 1])
+    ids, values = i32([5, 600, 7]), torch.tensor([1.0, 2.0, 4.0], device=DEV)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    y = nt.ninfer_logits_process(x, bias_offsets=offsets, bias_ids=ids, bias_values=values, status=status)
+    want = x.clone()
+    want[3, 5] += 1.0           # from -2^31 to 2: the first two entries
+    want[3, 600] += 2.0
+    want[4, 7] += 4.0           # from 2 to past the end: the last one
+    assert torch.equal(y, want) and int(status) == 0
