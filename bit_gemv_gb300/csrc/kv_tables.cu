@@ -98,12 +98,23 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
 
     // outputs by request: the runs are dealt out to the CTAs
     if (tid % gridDim.x == blockIdx.x) {
-        uint64_t at = t;
+        uint64_t at = t, base = s_pages[tid];
         for (uint64_t i = first; i < last; ++i) {
             const Request r = request(p, (uint32_t)i);
             if (p.offsets) p.offsets[i] = clamp31(at);
             if (p.lengths_out) p.lengths_out[i] = clamp31((uint64_t)r.length + r.fresh);
+            // pages whose first token is past the slots: entered here, since the loop over tokens ends with the slots
+            // (lengths are whatever the buffer holds, up to 2^31 - 1 a request, and no loop may follow them that far)
+            if (at + r.fresh > p.capacity) {
+                const uint64_t skip = p.capacity > at ? r.length + (p.capacity - at) : r.length;
+                const uint64_t end = min((uint64_t)r.held + r.pages, (uint64_t)p.table_pages);
+                for (uint64_t pi = max((uint64_t)r.held, (skip + p.page.d - 1) / p.page.d); pi < end; ++pi) {
+                    const uint64_t q = base + (pi - r.held);
+                    p.table[i * p.table_stride + pi] = q < p.free_count ? p.free_pages[q] : -1;
+                }
+            }
             at += r.fresh;
+            base += r.pages;
         }
     }
     if (blockIdx.x == 0) {
@@ -121,8 +132,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
 
     // outputs by token, four neighbours a thread (of one request, mostly: one search); the first new
     // token of a fresh page also enters the page
-    const uint64_t all = max(total, (uint64_t)p.capacity);
-    for (uint64_t k0 = 4 * ((uint64_t)blockIdx.x * kThreads + tid); k0 < all; k0 += 4ull * gridDim.x * kThreads) {
+    const uint64_t real = min(total, (uint64_t)p.capacity);
+    for (uint64_t k0 = 4 * ((uint64_t)blockIdx.x * kThreads + tid); k0 < p.capacity; k0 += 4ull * gridDim.x * kThreads) {
         uint32_t lo = 0;                     // last thread whose run starts at or before k0
 #pragma unroll
         for (uint32_t s = kThreads / 2; s; s >>= 1)
@@ -130,15 +141,15 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
         uint64_t at = s_tokens[lo], base = s_pages[lo];
         uint32_t i = lo * p.run;
         Request r = {};
-        if (k0 < total) r = request(p, i);
+        if (k0 < real) r = request(p, i);
         int64_t slot[4];
         int32_t position[4], row[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint64_t k = k0 + j;
             slot[j] = position[j] = row[j] = -1;
-            if (k >= total) continue;
-            while (k >= at + r.fresh) {      // ends: k < total
+            if (k >= real) continue;
+            while (k >= at + r.fresh) {      // ends: k < real
                 at += r.fresh;
                 base += r.pages;
                 r = request(p, ++i);

@@ -100,6 +100,53 @@ def test_tables_rows_too_short(lengths, new, page, table, status):
     assert not status or -1 in t.slots[:int(t.counts[0])].tolist()
 
 
+def test_tables_of_lengths_that_hold_anything_end_with_their_buffers():
+    """The largest new counts for every request (3e11 tokens in all): the work is that of the buffers' sizes."""
+    n = 150
+    rng = np.random.default_rng(3)
+    lengths, new = rng.integers(0, 40, n), np.full(n, 2 ** 31 - 1)
+    new[[5, 77]] = 0
+    table, free = np.full((n, 6), -1), rng.permutation(800)
+    held = -(-lengths // 8)
+    table[np.arange(6) < held[:, None]] = 1000 + np.arange(held.sum())
+    for capacity in (0, 1, 30, 1000):
+        word = torch.zeros(1, dtype=torch.int32, device=DEV)
+        t = nt.ninfer_kv_tables(i32(lengths), i32(new), 8, i32(free), i32(table), capacity, status=word)
+        torch.cuda.synchronize()
+        # page counts run up to 2^28 a request, so that the first request takes the whole list; the others' entries are -1
+        want = table.copy()
+        for i in range(n):
+            if new[i]:
+                want[i, held[i]:] = free[:6 - held[i]] if i == 0 else -1
+        assert np.array_equal(t.block_table.cpu().numpy(), want), capacity
+        assert t.counts.tolist() == [2 ** 31 - 1] * 2
+        position = np.arange(lengths[0], lengths[0] + capacity)
+        entry = want[0][np.minimum(position // 8, 5)]
+        slots = np.where(position // 8 < 6, entry * 8 + position % 8, -1)
+        assert np.array_equal(t.slots.cpu().numpy(), slots) and np.array_equal(t.positions.cpu().numpy(), position)
+        assert not t.token_rows.any() and t.offsets.tolist()[:2] == [0, 2 ** 31 - 1]
+        assert int(word) == nt.KV_OUT_OF_PAGES | nt.KV_ROW_TOO_SHORT | nt.KV_OUT_OF_SLOTS | nt.KV_BAD_LENGTH
+
+
+@pytest.mark.parametrize("page", [1, 7, 16])
+@pytest.mark.parametrize("requests", [3, 1500])
+def test_tables_with_fewer_slots_than_tokens(requests, page):
+    """Whole tables whatever the slots hold: none of them, the middle of a page or of a request, all but one."""
+    rng = np.random.default_rng(requests)
+    lengths, new = rng.integers(0, 50, requests), rng.integers(0, 60, requests)
+    held, last = -(-lengths // page), -(-(lengths + new) // page)
+    pool = rng.permutation(int(last.sum()))
+    table = np.full((requests, int(last.max())), -1, np.int64)
+    table[np.arange(table.shape[1]) < held[:, None]] = pool[:held.sum()]
+    total = int(new.sum())
+    for capacity in (0, 1, 5, total // 3, total // 2 + 1, total - 1, total, total + 9):
+        for width in (table.shape[1], 3):
+            for free in (pool[held.sum():], pool[held.sum():][:20]):
+                t = nt.ninfer_kv_tables(i32(lengths), i32(new), page, i32(free), i32(table[:, :width]), capacity)
+                for a, b in zip(t, od.kv_tables(lengths, new, page, free, table[:, :width], capacity)):
+                    assert np.array_equal(a.cpu().numpy(), b)
+
+
 # ----------------------------------------------------------------- append ---
 @pytest.mark.parametrize("scale", [0.0137, 0.0625, 0.31, 1.7, 3.0, 2.0 ** -130, 1e30])
 @pytest.mark.parametrize("src", ["f32", "bf16", "f16"])
