@@ -434,7 +434,8 @@ class KvTables(namedtuple("KvTables", ("block_table", "slots", "positions", "tok
 def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_table, capacity: int, out=None, status=None):
     """Block tables and slot maps of a step's new tokens from the requests'
     lengths: fills the fresh entries of block_table in place and returns a
-    KvTables. new_tokens None: one a request; free_pages None: no free page."""
+    KvTables. new_tokens None: one a request; free_pages None: no free page.
+    out.lengths may not be lengths: copy them once the step has read both."""
     _TYPES or _types()
     if out is None:
         out = KvTables.empty(block_table, capacity)

@@ -188,6 +188,21 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TablesParams p) 
     }
 }
 
+// A contiguous buffer, and whether it shares memory with rows of `row` bytes, `stride` apart.
+struct Buffer {
+    const void *at;
+    uint64_t bytes;
+    bool meets(const void *rows, uint64_t count, uint64_t row, uint64_t stride) const {
+        const uint64_t a = reinterpret_cast<uint64_t>(at), b = reinterpret_cast<uint64_t>(rows);
+        if (!at || !rows || !bytes || !row || !count) return false;
+        if (count == 1) stride = row;
+        if (a + bytes <= b || a >= b + (count - 1) * stride + row) return false;
+        if (a <= b) return true;
+        const uint64_t in = (a - b) % stride;
+        return in < row || in + bytes > stride;
+    }
+};
+
 }  // namespace
 }  // namespace ninfer
 
@@ -213,6 +228,18 @@ extern "C" int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_token
                           (const void *)offsets, (const void *)lengths_out, (const void *)counts, (const void *)status})
         if (!aligned(a, 4)) return fail(NINFER_ERR_ALIGNMENT, "tables: int32 buffers must be 4-byte aligned");
     if (!aligned(slots, 8)) return fail(NINFER_ERR_ALIGNMENT, "tables: slots must be 8-byte aligned");
+    // every CTA reads the inputs while others write (the row of a table that another one fills is not read)
+    const Buffer in[] = {{lengths, 4 * requests}, {new_tokens, 4 * requests}, {free_pages, 4 * free_count}};
+    const Buffer outs[] = {{slots, 8 * capacity}, {positions, 4 * capacity}, {token_rows, 4 * capacity}, {offsets, 4 * (requests + 1)},
+                           {lengths_out, 4 * requests}, {counts, 8}, {status, 4}};
+    for (const Buffer &i : in) {
+        bool shared = i.meets(block_table, requests, 4 * table_pages, 4 * table_stride);
+        for (const Buffer &o : outs) shared |= o.meets(i.at, 1, i.bytes, i.bytes);
+        if (shared) return fail(NINFER_ERR_INVALID_ARGUMENT, "tables: an output overlaps an input (lengths_out may not be lengths)");
+    }
+    for (const Buffer &o : outs)
+        if (o.meets(block_table, requests, 4 * table_pages, 4 * table_stride))
+            return fail(NINFER_ERR_INVALID_ARGUMENT, "tables: an output overlaps block_table");
     TablesParams p;
     p.lengths = lengths;
     p.fresh = new_tokens;

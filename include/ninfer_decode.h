@@ -83,12 +83,12 @@ enum {
  *     last new token are set to -1 (append skips them), so that a captured step can have
  *     a fixed size; offsets int32[requests + 1], lengths_out int32[requests] (lengths +
  *     new), counts int32[2] (new tokens, pages taken). Any of the six may be NULL.
- *     Outputs may not overlap inputs.
+ *     Outputs may not overlap inputs or block_table (a loop cannot write its lengths in place).
  *   A token that got no page (list or row too short) has slot -1, and its table entry
  *   (if there is one) is -1; offsets, lengths_out and counts are unaffected. Negative
  *   lengths count as 0; results past 2^31 - 1 are clamped to it.
  * Errors: INVALID_ARGUMENT (NULL lengths or block_table; free_pages NULL with a
- *   count), SHAPE (requests, page_size or table_pages 0; any of them, or capacity or
+ *   count; an output that overlaps an input or block_table), SHAPE (requests, page_size or table_pages 0; any of them, or capacity or
  *   free_count, over 2^31 - 1; table_stride < table_pages), ALIGNMENT, CUDA.
  */
 int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_tokens, uint64_t requests,

@@ -28,3 +28,23 @@ def test_logits_histories_are_shorter_than_a_table_entry_counts():
     for stride in (2 ** 30, 2 ** 31 - 9000, 2 ** 31 - 1):
         assert logits(history=FAKE, history_lengths=FAKE, history_stride=stride) == SHAPE
     assert b"history_stride" in lib.ninfer_last_error()
+
+
+def tables(lengths=FAKE, new=2 * FAKE, n=4, free=3 * FAKE, count=9, table=4 * FAKE, width=5, stride=8, slots=5 * FAKE, pos=6 * FAKE,
+           rows=7 * FAKE, cap=8, off=8 * FAKE, lo=9 * FAKE, counts=10 * FAKE, status=11 * FAKE):
+    return lib.ninfer_kv_tables(lengths, new, n, 16, free, count, table, width, stride, slots, pos, rows, cap, off, lo, counts,
+                                status, None)
+
+
+def test_tables_outputs_that_overlap_inputs():
+    # lengths_out = lengths is what a loop would write: CTAs that come later would count from the new lengths
+    assert tables(lo=FAKE) == INVALID
+    assert b"lengths_out may not be lengths" in lib.ninfer_last_error()
+    assert tables(lo=FAKE + 12) == INVALID and tables(lo=FAKE - 12) == INVALID
+    assert tables(lo=2 * FAKE) == INVALID and tables(off=FAKE - 16) == INVALID and tables(slots=3 * FAKE + 32) == INVALID
+    assert tables(pos=FAKE - 28) == INVALID and tables(rows=2 * FAKE + 8) == INVALID
+    assert tables(counts=3 * FAKE + 32) == INVALID and tables(status=2 * FAKE + 12) == INVALID
+    # rows of 20 bytes, 32 apart
+    assert tables(table=FAKE) == INVALID and tables(table=3 * FAKE - 96) == INVALID
+    assert tables(counts=4 * FAKE + 32 + 16) == INVALID and tables(counts=4 * FAKE + 3 * 32 - 4) == INVALID
+    assert tables(slots=4 * FAKE + 24) == INVALID and tables(status=4 * FAKE + 3 * 32 + 16) == INVALID

@@ -147,6 +147,18 @@ def test_tables_with_fewer_slots_than_tokens(requests, page):
                     assert np.array_equal(a.cpu().numpy(), b)
 
 
+def test_tables_outputs_between_a_tables_rows():
+    """Lengths in place are refused; what lies between the rows of a wider buffer is no part of the table."""
+    wide = torch.full((3, 8), -1, dtype=torch.int32, device=DEV)
+    table, lengths, free = wide[:, :5], i32([0, 3, 9]), i32([7, 2, 5])
+    out = nt.KvTables.empty(table, 3)
+    with pytest.raises(nt.NinferError) as e:
+        nt.ninfer_kv_tables(lengths, None, 8, free, table, 3, out=out._replace(lengths=lengths))
+    assert e.value.status == 1 and (wide == -1).all()
+    t = nt.ninfer_kv_tables(lengths, None, 8, free, table, 3, out=out._replace(counts=wide[1, 5:7]))
+    assert wide.tolist() == [[7] + [-1] * 7, [-1] * 5 + [3, 1, -1], [-1] * 8] and t.lengths.tolist() == [1, 4, 10]
+
+
 # ----------------------------------------------------------------- append ---
 @pytest.mark.parametrize("scale", [0.0137, 0.0625, 0.31, 1.7, 3.0, 2.0 ** -130, 1e30])
 @pytest.mark.parametrize("src", ["f32", "bf16", "f16"])
