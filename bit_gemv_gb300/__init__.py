@@ -389,24 +389,39 @@ def _table(t, name):
 class KvCache:
     """A paged key/value cache over two pools indexed [page][token][head][element]
     (any strides, the last dimension contiguous; bfloat16, float16 or
-    float8_e4m3fn). A stored value stands for itself times k_scale (v_scale)."""
+    float8_e4m3fn). A stored value stands for itself times k_scale (v_scale). The
+    pools are read and checked when the cache is made, and again by the next call
+    where their memory was replaced (resize_, set_, .data)."""
 
     def __init__(self, k, v, k_scale: float = 1.0, v_scale: float = 1.0):
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._read()
+
+    def _read(self):
+        k, v = self.k, self.v
         code, strides = _rows(k, "k", 4, (BF16, F16, E4M3))
         if _rows(v, "v", 4, (BF16, F16, E4M3)) != (code, strides) or v.shape != k.shape or v.device != k.device:
             raise ValueError("k and v must have the same dtype, shape, strides and device")
-        self.k, self.v = k, v
         pages, page_size, heads, dim = k.shape
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
         strides = [s if n > 1 else 0 for s, n in zip(strides, k.shape)]
         self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dim, strides[0], strides[1],
-                                      strides[2], k_scale, v_scale, code, 0)
+                                      strides[2], self.k_scale, self.v_scale, code, 0)
         self._ref = C.byref(self._struct)
+        self._seen = k.data_ptr(), v.data_ptr()
+        self._held = k.detach(), v.detach()
+
+    def _current(self):
+        """The library's description of the pools as they are now."""
+        if self._seen != (self.k.data_ptr(), self.v.data_ptr()):
+            self._read()
+        return self._ref
 
 
 class KvTables(namedtuple("KvTables", ("block_table", "slots", "positions", "token_rows", "offsets", "lengths", "counts"))):
     """What ninfer_kv_tables writes; give one back as `out` to reuse its buffers,
-    which are checked when it is first used."""
+    which are checked when it is first used and again where the memory of one was
+    replaced (resize_, set_, .data) or the table has another shape."""
 
     @classmethod
     def empty(cls, block_table, capacity: int):
@@ -418,16 +433,20 @@ class KvTables(namedtuple("KvTables", ("block_table", "slots", "positions", "tok
                    new(n, i32), new(2, i32))
 
     def _addresses(self, capacity: int):
+        # Aliases keep the checked memory alive, so that an address that is still the same is the same memory.
+        table, t, p, r, o, n, c = self
+        seen = (capacity, table.data_ptr(), table.shape, table.stride(), t is None or t.data_ptr(),
+                p is None or p.data_ptr(), r is None or r.data_ptr(), o is None or o.data_ptr(),
+                n is None or n.data_ptr(), c is None or c.data_ptr())
         known = self.__dict__.get("_known")
-        if known is None or known[0] != capacity:
-            table = _table(self.block_table, "block_table")
-            n = table[1]
+        if known is None or known[0] != seen:
+            rows = _table(table, "block_table")
+            requests = rows[1]
             known = self.__dict__["_known"] = (
-                capacity, table,
-                (_arg(self.slots, "slots", _I64, capacity), _arg(self.positions, "positions", _I32, capacity),
-                 _arg(self.token_rows, "token_rows", _I32, capacity)),
-                (_arg(self.offsets, "offsets", _I32, n + 1), _arg(self.lengths, "lengths", _I32, n),
-                 _arg(self.counts, "counts", _I32, 2)))
+                seen, rows,
+                (_arg(t, "slots", _I64, capacity), _arg(p, "positions", _I32, capacity), _arg(r, "token_rows", _I32, capacity)),
+                (_arg(o, "offsets", _I32, requests + 1), _arg(n, "lengths", _I32, requests), _arg(c, "counts", _I32, 2)),
+                [x.detach() for x in self if x is not None])
         return known
 
 
@@ -441,7 +460,7 @@ def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_tabl
         out = KvTables.empty(block_table, capacity)
     elif out.block_table is not block_table:
         out = out._replace(block_table=block_table)
-    _, (table, n, width, stride), tokens, requests = out._addresses(capacity)
+    _, (table, n, width, stride), tokens, requests, _ = out._addresses(capacity)
     free = free_pages.numel() if free_pages is not None else 0
     _check(_lib.ninfer_kv_tables(
         _arg(lengths, "lengths", _I32, n), _arg(new_tokens, "new_tokens", _I32, n), n, page_size,
@@ -452,6 +471,7 @@ def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_tabl
 
 def ninfer_kv_append(cache: KvCache, k, v, slots, status=None) -> None:
     """Writes the new keys and values k, v (tokens, kv_heads, head_dim) into the cache's slots."""
+    ref = cache._current()
     code, ks = _rows(k, "k", 3, (F32, BF16, F16))
     code_v, vs = _rows(v, "v", 3, (F32, BF16, F16))
     shape = k.shape
@@ -459,13 +479,13 @@ def ninfer_kv_append(cache: KvCache, k, v, slots, status=None) -> None:
         raise ValueError("k and v must be (tokens, kv_heads, head_dim) of the cache and of one dtype")
     tokens = shape[0]
     _check(_lib.ninfer_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1],
-                                 _arg(slots, "slots", _I64, tokens), cache._ref, _arg(status, "status", _I32, 1),
+                                 _arg(slots, "slots", _I64, tokens), ref, _arg(status, "status", _I32, 1),
                                  _raw_stream(k.get_device())))
 
 
 def ninfer_kv_attention_workspace(cache: KvCache, requests: int, q_heads: int) -> int:
     b = C.c_uint64()
-    _check(_lib.ninfer_kv_attention_workspace(cache._ref, requests, q_heads, C.byref(b)))
+    _check(_lib.ninfer_kv_attention_workspace(cache._current(), requests, q_heads, C.byref(b)))
     return b.value
 
 
@@ -475,6 +495,7 @@ def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, win
     over the cache's pages in block_table (requests, table_pages); lengths count
     the new token. scale: head_dim ** -0.5 unless given; window 0: every key.
     lse: a float32 (requests, q_heads) tensor to be written, or None."""
+    ref = cache._current()
     code, strides = _rows(q, "q", 3, (F32, BF16, F16))
     requests, heads, dim = q.shape
     if dim != cache.head_dim:
@@ -491,7 +512,7 @@ def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, win
         raise ValueError("workspace must be a contiguous CUDA tensor")
     dtype = out.dtype
     _check(_lib.ninfer_kv_attention(
-        q.data_ptr(), code, requests, heads, strides[0], strides[1], cache._ref, table, width, stride,
+        q.data_ptr(), code, requests, heads, strides[0], strides[1], ref, table, width, stride,
         _arg(lengths, "lengths", _I32, requests), dim ** -0.5 if scale is None else scale, window,
         _arg(out, "out", dtype, requests * heads * dim), _TYPES.get(dtype, -1), _arg(lse, "lse", _F32, requests * heads),
         workspace.data_ptr(), workspace.nbytes, _raw_stream(q.get_device())))

@@ -1,7 +1,10 @@
 """Decode-step operators where results or memory are easily lost, the part that needs no
 GPU: the oracle at such inputs, and calls that are refused before any device work (fake aligned
 addresses stand in for device buffers)."""
+import copy
 import ctypes as C
+
+import pytest
 
 import bit_gemv_gb300 as nt
 from oracle import decode as od
@@ -48,3 +51,90 @@ def test_tables_outputs_that_overlap_inputs():
     assert tables(table=FAKE) == INVALID and tables(table=3 * FAKE - 96) == INVALID
     assert tables(counts=4 * FAKE + 32 + 16) == INVALID and tables(counts=4 * FAKE + 3 * 32 - 4) == INVALID
     assert tables(slots=4 * FAKE + 24) == INVALID and tables(status=4 * FAKE + 3 * 32 + 16) == INVALID
+
+
+# ---------------------------------------------------------------- binding ---
+class Tensor:
+    """What the binding asks of a contiguous CUDA tensor."""
+    is_cuda = True
+
+    def __init__(self, at, dtype, *shape, device=0):
+        self.at, self.dtype, self.shape, self.index = at, dtype, shape, device
+
+    def data_ptr(self):
+        return self.at
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def stride(self):
+        strides = [1]
+        for s in self.shape[:0:-1]:
+            strides.insert(0, strides[0] * s)
+        return tuple(strides)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.index
+
+    @property
+    def device(self):
+        return "cuda:%d" % self.index
+
+    def detach(self):
+        return copy.copy(self)
+
+
+def buffers(device=0, requests=3, capacity=5):
+    torch = pytest.importorskip("torch")
+    i32 = lambda at, n: Tensor(at * FAKE, torch.int32, n, device=device)  # noqa: E731
+    return nt.KvTables(Tensor(FAKE, torch.int32, requests, 4, device=device), Tensor(2 * FAKE, torch.int64, capacity, device=device),
+                       i32(3, capacity), i32(4, capacity), i32(5, requests + 1), i32(6, requests), i32(7, 2))
+
+
+def test_kv_tables_looks_at_its_buffers_again():
+    nt._types()
+    t = buffers()
+    _, table, tokens, requests, *_ = t._addresses(5)
+    assert table == (FAKE, 3, 4, 4) and tokens == (2 * FAKE, 3 * FAKE, 4 * FAKE) and requests == (5 * FAKE, 6 * FAKE, 7 * FAKE)
+    t.positions.at = 30 * FAKE                              # memory replaced in place, as by resize_ or set_
+    t.lengths.at = 60 * FAKE
+    _, _, tokens, requests, *_ = t._addresses(5)
+    assert tokens == (2 * FAKE, 30 * FAKE, 4 * FAKE) and requests == (5 * FAKE, 60 * FAKE, 7 * FAKE)
+    t.block_table.shape = (3, 9)                            # longer rows at the same place
+    assert t._addresses(5)[1] == (FAKE, 3, 9, 9)
+    t.block_table.at = 10 * FAKE
+    assert t._addresses(5)[1] == (10 * FAKE, 3, 9, 9)
+    t.slots.at, t.slots.shape = 20 * FAKE, (4,)
+    for _ in range(2):
+        with pytest.raises(ValueError):
+            t._addresses(5)
+
+
+def test_kv_tables_copies_have_buffers_of_their_own():
+    nt._types()
+    t = buffers()
+    t._addresses(5)
+    other = copy.deepcopy(t)
+    for x in other:
+        x.at += FAKE // 2
+    assert other._addresses(5)[2] == tuple(a + FAKE // 2 for a in t._addresses(5)[2])
+
+
+def test_kv_cache_looks_at_its_pools_again():
+    torch = pytest.importorskip("torch")
+    k, v = (Tensor(at * FAKE, torch.bfloat16, 8, 16, 2, 64) for at in (1, 2))
+    c = nt.KvCache(k, v, 0.5, 0.25)
+    k.at, v.at = 3 * FAKE, 4 * FAKE
+    for t in (k, v):
+        t.shape = (32, 16, 2, 64)
+    s = c._current()._obj
+    assert (s.k, s.v, s.pages, s.page_stride, s.k_scale, s.v_scale) == (3 * FAKE, 4 * FAKE, 32, 2048, 0.5, 0.25) and c.pages == 32
+    k.at, k.shape = 5 * FAKE, (16, 16, 2, 64)               # one pool alone
+    with pytest.raises(ValueError):
+        c._current()

@@ -4,6 +4,8 @@ every path of the attention, and sums and roundings held to the arithmetic that 
 The attention has three paths, chosen from the block table's width: a CTA a row, a cluster
 of CTAs a row, and the division of all keys with a second kernel. Only the last one writes to
 its workspace, which is how a test sees that it reached the path that it is about."""
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -157,6 +159,36 @@ def test_tables_outputs_between_a_tables_rows():
     assert e.value.status == 1 and (wide == -1).all()
     t = nt.ninfer_kv_tables(lengths, None, 8, free, table, 3, out=out._replace(counts=wide[1, 5:7]))
     assert wide.tolist() == [[7] + [-1] * 7, [-1] * 5 + [3, 1, -1], [-1] * 8] and t.lengths.tolist() == [1, 4, 10]
+
+
+def test_tables_and_cache_follow_memory_that_is_replaced():
+    """A batch whose rows get more pages, and a cache that gets more of them, in place."""
+    table, free = torch.full((2, 2), -1, dtype=torch.int32, device=DEV), i32([3, 1, 0, 2, 7, 6, 5, 4])
+    out = nt.KvTables.empty(table, 2)
+    nt.ninfer_kv_tables(i32([0, 7]), None, 8, free, table, 2, out=out)
+    old = table.detach().clone()
+    twin = copy.deepcopy(out)
+    nt.ninfer_kv_tables(i32([16, 40]), None, 8, free, twin.block_table, 2, out=twin)
+    assert torch.equal(out.block_table, old) and out.lengths.tolist() == [1, 8] and twin.lengths.tolist() == [17, 41]
+    table.resize_(2, 6).fill_(-1)
+    t = nt.ninfer_kv_tables(i32([16, 40]), None, 8, free, table, 2, out=out)
+    assert table.tolist() == [[-1, -1, 3, -1, -1, -1], [-1] * 5 + [1]] and t.slots.tolist() == [24, 8]
+    table.data = table.clone().fill_(-1)
+    out.slots.data = torch.zeros(2, dtype=torch.int64, device=DEV)
+    t = nt.ninfer_kv_tables(i32([16, 40]), None, 8, free, table, 2, out=out)
+    assert table.tolist() == [[-1, -1, 3, -1, -1, -1], [-1] * 5 + [1]] and out.slots.tolist() == [24, 8]
+
+    k, v = torch.zeros(2, 8, 1, 16, dtype=torch.bfloat16, device=DEV), torch.zeros(2, 8, 1, 16, dtype=torch.bfloat16, device=DEV)
+    cache = nt.KvCache(k, v)
+    x = torch.ones(2, 1, 16, dtype=torch.bfloat16, device=DEV)
+    nt.ninfer_kv_append(cache, x, x, torch.tensor([3, 15], device=DEV))
+    for p in (k, v):
+        p.resize_(4, 8, 1, 16)
+        p[2:] = 0
+    nt.ninfer_kv_append(cache, x * 2, x * 3, t.slots)
+    assert (k[3, 0] == 2).all() and (v[1, 0] == 3).all() and (k[0, 3] == 1).all() and (k[1, 7] == 1).all()
+    y = nt.ninfer_kv_attention(x[:, :, :16].contiguous(), cache, i32([[3], [1]]), i32([1, 1]))
+    assert torch.equal(y[0], v[3, 0]) and (y[1] == 3).all()
 
 
 # ----------------------------------------------------------------- append ---
