@@ -345,43 +345,53 @@ def ninfer_ternary_embed(fmt, payload, n: int, k: int, ids, signs=None, out=None
 # go to the library as plain integers, the controls of the logits as packed bytes.
 _TYPES: dict = {}       # torch dtype -> library dtype
 _I32 = _I64 = _F32 = _raw_stream = None
+_several = False        # whether torch sees more than one GPU
 _CONTROLS = struct.Struct("=15Q")
 
 
 def _types():
-    global _I32, _I64, _F32, _raw_stream
+    global _I32, _I64, _F32, _raw_stream, _several
     if not _TYPES:
         torch = _torch()
+        _several = torch.cuda.device_count() > 1
         _I32, _I64, _F32, _raw_stream = torch.int32, torch.int64, torch.float32, torch._C._cuda_getCurrentRawStream
         _TYPES.update({torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16, torch.float8_e4m3fn: E4M3})
     return _TYPES
 
 
-def _arg(t, name, dtype, count):
-    """Address of a contiguous CUDA tensor of one dtype and `count` elements; None is 0."""
+def _on(t, name):
+    """The GPU that a call's first tensor lies on, and with it all others: the current one, where the library launches."""
+    device = t.get_device()
+    if device < 0 or _several and device != _torch().cuda.current_device():
+        raise ValueError(f"{name} must be a CUDA tensor on the current device, not on {t.device}")
+    return device
+
+
+def _arg(t, name, dtype, count, device):
+    """Address of a contiguous tensor of one dtype and `count` elements on a GPU; None is 0."""
     if t is None:
         return 0
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or t.numel() != count:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {count} elements of {dtype}, "
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous tensor of {count} elements of {dtype} on cuda:{device}, "
                          f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
     return t.data_ptr()
 
 
-def _rows(t, name, dims, dtypes):
-    """Checks a CUDA tensor whose last dimension is contiguous and whose other
+def _rows(t, name, dims, dtypes, device):
+    """Checks a tensor on a GPU whose last dimension is contiguous and whose other
     strides are free; returns its library dtype and its strides."""
-    code = (_TYPES or _types()).get(t.dtype, -1)
+    code = _TYPES.get(t.dtype, -1)
     strides = t.stride()
-    if not t.is_cuda or len(strides) != dims or code not in dtypes or (strides[-1] != 1 and t.shape[-1] > 1):
-        raise ValueError(f"{name} must be a CUDA tensor of {dims} dimensions, the last one contiguous, of a supported dtype")
+    if t.get_device() != device or len(strides) != dims or code not in dtypes or (strides[-1] != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} must be a tensor of {dims} dimensions, the last one contiguous, of a supported dtype on cuda:{device}")
     return code, strides
 
 
-def _table(t, name):
+def _table(t, name, device):
     """Address, width and row stride of an int32 table with contiguous rows."""
     strides = t.stride()
-    if t.dtype is not _I32 or not t.is_cuda or len(strides) != 2 or (strides[1] != 1 and t.shape[1] > 1):
-        raise ValueError(f"{name} must be a two-dimensional int32 CUDA tensor with contiguous rows")
+    if t.dtype is not _I32 or t.get_device() != device or len(strides) != 2 or (strides[1] != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a two-dimensional int32 tensor with contiguous rows on cuda:{device}")
     n, width = t.shape
     return t.data_ptr(), n, width, strides[0] if n > 1 else width
 
@@ -399,8 +409,10 @@ class KvCache:
 
     def _read(self):
         k, v = self.k, self.v
-        code, strides = _rows(k, "k", 4, (BF16, F16, E4M3))
-        if _rows(v, "v", 4, (BF16, F16, E4M3)) != (code, strides) or v.shape != k.shape or v.device != k.device:
+        _TYPES or _types()
+        device = _on(k, "k")
+        code, strides = _rows(k, "k", 4, (BF16, F16, E4M3), device)
+        if _rows(v, "v", 4, (BF16, F16, E4M3), device) != (code, strides) or v.shape != k.shape:
             raise ValueError("k and v must have the same dtype, shape, strides and device")
         pages, page_size, heads, dim = k.shape
         self.pages, self.page_size, self.kv_heads, self.head_dim = pages, page_size, heads, dim
@@ -408,13 +420,15 @@ class KvCache:
         self._struct = _KvCacheStruct(k.data_ptr(), v.data_ptr(), pages, page_size, heads, dim, strides[0], strides[1],
                                       strides[2], self.k_scale, self.v_scale, code, 0)
         self._ref = C.byref(self._struct)
-        self._seen = k.data_ptr(), v.data_ptr()
+        self._device, self._seen = device, (k.data_ptr(), v.data_ptr())
         self._held = k.detach(), v.detach()
 
-    def _current(self):
-        """The library's description of the pools as they are now."""
+    def _current(self, device):
+        """The library's description of the pools as they are now, for a call on a GPU."""
         if self._seen != (self.k.data_ptr(), self.v.data_ptr()):
             self._read()
+        if self._device != device:
+            raise ValueError(f"the cache lies on cuda:{self._device}, not on cuda:{device}")
         return self._ref
 
 
@@ -432,20 +446,22 @@ class KvTables(namedtuple("KvTables", ("block_table", "slots", "positions", "tok
         return cls(block_table, new(capacity, torch.int64), new(capacity, i32), new(capacity, i32), new(n + 1, i32),
                    new(n, i32), new(2, i32))
 
-    def _addresses(self, capacity: int):
+    def _addresses(self, capacity: int, device: int):
         # Aliases keep the checked memory alive, so that an address that is still the same is the same memory.
         table, t, p, r, o, n, c = self
-        seen = (capacity, table.data_ptr(), table.shape, table.stride(), t is None or t.data_ptr(),
+        seen = (capacity, device, table.data_ptr(), table.shape, table.stride(), t is None or t.data_ptr(),
                 p is None or p.data_ptr(), r is None or r.data_ptr(), o is None or o.data_ptr(),
                 n is None or n.data_ptr(), c is None or c.data_ptr())
         known = self.__dict__.get("_known")
         if known is None or known[0] != seen:
-            rows = _table(table, "block_table")
+            rows = _table(table, "block_table", device)
             requests = rows[1]
             known = self.__dict__["_known"] = (
                 seen, rows,
-                (_arg(t, "slots", _I64, capacity), _arg(p, "positions", _I32, capacity), _arg(r, "token_rows", _I32, capacity)),
-                (_arg(o, "offsets", _I32, requests + 1), _arg(n, "lengths", _I32, requests), _arg(c, "counts", _I32, 2)),
+                (_arg(t, "slots", _I64, capacity, device), _arg(p, "positions", _I32, capacity, device),
+                 _arg(r, "token_rows", _I32, capacity, device)),
+                (_arg(o, "offsets", _I32, requests + 1, device), _arg(n, "lengths", _I32, requests, device),
+                 _arg(c, "counts", _I32, 2, device)),
                 [x.detach() for x in self if x is not None])
         return known
 
@@ -456,36 +472,38 @@ def ninfer_kv_tables(lengths, new_tokens, page_size: int, free_pages, block_tabl
     KvTables. new_tokens None: one a request; free_pages None: no free page.
     out.lengths may not be lengths: copy them once the step has read both."""
     _TYPES or _types()
+    device = _on(lengths, "lengths")
     if out is None:
         out = KvTables.empty(block_table, capacity)
     elif out.block_table is not block_table:
         out = out._replace(block_table=block_table)
-    _, (table, n, width, stride), tokens, requests, _ = out._addresses(capacity)
+    _, (table, n, width, stride), tokens, requests, _ = out._addresses(capacity, device)
     free = free_pages.numel() if free_pages is not None else 0
     _check(_lib.ninfer_kv_tables(
-        _arg(lengths, "lengths", _I32, n), _arg(new_tokens, "new_tokens", _I32, n), n, page_size,
-        _arg(free_pages, "free_pages", _I32, free), free, table, width, stride, *tokens, capacity, *requests,
-        _arg(status, "status", _I32, 1), _raw_stream(lengths.get_device())))
+        _arg(lengths, "lengths", _I32, n, device), _arg(new_tokens, "new_tokens", _I32, n, device), n, page_size,
+        _arg(free_pages, "free_pages", _I32, free, device), free, table, width, stride, *tokens, capacity, *requests,
+        _arg(status, "status", _I32, 1, device), _raw_stream(device)))
     return out
 
 
 def ninfer_kv_append(cache: KvCache, k, v, slots, status=None) -> None:
     """Writes the new keys and values k, v (tokens, kv_heads, head_dim) into the cache's slots."""
-    ref = cache._current()
-    code, ks = _rows(k, "k", 3, (F32, BF16, F16))
-    code_v, vs = _rows(v, "v", 3, (F32, BF16, F16))
+    device = _on(k, "k")
+    ref = cache._current(device)
+    code, ks = _rows(k, "k", 3, (F32, BF16, F16), device)
+    code_v, vs = _rows(v, "v", 3, (F32, BF16, F16), device)
     shape = k.shape
     if code != code_v or shape != v.shape or shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
         raise ValueError("k and v must be (tokens, kv_heads, head_dim) of the cache and of one dtype")
     tokens = shape[0]
     _check(_lib.ninfer_kv_append(k.data_ptr(), v.data_ptr(), code, tokens, ks[0], ks[1], vs[0], vs[1],
-                                 _arg(slots, "slots", _I64, tokens), ref, _arg(status, "status", _I32, 1),
-                                 _raw_stream(k.get_device())))
+                                 _arg(slots, "slots", _I64, tokens, device), ref, _arg(status, "status", _I32, 1, device),
+                                 _raw_stream(device)))
 
 
 def ninfer_kv_attention_workspace(cache: KvCache, requests: int, q_heads: int) -> int:
     b = C.c_uint64()
-    _check(_lib.ninfer_kv_attention_workspace(cache._current(), requests, q_heads, C.byref(b)))
+    _check(_lib.ninfer_kv_attention_workspace(cache._current(cache._device), requests, q_heads, C.byref(b)))
     return b.value
 
 
@@ -495,12 +513,13 @@ def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, win
     over the cache's pages in block_table (requests, table_pages); lengths count
     the new token. scale: head_dim ** -0.5 unless given; window 0: every key.
     lse: a float32 (requests, q_heads) tensor to be written, or None."""
-    ref = cache._current()
-    code, strides = _rows(q, "q", 3, (F32, BF16, F16))
+    device = _on(q, "q")
+    ref = cache._current(device)
+    code, strides = _rows(q, "q", 3, (F32, BF16, F16), device)
     requests, heads, dim = q.shape
     if dim != cache.head_dim:
         raise ValueError(f"q has head_dim {dim}, the cache {cache.head_dim}")
-    table, n, width, stride = _table(block_table, "block_table")
+    table, n, width, stride = _table(block_table, "block_table", device)
     if n != requests:
         raise ValueError(f"block_table has {n} rows for {requests} requests")
     if out is None:
@@ -508,14 +527,14 @@ def ninfer_kv_attention(q, cache: KvCache, block_table, lengths, scale=None, win
     if workspace is None:
         need = ninfer_kv_attention_workspace(cache, requests, heads)
         workspace = _torch().empty(need, dtype=_torch().uint8, device=q.device)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor")
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
     dtype = out.dtype
     _check(_lib.ninfer_kv_attention(
         q.data_ptr(), code, requests, heads, strides[0], strides[1], ref, table, width, stride,
-        _arg(lengths, "lengths", _I32, requests), dim ** -0.5 if scale is None else scale, window,
-        _arg(out, "out", dtype, requests * heads * dim), _TYPES.get(dtype, -1), _arg(lse, "lse", _F32, requests * heads),
-        workspace.data_ptr(), workspace.nbytes, _raw_stream(q.get_device())))
+        _arg(lengths, "lengths", _I32, requests, device), dim ** -0.5 if scale is None else scale, window,
+        _arg(out, "out", dtype, requests * heads * dim, device), _TYPES.get(dtype, -1), _arg(lse, "lse", _F32, requests * heads, device),
+        workspace.data_ptr(), workspace.nbytes, _raw_stream(device)))
     return out
 
 
@@ -525,11 +544,13 @@ def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, 
     """Penalties, biases and grammar masks on logits (rows, vocab); out may be
     logits itself. history: int32 (rows, longest); mask: int32 words (mask rows,
     ceil(vocab / 32)), bit set where a token is allowed."""
-    code, strides = _rows(logits, "logits", 2, (F32, BF16, F16))
+    _TYPES or _types()
+    device = _on(logits, "logits")
+    code, strides = _rows(logits, "logits", 2, (F32, BF16, F16), device)
     rows, vocab = logits.shape
     if out is None:
         out = _torch().empty((rows, vocab), dtype=logits.dtype, device=logits.device)
-    code_out, out_strides = _rows(out, "out", 2, (code,))
+    code_out, out_strides = _rows(out, "out", 2, (code,), device)
     if out is not logits and out.shape != (rows, vocab):
         raise ValueError("out must have the shape and dtype of logits")
     h = n = p = longest = offsets = ids = values = count = m = m_rows = m_count = m_stride = 0
@@ -537,22 +558,22 @@ def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, 
         if history.dim() != 2:
             raise ValueError("history must be (rows, longest)")
         longest = history.shape[1]
-        h = _arg(history, "history", _I32, rows * longest)
-        n = _arg(history_lengths, "history_lengths", _I32, rows)
-        p = _arg(prompt_lengths, "prompt_lengths", _I32, rows)
+        h = _arg(history, "history", _I32, rows * longest, device)
+        n = _arg(history_lengths, "history_lengths", _I32, rows, device)
+        p = _arg(prompt_lengths, "prompt_lengths", _I32, rows, device)
     if bias_ids is not None and (count := bias_ids.numel()):
-        offsets = _arg(bias_offsets, "bias_offsets", _I32, rows + 1)
-        ids = _arg(bias_ids, "bias_ids", _I32, count)
-        values = _arg(bias_values, "bias_values", _F32, count)
+        offsets = _arg(bias_offsets, "bias_offsets", _I32, rows + 1, device)
+        ids = _arg(bias_ids, "bias_ids", _I32, count, device)
+        values = _arg(bias_values, "bias_values", _F32, count, device)
     if mask is not None:
-        m, m_count, width, m_stride = _table(mask, "mask")
+        m, m_count, width, m_stride = _table(mask, "mask", device)
         if width * 32 < vocab:
             raise ValueError(f"mask has {width} words a row for {vocab} tokens")
-        m_rows = _arg(mask_rows, "mask_rows", _I32, rows)
+        m_rows = _arg(mask_rows, "mask_rows", _I32, rows, device)
     controls = _CONTROLS.pack(
-        h, n, p, longest, _arg(repetition, "repetition", _F32, rows), _arg(presence, "presence", _F32, rows),
-        _arg(frequency, "frequency", _F32, rows), offsets, ids, values, count, m, m_rows, m_count, m_stride)
+        h, n, p, longest, _arg(repetition, "repetition", _F32, rows, device), _arg(presence, "presence", _F32, rows, device),
+        _arg(frequency, "frequency", _F32, rows, device), offsets, ids, values, count, m, m_rows, m_count, m_stride)
     _check(_lib.ninfer_logits_process(
         logits.data_ptr(), strides[0] if rows > 1 else vocab, out.data_ptr(), out_strides[0] if rows > 1 else vocab, code,
-        rows, vocab, controls, _arg(status, "status", _I32, 1), _raw_stream(logits.get_device())))
+        rows, vocab, controls, _arg(status, "status", _I32, 1, device), _raw_stream(device)))
     return out

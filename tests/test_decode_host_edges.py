@@ -100,30 +100,30 @@ def buffers(device=0, requests=3, capacity=5):
 def test_kv_tables_looks_at_its_buffers_again():
     nt._types()
     t = buffers()
-    _, table, tokens, requests, *_ = t._addresses(5)
+    _, table, tokens, requests, *_ = t._addresses(5, 0)
     assert table == (FAKE, 3, 4, 4) and tokens == (2 * FAKE, 3 * FAKE, 4 * FAKE) and requests == (5 * FAKE, 6 * FAKE, 7 * FAKE)
     t.positions.at = 30 * FAKE                              # memory replaced in place, as by resize_ or set_
     t.lengths.at = 60 * FAKE
-    _, _, tokens, requests, *_ = t._addresses(5)
+    _, _, tokens, requests, *_ = t._addresses(5, 0)
     assert tokens == (2 * FAKE, 30 * FAKE, 4 * FAKE) and requests == (5 * FAKE, 60 * FAKE, 7 * FAKE)
     t.block_table.shape = (3, 9)                            # longer rows at the same place
-    assert t._addresses(5)[1] == (FAKE, 3, 9, 9)
+    assert t._addresses(5, 0)[1] == (FAKE, 3, 9, 9)
     t.block_table.at = 10 * FAKE
-    assert t._addresses(5)[1] == (10 * FAKE, 3, 9, 9)
+    assert t._addresses(5, 0)[1] == (10 * FAKE, 3, 9, 9)
     t.slots.at, t.slots.shape = 20 * FAKE, (4,)
     for _ in range(2):
         with pytest.raises(ValueError):
-            t._addresses(5)
+            t._addresses(5, 0)
 
 
 def test_kv_tables_copies_have_buffers_of_their_own():
     nt._types()
     t = buffers()
-    t._addresses(5)
+    t._addresses(5, 0)
     other = copy.deepcopy(t)
     for x in other:
         x.at += FAKE // 2
-    assert other._addresses(5)[2] == tuple(a + FAKE // 2 for a in t._addresses(5)[2])
+    assert other._addresses(5, 0)[2] == tuple(a + FAKE // 2 for a in t._addresses(5, 0)[2])
 
 
 def test_kv_cache_looks_at_its_pools_again():
@@ -133,8 +133,47 @@ def test_kv_cache_looks_at_its_pools_again():
     k.at, v.at = 3 * FAKE, 4 * FAKE
     for t in (k, v):
         t.shape = (32, 16, 2, 64)
-    s = c._current()._obj
+    s = c._current(0)._obj
     assert (s.k, s.v, s.pages, s.page_stride, s.k_scale, s.v_scale) == (3 * FAKE, 4 * FAKE, 32, 2048, 0.5, 0.25) and c.pages == 32
     k.at, k.shape = 5 * FAKE, (16, 16, 2, 64)               # one pool alone
     with pytest.raises(ValueError):
-        c._current()
+        c._current(0)
+
+
+def test_arguments_on_different_devices_are_refused(monkeypatch):
+    """Before the library is asked: it would read one GPU's memory from another."""
+    torch = pytest.importorskip("torch")
+    nt._types()
+    bf16, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    monkeypatch.setattr(nt, "_several", False)
+
+    def pools(k=0, v=0):
+        return Tensor(FAKE, bf16, 8, 16, 2, 64, device=k), Tensor(2 * FAKE, bf16, 8, 16, 2, 64, device=v)
+    with pytest.raises(ValueError):
+        nt.KvCache(*pools(0, 1))
+    for cache, first, others in ((1, 0, [0] * 4), (0, 0, [1, 0, 0, 0]), (0, 0, [0, 1, 0, 0]), (0, 0, [0, 0, 1, 0]), (0, 0, [0, 0, 0, 1])):
+        c = nt.KvCache(*pools(cache, cache))
+        with pytest.raises(ValueError):
+            nt.ninfer_kv_attention(Tensor(3 * FAKE, bf16, 3, 4, 64, device=first), c, Tensor(4 * FAKE, i32, 3, 2, device=others[0]),
+                                   Tensor(5 * FAKE, i32, 3, device=others[1]), out=Tensor(6 * FAKE, bf16, 3, 4, 64, device=others[2]),
+                                   workspace=Tensor(7 * FAKE, torch.uint8, 1 << 30, device=others[3]))
+        if others[2] == others[3] == 0:
+            with pytest.raises(ValueError):
+                nt.ninfer_kv_append(c, Tensor(3 * FAKE, bf16, 3, 2, 64, device=first), Tensor(4 * FAKE, bf16, 3, 2, 64, device=others[0]),
+                                    Tensor(5 * FAKE, i64, 3, device=others[1]))
+    lengths, free = Tensor(12 * FAKE, i32, 3), Tensor(13 * FAKE, i32, 7)
+    for out, fr, table in ((buffers(1), free, None), (buffers(), Tensor(FAKE, i32, 7, device=1), None),
+                           (buffers(), free, Tensor(FAKE, i32, 3, 4, device=1))):
+        with pytest.raises(ValueError):
+            nt.ninfer_kv_tables(lengths, None, 16, fr, table or out.block_table, 5, out=out)
+    x = Tensor(FAKE, torch.float32, 2, 100)
+    for kw in (dict(out=Tensor(2 * FAKE, torch.float32, 2, 100, device=1)), dict(repetition=Tensor(2 * FAKE, torch.float32, 2, device=1)),
+               dict(mask=Tensor(2 * FAKE, i32, 2, 4, device=1))):
+        with pytest.raises(ValueError):
+            nt.ninfer_logits_process(x, **dict(dict(out=Tensor(3 * FAKE, torch.float32, 2, 100)), **kw))
+    # where there are several, the current one is the one that the library launches on
+    monkeypatch.setattr(nt, "_several", True)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    with pytest.raises(ValueError):
+        nt.KvCache(*pools())
+    nt.KvCache(*pools(1, 1))
