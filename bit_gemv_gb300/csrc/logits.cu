@@ -179,9 +179,13 @@ __global__ void __launch_bounds__(kThreads, kResident) logits_kernel(const __gri
     __syncthreads();
 
     const typename E::Word *entries = reinterpret_cast<const typename E::Word *>(table);
+    // The product with the reciprocal rounds once more than a division (of each seen token: 29.5 against 28.4 us for the
+    // 64 rows); a repetition whose reciprocal is no normal number would lose bits or the value, and divides.
     const float less = 1.f / rep;
+    const bool divide = !(fabsf(less) >= 0x1p-126f && fabsf(less) < INFINITY);
     auto penalised = [&](float v, uint32_t e) {         // an empty entry leaves v as it is
-        v *= e ? v > 0.f ? less : rep : 1.f;
+        if (divide) v = e ? v > 0.f ? v / rep : v * rep : v;
+        else v *= e ? v > 0.f ? less : rep : 1.f;
         return v - (e & E::kCount ? fmaf(freq, (float)(e & E::kCount), pres) : 0.f);
     };
     auto one = [&](uint32_t i, float v, float bias) {       // token `i` of the slice, whose logit is v

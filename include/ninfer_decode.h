@@ -88,8 +88,9 @@ enum {
  *   (if there is one) is -1; offsets, lengths_out and counts are unaffected. Negative
  *   lengths count as 0; results past 2^31 - 1 are clamped to it.
  * Errors: INVALID_ARGUMENT (NULL lengths or block_table; free_pages NULL with a
- *   count; an output that overlaps an input or block_table), SHAPE (requests, page_size or table_pages 0; any of them, or capacity or
- *   free_count, over 2^31 - 1; table_stride < table_pages), ALIGNMENT, CUDA.
+ *   count; an output that overlaps an input or block_table), SHAPE (requests, page_size
+ *   or table_pages 0; any of them, or capacity or free_count, over 2^31 - 1;
+ *   table_stride < table_pages), ALIGNMENT, CUDA.
  */
 int ninfer_kv_tables(const int32_t *lengths, const int32_t *new_tokens, uint64_t requests,
                      uint64_t page_size, const int32_t *free_pages, uint64_t free_count,
@@ -158,7 +159,8 @@ int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests, uint64_t 
  *   x += bias                                             if v is listed with one,
  *   x = -infinity                                         if row mask_rows[b] of the mask forbids v,
  *   n = history_lengths[b], p = prompt_lengths[b] (the prompt is known, not answered with).
- * Computed in fp32, rounded once to dtype.
+ * Computed in fp32 (the quotient as the product with the reciprocal, where that is a normal number), rounded
+ * once to dtype.
  *   logits, out: device, dtype f32, bf16 or f16, row b at b * stride elements; out may be
  *     logits itself (same stride).
  *   history: device int32, row b at b * history_stride, below 2^30 (tokens outside [0, vocab) are ignored and

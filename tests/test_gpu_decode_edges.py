@@ -234,3 +234,23 @@ def test_logits_bias_offsets_are_cut_at_both_ends():
     want[3, 600] += 2.0
     want[4, 7] += 4.0           # from 2 to past the end: the last one
     assert torch.equal(y, want) and int(status) == 0
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("vocab", [4096, 4099])
+def test_logits_repetitions_without_a_reciprocal(dtype, vocab):
+    """Repetitions whose reciprocal is no normal fp32 number: one rounding of the quotient, then of the type."""
+    rng = np.random.default_rng(vocab)
+    rep = np.array([1e-39, 3e38, 0.0, float("inf"), 1e-45, 2.0 ** 127], np.float32)
+    x = torch.from_numpy(rng.standard_normal((6, vocab)).astype(np.float32)).to(DEV)
+    x[0] *= 1e-38
+    x[4] *= 1e-44
+    x[5] *= 2.0 ** 100
+    x = x.to(TORCH[dtype])
+    h = torch.arange(vocab, dtype=torch.int32, device=DEV).expand(6, vocab).contiguous()
+    y = nt.ninfer_logits_process(x, history=h, history_lengths=i32([vocab] * 6), repetition=torch.from_numpy(rep).to(DEV))
+    x64, r64 = f64(x), rep.astype(np.float64)[:, None]
+    with np.errstate(all="ignore"):
+        want = od.round_to(np.where(x64 > 0, x64 / r64, x64 * r64), "f32")
+        want = want if dtype == "f32" else od.round_to(want, dtype)
+    assert np.array_equal(f64(y), want, equal_nan=True)
