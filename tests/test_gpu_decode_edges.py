@@ -86,6 +86,79 @@ def test_attention_rows_of_minus_infinity_on_every_path(width):
     assert (out == 0).all() and (lse == -float("inf")).all()
 
 
+# Exact results (float32 queries and results). Units of the last place are 2^-24 of a value.
+#   Operands: three bfloat16 terms hold 24 bits, two binary16 terms 22, a weight's exponential 22.
+#   A tensor-core sum is cut off at each of its steps of 16 elements; a score of d elements adds up to d / 64
+#   sums of 4 steps, and a result's steps are added in fp32, rounded.
+@pytest.mark.parametrize("cache", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("heads,dim", [(1, 64), (8, 128), (16, 128), (8, 256), (16, 64), (4, 192)])
+@pytest.mark.parametrize("width", [1, 400])
+def test_attention_scores_hold_every_term_of_a_query(cache, heads, dim, width):
+    """One key: the log-sum-exp is its score, the result its value.
+
+    Query elements are 1 + 2^-9 + 0.9 * 2^-17, so that what a missing term would hold adds up over the elements:
+    0.9 * 2^-17 of the score without a third bfloat16 term, 2^-9 without a second binary16 one. Bound, of sum |q k| scale:
+    operands 2^-22, the steps of a score 2^-24 each and at most 16 of them (2^-20, all cut the same way), the scale's and
+    the logarithm's roundings 4 * 2^-24, and 2^-20 for the shift by the binary16 weights' factor 2^14."""
+    g = torch.Generator(DEV).manual_seed(dim + heads)
+    k, v = (torch.randn(1, 16, 1, dim, generator=g, device=DEV).abs().to(TORCH[cache]) for _ in range(2))
+    q = torch.full((1, heads, dim), 1 + 2.0 ** -9 + 0.9 * 2.0 ** -17, device=DEV)
+    q *= 2.0 ** torch.arange(heads, device=DEV)[None, :, None].clamp(max=3)
+    out, lse, divided = attend(q, k, v, [[0]], [1], width, out_dtype=torch.float32)
+    assert divided == (width > 100 or dim > 128 and width > 1)
+    score = (f64(q) * f64(k)[0, 0]).sum(-1) * dim ** -0.5           # all products are positive
+    assert (np.abs(f64(lse) - score) <= score * (2.0 ** -20 + 2.0 ** -22 + 2.0 ** -22) + 2.0 ** -20).all()
+    assert torch.equal(out[0], v[0, 0].float().expand(heads, dim))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("heads,dim", [(1, 64), (8, 128), (16, 128), (8, 256), (16, 64), (4, 192)])
+@pytest.mark.parametrize("width", [13, 60, 400])
+def test_attention_results_hold_every_term_of_a_weight(cache, heads, dim, width):
+    """Equal values are their own average, whatever the weights; weights are 1 and 1/2 + 2^-10 + 0.45 * 2^-17 of it, so that
+    what a missing term would hold adds up over the keys.
+
+    Bound: the weights' terms 2^-22, the sums of 16 keys 3 * 2^-24, cut (one for each term), their additions and the sum
+    of the weights 2^-24 each, rounded, for at most 13 of a row of 200 keys: 2^-19.2, 2^-19 allowed (a missing third bfloat16
+    term is 0.9 * 2^-17, a second binary16 one 2^-12)."""
+    k = torch.zeros(13, 16, 1, dim, device=DEV)
+    q = torch.zeros(1, heads, dim, device=DEV)
+    k[..., 0] = 1.0
+    k[0, 0, 0, 0] = 0.0
+    q[..., 0] = float(np.log(0.5 + 2.0 ** -10 + 0.45 * 2.0 ** -17) * dim ** 0.5)
+    v = torch.full((13, 16, 1, dim), 1.5, device=DEV)
+    out, lse, _ = attend(q, k.to(TORCH[cache]), v.to(TORCH[cache]), [list(range(13))], [200], width, out_dtype=torch.float32)
+    assert (np.abs(f64(out) - 1.5) <= 1.5 * 2.0 ** -19).all()
+    assert np.abs(f64(lse) - np.log(1 + 199 * (0.5 + 2.0 ** -10 + 0.45 * 2.0 ** -17))).max() < 2.0 ** -18
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f16", "e4m3"])
+@pytest.mark.parametrize("heads,kvh,dim", [(2, 1, 64), (8, 1, 128), (16, 1, 128), (12, 1, 64), (8, 1, 256), (20, 2, 256), (6, 2, 192)])
+@pytest.mark.parametrize("lengths,width", [([190], 13), ([200, 130], 60), ([900], 60), ([2000, 77], 130), ([3000, 1, 20001], 1251)])
+def test_attention_exact_results_on_every_path(cache, heads, kvh, dim, lengths, width):
+    """float32 results against 64 bits, 2-norm of the whole result, keys, values and queries of unit variance.
+
+    Relative error: weights 2^-22 from the operands' terms and 2^-22 from the exponential, scores 2^-21 (the cut sums of
+    scores of about one), each 16 keys' sum 2^-22, and the additions 2^-22: 8e-7 in quadrature, 2^-19 allowed."""
+    rng = np.random.default_rng(heads * dim)
+    pages = sum(-(-n // 16) for n in lengths)
+    k, v = (torch.from_numpy(rng.standard_normal((pages, 16, kvh, dim)).astype(np.float32)).to(DEV).to(TORCH[cache]) for _ in range(2))
+    q = torch.from_numpy(rng.standard_normal((len(lengths), heads, dim)).astype(np.float32)).to(DEV)
+    table, at = np.full((len(lengths), max(-(-n // 16) for n in lengths)), -1), 0
+    for r, n in enumerate(lengths):
+        table[r, :-(-n // 16)] = at + np.arange(-(-n // 16))
+        at += -(-n // 16)
+    out, lse, _ = attend(q, k, v, table, lengths, width, out_dtype=torch.float32)
+    for r, n in enumerate(lengths):
+        used = torch.from_numpy(table[r, :-(-n // 16)]).to(DEV)
+        for h in range(heads):
+            keys, values = ((x.float() if cache == "e4m3" else x)[used][:, :, h // (heads // kvh)].reshape(-1, dim)[:n].double() for x in (k, v))
+            s = keys @ q[r, h].double() * dim ** -0.5
+            want = torch.softmax(s, 0) @ values
+            assert (out[r, h].double() - want).norm() <= 2.0 ** -19 * want.norm(), (r, h)
+            assert (lse[r, h].double() - torch.logsumexp(s, 0)).abs() <= 2.0 ** -18, (r, h)
+
+
 # ----------------------------------------------------------------- tables ---
 @pytest.mark.parametrize("lengths,new,page,table,status", [
     ([40], None, 16, [[1, 2]], nt.KV_ROW_TOO_SHORT),                       # in a page that the row has no entry for, taking none
