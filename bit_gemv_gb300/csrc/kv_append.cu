@@ -5,10 +5,11 @@
 // written once, so HBM bounds it (latency, for the few rows of a decode step).
 // One thread moves one 16-byte unit of the stored row (8 or 16 elements) of K and of V,
 // all of its loads under way at once: 30011 tokens of 4 x 256 from fp32 rows into a bfloat16
-// cache, 369 MB, 53.6 us (6.89 TB/s, the rate of a copy; K and V in threads of their own: 59.9 us).
-// Scales cost what their quotients take to round once: the same tokens from bfloat16 into 8 bits 35.5 us for a power of
-// two, 45.9 for 0.0137 and 56.9 for 0.3 (where each third bfloat16 value gives a quotient near a halfway point); with an fp32
-// division each, which rounds twice, 53 us on that machine.
+// cache, 369 MB, 53.5 us (6.9 TB/s, the rate of a copy; K and V in threads of their own: 59.9 us).
+// Scales cost what it takes to round their quotients once: the same tokens from bfloat16 into 8 bits 40.9 us for a power of
+// two and for 0.0137, 58 for 0.3 (where each third bfloat16 value gives a quotient near a halfway point), from fp32 45.5; from
+// bfloat16 into bfloat16 38.8 without a scale, 51 by 0.5, 72 by 0.3. An fp32 division each, which rounds twice, took 48, 47
+// and 49 us.
 #include "decode.cuh"
 
 namespace ninfer {
@@ -77,39 +78,57 @@ __device__ __forceinline__ void pack8(const float (&x)[8], uint32_t *out) {
 template <int kDtype>
 constexpr uint32_t kBelow = (1u << (kDtype == NINFER_BF16 ? 15 : kDtype == NINFER_F16 ? 12 : 19)) - 1;
 
-// `near`, a value with zeros for those bits, or its neighbour on the side where x / scale lies: rounding it to the cache's
-// type is rounding x / scale once. `other` where there is no remainder (infinite x, NaN).
-__device__ __forceinline__ float beside(float near, float other, float x, float scale) {
-    // the remainder's lowest bit is at least 2^-36 of x, so that it is exact (and not lost under 2^-149) from 2^-113 on
-    const float up = fabsf(x) < 0x1p-100f ? 0x1p64f : 1.f;
-    const float r = fmaf(-near, scale * up, x * up);
-    if (!(r > 0.f) && !(r < 0.f)) return r == 0.f ? near : other;
-    const uint32_t bits = __float_as_uint(near);
-    return __uint_as_float((r > 0.f) == (bits >> 31 == 0) ? bits + 1 : bits - 1);
+// `near`, a value with zeros for those bits, or its neighbour on the side that the remainder r = x - near * scale tells:
+// rounding it to the cache's type is rounding x / scale once. `other` where there is no remainder (infinite x, NaN).
+__device__ __forceinline__ float beside(float near, float other, float r) {
+    const int32_t bits = __float_as_int(near), step = (__float_as_int(r) ^ bits) >> 31 | 1;
+    return r != r ? other : __int_as_float(r == 0.f ? bits : bits + step);
 }
 
-// x / scale from the fp32 quotient; seldom called, and kept out of the way.
+// x / scale from the fp32 quotient; for values that few caches see.
 template <int kDtype>
 __device__ __noinline__ float quotient(float x, float scale) {
     const float q = __fdiv_rn(x, scale);
-    return __float_as_uint(q) & kBelow<kDtype> ? q : beside(q, q, x, scale);
+    if (__float_as_uint(q) & kBelow<kDtype>) return q;
+    // the remainder's lowest bit is at least 2^-36 of x, so that it is exact (and not lost under 2^-149) from 2^-113 on
+    const float up = fabsf(x) < 0x1p-100f ? 0x1p64f : 1.f;
+    return beside(q, q, fmaf(-q, scale * up, x * up));
 }
 
-// x / scale for one rounding to the cache's type, which the caller does. The product with 1 / scale is x / scale
-// where scale is a power of two (kExact), and otherwise at most two units in its last place off, so that it
-// rounds as x / scale does unless it lies within three of a halfway point. Under 2^-100, where a product may have lost
-// bits, only bfloat16 has values at all.
-template <int kDtype, bool kExact>
-__device__ __forceinline__ float divided(float x, float scale, float inverse) {
-    const float q = x * inverse;
-    if (kDtype == NINFER_BF16 && fabsf(q) < 0x1p-100f && q != 0.f) return quotient<kDtype>(x, scale);
-    const uint32_t bits = __float_as_uint(q) + 3;
-    if (kExact || (bits & kBelow<kDtype>) > 6) return q;
-    return beside(__uint_as_float(bits & ~kBelow<kDtype>), q, x, scale);
-}
-
+// x / scale for one rounding to the cache's type, which pack8 does. The product with 1 / scale is x / scale where scale is
+// a power of two, and otherwise at most two units in its last place off, so that it rounds as x / scale does unless it
+// lies within three of a halfway point. Under 2^-100 a remainder, and a product that bfloat16 holds, may lose bits.
 template <int kDtype>
-__global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ AppendParams p) {
+__device__ __forceinline__ void divide8(float (&x)[8], float scale, float inverse, bool exact) {
+    float q[8];
+    bool near = false, small = inverse == 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q[i] = x[i] * inverse;
+        near |= ((__float_as_uint(q[i]) + 3) & kBelow<kDtype>) <= 6;
+        small |= (kDtype == NINFER_BF16 ? fminf(fabsf(x[i]), fabsf(q[i])) : fabsf(x[i])) < 0x1p-100f && x[i] != 0.f;
+    }
+    if (small) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = quotient<kDtype>(x[i], scale);
+        return;
+    }
+    if (near && !exact) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t bits = __float_as_uint(q[i]) + 3;
+            const float mid = __uint_as_float(bits & ~kBelow<kDtype>);
+            if ((bits & kBelow<kDtype>) <= 6) q[i] = beside(mid, q[i], fmaf(-mid, scale, x[i]));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = q[i];
+}
+
+// kScaled: a scale that is not 1. Caches without one go without the registers for it (32 against 40 or more: bfloat16
+// into bfloat16 38.8 us, 43.8 in one instance for both).
+template <int kDtype, bool kScaled>
+__global__ void __launch_bounds__(256, kDtype == NINFER_E4M3 ? (kScaled ? 4 : 5) : kScaled ? 6 : 8) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr uint32_t kEs = kDtype == NINFER_E4M3 ? 1 : 2, kUnit = 16 / kEs;
     pdl_launch_dependents();
     pdl_wait();
@@ -141,23 +160,20 @@ __global__ void __launch_bounds__(256) append_kernel(const __grid_constant__ App
     const uint64_t to = (page * p.page_stride + in * p.token_stride + head * p.head_stride + unit * kUnit) * kEs;
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        const float scale = p.scale[w], inverse = p.inverse[w];
-        if (p.exact[w]) {
-            if (scale != 1.f)
-#pragma unroll
-                for (uint32_t j = 0; j < kUnit; ++j) x[w][j] = divided<kDtype, true>(x[w][j], scale, inverse);
-        } else if (inverse != 0.f) {
-#pragma unroll
-            for (uint32_t j = 0; j < kUnit; ++j) x[w][j] = divided<kDtype, false>(x[w][j], scale, inverse);
-        } else {
-#pragma unroll
-            for (uint32_t j = 0; j < kUnit; ++j) x[w][j] = quotient<kDtype>(x[w][j], scale);
-        }
         uint32_t o[4];
 #pragma unroll
-        for (uint32_t j = 0; j < kUnit; j += 8) pack8<kDtype>(*reinterpret_cast<float(*)[8]>(x[w] + j), o + j / 4);
+        for (uint32_t j = 0; j < kUnit; j += 8) {
+            float(&eight)[8] = *reinterpret_cast<float(*)[8]>(x[w] + j);
+            if (kScaled) divide8<kDtype>(eight, p.scale[w], p.inverse[w], p.exact[w]);
+            pack8<kDtype>(eight, o + j / 4);
+        }
         *reinterpret_cast<uint4 *>(p.dst[w] + to) = make_uint4(o[0], o[1], o[2], o[3]);
     }
+}
+
+template <int kDtype>
+auto kernel_of(bool scaled) {
+    return scaled ? append_kernel<kDtype, true> : append_kernel<kDtype, false>;
 }
 
 }  // namespace
@@ -204,9 +220,10 @@ extern "C" int ninfer_kv_append(const void *k_new, const void *v_new, int src_dt
     p.page = FastDiv((uint32_t)cache->page_size);
     p.src_dtype = src_dtype;
     p.status = status;
-    const auto kernel = cache->dtype == NINFER_BF16  ? append_kernel<NINFER_BF16>
-                        : cache->dtype == NINFER_F16 ? append_kernel<NINFER_F16>
-                                                     : append_kernel<NINFER_E4M3>;
+    const bool scaled = cache->k_scale != 1.f || cache->v_scale != 1.f;
+    const auto kernel = cache->dtype == NINFER_BF16  ? kernel_of<NINFER_BF16>(scaled)
+                        : cache->dtype == NINFER_F16 ? kernel_of<NINFER_F16>(scaled)
+                                                     : kernel_of<NINFER_E4M3>(scaled);
     // fewer than 2^31 units a launch: the kernel counts them in 32 bits
     const uint64_t step = ((1ull << 31) - 1) / per_token;
     for (uint64_t t = 0; t < tokens; t += step) {
