@@ -6,10 +6,10 @@
 // One thread moves one 16-byte unit of the stored row (8 or 16 elements) of K and of V,
 // all of its loads under way at once: 30011 tokens of 4 x 256 from fp32 rows into a bfloat16
 // cache, 369 MB, 53.5 us (6.9 TB/s, the rate of a copy; K and V in threads of their own: 59.9 us).
-// Scales cost what it takes to round their quotients once: the same tokens from bfloat16 into 8 bits 40.9 us for a power of
-// two and for 0.0137, 58 for 0.3 (where each third bfloat16 value gives a quotient near a halfway point), from fp32 45.5; from
-// bfloat16 into bfloat16 38.8 without a scale, 51 by 0.5, 72 by 0.3. An fp32 division each, which rounds twice, took 48, 47
-// and 49 us.
+// Scales cost what it takes to round their quotients once: the same tokens from bfloat16 into 8 bits 41.5 us for a power of
+// two and for 0.0137, 58 for 0.3 (where each third bfloat16 value gives a quotient near a halfway point), 31.5 without a
+// scale; from fp32 45.4 and 44.8; from bfloat16 into bfloat16 51 by 0.5, 72 by 0.3, 39.1 without. With an fp32 division
+// each, which rounds twice, those with a scale took 49, 47 and 49.5 us.
 #include "decode.cuh"
 
 namespace ninfer {
@@ -126,7 +126,8 @@ __device__ __forceinline__ void divide8(float (&x)[8], float scale, float invers
 }
 
 // kScaled: a scale that is not 1. Caches without one go without the registers for it (32 against 40 or more: bfloat16
-// into bfloat16 38.8 us, 43.8 in one instance for both).
+// into bfloat16 39.1 us, 43.8 in one instance for both). The least CTAs an SM are what each instance's registers allow
+// with few spills or none (16-bit with a scale: 5, 6 and 8 CTAs 53.4, 50.7 and 60.0 us by 0.5).
 template <int kDtype, bool kScaled>
 __global__ void __launch_bounds__(256, kDtype == NINFER_E4M3 ? (kScaled ? 4 : 5) : kScaled ? 6 : 8) append_kernel(const __grid_constant__ AppendParams p) {
     constexpr uint32_t kEs = kDtype == NINFER_E4M3 ? 1 : 2, kUnit = 16 / kEs;

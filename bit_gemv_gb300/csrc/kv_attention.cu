@@ -133,7 +133,8 @@ extern "C" int ninfer_kv_attention(const void *q, int q_dtype, uint64_t requests
     p.q_dtype = q_dtype;
     p.out_dtype = out_dtype;
     // Few and short rows: a CTA, or a cluster of two, four or eight, for each, without a schedule and
-    // a second kernel. On the GPU that costs 5 us (clusters: 7) and 1.8 us for every 8 units of a
+    // a second kernel. The lengths are on the device, so that the table's width (or the window) stands for the longest row:
+    // short rows under a table that is wider than these sizes are divided like long ones. On the GPU that costs 5 us (clusters: 7) and 1.8 us for every 8 units of a
     // CTA's part of the longest row; the division of the line costs 9 us (256 elements: 11) and
     // 1.8 us for every unit a warp. Measured, rows of 128 elements in 16 bits, clusters against the line:
     //   4 rows of 64 units 9.1 / 9.7 us, of 80 10.2 / 9.9;  16 of 32 8.0 / 9.5, of 80 10.9 / 10.2;  32 of 64

@@ -40,10 +40,10 @@
 // 80 elements in pages of 24. Keys outside a request are filled with zeros in shared
 // memory, so that nothing a page holds behind them reaches a product.
 //
-// Measured (a plain copy runs at 6791 GB/s): 128 requests of 1000 to 16000 keys, 2.85 GB, 438 us (6.51 TB/s);
-// one of 131071, 537 MB, 87.8 us (6.11 TB/s); 16 of 20000 to 60000 on an 8-bit cache, 1.2 GB,
-// 188 us (6.39 TB/s); 32 of 200 to 4500, 184 MB, 39.3 us, of which about 12 are the beginning and
-// the joins.
+// Measured, from the fastest machine to the slowest (a plain copy runs at 6685 to 6791 GB/s): 128 requests of
+// 1000 to 16000 keys, 2.85 GB, 438 to 449 us (6.51 to 6.36 TB/s); one of 131071, 537 MB, 87.8 to 89.8 us (6.11 to
+// 5.98 TB/s); 16 of 20000 to 60000 on an 8-bit cache, 1.2 GB, 188 to 212 us (6.39 to 5.66 TB/s); 32 of 200 to 4500, 184 MB,
+// 39.5 to 40.5 us, of which about 12 are the beginning and the joins.
 #pragma once
 
 #include <cmath>

@@ -1,4 +1,7 @@
-// Attention over binary16 caches. HBM bounds them whatever is computed of a row's padding.
+// Attention over binary16 caches. HBM bounds long rows whatever is computed of their padding (128 requests of 1000 to
+// 16000 keys: 0.93 to 0.96 of a copy's rate). Many short rows it does not (24 requests of 1 to 3001 keys, 16 key heads
+// of 80 elements in binary16, 47 MB: 21 us, a third of that rate): there the beginning of each row, the joins and the second
+// kernel weigh most, and what the 48 elements of padding cost has not been measured apart.
 #include "kv_attention.cuh"
 
 namespace ninfer {

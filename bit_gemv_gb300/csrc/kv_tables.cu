@@ -8,7 +8,7 @@
 // threads' sums, and a token then finds its run by binary search among them in
 // shared memory and its request by walking the run. Four neighbouring tokens share one
 // search and go out in 16-byte stores (7.2 us one by one, 6.0 us so, which is what the
-// host takes to launch it, for 512 requests with 465,000 new tokens, 7.75 MB).
+// host took to launch it, for 512 requests with 465,000 new tokens, 7.75 MB).
 #include "decode.cuh"
 
 namespace ninfer {

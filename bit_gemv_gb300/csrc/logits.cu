@@ -15,7 +15,7 @@
 // rows are 7 slices of about 35,500 tokens each. Twice as many measured 2 us less for
 // 64 rows and 2 to 4 us more for 11 to 47.
 //
-// Measured: 64 rows of 248320 fp32 logits with histories of 16 to 8000 tokens, 28.1 us for
+// Measured: 64 rows of 248320 fp32 logits with histories of 16 to 8000 tokens, 28.1 to 28.7 us for
 // 128 MB (18.8 us at the rate of a copy): 3.7 us until the table stands, 18 us of streaming, and the
 // launch. Copying the untouched tokens at once, and doing the touched ones after the
 // table, took 52 us (a dependent read for each of them). One row takes 2.3 us on the GPU.
