@@ -578,12 +578,13 @@ __global__ void __launch_bounds__(kThreads, 1) attention_kernel(const __grid_con
                     }
                 float sc = p.scale, down = 1.f;
                 if (!S::kBf16) {
-                    // binary16 operands: a power of two brings the head's largest element to about 1
+                    // binary16 operands: a power of two brings the head's largest element to between 2^14 and 2^15, so that
+                    // elements 2^-28 of it still have all of their bits (keys of zero may meet the largest one)
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-                    const int e = top > 0.f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 27), 253) : 127;
-                    down = __uint_as_float((uint32_t)(254 - e) << 23);
-                    sc *= __uint_as_float((uint32_t)e << 23);
+                    const int e = top > 0.f && top < INFINITY ? min(max((int)(__float_as_uint(top) >> 23), 27), 254) : 127 + 14;
+                    down = __uint_as_float((uint32_t)(254 + 14 - e) << 23);
+                    sc *= __uint_as_float((uint32_t)(e - 14) << 23);
                 }
                 sc0[ht] = __shfl_sync(~0u, sc, 8 * t);
                 sc1[ht] = __shfl_sync(~0u, sc, 8 * t + 4);

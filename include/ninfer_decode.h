@@ -137,8 +137,8 @@ int ninfer_kv_append(const void *k_new, const void *v_new, int src_dtype, uint64
  *     its contents are not preserved.
  * Arithmetic: products of 16-bit operands with fp32 sums on the tensor cores. fp32 queries,
  * and the weights e^{s - m} of fp32 results, enter as sums of 16-bit terms that hold 22 bits
- * (NINFER_F16 and NINFER_E4M3 caches) or 24; other weights have 16 bits (NINFER_BF16) or 11
- * and more. Running maxima and sums are fp32.
+ * (NINFER_F16 and NINFER_E4M3 caches; of a query's elements no bit under 2^-39 of its head's
+ * largest one) or 24; other weights have 16 bits (NINFER_BF16) or 11 and more. Running maxima and sums are fp32.
  * How the work is divided follows from the lengths of the call's requests and, for few rows, from
  * table_pages * page_size and the window, which bound them: where these stay the same, results repeat
  * bit for bit. Few and short rows are fastest under a table no wider than they need (a view of a wider

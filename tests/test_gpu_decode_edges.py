@@ -86,6 +86,26 @@ def test_attention_rows_of_minus_infinity_on_every_path(width):
     assert (out == 0).all() and (lse == -float("inf")).all()
 
 
+@pytest.mark.parametrize("cache", ["f16", "e4m3", "bf16"])
+@pytest.mark.parametrize("q_dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("f32", "bf16")])
+@pytest.mark.parametrize("factor", [1.0, 1e30, 1e-30])
+def test_attention_query_elements_far_below_the_largest(cache, q_dtype, out, factor):
+    """A query's largest element meets keys of zero, so that elements 2^-20 of it decide.
+
+    A score may be 2^-15 of sum |q k| scale off, a weight by twice that and by its own rounding (2^-12 at most), and the
+    result's format adds half a step."""
+    rng = np.random.default_rng(11)
+    q = torch.from_numpy(rng.standard_normal((1, 4, 64)).astype(np.float32)).to(DEV) * 2
+    q[:, :, 7] = torch.tensor([2.0 ** 20, -1.9 * 2.0 ** 20, 2.0 ** 20, 1.0], device=DEV)
+    q = (q * factor).to(TORCH[q_dtype])
+    k, v = (torch.from_numpy(rng.standard_normal((4, 16, 1, 64)).astype(np.float32)).to(DEV).to(TORCH[cache]) for _ in range(2))
+    (k.view(torch.uint8) if cache == "e4m3" else k)[..., 7] = 0
+    y = nt.ninfer_kv_attention(q, nt.KvCache(k, v), i32([[0, 1, 2, 3]]), i32([61]), scale=0.125 / factor, out_dtype=TORCH[out])
+    want, _, mag, big = od.kv_attention(f64(q), f64(k), f64(v), np.arange(4)[None], [61], np.float32(0.125 / factor).astype(np.float64))
+    bound = (2 * big[..., None] * 2.0 ** -15 + 2.0 ** -12) * mag + (2.0 ** -8 if out == "bf16" else 2.0 ** -24) * np.abs(want)
+    assert (np.abs(f64(y) - want) <= bound).all()
+
+
 # Exact results (float32 queries and results). Units of the last place are 2^-24 of a value.
 #   Operands: three bfloat16 terms hold 24 bits, two binary16 terms 22, a weight's exponential 22.
 #   A tensor-core sum is cut off at each of its steps of 16 elements; a score of d elements adds up to d / 64
