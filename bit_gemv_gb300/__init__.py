@@ -3,8 +3,8 @@ projection). Argument marshalling only: every step of the computation runs in
 the library's CUDA kernels or its host C++ code. There is no fallback: if the
 shared library is missing, importing this package raises ImportError.
 
-Names match the C entry points of include/ninfer_ternary.h and
-include/ninfer_decode.h. Host entry points take and return numpy arrays; device entry points take torch CUDA tensors and
+Names match the C entry points of include/ninfer_ternary.h,
+include/ninfer_decode.h and include/ninfer_layer.h. Host entry points take and return numpy arrays; device entry points take torch CUDA tensors and
 run on the current torch CUDA stream.
 """
 from __future__ import annotations
@@ -30,6 +30,8 @@ FORMATS = {"PQ2_0_G128": PQ2_0_G128, "PTQ1_0_G128": PTQ1_0_G128}
 F32, BF16, F16, E4M3 = 0, 1, 2, 3
 # bits of the status words of the decode-step operators
 KV_OUT_OF_PAGES, KV_ROW_TOO_SHORT, KV_OUT_OF_SLOTS, KV_BAD_LENGTH, KV_BAD_SLOT, LOGITS_BAD_TOKEN = 1, 2, 4, 8, 16, 32
+DELTA_BAD_SLOT = 64
+ROTARY_SCALINGS = {"none": 0, "linear": 1, "dimensions": 2, "turns": 3}
 
 GEOMETRY_FIELDS = ("n", "k", "k_pad", "groups_per_row", "base_bytes_per_group",
                    "high_bytes_per_group", "base_row_bytes", "high_row_bytes",
@@ -96,6 +98,13 @@ _sig = {
     "ninfer_kv_attention": (_int, [_vp, _int, _u64, _u64, _u64, _u64, C.POINTER(_KvCacheStruct), _vp, _u64, _u64, _vp,
                                    C.c_float, _u64, _vp, _int, _vp, _vp, _u64, _vp]),
     "ninfer_logits_process": (_int, [_vp, _u64, _vp, _u64, _int, _u64, _u64, _vp, _vp, _vp]),
+    "ninfer_norm": (_int, [_vp, _vp]),
+    "ninfer_rotary_frequencies": (_int, [_u64, C.c_double, _int, C.c_double, C.c_double, C.c_double, C.c_double, _vp,
+                                         C.POINTER(C.c_float)]),
+    "ninfer_rotary": (_int, [_vp, _vp]),
+    "ninfer_gated_delta_workspace": (_int, [_u64, _u64, _u64, _u64, _u64, _u64, C.POINTER(_u64)]),
+    "ninfer_gated_delta": (_int, [_vp, _vp, _u64, _vp]),
+    "ninfer_sample": (_int, [_vp, _vp]),
 }
 NOALLOC_SCRATCH_BYTES = 4 * 1024 * 1024
 for _name, (_res, _args) in _sig.items():
@@ -576,4 +585,194 @@ def ninfer_logits_process(logits, out=None, history=None, history_lengths=None, 
     _check(_lib.ninfer_logits_process(
         logits.data_ptr(), strides[0] if rows > 1 else vocab, out.data_ptr(), out_strides[0] if rows > 1 else vocab, code,
         rows, vocab, controls, _arg(status, "status", _I32, 1, device), _raw_stream(device)))
+    return out
+
+
+# ------------------------------------------------------------- layer's step ---
+# The C argument structures of ninfer_layer.h as packed bytes.
+_NORM = struct.Struct("=14Q2f6i")
+_ROTARY = struct.Struct("=21Q3f3i")
+_DELTA = struct.Struct("=27Q2f2i")
+_SAMPLE = struct.Struct("=11Q2i")
+_ANY = (F32, BF16, F16)
+
+
+def _vector(t, name, count, device):
+    """Address and library dtype of a contiguous tensor of `count` elements; (0, 0) for None."""
+    if t is None:
+        return 0, 0
+    code = _TYPES.get(t.dtype, -1)
+    if t.get_device() != device or code not in _ANY or not t.is_contiguous() or t.numel() != count:
+        raise ValueError(f"{name} must be a contiguous tensor of {count} elements of a supported dtype on cuda:{device}, "
+                         f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr(), code
+
+
+def _matrix(t, name, shape, device):
+    """Address, library dtype and row stride of a tensor of rows; zeros for None."""
+    if t is None:
+        return 0, 0, 0
+    code, strides = _rows(t, name, 2, _ANY, device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    return t.data_ptr(), code, strides[0] if shape[0] > 1 else shape[1]
+
+
+def ninfer_norm(x, weight=None, eps: float = 1e-6, residual=None, sum=None, gate=None, group=None, weight_offset: float = 0.0,
+                out=None, out_dtype=None):
+    """Root-mean-square norm of x (rows, cols), of x + residual where one is given (its sum goes to `sum`, which may be the
+    residual itself), over groups of `group` neighbouring columns (all of them unless given), times weight + weight_offset
+    (weight: `group` elements), times gate / (1 + e^-gate). All but weight are (rows, cols) with contiguous rows."""
+    _TYPES or _types()
+    device = _on(x, "x")
+    shape = x.shape
+    x_at, x_code, x_stride = _matrix(x, "x", shape, device)
+    rows, cols = shape
+    if out is None:
+        out = _torch().empty(shape, dtype=out_dtype or x.dtype, device=x.device)
+    r_at, r_code, r_stride = _matrix(residual, "residual", shape, device)
+    s_at, s_code, s_stride = _matrix(sum, "sum", shape, device)
+    if s_at and s_code != r_code:
+        raise ValueError("sum must have the residual's dtype")
+    g_at, g_code, g_stride = _matrix(gate, "gate", shape, device)
+    o_at, o_code, o_stride = _matrix(out, "out", shape, device)
+    group = cols if group is None else group
+    w_at, w_code = _vector(weight, "weight", group, device)
+    _check(_lib.ninfer_norm(_NORM.pack(x_at, r_at, g_at, w_at, s_at, o_at, rows, cols, group, x_stride, r_stride, g_stride,
+                                       s_stride, o_stride, eps, weight_offset, x_code, r_code, g_code, w_code, o_code, 0),
+                            _raw_stream(device)))
+    return out
+
+
+def ninfer_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling="none", factor: float = 1.0, context: float = 0.0,
+                              slow: float = 1.0, fast: float = 32.0):
+    """The table that ninfer_rotary reads (numpy int64, rotary_dim / 2 turns a position times 2^64, as bits; copy it to the
+    GPU) and the magnitude. scaling: "none", "linear", "dimensions" or "turns" (see ninfer_layer.h)."""
+    if scaling not in ROTARY_SCALINGS:
+        raise ValueError(f"scaling must be one of {', '.join(ROTARY_SCALINGS)}, not {scaling!r}")
+    out, magnitude = np.empty(max(rotary_dim // 2, 0), np.uint64), C.c_float()
+    _check(_lib.ninfer_rotary_frequencies(rotary_dim, base, ROTARY_SCALINGS[scaling], factor, context, slow, fast, _np_ptr(out),
+                                          C.byref(magnitude)))
+    return out.view(np.int64), magnitude.value
+
+
+def _heads(t, name, tokens, codes, device):
+    """Address, library dtype, strides and shape of a (tokens, heads, elements) tensor."""
+    code, strides = _rows(t, name, 3, codes, device)
+    if t.shape[0] != tokens:
+        raise ValueError(f"{name} must have {tokens} tokens, not {t.shape[0]}")
+    return t.data_ptr(), code, strides[0], strides[1], t.shape
+
+
+def ninfer_rotary(q, k, positions, frequencies, magnitude: float = 1.0, interleaved: bool = False, q_weight=None, k_weight=None,
+                  eps: float = 1e-6, weight_offset: float = 0.0, q_out=None, k_out=None):
+    """Rotary positions of queries q (tokens, q_heads, head_dim) and keys k (tokens, kv_heads, head_dim; None: queries
+    alone), in place unless q_out and k_out are given; the first 2 * len(frequencies) elements of a head turn. With
+    weights (head_dim elements, one dtype) each head is normed first. Tokens of a negative position are left out."""
+    _TYPES or _types()
+    device = _on(q, "q")
+    tokens = q.shape[0]
+    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, _ANY, device)
+    q_heads, dim = shape[1], shape[2]
+    o_at, o_token, o_head = q_at, q_token, q_head
+    if q_out is not None:
+        o_at, _, o_token, o_head, o_shape = _heads(q_out, "q_out", tokens, (code,), device)
+        if o_shape != shape:
+            raise ValueError("q_out must have the shape and dtype of q")
+    k_at = k_token = k_head = kv_heads = p_at = p_token = p_head = 0
+    if k is not None:
+        k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, (code,), device)
+        kv_heads = k_shape[1]
+        if k_shape[2] != dim:
+            raise ValueError("q and k must have one dtype and head_dim")
+        p_at, p_token, p_head = k_at, k_token, k_head
+        if k_out is not None:
+            p_at, _, p_token, p_head, p_shape = _heads(k_out, "k_out", tokens, (code,), device)
+            if p_shape != k_shape:
+                raise ValueError("k_out must have the shape and dtype of k")
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out and k_weight need k")
+    turns = frequencies.numel()
+    w_at, w_code = _vector(q_weight, "q_weight", dim, device)
+    x_at, x_code = _vector(k_weight, "k_weight", dim, device)
+    if w_at and x_at and w_code != x_code:
+        raise ValueError("q_weight and k_weight must have one dtype")
+    _check(_lib.ninfer_rotary(_ROTARY.pack(
+        q_at, k_at, w_at, x_at, o_at, p_at, _arg(positions, "positions", _I32, tokens, device),
+        _arg(frequencies, "frequencies", _I64, turns, device), tokens, q_heads, kv_heads, dim, 2 * turns, q_token, q_head, k_token,
+        k_head, o_token, o_head, p_token, p_head, magnitude, eps, weight_offset, code, w_code or x_code, int(interleaved)),
+        _raw_stream(device)))
+    return (q if q_out is None else q_out), (k if k_out is None else k_out)
+
+
+def ninfer_gated_delta_workspace(tokens: int, requests: int, k_heads: int, v_heads: int, k_dim: int, v_dim: int) -> int:
+    b = C.c_uint64()
+    _check(_lib.ninfer_gated_delta_workspace(tokens, requests, k_heads, v_heads, k_dim, v_dim, C.byref(b)))
+    return b.value
+
+
+def ninfer_gated_delta(q, k, v, log_decay, beta, state, offsets=None, slots=None, lengths=None, scale=None, norm_eps=None, out=None,
+                       out_dtype=None, workspace=None, status=None):
+    """The gated delta rule: q, k (tokens, k_heads, k_dim), v (tokens, v_heads, v_dim), log_decay and beta float32
+    (tokens, v_heads), state float32 (slots, v_heads, k_dim, v_dim), updated in place. offsets (requests + 1): each
+    request's tokens, as ninfer_kv_tables gives them; None: one token a request. slots: the state of each request (None: its
+    index). lengths: tokens that each state has seen, 0 for one that begins with zeros (None: all are read). scale:
+    k_dim ** -0.5 unless given; norm_eps: q and k are divided by sqrt(sum of squares + norm_eps), None: not."""
+    _TYPES or _types()
+    device = _on(q, "q")
+    tokens = q.shape[0]
+    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, _ANY, device)
+    k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, (code,), device)
+    v_at, _, v_token, v_head, v_shape = _heads(v, "v", tokens, (code,), device)
+    _, k_heads, k_dim = shape
+    _, v_heads, v_dim = v_shape
+    if k_shape != shape:
+        raise ValueError("q and k must have one shape")
+    d_at, d_code, d_stride = _matrix(log_decay, "log_decay", (tokens, v_heads), device)
+    b_at, b_code, b_stride = _matrix(beta, "beta", (tokens, v_heads), device)
+    s_strides = state.stride()
+    if d_code or b_code or state.dtype is not _F32 or state.get_device() != device:
+        raise ValueError(f"log_decay, beta and state must be float32 on cuda:{device}")
+    if state.dim() != 4 or state.shape[1:] != (v_heads, k_dim, v_dim) or not state[0].is_contiguous():
+        raise ValueError(f"state must be (slots, {v_heads}, {k_dim}, {v_dim}) with contiguous slots")
+    n = state.shape[0]
+    requests = tokens if offsets is None else offsets.numel() - 1
+    if slots is not None and offsets is None:
+        requests = slots.numel()
+    if out is None:
+        out = _torch().empty(v_shape, dtype=out_dtype or v.dtype, device=v.device)
+    w_at = w_bytes = 0
+    need = ninfer_gated_delta_workspace(tokens, requests, k_heads, v_heads, k_dim, v_dim) if workspace is None else 0
+    if need:
+        workspace = _torch().empty(need, dtype=_torch().uint8, device=q.device)
+    if workspace is not None:
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")
+        w_at, w_bytes = workspace.data_ptr(), workspace.nbytes
+    o_dtype = out.dtype
+    _check(_lib.ninfer_gated_delta(_DELTA.pack(
+        q_at, k_at, v_at, d_at, b_at, state.data_ptr(), _arg(slots, "slots", _I32, requests, device),
+        _arg(offsets, "offsets", _I32, requests + 1, device), _arg(lengths, "lengths", _I32, requests, device),
+        _arg(out, "out", o_dtype, tokens * v_heads * v_dim, device), _arg(status, "status", _I32, 1, device), tokens, requests, n,
+        k_heads, v_heads, k_dim, v_dim, q_token, q_head, k_token, k_head, v_token, v_head, d_stride, b_stride,
+        s_strides[0] if n > 1 else v_heads * k_dim * v_dim, k_dim ** -0.5 if scale is None else scale,
+        -1.0 if norm_eps is None else norm_eps, code, _TYPES.get(o_dtype, -1)), w_at, w_bytes, _raw_stream(device)))
+    return out
+
+
+def ninfer_sample(logits, random, temperature=None, top_k=None, top_p=None, min_p=None, out=None, logprobs=None):
+    """The next token of each row of logits (rows, vocab), int32 (rows,), by temperature (0: the largest logit), top_k
+    (int32, 0: all), top_p and min_p (float32), each (rows,) or None, and random (float32 (rows,), in [0, 1)). logprobs:
+    a float32 (rows,) tensor that gets the logarithm of the token's share of what is kept, or None."""
+    _TYPES or _types()
+    device = _on(logits, "logits")
+    code, strides = _rows(logits, "logits", 2, _ANY, device)
+    rows, vocab = logits.shape
+    if out is None:
+        out = _torch().empty(rows, dtype=_I32, device=logits.device)
+    _check(_lib.ninfer_sample(_SAMPLE.pack(
+        logits.data_ptr(), _arg(temperature, "temperature", _F32, rows, device), _arg(top_p, "top_p", _F32, rows, device),
+        _arg(min_p, "min_p", _F32, rows, device), _arg(top_k, "top_k", _I32, rows, device),
+        _arg(random, "random", _F32, rows, device) if random is not None else 0, _arg(out, "out", _I32, rows, device),
+        _arg(logprobs, "logprobs", _F32, rows, device), rows, vocab, strides[0] if rows > 1 else vocab, code, 0), _raw_stream(device)))
     return out

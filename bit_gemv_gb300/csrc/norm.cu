@@ -1,0 +1,315 @@
+// ninfer_norm: root-mean-square norm of groups of a row, with the residual's
+// addition before it and a gate behind it.
+//
+// Each element is read once and written once, so HBM bounds a prompt and latency a single row. A group's
+// values stay in the registers of the threads that read them between the sum of squares and the product:
+// of a few lanes for the heads of a row (norm_team_kernel), of a CTA for a hidden state (norm_row_kernel). Only groups of more
+// than 32768 elements are read twice (norm_long_kernel).
+#include <cmath>
+
+#include "decode.cuh"
+#include "gemv.h"
+#include "ninfer_layer.h"
+
+namespace ninfer {
+namespace {
+
+constexpr int kTeamThreads = 256;
+constexpr uint32_t kMostTeam = 256, kMostRow = 32768;   // elements of a group: 8 a lane, 32 a thread
+
+struct NormParams {
+    ninfer_norm_args a;
+    FastDiv groups;         // of a row
+    uint32_t total;         // groups in all
+    float inverse;          // 1 / group
+};
+
+// 8 neighbouring elements as they lie in memory: all loads of a thread are under way before the first conversion
+struct Raw8 {
+    uint4 lo, hi;
+};
+
+__device__ __forceinline__ Raw8 raw8(const void *base, uint64_t at, int dtype) {
+    Raw8 r;
+    const uint8_t *p = static_cast<const uint8_t *>(base) + at * (dtype == NINFER_F32 ? 4 : 2);
+    r.lo = *reinterpret_cast<const uint4 *>(p);
+    if (dtype == NINFER_F32) r.hi = *reinterpret_cast<const uint4 *>(p + 16);
+    return r;
+}
+
+__device__ __forceinline__ void widen(const Raw8 &r, int dtype, float (&o)[8]) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if (dtype == NINFER_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(w[i]);
+    } else if (dtype == NINFER_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            o[2 * i] = f.x;
+            o[2 * i + 1] = f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ float gated(float y, float z) { return y * (z / (1.f + expf(-z))); }
+
+// Where element `at` of group `group` lies in the row's tensors.
+struct Place {
+    uint64_t row;
+    uint32_t first;     // of the group within its row
+};
+
+__device__ __forceinline__ Place place_of(const NormParams &p, uint32_t index) {
+    const uint32_t row = p.groups.div(index);
+    return {row, (index - row * p.groups.d) * (uint32_t)p.a.group};
+}
+
+// A group to a team of kLanes lanes, 8 elements a lane.
+template <int kLanes>
+__global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(const __grid_constant__ NormParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const ninfer_norm_args &a = p.a;
+    const uint32_t index = blockIdx.x * (kTeamThreads / kLanes) + threadIdx.x / kLanes, e = threadIdx.x % kLanes * 8;
+    const bool on = index < p.total && e < a.group;
+    const Place at = place_of(p, on ? index : 0);
+    const uint64_t col = at.first + e;
+    Raw8 x, r, z, w;
+    if (on) {
+        x = raw8(a.x, at.row * a.x_stride + col, a.x_dtype);
+        if (a.residual) r = raw8(a.residual, at.row * a.residual_stride + col, a.residual_dtype);
+        if (a.gate) z = raw8(a.gate, at.row * a.gate_stride + col, a.gate_dtype);
+        if (a.weight) w = raw8(a.weight, e, a.weight_dtype);
+    }
+    float s[8] = {}, t[8], sum = 0.f;
+    if (on) {
+        widen(x, a.x_dtype, s);
+        if (a.residual) {
+            widen(r, a.residual_dtype, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] += t[i];
+            if (a.sum) store8(a.sum, at.row * a.sum_stride + col, a.residual_dtype, s);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(s[i], s[i], sum);
+#pragma unroll
+    for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
+    if (!on) return;
+    const float scale = 1.f / sqrtf(fmaf(sum, p.inverse, a.eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] *= scale;
+    if (a.weight) {
+        widen(w, a.weight_dtype, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] *= t[i] + a.weight_offset;
+    }
+    if (a.gate) {
+        widen(z, a.gate_dtype, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = gated(s[i], t[i]);
+    }
+    store8(a.out, at.row * a.out_stride + col, a.out_dtype, s);
+}
+
+// The CTA's sum; every thread gets it, the same bits.
+__device__ __forceinline__ float sum_of_all(float v) {
+    __shared__ float part[32];
+#pragma unroll
+    for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+    __syncthreads();
+    v = threadIdx.x % 32 < blockDim.x / 32 ? part[threadIdx.x % 32] : 0.f;
+#pragma unroll
+    for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
+    return v;
+}
+
+// A group to a CTA, kPer times 8 elements a thread: neighbouring ones in vectors, or (rows off 16-byte boundaries,
+// groups of no multiple of 8) one by one.
+template <int kPer, bool kVec>
+__global__ void __launch_bounds__(1024) norm_row_kernel(const __grid_constant__ NormParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const ninfer_norm_args &a = p.a;
+    const Place at = place_of(p, blockIdx.x);
+    const uint32_t group = (uint32_t)a.group, threads = blockDim.x, tid = threadIdx.x;
+    const uint64_t x_at = at.row * a.x_stride + at.first, r_at = at.row * a.residual_stride + at.first;
+    const uint64_t z_at = at.row * a.gate_stride + at.first, sum_at = at.row * a.sum_stride + at.first;
+    const uint64_t out_at = at.row * a.out_stride + at.first;
+    float s[kPer][8], sum = 0.f;
+    if (kVec) {
+        Raw8 x[kPer], r[kPer];
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t e = (tid + j * threads) * 8;
+            if (e >= group) continue;
+            x[j] = raw8(a.x, x_at + e, a.x_dtype);
+            if (a.residual) r[j] = raw8(a.residual, r_at + e, a.residual_dtype);
+        }
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+            const uint32_t e = (tid + j * threads) * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[j][i] = 0.f;
+            if (e >= group) continue;
+            widen(x[j], a.x_dtype, s[j]);
+            if (a.residual) {
+                float t[8];
+                widen(r[j], a.residual_dtype, t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[j][i] += t[i];
+                if (a.sum) store8(a.sum, sum_at + e, a.residual_dtype, s[j]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t e = tid + (j * 8 + i) * threads;
+                s[j][i] = 0.f;
+                if (e >= group) continue;
+                s[j][i] = load1(a.x, x_at + e, a.x_dtype);
+                if (a.residual) {
+                    s[j][i] += load1(a.residual, r_at + e, a.residual_dtype);
+                    if (a.sum) store1(a.sum, sum_at + e, a.residual_dtype, s[j][i]);
+                }
+            }
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(s[j][i], s[j][i], sum);
+    const float scale = 1.f / sqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+        if (kVec) {
+            const uint32_t e = (tid + j * threads) * 8;
+            if (e >= group) break;
+            float t[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[j][i] *= scale;
+            if (a.weight) {
+                widen(raw8(a.weight, e, a.weight_dtype), a.weight_dtype, t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[j][i] *= t[i] + a.weight_offset;
+            }
+            if (a.gate) {
+                widen(raw8(a.gate, z_at + e, a.gate_dtype), a.gate_dtype, t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[j][i] = gated(s[j][i], t[i]);
+            }
+            store8(a.out, out_at + e, a.out_dtype, s[j]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t e = tid + (j * 8 + i) * threads;
+                if (e >= group) break;
+                float y = s[j][i] * scale;
+                if (a.weight) y *= load1(a.weight, e, a.weight_dtype) + a.weight_offset;
+                if (a.gate) y = gated(y, load1(a.gate, z_at + e, a.gate_dtype));
+                store1(a.out, out_at + e, a.out_dtype, y);
+            }
+        }
+    }
+}
+
+// A group of any size to a CTA, read twice; an element's outputs are written by the thread that reads it last.
+__global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__ NormParams p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const ninfer_norm_args &a = p.a;
+    const Place at = place_of(p, blockIdx.x);
+    const uint64_t x_at = at.row * a.x_stride + at.first, r_at = at.row * a.residual_stride + at.first;
+    auto value = [&](uint64_t e) {
+        float s = load1(a.x, x_at + e, a.x_dtype);
+        if (a.residual) s += load1(a.residual, r_at + e, a.residual_dtype);
+        return s;
+    };
+    float sum = 0.f;
+    for (uint64_t e = threadIdx.x; e < a.group; e += 1024) {
+        const float s = value(e);
+        sum = fmaf(s, s, sum);
+    }
+    const float scale = 1.f / sqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
+    for (uint64_t e = threadIdx.x; e < a.group; e += 1024) {
+        const float s = value(e);
+        float y = s * scale;
+        if (a.weight) y *= load1(a.weight, e, a.weight_dtype) + a.weight_offset;
+        if (a.gate) y = gated(y, load1(a.gate, at.row * a.gate_stride + at.first + e, a.gate_dtype));
+        if (a.sum) store1(a.sum, at.row * a.sum_stride + at.first + e, a.residual_dtype, s);
+        store1(a.out, at.row * a.out_stride + at.first + e, a.out_dtype, y);
+    }
+}
+
+}  // namespace
+}  // namespace ninfer
+
+using namespace ninfer;
+
+extern "C" int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream) {
+    if (!args || !args->x || !args->out) return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: NULL args, x or out");
+    const ninfer_norm_args &a = *args;
+    if (a.sum && !a.residual) return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: sum without a residual");
+    if (a.reserved) return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: reserved must be 0");
+    if (!(a.eps >= 0.f) || !std::isfinite(a.eps) || !std::isfinite(a.weight_offset))
+        return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: eps must be finite and 0 or more, weight_offset finite");
+    if (!a.rows || !a.cols || !a.group || a.cols % a.group || a.cols > 0x7fffffffull)
+        return fail(NINFER_ERR_SHAPE, "norm: %llu rows of %llu in groups of %llu", (unsigned long long)a.rows,
+                    (unsigned long long)a.cols, (unsigned long long)a.group);
+    const struct {
+        const void *p;
+        uint64_t stride;
+        int dtype;
+        const char *name;
+    } tensors[] = {{a.x, a.x_stride, a.x_dtype, "x"},
+                   {a.residual, a.residual_stride, a.residual_dtype, "residual"},
+                   {a.sum, a.sum_stride, a.residual_dtype, "sum"},
+                   {a.gate, a.gate_stride, a.gate_dtype, "gate"},
+                   {a.out, a.out_stride, a.out_dtype, "out"},
+                   {a.weight, a.cols, a.weight_dtype, "weight"}};
+    bool vec = a.group % 8 == 0;
+    for (const auto &t : tensors) {
+        if (!t.p) continue;
+        if (!dtype_valid(t.dtype)) return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: %s dtype %d unsupported", t.name, t.dtype);
+        const size_t es = dtype_size(t.dtype);
+        if (!aligned(t.p, es)) return fail(NINFER_ERR_ALIGNMENT, "norm: %s is not aligned to its elements", t.name);
+        if (a.rows > 1 && t.stride < a.cols) return fail(NINFER_ERR_SHAPE, "norm: %s stride below cols", t.name);
+        if (a.rows > 1 && t.stride >= (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "norm: %s stride of 2^40 or more", t.name);
+        vec = vec && aligned(t.p, 16) && (a.rows == 1 || t.p == a.weight || t.stride * es % 16 == 0);
+    }
+    const uint64_t groups = a.cols / a.group;
+    uint64_t total;
+    if (!mul_ok(a.rows, groups, &total) || total > 0x7fffffffull)
+        return fail(NINFER_ERR_OVERFLOW, "norm: rows * groups over 2^31 - 1");
+    NormParams p;
+    p.a = a;
+    p.groups = FastDiv((uint32_t)groups);
+    p.total = (uint32_t)total;
+    p.inverse = 1.f / (float)a.group;
+    const cudaStream_t st = (cudaStream_t)stream;
+    if (vec && a.group <= kMostTeam) {
+        const unsigned lanes = a.group <= 32 ? 4 : a.group <= 64 ? 8 : a.group <= 128 ? 16 : 32;
+        const auto kernel = lanes == 4    ? norm_team_kernel<4>
+                            : lanes == 8  ? norm_team_kernel<8>
+                            : lanes == 16 ? norm_team_kernel<16>
+                                          : norm_team_kernel<32>;
+        const unsigned teams = kTeamThreads / lanes;
+        return launch_dependent("norm", kernel, dim3((unsigned)((total + teams - 1) / teams)), dim3(kTeamThreads), 0, st, p);
+    }
+    if (a.group > kMostRow) return launch_dependent("norm", norm_long_kernel, dim3(p.total), dim3(1024), 0, st, p);
+    const unsigned eights = (unsigned)((a.group + 7) / 8);
+    const unsigned per = eights > 2048 ? 4 : eights > 1024 ? 2 : 1;
+    const unsigned threads = (eights + 32 * per - 1) / (32 * per) * 32;
+    const auto kernel = vec ? (per == 4 ? norm_row_kernel<4, true> : per == 2 ? norm_row_kernel<2, true> : norm_row_kernel<1, true>)
+                            : (per == 4 ? norm_row_kernel<4, false> : per == 2 ? norm_row_kernel<2, false> : norm_row_kernel<1, false>);
+    return launch_dependent("norm", kernel, dim3(p.total), dim3(threads), 0, st, p);
+}
