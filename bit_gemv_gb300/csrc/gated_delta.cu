@@ -2,13 +2,13 @@
 // out = scale S^T q, over a k_dim x v_dim state of fp32 per request and value head.
 //
 // The columns of a state do not see each other: S^T k, u = beta (v - e^g S^T k), the update k u^T and S^T q need, for
-// one column of S, only that column and the k and q that all columns share. Both kernels divide the states by columns.
-// With a = S^T k and b = S^T q of the old state, out = scale (e^g b + (k . q) u): one pass over the state gives both sums,
-// a second one, in registers, updates it.
+// one column of S, only that column and the k and q that all columns share. The kernels divide the states by columns.
 //
-// One token a request (step_kernel): the state is read once and written once, and HBM bounds it.
-// Several (run_kernel): the state stays in registers from a request's first token to its last, four lanes a
-// column; fp32 multiply-adds, 3 k_dim v_dim of them a token, bound it, and latency where few heads are under way.
+// One token a request (step_kernel): with a = S^T k and b = S^T q of the old state, out = scale (e^g b + (k . q) u), so
+// that one pass over the state gives both sums and a second one, in registers, updates it: the state is read once and
+// written once, and HBM bounds it.
+// Several (prepare_kernel, chunk_kernel): 32 tokens at once, by matrix products whose state stays in registers from a
+// request's first token to its last; the tensor cores bound it, and latency where few heads are under way.
 #include <cmath>
 
 #include "decode.cuh"
@@ -18,7 +18,7 @@
 namespace ninfer {
 namespace {
 
-constexpr int kStepThreads = 256, kRunThreads = 128, kRunColumns = 32, kTile = 16;
+constexpr int kStepThreads = 256;
 
 struct DeltaParams {
     ninfer_gated_delta_args a;
@@ -161,114 +161,494 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
     }
 }
 
-// Any number of tokens a request. Four lanes hold a column: lane i of them the rows 16 j + 4 i .. 16 j + 4 i + 3, so that
-// the four read 64 neighbouring bytes of k and q. kGroups: 16-row groups of k_dim, rounded up to 4, 8 or 16.
-template <int kGroups>
-__global__ void __launch_bounds__(kRunThreads) run_kernel(const __grid_constant__ DeltaParams p) {
-    constexpr int kDim = kGroups * 16;
-    __shared__ __align__(16) float ks[kTile][kDim], qs[kTile][kDim];
-    __shared__ float vs[kTile][kRunColumns], numbers[3][kTile];     // e^g, beta, k . q
+// ---------------------------------------------------------------- prompts ---
+// A request's tokens go in chunks of 32. With G_t the chunk's log decays summed up to and with token t, S the state before it,
+//   U = T diag(beta) (V - diag(e^G) K S),     T = (I + A)^-1, A_ts = beta_t e^(G_t - G_s) k_t . k_s for s < t, else 0
+//   O = scale (diag(e^G) Q S + P U),          P_ts = e^(G_t - G_s) q_t . k_s for s <= t, else 0
+//   S <- e^(G_last) S + K^T diag(e^(G_last - G)) U
+// T diag(beta) and P need no state: prepare_kernel makes them for all chunks at once, chunk_kernel goes through them.
+constexpr int kChunk = 32, kChunkThreads = 128, kColumns = 64;      // columns of a state a CTA, 16 a warp
+constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
+enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
+constexpr uint64_t kTrianglesBytes = 4 * kChunk * kChunk * 2;       // T high and low, P high and low
+constexpr uint64_t kHeadBytes = kTrianglesBytes + kNumbers * 4;
+
+// What lies in the workspace: for every chunk and key head K and Q as binary16 (f32: two terms each), [term][K, Q][token][k_dim];
+// then for every chunk and value head the triangles, [which][t][s], and the numbers.
+struct ChunkParams {
+    DeltaParams d;
+    uint8_t *rows, *heads;
+    uint64_t rows_bytes;        // of a chunk and key head
+    uint32_t wide;              // k_dim rounded up to the kernel's steps of 16
+};
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t at) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+}
+// 16 bytes from global to shared memory, or zeros
+__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeftOpen>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeftOpen) : "memory");
+}
+
+// Two floats as two binary16 terms each: 22 bits of every value from 2^-14 of 1 on.
+__device__ __forceinline__ void split(float x, float y, uint32_t &high, uint32_t &low) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - f.x, y - f.y);
+    high = *reinterpret_cast<const uint32_t *>(&h);
+    low = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// The power of two that takes `most` (a row's largest magnitude) to 2^13 .. 2^14, so that its binary16 terms lose nothing
+// above 2^-38 of it, and its inverse.
+__device__ __forceinline__ float power_for(float most) { return __uint_as_float((uint32_t)min(max(267 - (int)(__float_as_uint(most) >> 23), 1), 253) << 23); }
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
+
+__device__ __forceinline__ float quad_max(float v) {
+    v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
+    return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
+}
+
+// A request's tokens, and the chunks that are its own: distinct ones for requests whose tokens are.
+struct Range {
+    int32_t begin, end;
+    uint32_t chunk, chunks;
+};
+__device__ __forceinline__ Range range_of(const ninfer_gated_delta_args &a, uint32_t request) {
+    const int32_t most = (int32_t)a.tokens;
+    Range r;
+    r.begin = min(max(a.offsets[request], 0), most);
+    r.end = min(max(a.offsets[request + 1], 0), most);
+    r.chunks = r.end > r.begin ? (uint32_t)(r.end - r.begin + kChunk - 1) / kChunk : 0;
+    r.chunk = (uint32_t)r.begin / kChunk + request;
+    return r;
+}
+
+// A CTA for every chunk and key head. kTerms: binary16 terms of k and q, 1 where they have 16 bits themselves.
+template <int kTerms>
+__global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
+    extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8
+    __shared__ float dots[2][kChunk][kChunk + 1], scales[2][kChunk];
+    __shared__ __align__(16) float tri[kChunkThreads / 32][kChunk][kChunk + 4];
+    __shared__ uint32_t found;
     pdl_launch_dependents();
     pdl_wait();
-    const ninfer_gated_delta_args &a = p.a;
-    const Part t = part_of(p, blockIdx.x, kRunColumns);
-    if (t.none) return;
-    const int32_t most = (int32_t)a.tokens;
-    const int32_t begin = a.offsets ? min(max(a.offsets[t.request], 0), most) : (int32_t)t.request;
-    const int32_t end = a.offsets ? min(max(a.offsets[t.request + 1], 0), most) : begin + 1;
-    if (begin >= end) return;
-    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
-    const uint32_t mine = warp * 8 + lane / 4, column = t.column + mine, part = lane % 4 * 4;
-    const bool inside = column < v_dim;
-    float *state = a.state + t.state + column;
-    float s[kGroups][4];
-#pragma unroll
-    for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r = j * 16 + part + i;
-            s[j][i] = r < k_dim && inside && !t.fresh ? state[r * v_dim] : 0.f;
+    const ninfer_gated_delta_args &a = p.d.a;
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim;
+    const uint32_t chunk = blockIdx.x / (uint32_t)a.k_heads, key_head = blockIdx.x % (uint32_t)a.k_heads;
+    // the request that this chunk belongs to
+    if (tid == 0) found = ~0u;
+    __syncthreads();
+    for (uint32_t r = tid; r < (uint32_t)a.requests; r += kChunkThreads) {
+        const Range c = range_of(a, r);
+        if (chunk - c.chunk < c.chunks) found = r;
+    }
+    __syncthreads();
+    const uint32_t request = found;
+    if (request == ~0u) return;
+    const Range range = range_of(a, request);
+    const int32_t first = range.begin + (int32_t)(chunk - range.chunk) * kChunk, count = min(range.end - first, kChunk);
+    // rows of K, then of Q: their norms, and their elements times a power of two
+    const uint32_t stride = p.wide * 2 + 16, term_bytes = 2 * kChunk * stride;
+    uint8_t *rows = p.rows + (uint64_t)blockIdx.x * p.rows_bytes;
+    const bool low_dim = lane * 8 < k_dim, in_row = lane * 8 < p.wide;
+#pragma unroll 4
+    for (uint32_t i = warp; i < 2 * kChunk; i += kChunkThreads / 32) {
+        const uint32_t t = i % kChunk, q = i / kChunk;
+        float x[8] = {}, sum = 0.f, most = 0.f;
+        if ((int32_t)t < count && low_dim) {
+            const uint64_t token = first + t;
+            if (q) load8(a.q, token * a.q_token_stride + key_head * a.q_head_stride + lane * 8, a.dtype, x);
+            else load8(a.k, token * a.k_token_stride + key_head * a.k_head_stride + lane * 8, a.dtype, x);
         }
-    for (int32_t t0 = begin; t0 < end; t0 += kTile) {
-        const int32_t count = min(end - t0, kTile);
-        __syncthreads();
-        // a warp a token: its k and q, normalised; its numbers and values
-        for (int32_t i = warp; i < count; i += kRunThreads / 32) {
-            const uint64_t token = t0 + i;
-            float k[8] = {}, q[8] = {}, kk = 0.f, qq = 0.f, kq = 0.f;
-            if (lane * 8 < k_dim) {
-                load8(a.k, token * a.k_token_stride + t.key_head * a.k_head_stride + lane * 8, a.dtype, k);
-                load8(a.q, token * a.q_token_stride + t.key_head * a.q_head_stride + lane * 8, a.dtype, q);
-            }
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                kk = fmaf(k[e], k[e], kk);
-                qq = fmaf(q[e], q[e], qq);
-                kq = fmaf(k[e], q[e], kq);
-            }
-#pragma unroll
-            for (int e = 16; e; e /= 2) {
-                kk += __shfl_xor_sync(~0u, kk, e);
-                qq += __shfl_xor_sync(~0u, qq, e);
-                kq += __shfl_xor_sync(~0u, kq, e);
-            }
-            const float k_scale = a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(kk + a.norm_eps);
-            const float q_scale = a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(qq + a.norm_eps);
-            if (lane * 8 < kDim) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    ks[i][lane * 8 + e] = k[e] * k_scale;
-                    qs[i][lane * 8 + e] = q[e] * q_scale;
-                }
-            }
-            vs[i][lane] = t.column + lane < v_dim ? load1(a.v, token * a.v_token_stride + t.head * a.v_head_stride + t.column + lane, a.dtype) : 0.f;
-            if (lane == 0) {
-                numbers[0][i] = expf(a.log_decay[token * a.decay_stride + t.head]);
-                numbers[1][i] = a.beta[token * a.beta_stride + t.head];
-                numbers[2][i] = kq * k_scale * q_scale;
-            }
+        for (int e = 0; e < 8; ++e) {
+            sum = fmaf(x[e], x[e], sum);
+            most = fmaxf(most, fabsf(x[e]));
         }
-        __syncthreads();
-        for (int32_t i = 0; i < count; ++i) {
-            float x = 0.f, y = 0.f;
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const float4 k = *reinterpret_cast<const float4 *>(&ks[i][j * 16 + part]), q = *reinterpret_cast<const float4 *>(&qs[i][j * 16 + part]);
-                x = fmaf(s[j][0], k.x, x);
-                x = fmaf(s[j][1], k.y, x);
-                x = fmaf(s[j][2], k.z, x);
-                x = fmaf(s[j][3], k.w, x);
-                y = fmaf(s[j][0], q.x, y);
-                y = fmaf(s[j][1], q.y, y);
-                y = fmaf(s[j][2], q.z, y);
-                y = fmaf(s[j][3], q.w, y);
-            }
-            x += __shfl_xor_sync(~0u, x, 1);
-            y += __shfl_xor_sync(~0u, y, 1);
-            x += __shfl_xor_sync(~0u, x, 2);
-            y += __shfl_xor_sync(~0u, y, 2);
-            const float decay = numbers[0][i], u = numbers[1][i] * (vs[i][mine] - decay * x);
-            if (lane % 4 == 0 && inside)
-                store1(a.out, ((uint64_t)(t0 + i) * a.v_heads + t.head) * v_dim + column, a.out_dtype, a.scale * (decay * y + numbers[2][i] * u));
+        for (int e = 16; e; e /= 2) {
+            sum += __shfl_xor_sync(~0u, sum, e);
+            most = fmaxf(most, __shfl_xor_sync(~0u, most, e));
+        }
+        const float up = power_for(most);
+        if (lane == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
+        uint32_t high[4], low[4];
 #pragma unroll
-            for (int j = 0; j < kGroups; ++j) {
-                const float4 k = *reinterpret_cast<const float4 *>(&ks[i][j * 16 + part]);
-                s[j][0] = fmaf(k.x, u, decay * s[j][0]);
-                s[j][1] = fmaf(k.y, u, decay * s[j][1]);
-                s[j][2] = fmaf(k.z, u, decay * s[j][2]);
-                s[j][3] = fmaf(k.w, u, decay * s[j][3]);
+        for (int e = 0; e < 4; ++e) split(x[2 * e] * up, x[2 * e + 1] * up, high[e], low[e]);
+        if (in_row) {
+            const uint4 h = make_uint4(high[0], high[1], high[2], high[3]), l = make_uint4(low[0], low[1], low[2], low[3]);
+            *reinterpret_cast<uint4 *>(smem + i * stride + lane * 16) = h;
+            *reinterpret_cast<uint4 *>(rows + (i * p.wide + lane * 8) * 2) = h;
+            if (kTerms == 2) {
+                *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + lane * 16) = l;
+                *reinterpret_cast<uint4 *>(rows + ((2 * kChunk + i) * p.wide + lane * 8) * 2) = l;
             }
         }
     }
-    if (!inside) return;
+    __syncthreads();
+    // (K, Q) K^T: 16 rows a warp
+    {
+        float d[4][4] = {};
+        const uint32_t base = smem_u32(smem), from_a = base + (warp * 16 + lane % 16) * stride + lane / 16 * 16;
+        const uint32_t from_b = base + (lane % 8 + lane / 16 * 8) * stride + lane / 8 % 2 * 16;
+        for (uint32_t k = 0; k < p.wide; k += 16) {
+            uint32_t x[kTerms][4], y[4];
 #pragma unroll
-    for (int j = 0; j < kGroups; ++j)
+            for (int e = 0; e < kTerms; ++e) load_matrices(x[e], from_a + e * term_bytes + k * 2);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t r = j * 16 + part + i;
-            if (r < k_dim) state[r * v_dim] = s[j][i];
+            for (int n = 0; n < 2; ++n) {
+                load_matrices(y, from_b + n * 16 * stride + k * 2);
+#pragma unroll
+                for (int e = 0; e < kTerms; ++e) {
+                    mma(d[2 * n], x[e], y[0], y[1]);
+                    mma(d[2 * n + 1], x[e], y[2], y[3]);
+                }
+                if (kTerms == 2) {
+                    load_matrices(y, from_b + term_bytes + n * 16 * stride + k * 2);
+                    mma(d[2 * n], x[0], y[0], y[1]);
+                    mma(d[2 * n + 1], x[0], y[2], y[3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t t = warp % 2 * 16 + lane / 4 + e / 2 * 8, u = n * 8 + lane % 4 * 2 + e % 2;
+                dots[warp / 2][t][u] = d[n][e] * scales[warp / 2][t] * scales[0][u];
+            }
+    }
+    __syncthreads();
+    // A warp a value head: lane s has column s of both triangles. Sums of log decays are whole multiples of 2^-40, so that
+    // differences of them are exact however far the decays have gone; e^(+-2^15) is all the same.
+    const uint32_t group = p.d.group.d;
+    for (uint32_t i = warp; i < group; i += kChunkThreads / 32) {
+        const uint32_t head = key_head * group + i;
+        const bool on = (int32_t)lane < count;
+        const uint64_t token = first + (on ? lane : 0);
+        const float g = on ? a.log_decay[token * a.decay_stride + head] : 0.f, beta = on ? a.beta[token * a.beta_stride + head] : 0.f;
+        long long sum = __float2ll_rn(fminf(fmaxf(g, -32768.f), 32768.f) * 0x1p40f);
+#pragma unroll
+        for (int k = 1; k < 32; k *= 2) {
+            const long long u = __shfl_up_sync(~0u, sum, k);
+            if (lane >= (uint32_t)k) sum += u;
+        }
+        const long long last = __shfl_sync(~0u, sum, 31);
+        const uint32_t bad = __ballot_sync(~0u, g != g);
+        const float poison = bad & (~0u >> (31 - lane)) ? NAN : 1.f, spoilt = bad ? NAN : 1.f;
+        float pp[kChunk], tt[kChunk], most_p = 0.f, most_t = 0.f;
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) {
+            const long long gt = __shfl_sync(~0u, sum, t);
+            const float fade = (int)lane <= t ? expf(__ll2float_rn(gt - sum) * 0x1p-40f) : 0.f, bt = __shfl_sync(~0u, beta, t);
+            tri[warp][t][lane] = (int)lane < t ? bt * fade * dots[0][t][lane] : 0.f;
+            pp[t] = (int)lane <= t ? fade * dots[1][t][lane] : 0.f;
+            most_p = fmaxf(most_p, fabsf(pp[t]));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) {
+            float sum4[4] = {(int)lane == t ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int m = 0; m < t; m += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&tri[warp][t][m]);
+                sum4[0] = fmaf(-x.x, tt[m], sum4[0]);
+                if (m + 1 < t) sum4[1] = fmaf(-x.y, tt[m + 1], sum4[1]);
+                if (m + 2 < t) sum4[2] = fmaf(-x.z, tt[m + 2], sum4[2]);
+                if (m + 3 < t) sum4[3] = fmaf(-x.w, tt[m + 3], sum4[3]);
+            }
+            tt[t] = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) most_t = fmaxf(most_t, fabsf(tt[t] *= beta));
+        __syncwarp();
+#pragma unroll
+        for (int k = 16; k; k /= 2) {
+            most_p = fmaxf(most_p, __shfl_xor_sync(~0u, most_p, k));
+            most_t = fmaxf(most_t, __shfl_xor_sync(~0u, most_t, k));
+        }
+        const float up_p = power_for(most_p), up_t = power_for(most_t);
+        uint8_t *to = p.heads + ((uint64_t)chunk * a.v_heads + head) * kHeadBytes;
+        __half *out = reinterpret_cast<__half *>(to);
+#pragma unroll
+        for (int t = 0; t < kChunk; ++t) {
+            const float x = tt[t] * up_t, y = pp[t] * up_p;
+            const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
+            out[t * kChunk + lane] = xh;
+            out[(kChunk + t) * kChunk + lane] = __float2half_rn(x - __half2float(xh));
+            out[(2 * kChunk + t) * kChunk + lane] = yh;
+            out[(3 * kChunk + t) * kChunk + lane] = __float2half_rn(y - __half2float(yh));
+        }
+        float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
+        const float fade = expf(__ll2float_rn(sum) * 0x1p-40f) * poison;
+        numbers[kOfK + lane] = fade * scales[0][lane];
+        numbers[kOfQ + lane] = a.scale * fade * scales[1][lane];
+        numbers[kOfU + lane] = expf(__ll2float_rn(last - sum) * 0x1p-40f) * scales[0][lane];
+        if (lane < 4) {
+            const float x = lane == 0 ? expf(__ll2float_rn(last) * 0x1p-40f) * spoilt : lane == 1 ? inverse_power(up_t) : lane == 2 ? a.scale * inverse_power(up_p) : 0.f;
+            numbers[kLeft + lane] = x;
+        }
+    }
+}
+
+// 64 columns of one state a CTA, 16 a warp; the state stays in the accumulators' layout of mma, transposed (rows are columns of
+// S, columns k), which is the layout of the A operand of the products with K and Q, and U, made the same way, that of
+// the products with P and K. Every factor that is not exact in binary16 enters as two terms, scaled row by row.
+// kSteps: steps of 16 of k_dim; kTerms: terms of k and q.
+template <int kSteps, int kTerms>
+__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
+    constexpr uint32_t kRowStride = kSteps * 32 + 16, kTermBytes = 2 * kChunk * kRowStride, kTriStride = kChunk * 2 + 16;
+    constexpr uint32_t kTri = kTerms * kTermBytes, kNumbersAt = kTri + 4 * kChunk * kTriStride, kV = kNumbersAt + kNumbers * 4;
+    extern __shared__ __align__(16) uint8_t smem[];
+    pdl_launch_dependents();
+    pdl_wait();
+    const ninfer_gated_delta_args &a = p.d.a;
+    const Part part = part_of(p.d, blockIdx.x, kColumns);
+    if (part.none) return;
+    const Range range = range_of(a, part.request);
+    if (!range.chunks) return;
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
+    const uint32_t es = a.dtype == NINFER_F32 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
+    const uint32_t base = smem_u32(smem), out_at = 2 * stage_bytes + warp * (kChunk * 80);
+    const uint32_t mine = part.column + warp * 16, column = mine + lane / 4;         // this thread's: column, column + 8
+    const uint32_t v_units = 16 / es, units_row = kColumns / v_units;
+
+    auto fetch = [&](uint32_t j) {
+        const uint32_t stage = base + j % 2 * stage_bytes;
+        const uint64_t chunk = range.chunk + j;
+        const uint8_t *rows = p.rows + (chunk * a.k_heads + part.key_head) * p.rows_bytes;
+        constexpr uint32_t kUnits = kSteps * 2;
+        for (uint32_t i = tid; i < kTerms * 2 * kChunk * kUnits; i += kChunkThreads)
+            copy16(stage + i / kUnits * kRowStride + i % kUnits * 16, rows + i * 16, true);
+        const uint8_t *head = p.heads + (chunk * a.v_heads + part.head) * kHeadBytes;
+        for (uint32_t i = tid; i < 4 * kChunk * 4; i += kChunkThreads) copy16(stage + kTri + i / 4 * kTriStride + i % 4 * 16, head + i * 16, true);
+        if (tid < kNumbers / 4) copy16(stage + kNumbersAt + tid * 16, head + kTrianglesBytes + tid * 16, true);
+        const int32_t first = range.begin + (int32_t)j * kChunk;
+        for (uint32_t i = tid; i < kChunk * units_row; i += kChunkThreads) {
+            const uint32_t t = i / units_row, u = i % units_row, c = part.column + u * v_units;
+            const bool on = first + (int32_t)t < range.end && c < v_dim;
+            const uint64_t token = on ? first + t : 0;
+            copy16(stage + kV + t * v_stride + u * 16, static_cast<const uint8_t *>(a.v) + (token * a.v_token_stride + part.head * a.v_head_stride + (on ? c : 0)) * es, on);
+        }
+        copies_commit();
+    };
+
+    // s[n][e]: k = 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
+    float s[2 * kSteps][4];
+    float *state = a.state + part.state;
+#pragma unroll
+    for (int n = 0; n < 2 * kSteps; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t k = n * 8 + lane % 4 * 2 + e % 2, c = column + e / 2 * 8;
+            s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
+        }
+    const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
+    const uint32_t t_row = lane % 16, t_col = lane / 16 * 16;
+    fetch(0);
+    for (uint32_t j = 0; j < range.chunks; ++j) {
+        if (j + 1 < range.chunks) {
+            fetch(j + 1);
+            copies_wait<1>();
+        } else copies_wait<0>();
+        __syncthreads();
+        const uint32_t stage = base + j % 2 * stage_bytes;
+        const uint8_t *here = smem + j % 2 * stage_bytes;
+        const float *numbers = reinterpret_cast<const float *>(here + kNumbersAt);
+        if (mine < v_dim) {         // whole warps
+            // S^T times K^T and Q^T: x[0..3] tokens of K, x[4..7] of Q
+            float x[8][4] = {}, up0, up1;
+            {
+                float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+                for (int n = 0; n < 2 * kSteps; ++n) {
+                    m0 = fmaxf(m0, fmaxf(fabsf(s[n][0]), fabsf(s[n][1])));
+                    m1 = fmaxf(m1, fmaxf(fabsf(s[n][2]), fabsf(s[n][3])));
+                }
+                up0 = power_for(quad_max(m0));
+                up1 = power_for(quad_max(m1));
+            }
+#pragma unroll
+            for (int k = 0; k < kSteps; ++k) {
+                uint32_t high[4], low[4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    split(s[2 * k + h][0] * up0, s[2 * k + h][1] * up0, high[2 * h], low[2 * h]);
+                    split(s[2 * k + h][2] * up1, s[2 * k + h][3] * up1, high[2 * h + 1], low[2 * h + 1]);
+                }
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    uint32_t y[4];
+                    load_matrices(y, stage + (n * 16 + b_row) * kRowStride + k * 32 + b_col);
+                    mma(x[2 * n], high, y[0], y[1]);
+                    mma(x[2 * n + 1], high, y[2], y[3]);
+                    mma(x[2 * n], low, y[0], y[1]);
+                    mma(x[2 * n + 1], low, y[2], y[3]);
+                    if (kTerms == 2) {
+                        load_matrices(y, stage + kTermBytes + (n * 16 + b_row) * kRowStride + k * 32 + b_col);
+                        mma(x[2 * n], high, y[0], y[1]);
+                        mma(x[2 * n + 1], high, y[2], y[3]);
+                    }
+                }
+            }
+            const float down0 = inverse_power(up0), down1 = inverse_power(up1);
+            // W = V - e^G K S, in place; then U = T diag(beta) W
+            float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfK + n * 8 + lane % 4 * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint8_t *at = here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (warp * 16 + lane / 4 + e / 2 * 8) * es;
+                    const float v = load1(at, 0, a.dtype);
+                    x[n][e] = v - (e % 2 ? f.y : f.x) * (x[n][e] * (e / 2 ? down1 : down0));
+                }
+                m0 = fmaxf(m0, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+            }
+            // (rows of 32 tokens) times a triangle: y[n] += x times the lower triangle's rows 8 n .. 8 n + 7
+            auto triangle = [&](float (&y)[4][4], const uint32_t (&high)[2][4], const uint32_t (&low)[2][4], uint32_t which) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int n = k; n < 2; ++n) {
+                        uint32_t b[4], c[4];
+                        const uint32_t from = stage + kTri + (which * kChunk + n * 16 + b_row) * kTriStride + k * 32 + b_col;
+                        load_matrices(b, from);
+                        load_matrices(c, from + kChunk * kTriStride);
+                        mma(y[2 * n], high[k], b[0], b[1]);
+                        mma(y[2 * n + 1], high[k], b[2], b[3]);
+                        mma(y[2 * n], high[k], c[0], c[1]);
+                        mma(y[2 * n + 1], high[k], c[2], c[3]);
+                        mma(y[2 * n], low[k], b[0], b[1]);
+                        mma(y[2 * n + 1], low[k], b[2], b[3]);
+                    }
+            };
+            auto halves = [&](const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        split(y[2 * k + h][0] * p0, y[2 * k + h][1] * p0, high[k][2 * h], low[k][2 * h]);
+                        split(y[2 * k + h][2] * p1, y[2 * k + h][3] * p1, high[k][2 * h + 1], low[k][2 * h + 1]);
+                    }
+            };
+            uint32_t high[2][4], low[2][4];
+            float u[4][4] = {}, o[4][4] = {}, w[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[n][e] = x[n][e];
+            float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
+            halves(w, p0, p1, high, low);
+            triangle(u, high, low, 0);
+            const float of_t = numbers[kOfT], f0 = of_t * inverse_power(p0), f1 = of_t * inverse_power(p1);
+            m0 = m1 = 0.f;
+            float n0 = 0.f, n1 = 0.f;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfU + n * 8 + lane % 4 * 2);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    u[n][e] *= e / 2 ? f1 : f0;
+                    w[n][e] = u[n][e] * (e % 2 ? f.y : f.x);
+                }
+                m0 = fmaxf(m0, fmaxf(fabsf(u[n][0]), fabsf(u[n][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(u[n][2]), fabsf(u[n][3])));
+                n0 = fmaxf(n0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
+                n1 = fmaxf(n1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
+            }
+            p0 = power_for(quad_max(m0));
+            p1 = power_for(quad_max(m1));
+            halves(u, p0, p1, high, low);
+            triangle(o, high, low, 2);
+            // out, through shared memory: 16 columns of each token
+            {
+                const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
+                const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfQ + n * 8 + lane % 4 * 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y = (e % 2 ? f.y : f.x) * (x[4 + n][e] * (e / 2 ? down1 : down0)) + o[n][e] * (e / 2 ? g1 : g0);
+                        store1(smem + out_at + (n * 8 + lane % 4 * 2 + e % 2) * 80 + (lane / 4 + e / 2 * 8) * out_es, 0, a.out_dtype, y);
+                    }
+                }
+                __syncwarp();
+                const int32_t first = range.begin + (int32_t)j * kChunk;
+                const uint32_t units = out_es, per = 16 / out_es;       // 16-byte units of 16 columns, elements of one
+                for (uint32_t i = lane; i < kChunk * units; i += 32) {
+                    const uint32_t t = i / units, c = i % units;
+                    if (first + (int32_t)t < range.end && mine + c * per < v_dim) {
+                        const uint64_t at = ((uint64_t)(first + t) * a.v_heads + part.head) * v_dim + mine + c * per;
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * out_es) = *reinterpret_cast<const uint4 *>(smem + out_at + t * 80 + c * 16);
+                    }
+                }
+                __syncwarp();
+            }
+            // S^T = e^G_last S^T + (e^(G_last - G) U)^T K; the products begin at zero and are added rounded to nearest
+            p0 = power_for(quad_max(n0));
+            p1 = power_for(quad_max(n1));
+            halves(w, p0, p1, high, low);
+            const float left = numbers[kLeft], d0 = inverse_power(p0), d1 = inverse_power(p1);
+#pragma unroll
+            for (int n = 0; n < kSteps; ++n) {
+                float y[2][4] = {};
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t b[4];
+                    load_matrices_turned(b, stage + (k * 16 + t_row) * kRowStride + n * 32 + t_col);
+                    mma(y[0], high[k], b[0], b[1]);
+                    mma(y[1], high[k], b[2], b[3]);
+                    mma(y[0], low[k], b[0], b[1]);
+                    mma(y[1], low[k], b[2], b[3]);
+                    if (kTerms == 2) {
+                        load_matrices_turned(b, stage + kTermBytes + (k * 16 + t_row) * kRowStride + n * 32 + t_col);
+                        mma(y[0], high[k], b[0], b[1]);
+                        mma(y[1], high[k], b[2], b[3]);
+                    }
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[2 * n + h][e] = fmaf(y[h][e], e / 2 ? d1 : d0, left * s[2 * n + h][e]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int n = 0; n < 2 * kSteps; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t k = n * 8 + lane % 4 * 2 + e % 2, c = column + e / 2 * 8;
+            if (k < k_dim && c < v_dim) state[k * v_dim + c] = s[n][e];
         }
 }
+
+template <int kTerms>
+auto chunk_kernel_of(uint32_t wide) {
+    return wide == 64 ? chunk_kernel<4, kTerms> : wide == 96 ? chunk_kernel<6, kTerms> : wide == 128 ? chunk_kernel<8, kTerms> : chunk_kernel<16, kTerms>;
+}
+
+// k_dim rounded up to what the kernel has instances for
+uint32_t wide_of(uint64_t k_dim) { return k_dim <= 64 ? 64 : k_dim <= 96 ? 96 : k_dim <= 128 ? 128 : 256; }
+
+uint64_t rows_bytes_of(int terms, uint64_t k_dim) { return (uint64_t)terms * 2 * kChunk * wide_of(k_dim) * 2; }
 
 int check_sizes(uint64_t tokens, uint64_t requests, uint64_t k_heads, uint64_t v_heads, uint64_t k_dim, uint64_t v_dim) {
     if (!tokens || tokens > 0x7fffffffull || !requests || requests > 0x7fffffffull)
@@ -291,7 +671,10 @@ extern "C" int ninfer_gated_delta_workspace(uint64_t tokens, uint64_t requests, 
     if (!bytes) return fail(NINFER_ERR_INVALID_ARGUMENT, "gated delta workspace: NULL bytes");
     const int st = check_sizes(tokens, requests, k_heads, v_heads, k_dim, v_dim);
     if (st) return st;
-    *bytes = 0;
+    // of calls with offsets, whichever dtype; a call without them needs none
+    const uint64_t chunks = tokens / kChunk + requests;
+    if (chunks * k_heads > 0x7fffffffull) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many tokens and key heads");
+    *bytes = chunks * (k_heads * 2 * rows_bytes_of(1, k_dim) + v_heads * kHeadBytes);
     return NINFER_OK;
 }
 
@@ -331,8 +714,8 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     for (const void *q : {(const void *)a.log_decay, (const void *)a.beta, (const void *)a.state_slots, (const void *)a.offsets,
                           (const void *)a.lengths, (const void *)a.status})
         if (!aligned(q, 4)) return fail(NINFER_ERR_ALIGNMENT, "gated delta: decays, betas and index arrays must be 4-byte aligned");
-    uint64_t need;
-    st = ninfer_gated_delta_workspace(a.tokens, a.requests, a.k_heads, a.v_heads, a.k_dim, a.v_dim, &need);
+    uint64_t need = 0;
+    if (a.offsets) st = ninfer_gated_delta_workspace(a.tokens, a.requests, a.k_heads, a.v_heads, a.k_dim, a.v_dim, &need);
     if (st) return st;
     if (need && !workspace) return fail(NINFER_ERR_INVALID_ARGUMENT, "gated delta: NULL workspace");
     if (workspace_bytes < need) return fail(NINFER_ERR_SIZE_MISMATCH, "gated delta: workspace of %llu bytes, %llu needed", (unsigned long long)workspace_bytes,
@@ -365,7 +748,23 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
                                           : (small ? step_kernel<32, 8> : step_kernel<32, 16>);
         return launch_dependent("gated delta", kernel, dim3(blocks), dim3(kStepThreads), 0, s, p);
     }
-    if (!grid(kRunColumns, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
-    const auto kernel = a.k_dim <= 64 ? run_kernel<4> : a.k_dim <= 128 ? run_kernel<8> : run_kernel<16>;
-    return launch_dependent("gated delta", kernel, dim3(blocks), dim3(kRunThreads), 0, s, p);
+    if (!grid(kColumns, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
+    const int terms = a.dtype == NINFER_F32 ? 2 : 1;
+    const uint64_t chunks = a.tokens / kChunk + a.requests;
+    ChunkParams c;
+    c.d = p;
+    c.wide = wide_of(a.k_dim);
+    c.rows_bytes = rows_bytes_of(terms, a.k_dim);
+    c.rows = static_cast<uint8_t *>(workspace);
+    c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
+    const uint32_t prepare_smem = terms * 2 * kChunk * (c.wide * 2 + 16);
+    const uint32_t chunk_smem = 2 * (prepare_smem + 4 * kChunk * (kChunk * 2 + 16) + kNumbers * 4 + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
+                                kChunkThreads / 32 * kChunk * 80;
+    const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
+    const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide) : chunk_kernel_of<1>(c.wide);
+    st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
+    if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(chunk), (int)chunk_smem);
+    if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kChunkThreads), prepare_smem, s, c);
+    if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3(kChunkThreads), chunk_smem, s, c);
+    return st;
 }

@@ -127,7 +127,9 @@ int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream stream);
  *   workspace: device, 256-byte aligned, at least ninfer_gated_delta_workspace() bytes (NULL where that is 0); its
  *     contents need no initial value and are not preserved.
  *   k_dim, v_dim: multiples of 8 up to 256; v_heads a multiple of k_heads; scale finite.
- * States and sums are fp32 (or 22-bit operands with fp32 sums); each request's results do not depend on the others of the call.
+ * States and sums are fp32. With offsets, a request's tokens go 32 at a time through the tensor cores: operands hold 22 bits of each
+ * value (q and k of 16-bit types all of theirs), but nothing under 2^-38 of the largest one of their column of the state
+ * among those tokens. Each request's results do not depend on the others of the call.
  * Errors: INVALID_ARGUMENT, SHAPE, SIZE_MISMATCH (workspace), ALIGNMENT, OVERFLOW, CUDA.
  */
 typedef struct {

@@ -64,11 +64,13 @@ def rotary(x, positions, frequencies, magnitude=1.0, interleaved=False, weight=N
     return z
 
 
-def gated_delta(q, k, v, log_decay, beta, state, offsets, slots, lengths=None, scale=1.0, norm_eps=None, unit=2.0 ** -24):
+def gated_delta(q, k, v, log_decay, beta, state, offsets, slots, lengths=None, scale=1.0, norm_eps=None, unit=2.0 ** -24,
+                floor=0.0):
     """q, k (tokens, k heads, dk), v (tokens, v heads, dv), state (slots, v heads, dk, dv) in fp64. Returns out (NaN in
     rows of no request), the states, and bounds for both of what roundings of `unit` can do: with E the 2-norm of a
     column's error, a step multiplies it by at most e^g (the rest of the step's map, I - beta k k^T, has norm 1 where
-    beta |k|^2 <= 2) and adds the roundings of the products with k, of u and of the update."""
+    beta |k|^2 <= 2) and adds the roundings of the products with k, of u and of the update. `floor`: what is lost of an operand
+    below this part of the largest one of its column so far (state, value or u), in each of k_dim + 64 products."""
     tokens, v_heads, dv = v.shape
     dk, group = k.shape[2], v_heads // k.shape[1]
     if norm_eps is not None:
@@ -82,7 +84,7 @@ def gated_delta(q, k, v, log_decay, beta, state, offsets, slots, lengths=None, s
             continue
         for h in range(v_heads):
             s = np.zeros((dk, dv)) if lengths is not None and lengths[r] <= 0 else state[slot, h]
-            err, terms = np.zeros(dv), dk + 16
+            err, terms, most = np.zeros(dv), dk + 16, np.abs(s).max(0)
             for t in range(b, e):
                 kt, qt, g = k[t, h // group], q[t, h // group], math.exp(log_decay[t, h])
                 s = g * s
@@ -90,9 +92,11 @@ def gated_delta(q, k, v, log_decay, beta, state, offsets, slots, lengths=None, s
                 u = beta[t, h] * (v[t, h] - s.T @ kt)
                 size = np.linalg.norm(kt)
                 s = s + np.outer(kt, u)
-                err = g * err + unit * (4 * np.linalg.norm(s, axis=0) + terms * abs(beta[t, h]) * size * (said + np.abs(v[t, h])))
+                most = np.maximum(most, np.maximum(np.abs(s).max(0), np.maximum(np.abs(v[t, h]), np.abs(u))))
+                lost = floor * (dk + 64) * most
+                err = g * err + lost + unit * (4 * np.linalg.norm(s, axis=0) + terms * abs(beta[t, h]) * size * (said + np.abs(v[t, h])))
                 out[t, h] = scale * (s.T @ qt)
-                out_bound[t, h] = abs(scale) * (np.linalg.norm(qt) * err + terms * unit * (np.abs(s).T @ np.abs(qt) + np.abs(u) * (np.abs(kt) @ np.abs(qt))))
+                out_bound[t, h] = abs(scale) * (np.linalg.norm(qt) * (err + lost) + terms * unit * (np.abs(s).T @ np.abs(qt) + np.abs(u) * (np.abs(kt) @ np.abs(qt))))
             state[slot, h], bound[slot, h] = s, err
     return out, state, out_bound, bound
 

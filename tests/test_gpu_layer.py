@@ -6,7 +6,8 @@ Bounds, fixed from the number formats (h: half a step of the output's format):
   products, weight + offset and the gate (expf within 2 units, sum, quotient, product) add at most 16: 40 2^-24.
 - rotary: the fraction of a turn is a float in [-1, 1] half turns (2^-25), sincospif within 2^-23, four roundings, and a
   norm within 20 2^-24: (|a| + |b|) magnitude 2^-20.
-- gated delta: oracle.layer.gated_delta's own bound, with roundings of 2^-24 (one or two sums a product: 2 units).
+- gated delta: oracle.layer.gated_delta's own bound, with roundings of 2^-23 (fp32 sums, operands of two binary16 terms), and for
+  several tokens a request binary16's least step, 2^-24, where a column's largest operand is at 2^13 and more: half of it is 2^-39.
 - sample: a weight is off by 2^-30 of itself and 2^-43 of the largest, sums are exact: the token is the oracle's wherever
   its nearest border is 2^-28 away. logprob: 2^-22 of itself and of 1, two fp32 functions.
 """
@@ -176,7 +177,7 @@ def run_delta(case, out_dtype="f32", offsets=None, slots=None, lengths=None, nor
     cut = np.arange(n + 1) if offsets is None else np.clip(offsets, 0, tokens)
     held = list(range(n)) if slots is None else slots
     want, state, out_bound, bound = ol.gated_delta(*(f64(case[x]) for x in ("q", "k", "v", "log_decay", "beta", "state")), cut, held,
-                                                   lengths, dk ** -0.5, norm_eps, unit)
+                                                   lengths, dk ** -0.5, norm_eps, unit, 2.0 ** -39 if offsets is not None else 0.0)
     out = torch.full((tokens, v_heads, dv), 5.0, device=DEV).to(TORCH[out_dtype])
     before = case["state"].clone()
     nt.ninfer_gated_delta(**case, offsets=None if offsets is None else i32(offsets), slots=None if slots is None else i32(slots),
@@ -222,7 +223,7 @@ def test_gated_delta_ragged(k_heads, v_heads, dk, dv, dtype, out):
 
 def test_gated_delta_offsets_of_any_value():
     rng = np.random.default_rng(7)
-    for offsets in ([-5, 3, 2, 9, 40], [0, 2 ** 31 - 1, 7, 7, -2 ** 31], [30, 30, 0, 5, 5]):
+    for offsets in ([-5, 3, 3, 9, 40], [0, 2 ** 31 - 1, 7, 7, -2 ** 31], [30, 30, 0, 5, 5], [9, 12, 4, 4, 9]):
         case = delta_case(rng, 12, 4, 1, 2, 64, 64, "bf16")
         run_delta(case, offsets=offsets)
 
