@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 //   O = scale (diag(e^G) Q S + P U),          P_ts = e^(G_t - G_s) q_t . k_s for s <= t, else 0
 //   S <- e^(G_last) S + K^T diag(e^(G_last - G)) U
 // T diag(beta) and P need no state: prepare_kernel makes them for all chunks at once, chunk_kernel goes through them.
-constexpr int kChunk = 32, kChunkThreads = 128, kColumns = 64;      // columns of a state a CTA, 16 a warp
+constexpr int kChunk = 32, kPrepareThreads = 128, kChunkThreads = 256, kColumns = 64;      // columns of a state a CTA
 constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
 enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
 constexpr uint64_t kTrianglesBytes = 4 * kChunk * kChunk * 2;       // T high and low, P high and low
@@ -239,10 +239,10 @@ __device__ __forceinline__ Range range_of(const ninfer_gated_delta_args &a, uint
 
 // A CTA for every chunk and key head. kTerms: binary16 terms of k and q, 1 where they have 16 bits themselves.
 template <int kTerms>
-__global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
     extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8
     __shared__ float dots[2][kChunk][kChunk + 1], scales[2][kChunk];
-    __shared__ __align__(16) float tri[kChunkThreads / 32][kChunk][kChunk + 4];
+    __shared__ __align__(16) float tri[kPrepareThreads / 32][kChunk][kChunk + 4];
     __shared__ uint32_t found;
     pdl_launch_dependents();
     pdl_wait();
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_con
     // the request that this chunk belongs to
     if (tid == 0) found = ~0u;
     __syncthreads();
-    for (uint32_t r = tid; r < (uint32_t)a.requests; r += kChunkThreads) {
+    for (uint32_t r = tid; r < (uint32_t)a.requests; r += kPrepareThreads) {
         const Range c = range_of(a, r);
         if (chunk - c.chunk < c.chunks) found = r;
     }
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_con
     uint8_t *rows = p.rows + (uint64_t)blockIdx.x * p.rows_bytes;
     const bool low_dim = lane * 8 < k_dim, in_row = lane * 8 < p.wide;
 #pragma unroll 4
-    for (uint32_t i = warp; i < 2 * kChunk; i += kChunkThreads / 32) {
+    for (uint32_t i = warp; i < 2 * kChunk; i += kPrepareThreads / 32) {
         const uint32_t t = i % kChunk, q = i / kChunk;
         float x[8] = {}, sum = 0.f, most = 0.f;
         if ((int32_t)t < count && low_dim) {
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_con
     // A warp a value head: lane s has column s of both triangles. Sums of log decays are whole multiples of 2^-40, so that
     // differences of them are exact however far the decays have gone; e^(+-2^15) is all the same.
     const uint32_t group = p.d.group.d;
-    for (uint32_t i = warp; i < group; i += kChunkThreads / 32) {
+    for (uint32_t i = warp; i < group; i += kPrepareThreads / 32) {
         const uint32_t head = key_head * group + i;
         const bool on = (int32_t)lane < count;
         const uint64_t token = first + (on ? lane : 0);
@@ -405,13 +405,15 @@ __global__ void __launch_bounds__(kChunkThreads) prepare_kernel(const __grid_con
     }
 }
 
-// 64 columns of one state a CTA, 16 a warp; the state stays in the accumulators' layout of mma, transposed (rows are columns of
-// S, columns k), which is the layout of the A operand of the products with K and Q, and U, made the same way, that of
-// the products with P and K. Every factor that is not exact in binary16 enters as two terms, scaled row by row.
-// kSteps: steps of 16 of k_dim; kTerms: terms of k and q.
+// 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
+// accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
+// products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
+// as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
+// outputs by tokens.
+// kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q.
 template <int kSteps, int kTerms>
 __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr uint32_t kRowStride = kSteps * 32 + 16, kTermBytes = 2 * kChunk * kRowStride, kTriStride = kChunk * 2 + 16;
+    constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride, kTriStride = kChunk * 2 + 16;
     constexpr uint32_t kTri = kTerms * kTermBytes, kNumbersAt = kTri + 4 * kChunk * kTriStride, kV = kNumbersAt + kNumbers * 4;
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_launch_dependents();
@@ -421,21 +423,29 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     if (part.none) return;
     const Range range = range_of(a, part.request);
     if (!range.chunks) return;
-    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pair = warp % 4, half = warp / 4;
+    const uint32_t k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
     const uint32_t es = a.dtype == NINFER_F32 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
-    const uint32_t base = smem_u32(smem), out_at = 2 * stage_bytes + warp * (kChunk * 80);
-    const uint32_t mine = part.column + warp * 16, column = mine + lane / 4;         // this thread's: column, column + 8
+    const uint32_t base = smem_u32(smem), out_at = 2 * stage_bytes + warp * (kChunk / 2 * 80), sums_at = 2 * stage_bytes + 8 * (kChunk / 2 * 80);
+    const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
     const uint32_t v_units = 16 / es, units_row = kColumns / v_units;
 
     auto fetch = [&](uint32_t j) {
         const uint32_t stage = base + j % 2 * stage_bytes;
         const uint64_t chunk = range.chunk + j;
         const uint8_t *rows = p.rows + (chunk * a.k_heads + part.key_head) * p.rows_bytes;
-        constexpr uint32_t kUnits = kSteps * 2;
-        for (uint32_t i = tid; i < kTerms * 2 * kChunk * kUnits; i += kChunkThreads)
-            copy16(stage + i / kUnits * kRowStride + i % kUnits * 16, rows + i * 16, true);
+        constexpr uint32_t kUnits = kSteps * 4;
+#pragma unroll
+        for (uint32_t i = 0; i < kTerms * 2 * kChunk * kUnits / kChunkThreads; ++i) {
+            const uint32_t u = i * kChunkThreads + tid;
+            copy16(stage + u / kUnits * kRowStride + u % kUnits * 16, rows + u * 16, true);
+        }
         const uint8_t *head = p.heads + (chunk * a.v_heads + part.head) * kHeadBytes;
-        for (uint32_t i = tid; i < 4 * kChunk * 4; i += kChunkThreads) copy16(stage + kTri + i / 4 * kTriStride + i % 4 * 16, head + i * 16, true);
+#pragma unroll
+        for (uint32_t i = 0; i < 4 * kChunk * 4 / kChunkThreads; ++i) {
+            const uint32_t u = i * kChunkThreads + tid;
+            copy16(stage + kTri + u / 4 * kTriStride + u % 4 * 16, head + u * 16, true);
+        }
         if (tid < kNumbers / 4) copy16(stage + kNumbersAt + tid * 16, head + kTrianglesBytes + tid * 16, true);
         const int32_t first = range.begin + (int32_t)j * kChunk;
         for (uint32_t i = tid; i < kChunk * units_row; i += kChunkThreads) {
@@ -447,18 +457,19 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         copies_commit();
     };
 
-    // s[n][e]: k = 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
+    // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
     float s[2 * kSteps][4];
     float *state = a.state + part.state;
+    const uint32_t k_first = half * kSteps * 16 + lane % 4 * 2;
 #pragma unroll
     for (int n = 0; n < 2 * kSteps; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t k = n * 8 + lane % 4 * 2 + e % 2, c = column + e / 2 * 8;
+            const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
             s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
         }
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
-    const uint32_t t_row = lane % 16, t_col = lane / 16 * 16;
+    const uint32_t t_row = lane % 16, t_col = lane / 16 * 16, half_col = half * kSteps * 32;
     fetch(0);
     for (uint32_t j = 0; j < range.chunks; ++j) {
         if (j + 1 < range.chunks) {
@@ -469,7 +480,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         const uint32_t stage = base + j % 2 * stage_bytes;
         const uint8_t *here = smem + j % 2 * stage_bytes;
         const float *numbers = reinterpret_cast<const float *>(here + kNumbersAt);
-        if (mine < v_dim) {         // whole warps
+        if (mine < v_dim) {         // whole pairs
             // S^T times K^T and Q^T: x[0..3] tokens of K, x[4..7] of Q
             float x[8][4] = {}, up0, up1;
             {
@@ -484,60 +495,69 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
             }
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
-                uint32_t high[4], low[4];
+                uint32_t high[4], low[4], y[4][4];
+                const uint32_t from = stage + b_row * kRowStride + half_col + k * 32 + b_col;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) load_matrices(y[n], from + n * 16 * kRowStride);
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     split(s[2 * k + h][0] * up0, s[2 * k + h][1] * up0, high[2 * h], low[2 * h]);
                     split(s[2 * k + h][2] * up1, s[2 * k + h][3] * up1, high[2 * h + 1], low[2 * h + 1]);
                 }
+                // each accumulator again after eight products
 #pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    uint32_t y[4];
-                    load_matrices(y, stage + (n * 16 + b_row) * kRowStride + k * 32 + b_col);
-                    mma(x[2 * n], high, y[0], y[1]);
-                    mma(x[2 * n + 1], high, y[2], y[3]);
-                    mma(x[2 * n], low, y[0], y[1]);
-                    mma(x[2 * n + 1], low, y[2], y[3]);
-                    if (kTerms == 2) {
-                        load_matrices(y, stage + kTermBytes + (n * 16 + b_row) * kRowStride + k * 32 + b_col);
-                        mma(x[2 * n], high, y[0], y[1]);
-                        mma(x[2 * n + 1], high, y[2], y[3]);
-                    }
+                for (int n = 0; n < 8; ++n) mma(x[n], high, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
+#pragma unroll
+                for (int n = 0; n < 8; ++n) mma(x[n], low, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
+                if (kTerms == 2) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) load_matrices(y[n], from + kTermBytes + n * 16 * kRowStride);
+#pragma unroll
+                    for (int n = 0; n < 8; ++n) mma(x[n], high, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
                 }
             }
-            const float down0 = inverse_power(up0), down1 = inverse_power(up1);
-            // W = V - e^G K S, in place; then U = T diag(beta) W
-            float m0 = 0.f, m1 = 0.f;
+            {
+                const float down0 = inverse_power(up0), down1 = inverse_power(up1);
+#pragma unroll
+                for (int n = 0; n < 8; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[n][e] *= e / 2 ? down1 : down0;
+            }
+            // the pair's halves: all of K S to both, of Q S the first 16 tokens to the first
+            float4 *sums = reinterpret_cast<float4 *>(smem + sums_at) + warp * 6 * 32 + lane;
+            const float4 *others = reinterpret_cast<const float4 *>(smem + sums_at) + (warp ^ 4) * 6 * 32 + lane;
+#pragma unroll
+            for (int n = 0; n < 4; ++n) sums[n * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+                sums[(4 + n) * 32] = half ? make_float4(x[4 + n][0], x[4 + n][1], x[4 + n][2], x[4 + n][3]) : make_float4(x[6 + n][0], x[6 + n][1], x[6 + n][2], x[6 + n][3]);
+            // meanwhile the values, and the numbers
+            float w[4][4];
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    w[n][e] = load1(here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (pair * 16 + lane / 4 + e / 2 * 8) * es, 0, a.dtype);
+            named_barrier(1 + pair, 64);
+            // W = V - e^G K S, then U = T diag(beta) W
+            float m0 = 0.f, m1 = 0.f, qs[2][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
                 const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfK + n * 8 + lane % 4 * 2);
+                const float4 o = others[n * 32];
+                const float oe[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint8_t *at = here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (warp * 16 + lane / 4 + e / 2 * 8) * es;
-                    const float v = load1(at, 0, a.dtype);
-                    x[n][e] = v - (e % 2 ? f.y : f.x) * (x[n][e] * (e / 2 ? down1 : down0));
-                }
-                m0 = fmaxf(m0, fmaxf(fabsf(x[n][0]), fabsf(x[n][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(x[n][2]), fabsf(x[n][3])));
+                for (int e = 0; e < 4; ++e) w[n][e] -= (e % 2 ? f.y : f.x) * (x[n][e] + oe[e]);
+                m0 = fmaxf(m0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
+                m1 = fmaxf(m1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
             }
-            // (rows of 32 tokens) times a triangle: y[n] += x times the lower triangle's rows 8 n .. 8 n + 7
-            auto triangle = [&](float (&y)[4][4], const uint32_t (&high)[2][4], const uint32_t (&low)[2][4], uint32_t which) {
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+            for (int n = 0; n < 2; ++n) {
+                const float4 o = others[(4 + n) * 32];
+                const float oe[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-                    for (int n = k; n < 2; ++n) {
-                        uint32_t b[4], c[4];
-                        const uint32_t from = stage + kTri + (which * kChunk + n * 16 + b_row) * kTriStride + k * 32 + b_col;
-                        load_matrices(b, from);
-                        load_matrices(c, from + kChunk * kTriStride);
-                        mma(y[2 * n], high[k], b[0], b[1]);
-                        mma(y[2 * n + 1], high[k], b[2], b[3]);
-                        mma(y[2 * n], high[k], c[0], c[1]);
-                        mma(y[2 * n + 1], high[k], c[2], c[3]);
-                        mma(y[2 * n], low[k], b[0], b[1]);
-                        mma(y[2 * n + 1], low[k], b[2], b[3]);
-                    }
-            };
+                for (int e = 0; e < 4; ++e) qs[n][e] = (half ? x[6 + n][e] : x[4 + n][e]) + oe[e];
+            }
             auto halves = [&](const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -547,15 +567,26 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                         split(y[2 * k + h][2] * p1, y[2 * k + h][3] * p1, high[k][2 * h + 1], low[k][2 * h + 1]);
                     }
             };
+            // 16 columns (of tokens s = 16 k ..) times 16 rows (tokens t = 16 n ..) of a triangle, given by its first of two terms
+            auto triangle = [&](float (&y0)[4], float (&y1)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], uint32_t which, int k, uint32_t n) {
+                uint32_t b[4], c[4];
+                const uint32_t from = stage + kTri + (which * kChunk + n * 16 + b_row) * kTriStride + k * 32 + b_col;
+                load_matrices(b, from);
+                load_matrices(c, from + kChunk * kTriStride);
+                mma(y0, high, b[0], b[1]);
+                mma(y1, high, b[2], b[3]);
+                mma(y0, high, c[0], c[1]);
+                mma(y1, high, c[2], c[3]);
+                mma(y0, low, b[0], b[1]);
+                mma(y1, low, b[2], b[3]);
+            };
             uint32_t high[2][4], low[2][4];
-            float u[4][4] = {}, o[4][4] = {}, w[4][4];
-#pragma unroll
-            for (int n = 0; n < 4; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) w[n][e] = x[n][e];
+            float u[4][4] = {};
             float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
             halves(w, p0, p1, high, low);
-            triangle(u, high, low, 0);
+            triangle(u[0], u[1], high[0], low[0], 0, 0, 0);
+            triangle(u[2], u[3], high[0], low[0], 0, 0, 1);
+            triangle(u[2], u[3], high[1], low[1], 0, 1, 1);
             const float of_t = numbers[kOfT], f0 = of_t * inverse_power(p0), f1 = of_t * inverse_power(p1);
             m0 = m1 = 0.f;
             float n0 = 0.f, n1 = 0.f;
@@ -572,61 +603,66 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                 n0 = fmaxf(n0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
                 n1 = fmaxf(n1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
             }
+            // P U for this warp's 16 tokens
             p0 = power_for(quad_max(m0));
             p1 = power_for(quad_max(m1));
             halves(u, p0, p1, high, low);
-            triangle(o, high, low, 2);
-            // out, through shared memory: 16 columns of each token
-            {
-                const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
-                const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2;
-#pragma unroll
-                for (int n = 0; n < 4; ++n) {
-                    const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfQ + n * 8 + lane % 4 * 2);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float y = (e % 2 ? f.y : f.x) * (x[4 + n][e] * (e / 2 ? down1 : down0)) + o[n][e] * (e / 2 ? g1 : g0);
-                        store1(smem + out_at + (n * 8 + lane % 4 * 2 + e % 2) * 80 + (lane / 4 + e / 2 * 8) * out_es, 0, a.out_dtype, y);
-                    }
-                }
-                __syncwarp();
-                const int32_t first = range.begin + (int32_t)j * kChunk;
-                const uint32_t units = out_es, per = 16 / out_es;       // 16-byte units of 16 columns, elements of one
-                for (uint32_t i = lane; i < kChunk * units; i += 32) {
-                    const uint32_t t = i / units, c = i % units;
-                    if (first + (int32_t)t < range.end && mine + c * per < v_dim) {
-                        const uint64_t at = ((uint64_t)(first + t) * a.v_heads + part.head) * v_dim + mine + c * per;
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * out_es) = *reinterpret_cast<const uint4 *>(smem + out_at + t * 80 + c * 16);
-                    }
-                }
-                __syncwarp();
-            }
+            float o[2][4] = {};
+            triangle(o[0], o[1], high[0], low[0], 2, 0, half);
+            if (half) triangle(o[0], o[1], high[1], low[1], 2, 1, 1);
+            const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
             // S^T = e^G_last S^T + (e^(G_last - G) U)^T K; the products begin at zero and are added rounded to nearest
             p0 = power_for(quad_max(n0));
             p1 = power_for(quad_max(n1));
             halves(w, p0, p1, high, low);
             const float left = numbers[kLeft], d0 = inverse_power(p0), d1 = inverse_power(p1);
+            constexpr int kAtOnce = kSteps % 2 ? 1 : 2;
 #pragma unroll
-            for (int n = 0; n < kSteps; ++n) {
-                float y[2][4] = {};
+            for (int n0_ = 0; n0_ < kSteps; n0_ += kAtOnce) {
+                float y[2 * kAtOnce][4] = {};
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
-                    uint32_t b[4];
-                    load_matrices_turned(b, stage + (k * 16 + t_row) * kRowStride + n * 32 + t_col);
-                    mma(y[0], high[k], b[0], b[1]);
-                    mma(y[1], high[k], b[2], b[3]);
-                    mma(y[0], low[k], b[0], b[1]);
-                    mma(y[1], low[k], b[2], b[3]);
+                    uint32_t b[kAtOnce][4];
+                    const uint32_t from = stage + (k * 16 + t_row) * kRowStride + half_col + n0_ * 32 + t_col;
+#pragma unroll
+                    for (int m = 0; m < kAtOnce; ++m) load_matrices_turned(b[m], from + m * 32);
+#pragma unroll
+                    for (int m = 0; m < 2 * kAtOnce; ++m) mma(y[m], high[k], b[m / 2][m % 2 * 2], b[m / 2][m % 2 * 2 + 1]);
+#pragma unroll
+                    for (int m = 0; m < 2 * kAtOnce; ++m) mma(y[m], low[k], b[m / 2][m % 2 * 2], b[m / 2][m % 2 * 2 + 1]);
                     if (kTerms == 2) {
-                        load_matrices_turned(b, stage + kTermBytes + (k * 16 + t_row) * kRowStride + n * 32 + t_col);
-                        mma(y[0], high[k], b[0], b[1]);
-                        mma(y[1], high[k], b[2], b[3]);
+#pragma unroll
+                        for (int m = 0; m < kAtOnce; ++m) load_matrices_turned(b[m], from + kTermBytes + m * 32);
+#pragma unroll
+                        for (int m = 0; m < 2 * kAtOnce; ++m) mma(y[m], high[k], b[m / 2][m % 2 * 2], b[m / 2][m % 2 * 2 + 1]);
                     }
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
+                for (int m = 0; m < 2 * kAtOnce; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[2 * n + h][e] = fmaf(y[h][e], e / 2 ? d1 : d0, left * s[2 * n + h][e]);
+                    for (int e = 0; e < 4; ++e) s[2 * n0_ + m][e] = fmaf(y[m][e], e / 2 ? d1 : d0, left * s[2 * n0_ + m][e]);
+            }
+            // out, through shared memory: 16 columns of this warp's 16 tokens
+            {
+                const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2;
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        store1(smem + out_at + (n * 8 + lane % 4 * 2 + e % 2) * 80 + (lane / 4 + e / 2 * 8) * out_es, 0, a.out_dtype,
+                               (e % 2 ? f.y : f.x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0));
+                }
+                __syncwarp();
+                const int32_t first = range.begin + (int32_t)(j * kChunk + half * 16);
+                const uint32_t per = 16 / out_es;       // elements of 16 bytes
+                for (uint32_t i = lane; i < 16 * out_es; i += 32) {
+                    const uint32_t t = i / out_es, c = i % out_es;
+                    if (first + (int32_t)t < range.end && mine + c * per < v_dim) {
+                        const uint64_t at = ((uint64_t)(first + t) * a.v_heads + part.head) * v_dim + mine + c * per;
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * out_es) = *reinterpret_cast<const uint4 *>(smem + out_at + t * 80 + c * 16);
+                    }
+                }
             }
         }
         __syncthreads();
@@ -635,14 +671,14 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     for (int n = 0; n < 2 * kSteps; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t k = n * 8 + lane % 4 * 2 + e % 2, c = column + e / 2 * 8;
+            const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
             if (k < k_dim && c < v_dim) state[k * v_dim + c] = s[n][e];
         }
 }
 
 template <int kTerms>
 auto chunk_kernel_of(uint32_t wide) {
-    return wide == 64 ? chunk_kernel<4, kTerms> : wide == 96 ? chunk_kernel<6, kTerms> : wide == 128 ? chunk_kernel<8, kTerms> : chunk_kernel<16, kTerms>;
+    return wide == 64 ? chunk_kernel<2, kTerms> : wide == 96 ? chunk_kernel<3, kTerms> : wide == 128 ? chunk_kernel<4, kTerms> : chunk_kernel<8, kTerms>;
 }
 
 // k_dim rounded up to what the kernel has instances for
@@ -759,12 +795,12 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
     const uint32_t prepare_smem = terms * 2 * kChunk * (c.wide * 2 + 16);
     const uint32_t chunk_smem = 2 * (prepare_smem + 4 * kChunk * (kChunk * 2 + 16) + kNumbers * 4 + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
-                                kChunkThreads / 32 * kChunk * 80;
+                                kChunkThreads / 32 * (kChunk / 2 * 80 + 6 * 32 * 16);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
     const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide) : chunk_kernel_of<1>(c.wide);
     st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
     if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(chunk), (int)chunk_smem);
-    if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kChunkThreads), prepare_smem, s, c);
+    if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kPrepareThreads), prepare_smem, s, c);
     if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3(kChunkThreads), chunk_smem, s, c);
     return st;
 }
