@@ -183,15 +183,15 @@ struct ChunkParams {
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 __device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t at) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
 // 16 bytes from global to shared memory, or zeros
 __device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
@@ -243,6 +243,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8
     __shared__ float dots[2][kChunk][kChunk + 1], scales[2][kChunk];
     __shared__ __align__(16) float tri[kPrepareThreads / 32][kChunk][kChunk + 4];
+    __shared__ float4 sums[kPrepareThreads / 32][kChunk];      // the log decays' sums in two floats, beta
     __shared__ uint32_t found;
     pdl_launch_dependents();
     pdl_wait();
@@ -264,38 +265,44 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     // rows of K, then of Q: their norms, and their elements times a power of two
     const uint32_t stride = p.wide * 2 + 16, term_bytes = 2 * kChunk * stride;
     uint8_t *rows = p.rows + (uint64_t)blockIdx.x * p.rows_bytes;
-    const bool low_dim = lane * 8 < k_dim, in_row = lane * 8 < p.wide;
+    // 16 lanes a row where it has no more than 128 elements
+    const uint32_t row_lanes = p.wide <= 128 ? 16 : 32, at_once = kPrepareThreads / row_lanes, e0 = tid % row_lanes * 8;
+    const bool low_dim = e0 < k_dim, in_row = e0 < p.wide;
 #pragma unroll 4
-    for (uint32_t i = warp; i < 2 * kChunk; i += kPrepareThreads / 32) {
+    for (uint32_t i = tid / row_lanes; i < 2 * kChunk; i += at_once) {
         const uint32_t t = i % kChunk, q = i / kChunk;
         float x[8] = {}, sum = 0.f, most = 0.f;
         if ((int32_t)t < count && low_dim) {
             const uint64_t token = first + t;
-            if (q) load8(a.q, token * a.q_token_stride + key_head * a.q_head_stride + lane * 8, a.dtype, x);
-            else load8(a.k, token * a.k_token_stride + key_head * a.k_head_stride + lane * 8, a.dtype, x);
+            const uint64_t at = q ? token * a.q_token_stride + key_head * a.q_head_stride : token * a.k_token_stride + key_head * a.k_head_stride;
+            load8(q ? a.q : a.k, at + e0, a.dtype, x);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             sum = fmaf(x[e], x[e], sum);
             most = fmaxf(most, fabsf(x[e]));
         }
+        if (row_lanes == 32) {
+            sum += __shfl_xor_sync(~0u, sum, 16);
+            most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
+        }
 #pragma unroll
-        for (int e = 16; e; e /= 2) {
+        for (int e = 8; e; e /= 2) {
             sum += __shfl_xor_sync(~0u, sum, e);
             most = fmaxf(most, __shfl_xor_sync(~0u, most, e));
         }
         const float up = power_for(most);
-        if (lane == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
+        if (e0 == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
         uint32_t high[4], low[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) split(x[2 * e] * up, x[2 * e + 1] * up, high[e], low[e]);
         if (in_row) {
             const uint4 h = make_uint4(high[0], high[1], high[2], high[3]), l = make_uint4(low[0], low[1], low[2], low[3]);
-            *reinterpret_cast<uint4 *>(smem + i * stride + lane * 16) = h;
-            *reinterpret_cast<uint4 *>(rows + (i * p.wide + lane * 8) * 2) = h;
+            *reinterpret_cast<uint4 *>(smem + i * stride + e0 * 2) = h;
+            *reinterpret_cast<uint4 *>(rows + (i * p.wide + e0) * 2) = h;
             if (kTerms == 2) {
-                *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + lane * 16) = l;
-                *reinterpret_cast<uint4 *>(rows + ((2 * kChunk + i) * p.wide + lane * 8) * 2) = l;
+                *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + e0 * 2) = l;
+                *reinterpret_cast<uint4 *>(rows + ((2 * kChunk + i) * p.wide + e0) * 2) = l;
             }
         }
     }
@@ -333,29 +340,36 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
             }
     }
     __syncthreads();
-    // A warp a value head: lane s has column s of both triangles. Sums of log decays are whole multiples of 2^-40, so that
-    // differences of them are exact however far the decays have gone; e^(+-2^15) is all the same.
+    // A warp a value head: lane s has column s of both triangles. Log decays are added up in units of ln 2 and in two floats, so that
+    // differences of far sums are as exact as those of near ones; 2^(+-2^15) is all the same.
     const uint32_t group = p.d.group.d;
     for (uint32_t i = warp; i < group; i += kPrepareThreads / 32) {
         const uint32_t head = key_head * group + i;
         const bool on = (int32_t)lane < count;
         const uint64_t token = first + (on ? lane : 0);
         const float g = on ? a.log_decay[token * a.decay_stride + head] : 0.f, beta = on ? a.beta[token * a.beta_stride + head] : 0.f;
-        long long sum = __float2ll_rn(fminf(fmaxf(g, -32768.f), 32768.f) * 0x1p40f);
+        const float bound = fminf(fmaxf(g, -32768.f), 32768.f);
+        float high = bound * 1.44269504f, low = fmaf(bound, 1.44269504f, -high) + bound * 1.92596299e-8f;
 #pragma unroll
         for (int k = 1; k < 32; k *= 2) {
-            const long long u = __shfl_up_sync(~0u, sum, k);
-            if (lane >= (uint32_t)k) sum += u;
+            const float u = __shfl_up_sync(~0u, high, k), v = __shfl_up_sync(~0u, low, k);
+            if (lane >= (uint32_t)k) {
+                const float sum = high + u, w = sum - high;
+                low += v + ((high - (sum - w)) + (u - w));
+                high = sum;
+            }
         }
-        const long long last = __shfl_sync(~0u, sum, 31);
+        const float last_high = __shfl_sync(~0u, high, 31), last_low = __shfl_sync(~0u, low, 31);
         const uint32_t bad = __ballot_sync(~0u, g != g);
         const float poison = bad & (~0u >> (31 - lane)) ? NAN : 1.f, spoilt = bad ? NAN : 1.f;
+        sums[warp][lane] = make_float4(high, low, beta, 0.f);
+        __syncwarp();
         float pp[kChunk], tt[kChunk], most_p = 0.f, most_t = 0.f;
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) {
-            const long long gt = __shfl_sync(~0u, sum, t);
-            const float fade = (int)lane <= t ? expf(__ll2float_rn(gt - sum) * 0x1p-40f) : 0.f, bt = __shfl_sync(~0u, beta, t);
-            tri[warp][t][lane] = (int)lane < t ? bt * fade * dots[0][t][lane] : 0.f;
+            const float4 at = sums[warp][t];
+            const float fade = exp2f((at.x - high) + (at.y - low));
+            tri[warp][t][lane] = (int)lane < t ? at.z * fade * dots[0][t][lane] : 0.f;
             pp[t] = (int)lane <= t ? fade * dots[1][t][lane] : 0.f;
             most_p = fmaxf(most_p, fabsf(pp[t]));
         }
@@ -394,16 +408,19 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
             out[(3 * kChunk + t) * kChunk + lane] = __float2half_rn(y - __half2float(yh));
         }
         float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
-        const float fade = expf(__ll2float_rn(sum) * 0x1p-40f) * poison;
+        const float fade = exp2f(high + low) * poison;
         numbers[kOfK + lane] = fade * scales[0][lane];
         numbers[kOfQ + lane] = a.scale * fade * scales[1][lane];
-        numbers[kOfU + lane] = expf(__ll2float_rn(last - sum) * 0x1p-40f) * scales[0][lane];
+        numbers[kOfU + lane] = exp2f((last_high - high) + (last_low - low)) * scales[0][lane];
         if (lane < 4) {
-            const float x = lane == 0 ? expf(__ll2float_rn(last) * 0x1p-40f) * spoilt : lane == 1 ? inverse_power(up_t) : lane == 2 ? a.scale * inverse_power(up_p) : 0.f;
+            const float x = lane == 0 ? exp2f(last_high + last_low) * spoilt : lane == 1 ? inverse_power(up_t) : lane == 2 ? a.scale * inverse_power(up_p) : 0.f;
             numbers[kLeft + lane] = x;
         }
     }
 }
+
+// Chunks in shared memory at once: what fits an SM.
+__host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
 
 // 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
@@ -414,7 +431,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 template <int kSteps, int kTerms>
 __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride, kTriStride = kChunk * 2 + 16;
-    constexpr uint32_t kTri = kTerms * kTermBytes, kNumbersAt = kTri + 4 * kChunk * kTriStride, kV = kNumbersAt + kNumbers * 4;
+    constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + 4 * kChunk * kTriStride, kV = kNumbersAt + kNumbers * 4;
     extern __shared__ __align__(16) uint8_t smem[];
     pdl_launch_dependents();
     pdl_wait();
@@ -425,13 +442,15 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     if (!range.chunks) return;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pair = warp % 4, half = warp / 4;
     const uint32_t k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
-    const uint32_t es = a.dtype == NINFER_F32 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
-    const uint32_t base = smem_u32(smem), out_at = 2 * stage_bytes + warp * (kChunk / 2 * 80), sums_at = 2 * stage_bytes + 8 * (kChunk / 2 * 80);
+    const bool bf16 = a.dtype == NINFER_BF16;
+    constexpr uint32_t es = kTerms == 2 ? 4 : 2;
+    const uint32_t v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
+    const uint32_t base = smem_u32(smem), out_at = kStages * stage_bytes + warp * (kChunk / 2 * 80), sums_at = kStages * stage_bytes + 8 * (kChunk / 2 * 80);
     const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
     const uint32_t v_units = 16 / es, units_row = kColumns / v_units;
 
     auto fetch = [&](uint32_t j) {
-        const uint32_t stage = base + j % 2 * stage_bytes;
+        const uint32_t stage = base + j % kStages * stage_bytes;
         const uint64_t chunk = range.chunk + j;
         const uint8_t *rows = p.rows + (chunk * a.k_heads + part.key_head) * p.rows_bytes;
         constexpr uint32_t kUnits = kSteps * 4;
@@ -471,27 +490,27 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
     const uint32_t t_row = lane % 16, t_col = lane / 16 * 16, half_col = half * kSteps * 32;
     fetch(0);
+    if (kStages == 3 && range.chunks > 1) fetch(1);
     for (uint32_t j = 0; j < range.chunks; ++j) {
-        if (j + 1 < range.chunks) {
-            fetch(j + 1);
-            copies_wait<1>();
-        } else copies_wait<0>();
-        __syncthreads();
-        const uint32_t stage = base + j % 2 * stage_bytes;
-        const uint8_t *here = smem + j % 2 * stage_bytes;
+        if (kStages == 3 && j + 1 < range.chunks) copies_wait<1>();
+        else copies_wait<0>();
+        __syncthreads();            // chunk j is there, and the one before it done with
+        if (j + kStages - 1 < range.chunks) fetch(j + kStages - 1);
+        const uint32_t stage = base + j % kStages * stage_bytes;
+        const uint8_t *here = smem + j % kStages * stage_bytes;
         const float *numbers = reinterpret_cast<const float *>(here + kNumbersAt);
         if (mine < v_dim) {         // whole pairs
             // S^T times K^T and Q^T: x[0..3] tokens of K, x[4..7] of Q
             float x[8][4] = {}, up0, up1;
             {
-                float m0 = 0.f, m1 = 0.f;
+                float m[4] = {};
 #pragma unroll
                 for (int n = 0; n < 2 * kSteps; ++n) {
-                    m0 = fmaxf(m0, fmaxf(fabsf(s[n][0]), fabsf(s[n][1])));
-                    m1 = fmaxf(m1, fmaxf(fabsf(s[n][2]), fabsf(s[n][3])));
+                    m[n % 2] = fmaxf(m[n % 2], fmaxf(fabsf(s[n][0]), fabsf(s[n][1])));
+                    m[2 + n % 2] = fmaxf(m[2 + n % 2], fmaxf(fabsf(s[n][2]), fabsf(s[n][3])));
                 }
-                up0 = power_for(quad_max(m0));
-                up1 = power_for(quad_max(m1));
+                up0 = power_for(quad_max(fmaxf(m[0], m[1])));
+                up1 = power_for(quad_max(fmaxf(m[2], m[3])));
             }
 #pragma unroll
             for (int k = 0; k < kSteps; ++k) {
@@ -536,8 +555,14 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
 #pragma unroll
             for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[n][e] = load1(here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (pair * 16 + lane / 4 + e / 2 * 8) * es, 0, a.dtype);
+                for (int e = 0; e < 4; ++e) {
+                    const uint8_t *at = here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (pair * 16 + lane / 4 + e / 2 * 8) * es;
+                    if (kTerms == 2) w[n][e] = *reinterpret_cast<const float *>(at);
+                    else {
+                        const uint16_t v = *reinterpret_cast<const uint16_t *>(at);
+                        w[n][e] = bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+                    }
+                }
             named_barrier(1 + pair, 64);
             // W = V - e^G K S, then U = T diag(beta) W
             float m0 = 0.f, m1 = 0.f, qs[2][4];
@@ -567,26 +592,34 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                         split(y[2 * k + h][2] * p1, y[2 * k + h][3] * p1, high[k][2 * h + 1], low[k][2 * h + 1]);
                     }
             };
-            // 16 columns (of tokens s = 16 k ..) times 16 rows (tokens t = 16 n ..) of a triangle, given by its first of two terms
-            auto triangle = [&](float (&y0)[4], float (&y1)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], uint32_t which, int k, uint32_t n) {
-                uint32_t b[4], c[4];
+            // 16 tokens t = 16 n .. of a triangle, given by its first of two terms, as the B operand: columns s = 16 k ..
+            auto triangle = [&](uint32_t (&b)[2][4], uint32_t which, int k, uint32_t n) {
                 const uint32_t from = stage + kTri + (which * kChunk + n * 16 + b_row) * kTriStride + k * 32 + b_col;
-                load_matrices(b, from);
-                load_matrices(c, from + kChunk * kTriStride);
-                mma(y0, high, b[0], b[1]);
-                mma(y1, high, b[2], b[3]);
-                mma(y0, high, c[0], c[1]);
-                mma(y1, high, c[2], c[3]);
-                mma(y0, low, b[0], b[1]);
-                mma(y1, low, b[2], b[3]);
+                load_matrices(b[0], from);
+                load_matrices(b[1], from + kChunk * kTriStride);
+            };
+            auto times = [&](float (&y)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], const uint32_t (&b)[2][4], int i, int term) {
+                mma(y, term == 2 ? low : high, b[term == 1][2 * i], b[term == 1][2 * i + 1]);
             };
             uint32_t high[2][4], low[2][4];
             float u[4][4] = {};
             float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
             halves(w, p0, p1, high, low);
-            triangle(u[0], u[1], high[0], low[0], 0, 0, 0);
-            triangle(u[2], u[3], high[0], low[0], 0, 0, 1);
-            triangle(u[2], u[3], high[1], low[1], 0, 1, 1);
+            uint32_t t00[2][4], t01[2][4], t11[2][4];
+            triangle(t00, 0, 0, 0);
+            triangle(t01, 0, 0, 1);
+            triangle(t11, 0, 1, 1);
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    times(u[i], high[0], low[0], t00, i, term);
+                    times(u[2 + i], high[0], low[0], t01, i, term);
+                }
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) times(u[2 + i], high[1], low[1], t11, i, term);
             const float of_t = numbers[kOfT], f0 = of_t * inverse_power(p0), f1 = of_t * inverse_power(p1);
             m0 = m1 = 0.f;
             float n0 = 0.f, n1 = 0.f;
@@ -608,8 +641,18 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
             p1 = power_for(quad_max(m1));
             halves(u, p0, p1, high, low);
             float o[2][4] = {};
-            triangle(o[0], o[1], high[0], low[0], 2, 0, half);
-            if (half) triangle(o[0], o[1], high[1], low[1], 2, 1, 1);
+            triangle(t00, 2, 0, half);
+            triangle(t11, 2, 1, 1);
+#pragma unroll
+            for (int term = 0; term < 3; ++term)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) times(o[i], high[0], low[0], t00, i, term);
+            if (half) {
+#pragma unroll
+                for (int term = 0; term < 3; ++term)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) times(o[i], high[1], low[1], t11, i, term);
+            }
             const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
             // S^T = e^G_last S^T + (e^(G_last - G) U)^T K; the products begin at zero and are added rounded to nearest
             p0 = power_for(quad_max(n0));
@@ -649,9 +692,20 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                 for (int n = 0; n < 2; ++n) {
                     const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        store1(smem + out_at + (n * 8 + lane % 4 * 2 + e % 2) * 80 + (lane / 4 + e / 2 * 8) * out_es, 0, a.out_dtype,
-                               (e % 2 ? f.y : f.x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0));
+                    for (int e = 0; e < 4; ++e) o[n][e] = (e % 2 ? f.y : f.x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0);
+                }
+                uint8_t *to = smem + out_at + lane % 4 * 160 + lane / 4 * out_es;
+                if (a.out_dtype == NINFER_F32) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(to + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 32) = o[i / 4][i % 4];
+                } else {
+                    const bool to_bf16 = a.out_dtype == NINFER_BF16;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float y = o[i / 4][i % 4];
+                        *reinterpret_cast<uint16_t *>(to + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 16) =
+                            to_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+                    }
                 }
                 __syncwarp();
                 const int32_t first = range.begin + (int32_t)(j * kChunk + half * 16);
@@ -665,7 +719,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                 }
             }
         }
-        __syncthreads();
     }
 #pragma unroll
     for (int n = 0; n < 2 * kSteps; ++n)
@@ -794,7 +847,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     c.rows = static_cast<uint8_t *>(workspace);
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
     const uint32_t prepare_smem = terms * 2 * kChunk * (c.wide * 2 + 16);
-    const uint32_t chunk_smem = 2 * (prepare_smem + 4 * kChunk * (kChunk * 2 + 16) + kNumbers * 4 + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
+    const uint32_t chunk_smem = stages_of(c.wide, terms) * (prepare_smem + 4 * kChunk * (kChunk * 2 + 16) + kNumbers * 4 + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
                                 kChunkThreads / 32 * (kChunk / 2 * 80 + 6 * 32 * 16);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
     const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide) : chunk_kernel_of<1>(c.wide);
