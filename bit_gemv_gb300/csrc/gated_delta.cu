@@ -170,16 +170,19 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 constexpr int kChunk = 32, kPrepareThreads = 128, kChunkThreads = 256, kColumns = 64;      // columns of a state a CTA
 constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
 enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
-constexpr uint64_t kTrianglesBytes = 4 * kChunk * kChunk * 2;       // T high and low, P high and low
-constexpr uint64_t kHeadBytes = kTrianglesBytes + kNumbers * 4;
+constexpr uint32_t kTriStride = kChunk * 2 + 16, kTrianglesBytes = 4 * kChunk * kTriStride;     // T high and low, P high and low
+constexpr uint32_t kHeadBytes = kTrianglesBytes + kNumbers * 4;
 
 // What lies in the workspace: for every chunk and key head K and Q as binary16 (f32: two terms each), [term][K, Q][token][k_dim];
-// then for every chunk and value head the triangles, [which][t][s], and the numbers.
+// then for every chunk and value head the triangles, [which][t][s], and the numbers. Rows are 16 bytes longer than their elements, as
+// they are to lie in shared memory (eight of them in different banks), so that one copy moves a chunk's.
 struct ChunkParams {
     DeltaParams d;
     uint8_t *rows, *heads;
     uint64_t rows_bytes;        // of a chunk and key head
     uint32_t wide;              // k_dim rounded up to the kernel's steps of 16
+    uint32_t *error;            // the library's error word
+    long long wait_limit;
 };
 
 __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -193,14 +196,15 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
 __device__ __forceinline__ void load_matrices_turned(uint32_t (&r)[4], uint32_t at) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at));
 }
-// 16 bytes from global to shared memory, or zeros
-__device__ __forceinline__ void copy16(uint32_t to, const void *from, bool on) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+__device__ __forceinline__ void store_matrices_turned(uint32_t at, const uint32_t (&r)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
 }
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeftOpen>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kLeftOpen) : "memory");
+// 16 bytes from global to shared memory; an arrival at a barrier once the thread's copies so far have landed.
+__device__ __forceinline__ void copy16(uint32_t to, const void *from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
 // Two floats as two binary16 terms each: 22 bits of every value from 2^-14 of 1 on.
@@ -299,10 +303,10 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
         if (in_row) {
             const uint4 h = make_uint4(high[0], high[1], high[2], high[3]), l = make_uint4(low[0], low[1], low[2], low[3]);
             *reinterpret_cast<uint4 *>(smem + i * stride + e0 * 2) = h;
-            *reinterpret_cast<uint4 *>(rows + (i * p.wide + e0) * 2) = h;
+            *reinterpret_cast<uint4 *>(rows + i * stride + e0 * 2) = h;
             if (kTerms == 2) {
                 *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + e0 * 2) = l;
-                *reinterpret_cast<uint4 *>(rows + ((2 * kChunk + i) * p.wide + e0) * 2) = l;
+                *reinterpret_cast<uint4 *>(rows + term_bytes + i * stride + e0 * 2) = l;
             }
         }
     }
@@ -402,10 +406,11 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
         for (int t = 0; t < kChunk; ++t) {
             const float x = tt[t] * up_t, y = pp[t] * up_p;
             const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
-            out[t * kChunk + lane] = xh;
-            out[(kChunk + t) * kChunk + lane] = __float2half_rn(x - __half2float(xh));
-            out[(2 * kChunk + t) * kChunk + lane] = yh;
-            out[(3 * kChunk + t) * kChunk + lane] = __float2half_rn(y - __half2float(yh));
+            constexpr uint32_t kRow = kTriStride / 2;
+            out[t * kRow + lane] = xh;
+            out[(kChunk + t) * kRow + lane] = __float2half_rn(x - __half2float(xh));
+            out[(2 * kChunk + t) * kRow + lane] = yh;
+            out[(3 * kChunk + t) * kRow + lane] = __float2half_rn(y - __half2float(yh));
         }
         float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
         const float fade = exp2f(high + low) * poison;
@@ -419,20 +424,24 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     }
 }
 
-// Chunks in shared memory at once: what fits an SM.
+// Chunks in shared memory at once, and buffers for the sums: what fits an SM.
 __host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
+__host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 1 : 2; }
 
 // 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
 // products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
 // as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
-// outputs by tokens.
+// outputs by tokens. The first warp keeps the next chunks coming (bulk copies, mbarriers; a ninth warp for it would take a third of the
+// registers); nothing else holds pairs together, so that of two pairs on a scheduler one multiplies while the other splits and scales.
 // kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q.
 template <int kSteps, int kTerms>
 __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
-    constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride, kTriStride = kChunk * 2 + 16;
-    constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + 4 * kChunk * kTriStride, kV = kNumbersAt + kNumbers * 4;
+    constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride;
+    constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + kTrianglesBytes, kV = kTri + kHeadBytes;
+    constexpr uint32_t kSums = sums_of(kSteps * 32, kTerms), es = kTerms == 2 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
     extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_gated_delta_args &a = p.d.a;
@@ -440,41 +449,21 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     if (part.none) return;
     const Range range = range_of(a, part.request);
     if (!range.chunks) return;
-    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, pair = warp % 4, half = warp / 4;
-    const uint32_t k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
+    const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
+    const uint32_t base = smem_u32(smem), columns = min(v_dim - part.column, (uint32_t)kColumns);
+    if (tid == 0) {
+        for (uint32_t i = 0; i < kStages; ++i) {
+            mbar_init(smem_u32(&full[i]), 1 + 32);          // the bulk copies, and each lane's of the values
+            mbar_init(smem_u32(&empty[i]), (columns + 15) / 16 * 2);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    const uint32_t pair = warp / 2, half = warp % 2;
     const bool bf16 = a.dtype == NINFER_BF16;
-    constexpr uint32_t es = kTerms == 2 ? 4 : 2;
-    const uint32_t v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
-    const uint32_t base = smem_u32(smem), out_at = kStages * stage_bytes + warp * (kChunk / 2 * 80), sums_at = kStages * stage_bytes + 8 * (kChunk / 2 * 80);
+    const uint32_t out_at = kStages * stage_bytes + warp * (kChunk / 2 * 80), sums_at = kStages * stage_bytes + 8 * (kChunk / 2 * 80);
     const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
-    const uint32_t v_units = 16 / es, units_row = kColumns / v_units;
-
-    auto fetch = [&](uint32_t j) {
-        const uint32_t stage = base + j % kStages * stage_bytes;
-        const uint64_t chunk = range.chunk + j;
-        const uint8_t *rows = p.rows + (chunk * a.k_heads + part.key_head) * p.rows_bytes;
-        constexpr uint32_t kUnits = kSteps * 4;
-#pragma unroll
-        for (uint32_t i = 0; i < kTerms * 2 * kChunk * kUnits / kChunkThreads; ++i) {
-            const uint32_t u = i * kChunkThreads + tid;
-            copy16(stage + u / kUnits * kRowStride + u % kUnits * 16, rows + u * 16, true);
-        }
-        const uint8_t *head = p.heads + (chunk * a.v_heads + part.head) * kHeadBytes;
-#pragma unroll
-        for (uint32_t i = 0; i < 4 * kChunk * 4 / kChunkThreads; ++i) {
-            const uint32_t u = i * kChunkThreads + tid;
-            copy16(stage + kTri + u / 4 * kTriStride + u % 4 * 16, head + u * 16, true);
-        }
-        if (tid < kNumbers / 4) copy16(stage + kNumbersAt + tid * 16, head + kTrianglesBytes + tid * 16, true);
-        const int32_t first = range.begin + (int32_t)j * kChunk;
-        for (uint32_t i = tid; i < kChunk * units_row; i += kChunkThreads) {
-            const uint32_t t = i / units_row, u = i % units_row, c = part.column + u * v_units;
-            const bool on = first + (int32_t)t < range.end && c < v_dim;
-            const uint64_t token = on ? first + t : 0;
-            copy16(stage + kV + t * v_stride + u * 16, static_cast<const uint8_t *>(a.v) + (token * a.v_token_stride + part.head * a.v_head_stride + (on ? c : 0)) * es, on);
-        }
-        copies_commit();
-    };
+    if (mine >= v_dim) return;      // whole pairs
 
     // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
     float s[2 * kSteps][4];
@@ -489,17 +478,51 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         }
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
     const uint32_t t_row = lane % 16, t_col = lane / 16 * 16, half_col = half * kSteps * 32;
-    fetch(0);
-    if (kStages == 3 && range.chunks > 1) fetch(1);
+    uint32_t sent = 0;
+    bool good = true;       // once a wait has run out, none is made and nothing is stored
+    // The first warp's: chunk j into its stage, which all warps have left. Lanes whose 16 bytes of values lie past the last column copy
+    // the last ones there are; what they get is part of no result.
+    constexpr uint32_t kUnits = kColumns * es / 16;
+    constexpr int32_t kRowsAtOnce = 32 / kUnits;
+    const uint8_t *next_rows = p.rows + ((uint64_t)range.chunk * a.k_heads + part.key_head) * p.rows_bytes;
+    const uint8_t *next_head = p.heads + ((uint64_t)range.chunk * a.v_heads + part.head) * kHeadBytes;
+    const uint8_t *next_v = static_cast<const uint8_t *>(a.v) +
+                            ((uint64_t)(range.begin + lane / kUnits) * a.v_token_stride + part.head * a.v_head_stride + part.column) * es + min(lane % kUnits, columns * es / 16 - 1) * 16;
+    const uint64_t rows_step = a.k_heads * p.rows_bytes, head_step = a.v_heads * kHeadBytes, v_step = kRowsAtOnce * a.v_token_stride * es;
+    auto send = [&](uint32_t j) {
+        if (j >= kStages) good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&empty[j % kStages]), (j / kStages - 1) & 1, p.error, p.wait_limit)));
+        if (!good) return;
+        const uint32_t stage = base + j % kStages * stage_bytes, bar = smem_u32(&full[j % kStages]);
+        const int32_t left = range.end - range.begin - (int32_t)j * kChunk - (int32_t)(lane / kUnits);      // tokens from this lane's first on
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, kTri + kHeadBytes);
+            bulk_g2s(stage, next_rows, kTri, bar);
+            bulk_g2s(stage + kTri, next_head, kHeadBytes, bar);
+        }
+        next_rows += rows_step;
+        next_head += head_step;
+        // the values, 16 bytes at a time (a bulk copy a row took 80 cycles to issue, each)
+        const uint32_t to = stage + kV + lane / kUnits * v_stride + lane % kUnits * 16;
+        const uint8_t *from = next_v;
+        if (left >= kChunk) {
+#pragma unroll
+            for (int32_t i = 0; i < kChunk / kRowsAtOnce; ++i, from += v_step) copy16(to + i * kRowsAtOnce * v_stride, from);
+        } else {
+            for (int32_t i = 0; i * kRowsAtOnce < left; ++i, from += v_step) copy16(to + i * kRowsAtOnce * v_stride, from);
+        }
+        next_v += v_step * (kChunk / kRowsAtOnce);
+        copies_arrive(bar);
+        sent = j + 1;
+    };
+    if (warp == 0)
+        for (uint32_t j = 0; j < min(kStages - 1, range.chunks); ++j) send(j);
     for (uint32_t j = 0; j < range.chunks; ++j) {
-        if (kStages == 3 && j + 1 < range.chunks) copies_wait<1>();
-        else copies_wait<0>();
-        __syncthreads();            // chunk j is there, and the one before it done with
-        if (j + kStages - 1 < range.chunks) fetch(j + kStages - 1);
+        good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit)));
         const uint32_t stage = base + j % kStages * stage_bytes;
         const uint8_t *here = smem + j % kStages * stage_bytes;
         const float *numbers = reinterpret_cast<const float *>(here + kNumbersAt);
-        if (mine < v_dim) {         // whole pairs
+        const int32_t first = range.begin + (int32_t)j * kChunk, count = min(range.end - first, kChunk);
+        {
             // S^T times K^T and Q^T: x[0..3] tokens of K, x[4..7] of Q
             float x[8][4] = {}, up0, up1;
             {
@@ -535,6 +558,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                     for (int n = 0; n < 8; ++n) mma(x[n], high, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
                 }
             }
+            if (warp == 0 && j + kStages - 1 < range.chunks) send(j + kStages - 1);
             {
                 const float down0 = inverse_power(up0), down1 = inverse_power(up1);
 #pragma unroll
@@ -542,9 +566,10 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[n][e] *= e / 2 ? down1 : down0;
             }
-            // the pair's halves: all of K S to both, of Q S the first 16 tokens to the first
-            float4 *sums = reinterpret_cast<float4 *>(smem + sums_at) + warp * 6 * 32 + lane;
-            const float4 *others = reinterpret_cast<const float4 *>(smem + sums_at) + (warp ^ 4) * 6 * 32 + lane;
+            // the pair's halves: all of K S to both, of Q S the first 16 tokens to the first. Two buffers: who writes one again has
+            // passed the barrier between, and with it the other's reads.
+            float4 *sums = reinterpret_cast<float4 *>(smem + sums_at) + (j % kSums * 8 + warp) * 6 * 32 + lane;
+            const float4 *others = reinterpret_cast<const float4 *>(smem + sums_at) + (j % kSums * 8 + (warp ^ 1)) * 6 * 32 + lane;
 #pragma unroll
             for (int n = 0; n < 4; ++n) sums[n * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
 #pragma unroll
@@ -552,17 +577,32 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                 sums[(4 + n) * 32] = half ? make_float4(x[4 + n][0], x[4 + n][1], x[4 + n][2], x[4 + n][3]) : make_float4(x[6 + n][0], x[6 + n][1], x[6 + n][2], x[6 + n][3]);
             // meanwhile the values, and the numbers
             float w[4][4];
+            if (kTerms == 2) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n)
+                for (int n = 0; n < 4; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint8_t *at = here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (pair * 16 + lane / 4 + e / 2 * 8) * es;
-                    if (kTerms == 2) w[n][e] = *reinterpret_cast<const float *>(at);
-                    else {
-                        const uint16_t v = *reinterpret_cast<const uint16_t *>(at);
-                        w[n][e] = bf16 ? __uint_as_float((uint32_t)v << 16) : __half2float(__ushort_as_half(v));
+                    for (int e = 0; e < 4; ++e)
+                        w[n][e] = *reinterpret_cast<const float *>(here + kV + (n * 8 + lane % 4 * 2 + e % 2) * v_stride + (pair * 16 + lane / 4 + e / 2 * 8) * es);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {       // 16 tokens: pairs of them, of this thread's two columns
+                    uint32_t v[4];
+                    load_matrices_turned(v, stage + kV + (k * 16 + b_row) * v_stride + pair * 32 + b_col);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&v[i]));
+                        w[2 * k + i / 2][i % 2 * 2] = bf16 ? __uint_as_float(v[i] << 16) : f.x;
+                        w[2 * k + i / 2][i % 2 * 2 + 1] = bf16 ? __uint_as_float(v[i] & 0xffff0000u) : f.y;
                     }
                 }
+            }
+            if (count < kChunk) {       // rows that were not copied
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (n * 8 + (int32_t)(lane % 4) * 2 + e % 2 >= count) w[n][e] = 0.f;
+            }
             named_barrier(1 + pair, 64);
             // W = V - e^G K S, then U = T diag(beta) W
             float m0 = 0.f, m1 = 0.f, qs[2][4];
@@ -583,6 +623,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
 #pragma unroll
                 for (int e = 0; e < 4; ++e) qs[n][e] = (half ? x[6 + n][e] : x[4 + n][e]) + oe[e];
             }
+            if (kSums == 1) named_barrier(1 + pair, 64);
             auto halves = [&](const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
@@ -685,40 +726,50 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[2 * n0_ + m][e] = fmaf(y[m][e], e / 2 ? d1 : d0, left * s[2 * n0_ + m][e]);
             }
+            float2 of_q[2];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) of_q[n] = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[j % kStages]));
             // out, through shared memory: 16 columns of this warp's 16 tokens
-            {
+            if (good) {
                 const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    const float2 f = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][e] = (e % 2 ? f.y : f.x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0);
+                    for (int e = 0; e < 4; ++e) o[n][e] = (e % 2 ? of_q[n].y : of_q[n].x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0);
                 }
-                uint8_t *to = smem + out_at + lane % 4 * 160 + lane / 4 * out_es;
                 if (a.out_dtype == NINFER_F32) {
+                    uint8_t *to = smem + out_at + lane % 4 * 160 + lane / 4 * 4;
 #pragma unroll
                     for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(to + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 32) = o[i / 4][i % 4];
                 } else {
-                    const bool to_bf16 = a.out_dtype == NINFER_BF16;
+                    uint32_t r[4];          // pairs of tokens, turned as they are stored
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float y = o[i / 4][i % 4];
-                        *reinterpret_cast<uint16_t *>(to + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 16) =
-                            to_bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(y)) : __half_as_ushort(__float2half_rn(y));
+                    for (int i = 0; i < 4; ++i) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
+                        const __half2 h = __floats2half2_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
+                        r[i] = a.out_dtype == NINFER_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
                     }
+                    store_matrices_turned(base + out_at + b_row * 80 + b_col, r);
                 }
                 __syncwarp();
-                const int32_t first = range.begin + (int32_t)(j * kChunk + half * 16);
-                const uint32_t per = 16 / out_es;       // elements of 16 bytes
-                for (uint32_t i = lane; i < 16 * out_es; i += 32) {
-                    const uint32_t t = i / out_es, c = i % out_es;
-                    if (first + (int32_t)t < range.end && mine + c * per < v_dim) {
-                        const uint64_t at = ((uint64_t)(first + t) * a.v_heads + part.head) * v_dim + mine + c * per;
+                const uint32_t shift = out_es == 4 ? 2 : 1, per = 16 / out_es;       // 16-byte units of a token, elements of one
+                for (uint32_t i = lane; i < 16u << shift; i += 32) {
+                    const uint32_t t = i >> shift, c = i & (out_es - 1);
+                    if ((int32_t)(half * 16 + t) < count && mine + c * per < v_dim) {
+                        const uint64_t at = ((uint64_t)(first + half * 16 + t) * a.v_heads + part.head) * v_dim + mine + c * per;
                         *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * out_es) = *reinterpret_cast<const uint4 *>(smem + out_at + t * 80 + c * 16);
                     }
                 }
+                __syncwarp();
             }
         }
+    }
+    if (!good) {        // no CTA ends with copies under way
+        if (warp == 0)
+            for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit);
+        return;
     }
 #pragma unroll
     for (int n = 0; n < 2 * kSteps; ++n)
@@ -737,7 +788,7 @@ auto chunk_kernel_of(uint32_t wide) {
 // k_dim rounded up to what the kernel has instances for
 uint32_t wide_of(uint64_t k_dim) { return k_dim <= 64 ? 64 : k_dim <= 96 ? 96 : k_dim <= 128 ? 128 : 256; }
 
-uint64_t rows_bytes_of(int terms, uint64_t k_dim) { return (uint64_t)terms * 2 * kChunk * wide_of(k_dim) * 2; }
+uint64_t rows_bytes_of(int terms, uint64_t k_dim) { return (uint64_t)terms * 2 * kChunk * (wide_of(k_dim) * 2 + 16); }
 
 int check_sizes(uint64_t tokens, uint64_t requests, uint64_t k_heads, uint64_t v_heads, uint64_t k_dim, uint64_t v_dim) {
     if (!tokens || tokens > 0x7fffffffull || !requests || requests > 0x7fffffffull)
@@ -846,9 +897,12 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     c.rows_bytes = rows_bytes_of(terms, a.k_dim);
     c.rows = static_cast<uint8_t *>(workspace);
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
-    const uint32_t prepare_smem = terms * 2 * kChunk * (c.wide * 2 + 16);
-    const uint32_t chunk_smem = stages_of(c.wide, terms) * (prepare_smem + 4 * kChunk * (kChunk * 2 + 16) + kNumbers * 4 + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
-                                kChunkThreads / 32 * (kChunk / 2 * 80 + 6 * 32 * 16);
+    st = device_error_word(&c.error);
+    if (st) return st;
+    c.wait_limit = wait_limit_cycles();
+    const uint32_t prepare_smem = (uint32_t)c.rows_bytes;
+    const uint32_t chunk_smem = stages_of(c.wide, terms) * ((uint32_t)c.rows_bytes + kHeadBytes + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
+                                8 * (kChunk / 2 * 80 + sums_of(c.wide, terms) * 6 * 32 * 16);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
     const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide) : chunk_kernel_of<1>(c.wide);
     st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
