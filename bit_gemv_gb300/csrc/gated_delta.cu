@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 //   O = scale (diag(e^G) Q S + P U),          P_ts = e^(G_t - G_s) q_t . k_s for s <= t, else 0
 //   S <- e^(G_last) S + K^T diag(e^(G_last - G)) U
 // T diag(beta) and P need no state: prepare_kernel makes them for all chunks at once, chunk_kernel goes through them.
-constexpr int kChunk = 32, kPrepareThreads = 128, kChunkThreads = 256, kColumns = 64;      // columns of a state a CTA
+constexpr int kChunk = 32, kPrepareThreads = 128, kColumns = 64;      // columns of a state a CTA
 constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
 enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
 constexpr uint32_t kTriStride = kChunk * 2 + 16, kTrianglesBytes = 4 * kChunk * kTriStride;     // T high and low, P high and low
@@ -424,6 +424,9 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     }
 }
 
+// Eight warps that compute, and one that copies where it leaves them registers enough (else the first one does that too).
+__host__ __device__ constexpr int chunk_threads(int steps) { return steps < 8 ? 288 : 256; }
+
 // Chunks in shared memory at once, and buffers for the sums: what fits an SM.
 __host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
 __host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 1 : 2; }
@@ -432,11 +435,11 @@ __host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms) { retur
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
 // products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
 // as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
-// outputs by tokens. The first warp keeps the next chunks coming (bulk copies, mbarriers; a ninth warp for it would take a third of the
-// registers); nothing else holds pairs together, so that of two pairs on a scheduler one multiplies while the other splits and scales.
+// outputs by tokens. A ninth warp keeps the next chunks coming (bulk copies, mbarriers); nothing else holds pairs together, so
+// that of two pairs on a scheduler one multiplies while the other splits and scales.
 // kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q.
 template <int kSteps, int kTerms>
-__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride;
     constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + kTrianglesBytes, kV = kTri + kHeadBytes;
     constexpr uint32_t kSums = sums_of(kSteps * 32, kTerms), es = kTerms == 2 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
@@ -463,24 +466,11 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
     const bool bf16 = a.dtype == NINFER_BF16;
     const uint32_t out_at = kStages * stage_bytes + warp * (kChunk / 2 * 80), sums_at = kStages * stage_bytes + 8 * (kChunk / 2 * 80);
     const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
-    if (mine >= v_dim) return;      // whole pairs
-
-    // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
-    float s[2 * kSteps][4];
-    float *state = a.state + part.state;
-    const uint32_t k_first = half * kSteps * 16 + lane % 4 * 2;
-#pragma unroll
-    for (int n = 0; n < 2 * kSteps; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
-            s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
-        }
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
     const uint32_t t_row = lane % 16, t_col = lane / 16 * 16, half_col = half * kSteps * 32;
     uint32_t sent = 0;
     bool good = true;       // once a wait has run out, none is made and nothing is stored
-    // The first warp's: chunk j into its stage, which all warps have left. Lanes whose 16 bytes of values lie past the last column copy
+    // The copying warp's: chunk j into its stage, which all warps have left. Lanes whose 16 bytes of values lie past the last column copy
     // the last ones there are; what they get is part of no result.
     constexpr uint32_t kUnits = kColumns * es / 16;
     constexpr int32_t kRowsAtOnce = 32 / kUnits;
@@ -514,8 +504,30 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
         copies_arrive(bar);
         sent = j + 1;
     };
-    if (warp == 0)
+    // no CTA ends with copies under way, not where a wait has run out either
+    auto drain = [&]() {
+        for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit);
+    };
+    constexpr bool kSender = chunk_threads(kSteps) > 256;
+    if (kSender && warp == 8) {
+        for (uint32_t j = 0; j < range.chunks && good; ++j) send(j);
+        if (!good) drain();
+        return;
+    }
+    if (mine >= v_dim) return;      // whole pairs
+    if (!kSender && warp == 0)
         for (uint32_t j = 0; j < min(kStages - 1, range.chunks); ++j) send(j);
+    // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
+    float s[2 * kSteps][4];
+    float *state = a.state + part.state;
+    const uint32_t k_first = half * kSteps * 16 + lane % 4 * 2;
+#pragma unroll
+    for (int n = 0; n < 2 * kSteps; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
+            s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
+        }
     for (uint32_t j = 0; j < range.chunks; ++j) {
         good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit)));
         const uint32_t stage = base + j % kStages * stage_bytes;
@@ -558,7 +570,7 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
                     for (int n = 0; n < 8; ++n) mma(x[n], high, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
                 }
             }
-            if (warp == 0 && j + kStages - 1 < range.chunks) send(j + kStages - 1);
+            if (!kSender && warp == 0 && j + kStages - 1 < range.chunks) send(j + kStages - 1);
             {
                 const float down0 = inverse_power(up0), down1 = inverse_power(up1);
 #pragma unroll
@@ -766,9 +778,8 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(const __grid_const
             }
         }
     }
-    if (!good) {        // no CTA ends with copies under way
-        if (warp == 0)
-            for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit);
+    if (!good) {
+        if (!kSender && warp == 0) drain();
         return;
     }
 #pragma unroll
@@ -908,6 +919,6 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
     if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(chunk), (int)chunk_smem);
     if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kPrepareThreads), prepare_smem, s, c);
-    if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3(kChunkThreads), chunk_smem, s, c);
+    if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3(chunk_threads((int)c.wide / 32)), chunk_smem, s, c);
     return st;
 }
