@@ -26,6 +26,8 @@ bool prefetch_before_dependency();
 long long wait_limit_cycles();
 // cudaFuncSetAttribute(MaxDynamicSharedMemorySize) once per kernel, device and size.
 int set_smem_attribute(const void *kernel, int bytes);
+// Lets a kernel run in clusters of more than eight CTAs; once per kernel and device.
+int set_wide_clusters(const void *kernel);
 
 // Rows of a plane as a 2-D byte tensor {row_bytes, rows}, for 2-D box loads:
 // boxes of box_bytes x box_rows, optionally 128-byte swizzled.

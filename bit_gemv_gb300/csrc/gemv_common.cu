@@ -67,6 +67,26 @@ int set_smem_attribute(const void *kernel, int bytes) {
     return NINFER_OK;
 }
 
+int set_wide_clusters(const void *kernel) {
+    struct Key {
+        const void *kernel;
+        int dev;
+    };
+    static std::mutex mu;
+    static Key done[64];
+    static int ndone = 0;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail(NINFER_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < ndone; ++i)
+        if (done[i].kernel == kernel && done[i].dev == dev) return NINFER_OK;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return fail(NINFER_ERR_CUDA, "cluster-size attribute: %s", cudaGetErrorString(e));
+    if (ndone < 64) done[ndone++] = Key{kernel, dev};
+    return NINFER_OK;
+}
+
 namespace {
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,

@@ -2,17 +2,21 @@
 // top-p and min-p from given random numbers.
 //
 // What is kept is a beginning of the tokens in falling order of their logits (equal ones in rising order of their
-// place), so that a border, a logit's order-preserving 32-bit key and the place of its last equal one, describes it: top-k and
-// top-p each find one by descending through the key's bits (11, 11 and 10 at a time) with histograms in shared memory, of
-// counts or of weights. The token is then the first whose running sum in the order of the row passes the
-// random number's share of the whole.
+// place), so that a border, a logit's order-preserving 32-bit key and the place of its last equal one, describes it, whatever the
+// number of tokens. The token is then the first whose running sum in the order of the row passes the random number's share
+// of the whole.
 //
-// Weights are whole numbers (units of 2^-kScale of the largest one), exact to 2^-30 of themselves: sums of them do not
+// Weights are whole numbers (units of 2^-scale of the largest one), exact to 2^-30 of themselves: sums of them do not
 // depend on the order in which threads and CTAs add, which makes borders and choices the same however a row is divided. A
 // weight is 2^t, t = (x - m) log2(e) / T in two floats: a table of 64 powers for the fraction's first six bits, the
 // exponential's series for the rest, everything else in integers.
 //
-// A row is divided among the CTAs of a cluster, which exchange maxima, sums and histograms through distributed shared memory.
+// A row is divided among the CTAs of a cluster, which hold it in shared memory (read once from HBM) and exchange maxima, sums and
+// histograms through distributed shared memory. A border is found in two passes: a histogram of 2048 bins, 1/64 of a
+// power of two wide, from the largest logit down, of counts (top-k) or weights to 16 bits (top-p), tells the bin or the few bins
+// in which it lies; their tokens, seldom more than a few hundred, are sorted by the cluster's first CTA, which adds their exact weights
+// to the exact sum of what lies above. Where more than 2048 tokens lie there (equal logits without end), the border comes from the
+// key's bits, eight at a time. Rows that keep few tokens (top-k up to 1024, min-p) have all of them sorted and chosen from by that CTA.
 #include <cmath>
 
 #include "decode.cuh"
@@ -22,7 +26,9 @@
 namespace ninfer {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kMostCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kResident = 2;    // CTAs an SM
+constexpr uint32_t kBins = 2048, kListed = 2048, kFew = 1024, kMostCluster = 16;
+constexpr uint32_t kSliceBytes = 64 * 1024, kMostSliceBytes = 176 * 1024, kLeastSlice = 2048;  // two CTAs an SM, one; tokens
 
 // 2^(30 + j / 64), rounded
 __device__ const uint32_t kPowers[64] = {
@@ -37,8 +43,10 @@ __device__ const uint32_t kPowers[64] = {
 
 struct SampleParams {
     ninfer_sample_args a;
-    uint32_t slice;         // tokens a CTA, a multiple of 8
+    uint32_t vectors;       // 16-byte vectors of a row a CTA
     int scale;              // weights are whole multiples of 2^-scale
+    bool held;              // in shared memory
+    float unit, slack;      // of the histogram's weights: a bin's largest is `unit`; sums are too small by less than `slack` of themselves
 };
 
 __device__ __forceinline__ uint64_t ld_cluster_u64(const void *local, uint32_t rank) {
@@ -46,13 +54,22 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(const void *local, uint32_t r
     asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
     return v;
 }
-__device__ __forceinline__ uint2 ld_cluster_v2(const void *local, uint32_t rank) {
-    uint2 v;
-    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
+__device__ __forceinline__ uint32_t ld_cluster_u32(const void *local, uint32_t rank) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(mapa_shared(smem_u32(local), rank)) : "memory");
     return v;
 }
 __device__ __forceinline__ void st_cluster_u64(const void *local, uint32_t rank, uint64_t v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u32(const void *local, uint32_t rank, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(mapa_shared(smem_u32(local), rank)), "r"(v) : "memory");
+}
+
+// The cluster's barrier, which wants whole warps.
+__device__ __forceinline__ void join() {
+    __syncwarp();
+    cluster_sync();
 }
 
 // Order-preserving key of a logit without NaN; equal values (both zeros) have equal keys.
@@ -63,20 +80,30 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 constexpr uint32_t kLowest = 0x007fffffu;       // the key of -infinity
 
-struct Shared {
+struct alignas(16) Shared {
     uint32_t powers[64];
-    uint64_t part[kWarps], slot[2], total, found[2], totals[kBins];
-    uint2 hist[kBins];      // low and high words
-    uint64_t above, inside;
-    uint32_t bin;
+    uint64_t part[kWarps], slot[2][2], found[2][2];
+    uint32_t hist[kBins], totals[kBins], list[kListed], listed, first;
+    uint64_t sorted[kListed];
+    float part_f[kWarps];
     float c_hi, c_lo;
+    struct {
+        uint64_t above, inside;
+        uint32_t bin, bin2, border, last;
+        bool over;
+    } cut;
+    uint64_t target;
+    uint64_t least;
 };
 
 template <int kDtype>
 struct Row {
-    const void *x;
+    static constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs;
+    const uint8_t *x;
     Shared &s;
-    uint32_t lo, hi;        // this CTA's tokens
+    const uint4 *held;          // the slice in shared memory, or null
+    uint32_t vocab, shift;      // elements between the last 16-byte boundary and the row's first
+    uint32_t v0, v1;            // this CTA's 16-byte vectors, counted from that boundary
     uint32_t rank, ranks;
     int scale;
     uint32_t phase = 0;
@@ -86,28 +113,65 @@ struct Row {
     uint32_t border = kLowest + 1, last = ~0u;
     uint64_t least = 0;
 
-    __device__ Row(const void *x, Shared &s, uint32_t lo, uint32_t hi, int scale)
-        : x(x), s(s), lo(lo), hi(hi), rank(cluster_ctarank()), ranks(cluster_nctarank()), scale(scale) {}
-
-    __device__ __forceinline__ uint32_t key(uint32_t i) const {
-        const float v = load1(x, i, kDtype);
-        return v == v ? key_of(v) : kLowest;
+    __device__ Row(const uint8_t *x, Shared &s, const uint4 *held, uint32_t vocab, int scale) : x(x), s(s), held(held), vocab(vocab), scale(scale) {
+        shift = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) / kEs;
+        rank = cluster_ctarank();
+        ranks = cluster_nctarank();
     }
+
+    // The 16 bytes of vector v from global memory; -infinity for what is not of the row
+    __device__ __forceinline__ uint4 read(uint32_t v) const {
+        const int64_t first = (int64_t)v * kVec - shift;
+        if (first >= 0 && first + kVec <= vocab) return *reinterpret_cast<const uint4 *>(x + first * kEs);
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const int64_t i = first + j;
+            const bool in = i >= 0 && i < vocab;
+            if (kEs == 4) w[j] = in ? reinterpret_cast<const uint32_t *>(x)[i] : 0xff800000u;
+            else {
+                const uint32_t h = in ? reinterpret_cast<const uint16_t *>(x)[i] : kDtype == NINFER_BF16 ? 0xff80u : 0xfc00u;
+                w[j / 2] = j & 1 ? w[j / 2] | h << 16 : h;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    // f(x, place) for every element of vectors from + first, from + first + step ..., NaN as -infinity, until `to`; places before the row's
+    // first and behind its last have -infinity
+    template <class F>
+    __device__ __forceinline__ void over(uint32_t from, uint32_t to, uint32_t step, F f) const {
+        for (uint32_t v = from; v < to; v += step) {
+            const uint4 u = held ? held[v - v0] : read(v);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) {
+                const uint32_t h = w[j * kEs / 4];
+                const float y = kEs == 4 ? __uint_as_float(h)
+                                : kDtype == NINFER_BF16 ? __uint_as_float(j & 1 ? h & 0xffff0000u : h << 16)
+                                                        : __half2float(__ushort_as_half((uint16_t)(j & 1 ? h >> 16 : h & 0xffff)));
+                f(fmaxf(y, -INFINITY), v * kVec - shift + j);
+            }
+        }
+    }
+    template <class F>
+    __device__ __forceinline__ void each(F f) const { over(v0 + threadIdx.x, v1, kThreads, f); }
+
+    __device__ __forceinline__ uint32_t key_at(uint32_t i) const { return key_of(fmaxf(load1(x, i, kDtype), -INFINITY)); }
     __device__ __forceinline__ bool kept(uint32_t key, uint32_t i) const { return key > border || (key == border && i <= last); }
 
     // t as two floats; false where 2^t is no more than 2^-100 (or the logit infinitely far away)
     __device__ __forceinline__ bool exponent(float v, float &p, float &rest) const {
         p = rest = 0.f;
         if (v == m) return true;
-        const float d = v - m, b = d + m, e = (v - b) + (m - (b - d)) * -1.f;     // d + e = v - m exactly
+        const float d = v - m, b = d + m, e = (v - b) - (m - (b - d));      // d + e = v - m exactly
         p = d * c_hi;
         if (!(p >= -100.f)) return false;
         rest = fmaf(d, c_hi, -p) + fmaf(d, c_lo, e * c_hi);
         return true;
     }
-    __device__ __forceinline__ uint64_t weight(uint32_t key) const {
+    __device__ __forceinline__ uint64_t weight(float v) const {
         float p, rest;
-        if (!exponent(logit_of(key), p, rest)) return 0;
+        if (!exponent(v, p, rest)) return 0;
         const int n = __float2int_rn(p * 64.f);
         const float r = fmaf((float)n, -1.f / 64.f, p) + rest;       // exact but for `rest`, at most 1 / 128
         const float y = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);        // 2^r - 1
@@ -117,7 +181,15 @@ struct Row {
         if (shift >= 0) return (uint64_t)w << shift;
         return shift < -31 ? 0 : ((uint64_t)w + (1ull << (-shift - 1))) >> -shift;
     }
+    // How many bins a logit lies below the largest one, kBins and more for none; falling logits have rising bins. `part`: of a bin.
+    __device__ __forceinline__ uint32_t bin_of(float v, float &part) const {
+        const float u = v == m ? 0.f : (m - v) * (c_hi * 64.f);
+        const float low = floorf(u);
+        part = u - low;
+        return u < (float)kBins ? (uint32_t)low : kBins;
+    }
 
+    // Sum over the CTA; every thread gets it.
     __device__ uint64_t block_sum(uint64_t v) {
 #pragma unroll
         for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
@@ -126,153 +198,288 @@ struct Row {
         __syncthreads();
         v = threadIdx.x % 32 < kWarps ? s.part[threadIdx.x % 32] : 0;
 #pragma unroll
-        for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
-        return v;
+        for (int k = 8; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
+        return __shfl_sync(~0u, v, 0);
     }
-    __device__ uint64_t block_max(uint64_t v) {
-#pragma unroll
-        for (int k = 16; k; k /= 2) v = max(v, __shfl_xor_sync(~0u, v, k));
-        __syncthreads();
-        if (threadIdx.x % 32 == 0) s.part[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = threadIdx.x % 32 < kWarps ? s.part[threadIdx.x % 32] : 0;
-#pragma unroll
-        for (int k = 16; k; k /= 2) v = max(v, __shfl_xor_sync(~0u, v, k));
-        return v;
-    }
-    // Puts one value of each CTA where the others see it. The slot of two exchanges ago is free: every CTA has read it
+    // Puts two values of each CTA where the others see them. The slot of two exchanges ago is free: every CTA has read it
     // before it came to the barrier of the last one.
-    __device__ void exchange(uint64_t v) {
+    __device__ void exchange(uint64_t v, uint64_t w = 0) {
         phase ^= 1;
-        if (threadIdx.x == 0) s.slot[phase] = v;
-        cluster_sync();
+        if (threadIdx.x == 0) {
+            s.slot[phase][0] = v;
+            s.slot[phase][1] = w;
+        }
+        join();
+    }
+    // The sums of both over the cluster.
+    __device__ uint64_t collect(int which = 0) const {
+        uint64_t t = threadIdx.x % 32 < ranks ? ld_cluster_u64(&s.slot[phase][which], threadIdx.x % 32) : 0;
+#pragma unroll
+        for (int k = 8; k; k /= 2) t += __shfl_xor_sync(~0u, t, k);
+        return __shfl_sync(~0u, t, 0);
     }
     __device__ uint64_t cluster_sum(uint64_t v) {
         exchange(block_sum(v));
-        uint64_t t = 0;
-        for (uint32_t r = 0; r < ranks; ++r) t += ld_cluster_u64(&s.slot[phase], r);
-        return t;
+        return collect();
     }
-    __device__ uint64_t cluster_max(uint64_t v) {
-        exchange(block_max(v));
-        uint64_t t = 0;
-        for (uint32_t r = 0; r < ranks; ++r) t = max(t, ld_cluster_u64(&s.slot[phase], r));
-        return t;
+    // The largest float over the cluster.
+    __device__ float cluster_max(float v) {
+#pragma unroll
+        for (int k = 16; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
+        if (threadIdx.x % 32 == 0) s.part_f[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = threadIdx.x % 32 < kWarps ? s.part_f[threadIdx.x % 32] : -INFINITY;
+#pragma unroll
+        for (int k = 8; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
+        exchange(__float_as_uint(v));
+        v = threadIdx.x % 32 < ranks ? __uint_as_float((uint32_t)ld_cluster_u64(&s.slot[phase][0], threadIdx.x % 32)) : -INFINITY;
+#pragma unroll
+        for (int k = 8; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
+        return __shfl_sync(~0u, v, 0);
     }
 
-    // The first place, in the order of the row, at which the running sum of value(place) passes `target` (which the
-    // whole sum does).
-    template <class F>
-    __device__ uint32_t locate(uint64_t target, F value) {
+    // The first place, in the order of the row, at which the running sum of value(x, place) passes target(whole sum).
+    template <class F, class T>
+    __device__ uint32_t locate(T target, F value, uint64_t *whole = nullptr) {
         const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        const uint32_t each = ((hi - lo + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const uint32_t from = min(lo + warp * each, hi), to = min(from + each, hi);
+        const uint32_t each_ = ((v1 - v0 + kWarps - 1) / kWarps + 31) / 32 * 32;
+        const uint32_t from = min(v0 + warp * each_, v1), to = min(from + each_, v1);
         uint64_t sum = 0;
-        for (uint32_t i = from + lane; i < to; i += 32) sum += value(i);
+        over(from + lane, to, 32, [&](float v, uint32_t i) { sum += value(v, i); });
 #pragma unroll
         for (int k = 16; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
         __syncthreads();
         if (lane == 0) s.part[warp] = sum;
         __syncthreads();
-        uint64_t before = 0, all = 0;
-        for (uint32_t w = 0; w < kWarps; ++w) {
-            if (w < warp) before += s.part[w];
-            all += s.part[w];
+        const uint64_t mine = lane < kWarps ? s.part[lane] : 0;
+        uint64_t before = lane < warp ? mine : 0, all = mine;
+#pragma unroll
+        for (int k = 16; k; k /= 2) {
+            before += __shfl_xor_sync(~0u, before, k);
+            all += __shfl_xor_sync(~0u, all, k);
         }
         exchange(all);
-        for (uint32_t r = 0; r < rank; ++r) before += ld_cluster_u64(&s.slot[phase], r);
-        if (target >= before && target - before < sum) {            // one warp of the cluster
-            uint64_t run = target - before;                          // what is still to be passed
-            for (uint32_t i0 = from; i0 < to; i0 += 32) {
-                uint64_t v = i0 + lane < to ? value(i0 + lane) : 0;
+        const uint64_t total = collect();
+        if (whole) *whole = total;
+        uint64_t ahead = lane < rank ? ld_cluster_u64(&s.slot[phase][0], lane) : 0;
+#pragma unroll
+        for (int k = 16; k; k /= 2) ahead += __shfl_xor_sync(~0u, ahead, k);
+        before += ahead;
+        if (threadIdx.x == 0) s.target = target(total);
+        __syncthreads();
+        const uint64_t goal = s.target;
+        if (goal >= before && goal - before < sum) {                // one warp of the cluster
+            uint64_t run = goal - before;                            // what is still to be passed
+            for (uint32_t v = from; v < to; v += 32) {
+                uint64_t here[kVec], lanes = 0;
+                int n = 0;
+                over(v + lane < to ? v + lane : to, to, 32 * kThreads, [&](float y, uint32_t i) { lanes += here[n++] = value(y, i); });
+                uint64_t u = lanes;
 #pragma unroll
                 for (int k = 1; k < 32; k *= 2) {
-                    const uint64_t u = __shfl_up_sync(~0u, v, k);
-                    if (lane >= (uint32_t)k) v += u;
+                    const uint64_t w = __shfl_up_sync(~0u, u, k);
+                    if (lane >= (uint32_t)k) u += w;
                 }
-                const uint32_t passed = __ballot_sync(~0u, v > run);
+                const uint32_t passed = __ballot_sync(~0u, u > run);
                 if (passed) {
-                    if (lane < ranks) st_cluster_u64(&s.found[phase], lane, i0 + __ffs(passed) - 1);
+                    if (lane == (uint32_t)__ffs(passed) - 1) {
+                        uint64_t w = u - lanes;
+                        int j = 0;
+                        for (; j < n - 1 && (w += here[j]) <= run; ++j) {}
+                        for (uint32_t r = 0; r < ranks; ++r) st_cluster_u64(&s.found[phase][0], r, (v + lane) * kVec - shift + j);
+                    }
                     break;
                 }
-                run -= __shfl_sync(~0u, v, 31);
+                run -= __shfl_sync(~0u, u, 31);
             }
         }
-        cluster_sync();
-        return (uint32_t)s.found[phase];
+        join();
+        return (uint32_t)s.found[phase][0];
+    }
+
+    // Adds up the cluster's histograms (counts, or weights of which a bin's largest times `unit` is 1) into `totals` of every CTA: a part each.
+    template <bool kWeights>
+    __device__ void merge(float unit) {
+        join();
+        const uint32_t part = kBins / ranks;
+        for (uint32_t i = threadIdx.x; i < part; i += kThreads) {
+            const uint32_t b = rank * part + i;
+            uint64_t t = 0;
+            for (uint32_t r = 0; r < ranks; ++r) t += ld_cluster_u32(&s.hist[b], r);
+            // a weight as a float, of the row's largest one
+            const uint32_t word = kWeights ? __float_as_uint((float)t * unit * exp2f((float)b * (-1.f / 64.f))) : (uint32_t)t;
+            for (uint32_t r = 0; r < ranks; ++r) st_cluster_u32(&s.totals[b], r, word);
+        }
+        join();
+    }
+    // Running sums over the bins' totals up to and with this thread's bins 4 tid .. 4 tid + 3.
+    template <class T>
+    __device__ void running(T (&sums)[4]) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(&s.totals[threadIdx.x * 4]);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w}, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        T v[4], run = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = sizeof(T) == 4 ? (T)__uint_as_float(w[j]) : (T)w[j];
+            run += v[j];
+        }
+        const T mine = run;
+#pragma unroll
+        for (int k = 1; k < 32; k *= 2) {
+            const T o = __shfl_up_sync(~0u, run, k);
+            if (lane >= (uint32_t)k) run += o;
+        }
+        __syncthreads();
+        T *parts = reinterpret_cast<T *>(s.part);
+        if (lane == 31) parts[warp] = run;
+        __syncthreads();
+        run -= mine;
+        for (uint32_t k = 0; k < warp; ++k) run += parts[k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[j] = run += v[j];
+    }
+
+    __device__ void clear() {
+        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
+        if (threadIdx.x == 0) {
+            s.listed = 0;
+            s.cut.bin = s.cut.bin2 = kBins;
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void list(uint32_t place) {
+        const uint32_t at = atomicAdd(&s.listed, 1u);
+        if (at < kListed) s.list[at] = place;
+    }
+
+    // The first CTA: the lists of all, as (key, place) in falling order of keys and rising of places, in `sorted`; returns how many.
+    __device__ uint32_t gather() {
+        uint32_t n = 0;
+        for (uint32_t r = 0; r < ranks; ++r) {
+            const uint32_t count = ld_cluster_u32(&s.listed, r);
+            for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+                const uint32_t place = ld_cluster_u32(&s.list[i], r);
+                s.sorted[n + i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
+            }
+            n += count;
+        }
+        __syncthreads();
+        sort(n);
+        return n;
+    }
+    // `sorted` in falling order, with zeros behind the n first.
+    __device__ void sort(uint32_t n) {
+        uint32_t size = 64;
+        while (size < n) size *= 2;
+        for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) s.sorted[i] = 0;
+        __syncthreads();
+        for (uint32_t k = 2; k <= size; k *= 2)
+            for (uint32_t j = k / 2; j; j /= 2) {
+                for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
+                    const uint32_t a = 2 * i - (i & (j - 1)), b = a + j;
+                    const uint64_t x = s.sorted[a], y = s.sorted[b];
+                    if ((x < y) == ((a & k) == 0)) {
+                        s.sorted[a] = y;
+                        s.sorted[b] = x;
+                    }
+                }
+                // pairs less than 64 apart stay with a warp
+                if (j > 32 || j == 1) __syncthreads();
+                else __syncwarp();
+            }
+    }
+    // Running sums of w (4 a thread: numbers 4 tid .. 4 tid + 3) up to and with each.
+    __device__ void scan(const uint64_t (&w)[4], uint64_t (&sums)[4]) {
+        const uint32_t lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+        uint64_t run = (w[0] + w[1]) + (w[2] + w[3]);
+        const uint64_t mine = run;
+#pragma unroll
+        for (int k = 1; k < 32; k *= 2) {
+            const uint64_t o = __shfl_up_sync(~0u, run, k);
+            if (lane >= (uint32_t)k) run += o;
+        }
+        __syncthreads();
+        if (lane == 31) s.part[warp] = run;
+        __syncthreads();
+        run -= mine;
+        for (uint32_t k = 0; k < warp; ++k) run += s.part[k];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[j] = run += w[j];
+    }
+    // Running sums of the weights of `sorted`.
+    __device__ void sorted_sums(uint32_t n, uint64_t (&w)[4], uint64_t (&sums)[4]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t i = threadIdx.x * 4 + j;
+            w[j] = i < n ? weight(logit_of((uint32_t)(s.sorted[i] >> 32))) : 0;
+        }
+        scan(w, sums);
+    }
+    // Gives the border that the first CTA has put into s.cut to all.
+    __device__ void adopt() {
+        phase ^= 1;
+        if (rank == 0 && threadIdx.x < ranks) {
+            st_cluster_u64(&s.found[phase][0], threadIdx.x, (uint64_t)s.cut.border << 32 | s.cut.last);
+        }
+        join();
+        border = (uint32_t)(s.found[phase][0] >> 32);
+        last = (uint32_t)s.found[phase][0];
     }
 
     // Moves the border to where the kept tokens' counts (kWeighted: weights), from the largest on, reach `target`, which
-    // their sum does; its last token included.
+    // their sum does, its last token included; by the keys' bits, eight at a time.
     template <bool kWeighted>
-    __device__ void cut(uint64_t target) {
+    __device__ __noinline__ void cut_by_bits(uint64_t target) {
+        uint2 *hist = reinterpret_cast<uint2 *>(s.hist);                // low and high words
+        uint64_t *totals = reinterpret_cast<uint64_t *>(s.totals);
         uint32_t prefix = 0;
         uint64_t above = 0;
-        for (int level = 0; level < 3; ++level) {
-            const int shift = level == 0 ? 21 : level == 1 ? 10 : 0, bits = level == 2 ? 10 : 11;
-            for (int i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = make_uint2(0, 0);
+        for (int shift_ = 24; shift_ >= 0; shift_ -= 8) {
             __syncthreads();
-            for (uint32_t i = lo + threadIdx.x; i < hi; i += kThreads) {
-                const uint32_t k = key(i);
-                if (!kept(k, i) || (level && k >> (shift + bits) != prefix)) continue;
-                uint2 *bin = &s.hist[k >> shift & ((1u << bits) - 1)];
+            if (threadIdx.x < 256) hist[threadIdx.x] = make_uint2(0, 0);
+            __syncthreads();
+            each([&](float v, uint32_t i) {
+                const uint32_t k = key_of(v);
+                if (!kept(k, i) || (shift_ < 24 && k >> (shift_ + 8) != prefix)) return;
+                uint2 *bin = &hist[k >> shift_ & 255];
                 if (kWeighted) {
-                    const uint64_t w = weight(k);
+                    const uint64_t w = weight(v);
                     const uint32_t old = atomicAdd(&bin->x, (uint32_t)w);
                     const uint32_t more = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
                     if (more) atomicAdd(&bin->y, more);
                 } else atomicAdd(&bin->x, 1u);
-            }
-            cluster_sync();
-            // each CTA adds up its part of the bins and gives the sums to all
-            const uint32_t each = kBins / ranks;
-            for (uint32_t i = threadIdx.x; i < each; i += kThreads) {
-                const uint32_t b = rank * each + i;
+            });
+            join();
+            const uint32_t part = 256 / ranks;
+            if (threadIdx.x < part) {
+                const uint32_t b = rank * part + threadIdx.x;
                 uint64_t t = 0;
-                for (uint32_t r = 0; r < ranks; ++r) {
-                    const uint2 v = ld_cluster_v2(&s.hist[b], r);
-                    t += (uint64_t)v.y << 32 | v.x;
-                }
-                for (uint32_t r = 0; r < ranks; ++r) st_cluster_u64(&s.totals[b], r, t);
+                for (uint32_t r = 0; r < ranks; ++r) t += ld_cluster_u64(&hist[b], r);
+                for (uint32_t r = 0; r < ranks; ++r) st_cluster_u64(&totals[b], r, t);
             }
-            cluster_sync();
+            join();
             // from the highest bin on: the one in which the sum reaches the target
-            constexpr int kEach = kBins / kThreads;
-            const uint32_t top = kBins - 1 - threadIdx.x * kEach, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-            uint64_t t[kEach], mine = 0;
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) mine += t[j] = s.totals[top - j];
-            uint64_t run = mine;
-#pragma unroll
-            for (int k = 1; k < 32; k *= 2) {
-                const uint64_t u = __shfl_up_sync(~0u, run, k);
-                if (lane >= (uint32_t)k) run += u;
-            }
-            if (lane == 31) s.part[warp] = run;
-            __syncthreads();
-            run += above - mine;
-            for (uint32_t w = 0; w < warp; ++w) run += s.part[w];
-#pragma unroll
-            for (int j = 0; j < kEach; ++j) {
-                if (run < target && target - run <= t[j]) {
-                    s.above = run;
-                    s.inside = t[j];
-                    s.bin = top - j;
-                }
-                run += t[j];
+            const uint64_t mine = threadIdx.x < 256 ? totals[255 - threadIdx.x] : 0;
+            uint64_t sums[4], w[4] = {mine, 0, 0, 0};
+            scan(w, sums);
+            const uint64_t before = above + sums[0] - mine;
+            if (mine && before < target && target - before <= mine) {
+                s.cut.above = before;
+                s.cut.inside = mine;
+                s.cut.bin = 255 - threadIdx.x;
             }
             __syncthreads();
-            above = s.above;
-            prefix = prefix << bits | s.bin;
-            __syncthreads();
+            above = s.cut.above;
+            prefix = prefix << 8 | s.cut.bin;
         }
         // the border's key is known; of the tokens that share it, the first in the row's order
-        const uint64_t each = kWeighted ? weight(prefix) : 1, ties = s.inside / each;
-        const uint64_t wanted = (target - above + each - 1) / each;
+        const uint64_t one = kWeighted ? weight(logit_of(prefix)) : 1, ties = s.cut.inside / one;
+        const uint64_t wanted = (target - above + one - 1) / one;
         uint32_t at = prefix == border ? last : ~0u;
         if (wanted < ties) {
             const uint32_t old = border, old_last = last;
-            at = locate(wanted - 1, [&](uint32_t i) -> uint64_t { return key(i) == prefix && (prefix != old || i <= old_last); });
+            at = locate([&](uint64_t) { return wanted - 1; },
+                        [&](float v, uint32_t i) -> uint64_t { return key_of(v) == prefix && (prefix != old || i <= old_last); });
         }
         border = prefix;
         last = at;
@@ -280,17 +487,21 @@ struct Row {
 };
 
 template <int kDtype>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant__ SampleParams p) {
+__global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __grid_constant__ SampleParams p) {
+    using R = Row<kDtype>;
+    extern __shared__ __align__(16) uint4 slice[];
     __shared__ Shared s;
-    const uint32_t tid = threadIdx.x;
+    const uint32_t tid = threadIdx.x, lane = tid % 32;
     if (tid < 64) s.powers[tid] = kPowers[tid];
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_sample_args &a = p.a;
     const uint32_t ranks = cluster_nctarank(), vocab = (uint32_t)a.vocab;
     const uint64_t b = blockIdx.x / ranks;
-    const uint32_t lo = min(cluster_ctarank() * p.slice, vocab), hi = min(lo + p.slice, vocab);
-    Row<kDtype> row(static_cast<const uint8_t *>(a.logits) + b * a.stride * (kDtype == NINFER_F32 ? 4 : 2), s, lo, hi, p.scale);
+    R row(static_cast<const uint8_t *>(a.logits) + b * a.stride * R::kEs, s, p.held ? slice : nullptr, vocab, p.scale);
+    const uint32_t all = (row.shift + vocab + R::kVec - 1) / R::kVec;      // the row's vectors
+    row.v0 = min(row.rank * p.vectors, all);
+    row.v1 = min(row.v0 + p.vectors, all);
 
     const float temperature = a.temperature ? a.temperature[b] : 1.f, top_p = a.top_p ? a.top_p[b] : 1.f;
     const float min_p = a.min_p ? a.min_p[b] : 0.f, random = a.random[b];
@@ -299,64 +510,263 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const __grid_constant_
         const double c = 1.4426950408889634 / (double)temperature;
         s.c_hi = (float)c;
         s.c_lo = (float)(c - (double)s.c_hi);
+        s.least = min_p > 0.f ? (uint64_t)ceil(ldexp((double)fminf(min_p, 1.f), p.scale)) : 0;
+        s.first = ~0u;
     }
-    // the largest logit, the first place that has it; how many take part
-    uint64_t best = 0, count = 0;
-    for (uint32_t i = lo + tid; i < hi; i += kThreads) {
-        const uint32_t k = row.key(i);
-        count += k > kLowest;
-        best = max(best, (uint64_t)k << 32 | (uint32_t)~i);
-    }
-    best = row.cluster_max(best);
-    const bool lead = tid == 0 && row.rank == 0;
-    const uint32_t top = (uint32_t)(best >> 32);
-    if (top <= kLowest || !(temperature > 0.f)) {
-        if (lead) {
-            a.tokens[b] = top <= kLowest ? -1 : (int32_t)~(uint32_t)best;
-            if (a.logprobs) a.logprobs[b] = top <= kLowest ? -INFINITY : 0.f;
+    // the row into shared memory, and its largest logit
+    float most = -INFINITY;
+    if (p.held) {
+        for (uint32_t v = row.v0 + tid; v < row.v1; v += 4 * kThreads) {
+            uint4 u[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (v + j * kThreads < row.v1) u[j] = row.read(v + j * kThreads);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (v + j * kThreads < row.v1) slice[v + j * kThreads - row.v0] = u[j];
         }
-        cluster_sync();         // no CTA leaves while another reads its shared memory
+    }
+    row.each([&](float v, uint32_t) { most = fmaxf(most, v); });        // what this thread has read itself
+    const float top = row.cluster_max(most);
+    const bool lead = tid == 0 && row.rank == 0;
+    const bool none = top == -INFINITY;
+    if (none || !(temperature > 0.f)) {
+        uint32_t place = ~0u;
+        if (!none) {
+            row.each([&](float v, uint32_t i) {
+                if (v == top) place = min(place, i);
+            });
+            place = __reduce_min_sync(~0u, place);
+            if (lane == 0 && place != ~0u) atomicMin(&s.first, place);
+            __syncthreads();
+            row.exchange(s.first);
+            place = lane < ranks ? (uint32_t)ld_cluster_u64(&s.slot[row.phase][0], lane) : ~0u;
+            place = __reduce_min_sync(~0u, place);
+        }
+        if (lead) {
+            a.tokens[b] = (int32_t)place;
+            if (a.logprobs) a.logprobs[b] = none ? -INFINITY : 0.f;
+        }
+        join();         // no CTA leaves while another reads its shared memory
         return;
     }
-    row.m = logit_of(top);
+    row.m = top;
     row.c_hi = s.c_hi;
     row.c_lo = isfinite(s.c_hi) ? s.c_lo : 0.f;
-    auto weight_at = [&](uint32_t i) -> uint64_t {
-        const uint32_t k = row.key(i);
-        if (!row.kept(k, i)) return 0;
-        const uint64_t w = row.weight(k);
-        return w >= row.least ? w : 0;
+    row.least = s.least;
+    const bool by_k = top_k > 0 && (uint32_t)top_k < vocab, by_p = top_p < 1.f, by_m = min_p > 0.f;
+    // the share of a whole that the random number says, and the logarithm of a token's share
+    auto share = [&](uint64_t whole) {
+        const uint64_t t = (uint64_t)((double)fminf(fmaxf(random, 0.f), 1.f) * (double)whole);
+        return min(t, whole - 1);
     };
-    auto whole = [&]() {
-        uint64_t sum = 0;
-        for (uint32_t i = lo + tid; i < hi; i += kThreads) sum += weight_at(i);
-        return row.cluster_sum(sum);
-    };
-    if (top_k > 0) {
-        count = row.cluster_sum(count);
-        if ((uint64_t)top_k < count) row.template cut<false>((uint64_t)top_k);
-    }
-    if (top_p < 1.f) {
-        const uint64_t sum = whole();
-        const double target = ceil((double)fmaxf(top_p, 0.f) * (double)sum);
-        row.template cut<true>(max((uint64_t)target, (uint64_t)1));
-    }
-    if (min_p > 0.f) row.least = (uint64_t)ceil(ldexp((double)fminf(min_p, 1.f), p.scale));
-    const uint64_t sum = whole();
-    const uint64_t share = (uint64_t)((double)fminf(fmaxf(random, 0.f), 1.f) * (double)sum);
-    const uint32_t token = row.locate(min(share, sum - 1), weight_at);
-    if (lead) {
+    auto answer = [&](uint32_t token, float logit, uint64_t whole) {
         a.tokens[b] = (int32_t)token;
-        if (a.logprobs) {
-            float t, rest;
-            row.exponent(logit_of(row.key(token)), t, rest);
-            // ln of the sum in units of the largest weight, which is 2^scale and among those kept
-            const uint64_t others = sum - (1ull << p.scale);
-            const float of = (float)((double)others * ldexp(1.0, -p.scale));
-            a.logprobs[b] = (t + rest) * 0.69314718f - log1pf(of);
+        if (!a.logprobs) return;
+        float t, rest;
+        row.exponent(logit, t, rest);
+        // the sum in units of the largest weight, which is 2^scale and among those kept
+        a.logprobs[b] = (t + rest) * 0.69314718f - log1pf((float)(whole - (1ull << p.scale)) * __uint_as_float((uint32_t)(127 - p.scale) << 23));
+    };
+
+    // few tokens kept: those down to bin `few` hold them all
+    uint32_t few = kBins;
+    bool cut_k = by_k;
+    if (by_k) {
+        row.clear();
+        row.each([&](float v, uint32_t) {
+            float part;
+            const uint32_t bin = v == -INFINITY ? kBins : row.bin_of(v, part);
+            if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
+        });
+        row.template merge<false>(1.f);
+        uint64_t sums[4];
+        row.running(sums);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint64_t before = sums[j] - s.totals[tid * 4 + j];
+            if (before < (uint32_t)top_k && sums[j] >= (uint32_t)top_k) {
+                s.cut.bin = tid * 4 + j;
+                s.cut.above = before;
+                s.cut.inside = sums[j];
+            }
+        }
+        __syncthreads();
+        if (s.cut.bin < kBins && s.cut.inside <= kListed && top_k <= (int32_t)kFew) few = s.cut.bin;
+    }
+    if (!by_k && by_m && !by_p) {
+        row.clear();
+        const float u = -64.f * log2f(fminf(min_p, 1.f)) + 1.f;       // a bin further, for what the logarithm and the bins round
+        if (u < (float)kBins) few = (uint32_t)u;
+    }
+    if (few < kBins) {
+        row.each([&](float v, uint32_t i) {
+            float part;
+            if (v != -INFINITY && row.bin_of(v, part) <= few) row.list(i);
+        });
+        __syncthreads();
+        row.exchange(s.listed);
+        if (row.collect() <= kListed) {
+            if (row.rank == 0) {
+                const uint32_t n = row.gather();
+                uint64_t w[4], sums[4];
+                row.sorted_sums(n, w, sums);
+                // A, its sum, and where B and C end: a number of `sorted` each
+                const uint32_t first_k = by_k ? min((uint32_t)top_k, n) : n;
+                uint64_t whole = 0;
+                if (first_k && tid == (first_k - 1) / 4) s.target = sums[(first_k - 1) % 4];
+                __syncthreads();
+                whole = s.target;
+                __syncthreads();
+                if (tid == 0) {
+                    s.target = by_p ? max((uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)whole), (uint64_t)1) : ~0ull;
+                    s.cut.bin2 = 0;
+                }
+                __syncthreads();
+                const uint64_t goal = s.target;
+                uint64_t mine = 0;
+                uint32_t end = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t i = tid * 4 + j;
+                    const bool in = i < first_k && sums[j] - w[j] < goal && w[j] >= row.least;
+                    if (in) {
+                        mine += w[j];
+                        end = i + 1;
+                    }
+                }
+                end = __reduce_max_sync(~0u, end);
+                if (lane == 0) atomicMax(&s.cut.bin2, end);
+                whole = row.block_sum(mine);        // of those kept: the first s.cut.bin2
+                if (tid == 0) s.target = share(whole);
+                __syncthreads();
+                const uint32_t kept = s.cut.bin2;
+                const uint64_t passed = s.target;
+                // sorted by places, the one whose running sum is the first past the share
+                uint64_t *weights = reinterpret_cast<uint64_t *>(s.hist);       // hist and totals, which are done with
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t i = tid * 4 + j;
+                    if (i >= kept) break;
+                    weights[i] = w[j];
+                    s.sorted[i] = (s.sorted[i] & 0xffffffffull) << 32 | i;      // ~place, number
+                }
+                row.sort(kept);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) w[j] = tid * 4 + j < kept ? weights[(uint32_t)s.sorted[tid * 4 + j]] : 0;
+                row.scan(w, sums);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (sums[j] - w[j] <= passed && passed < sums[j]) {
+                        const uint32_t place = ~(uint32_t)(s.sorted[tid * 4 + j] >> 32);
+                        answer(place, logit_of(row.key_at(place)), whole);
+                    }
+            }
+            join();
+            return;
         }
     }
-    cluster_sync();
+    if (cut_k) {
+        // many: the border alone
+        const uint32_t bin = s.cut.bin;
+        const uint64_t above = s.cut.above, inside = s.cut.inside - above;
+        __syncthreads();
+        if (bin < kBins && inside <= kListed) {
+            if (tid == 0) s.listed = 0;
+            __syncthreads();
+            row.each([&](float v, uint32_t i) {
+                float part;
+                if (v != -INFINITY && row.bin_of(v, part) == bin) row.list(i);
+            });
+            join();
+            if (row.rank == 0) {
+                row.gather();
+                if (tid == 0) {
+                    const uint64_t e = s.sorted[(uint32_t)(top_k - above) - 1];
+                    s.cut.border = (uint32_t)(e >> 32);
+                    s.cut.last = (uint32_t)~e;
+                }
+                __syncthreads();
+            }
+            row.adopt();
+        } else {
+            uint64_t count = 0;
+            row.each([&](float v, uint32_t) { count += v > -INFINITY; });
+            count = row.cluster_sum(count);
+            if ((uint64_t)top_k < count) row.template cut_by_bits<false>((uint64_t)top_k);
+        }
+    }
+    if (by_p) {
+        // the exact sum, and the weights by bins
+        row.clear();
+        uint64_t sum = 0;
+        row.each([&](float v, uint32_t i) {
+            if (!row.kept(key_of(v), i)) return;
+            sum += row.weight(v);
+            float part;
+            const uint32_t bin = row.bin_of(v, part);
+            if (bin < kBins) atomicAdd(&s.hist[bin], (uint32_t)(exp2f(part * (-1.f / 64.f)) * p.unit));
+        });
+        sum = row.block_sum(sum);
+        row.exchange(sum);
+        sum = row.collect();
+        if (tid == 0) s.target = max((uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)sum), (uint64_t)1);
+        row.template merge<true>(1.f / p.unit);
+        const uint64_t target = s.target;
+        // the border lies between where the bins' sums with all that they may lack reach the target and where they do with as much less
+        const float goal = (float)target * __uint_as_float((uint32_t)(127 - p.scale) << 23);
+        float sums[4];
+        row.running(sums);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (sums[j] * (1.f + p.slack) >= goal) atomicMin(&s.cut.bin, tid * 4 + j);
+            if (sums[j] * (1.f - p.slack) >= goal) atomicMin(&s.cut.bin2, tid * 4 + j);
+        }
+        __syncthreads();
+        const uint32_t bin = s.cut.bin, bin2 = s.cut.bin2;
+        bool done = bin2 < kBins;
+        if (done) {
+            uint64_t over = 0;
+            row.each([&](float v, uint32_t i) {
+                float part;
+                const uint32_t at = v == -INFINITY ? kBins : row.bin_of(v, part);
+                if (at > bin2 || !row.kept(key_of(v), i)) return;
+                if (at < bin) over += row.weight(v);
+                else row.list(i);
+            });
+            over = row.block_sum(over);
+            row.exchange(over, s.listed);
+            over = row.collect();
+            const uint64_t n_all = row.collect(1);
+            done = n_all <= kListed;
+            if (done) {
+                if (row.rank == 0) {
+                    const uint32_t n = row.gather();
+                    uint64_t w[4], sums_[4];
+                    row.sorted_sums(n, w, sums_);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t i = tid * 4 + j;
+                        if (i < n && over + sums_[j] - w[j] < target && over + sums_[j] >= target) {
+                            s.cut.border = (uint32_t)(s.sorted[i] >> 32);
+                            s.cut.last = (uint32_t)~s.sorted[i];
+                        }
+                    }
+                    __syncthreads();
+                }
+                row.adopt();
+            }
+        }
+        if (!done) row.template cut_by_bits<true>(target);
+    }
+    uint64_t whole;
+    const uint32_t token = row.locate(share, [&](float v, uint32_t i) -> uint64_t {
+        if (!row.kept(key_of(v), i)) return 0;
+        const uint64_t w = row.weight(v);
+        return w >= row.least ? w : 0;
+    }, &whole);
+    if (lead) answer(token, logit_of(row.key_at(token)), whole);
+    join();
 }
 
 }  // namespace
@@ -379,15 +789,32 @@ extern "C" int ninfer_sample(const ninfer_sample_args *args, ninfer_stream strea
     for (const void *q : {(const void *)a.temperature, (const void *)a.top_p, (const void *)a.min_p, (const void *)a.top_k,
                           (const void *)a.random, (const void *)a.tokens, (const void *)a.logprobs})
         if (!aligned(q, 4)) return fail(NINFER_ERR_ALIGNMENT, "sample: controls and outputs must be 4-byte aligned");
+    DeviceInfo d;
+    int st = device_info(&d);
+    if (st) return st;
     SampleParams p;
     p.a = a;
     int bits = 1;
     while ((1ull << bits) < a.vocab) ++bits;
     p.scale = 62 - bits;
-    const unsigned ranks = kMostCluster;
-    p.slice = (uint32_t)((a.vocab + ranks - 1) / ranks + 7) / 8 * 8;
+    // CTAs a row: as many as make a slice fit two times into an SM, more where few rows leave SMs without work
+    const uint64_t es = dtype_size(a.dtype), vectors = (a.vocab * es + 15) / 16 + 1;
+    unsigned ranks = 1;
+    while (ranks < kMostCluster && ((vectors + ranks - 1) / ranks * 16 > kSliceBytes ||
+                                    (a.rows * ranks * 2 <= (uint64_t)d.sms * kResident && a.vocab > (uint64_t)ranks * kLeastSlice)))
+        ranks *= 2;
+    p.vectors = (uint32_t)((vectors + ranks - 1) / ranks);
+    // a CTA's sums in 32 bits; beside a unit's rounding, the bins' and the floats' that add them up are under 2^-12
+    const uint64_t tokens = p.vectors * (16 / es);
+    p.unit = (float)std::min<uint64_t>(65535, 0xfffffff0ull / tokens);
+    p.slack = 0x1p-12f + 1.02f / p.unit;
+    p.held = p.vectors * 16ull <= kMostSliceBytes;
     const auto kernel = a.dtype == NINFER_F32    ? sample_kernel<NINFER_F32>
                         : a.dtype == NINFER_BF16 ? sample_kernel<NINFER_BF16>
                                                  : sample_kernel<NINFER_F16>;
-    return launch_clusters("sample", ranks, kernel, dim3((unsigned)(a.rows * ranks)), dim3(kThreads), 0, (cudaStream_t)stream, p);
+    const uint32_t smem = p.held ? p.vectors * 16 : 0;
+    st = set_smem_attribute(reinterpret_cast<const void *>(kernel), kMostSliceBytes);
+    if (!st && ranks > 8) st = set_wide_clusters(reinterpret_cast<const void *>(kernel));
+    if (st) return st;
+    return launch_clusters("sample", ranks, kernel, dim3((unsigned)(a.rows * ranks)), dim3(kThreads), smem, (cudaStream_t)stream, p);
 }

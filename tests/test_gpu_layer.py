@@ -306,6 +306,30 @@ def test_sample(vocab, dtype):
     check_sample(x, random, **controls)
 
 
+@pytest.mark.parametrize("rows,vocab,dtype", [(2, 1500001, "f32"), (1, 6000000, "bf16"), (40, 100003, "f16"), (200, 9001, "f32"), (330, 2049, "bf16")])
+def test_sample_other_divisions(rows, vocab, dtype):
+    """Rows too long for shared memory, rows of two to eight CTAs, of one."""
+    g = torch.Generator("cuda").manual_seed(vocab)
+    x = (torch.randn(rows, vocab, generator=g, device=DEV) * 2).to(TORCH[dtype])
+    rng = np.random.default_rng(rows)
+    pick = [CONTROLS[int(i)] for i in rng.integers(0, len(CONTROLS), rows)]
+    pick[0] = dict(top_p=0.95)
+    controls = {n: [{**DEFAULT, **c}[n] for c in pick] for n in DEFAULT}
+    check_sample(x, rng.random(rows), **controls)
+
+
+def test_sample_large_sets():
+    """Nuclei and top-k of most of a row, borders inside thousands of equal logits."""
+    rng = np.random.default_rng(21)
+    x = randn(rng, (12, 60000), "f32", 0.3)
+    x[6:] = (x[6:] * 4).round() / 4
+    controls = dict(top_k=[0, 50000, 3000, 1500, 59999, 0, 0, 50000, 3000, 1500, 59999, 0],
+                    top_p=[0.9, 1, 0.7, 1, 0.99, 0.9995, 0.9, 1, 0.7, 1, 0.99, 0.9995], temperature=[1, 2, 1, 1, 0.5, 3] * 2)
+    for seed in range(3):
+        check_sample(x, np.random.default_rng(seed).random(12), **controls)
+    check_sample(x, rng.random(12), min_p=[0.2] * 12)
+
+
 def test_sample_one_row_without_controls():
     rng = np.random.default_rng(4)
     x = randn(rng, (1, 248320), "f32", 3)
