@@ -18,6 +18,7 @@
 // to the exact sum of what lies above. Where more than 2048 tokens lie there (equal logits without end), the border comes from the
 // key's bits, eight at a time. Rows that keep few tokens (top-k up to 1024, min-p) have all of them sorted and chosen from by that CTA.
 #include <cmath>
+#include <cstddef>
 
 #include "decode.cuh"
 #include "gemv.h"
@@ -80,28 +81,43 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 constexpr uint32_t kLowest = 0x007fffffu;       // the key of -infinity
 
+// f * whole for 0 <= f <= 1, exactly, rounded down (up).
+__device__ __forceinline__ uint64_t times(float f, uint64_t whole, bool up) {
+    const uint32_t bits = __float_as_uint(f), e = max(bits >> 23, 1u), k = 150 - e;      // f = mantissa 2^-k, k from 23 on
+    const uint64_t mantissa = (bits & 0x7fffffu) | (bits >> 23 ? 0x800000u : 0u);
+    const uint64_t low = whole * mantissa, high = __umul64hi(whole, mantissa);
+    uint64_t t = k < 64 ? high << (64 - k) | low >> k : k < 128 ? high >> (k - 64) : 0;
+    if (up && (k < 64 ? low << (64 - k) : low | (k < 128 ? k > 64 ? high << (128 - k) : 0 : high))) ++t;
+    return t;
+}
+
 struct alignas(16) Shared {
     uint32_t powers[64];
     uint64_t part[kWarps], slot[2][2], found[2][2];
-    uint32_t hist[kBins], totals[kBins], list[kListed], listed, first;
-    uint64_t sorted[kListed];
+    alignas(16) uint32_t hist[kBins];           // hist and totals: together also the weights of kListed tokens
+    alignas(16) uint32_t totals[kBins];
+    alignas(16) uint64_t sorted[kListed];
+    uint32_t list[kListed], listed, first;
     float part_f[kWarps];
-    float c_hi, c_lo;
     struct {
         uint64_t above, inside;
         uint32_t bin, bin2, border, last;
         bool over;
     } cut;
     uint64_t target;
-    uint64_t least;
+    uint32_t starts[kMostCluster + 1];
 };
+
+static_assert(offsetof(Shared, hist) % 16 == 0 && offsetof(Shared, totals) == offsetof(Shared, hist) + kBins * 4 && offsetof(Shared, totals) % 16 == 0 &&
+                  offsetof(Shared, sorted) % 16 == 0 && 2 * kBins * 4 >= kListed * 8 && kBins == 4 * kThreads && kListed == 4 * kThreads,
+              "vector loads, and arrays that serve twice");
 
 template <int kDtype>
 struct Row {
     static constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs;
     const uint8_t *x;
     Shared &s;
-    const uint4 *held;          // the slice in shared memory, or null
+    const bool held;            // the slice, in shared memory
     uint32_t vocab, shift;      // elements between the last 16-byte boundary and the row's first
     uint32_t v0, v1;            // this CTA's 16-byte vectors, counted from that boundary
     uint32_t rank, ranks;
@@ -113,7 +129,7 @@ struct Row {
     uint32_t border = kLowest + 1, last = ~0u;
     uint64_t least = 0;
 
-    __device__ Row(const uint8_t *x, Shared &s, const uint4 *held, uint32_t vocab, int scale) : x(x), s(s), held(held), vocab(vocab), scale(scale) {
+    __device__ Row(const uint8_t *x, Shared &s, bool held, uint32_t vocab, int scale) : x(x), s(s), held(held), vocab(vocab), scale(scale) {
         shift = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) / kEs;
         rank = cluster_ctarank();
         ranks = cluster_nctarank();
@@ -136,21 +152,28 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    // f(x, place) for every element of vectors from + first, from + first + step ..., NaN as -infinity, until `to`; places before the row's
+    template <class F>
+    __device__ __forceinline__ void elements(const uint4 &u, uint32_t first, F f) const {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < kVec; ++j) {
+            const uint32_t h = w[j * kEs / 4];
+            const float y = kEs == 4 ? __uint_as_float(h)
+                            : kDtype == NINFER_BF16 ? __uint_as_float(j & 1 ? h & 0xffff0000u : h << 16)
+                                                    : __half2float(__ushort_as_half((uint16_t)(j & 1 ? h >> 16 : h & 0xffff)));
+            f(fmaxf(y, -INFINITY), first + j);
+        }
+    }
+    // f(x, place) for every element of vectors from, from + step ..., NaN as -infinity, until `to`; places before the row's
     // first and behind its last have -infinity
     template <class F>
     __device__ __forceinline__ void over(uint32_t from, uint32_t to, uint32_t step, F f) const {
+        extern __shared__ __align__(16) uint4 slice[];
         for (uint32_t v = from; v < to; v += step) {
-            const uint4 u = held ? held[v - v0] : read(v);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int j = 0; j < kVec; ++j) {
-                const uint32_t h = w[j * kEs / 4];
-                const float y = kEs == 4 ? __uint_as_float(h)
-                                : kDtype == NINFER_BF16 ? __uint_as_float(j & 1 ? h & 0xffff0000u : h << 16)
-                                                        : __half2float(__ushort_as_half((uint16_t)(j & 1 ? h >> 16 : h & 0xffff)));
-                f(fmaxf(y, -INFINITY), v * kVec - shift + j);
-            }
+            uint4 u;
+            if (held) u = slice[v - v0];
+            else u = read(v);
+            elements(u, v * kVec - shift, f);
         }
     }
     template <class F>
@@ -159,27 +182,24 @@ struct Row {
     __device__ __forceinline__ uint32_t key_at(uint32_t i) const { return key_of(fmaxf(load1(x, i, kDtype), -INFINITY)); }
     __device__ __forceinline__ bool kept(uint32_t key, uint32_t i) const { return key > border || (key == border && i <= last); }
 
-    // t as two floats; false where 2^t is no more than 2^-100 (or the logit infinitely far away)
-    __device__ __forceinline__ bool exponent(float v, float &p, float &rest) const {
-        p = rest = 0.f;
-        if (v == m) return true;
-        const float d = v - m, b = d + m, e = (v - b) - (m - (b - d));      // d + e = v - m exactly
-        p = d * c_hi;
-        if (!(p >= -100.f)) return false;
-        rest = fmaf(d, c_hi, -p) + fmaf(d, c_lo, e * c_hi);
-        return true;
+    // t as two floats; -100 and less as -100 (and `rest` without a meaning)
+    __device__ __forceinline__ float exponent(float v, float &rest) const {
+        const float d = v == m ? 0.f : v - m, b = d + m, e = (v - b) - (m - (b - d));      // d + e = v - m exactly
+        const float p = d * c_hi;
+        rest = v == m ? 0.f : fmaf(d, c_hi, -p) + fmaf(d, c_lo, e * c_hi);
+        return fmaxf(p, -100.f);
     }
     __device__ __forceinline__ uint64_t weight(float v) const {
-        float p, rest;
-        if (!exponent(v, p, rest)) return 0;
+        float rest;
+        const float p = exponent(v, rest);
         const int n = __float2int_rn(p * 64.f);
         const float r = fmaf((float)n, -1.f / 64.f, p) + rest;       // exact but for `rest`, at most 1 / 128
         const float y = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);        // 2^r - 1
         const int power = (int)s.powers[n & 63];
         const uint32_t w = (uint32_t)(power + __mulhi(power, __float2int_rn(y * 0x1p32f)));     // of 2^(t - n / 64's whole part), times 2^30
-        const int shift = (n >> 6) + scale - 30;
-        if (shift >= 0) return (uint64_t)w << shift;
-        return shift < -31 ? 0 : ((uint64_t)w + (1ull << (-shift - 1))) >> -shift;
+        // times 2^(n / 64 + scale - 30), which is at most 2^31, rounded; nothing is left of what is 2^-100 and less, whatever w
+        const int right = min(61 - scale - (n >> 6), 63);
+        return (((uint64_t)(w & 0x7fffffffu) << 31) + ((1ull << right) >> 1)) >> right;
     }
     // How many bins a logit lies below the largest one, kBins and more for none; falling logits have rising bins. `part`: of a bin.
     __device__ __forceinline__ uint32_t bin_of(float v, float &part) const {
@@ -265,9 +285,7 @@ struct Row {
 #pragma unroll
         for (int k = 16; k; k /= 2) ahead += __shfl_xor_sync(~0u, ahead, k);
         before += ahead;
-        if (threadIdx.x == 0) s.target = target(total);
-        __syncthreads();
-        const uint64_t goal = s.target;
+        const uint64_t goal = target(total);
         if (goal >= before && goal - before < sum) {                // one warp of the cluster
             uint64_t run = goal - before;                            // what is still to be passed
             for (uint32_t v = from; v < to; v += 32) {
@@ -301,14 +319,18 @@ struct Row {
     template <bool kWeights>
     __device__ void merge(float unit) {
         join();
-        const uint32_t part = kBins / ranks;
-        for (uint32_t i = threadIdx.x; i < part; i += kThreads) {
-            const uint32_t b = rank * part + i;
-            uint64_t t = 0;
-            for (uint32_t r = 0; r < ranks; ++r) t += ld_cluster_u32(&s.hist[b], r);
+        // a lane a CTA: kBins words in all, four a thread
+        const uint32_t from = threadIdx.x % ranks, part = kBins / ranks, step = kThreads / ranks, first = rank * part + threadIdx.x / ranks;
+        uint64_t t[kBins / kThreads];
+#pragma unroll
+        for (int i = 0; i < (int)(kBins / kThreads); ++i) t[i] = ld_cluster_u32(&s.hist[first + i * step], from);
+#pragma unroll
+        for (int i = 0; i < (int)(kBins / kThreads); ++i) {
+            const uint32_t b = first + i * step;
+            for (uint32_t k = ranks / 2; k; k /= 2) t[i] += __shfl_xor_sync(~0u, t[i], k);
             // a weight as a float, of the row's largest one
-            const uint32_t word = kWeights ? __float_as_uint((float)t * unit * exp2f((float)b * (-1.f / 64.f))) : (uint32_t)t;
-            for (uint32_t r = 0; r < ranks; ++r) st_cluster_u32(&s.totals[b], r, word);
+            const uint32_t word = kWeights ? __float_as_uint((float)t[i] * unit * exp2f((float)b * (-1.f / 64.f))) : (uint32_t)t[i];
+            st_cluster_u32(&s.totals[b], from, word);
         }
         join();
     }
@@ -354,22 +376,46 @@ struct Row {
 
     // The first CTA: the lists of all, as (key, place) in falling order of keys and rising of places, in `sorted`; returns how many.
     __device__ uint32_t gather() {
-        uint32_t n = 0;
-        for (uint32_t r = 0; r < ranks; ++r) {
-            const uint32_t count = ld_cluster_u32(&s.listed, r);
-            for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
-                const uint32_t place = ld_cluster_u32(&s.list[i], r);
-                s.sorted[n + i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
+        if (threadIdx.x < 32) {
+            uint32_t count = threadIdx.x < ranks ? ld_cluster_u32(&s.listed, threadIdx.x) : 0;
+#pragma unroll
+            for (int k = 1; k < 32; k *= 2) {
+                const uint32_t u = __shfl_up_sync(~0u, count, k);
+                if (threadIdx.x >= (uint32_t)k) count += u;
             }
-            n += count;
+            if (threadIdx.x < ranks) s.starts[threadIdx.x + 1] = count;
+            if (threadIdx.x == 0) s.starts[0] = 0;
         }
         __syncthreads();
+        const uint32_t n = s.starts[ranks];
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+            uint32_t r = 0;
+            while (i >= s.starts[r + 1]) ++r;
+            const uint32_t place = ld_cluster_u32(&s.list[i - s.starts[r]], r);
+            s.sorted[i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
+        }
         sort(n);
         return n;
     }
     // `sorted` in falling order, with zeros behind the n first.
     __device__ void sort(uint32_t n) {
-        uint32_t size = 64;
+        __syncthreads();
+        if (n <= kThreads) {        // each one's number is how many are larger
+            const uint64_t mine = threadIdx.x < n ? s.sorted[threadIdx.x] : 0;
+            if (threadIdx.x == n) s.sorted[n] = 0;
+            __syncthreads();
+            uint32_t larger = 0;
+            if (threadIdx.x < n)
+                for (uint32_t i = 0; i < n; i += 2) {
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.sorted[i]);
+                    larger += (two.x > mine) + (two.y > mine);
+                }
+            __syncthreads();
+            if (threadIdx.x < n) s.sorted[larger] = mine;
+            __syncthreads();
+            return;
+        }
+        uint32_t size = 1024;
         while (size < n) size *= 2;
         for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) s.sorted[i] = 0;
         __syncthreads();
@@ -450,12 +496,11 @@ struct Row {
                 } else atomicAdd(&bin->x, 1u);
             });
             join();
-            const uint32_t part = 256 / ranks;
-            if (threadIdx.x < part) {
-                const uint32_t b = rank * part + threadIdx.x;
-                uint64_t t = 0;
-                for (uint32_t r = 0; r < ranks; ++r) t += ld_cluster_u64(&hist[b], r);
-                for (uint32_t r = 0; r < ranks; ++r) st_cluster_u64(&totals[b], r, t);
+            if (threadIdx.x < 256) {
+                const uint32_t from = threadIdx.x % ranks, b = rank * (256 / ranks) + threadIdx.x / ranks;
+                uint64_t t = ld_cluster_u64(&hist[b], from);
+                for (uint32_t k = ranks / 2; k; k /= 2) t += __shfl_xor_sync(~0u, t, k);
+                st_cluster_u64(&totals[b], from, t);
             }
             join();
             // from the highest bin on: the one in which the sum reaches the target
@@ -498,7 +543,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     const ninfer_sample_args &a = p.a;
     const uint32_t ranks = cluster_nctarank(), vocab = (uint32_t)a.vocab;
     const uint64_t b = blockIdx.x / ranks;
-    R row(static_cast<const uint8_t *>(a.logits) + b * a.stride * R::kEs, s, p.held ? slice : nullptr, vocab, p.scale);
+    R row(static_cast<const uint8_t *>(a.logits) + b * a.stride * R::kEs, s, p.held, vocab, p.scale);
     const uint32_t all = (row.shift + vocab + R::kVec - 1) / R::kVec;      // the row's vectors
     row.v0 = min(row.rank * p.vectors, all);
     row.v1 = min(row.v0 + p.vectors, all);
@@ -506,13 +551,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     const float temperature = a.temperature ? a.temperature[b] : 1.f, top_p = a.top_p ? a.top_p[b] : 1.f;
     const float min_p = a.min_p ? a.min_p[b] : 0.f, random = a.random[b];
     const int32_t top_k = a.top_k ? a.top_k[b] : 0;
-    if (tid == 0) {
-        const double c = 1.4426950408889634 / (double)temperature;
-        s.c_hi = (float)c;
-        s.c_lo = (float)(c - (double)s.c_hi);
-        s.least = min_p > 0.f ? (uint64_t)ceil(ldexp((double)fminf(min_p, 1.f), p.scale)) : 0;
-        s.first = ~0u;
-    }
+    if (tid == 0) s.first = ~0u;
     // the row into shared memory, and its largest logit
     float most = -INFINITY;
     if (p.held) {
@@ -551,50 +590,51 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         return;
     }
     row.m = top;
-    row.c_hi = s.c_hi;
-    row.c_lo = isfinite(s.c_hi) ? s.c_lo : 0.f;
-    row.least = s.least;
+    // log2(e) / temperature
+    row.c_hi = __fdiv_rn(1.44269504f, temperature);
+    row.c_lo = __fdiv_rn(fmaf(-row.c_hi, temperature, 1.44269504f) + 1.92596299e-8f, temperature);
+    if (!isfinite(row.c_lo)) row.c_lo = 0.f;
+    if (min_p > 0.f) row.least = times(fminf(min_p, 1.f), 1ull << p.scale, true);
     const bool by_k = top_k > 0 && (uint32_t)top_k < vocab, by_p = top_p < 1.f, by_m = min_p > 0.f;
     // the share of a whole that the random number says, and the logarithm of a token's share
     auto share = [&](uint64_t whole) {
-        const uint64_t t = (uint64_t)((double)fminf(fmaxf(random, 0.f), 1.f) * (double)whole);
-        return min(t, whole - 1);
+        return min(times(fminf(fmaxf(random, 0.f), 1.f), whole, false), whole - 1);
     };
     auto answer = [&](uint32_t token, float logit, uint64_t whole) {
         a.tokens[b] = (int32_t)token;
         if (!a.logprobs) return;
-        float t, rest;
-        row.exponent(logit, t, rest);
+        float rest;
+        const float t = row.exponent(logit, rest);
         // the sum in units of the largest weight, which is 2^scale and among those kept
         a.logprobs[b] = (t + rest) * 0.69314718f - log1pf((float)(whole - (1ull << p.scale)) * __uint_as_float((uint32_t)(127 - p.scale) << 23));
     };
 
     // few tokens kept: those down to bin `few` hold them all
     uint32_t few = kBins;
-    bool cut_k = by_k;
-    if (by_k) {
-        row.clear();
-        row.each([&](float v, uint32_t) {
-            float part;
-            const uint32_t bin = v == -INFINITY ? kBins : row.bin_of(v, part);
-            if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
-        });
-        row.template merge<false>(1.f);
+    auto reach = [&](uint64_t wanted) {     // the bin in which the counts reach it, what lies above, and both
         uint64_t sums[4];
         row.running(sums);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint64_t before = sums[j] - s.totals[tid * 4 + j];
-            if (before < (uint32_t)top_k && sums[j] >= (uint32_t)top_k) {
+            if (before < wanted && sums[j] >= wanted) {
                 s.cut.bin = tid * 4 + j;
                 s.cut.above = before;
                 s.cut.inside = sums[j];
             }
         }
         __syncthreads();
-        if (s.cut.bin < kBins && s.cut.inside <= kListed && top_k <= (int32_t)kFew) few = s.cut.bin;
-    }
-    if (!by_k && by_m && !by_p) {
+        return s.cut.bin;
+    };
+    if (by_k && (uint32_t)top_k <= kFew && (uint32_t)top_k * 5 < ranks * kThreads * 4) {
+        // where top_k of the threads have a logit, top_k logits are: hardly more, while they are few among the threads
+        row.clear();
+        float part;
+        const uint32_t bin = most == -INFINITY ? kBins : row.bin_of(most, part);
+        if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
+        row.template merge<false>(1.f);
+        few = reach((uint32_t)top_k);
+    } else if (!by_k && by_m && !by_p) {
         row.clear();
         const float u = -64.f * log2f(fminf(min_p, 1.f)) + 1.f;       // a bin further, for what the logarithm and the bins round
         if (u < (float)kBins) few = (uint32_t)u;
@@ -618,12 +658,9 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 __syncthreads();
                 whole = s.target;
                 __syncthreads();
-                if (tid == 0) {
-                    s.target = by_p ? max((uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)whole), (uint64_t)1) : ~0ull;
-                    s.cut.bin2 = 0;
-                }
+                if (tid == 0) s.cut.bin2 = 0;
                 __syncthreads();
-                const uint64_t goal = s.target;
+                const uint64_t goal = by_p ? max(times(fmaxf(top_p, 0.f), whole, true), (uint64_t)1) : ~0ull;
                 uint64_t mine = 0;
                 uint32_t end = 0;
 #pragma unroll
@@ -638,10 +675,8 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 end = __reduce_max_sync(~0u, end);
                 if (lane == 0) atomicMax(&s.cut.bin2, end);
                 whole = row.block_sum(mine);        // of those kept: the first s.cut.bin2
-                if (tid == 0) s.target = share(whole);
-                __syncthreads();
                 const uint32_t kept = s.cut.bin2;
-                const uint64_t passed = s.target;
+                const uint64_t passed = share(whole);
                 // sorted by places, the one whose running sum is the first past the share
                 uint64_t *weights = reinterpret_cast<uint64_t *>(s.hist);       // hist and totals, which are done with
 #pragma unroll
@@ -666,9 +701,16 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             return;
         }
     }
-    if (cut_k) {
+    if (by_k) {
         // many: the border alone
-        const uint32_t bin = s.cut.bin;
+        row.clear();
+        row.each([&](float v, uint32_t) {
+            float part;
+            const uint32_t bin = v == -INFINITY ? kBins : row.bin_of(v, part);
+            if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
+        });
+        row.template merge<false>(1.f);
+        const uint32_t bin = reach((uint32_t)top_k);
         const uint64_t above = s.cut.above, inside = s.cut.inside - above;
         __syncthreads();
         if (bin < kBins && inside <= kListed) {
@@ -710,9 +752,8 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         sum = row.block_sum(sum);
         row.exchange(sum);
         sum = row.collect();
-        if (tid == 0) s.target = max((uint64_t)ceil((double)fmaxf(top_p, 0.f) * (double)sum), (uint64_t)1);
+        const uint64_t target = max(times(fmaxf(top_p, 0.f), sum, true), (uint64_t)1);
         row.template merge<true>(1.f / p.unit);
-        const uint64_t target = s.target;
         // the border lies between where the bins' sums with all that they may lack reach the target and where they do with as much less
         const float goal = (float)target * __uint_as_float((uint32_t)(127 - p.scale) << 23);
         float sums[4];
