@@ -17,6 +17,7 @@
 // in which it lies; their tokens, seldom more than a few hundred, are sorted by the cluster's first CTA, which adds their exact weights
 // to the exact sum of what lies above. Where more than 2048 tokens lie there (equal logits without end), the border comes from the
 // key's bits, eight at a time. Rows that keep few tokens (top-k up to 1024, min-p) have all of them sorted and chosen from by that CTA.
+#include <cfloat>
 #include <cmath>
 #include <cstddef>
 
@@ -30,6 +31,10 @@ namespace {
 constexpr int kThreads = 512, kWarps = kThreads / 32, kResident = 2;    // CTAs an SM
 constexpr uint32_t kBins = 2048, kListed = 2048, kFew = 1024, kMostCluster = 16;
 constexpr uint32_t kSliceBytes = 64 * 1024, kMostSliceBytes = 176 * 1024, kLeastSlice = 2048;  // two CTAs an SM, one; tokens
+
+// Added to a float below 2^22, it leaves the nearest whole number in the last bits (conversions go at a sixteenth of the rate of additions);
+// kDown, with the sum rounded down, the whole part of one from 0 to 2^23.
+constexpr float kRound = 12582912.f, kDown = 8388608.f;
 
 // 2^(30 + j / 64), rounded
 __device__ const uint32_t kPowers[64] = {
@@ -79,7 +84,6 @@ __device__ __forceinline__ uint32_t key_of(float x) {
     return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float logit_of(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
-constexpr uint32_t kLowest = 0x007fffffu;       // the key of -infinity
 
 // f * whole for 0 <= f <= 1, exactly, rounded down (up).
 __device__ __forceinline__ uint64_t times(float f, uint64_t whole, bool up) {
@@ -93,18 +97,17 @@ __device__ __forceinline__ uint64_t times(float f, uint64_t whole, bool up) {
 
 struct alignas(16) Shared {
     uint32_t powers[64];
-    uint64_t part[kWarps], slot[2][2], found[2][2];
+    uint64_t part[kWarps], slot[2][2][kMostCluster], found[2];
     alignas(16) uint32_t hist[kBins];           // hist and totals: together also the weights of kListed tokens
     alignas(16) uint32_t totals[kBins];
     alignas(16) uint64_t sorted[kListed];
-    uint32_t list[kListed], listed, first;
-    float part_f[kWarps];
+    uint32_t list[kListed], listed, lowest;     // lowest: ~0 before the kernel begins with it
     struct {
         uint64_t above, inside;
         uint32_t bin, bin2, border, last;
         bool over;
     } cut;
-    uint64_t target;
+    uint64_t target, all;
     uint32_t starts[kMostCluster + 1];
 };
 
@@ -116,8 +119,8 @@ template <int kDtype>
 struct Row {
     static constexpr int kEs = kDtype == NINFER_F32 ? 4 : 2, kVec = 16 / kEs;
     const uint8_t *x;
-    Shared &s;
-    const bool held;            // the slice, in shared memory
+    Shared *shared;
+    bool held;                  // the slice, in shared memory
     uint32_t vocab, shift;      // elements between the last 16-byte boundary and the row's first
     uint32_t v0, v1;            // this CTA's 16-byte vectors, counted from that boundary
     uint32_t rank, ranks;
@@ -125,11 +128,12 @@ struct Row {
     uint32_t phase = 0;
     // the row's largest logit, log2(e) / temperature in two floats
     float m = 0.f, c_hi = 0.f, c_lo = 0.f;
-    // what is kept: keys above `border`, and at it those up to place `last`; weights of at least `least`
-    uint32_t border = kLowest + 1, last = ~0u;
+    // what is kept: logits above `border`, and at it those up to place `last`; weights of at least `least`
+    float border = -FLT_MAX;
+    uint32_t last = ~0u;
     uint64_t least = 0;
 
-    __device__ Row(const uint8_t *x, Shared &s, bool held, uint32_t vocab, int scale) : x(x), s(s), held(held), vocab(vocab), scale(scale) {
+    __device__ Row(const uint8_t *x, Shared *shared, bool held, uint32_t vocab, int scale) : x(x), shared(shared), held(held), vocab(vocab), scale(scale) {
         shift = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) / kEs;
         rank = cluster_ctarank();
         ranks = cluster_nctarank();
@@ -152,88 +156,107 @@ struct Row {
         }
         return make_uint4(w[0], w[1], w[2], w[3]);
     }
-    template <class F>
-    __device__ __forceinline__ void elements(const uint4 &u, uint32_t first, F f) const {
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int j = 0; j < kVec; ++j) {
-            const uint32_t h = w[j * kEs / 4];
-            const float y = kEs == 4 ? __uint_as_float(h)
-                            : kDtype == NINFER_BF16 ? __uint_as_float(j & 1 ? h & 0xffff0000u : h << 16)
-                                                    : __half2float(__ushort_as_half((uint16_t)(j & 1 ? h >> 16 : h & 0xffff)));
-            f(fmaxf(y, -INFINITY), first + j);
-        }
-    }
-    // f(x, place) for every element of vectors from, from + step ..., NaN as -infinity, until `to`; places before the row's
-    // first and behind its last have -infinity
+    // f(four neighbouring logits, the first's place) for the 16-byte vectors from, from + step ... before `to`; NaN and what is not of the row as
+    // -infinity. Four at once, and f without branches but one around them all: a thread has few logits, and a chain of dependent
+    // instructions takes 150 to 250 cycles for each.
     template <class F>
     __device__ __forceinline__ void over(uint32_t from, uint32_t to, uint32_t step, F f) const {
         extern __shared__ __align__(16) uint4 slice[];
-        for (uint32_t v = from; v < to; v += step) {
+#pragma unroll 1
+        for (uint32_t i = from; i < to; i += step) {
             uint4 u;
-            if (held) u = slice[v - v0];
-            else u = read(v);
-            elements(u, v * kVec - shift, f);
+            if (held) u = slice[i - v0];
+            else u = read(i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int q = 0; q < kVec; q += 4) {
+                float v[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = fmaxf(element(w, q + j), -INFINITY);
+                f(v, i * kVec - shift + q);
+            }
         }
+    }
+    static __device__ __forceinline__ float element(const uint32_t (&w)[4], int j) {
+        const uint32_t h = w[j * kEs / 4];
+        return kEs == 4 ? __uint_as_float(h)
+               : kDtype == NINFER_BF16 ? __uint_as_float(j & 1 ? h & 0xffff0000u : h << 16)
+                                       : __half2float(__ushort_as_half((uint16_t)(j & 1 ? h >> 16 : h & 0xffff)));
     }
     template <class F>
     __device__ __forceinline__ void each(F f) const { over(v0 + threadIdx.x, v1, kThreads, f); }
+    // The sum of value(x) over the places for which wanted(x, place) says so.
+    template <class W, class V>
+    __device__ __forceinline__ uint64_t sum_over(uint32_t from, uint32_t to, uint32_t step, W wanted, V value) const {
+        uint64_t sum = 0;
+        over(from, to, step, [&](const float (&v)[4], uint32_t i) {
+            bool in[4], any = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= in[j] = wanted(v[j], i + j);
+            if (!any) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint64_t w = value(v[j]);
+                sum += in[j] ? w : 0;
+            }
+        });
+        return sum;
+    }
 
     __device__ __forceinline__ uint32_t key_at(uint32_t i) const { return key_of(fmaxf(load1(x, i, kDtype), -INFINITY)); }
-    __device__ __forceinline__ bool kept(uint32_t key, uint32_t i) const { return key > border || (key == border && i <= last); }
+    __device__ __forceinline__ bool kept(float v, uint32_t i) const { return v > border || (v == border && i <= last); }
 
-    // t as two floats; -100 and less as -100 (and `rest` without a meaning)
+    // t as two floats (but for the rounding of x - m: 2^-24 t, another one for each token); -100 and less as -100 (and `rest` without a
+    // meaning)
     __device__ __forceinline__ float exponent(float v, float &rest) const {
-        const float d = v == m ? 0.f : v - m, b = d + m, e = (v - b) - (m - (b - d));      // d + e = v - m exactly
-        const float p = d * c_hi;
-        rest = v == m ? 0.f : fmaf(d, c_hi, -p) + fmaf(d, c_lo, e * c_hi);
+        const float d = v == m ? 0.f : v - m, p = d * c_hi;
+        rest = fmaf(d, c_lo, fmaf(d, c_hi, -p));
         return fmaxf(p, -100.f);
     }
     __device__ __forceinline__ uint64_t weight(float v) const {
         float rest;
         const float p = exponent(v, rest);
-        const int n = __float2int_rn(p * 64.f);
-        const float r = fmaf((float)n, -1.f / 64.f, p) + rest;       // exact but for `rest`, at most 1 / 128
+        const float z = fmaf(p, 64.f, kRound);
+        const int n = __float_as_int(z) - __float_as_int(kRound);
+        const float r = fmaf(z - kRound, -1.f / 64.f, p) + rest;     // exact but for `rest`, at most 1 / 128
         const float y = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);        // 2^r - 1
-        const int power = (int)s.powers[n & 63];
-        const uint32_t w = (uint32_t)(power + __mulhi(power, __float2int_rn(y * 0x1p32f)));     // of 2^(t - n / 64's whole part), times 2^30
+        const int power = (int)shared->powers[n & 63];
+        // of 2^(t - n / 64's whole part), times 2^30
+        const uint32_t w = (uint32_t)(power + __mulhi(power, (__float_as_int(fmaf(y, 0x1p29f, kRound)) - __float_as_int(kRound)) << 3));
         // times 2^(n / 64 + scale - 30), which is at most 2^31, rounded; nothing is left of what is 2^-100 and less, whatever w
         const int right = min(61 - scale - (n >> 6), 63);
         return (((uint64_t)(w & 0x7fffffffu) << 31) + ((1ull << right) >> 1)) >> right;
     }
-    // How many bins a logit lies below the largest one, kBins and more for none; falling logits have rising bins. `part`: of a bin.
-    __device__ __forceinline__ uint32_t bin_of(float v, float &part) const {
-        const float u = v == m ? 0.f : (m - v) * (c_hi * 64.f);
-        const float low = floorf(u);
-        part = u - low;
-        return u < (float)kBins ? (uint32_t)low : kBins;
-    }
+    // How many bins a logit lies below the largest one, with a fraction; falling logits have rising ones. NaN, which is below no number of
+    // bins, where both the temperature and the distance are infinite.
+    __device__ __forceinline__ float below(float v, float scale) const { return v == m ? 0.f : (m - v) * scale; }
+    __device__ __forceinline__ float below(float v) const { return below(v, c_hi * 64.f); }
 
     // Sum over the CTA; every thread gets it.
     __device__ uint64_t block_sum(uint64_t v) {
 #pragma unroll
         for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
         __syncthreads();
-        if (threadIdx.x % 32 == 0) s.part[threadIdx.x / 32] = v;
+        if (threadIdx.x % 32 == 0) shared->part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = threadIdx.x % 32 < kWarps ? s.part[threadIdx.x % 32] : 0;
+        v = threadIdx.x % 32 < kWarps ? shared->part[threadIdx.x % 32] : 0;
 #pragma unroll
         for (int k = 8; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
         return __shfl_sync(~0u, v, 0);
     }
-    // Puts two values of each CTA where the others see them. The slot of two exchanges ago is free: every CTA has read it
-    // before it came to the barrier of the last one.
+    // Gives two values of each CTA to all. The slots of two exchanges ago are free: every CTA has read its own before it came to the
+    // barrier of the last one. Nothing of another CTA is read behind the barrier, so that a CTA may end there.
     __device__ void exchange(uint64_t v, uint64_t w = 0) {
         phase ^= 1;
-        if (threadIdx.x == 0) {
-            s.slot[phase][0] = v;
-            s.slot[phase][1] = w;
+        if (threadIdx.x < ranks) {
+            st_cluster_u64(&shared->slot[phase][0][rank], threadIdx.x, v);
+            st_cluster_u64(&shared->slot[phase][1][rank], threadIdx.x, w);
         }
         join();
     }
     // The sums of both over the cluster.
     __device__ uint64_t collect(int which = 0) const {
-        uint64_t t = threadIdx.x % 32 < ranks ? ld_cluster_u64(&s.slot[phase][which], threadIdx.x % 32) : 0;
+        uint64_t t = threadIdx.x % 32 < ranks ? shared->slot[phase][which][threadIdx.x % 32] : 0;
 #pragma unroll
         for (int k = 8; k; k /= 2) t += __shfl_xor_sync(~0u, t, k);
         return __shfl_sync(~0u, t, 0);
@@ -242,102 +265,132 @@ struct Row {
         exchange(block_sum(v));
         return collect();
     }
-    // The largest float over the cluster.
-    __device__ float cluster_max(float v) {
+    // The largest v over the cluster, and the least of least_key.
+    __device__ uint64_t cluster_max(uint64_t v, uint32_t &least_key) {
+        const uint32_t lane = threadIdx.x % 32;
+        const uint32_t low = __reduce_min_sync(~0u, least_key);
+        if (lane == 0) atomicMin(&shared->lowest, low);
 #pragma unroll
-        for (int k = 16; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
-        if (threadIdx.x % 32 == 0) s.part_f[threadIdx.x / 32] = v;
+        for (int k = 16; k; k /= 2) v = max(v, __shfl_xor_sync(~0u, v, k));
+        if (lane == 0) shared->part[threadIdx.x / 32] = v;
         __syncthreads();
-        v = threadIdx.x % 32 < kWarps ? s.part_f[threadIdx.x % 32] : -INFINITY;
+        v = lane < kWarps ? shared->part[lane] : 0;
 #pragma unroll
-        for (int k = 8; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
-        exchange(__float_as_uint(v));
-        v = threadIdx.x % 32 < ranks ? __uint_as_float((uint32_t)ld_cluster_u64(&s.slot[phase][0], threadIdx.x % 32)) : -INFINITY;
+        for (int k = 8; k; k /= 2) v = max(v, __shfl_xor_sync(~0u, v, k));
+        exchange(v, shared->lowest);
+        v = lane < ranks ? shared->slot[phase][0][lane] : 0;
+        least_key = __reduce_min_sync(~0u, lane < ranks ? (uint32_t)shared->slot[phase][1][lane] : ~0u);
 #pragma unroll
-        for (int k = 8; k; k /= 2) v = fmaxf(v, __shfl_xor_sync(~0u, v, k));
+        for (int k = 8; k; k /= 2) v = max(v, __shfl_xor_sync(~0u, v, k));
         return __shfl_sync(~0u, v, 0);
     }
 
-    // The first place, in the order of the row, at which the running sum of value(x, place) passes target(whole sum).
-    template <class F, class T>
-    __device__ uint32_t locate(T target, F value, uint64_t *whole = nullptr) {
+    // The first place, in the order of the row, at which the running sum of value(x) over the wanted ones passes target(whole sum).
+    template <class T, class W, class V>
+    __device__ uint32_t locate(T target, W wanted, V value, uint64_t *whole = nullptr) {
         const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        const uint32_t each_ = ((v1 - v0 + kWarps - 1) / kWarps + 31) / 32 * 32;
-        const uint32_t from = min(v0 + warp * each_, v1), to = min(from + each_, v1);
-        uint64_t sum = 0;
-        over(from + lane, to, 32, [&](float v, uint32_t i) { sum += value(v, i); });
-#pragma unroll
-        for (int k = 16; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
-        __syncthreads();
-        if (lane == 0) s.part[warp] = sum;
-        __syncthreads();
-        const uint64_t mine = lane < kWarps ? s.part[lane] : 0;
-        uint64_t before = lane < warp ? mine : 0, all = mine;
-#pragma unroll
-        for (int k = 16; k; k /= 2) {
-            before += __shfl_xor_sync(~0u, before, k);
-            all += __shfl_xor_sync(~0u, all, k);
-        }
-        exchange(all);
+        const uint32_t part = (v1 - v0 + kWarps - 1) / kWarps, from = min(v0 + warp * part, v1);
+        uint64_t sum = sum_over(from + lane, min(from + part, v1), 32, wanted, value);
+        uint64_t before;                        // what lies before this CTA, then before its part that has the token, then the part's part
+        uint32_t at;
+        warps_sums(sum);
+        exchange(shared->all);
         const uint64_t total = collect();
         if (whole) *whole = total;
-        uint64_t ahead = lane < rank ? ld_cluster_u64(&s.slot[phase][0], lane) : 0;
+        before = lane < rank ? shared->slot[phase][0][lane] : 0;
 #pragma unroll
-        for (int k = 16; k; k /= 2) ahead += __shfl_xor_sync(~0u, ahead, k);
-        before += ahead;
+        for (int k = 8; k; k /= 2) before += __shfl_xor_sync(~0u, before, k);
+        before = __shfl_sync(~0u, before, 0);
         const uint64_t goal = target(total);
-        if (goal >= before && goal - before < sum) {                // one warp of the cluster
-            uint64_t run = goal - before;                            // what is still to be passed
-            for (uint32_t v = from; v < to; v += 32) {
-                uint64_t here[kVec], lanes = 0;
-                int n = 0;
-                over(v + lane < to ? v + lane : to, to, 32 * kThreads, [&](float y, uint32_t i) { lanes += here[n++] = value(y, i); });
-                uint64_t u = lanes;
-#pragma unroll
-                for (int k = 1; k < 32; k *= 2) {
-                    const uint64_t w = __shfl_up_sync(~0u, u, k);
-                    if (lane >= (uint32_t)k) u += w;
-                }
-                const uint32_t passed = __ballot_sync(~0u, u > run);
-                if (passed) {
-                    if (lane == (uint32_t)__ffs(passed) - 1) {
-                        uint64_t w = u - lanes;
-                        int j = 0;
-                        for (; j < n - 1 && (w += here[j]) <= run; ++j) {}
-                        for (uint32_t r = 0; r < ranks; ++r) st_cluster_u64(&s.found[phase][0], r, (v + lane) * kVec - shift + j);
+        if (goal >= before && goal - before < shared->all) {              // one CTA of the cluster
+            at = passing(goal - before, before);
+            const uint32_t first = v0 + at * part, end = min(first + part, v1), less = (part + kWarps - 1) / kWarps;
+            const uint32_t here = min(first + warp * less, end);
+            sum = sum_over(here + lane, min(here + less, end), 32, wanted, value);
+            __syncthreads();
+            warps_sums(sum);
+            at = passing(goal - before, before);
+            if (warp == at) {
+                uint64_t run = goal - before;                        // what is still to be passed
+                const uint32_t until = min((here + less) * kVec - shift, vocab);
+                for (uint32_t i = here ? here * kVec - shift : 0; i < until; i += 32) {
+                    uint64_t u = 0;
+                    if (i + lane < until) {
+                        const float v = fmaxf(load1(x, i + lane, kDtype), -INFINITY);
+                        if (wanted(v, i + lane)) u = value(v);
                     }
-                    break;
+#pragma unroll
+                    for (int k = 1; k < 32; k *= 2) {
+                        const uint64_t w = __shfl_up_sync(~0u, u, k);
+                        if (lane >= (uint32_t)k) u += w;
+                    }
+                    const uint32_t passed = __ballot_sync(~0u, u > run);
+                    if (passed) {
+                        if (lane < ranks) st_cluster_u64(&shared->found[phase], lane, i + __ffs(passed) - 1);
+                        break;
+                    }
+                    run -= __shfl_sync(~0u, u, 31);
                 }
-                run -= __shfl_sync(~0u, u, 31);
             }
         }
         join();
-        return (uint32_t)s.found[phase][0];
+        return (uint32_t)shared->found[phase];
+    }
+    // Each warp's sum of v in shared->part, all of them in shared->all.
+    __device__ void warps_sums(uint64_t v) {
+        const uint32_t lane = threadIdx.x % 32;
+#pragma unroll
+        for (int k = 16; k; k /= 2) v += __shfl_xor_sync(~0u, v, k);
+        __syncthreads();
+        if (lane == 0) shared->part[threadIdx.x / 32] = v;
+        __syncthreads();
+        uint64_t t = lane < kWarps ? shared->part[lane] : 0;
+#pragma unroll
+        for (int k = 8; k; k /= 2) t += __shfl_xor_sync(~0u, t, k);
+        if (threadIdx.x == 0) shared->all = t;
+        __syncthreads();
+    }
+    // Which warp's sum passes `run`; adds those before it to `before`.
+    __device__ uint32_t passing(uint64_t run, uint64_t &before) const {
+        const uint32_t lane = threadIdx.x % 32;
+        const uint64_t mine = lane < kWarps ? shared->part[lane] : 0;
+        uint64_t sum = mine;
+#pragma unroll
+        for (int k = 1; k < kWarps; k *= 2) {
+            const uint64_t u = __shfl_up_sync(~0u, sum, k);
+            if (lane >= (uint32_t)k) sum += u;
+        }
+        const uint32_t at = __ffs(__ballot_sync(~0u, lane < kWarps && sum > run)) - 1;
+        before += __shfl_sync(~0u, sum - mine, at);
+        return at;
     }
 
     // Adds up the cluster's histograms (counts, or weights of which a bin's largest times `unit` is 1) into `totals` of every CTA: a part each.
     template <bool kWeights>
     __device__ void merge(float unit) {
         join();
-        // a lane a CTA: kBins words in all, four a thread
-        const uint32_t from = threadIdx.x % ranks, part = kBins / ranks, step = kThreads / ranks, first = rank * part + threadIdx.x / ranks;
-        uint64_t t[kBins / kThreads];
+        // a lane a bin: 32 neighbouring ones of each CTA at once
+        const uint32_t part = kBins / ranks;
+        for (uint32_t i = threadIdx.x; i < part; i += kThreads) {
+            const uint32_t b = rank * part + i;
+            uint32_t word[kMostCluster];
 #pragma unroll
-        for (int i = 0; i < (int)(kBins / kThreads); ++i) t[i] = ld_cluster_u32(&s.hist[first + i * step], from);
+            for (uint32_t r = 0; r < kMostCluster; ++r) word[r] = r < ranks ? ld_cluster_u32(&shared->hist[b], r) : 0;
+            uint64_t t = 0;
 #pragma unroll
-        for (int i = 0; i < (int)(kBins / kThreads); ++i) {
-            const uint32_t b = first + i * step;
-            for (uint32_t k = ranks / 2; k; k /= 2) t[i] += __shfl_xor_sync(~0u, t[i], k);
+            for (uint32_t r = 0; r < kMostCluster; ++r) t += word[r];
             // a weight as a float, of the row's largest one
-            const uint32_t word = kWeights ? __float_as_uint((float)t[i] * unit * exp2f((float)b * (-1.f / 64.f))) : (uint32_t)t[i];
-            st_cluster_u32(&s.totals[b], from, word);
+            const uint32_t sum = kWeights ? __float_as_uint((float)t * unit * exp2f((float)b * (-1.f / 64.f))) : (uint32_t)t;
+#pragma unroll
+            for (uint32_t r = 0; r < kMostCluster; ++r)
+                if (r < ranks) st_cluster_u32(&shared->totals[b], r, sum);
         }
         join();
     }
     // Running sums over the bins' totals up to and with this thread's bins 4 tid .. 4 tid + 3.
     template <class T>
     __device__ void running(T (&sums)[4]) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(&s.totals[threadIdx.x * 4]);
+        const uint4 u = *reinterpret_cast<const uint4 *>(&shared->totals[threadIdx.x * 4]);
         const uint32_t w[4] = {u.x, u.y, u.z, u.w}, lane = threadIdx.x % 32, warp = threadIdx.x / 32;
         T v[4], run = 0;
 #pragma unroll
@@ -352,7 +405,7 @@ struct Row {
             if (lane >= (uint32_t)k) run += o;
         }
         __syncthreads();
-        T *parts = reinterpret_cast<T *>(s.part);
+        T *parts = reinterpret_cast<T *>(shared->part);
         if (lane == 31) parts[warp] = run;
         __syncthreads();
         run -= mine;
@@ -362,37 +415,44 @@ struct Row {
     }
 
     __device__ void clear() {
-        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) s.hist[i] = 0;
+        for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) shared->hist[i] = 0;
         if (threadIdx.x == 0) {
-            s.listed = 0;
-            s.cut.bin = s.cut.bin2 = kBins;
+            shared->listed = 0;
+            shared->cut.bin = shared->cut.bin2 = kBins;
         }
         __syncthreads();
     }
+    // A logit's weight into its bin, if it has one.
+    __device__ __forceinline__ void count(float v, bool in, float unit) {
+        const float at = below(v), z = __fadd_rd(at, kDown);
+        // 2^-x of the bin's fraction by its series, within 2^-22
+        const float part = (at - (z - kDown)) * (1.f / 64.f), share = fmaf(part, fmaf(part, 0.2402f, -0.69314718f), 1.f) * unit;
+        if (in && at < (float)kBins) atomicAdd(&shared->hist[__float_as_uint(z) & (kBins - 1)], __float_as_uint(__fadd_rd(share, kDown)) & 0x7fffffu);
+    }
     __device__ __forceinline__ void list(uint32_t place) {
-        const uint32_t at = atomicAdd(&s.listed, 1u);
-        if (at < kListed) s.list[at] = place;
+        const uint32_t at = atomicAdd(&shared->listed, 1u);
+        if (at < kListed) shared->list[at] = place;
     }
 
     // The first CTA: the lists of all, as (key, place) in falling order of keys and rising of places, in `sorted`; returns how many.
     __device__ uint32_t gather() {
         if (threadIdx.x < 32) {
-            uint32_t count = threadIdx.x < ranks ? ld_cluster_u32(&s.listed, threadIdx.x) : 0;
+            uint32_t count = threadIdx.x < ranks ? ld_cluster_u32(&shared->listed, threadIdx.x) : 0;
 #pragma unroll
             for (int k = 1; k < 32; k *= 2) {
                 const uint32_t u = __shfl_up_sync(~0u, count, k);
                 if (threadIdx.x >= (uint32_t)k) count += u;
             }
-            if (threadIdx.x < ranks) s.starts[threadIdx.x + 1] = count;
-            if (threadIdx.x == 0) s.starts[0] = 0;
+            if (threadIdx.x < ranks) shared->starts[threadIdx.x + 1] = count;
+            if (threadIdx.x == 0) shared->starts[0] = 0;
         }
         __syncthreads();
-        const uint32_t n = s.starts[ranks];
+        const uint32_t n = shared->starts[ranks];
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
             uint32_t r = 0;
-            while (i >= s.starts[r + 1]) ++r;
-            const uint32_t place = ld_cluster_u32(&s.list[i - s.starts[r]], r);
-            s.sorted[i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
+            while (i >= shared->starts[r + 1]) ++r;
+            const uint32_t place = ld_cluster_u32(&shared->list[i - shared->starts[r]], r);
+            shared->sorted[i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
         }
         sort(n);
         return n;
@@ -401,32 +461,32 @@ struct Row {
     __device__ void sort(uint32_t n) {
         __syncthreads();
         if (n <= kThreads) {        // each one's number is how many are larger
-            const uint64_t mine = threadIdx.x < n ? s.sorted[threadIdx.x] : 0;
-            if (threadIdx.x == n) s.sorted[n] = 0;
+            const uint64_t mine = threadIdx.x < n ? shared->sorted[threadIdx.x] : 0;
+            if (threadIdx.x == n) shared->sorted[n] = 0;
             __syncthreads();
             uint32_t larger = 0;
             if (threadIdx.x < n)
                 for (uint32_t i = 0; i < n; i += 2) {
-                    const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&s.sorted[i]);
+                    const ulonglong2 two = *reinterpret_cast<const ulonglong2 *>(&shared->sorted[i]);
                     larger += (two.x > mine) + (two.y > mine);
                 }
             __syncthreads();
-            if (threadIdx.x < n) s.sorted[larger] = mine;
+            if (threadIdx.x < n) shared->sorted[larger] = mine;
             __syncthreads();
             return;
         }
         uint32_t size = 1024;
         while (size < n) size *= 2;
-        for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) s.sorted[i] = 0;
+        for (uint32_t i = n + threadIdx.x; i < size; i += kThreads) shared->sorted[i] = 0;
         __syncthreads();
         for (uint32_t k = 2; k <= size; k *= 2)
             for (uint32_t j = k / 2; j; j /= 2) {
                 for (uint32_t i = threadIdx.x; i < size / 2; i += kThreads) {
                     const uint32_t a = 2 * i - (i & (j - 1)), b = a + j;
-                    const uint64_t x = s.sorted[a], y = s.sorted[b];
+                    const uint64_t x = shared->sorted[a], y = shared->sorted[b];
                     if ((x < y) == ((a & k) == 0)) {
-                        s.sorted[a] = y;
-                        s.sorted[b] = x;
+                        shared->sorted[a] = y;
+                        shared->sorted[b] = x;
                     }
                 }
                 // pairs less than 64 apart stay with a warp
@@ -445,10 +505,10 @@ struct Row {
             if (lane >= (uint32_t)k) run += o;
         }
         __syncthreads();
-        if (lane == 31) s.part[warp] = run;
+        if (lane == 31) shared->part[warp] = run;
         __syncthreads();
         run -= mine;
-        for (uint32_t k = 0; k < warp; ++k) run += s.part[k];
+        for (uint32_t k = 0; k < warp; ++k) run += shared->part[k];
 #pragma unroll
         for (int j = 0; j < 4; ++j) sums[j] = run += w[j];
     }
@@ -457,46 +517,50 @@ struct Row {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const uint32_t i = threadIdx.x * 4 + j;
-            w[j] = i < n ? weight(logit_of((uint32_t)(s.sorted[i] >> 32))) : 0;
+            w[j] = i < n ? weight(logit_of((uint32_t)(shared->sorted[i] >> 32))) : 0;
         }
         scan(w, sums);
     }
-    // Gives the border that the first CTA has put into s.cut to all.
+    // Gives the border that the first CTA has put into shared->cut to all.
     __device__ void adopt() {
         phase ^= 1;
         if (rank == 0 && threadIdx.x < ranks) {
-            st_cluster_u64(&s.found[phase][0], threadIdx.x, (uint64_t)s.cut.border << 32 | s.cut.last);
+            st_cluster_u64(&shared->found[phase], threadIdx.x, (uint64_t)shared->cut.border << 32 | shared->cut.last);
         }
         join();
-        border = (uint32_t)(s.found[phase][0] >> 32);
-        last = (uint32_t)s.found[phase][0];
+        border = logit_of((uint32_t)(shared->found[phase] >> 32));
+        last = (uint32_t)shared->found[phase];
     }
 
     // Moves the border to where the kept tokens' counts (kWeighted: weights), from the largest on, reach `target`, which
     // their sum does, its last token included; by the keys' bits, eight at a time.
     template <bool kWeighted>
-    __device__ __noinline__ void cut_by_bits(uint64_t target) {
-        uint2 *hist = reinterpret_cast<uint2 *>(s.hist);                // low and high words
-        uint64_t *totals = reinterpret_cast<uint64_t *>(s.totals);
+    __device__ __forceinline__ void by_bits(uint64_t target) {
+        uint2 *hist = reinterpret_cast<uint2 *>(shared->hist);                // low and high words
+        uint64_t *totals = reinterpret_cast<uint64_t *>(shared->totals);
         uint32_t prefix = 0;
         uint64_t above = 0;
         for (int shift_ = 24; shift_ >= 0; shift_ -= 8) {
             __syncthreads();
             if (threadIdx.x < 256) hist[threadIdx.x] = make_uint2(0, 0);
             __syncthreads();
-            each([&](float v, uint32_t i) {
-                const uint32_t k = key_of(v);
-                if (!kept(k, i) || (shift_ < 24 && k >> (shift_ + 8) != prefix)) return;
-                uint2 *bin = &hist[k >> shift_ & 255];
-                if (kWeighted) {
-                    const uint64_t w = weight(v);
-                    const uint32_t old = atomicAdd(&bin->x, (uint32_t)w);
-                    const uint32_t more = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
-                    if (more) atomicAdd(&bin->y, more);
-                } else atomicAdd(&bin->x, 1u);
+            each([&](const float (&v)[4], uint32_t i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t k = key_of(v[j]);
+                    if (!kept(v[j], i + j) || (shift_ < 24 && k >> (shift_ + 8) != prefix)) continue;
+                    uint2 *bin = &hist[k >> shift_ & 255];
+                    if (kWeighted) {
+                        const uint64_t w = weight(v[j]);
+                        const uint32_t old = atomicAdd(&bin->x, (uint32_t)w);
+                        const uint32_t more = (uint32_t)(w >> 32) + (old + (uint32_t)w < old);
+                        if (more) atomicAdd(&bin->y, more);
+                    } else atomicAdd(&bin->x, 1u);
+                }
             });
             join();
             if (threadIdx.x < 256) {
+                // a lane a CTA
                 const uint32_t from = threadIdx.x % ranks, b = rank * (256 / ranks) + threadIdx.x / ranks;
                 uint64_t t = ld_cluster_u64(&hist[b], from);
                 for (uint32_t k = ranks / 2; k; k /= 2) t += __shfl_xor_sync(~0u, t, k);
@@ -509,27 +573,32 @@ struct Row {
             scan(w, sums);
             const uint64_t before = above + sums[0] - mine;
             if (mine && before < target && target - before <= mine) {
-                s.cut.above = before;
-                s.cut.inside = mine;
-                s.cut.bin = 255 - threadIdx.x;
+                shared->cut.above = before;
+                shared->cut.inside = mine;
+                shared->cut.bin = 255 - threadIdx.x;
             }
             __syncthreads();
-            above = s.cut.above;
-            prefix = prefix << 8 | s.cut.bin;
+            above = shared->cut.above;
+            prefix = prefix << 8 | shared->cut.bin;
         }
         // the border's key is known; of the tokens that share it, the first in the row's order
-        const uint64_t one = kWeighted ? weight(logit_of(prefix)) : 1, ties = s.cut.inside / one;
+        const float edge = logit_of(prefix);
+        const uint64_t one = kWeighted ? weight(edge) : 1, ties = shared->cut.inside / one;
         const uint64_t wanted = (target - above + one - 1) / one;
-        uint32_t at = prefix == border ? last : ~0u;
-        if (wanted < ties) {
-            const uint32_t old = border, old_last = last;
-            at = locate([&](uint64_t) { return wanted - 1; },
-                        [&](float v, uint32_t i) -> uint64_t { return key_of(v) == prefix && (prefix != old || i <= old_last); });
-        }
-        border = prefix;
+        uint32_t at = edge == border ? last : ~0u;
+        if (wanted < ties)
+            at = locate([&](uint64_t) { return wanted - 1; }, [&](float v, uint32_t i) { return v == edge && kept(v, i); }, [](float) -> uint64_t { return 1; });
+        border = edge;
         last = at;
     }
 };
+
+// The row with its border moved, for the rows that come to it; out of line, and of a copy, so that others stay in registers.
+template <bool kWeighted, int kDtype>
+__device__ __noinline__ Row<kDtype> cut_by_bits(Row<kDtype> row, uint64_t target) {
+    row.template by_bits<kWeighted>(target);
+    return row;
+}
 
 template <int kDtype>
 __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __grid_constant__ SampleParams p) {
@@ -538,55 +607,65 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid % 32;
     if (tid < 64) s.powers[tid] = kPowers[tid];
+    if (tid == 64) s.lowest = ~0u;
+    __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_sample_args &a = p.a;
     const uint32_t ranks = cluster_nctarank(), vocab = (uint32_t)a.vocab;
     const uint64_t b = blockIdx.x / ranks;
-    R row(static_cast<const uint8_t *>(a.logits) + b * a.stride * R::kEs, s, p.held, vocab, p.scale);
-    const uint32_t all = (row.shift + vocab + R::kVec - 1) / R::kVec;      // the row's vectors
+    R row(static_cast<const uint8_t *>(a.logits) + b * a.stride * R::kEs, &s, p.held, vocab, p.scale);
+    const uint32_t all = (row.shift + vocab + R::kVec - 1) / R::kVec;      // the row's 16-byte vectors, from the boundary before it
     row.v0 = min(row.rank * p.vectors, all);
     row.v1 = min(row.v0 + p.vectors, all);
 
     const float temperature = a.temperature ? a.temperature[b] : 1.f, top_p = a.top_p ? a.top_p[b] : 1.f;
     const float min_p = a.min_p ? a.min_p[b] : 0.f, random = a.random[b];
     const int32_t top_k = a.top_k ? a.top_k[b] : 0;
-    if (tid == 0) s.first = ~0u;
-    // the row into shared memory, and its largest logit
+    // the row into shared memory, and its largest logit, with the first place that has it where that is the answer
+    const bool greedy = !(temperature > 0.f);
     float most = -INFINITY;
+    uint32_t place = ~0u;
+    auto larger = [&](float v, uint32_t i) {
+        if (v > most) {
+            most = v;
+            place = i;
+        }
+    };
     if (p.held) {
-        for (uint32_t v = row.v0 + tid; v < row.v1; v += 4 * kThreads) {
-            uint4 u[4];
+        constexpr int kAhead = 8;
+        for (uint32_t v = row.v0 + tid; v < row.v1; v += kAhead * kThreads) {
+            uint4 u[kAhead];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < kAhead; ++j)
                 if (v + j * kThreads < row.v1) u[j] = row.read(v + j * kThreads);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (v + j * kThreads < row.v1) slice[v + j * kThreads - row.v0] = u[j];
+            for (int j = 0; j < kAhead; ++j) {
+                if (v + j * kThreads >= row.v1) break;
+                slice[v + j * kThreads - row.v0] = u[j];
+                const uint32_t w[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
+#pragma unroll
+                for (int e = 0; e < R::kVec; ++e) {
+                    const float y = R::element(w, e);
+                    if (greedy) larger(y, (v + j * kThreads) * R::kVec - row.shift + e);
+                    else most = fmaxf(most, y);
+                }
+            }
         }
-    }
-    row.each([&](float v, uint32_t) { most = fmaxf(most, v); });        // what this thread has read itself
-    const float top = row.cluster_max(most);
-    const bool lead = tid == 0 && row.rank == 0;
-    const bool none = top == -INFINITY;
-    if (none || !(temperature > 0.f)) {
-        uint32_t place = ~0u;
-        if (!none) {
-            row.each([&](float v, uint32_t i) {
-                if (v == top) place = min(place, i);
-            });
-            place = __reduce_min_sync(~0u, place);
-            if (lane == 0 && place != ~0u) atomicMin(&s.first, place);
-            __syncthreads();
-            row.exchange(s.first);
-            place = lane < ranks ? (uint32_t)ld_cluster_u64(&s.slot[row.phase][0], lane) : ~0u;
-            place = __reduce_min_sync(~0u, place);
-        }
+    } else
+        row.each([&](const float (&v)[4], uint32_t i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) larger(v[j], i + j);
+        });
+    uint32_t lowest = most == -INFINITY ? ~0u : key_of(most);       // of the threads' largest, which top-k looks at
+    const uint64_t best = row.cluster_max((uint64_t)key_of(most) << 32 | (uint32_t)~place, lowest);
+    const float top = logit_of((uint32_t)(best >> 32));
+    const bool lead = tid == 0 && row.rank == 0, none = top == -INFINITY;
+    if (none || greedy) {
         if (lead) {
-            a.tokens[b] = (int32_t)place;
+            a.tokens[b] = none ? -1 : (int32_t)~(uint32_t)best;
             if (a.logprobs) a.logprobs[b] = none ? -INFINITY : 0.f;
         }
-        join();         // no CTA leaves while another reads its shared memory
         return;
     }
     row.m = top;
@@ -626,23 +705,51 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         __syncthreads();
         return s.cut.bin;
     };
-    if (by_k && (uint32_t)top_k <= kFew && (uint32_t)top_k * 5 < ranks * kThreads * 4) {
-        // where top_k of the threads have a logit, top_k logits are: hardly more, while they are few among the threads
+    // What may be kept lies less than `limit` below the largest, in units of `scale`. With one logit for each thread, its largest: where top_k
+    // of those are, or as much weight as top_p wants, all that is kept is, and hardly more than that while it is few.
+    float limit = INFINITY, scale = row.c_hi * 64.f;
+    uint64_t all_weights = 0;
+    if (by_k) {
+        if ((uint32_t)top_k <= kFew && (uint32_t)top_k * 5 < ranks * kThreads * 4) {
+            scale = (float)(kBins - 1) / (top - logit_of(lowest));
+            if (!(scale < FLT_MAX)) scale = 0.f;            // one logit only; otherwise what lies off by rounding goes to the last bin
+            row.clear();
+            if (most > -INFINITY) atomicAdd(&s.hist[min((uint32_t)row.below(most, scale), kBins - 1)], 1u);
+            row.template merge<false>(1.f);
+            few = reach((uint32_t)top_k);
+            limit = few < kBins - 1 ? (float)(few + 1) : INFINITY;
+        }
+    } else if (by_p) {
+        uint64_t sum = row.sum_over(row.v0 + tid, row.v1, kThreads, [](float v, uint32_t) { return v > -INFINITY; }, [&](float v) { return row.weight(v); });
+        sum = row.block_sum(sum);
+        row.exchange(sum);
+        all_weights = row.collect();
         row.clear();
-        float part;
-        const uint32_t bin = most == -INFINITY ? kBins : row.bin_of(most, part);
-        if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
-        row.template merge<false>(1.f);
-        few = reach((uint32_t)top_k);
-    } else if (!by_k && by_m && !by_p) {
+        row.count(most, most > -INFINITY, p.unit);
+        row.template merge<true>(1.f / p.unit);
+        float sums[4];
+        row.running(sums);
+        const float goal = (float)times(fmaxf(top_p, 0.f), all_weights, true) * __uint_as_float((uint32_t)(127 - p.scale) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (sums[j] * (1.f - p.slack) >= goal) atomicMin(&s.cut.bin, tid * 4 + j);
+        __syncthreads();
+        few = s.cut.bin;
+        limit = (float)(few + 1);
+    } else if (by_m) {
         row.clear();
-        const float u = -64.f * log2f(fminf(min_p, 1.f)) + 1.f;       // a bin further, for what the logarithm and the bins round
-        if (u < (float)kBins) few = (uint32_t)u;
+        few = 0;
+        limit = -64.f * log2f(fminf(min_p, 1.f)) * (1.f + 0x1p-20f) + 0.01f;      // a little more, for what the logarithm and `below` round
     }
     if (few < kBins) {
-        row.each([&](float v, uint32_t i) {
-            float part;
-            if (v != -INFINITY && row.bin_of(v, part) <= few) row.list(i);
+        row.each([&](const float (&v)[4], uint32_t i) {
+            bool in[4], any = false;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) any |= in[j] = v[j] > -INFINITY && row.below(v[j], scale) < limit;
+            if (!any) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in[j]) row.list(i + j);
         });
         __syncthreads();
         row.exchange(s.listed);
@@ -660,6 +767,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 __syncthreads();
                 if (tid == 0) s.cut.bin2 = 0;
                 __syncthreads();
+                if (!by_k && by_p) whole = all_weights;
                 const uint64_t goal = by_p ? max(times(fmaxf(top_p, 0.f), whole, true), (uint64_t)1) : ~0ull;
                 uint64_t mine = 0;
                 uint32_t end = 0;
@@ -704,10 +812,12 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     if (by_k) {
         // many: the border alone
         row.clear();
-        row.each([&](float v, uint32_t) {
-            float part;
-            const uint32_t bin = v == -INFINITY ? kBins : row.bin_of(v, part);
-            if (bin < kBins) atomicAdd(&s.hist[bin], 1u);
+        row.each([&](const float (&v)[4], uint32_t) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float at = row.below(v[j]);
+                if (at < (float)kBins) atomicAdd(&s.hist[__float_as_uint(__fadd_rd(at, kDown)) & (kBins - 1)], 1u);
+            }
         });
         row.template merge<false>(1.f);
         const uint32_t bin = reach((uint32_t)top_k);
@@ -716,9 +826,12 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         if (bin < kBins && inside <= kListed) {
             if (tid == 0) s.listed = 0;
             __syncthreads();
-            row.each([&](float v, uint32_t i) {
-                float part;
-                if (v != -INFINITY && row.bin_of(v, part) == bin) row.list(i);
+            row.each([&](const float (&v)[4], uint32_t i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float at = row.below(v[j]);
+                    if (at >= (float)bin && at < (float)(bin + 1)) row.list(i + j);
+                }
             });
             join();
             if (row.rank == 0) {
@@ -733,25 +846,34 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             row.adopt();
         } else {
             uint64_t count = 0;
-            row.each([&](float v, uint32_t) { count += v > -INFINITY; });
+            row.each([&](const float (&v)[4], uint32_t) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) count += v[j] > -INFINITY;
+            });
             count = row.cluster_sum(count);
-            if ((uint64_t)top_k < count) row.template cut_by_bits<false>((uint64_t)top_k);
+            if ((uint64_t)top_k < count) row = cut_by_bits<false>(row, (uint64_t)top_k);
         }
     }
     if (by_p) {
         // the exact sum, and the weights by bins
         row.clear();
         uint64_t sum = 0;
-        row.each([&](float v, uint32_t i) {
-            if (!row.kept(key_of(v), i)) return;
-            sum += row.weight(v);
-            float part;
-            const uint32_t bin = row.bin_of(v, part);
-            if (bin < kBins) atomicAdd(&s.hist[bin], (uint32_t)(exp2f(part * (-1.f / 64.f)) * p.unit));
+        row.each([&](const float (&v)[4], uint32_t i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = row.kept(v[j], i + j);
+                if (by_k) {
+                    const uint64_t w = row.weight(v[j]);
+                    sum += in ? w : 0;
+                }
+                row.count(v[j], in, p.unit);
+            }
         });
-        sum = row.block_sum(sum);
-        row.exchange(sum);
-        sum = row.collect();
+        if (by_k) {
+            sum = row.block_sum(sum);
+            row.exchange(sum);
+            sum = row.collect();
+        } else sum = all_weights;
         const uint64_t target = max(times(fmaxf(top_p, 0.f), sum, true), (uint64_t)1);
         row.template merge<true>(1.f / p.unit);
         // the border lies between where the bins' sums with all that they may lack reach the target and where they do with as much less
@@ -768,12 +890,24 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         bool done = bin2 < kBins;
         if (done) {
             uint64_t over = 0;
-            row.each([&](float v, uint32_t i) {
-                float part;
-                const uint32_t at = v == -INFINITY ? kBins : row.bin_of(v, part);
-                if (at > bin2 || !row.kept(key_of(v), i)) return;
-                if (at < bin) over += row.weight(v);
-                else row.list(i);
+            const float sure = (float)bin, limit = (float)(bin2 + 1);
+            row.each([&](const float (&v)[4], uint32_t i) {
+                bool in[4], any = false;
+                float at[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    at[j] = row.below(v[j]);
+                    any |= in[j] = at[j] < limit && row.kept(v[j], i + j);
+                }
+                if (!any) return;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint64_t w = row.weight(v[j]);
+                    over += in[j] && at[j] < sure ? w : 0;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (in[j] && at[j] >= sure) row.list(i + j);
             });
             over = row.block_sum(over);
             row.exchange(over, s.listed);
@@ -798,16 +932,18 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 row.adopt();
             }
         }
-        if (!done) row.template cut_by_bits<true>(target);
+        if (!done) row = cut_by_bits<true>(row, target);
     }
     uint64_t whole;
-    const uint32_t token = row.locate(share, [&](float v, uint32_t i) -> uint64_t {
-        if (!row.kept(key_of(v), i)) return 0;
-        const uint64_t w = row.weight(v);
-        return w >= row.least ? w : 0;
-    }, &whole);
+    const uint64_t least = row.least;
+    const uint32_t token = row.locate(
+        share, [&](float v, uint32_t i) { return row.kept(v, i); },
+        [&](float v) -> uint64_t {
+            const uint64_t w = row.weight(v);
+            return w >= least ? w : 0;
+        },
+        &whole);
     if (lead) answer(token, logit_of(row.key_at(token)), whole);
-    join();
 }
 
 }  // namespace
