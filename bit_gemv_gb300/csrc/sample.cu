@@ -101,14 +101,13 @@ struct alignas(16) Shared {
     alignas(16) uint32_t hist[kBins];           // hist and totals: together also the weights of kListed tokens
     alignas(16) uint32_t totals[kBins];
     alignas(16) uint64_t sorted[kListed];
-    uint32_t list[kListed], listed, lowest;     // lowest: ~0 before the kernel begins with it
+    uint32_t listed, taken, lowest;             // listed: by this CTA; taken: of the first CTA's `sorted`
     struct {
         uint64_t above, inside;
         uint32_t bin, bin2, border, last;
         bool over;
     } cut;
     uint64_t target, all;
-    uint32_t starts[kMostCluster + 1];
 };
 
 static_assert(offsetof(Shared, hist) % 16 == 0 && offsetof(Shared, totals) == offsetof(Shared, hist) + kBins * 4 && offsetof(Shared, totals) % 16 == 0 &&
@@ -121,10 +120,12 @@ struct Row {
     const uint8_t *x;
     Shared *shared;
     bool held;                  // the slice, in shared memory
+    bool infinite = false;      // some logits are +infinity: they count as 0, all others as -infinity
     uint32_t vocab, shift;      // elements between the last 16-byte boundary and the row's first
     uint32_t v0, v1;            // this CTA's 16-byte vectors, counted from that boundary
     uint32_t rank, ranks;
-    int scale;
+    int right;                  // 61 - the weights' scale
+    uint64_t half;              // of its unit, that far to the left
     uint32_t phase = 0;
     // the row's largest logit, log2(e) / temperature in two floats
     float m = 0.f, c_hi = 0.f, c_lo = 0.f;
@@ -133,7 +134,7 @@ struct Row {
     uint32_t last = ~0u;
     uint64_t least = 0;
 
-    __device__ Row(const uint8_t *x, Shared *shared, bool held, uint32_t vocab, int scale) : x(x), shared(shared), held(held), vocab(vocab), scale(scale) {
+    __device__ Row(const uint8_t *x, Shared *shared, bool held, uint32_t vocab, int scale) : x(x), shared(shared), held(held), vocab(vocab), right(61 - scale), half((1ull << right) >> 1) {
         shift = (uint32_t)(reinterpret_cast<uintptr_t>(x) & 15) / kEs;
         rank = cluster_ctarank();
         ranks = cluster_nctarank();
@@ -173,6 +174,10 @@ struct Row {
                 float v[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) v[j] = fmaxf(element(w, q + j), -INFINITY);
+                if (infinite) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[j] = v[j] == INFINITY ? 0.f : -INFINITY;
+                }
                 f(v, i * kVec - shift + q);
             }
         }
@@ -185,7 +190,7 @@ struct Row {
     }
     template <class F>
     __device__ __forceinline__ void each(F f) const { over(v0 + threadIdx.x, v1, kThreads, f); }
-    // The sum of value(x) over the places for which wanted(x, place) says so.
+    // The sum of value(x) over the places for which wanted(x, place) says so; the value of -infinity is 0.
     template <class W, class V>
     __device__ __forceinline__ uint64_t sum_over(uint32_t from, uint32_t to, uint32_t step, W wanted, V value) const {
         uint64_t sum = 0;
@@ -195,21 +200,21 @@ struct Row {
             for (int j = 0; j < 4; ++j) any |= in[j] = wanted(v[j], i + j);
             if (!any) return;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint64_t w = value(v[j]);
-                sum += in[j] ? w : 0;
-            }
+            for (int j = 0; j < 4; ++j) sum += value(in[j] ? v[j] : -INFINITY);
         });
         return sum;
     }
 
-    __device__ __forceinline__ uint32_t key_at(uint32_t i) const { return key_of(fmaxf(load1(x, i, kDtype), -INFINITY)); }
+    __device__ __forceinline__ float logit_at(uint32_t i) const {
+        const float v = fmaxf(load1(x, i, kDtype), -INFINITY);
+        return !infinite ? v : v == INFINITY ? 0.f : -INFINITY;
+    }
     __device__ __forceinline__ bool kept(float v, uint32_t i) const { return v > border || (v == border && i <= last); }
 
     // t as two floats (but for the rounding of x - m: 2^-24 t, another one for each token); -100 and less as -100 (and `rest` without a
     // meaning)
     __device__ __forceinline__ float exponent(float v, float &rest) const {
-        const float d = v == m ? 0.f : v - m, p = d * c_hi;
+        const float d = v - m, p = d * c_hi;
         rest = fmaf(d, c_lo, fmaf(d, c_hi, -p));
         return fmaxf(p, -100.f);
     }
@@ -222,14 +227,16 @@ struct Row {
         const float y = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);        // 2^r - 1
         const int power = (int)shared->powers[n & 63];
         // of 2^(t - n / 64's whole part), times 2^30
-        const uint32_t w = (uint32_t)(power + __mulhi(power, (__float_as_int(fmaf(y, 0x1p29f, kRound)) - __float_as_int(kRound)) << 3));
-        // times 2^(n / 64 + scale - 30), which is at most 2^31, rounded; nothing is left of what is 2^-100 and less, whatever w
-        const int right = min(61 - scale - (n >> 6), 63);
-        return (((uint64_t)(w & 0x7fffffffu) << 31) + ((1ull << right) >> 1)) >> right;
+        uint32_t w = (uint32_t)(power + __mulhi(power, (__float_as_int(fmaf(y, 0x1p29f, kRound)) - __float_as_int(kRound)) << 3));
+        // times 2^(n / 64 + scale - 30), rounded: to the left up to 31, where more than that to the right is left out before, and to the
+        // right by the same for all tokens. Nothing is left of what is 2^-100 and less, whatever w.
+        const int left = max((n >> 6) + 31, 0), before = left - 31 - (n >> 6);
+        w = before < 32 ? w >> before : 0;
+        return ((uint64_t)w * (1u << left) + half) >> right;
     }
     // How many bins a logit lies below the largest one, with a fraction; falling logits have rising ones. NaN, which is below no number of
-    // bins, where both the temperature and the distance are infinite.
-    __device__ __forceinline__ float below(float v, float scale) const { return v == m ? 0.f : (m - v) * scale; }
+    // bins, for a logit of -infinity at an infinite temperature.
+    __device__ __forceinline__ float below(float v, float scale) const { return (m - v) * scale; }
     __device__ __forceinline__ float below(float v) const { return below(v, c_hi * 64.f); }
 
     // Sum over the CTA; every thread gets it.
@@ -316,7 +323,7 @@ struct Row {
                 for (uint32_t i = here ? here * kVec - shift : 0; i < until; i += 32) {
                     uint64_t u = 0;
                     if (i + lane < until) {
-                        const float v = fmaxf(load1(x, i + lane, kDtype), -INFINITY);
+                        const float v = logit_at(i + lane);
                         if (wanted(v, i + lane)) u = value(v);
                     }
 #pragma unroll
@@ -417,7 +424,7 @@ struct Row {
     __device__ void clear() {
         for (uint32_t i = threadIdx.x; i < kBins; i += kThreads) shared->hist[i] = 0;
         if (threadIdx.x == 0) {
-            shared->listed = 0;
+            shared->listed = shared->taken = 0;     // for lists behind the next barrier of the cluster
             shared->cut.bin = shared->cut.bin2 = kBins;
         }
         __syncthreads();
@@ -429,35 +436,15 @@ struct Row {
         const float part = (at - (z - kDown)) * (1.f / 64.f), share = fmaf(part, fmaf(part, 0.2402f, -0.69314718f), 1.f) * unit;
         if (in && at < (float)kBins) atomicAdd(&shared->hist[__float_as_uint(z) & (kBins - 1)], __float_as_uint(__fadd_rd(share, kDown)) & 0x7fffffu);
     }
-    __device__ __forceinline__ void list(uint32_t place) {
-        const uint32_t at = atomicAdd(&shared->listed, 1u);
-        if (at < kListed) shared->list[at] = place;
+    // Puts a token into the first CTA's `sorted`.
+    __device__ __forceinline__ void list(float v, uint32_t place) {
+        atomicAdd(&shared->listed, 1u);
+        uint32_t at;
+        asm volatile("atom.shared::cluster.add.u32 %0, [%1], 1;" : "=r"(at) : "r"(mapa_shared(smem_u32(&shared->taken), 0)) : "memory");
+        if (at < kListed) st_cluster_u64(&shared->sorted[at], 0, (uint64_t)key_of(v) << 32 | (uint32_t)~place);
     }
 
-    // The first CTA: the lists of all, as (key, place) in falling order of keys and rising of places, in `sorted`; returns how many.
-    __device__ uint32_t gather() {
-        if (threadIdx.x < 32) {
-            uint32_t count = threadIdx.x < ranks ? ld_cluster_u32(&shared->listed, threadIdx.x) : 0;
-#pragma unroll
-            for (int k = 1; k < 32; k *= 2) {
-                const uint32_t u = __shfl_up_sync(~0u, count, k);
-                if (threadIdx.x >= (uint32_t)k) count += u;
-            }
-            if (threadIdx.x < ranks) shared->starts[threadIdx.x + 1] = count;
-            if (threadIdx.x == 0) shared->starts[0] = 0;
-        }
-        __syncthreads();
-        const uint32_t n = shared->starts[ranks];
-        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-            uint32_t r = 0;
-            while (i >= shared->starts[r + 1]) ++r;
-            const uint32_t place = ld_cluster_u32(&shared->list[i - shared->starts[r]], r);
-            shared->sorted[i] = (uint64_t)key_at(place) << 32 | (uint32_t)~place;
-        }
-        sort(n);
-        return n;
-    }
-    // `sorted` in falling order, with zeros behind the n first.
+    // `sorted`, (key, place) of each, in falling order of keys and rising of places, with zeros behind the n first.
     __device__ void sort(uint32_t n) {
         __syncthreads();
         if (n <= kThreads) {        // each one's number is how many are larger
@@ -587,7 +574,7 @@ struct Row {
         const uint64_t wanted = (target - above + one - 1) / one;
         uint32_t at = edge == border ? last : ~0u;
         if (wanted < ties)
-            at = locate([&](uint64_t) { return wanted - 1; }, [&](float v, uint32_t i) { return v == edge && kept(v, i); }, [](float) -> uint64_t { return 1; });
+            at = locate([&](uint64_t) { return wanted - 1; }, [&](float v, uint32_t i) { return v == edge && kept(v, i); }, [](float v) -> uint64_t { return v > -INFINITY; });
         border = edge;
         last = at;
     }
@@ -607,7 +594,10 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     __shared__ Shared s;
     const uint32_t tid = threadIdx.x, lane = tid % 32;
     if (tid < 64) s.powers[tid] = kPowers[tid];
-    if (tid == 64) s.lowest = ~0u;
+    if (tid == 64) {
+        s.lowest = ~0u;
+        s.listed = s.taken = 0;
+    }
     __syncthreads();
     pdl_launch_dependents();
     pdl_wait();
@@ -668,9 +658,11 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         }
         return;
     }
-    row.m = top;
+    row.infinite = top == INFINITY;
+    row.m = row.infinite ? 0.f : top;
+    if (row.infinite) most = most == INFINITY ? 0.f : -INFINITY;
     // log2(e) / temperature
-    row.c_hi = __fdiv_rn(1.44269504f, temperature);
+    row.c_hi = fminf(__fdiv_rn(1.44269504f, temperature), 1e36f);
     row.c_lo = __fdiv_rn(fmaf(-row.c_hi, temperature, 1.44269504f) + 1.92596299e-8f, temperature);
     if (!isfinite(row.c_lo)) row.c_lo = 0.f;
     if (min_p > 0.f) row.least = times(fminf(min_p, 1.f), 1ull << p.scale, true);
@@ -711,8 +703,8 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     uint64_t all_weights = 0;
     if (by_k) {
         if ((uint32_t)top_k <= kFew && (uint32_t)top_k * 5 < ranks * kThreads * 4) {
-            scale = (float)(kBins - 1) / (top - logit_of(lowest));
-            if (!(scale < FLT_MAX)) scale = 0.f;            // one logit only; otherwise what lies off by rounding goes to the last bin
+            scale = (float)(kBins - 1) / (row.m - logit_of(lowest));
+            if (!(fabsf(scale) < FLT_MAX)) scale = 0.f;            // one logit only; otherwise what lies off by rounding goes to the last bin
             row.clear();
             if (most > -INFINITY) atomicAdd(&s.hist[min((uint32_t)row.below(most, scale), kBins - 1)], 1u);
             row.template merge<false>(1.f);
@@ -737,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         few = s.cut.bin;
         limit = (float)(few + 1);
     } else if (by_m) {
-        row.clear();
         few = 0;
         limit = -64.f * log2f(fminf(min_p, 1.f)) * (1.f + 0x1p-20f) + 0.01f;      // a little more, for what the logarithm and `below` round
     }
@@ -749,13 +740,14 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             if (!any) return;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (in[j]) row.list(i + j);
+                if (in[j]) row.list(v[j], i + j);
         });
         __syncthreads();
         row.exchange(s.listed);
-        if (row.collect() <= kListed) {
+        const uint32_t n = (uint32_t)row.collect();
+        if (n <= kListed) {
             if (row.rank == 0) {
-                const uint32_t n = row.gather();
+                row.sort(n);
                 uint64_t w[4], sums[4];
                 row.sorted_sums(n, w, sums);
                 // A, its sum, and where B and C end: a number of `sorted` each
@@ -802,10 +794,9 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 for (int j = 0; j < 4; ++j)
                     if (sums[j] - w[j] <= passed && passed < sums[j]) {
                         const uint32_t place = ~(uint32_t)(s.sorted[tid * 4 + j] >> 32);
-                        answer(place, logit_of(row.key_at(place)), whole);
+                        answer(place, row.logit_at(place), whole);
                     }
             }
-            join();
             return;
         }
     }
@@ -824,18 +815,16 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         const uint64_t above = s.cut.above, inside = s.cut.inside - above;
         __syncthreads();
         if (bin < kBins && inside <= kListed) {
-            if (tid == 0) s.listed = 0;
-            __syncthreads();
             row.each([&](const float (&v)[4], uint32_t i) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float at = row.below(v[j]);
-                    if (at >= (float)bin && at < (float)(bin + 1)) row.list(i + j);
+                    if (at >= (float)bin && at < (float)(bin + 1)) row.list(v[j], i + j);
                 }
             });
             join();
             if (row.rank == 0) {
-                row.gather();
+                row.sort((uint32_t)inside);
                 if (tid == 0) {
                     const uint64_t e = s.sorted[(uint32_t)(top_k - above) - 1];
                     s.cut.border = (uint32_t)(e >> 32);
@@ -907,16 +896,16 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (in[j] && at[j] >= sure) row.list(i + j);
+                    if (in[j] && at[j] >= sure) row.list(v[j], i + j);
             });
             over = row.block_sum(over);
             row.exchange(over, s.listed);
             over = row.collect();
-            const uint64_t n_all = row.collect(1);
-            done = n_all <= kListed;
+            const uint32_t n = (uint32_t)row.collect(1);
+            done = n <= kListed;
             if (done) {
                 if (row.rank == 0) {
-                    const uint32_t n = row.gather();
+                    row.sort(n);
                     uint64_t w[4], sums_[4];
                     row.sorted_sums(n, w, sums_);
 #pragma unroll
@@ -943,7 +932,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             return w >= least ? w : 0;
         },
         &whole);
-    if (lead) answer(token, logit_of(row.key_at(token)), whole);
+    if (lead) answer(token, row.logit_at(token), whole);
 }
 
 }  // namespace
