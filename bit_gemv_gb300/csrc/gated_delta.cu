@@ -891,7 +891,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
         st = device_info(&d);
         if (st) return st;
         const bool narrow = rows * ((a.v_dim + 127) / 128) < 2ull * d.sms;
-        const int lanes = narrow || a.v_dim <= 32 ? 8 : a.k_dim > 128 || a.v_dim <= 64 ? 16 : 32;
+        const int lanes = narrow || a.v_dim <= 32 ? 8 : 16;
         if (!grid(lanes * 4, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
         const bool small = a.k_dim <= (uint64_t)(8 * kStepThreads / lanes);
         const auto kernel = lanes == 8    ? step_kernel<8, 8>

@@ -14,7 +14,7 @@
 namespace ninfer {
 namespace {
 
-constexpr int kTeamThreads = 256;
+constexpr int kTeamThreads = 256, kGroups = 1;
 constexpr uint32_t kMostTeam = 256, kMostRow = 32768;   // elements of a group: 8 a lane, 32 a thread
 
 struct NormParams {
@@ -58,7 +58,14 @@ __device__ __forceinline__ void widen(const Raw8 &r, int dtype, float (&o)[8]) {
     }
 }
 
-__device__ __forceinline__ float gated(float y, float z) { return y * (z / (1.f + expf(-z))); }
+// y z / (1 + e^-z); the exponent's product rounded once more, so that e^-z is as exact for large z as for small ones
+__device__ __forceinline__ float gated(float y, float z) {
+    const float t = z * -1.44269504f, rest = fmaf(z, -1.44269504f, -t);
+    float e;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e = t < 126.f ? fmaf(e, rest * 0.69314718f, e) : e;
+    return y * __fdividef(z, 1.f + e);
+}
 
 // Where element `at` of group `group` lies in the row's tensors.
 struct Place {
@@ -71,52 +78,61 @@ __device__ __forceinline__ Place place_of(const NormParams &p, uint32_t index) {
     return {row, (index - row * p.groups.d) * (uint32_t)p.a.group};
 }
 
-// A group to a team of kLanes lanes, 8 elements a lane.
+// kGroups groups to a team of kLanes lanes, 8 elements of each a lane, all of their loads under way at once.
 template <int kLanes>
 __global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(const __grid_constant__ NormParams p) {
+    constexpr int kTeams = kTeamThreads / kLanes;
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_norm_args &a = p.a;
-    const uint32_t index = blockIdx.x * (kTeamThreads / kLanes) + threadIdx.x / kLanes, e = threadIdx.x % kLanes * 8;
-    const bool on = index < p.total && e < a.group;
-    const Place at = place_of(p, on ? index : 0);
-    const uint64_t col = at.first + e;
-    Raw8 x, r, z, w;
-    if (on) {
-        x = raw8(a.x, at.row * a.x_stride + col, a.x_dtype);
-        if (a.residual) r = raw8(a.residual, at.row * a.residual_stride + col, a.residual_dtype);
-        if (a.gate) z = raw8(a.gate, at.row * a.gate_stride + col, a.gate_dtype);
-        if (a.weight) w = raw8(a.weight, e, a.weight_dtype);
-    }
-    float s[8] = {}, t[8], sum = 0.f;
-    if (on) {
-        widen(x, a.x_dtype, s);
-        if (a.residual) {
-            widen(r, a.residual_dtype, t);
+    const uint32_t index = blockIdx.x * (kTeams * kGroups) + threadIdx.x / kLanes, e = threadIdx.x % kLanes * 8;
+    Raw8 x[kGroups], r[kGroups], z[kGroups], w;
+    Place at[kGroups];
+    bool on[kGroups];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += t[i];
-            if (a.sum) store8(a.sum, at.row * a.sum_stride + col, a.residual_dtype, s);
+    for (int g = 0; g < kGroups; ++g) {
+        on[g] = index + g * kTeams < p.total && e < a.group;
+        at[g] = place_of(p, on[g] ? index + g * kTeams : 0);
+        const uint64_t col = at[g].first + e;
+        if (!on[g]) continue;
+        x[g] = raw8(a.x, at[g].row * a.x_stride + col, a.x_dtype);
+        if (a.residual) r[g] = raw8(a.residual, at[g].row * a.residual_stride + col, a.residual_dtype);
+        if (a.gate) z[g] = raw8(a.gate, at[g].row * a.gate_stride + col, a.gate_dtype);
+    }
+    if (a.weight && e < a.group) w = raw8(a.weight, e, a.weight_dtype);
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+        const uint64_t col = at[g].first + e;
+        float s[8] = {}, t[8], sum = 0.f;
+        if (on[g]) {
+            widen(x[g], a.x_dtype, s);
+            if (a.residual) {
+                widen(r[g], a.residual_dtype, t);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s[i] += t[i];
+                if (a.sum) store8(a.sum, at[g].row * a.sum_stride + col, a.residual_dtype, s);
+            }
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = fmaf(s[i], s[i], sum);
+#pragma unroll
+        for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
+        if (!on[g]) continue;
+        const float scale = 1.f / sqrtf(fmaf(sum, p.inverse, a.eps));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] *= scale;
+        if (a.weight) {
+            widen(w, a.weight_dtype, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] *= t[i] + a.weight_offset;
+        }
+        if (a.gate) {
+            widen(z[g], a.gate_dtype, t);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s[i] = gated(s[i], t[i]);
+        }
+        store8(a.out, at[g].row * a.out_stride + col, a.out_dtype, s);
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) sum = fmaf(s[i], s[i], sum);
-#pragma unroll
-    for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
-    if (!on) return;
-    const float scale = 1.f / sqrtf(fmaf(sum, p.inverse, a.eps));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] *= scale;
-    if (a.weight) {
-        widen(w, a.weight_dtype, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] *= t[i] + a.weight_offset;
-    }
-    if (a.gate) {
-        widen(z, a.gate_dtype, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] = gated(s[i], t[i]);
-    }
-    store8(a.out, at.row * a.out_stride + col, a.out_dtype, s);
 }
 
 // The CTA's sum; every thread gets it, the same bits.
@@ -302,12 +318,12 @@ extern "C" int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream) {
                             : lanes == 8  ? norm_team_kernel<8>
                             : lanes == 16 ? norm_team_kernel<16>
                                           : norm_team_kernel<32>;
-        const unsigned teams = kTeamThreads / lanes;
+        const unsigned teams = kTeamThreads / lanes * kGroups;
         return launch_dependent("norm", kernel, dim3((unsigned)((total + teams - 1) / teams)), dim3(kTeamThreads), 0, st, p);
     }
     if (a.group > kMostRow) return launch_dependent("norm", norm_long_kernel, dim3(p.total), dim3(1024), 0, st, p);
     const unsigned eights = (unsigned)((a.group + 7) / 8);
-    const unsigned per = eights > 2048 ? 4 : eights > 1024 ? 2 : 1;
+    const unsigned per = eights > 2048 ? 4 : eights > 512 && total > 256 ? 2 : eights > 1024 ? 2 : 1;
     const unsigned threads = (eights + 32 * per - 1) / (32 * per) * 32;
     const auto kernel = vec ? (per == 4 ? norm_row_kernel<4, true> : per == 2 ? norm_row_kernel<2, true> : norm_row_kernel<1, true>)
                             : (per == 4 ? norm_row_kernel<4, false> : per == 2 ? norm_row_kernel<2, false> : norm_row_kernel<1, false>);

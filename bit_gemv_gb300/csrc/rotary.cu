@@ -25,24 +25,35 @@ struct RotaryParams {
     float inverse;              // 1 / head_dim
 };
 
-__device__ __forceinline__ void load_head8(const void *base, uint64_t at, int dtype, float (&o)[8]) {
-    if (dtype == NINFER_F32) {
-        const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + at);
-        const float4 x = p[0], y = p[1];
-        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
-        o[4] = y.x; o[5] = y.y; o[6] = y.z; o[7] = y.w;
-        return;
-    }
-    const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = dtype == NINFER_BF16 ? make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u))
-                                              : __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
-        o[2 * i] = f.x;
-        o[2 * i + 1] = f.y;
-    }
+// 8 neighbouring elements as they lie in memory
+struct Raw8 {
+    uint4 lo, hi;
+};
+
+template <int kDtype>
+__device__ __forceinline__ Raw8 raw8(const void *base, uint64_t at) {
+    Raw8 r;
+    if (kDtype == NINFER_F32) {
+        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
+        r.lo = p[0];
+        r.hi = p[1];
+    } else
+        r.lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
+    return r;
 }
+
+template <int kDtype>
+__device__ __forceinline__ void widen(const Raw8 &r, float (&o)[8]) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        o[i] = kDtype == NINFER_F32    ? __uint_as_float(w[i])
+               : kDtype == NINFER_BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16)
+                                       : __half2float(__ushort_as_half((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffff)));
+}
+
+// Heads of a team under way at once.
+__host__ __device__ constexpr uint32_t ahead_of(int dtype) { return dtype == NINFER_F32 ? 2 : 4; }
 
 // kLanes: lanes of a head, 8 elements each. kPairs: 0 neighbours; 1 halves whose distance is a multiple of 8 (partners in another
 // lane, the same place); 2 other halves (the head goes through shared memory).
@@ -56,22 +67,40 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     const uint32_t token = p.first + blockIdx.x, tid = threadIdx.x;
     const int32_t position = a.positions[token];
     if (position < 0) return;
-    for (uint32_t i = tid; i < p.half; i += kThreads) {
+    const uint32_t lane = tid % kLanes, team = tid / kLanes, e = lane * 8;
+    const bool inside = e < a.head_dim;
+    // a few heads of each team asked for at once, the first ones before the sines and cosines
+    constexpr uint32_t kAhead = ahead_of(kDtype);
+    const uint32_t teams = blockDim.x / kLanes;
+    Raw8 raw[kAhead];
+    auto fetch = [&](uint32_t h0) {
+#pragma unroll
+        for (uint32_t j = 0; j < kAhead; ++j) {
+            const uint32_t h = h0 + j * teams + team;
+            const bool key = h >= a.q_heads;
+            const uint64_t head = key ? h - a.q_heads : h;
+            if (inside && h < p.heads)
+                raw[j] = raw8<kDtype>(key ? a.k : a.q, key ? token * a.k_token_stride + head * a.k_head_stride + e : token * a.q_token_stride + head * a.q_head_stride + e);
+        }
+    };
+    fetch(0);
+    for (uint32_t i = tid; i < p.half; i += blockDim.x) {
         const int64_t part = (int64_t)((uint64_t)position * a.frequencies[i]);
         float s, c;
         sincospif(__ll2float_rn(part) * 0x1p-63f, &s, &c);
         turn[i] = make_float2(c * a.magnitude, s * a.magnitude);
     }
     __syncthreads();
-    const uint32_t lane = tid % kLanes, team = tid / kLanes, e = lane * 8;
-    const bool inside = e < a.head_dim;
-    for (uint32_t h0 = 0; h0 < p.heads; h0 += kThreads / kLanes) {
-        const uint32_t h = h0 + team;
+    for (uint32_t h0 = 0; h0 < p.heads; h0 += kAhead * teams) {
+      if (h0) fetch(h0);
+#pragma unroll
+      for (uint32_t j = 0; j < kAhead; ++j) {
+        const uint32_t h = h0 + j * teams + team;
+        if (h - team >= p.heads) break;
         const bool on = inside && h < p.heads, key = h >= a.q_heads;
         const uint64_t head = key ? h - a.q_heads : h;
         float x[8] = {};
-        if (on)
-            load_head8(key ? a.k : a.q, key ? token * a.k_token_stride + head * a.k_head_stride + e : token * a.q_token_stride + head * a.q_head_stride + e, kDtype, x);
+        if (on) widen<kDtype>(raw[j], x);
         const void *weight = key ? a.k_weight : a.q_weight;
         if (a.q_weight || a.k_weight) {
             float sum = 0.f;
@@ -126,6 +155,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
         }
         if (on)
             store8(key ? a.k_out : a.q_out, key ? token * a.k_out_token_stride + head * a.k_out_head_stride + e : token * a.q_out_token_stride + head * a.q_out_head_stride + e, kDtype, x);
+      }
     }
 }
 
@@ -222,5 +252,8 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
     const auto kernel = a.dtype == NINFER_F32    ? kernel_of<NINFER_F32>(lanes, pairs)
                         : a.dtype == NINFER_BF16 ? kernel_of<NINFER_BF16>(lanes, pairs)
                                                  : kernel_of<NINFER_F16>(lanes, pairs);
-    return launch_dependent("rotary", kernel, dim3(p.tokens), dim3(kThreads), 0, (cudaStream_t)stream, p);
+    // as many teams as take the heads in the fewest rounds
+    const unsigned ahead = ahead_of(a.dtype), rounds = (p.heads * lanes + ahead * kThreads - 1) / (ahead * kThreads);
+    const unsigned teams = (p.heads + ahead * rounds - 1) / (ahead * rounds), threads = (teams * lanes + 31) / 32 * 32;
+    return launch_dependent("rotary", kernel, dim3(p.tokens), dim3(threads), 0, (cudaStream_t)stream, p);
 }
