@@ -609,12 +609,13 @@ def _vector(t, name, count, device):
 
 
 def _matrix(t, name, shape, device):
-    """Address, library dtype and row stride of a tensor of rows; zeros for None."""
+    """Address, library dtype and row stride of a tensor of rows of a shape; zeros for None."""
     if t is None:
         return 0, 0, 0
-    code, strides = _rows(t, name, 2, _ANY, device)
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    code, strides = _TYPES.get(t.dtype, E4M3), t.stride()
+    if t.shape != shape or t.get_device() != device or code == E4M3 or (strides[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a tensor of {tuple(shape)} elements of a supported dtype on cuda:{device} with contiguous rows, "
+                         f"not {tuple(t.shape)} of {t.dtype} on {t.device}")
     return t.data_ptr(), code, strides[0] if shape[0] > 1 else shape[1]
 
 
@@ -626,8 +627,10 @@ def ninfer_norm(x, weight=None, eps: float = 1e-6, residual=None, sum=None, gate
     _TYPES or _types()
     device = _on(x, "x")
     shape = x.shape
-    x_at, x_code, x_stride = _matrix(x, "x", shape, device)
+    if len(shape) != 2:
+        raise ValueError(f"x must be (rows, cols), not {tuple(shape)}")
     rows, cols = shape
+    x_at, x_code, x_stride = _matrix(x, "x", shape, device)
     if out is None:
         out = _torch().empty(shape, dtype=out_dtype or x.dtype, device=x.device)
     r_at, r_code, r_stride = _matrix(residual, "residual", shape, device)
@@ -656,12 +659,14 @@ def ninfer_rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling="n
     return out.view(np.int64), magnitude.value
 
 
-def _heads(t, name, tokens, codes, device):
-    """Address, library dtype, strides and shape of a (tokens, heads, elements) tensor."""
-    code, strides = _rows(t, name, 3, codes, device)
-    if t.shape[0] != tokens:
-        raise ValueError(f"{name} must have {tokens} tokens, not {t.shape[0]}")
-    return t.data_ptr(), code, strides[0], strides[1], t.shape
+def _heads(t, name, tokens, code, device):
+    """Address, library dtype, strides and shape of a (tokens, heads, elements) tensor; `code`: the dtype that it must have, or None."""
+    found, strides, shape = _TYPES.get(t.dtype, E4M3), t.stride(), t.shape
+    if len(shape) != 3 or shape[0] != tokens or t.get_device() != device or (found != code if code is not None else found == E4M3) or \
+            (strides[2] != 1 and shape[2] > 1):
+        raise ValueError(f"{name} must be a tensor of ({tokens}, heads, elements) on cuda:{device} of a supported dtype, one for all, with the "
+                         f"last dimension contiguous, not {tuple(shape)} of {t.dtype} on {t.device}")
+    return t.data_ptr(), found, strides[0], strides[1], shape
 
 
 def ninfer_rotary(q, k, positions, frequencies, magnitude: float = 1.0, interleaved: bool = False, q_weight=None, k_weight=None,
@@ -672,22 +677,22 @@ def ninfer_rotary(q, k, positions, frequencies, magnitude: float = 1.0, interlea
     _TYPES or _types()
     device = _on(q, "q")
     tokens = q.shape[0]
-    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, _ANY, device)
+    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, None, device)
     q_heads, dim = shape[1], shape[2]
     o_at, o_token, o_head = q_at, q_token, q_head
     if q_out is not None:
-        o_at, _, o_token, o_head, o_shape = _heads(q_out, "q_out", tokens, (code,), device)
+        o_at, _, o_token, o_head, o_shape = _heads(q_out, "q_out", tokens, code, device)
         if o_shape != shape:
             raise ValueError("q_out must have the shape and dtype of q")
     k_at = k_token = k_head = kv_heads = p_at = p_token = p_head = 0
     if k is not None:
-        k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, (code,), device)
+        k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, code, device)
         kv_heads = k_shape[1]
         if k_shape[2] != dim:
             raise ValueError("q and k must have one dtype and head_dim")
         p_at, p_token, p_head = k_at, k_token, k_head
         if k_out is not None:
-            p_at, _, p_token, p_head, p_shape = _heads(k_out, "k_out", tokens, (code,), device)
+            p_at, _, p_token, p_head, p_shape = _heads(k_out, "k_out", tokens, code, device)
             if p_shape != k_shape:
                 raise ValueError("k_out must have the shape and dtype of k")
     elif k_out is not None or k_weight is not None:
@@ -721,21 +726,22 @@ def ninfer_gated_delta(q, k, v, log_decay, beta, state, offsets=None, slots=None
     _TYPES or _types()
     device = _on(q, "q")
     tokens = q.shape[0]
-    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, _ANY, device)
-    k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, (code,), device)
-    v_at, _, v_token, v_head, v_shape = _heads(v, "v", tokens, (code,), device)
+    q_at, code, q_token, q_head, shape = _heads(q, "q", tokens, None, device)
+    k_at, _, k_token, k_head, k_shape = _heads(k, "k", tokens, code, device)
+    v_at, _, v_token, v_head, v_shape = _heads(v, "v", tokens, code, device)
     _, k_heads, k_dim = shape
     _, v_heads, v_dim = v_shape
     if k_shape != shape:
         raise ValueError("q and k must have one shape")
     d_at, d_code, d_stride = _matrix(log_decay, "log_decay", (tokens, v_heads), device)
     b_at, b_code, b_stride = _matrix(beta, "beta", (tokens, v_heads), device)
-    s_strides = state.stride()
+    s_strides, s_shape, whole = state.stride(), state.shape, k_dim * v_dim
     if d_code or b_code or state.dtype is not _F32 or state.get_device() != device:
         raise ValueError(f"log_decay, beta and state must be float32 on cuda:{device}")
-    if state.dim() != 4 or state.shape[1:] != (v_heads, k_dim, v_dim) or not state[0].is_contiguous():
+    # the strides of contiguous slots; a dimension of one element may have any
+    if s_shape[1:] != (v_heads, k_dim, v_dim) or s_strides[1:] != (whole, v_dim, 1) and not state[:1].is_contiguous():
         raise ValueError(f"state must be (slots, {v_heads}, {k_dim}, {v_dim}) with contiguous slots")
-    n = state.shape[0]
+    n = s_shape[0]
     requests = tokens if offsets is None else offsets.numel() - 1
     if slots is not None and offsets is None:
         requests = slots.numel()
@@ -755,7 +761,7 @@ def ninfer_gated_delta(q, k, v, log_decay, beta, state, offsets=None, slots=None
         _arg(offsets, "offsets", _I32, requests + 1, device), _arg(lengths, "lengths", _I32, requests, device),
         _arg(out, "out", o_dtype, tokens * v_heads * v_dim, device), _arg(status, "status", _I32, 1, device), tokens, requests, n,
         k_heads, v_heads, k_dim, v_dim, q_token, q_head, k_token, k_head, v_token, v_head, d_stride, b_stride,
-        s_strides[0] if n > 1 else v_heads * k_dim * v_dim, k_dim ** -0.5 if scale is None else scale,
+        s_strides[0] if n > 1 else v_heads * whole, k_dim ** -0.5 if scale is None else scale,
         -1.0 if norm_eps is None else norm_eps, code, _TYPES.get(o_dtype, -1)), w_at, w_bytes, _raw_stream(device)))
     return out
 
@@ -766,13 +772,15 @@ def ninfer_sample(logits, random, temperature=None, top_k=None, top_p=None, min_
     a float32 (rows,) tensor that gets the logarithm of the token's share of what is kept, or None."""
     _TYPES or _types()
     device = _on(logits, "logits")
-    code, strides = _rows(logits, "logits", 2, _ANY, device)
+    if logits.dim() != 2:
+        raise ValueError(f"logits must be (rows, vocab), not {tuple(logits.shape)}")
     rows, vocab = logits.shape
+    at, code, stride = _matrix(logits, "logits", logits.shape, device)
     if out is None:
         out = _torch().empty(rows, dtype=_I32, device=logits.device)
     _check(_lib.ninfer_sample(_SAMPLE.pack(
-        logits.data_ptr(), _arg(temperature, "temperature", _F32, rows, device), _arg(top_p, "top_p", _F32, rows, device),
+        at, _arg(temperature, "temperature", _F32, rows, device), _arg(top_p, "top_p", _F32, rows, device),
         _arg(min_p, "min_p", _F32, rows, device), _arg(top_k, "top_k", _I32, rows, device),
         _arg(random, "random", _F32, rows, device) if random is not None else 0, _arg(out, "out", _I32, rows, device),
-        _arg(logprobs, "logprobs", _F32, rows, device), rows, vocab, strides[0] if rows > 1 else vocab, code, 0), _raw_stream(device)))
+        _arg(logprobs, "logprobs", _F32, rows, device), rows, vocab, stride, code, 0), _raw_stream(device)))
     return out

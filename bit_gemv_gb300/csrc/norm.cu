@@ -58,14 +58,7 @@ __device__ __forceinline__ void widen(const Raw8 &r, int dtype, float (&o)[8]) {
     }
 }
 
-// y z / (1 + e^-z); the exponent's product rounded once more, so that e^-z is as exact for large z as for small ones
-__device__ __forceinline__ float gated(float y, float z) {
-    const float t = z * -1.44269504f, rest = fmaf(z, -1.44269504f, -t);
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
-    e = t < 126.f ? fmaf(e, rest * 0.69314718f, e) : e;
-    return y * __fdividef(z, 1.f + e);
-}
+__device__ __forceinline__ float gated(float y, float z) { return y * __fdividef(z, 1.f + __expf(-z)); }
 
 // Where element `at` of group `group` lies in the row's tensors.
 struct Place {
@@ -118,7 +111,7 @@ __global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(const __grid_co
 #pragma unroll
         for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
         if (!on[g]) continue;
-        const float scale = 1.f / sqrtf(fmaf(sum, p.inverse, a.eps));
+        const float scale = rsqrtf(fmaf(sum, p.inverse, a.eps));
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] *= scale;
         if (a.weight) {
@@ -204,7 +197,7 @@ __global__ void __launch_bounds__(1024) norm_row_kernel(const __grid_constant__ 
     for (int j = 0; j < kPer; ++j)
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(s[j][i], s[j][i], sum);
-    const float scale = 1.f / sqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
+    const float scale = rsqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
         if (kVec) {
@@ -255,7 +248,7 @@ __global__ void __launch_bounds__(1024) norm_long_kernel(const __grid_constant__
         const float s = value(e);
         sum = fmaf(s, s, sum);
     }
-    const float scale = 1.f / sqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
+    const float scale = rsqrtf(fmaf(sum_of_all(sum), p.inverse, a.eps));
     for (uint64_t e = threadIdx.x; e < a.group; e += 1024) {
         const float s = value(e);
         float y = s * scale;
