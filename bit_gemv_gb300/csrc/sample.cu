@@ -292,12 +292,15 @@ struct Row {
         return __shfl_sync(~0u, v, 0);
     }
 
+    // Vectors of a warp, where each has neighbouring ones.
+    __device__ __forceinline__ uint32_t warps_part() const { return (v1 - v0 + kWarps - 1) / kWarps; }
     // The first place, in the order of the row, at which the running sum of value(x) over the wanted ones passes target(whole sum).
-    template <class T, class W, class V>
-    __device__ uint32_t locate(T target, W wanted, V value, uint64_t *whole = nullptr) {
+    // sum(from, to): the thread's part of that sum, over vectors from, from + 32 ..., where it is known cheaper than by adding all up.
+    template <class T, class S, class W, class V>
+    __device__ uint32_t locate(T target, S part_sum, W wanted, V value, uint64_t *whole = nullptr) {
         const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-        const uint32_t part = (v1 - v0 + kWarps - 1) / kWarps, from = min(v0 + warp * part, v1);
-        uint64_t sum = sum_over(from + lane, min(from + part, v1), 32, wanted, value);
+        const uint32_t part = warps_part(), from = min(v0 + warp * part, v1);
+        uint64_t sum = part_sum(from + lane, min(from + part, v1));
         uint64_t before;                        // what lies before this CTA, then before its part that has the token, then the part's part
         uint32_t at;
         warps_sums(sum);
@@ -573,8 +576,11 @@ struct Row {
         const uint64_t one = kWeighted ? weight(edge) : 1, ties = shared->cut.inside / one;
         const uint64_t wanted = (target - above + one - 1) / one;
         uint32_t at = edge == border ? last : ~0u;
-        if (wanted < ties)
-            at = locate([&](uint64_t) { return wanted - 1; }, [&](float v, uint32_t i) { return v == edge && kept(v, i); }, [](float v) -> uint64_t { return v > -INFINITY; });
+        if (wanted < ties) {
+            auto tied = [&](float v, uint32_t i) { return v == edge && kept(v, i); };
+            auto one_each = [](float v) -> uint64_t { return v > -INFINITY; };
+            at = locate([&](uint64_t) { return wanted - 1; }, [&](uint32_t from, uint32_t to) { return sum_over(from, to, 32, tied, one_each); }, tied, one_each);
+        }
         border = edge;
         last = at;
     }
@@ -843,6 +849,9 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             if ((uint64_t)top_k < count) row = cut_by_bits<false>(row, (uint64_t)top_k);
         }
     }
+    // by warps' parts: the exact weights of what is surely kept, and from where to where it is not sure
+    uint64_t sure_sum = 0;
+    float sure = 0.f, unsure = INFINITY;
     if (by_p) {
         // the exact sum, and the weights by bins
         row.clear();
@@ -879,8 +888,9 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         bool done = bin2 < kBins;
         if (done) {
             uint64_t over = 0;
-            const float sure = (float)bin, limit = (float)(bin2 + 1);
-            row.each([&](const float (&v)[4], uint32_t i) {
+            const float low = (float)bin, limit = (float)(bin2 + 1);
+            const uint32_t part = row.warps_part(), from = min(row.v0 + tid / 32 * part, row.v1);
+            row.over(from + lane, min(from + part, row.v1), 32, [&](const float (&v)[4], uint32_t i) {
                 bool in[4], any = false;
                 float at[4];
 #pragma unroll
@@ -892,12 +902,13 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint64_t w = row.weight(v[j]);
-                    over += in[j] && at[j] < sure ? w : 0;
+                    over += in[j] && at[j] < low ? w : 0;
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (in[j] && at[j] >= sure) row.list(v[j], i + j);
+                    if (in[j] && at[j] >= low) row.list(v[j], i + j);
             });
+            const uint64_t mine = over;
             over = row.block_sum(over);
             row.exchange(over, s.listed);
             over = row.collect();
@@ -919,19 +930,31 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
                     __syncthreads();
                 }
                 row.adopt();
+                if (!by_m) {
+                    sure_sum = mine;
+                    sure = low;
+                    unsure = limit;
+                }
             }
         }
         if (!done) row = cut_by_bits<true>(row, target);
     }
     uint64_t whole;
     const uint64_t least = row.least;
+    auto kept = [&](float v, uint32_t i) { return row.kept(v, i); };
+    auto value = [&](float v) -> uint64_t {
+        const uint64_t w = row.weight(v);
+        return w >= least ? w : 0;
+    };
     const uint32_t token = row.locate(
-        share, [&](float v, uint32_t i) { return row.kept(v, i); },
-        [&](float v) -> uint64_t {
-            const uint64_t w = row.weight(v);
-            return w >= least ? w : 0;
+        share,
+        [&](uint32_t from, uint32_t to) {
+            return sure_sum + row.sum_over(from, to, 32, [&](float v, uint32_t i) {
+                const float at = row.below(v);
+                return !(at < sure) && !(at >= unsure) && row.kept(v, i);
+            }, value);
         },
-        &whole);
+        kept, value, &whole);
     if (lead) answer(token, row.logit_at(token), whole);
 }
 
