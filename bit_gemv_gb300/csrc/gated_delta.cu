@@ -181,6 +181,7 @@ struct ChunkParams {
     uint8_t *rows, *heads;
     uint64_t rows_bytes;        // of a chunk and key head
     uint32_t wide;              // k_dim rounded up to the kernel's steps of 16
+    uint32_t slab;              // columns of a state a CTA
     uint32_t *error;            // the library's error word
     long long wait_limit;
 };
@@ -241,12 +242,13 @@ __device__ __forceinline__ Range range_of(const ninfer_gated_delta_args &a, uint
     return r;
 }
 
+constexpr uint32_t kTriRow = kChunk + 4, kTriSmem = kPrepareThreads / 32 * kChunk * kTriRow * 4;
+
 // A CTA for every chunk and key head. kTerms: binary16 terms of k and q, 1 where they have 16 bits themselves.
 template <int kTerms>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
-    extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8
+    extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8; then a triangle of each warp
     __shared__ float dots[2][kChunk][kChunk + 1], scales[2][kChunk];
-    __shared__ __align__(16) float tri[kPrepareThreads / 32][kChunk][kChunk + 4];
     __shared__ float4 sums[kPrepareThreads / 32][kChunk];      // the log decays' sums in two floats, beta
     __shared__ uint32_t found;
     pdl_launch_dependents();
@@ -346,6 +348,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     __syncthreads();
     // A warp a value head: lane s has column s of both triangles. Log decays are added up in units of ln 2 and in two floats, so that
     // differences of far sums are as exact as those of near ones; 2^(+-2^15) is all the same.
+    float(*tri)[kChunk][kTriRow] = reinterpret_cast<float(*)[kChunk][kTriRow]>(smem);
     const uint32_t group = p.d.group.d;
     for (uint32_t i = warp; i < group; i += kPrepareThreads / 32) {
         const uint32_t head = key_head * group + i;
@@ -448,12 +451,12 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_gated_delta_args &a = p.d.a;
-    const Part part = part_of(p.d, blockIdx.x, kColumns);
+    const Part part = part_of(p.d, blockIdx.x, p.slab);
     if (part.none) return;
     const Range range = range_of(a, part.request);
     if (!range.chunks) return;
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim, v_dim = (uint32_t)a.v_dim;
-    const uint32_t base = smem_u32(smem), columns = min(v_dim - part.column, (uint32_t)kColumns);
+    const uint32_t base = smem_u32(smem), columns = min(v_dim - part.column, p.slab);
     if (tid == 0) {
         for (uint32_t i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&full[i]), 1 + 32);          // the bulk copies, and each lane's of the values
@@ -514,7 +517,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
         if (!good) drain();
         return;
     }
-    if (mine >= v_dim) return;      // whole pairs
+    if (pair * 16 >= columns) return;      // whole pairs
     if (!kSender && warp == 0)
         for (uint32_t j = 0; j < min(kStages - 1, range.chunks); ++j) send(j);
     // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
@@ -899,19 +902,25 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
                                           : (small ? step_kernel<32, 8> : step_kernel<32, 16>);
         return launch_dependent("gated delta", kernel, dim3(blocks), dim3(kStepThreads), 0, s, p);
     }
-    if (!grid(kColumns, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
+    // 64 columns a CTA, or 48 where that gives work to more of the SMs without a second round
+    DeviceInfo d;
+    st = device_info(&d);
+    if (st) return st;
+    const uint64_t slab = rows * ((a.v_dim + 47) / 48) <= (uint64_t)d.sms ? 48 : kColumns;
+    if (!grid(slab, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
     const int terms = a.dtype == NINFER_F32 ? 2 : 1;
     const uint64_t chunks = a.tokens / kChunk + a.requests;
     ChunkParams c;
     c.d = p;
     c.wide = wide_of(a.k_dim);
+    c.slab = (uint32_t)slab;
     c.rows_bytes = rows_bytes_of(terms, a.k_dim);
     c.rows = static_cast<uint8_t *>(workspace);
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
     st = device_error_word(&c.error);
     if (st) return st;
     c.wait_limit = wait_limit_cycles();
-    const uint32_t prepare_smem = (uint32_t)c.rows_bytes;
+    const uint32_t prepare_smem = std::max((uint32_t)c.rows_bytes, kTriSmem);
     const uint32_t chunk_smem = stages_of(c.wide, terms) * ((uint32_t)c.rows_bytes + kHeadBytes + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
                                 8 * (kChunk / 2 * 80 + sums_of(c.wide, terms) * 6 * 32 * 16);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
