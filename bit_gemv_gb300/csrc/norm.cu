@@ -14,7 +14,7 @@
 namespace ninfer {
 namespace {
 
-constexpr int kTeamThreads = 256, kGroups = 1;
+constexpr int kTeamThreads = 256;
 constexpr uint32_t kMostTeam = 256, kMostRow = 32768;   // elements of a group: 8 a lane, 32 a thread
 
 struct NormParams {
@@ -71,61 +71,62 @@ __device__ __forceinline__ Place place_of(const NormParams &p, uint32_t index) {
     return {row, (index - row * p.groups.d) * (uint32_t)p.a.group};
 }
 
-// kGroups groups to a team of kLanes lanes, 8 elements of each a lane, all of their loads under way at once.
-template <int kLanes>
+// A group to a team of kLanes lanes, 8 elements a lane. kType: the type of x, gate and out where they have one and the weight is
+// float (or there is none), and there is no residual; -1 for all else. (A lane has few elements, so that the branches on four types and the
+// addresses are a third of the instructions that bound this kernel.)
+template <int kLanes, int kType>
 __global__ void __launch_bounds__(kTeamThreads) norm_team_kernel(const __grid_constant__ NormParams p) {
-    constexpr int kTeams = kTeamThreads / kLanes;
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_norm_args &a = p.a;
-    const uint32_t index = blockIdx.x * (kTeams * kGroups) + threadIdx.x / kLanes, e = threadIdx.x % kLanes * 8;
-    Raw8 x[kGroups], r[kGroups], z[kGroups], w;
-    Place at[kGroups];
-    bool on[kGroups];
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        on[g] = index + g * kTeams < p.total && e < a.group;
-        at[g] = place_of(p, on[g] ? index + g * kTeams : 0);
-        const uint64_t col = at[g].first + e;
-        if (!on[g]) continue;
-        x[g] = raw8(a.x, at[g].row * a.x_stride + col, a.x_dtype);
-        if (a.residual) r[g] = raw8(a.residual, at[g].row * a.residual_stride + col, a.residual_dtype);
-        if (a.gate) z[g] = raw8(a.gate, at[g].row * a.gate_stride + col, a.gate_dtype);
+    constexpr bool kOne = kType >= 0;
+    const int x_dtype = kOne ? kType : a.x_dtype, gate_dtype = kOne ? kType : a.gate_dtype, out_dtype = kOne ? kType : a.out_dtype;
+    const int weight_dtype = kOne ? (int)NINFER_F32 : a.weight_dtype;
+    const uint32_t index = blockIdx.x * (kTeamThreads / kLanes) + threadIdx.x / kLanes, e = threadIdx.x % kLanes * 8;
+    const bool on = index < p.total && e < a.group;
+    const Place at = place_of(p, on ? index : 0);
+    const uint64_t col = at.first + e;
+    Raw8 x, r, z, w;
+    if (on) {
+        x = raw8(a.x, at.row * a.x_stride + col, x_dtype);
+        if (!kOne && a.residual) r = raw8(a.residual, at.row * a.residual_stride + col, a.residual_dtype);
+        if (a.gate) z = raw8(a.gate, at.row * a.gate_stride + col, gate_dtype);
+        if (a.weight) w = raw8(a.weight, e, weight_dtype);
     }
-    if (a.weight && e < a.group) w = raw8(a.weight, e, a.weight_dtype);
+    float s[8] = {}, t[8], sum = 0.f;
+    if (on) {
+        widen(x, x_dtype, s);
+        if (!kOne && a.residual) {
+            widen(r, a.residual_dtype, t);
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-        const uint64_t col = at[g].first + e;
-        float s[8] = {}, t[8], sum = 0.f;
-        if (on[g]) {
-            widen(x[g], a.x_dtype, s);
-            if (a.residual) {
-                widen(r[g], a.residual_dtype, t);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s[i] += t[i];
-                if (a.sum) store8(a.sum, at[g].row * a.sum_stride + col, a.residual_dtype, s);
-            }
+            for (int i = 0; i < 8; ++i) s[i] += t[i];
+            if (a.sum) store8(a.sum, at.row * a.sum_stride + col, a.residual_dtype, s);
         }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) sum = fmaf(s[i], s[i], sum);
-#pragma unroll
-        for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
-        if (!on[g]) continue;
-        const float scale = rsqrtf(fmaf(sum, p.inverse, a.eps));
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] *= scale;
-        if (a.weight) {
-            widen(w, a.weight_dtype, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] *= t[i] + a.weight_offset;
-        }
-        if (a.gate) {
-            widen(z[g], a.gate_dtype, t);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] = gated(s[i], t[i]);
-        }
-        store8(a.out, at[g].row * a.out_stride + col, a.out_dtype, s);
     }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sum = fmaf(s[i], s[i], sum);
+#pragma unroll
+    for (int k = kLanes / 2; k; k /= 2) sum += __shfl_xor_sync(~0u, sum, k);
+    if (!on) return;
+    const float scale = rsqrtf(fmaf(sum, p.inverse, a.eps));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s[i] *= scale;
+    if (a.weight) {
+        widen(w, weight_dtype, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] *= t[i] + a.weight_offset;
+    }
+    if (a.gate) {
+        widen(z, gate_dtype, t);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = gated(s[i], t[i]);
+    }
+    store8(a.out, at.row * a.out_stride + col, out_dtype, s);
+}
+
+template <int kLanes>
+auto team_kernel_of(int type) {
+    return type == NINFER_BF16 ? norm_team_kernel<kLanes, NINFER_BF16> : type == NINFER_F16 ? norm_team_kernel<kLanes, NINFER_F16> : norm_team_kernel<kLanes, -1>;
 }
 
 // The CTA's sum; every thread gets it, the same bits.
@@ -307,11 +308,13 @@ extern "C" int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream) {
     const cudaStream_t st = (cudaStream_t)stream;
     if (vec && a.group <= kMostTeam) {
         const unsigned lanes = a.group <= 32 ? 4 : a.group <= 64 ? 8 : a.group <= 128 ? 16 : 32;
-        const auto kernel = lanes == 4    ? norm_team_kernel<4>
-                            : lanes == 8  ? norm_team_kernel<8>
-                            : lanes == 16 ? norm_team_kernel<16>
-                                          : norm_team_kernel<32>;
-        const unsigned teams = kTeamThreads / lanes * kGroups;
+        const bool one = !a.residual && a.out_dtype == a.x_dtype && (!a.gate || a.gate_dtype == a.x_dtype) && (!a.weight || a.weight_dtype == NINFER_F32);
+        const int type = one ? a.x_dtype : -1;
+        const auto kernel = lanes == 4    ? team_kernel_of<4>(type)
+                            : lanes == 8  ? team_kernel_of<8>(type)
+                            : lanes == 16 ? team_kernel_of<16>(type)
+                                          : team_kernel_of<32>(type);
+        const unsigned teams = kTeamThreads / lanes;
         return launch_dependent("norm", kernel, dim3((unsigned)((total + teams - 1) / teams)), dim3(kTeamThreads), 0, st, p);
     }
     if (a.group > kMostRow) return launch_dependent("norm", norm_long_kernel, dim3(p.total), dim3(1024), 0, st, p);

@@ -20,7 +20,7 @@ constexpr int kThreads = 256;
 
 struct RotaryParams {
     ninfer_rotary_args a;
-    uint32_t heads, half;       // q_heads + kv_heads, rotary_dim / 2
+    uint32_t heads, q_heads, half;      // heads: q_heads + kv_heads; half: rotary_dim / 2
     uint32_t first, tokens;     // of this launch
     float inverse;              // 1 / head_dim
 };
@@ -58,8 +58,8 @@ __host__ __device__ constexpr uint32_t ahead_of(int dtype) { return dtype == NIN
 // kLanes: lanes of a head, 8 elements each. kPairs: 0 neighbours; 1 halves whose distance is a multiple of 8 (partners in another
 // lane, the same place); 2 other halves (the head goes through shared memory).
 template <int kDtype, int kLanes, int kPairs>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryParams p) {
-    __shared__ float2 turn[128];
+__global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_constant__ RotaryParams p) {
+    __shared__ __align__(16) float2 turn[128];
     __shared__ float row[kPairs == 2 ? kThreads / kLanes : 1][kPairs == 2 ? kLanes * 8 : 1];
     pdl_launch_dependents();
     pdl_wait();
@@ -73,14 +73,15 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     constexpr uint32_t kAhead = ahead_of(kDtype);
     const uint32_t teams = blockDim.x / kLanes;
     Raw8 raw[kAhead];
+    const uint64_t q_in = token * a.q_token_stride + e, k_in = token * a.k_token_stride + e;
+    const uint64_t q_to = token * a.q_out_token_stride + e, k_to = token * a.k_out_token_stride + e;
     auto fetch = [&](uint32_t h0) {
 #pragma unroll
         for (uint32_t j = 0; j < kAhead; ++j) {
             const uint32_t h = h0 + j * teams + team;
-            const bool key = h >= a.q_heads;
-            const uint64_t head = key ? h - a.q_heads : h;
-            if (inside && h < p.heads)
-                raw[j] = raw8<kDtype>(key ? a.k : a.q, key ? token * a.k_token_stride + head * a.k_head_stride + e : token * a.q_token_stride + head * a.q_head_stride + e);
+            const bool key = h >= p.q_heads;
+            const uint32_t head = key ? h - p.q_heads : h;
+            if (inside && h < p.heads) raw[j] = raw8<kDtype>(key ? a.k : a.q, (key ? k_in : q_in) + head * (key ? a.k_head_stride : a.q_head_stride));
         }
     };
     fetch(0);
@@ -97,8 +98,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
       for (uint32_t j = 0; j < kAhead; ++j) {
         const uint32_t h = h0 + j * teams + team;
         if (h - team >= p.heads) break;
-        const bool on = inside && h < p.heads, key = h >= a.q_heads;
-        const uint64_t head = key ? h - a.q_heads : h;
+        const bool on = inside && h < p.heads, key = h >= p.q_heads;
+        const uint32_t head = key ? h - p.q_heads : h;
         float x[8] = {};
         if (on) widen<kDtype>(raw[j], x);
         const void *weight = key ? a.k_weight : a.q_weight;
@@ -117,13 +118,25 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             }
         }
         if (kPairs == 0) {
+            if (e + 8 <= a.rotary_dim) {
 #pragma unroll
-            for (int i = 0; i < 8; i += 2) {
-                if (e + i >= a.rotary_dim) break;
-                const float2 t = turn[(e + i) / 2];
-                const float u = x[i], v = x[i + 1];
-                x[i] = u * t.x - v * t.y;
-                x[i + 1] = v * t.x + u * t.y;
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 t = *reinterpret_cast<const float4 *>(&turn[(e + i) / 2]);
+                    const float u = x[i], v = x[i + 1], w = x[i + 2], y = x[i + 3];
+                    x[i] = u * t.x - v * t.y;
+                    x[i + 1] = v * t.x + u * t.y;
+                    x[i + 2] = w * t.z - y * t.w;
+                    x[i + 3] = y * t.z + w * t.w;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    if (e + i >= a.rotary_dim) break;
+                    const float2 t = turn[(e + i) / 2];
+                    const float u = x[i], v = x[i + 1];
+                    x[i] = u * t.x - v * t.y;
+                    x[i + 1] = v * t.x + u * t.y;
+                }
             }
         } else if (kPairs == 1) {
             const uint32_t apart = p.half / 8;
@@ -134,9 +147,10 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             for (int i = 0; i < 8; ++i) y[i] = __shfl_sync(~0u, x[i], from, kLanes);
             if (turned) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float2 t = turn[(low ? e : e - p.half) + i];
-                    x[i] = low ? x[i] * t.x - y[i] * t.y : x[i] * t.x + y[i] * t.y;
+                for (int i = 0; i < 8; i += 2) {
+                    const float4 t = *reinterpret_cast<const float4 *>(&turn[(low ? e : e - p.half) + i]);
+                    x[i] = fmaf(x[i], t.x, low ? -y[i] * t.y : y[i] * t.y);
+                    x[i + 1] = fmaf(x[i + 1], t.z, low ? -y[i + 1] * t.w : y[i + 1] * t.w);
                 }
             }
         } else {
@@ -154,7 +168,7 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
             __syncwarp();
         }
         if (on)
-            store8(key ? a.k_out : a.q_out, key ? token * a.k_out_token_stride + head * a.k_out_head_stride + e : token * a.q_out_token_stride + head * a.q_out_head_stride + e, kDtype, x);
+            store8(key ? a.k_out : a.q_out, (key ? k_to : q_to) + head * (key ? a.k_out_head_stride : a.q_out_head_stride), kDtype, x);
       }
     }
 }
@@ -243,6 +257,7 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
     RotaryParams p;
     p.a = a;
     p.half = (uint32_t)(a.rotary_dim / 2);
+    p.q_heads = (uint32_t)a.q_heads;
     p.heads = (uint32_t)(a.q_heads + (a.k ? a.kv_heads : 0));
     p.first = 0;
     p.tokens = (uint32_t)a.tokens;
