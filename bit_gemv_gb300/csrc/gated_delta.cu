@@ -315,25 +315,30 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     __syncthreads();
     // (K, Q) K^T: 16 rows a warp
     {
-        float d[4][4] = {};
+        // The tensor core cuts sums off towards zero: even and odd steps, and fp32's lower terms, have sums of their own.
+        float d[4][4] = {}, odd[4][4] = {}, lower[kTerms == 2 ? 4 : 1][4] = {};
         const uint32_t base = smem_u32(smem), from_a = base + (warp * 16 + lane % 16) * stride + lane / 16 * 16;
         const uint32_t from_b = base + (lane % 8 + lane / 16 * 8) * stride + lane / 8 % 2 * 16;
-        for (uint32_t k = 0; k < p.wide; k += 16) {
-            uint32_t x[kTerms][4], y[4];
+        for (uint32_t k0 = 0; k0 < p.wide; k0 += 32) {
 #pragma unroll
-            for (int e = 0; e < kTerms; ++e) load_matrices(x[e], from_a + e * term_bytes + k * 2);
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t k = (k0 + h * 16) * 2;
+                float(&sum)[4][4] = h ? odd : d;
+                uint32_t x[kTerms][4], y[4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                load_matrices(y, from_b + n * 16 * stride + k * 2);
+                for (int e = 0; e < kTerms; ++e) load_matrices(x[e], from_a + e * term_bytes + k);
 #pragma unroll
-                for (int e = 0; e < kTerms; ++e) {
-                    mma(d[2 * n], x[e], y[0], y[1]);
-                    mma(d[2 * n + 1], x[e], y[2], y[3]);
-                }
-                if (kTerms == 2) {
-                    load_matrices(y, from_b + term_bytes + n * 16 * stride + k * 2);
-                    mma(d[2 * n], x[0], y[0], y[1]);
-                    mma(d[2 * n + 1], x[0], y[2], y[3]);
+                for (int n = 0; n < 2; ++n) {
+                    load_matrices(y, from_b + n * 16 * stride + k);
+                    mma(sum[2 * n], x[0], y[0], y[1]);
+                    mma(sum[2 * n + 1], x[0], y[2], y[3]);
+                    if (kTerms == 2) {
+                        mma(lower[2 * n], x[kTerms - 1], y[0], y[1]);
+                        mma(lower[2 * n + 1], x[kTerms - 1], y[2], y[3]);
+                        load_matrices(y, from_b + term_bytes + n * 16 * stride + k);
+                        mma(lower[2 * n], x[0], y[0], y[1]);
+                        mma(lower[2 * n + 1], x[0], y[2], y[3]);
+                    }
                 }
             }
         }
@@ -342,7 +347,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t t = warp % 2 * 16 + lane / 4 + e / 2 * 8, u = n * 8 + lane % 4 * 2 + e % 2;
-                dots[warp / 2][t][u] = d[n][e] * scales[warp / 2][t] * scales[0][u];
+                dots[warp / 2][t][u] = (d[n][e] + odd[n][e] + (kTerms == 2 ? lower[kTerms == 2 ? n : 0][e] : 0.f)) * scales[warp / 2][t] * scales[0][u];
             }
     }
     __syncthreads();
