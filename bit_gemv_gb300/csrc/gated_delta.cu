@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 }
 
 // Eight warps that compute, and one that copies where it leaves them registers enough (else the first one does that too).
-__host__ __device__ constexpr int chunk_threads(int steps) { return steps < 8 ? 288 : 256; }
+__host__ __device__ constexpr int chunk_threads(int steps) { return steps < 4 ? 288 : 256; }
 
 // Chunks in shared memory at once, and buffers for the sums: what fits an SM.
 __host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
@@ -512,14 +512,15 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
         copies_arrive(bar);
         sent = j + 1;
     };
-    // no CTA ends with copies under way, not where a wait has run out either
+    // No CTA ends with copies under way, not where a wait has run out either: a limit of its own, a millisecond, for them to land.
+    constexpr long long kLanding = 2000000;
     auto drain = [&]() {
-        for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit);
+        for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, kLanding);
     };
     constexpr bool kSender = chunk_threads(kSteps) > 256;
     if (kSender && warp == 8) {
         for (uint32_t j = 0; j < range.chunks && good; ++j) send(j);
-        if (!good) drain();
+        drain();
         return;
     }
     if (pair * 16 >= columns) return;      // whole pairs
@@ -536,12 +537,18 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
             const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
             s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
         }
+    // this lane's first 16 bytes of a chunk's results: of 16 tokens by 16 columns, two (f32: four) a token
+    const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2, out_row = lane / out_es, out_col = lane % out_es * 16 / out_es;
+    const bool out_on = mine + out_col < v_dim;
+    const uint64_t out_step = a.v_heads * v_dim * out_es;
+    uint8_t *to_out = static_cast<uint8_t *>(a.out) + (uint64_t)(range.begin + half * 16 + out_row) * out_step + ((uint64_t)part.head * v_dim + mine + out_col) * out_es;
+    uint32_t slot = 0, parity = 0;
     for (uint32_t j = 0; j < range.chunks; ++j) {
-        good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, p.wait_limit)));
-        const uint32_t stage = base + j % kStages * stage_bytes;
-        const uint8_t *here = smem + j % kStages * stage_bytes;
+        good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[slot]), parity, p.error, p.wait_limit)));
+        const uint32_t stage = base + slot * stage_bytes;
+        const uint8_t *here = smem + slot * stage_bytes;
         const float *numbers = reinterpret_cast<const float *>(here + kNumbersAt);
-        const int32_t first = range.begin + (int32_t)j * kChunk, count = min(range.end - first, kChunk);
+        const int32_t count = min(range.end - range.begin - (int32_t)j * kChunk, kChunk);
         {
             // S^T times K^T and Q^T: x[0..3] tokens of K, x[4..7] of Q
             float x[8][4] = {}, up0, up1;
@@ -750,10 +757,13 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
 #pragma unroll
             for (int n = 0; n < 2; ++n) of_q[n] = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&empty[j % kStages]));
+            if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+            if (++slot == kStages) {
+                slot = 0;
+                parity ^= 1;
+            }
             // out, through shared memory: 16 columns of this warp's 16 tokens
             if (good) {
-                const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2;
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
 #pragma unroll
@@ -774,14 +784,11 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
                     store_matrices_turned(base + out_at + b_row * 80 + b_col, r);
                 }
                 __syncwarp();
-                const uint32_t shift = out_es == 4 ? 2 : 1, per = 16 / out_es;       // 16-byte units of a token, elements of one
-                for (uint32_t i = lane; i < 16u << shift; i += 32) {
-                    const uint32_t t = i >> shift, c = i & (out_es - 1);
-                    if ((int32_t)(half * 16 + t) < count && mine + c * per < v_dim) {
-                        const uint64_t at = ((uint64_t)(first + half * 16 + t) * a.v_heads + part.head) * v_dim + mine + c * per;
-                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(a.out) + at * out_es) = *reinterpret_cast<const uint4 *>(smem + out_at + t * 80 + c * 16);
-                    }
-                }
+                const uint8_t *from = smem + out_at + out_row * 80 + lane % out_es * 16;
+                if (out_on && (int32_t)(half * 16 + out_row) < count) *reinterpret_cast<uint4 *>(to_out) = *reinterpret_cast<const uint4 *>(from);
+                if (out_es == 4 && out_on && (int32_t)(half * 16 + out_row + 8) < count)
+                    *reinterpret_cast<uint4 *>(to_out + 8 * out_step) = *reinterpret_cast<const uint4 *>(from + 8 * 80);
+                to_out += kChunk * out_step;
                 __syncwarp();
             }
         }
@@ -884,12 +891,12 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     p.a = a;
     p.heads = FastDiv((uint32_t)a.v_heads);
     p.group = FastDiv((uint32_t)(a.v_heads / a.k_heads));
-    const uint64_t rows = a.requests * a.v_heads;
+    const uint64_t rows = a.requests * a.v_heads;       // below 2^47; of at most eight slabs each
+    if (rows * ((a.v_dim + 31) / 32) > 0x7fffffffull) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
     const auto grid = [&](uint64_t slab, unsigned *blocks) {
         const uint64_t slabs = (a.v_dim + slab - 1) / slab;
         p.slabs = FastDiv((uint32_t)slabs);
         *blocks = (unsigned)(rows * slabs);
-        return rows * slabs <= 0x7fffffffull;
     };
     unsigned blocks;
     const cudaStream_t s = (cudaStream_t)stream;
@@ -900,7 +907,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
         if (st) return st;
         const bool narrow = rows * ((a.v_dim + 127) / 128) < 2ull * d.sms;
         const int lanes = narrow || a.v_dim <= 32 ? 8 : 16;
-        if (!grid(lanes * 4, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
+        grid(lanes * 4, &blocks);
         const bool small = a.k_dim <= (uint64_t)(8 * kStepThreads / lanes);
         const auto kernel = lanes == 8    ? step_kernel<8, 8>
                             : lanes == 16 ? (small ? step_kernel<16, 8> : step_kernel<16, 16>)
@@ -912,7 +919,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     st = device_info(&d);
     if (st) return st;
     const uint64_t slab = rows * ((a.v_dim + 47) / 48) <= (uint64_t)d.sms ? 48 : kColumns;
-    if (!grid(slab, &blocks)) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
+    grid(slab, &blocks);
     const int terms = a.dtype == NINFER_F32 ? 2 : 1;
     const uint64_t chunks = a.tokens / kChunk + a.requests;
     ChunkParams c;

@@ -296,6 +296,11 @@ extern "C" int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream) {
         if (a.rows > 1 && t.stride >= (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "norm: %s stride of 2^40 or more", t.name);
         vec = vec && aligned(t.p, 16) && (a.rows == 1 || t.p == a.weight || t.stride * es % 16 == 0);
     }
+    // in place only where every element is written where it was read
+    const bool moved = a.rows > 1 && (a.out == a.x ? a.out_stride != a.x_stride : a.out == a.gate && a.out_stride != a.gate_stride);
+    if ((a.sum && a.sum == a.residual && a.rows > 1 && a.sum_stride != a.residual_stride) || moved || (a.out == a.x && a.out_dtype != a.x_dtype) ||
+        (a.out == a.gate && a.out_dtype != a.gate_dtype) || a.out == a.residual || a.out == a.sum || a.sum == a.x || (a.sum && a.sum == a.gate))
+        return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: out may be x or gate, sum the residual, with the same stride and dtype; no other outputs overlap");
     const uint64_t groups = a.cols / a.group;
     uint64_t total;
     if (!mul_ok(a.rows, groups, &total) || total > 0x7fffffffull)

@@ -252,6 +252,13 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
             return fail(NINFER_ERR_ALIGNMENT, "rotary: q, k and their outputs must have bases and strides of 16 bytes' multiples");
         if (token >= (1ull << 40) || head >= (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "rotary: a stride of 2^40 or more");
     }
+    const auto moved = [&](uint64_t token, uint64_t to_token, uint64_t head, uint64_t to_head, uint64_t heads) {
+        return (a.tokens > 1 && token != to_token) || (heads > 1 && head != to_head);
+    };
+    if ((a.q == a.q_out && moved(a.q_token_stride, a.q_out_token_stride, a.q_head_stride, a.q_out_head_stride, a.q_heads)) ||
+        (a.k && a.k == a.k_out && moved(a.k_token_stride, a.k_out_token_stride, a.k_head_stride, a.k_out_head_stride, a.kv_heads)) ||
+        a.q_out == a.k || (a.k && (a.q_out == a.k_out || a.q == a.k_out)))
+        return fail(NINFER_ERR_INVALID_ARGUMENT, "rotary: an output may be its own input with the same strides, and overlaps nothing else");
     if (!aligned(a.positions, 4) || !aligned(a.frequencies, 8) || !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16))
         return fail(NINFER_ERR_ALIGNMENT, "rotary: positions must be 4-byte, frequencies 8-byte, weights 16-byte aligned");
     RotaryParams p;

@@ -124,12 +124,13 @@ int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream stream);
  *     with zeros, whatever its slot holds. NULL: every state is read.
  *   out: device [tokens][v_heads][v_dim] of out_dtype; rows of no request are left as they were, and so are the states of
  *     requests without tokens.
- *   workspace: device, 256-byte aligned, at least ninfer_gated_delta_workspace() bytes (NULL where that is 0); its
- *     contents need no initial value and are not preserved.
+ *   workspace: with offsets, device, 256-byte aligned, at least ninfer_gated_delta_workspace() bytes; its contents need no
+ *     initial value and are not preserved, and no other call may use it at the same time. Without offsets it is not used (NULL will do).
  *   k_dim, v_dim: multiples of 8 up to 256; v_heads a multiple of k_heads; scale finite.
  * States and sums are fp32. With offsets, a request's tokens go 32 at a time through the tensor cores: operands hold 22 bits of each
  * value (q and k of 16-bit types all of theirs), but nothing under 2^-38 of the largest one of their column of the state
  * among those tokens. Each request's results do not depend on the others of the call.
+ * If a kernel's bounded wait runs out (ninfer_set_wait_limit), the device error word is set and the results are incomplete.
  * Errors: INVALID_ARGUMENT, SHAPE, SIZE_MISMATCH (workspace), ALIGNMENT, OVERFLOW, CUDA.
  */
 typedef struct {
@@ -165,8 +166,8 @@ int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *workspace, uin
  *   temperature, top_p, min_p: device float[rows], NULL: 1, 1, 0; top_k: device int32[rows], NULL: 0.
  *   random: device float[rows], in [0, 1) (cut to it).
  *   tokens: device int32[rows]; logprobs: device float[rows] or NULL.
- * Weights are whole multiples of a power of two far below the smallest that counts (2^-31 of each, and 2^(vocab's bits - 62)
- * of the largest), so that their sums are exact and do not depend on an order: equal rows give equal tokens.
+ * Weights are whole multiples of 2^(vocab's bits - 62) of the largest one, each off by less than 2^-29 and the rounding of x - m (2^-24 of
+ * the exponent) of itself; their sums are exact and do not depend on an order: equal rows give equal tokens, however they are divided.
  * Errors: INVALID_ARGUMENT, SHAPE (rows or vocab 0, vocab over 2^30, stride below vocab), ALIGNMENT, OVERFLOW, CUDA.
  */
 typedef struct {

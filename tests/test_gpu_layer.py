@@ -255,6 +255,24 @@ def test_gated_delta_parts_make_the_whole():
     assert torch.allclose(state, whole, rtol=0, atol=2e-5 * whole.abs().max().item())
 
 
+@pytest.mark.parametrize("dk", [96, 128, 256])
+def test_gated_delta_waits_that_run_out(dk):
+    """A bound of 0 makes every wait give up: the error word tells, no state or result of the call is stored, the next call is right."""
+    rng = np.random.default_rng(14)
+    case = delta_case(rng, 200, 2, 1, 2, dk, 64, "bf16")
+    offsets, before, out = i32([0, 40, 200]), case["state"].clone(), torch.full((200, 2, 64), 5.0, device=DEV)
+    assert nt.ninfer_device_errors() == 0
+    nt.ninfer_set_wait_limit(0)
+    try:
+        nt.ninfer_gated_delta(**case, offsets=offsets, norm_eps=1e-6, out=out)
+        torch.cuda.synchronize()
+    finally:
+        nt.ninfer_set_wait_limit(nt.WAIT_LIMIT_DEFAULT)
+    assert nt.ninfer_device_errors() & 1 and nt.ninfer_device_errors() == 0
+    assert torch.equal(case["state"], before) and (out == 5).all()
+    run_delta(case, offsets=[0, 40, 200])
+
+
 def test_gated_delta_extremes():
     """Decays that forget everything, states and values far apart in size, keys of zero, beta of zero and one."""
     rng = np.random.default_rng(10)

@@ -101,7 +101,11 @@ def norm(**kw):
     (dict(cols=2 ** 31, group=2 ** 31, x_stride=2 ** 31), SHAPE), (dict(x_stride=63), SHAPE), (dict(sum_stride=8), SHAPE),
     (dict(gate_stride=0), SHAPE), (dict(x_dtype=3), INVALID), (dict(out_dtype=-1), INVALID), (dict(weight_dtype=9), INVALID),
     (dict(x=FAKE + 1), ALIGN), (dict(weight=FAKE + 2, weight_dtype=nt.F32), ALIGN), (dict(out_stride=2 ** 40), OVERFLOW),
-    (dict(rows=2 ** 31), OVERFLOW), (dict(rows=2 ** 26, group=1), OVERFLOW), (dict(rows=2 ** 63, group=1), OVERFLOW)])
+    (dict(rows=2 ** 31), OVERFLOW), (dict(rows=2 ** 26, group=1), OVERFLOW), (dict(rows=2 ** 63, group=1), OVERFLOW),
+    # in place with another stride or type, outputs over each other or over other inputs
+    (dict(out=FAKE, out_stride=72), INVALID), (dict(out=FAKE, out_dtype=nt.F16), INVALID), (dict(out=FAKE * 3, gate_stride=72), INVALID),
+    (dict(out=FAKE * 3, gate_dtype=nt.F16), INVALID), (dict(sum=FAKE * 2, sum_stride=72), INVALID), (dict(out=FAKE * 2), INVALID),
+    (dict(out=FAKE * 5), INVALID), (dict(sum=FAKE), INVALID), (dict(sum=FAKE * 3), INVALID)])
 def test_norm_refusals(kw, status):
     assert norm(**kw) == status
     assert lib.ninfer_norm(None, None) == INVALID
@@ -113,7 +117,7 @@ ROTARY = ["q", "k", "q_weight", "k_weight", "q_out", "k_out", "positions", "freq
 
 
 def rotary(**kw):
-    a = dict(zip(ROTARY, [FAKE] * 8 + [3, 4, 2, 64, 32] + [256, 64, 128, 64] * 2 + [1.0, 1e-6, 0.0, nt.BF16, nt.F32, 0]))
+    a = dict(zip(ROTARY, [FAKE, 2 * FAKE, FAKE, FAKE, FAKE, 2 * FAKE, FAKE, FAKE] + [3, 4, 2, 64, 32] + [256, 64, 128, 64] * 2 + [1.0, 1e-6, 0.0, nt.BF16, nt.F32, 0]))
     a.update(kw)
     return lib.ninfer_rotary(nt._ROTARY.pack(*[a[n] for n in ROTARY]), None)
 
@@ -125,7 +129,8 @@ def rotary(**kw):
     (dict(q_heads=0), SHAPE), (dict(kv_heads=0), SHAPE), (dict(q_heads=65536), SHAPE), (dict(head_dim=60), SHAPE), (dict(head_dim=264), SHAPE),
     (dict(rotary_dim=0), SHAPE), (dict(rotary_dim=31), SHAPE), (dict(rotary_dim=66), SHAPE), (dict(q=FAKE + 8), ALIGN),
     (dict(k_out=FAKE + 2), ALIGN), (dict(q_token=260), ALIGN), (dict(k_out_head=65), ALIGN), (dict(positions=FAKE + 2), ALIGN),
-    (dict(frequencies=FAKE + 4), ALIGN), (dict(q_weight=FAKE + 4), ALIGN), (dict(k_token=2 ** 40), OVERFLOW)])
+    (dict(frequencies=FAKE + 4), ALIGN), (dict(q_weight=FAKE + 4), ALIGN), (dict(k_token=2 ** 40), OVERFLOW),
+    (dict(q_out_token=512), INVALID), (dict(k_out_head=128), INVALID), (dict(q_out=2 * FAKE), INVALID), (dict(k_out=FAKE), INVALID)])
 def test_rotary_refusals(kw, status):
     assert rotary(**kw) == status
     assert lib.ninfer_rotary(None, None) == INVALID
@@ -151,7 +156,7 @@ def delta(workspace=FAKE, bytes_=2 ** 40, **kw):
     (dict(beta_stride=0), SHAPE), (dict(q=FAKE + 8), ALIGN), (dict(q_token=132), ALIGN), (dict(v_head=33), ALIGN), (dict(k_token=2 ** 40), OVERFLOW),
     (dict(slot_stride=2 ** 40), OVERFLOW), (dict(slot_stride=8194), ALIGN), (dict(state=FAKE + 4), ALIGN), (dict(out=FAKE + 8), ALIGN),
     (dict(offsets=FAKE + 1), ALIGN), (dict(log_decay=FAKE + 2), ALIGN), (dict(status=FAKE + 2), ALIGN),
-    (dict(requests=2 ** 31 - 1, v_heads=4096, k_heads=1, slots=2 ** 31 - 1, slot_stride=2 ** 32, decay_stride=4096, beta_stride=4096), OVERFLOW)])
+    (dict(requests=2 ** 31 - 1, v_heads=4096, k_heads=1, slots=2 ** 31 - 1, slot_stride=2 ** 32, decay_stride=4096, beta_stride=4096, bytes_=2 ** 63), OVERFLOW)])
 def test_gated_delta_refusals(kw, status):
     assert delta(**kw) == status
     assert lib.ninfer_gated_delta(None, None, 0, None) == INVALID
