@@ -8,7 +8,11 @@
 // that one pass over the state gives both sums and a second one, in registers, updates it: the state is read once and
 // written once, and HBM bounds it.
 // Several (prepare_kernel, chunk_kernel): 32 tokens at once, by matrix products whose state stays in registers from a
-// request's first token to its last; the tensor cores bound it, and latency where few heads are under way.
+// request's first token to its last. The chain of dependent products bounds it (the tensor cores are busy for a third of it).
+//
+// Measured: 64 requests of one token, 48 states of 128 x 128 each, 405 MB, 69 us (5.9 TB/s; with 128 columns a CTA, one CTA an SM, 104).
+// A prompt of 8001 tokens with 48 heads: 117 us of preparation and 645 of chunks, 2.6 us each; token by token in fp32, four
+// lanes a column, 7390.
 #include <cmath>
 
 #include "decode.cuh"

@@ -5,8 +5,11 @@
 // a whole number of 2^-64 turns: position times frequency modulo 2^64 is exact in integers, and what
 // remains of it, as a signed fraction, goes through sincospif, so that position 2^31 is as exact as position 1
 // without 64-bit floats. The sines and cosines of a token serve all of its heads: a CTA takes one
-// token (or several, where they have few heads), puts them into shared memory and then turns its heads,
-// a few lanes each, 8 elements a lane.
+// token, asks for its first heads, puts the sines and cosines into shared memory and then turns its heads,
+// a few lanes each, 8 elements a lane, with as many threads as take them in the fewest rounds.
+//
+// Measured: 30011 tokens of 40 heads of 128 in bfloat16, 615 MB, 102 us (6.0 TB/s). Heads asked for only after the sines and
+// cosines: 140; 256 threads for every token: 125; 64 registers a thread instead of 48: 109.
 #include <cmath>
 
 #include "decode.cuh"

@@ -6,17 +6,24 @@
 // number of tokens. The token is then the first whose running sum in the order of the row passes the random number's share
 // of the whole.
 //
-// Weights are whole numbers (units of 2^-scale of the largest one), exact to 2^-30 of themselves: sums of them do not
-// depend on the order in which threads and CTAs add, which makes borders and choices the same however a row is divided. A
-// weight is 2^t, t = (x - m) log2(e) / T in two floats: a table of 64 powers for the fraction's first six bits, the
-// exponential's series for the rest, everything else in integers.
+// Weights are whole numbers (units of 2^-scale of the largest one), exact to 2^-30 of themselves but for the rounding of x - m: sums
+// of them do not depend on the order in which threads and CTAs add, which makes borders and choices the same however a row is
+// divided. A weight is 2^t, t = (x - m) log2(e) / T in two floats: a table of 64 powers for the fraction's first six bits, the
+// exponential's series for the rest, everything else in integers. Shares of sums are products of whole numbers too.
 //
 // A row is divided among the CTAs of a cluster, which hold it in shared memory (read once from HBM) and exchange maxima, sums and
-// histograms through distributed shared memory. A border is found in two passes: a histogram of 2048 bins, 1/64 of a
+// histograms through distributed shared memory. Whatever keeps few tokens is chosen from by the first CTA alone, to which all
+// push the tokens that may be kept, so that the others end: those of min-p by their weight; for top-k and top-p (whose sum over all tokens is
+// taken first) down to where a histogram of one logit for each thread, its largest, reaches the count or the share, which is
+// hardly further than where all logits do. Other borders are found in two passes: a histogram of 2048 bins, 1/64 of a
 // power of two wide, from the largest logit down, of counts (top-k) or weights to 16 bits (top-p), tells the bin or the few bins
-// in which it lies; their tokens, seldom more than a few hundred, are sorted by the cluster's first CTA, which adds their exact weights
+// in which it lies; their tokens, seldom more than a few hundred, are sorted by the first CTA, which adds their exact weights
 // to the exact sum of what lies above. Where more than 2048 tokens lie there (equal logits without end), the border comes from the
-// key's bits, eight at a time. Rows that keep few tokens (top-k up to 1024, min-p) have all of them sorted and chosen from by that CTA.
+// key's bits, eight at a time.
+//
+// What bounds it: HBM for nothing but greedy rows (64 of 248320 fp32 logits, 64 MB, 21 us); about 40 instructions for each exact weight
+// (temperature alone: 80 us; large nuclei, which need them twice: 140), and the chain of a cluster's exchanges (top-k 57, min-p 39; one row 9 to
+// 13 us, 40 with a nucleus of most of the row).
 #include <cfloat>
 #include <cmath>
 #include <cstddef>
