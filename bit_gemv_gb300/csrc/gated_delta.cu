@@ -248,6 +248,22 @@ __device__ __forceinline__ Range range_of(const ninfer_gated_delta_args &a, uint
 
 constexpr uint32_t kTriRow = kChunk + 4, kTriSmem = kPrepareThreads / 32 * kChunk * kTriRow * 4;
 
+// 32 rows by 32 columns, a lane's `x` its column, as two binary16 matrices under the power of two that fits the largest; its inverse.
+__device__ __forceinline__ float put_matrix(uint8_t *to, const float (&x)[kChunk], float most, uint32_t lane) {
+#pragma unroll
+    for (int k = 16; k; k /= 2) most = fmaxf(most, __shfl_xor_sync(~0u, most, k));
+    const float up = power_for(most);
+#pragma unroll
+    for (int t = 0; t < kChunk; ++t) {
+        const float y = x[t] * up;
+        const __half high = __float2half_rn(y);
+        __half *at = reinterpret_cast<__half *>(to + t * kTriStride) + lane;
+        at[0] = high;
+        at[kChunk * kTriStride / 2] = __float2half_rn(y - __half2float(high));
+    }
+    return inverse_power(up);
+}
+
 // A CTA for every chunk and key head. kTerms: binary16 terms of k and q, 1 where they have 16 bits themselves.
 template <int kTerms>
 __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
@@ -380,6 +396,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
         const float poison = bad & (~0u >> (31 - lane)) ? NAN : 1.f, spoilt = bad ? NAN : 1.f;
         sums[warp][lane] = make_float4(high, low, beta, 0.f);
         __syncwarp();
+        uint8_t *to = p.heads + ((uint64_t)chunk * a.v_heads + head) * kHeadBytes;       // T high and low, P high and low, the numbers
         float pp[kChunk], tt[kChunk], most_p = 0.f, most_t = 0.f;
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) {
@@ -389,6 +406,7 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
             pp[t] = (int)lane <= t ? fade * dots[1][t][lane] : 0.f;
             most_p = fmaxf(most_p, fabsf(pp[t]));
         }
+        const float of_p = put_matrix(to + 2 * kChunk * kTriStride, pp, most_p, lane);      // first, so that its registers are free for T
         __syncwarp();
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) {
@@ -406,33 +424,13 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
 #pragma unroll
         for (int t = 0; t < kChunk; ++t) most_t = fmaxf(most_t, fabsf(tt[t] *= beta));
         __syncwarp();
-#pragma unroll
-        for (int k = 16; k; k /= 2) {
-            most_p = fmaxf(most_p, __shfl_xor_sync(~0u, most_p, k));
-            most_t = fmaxf(most_t, __shfl_xor_sync(~0u, most_t, k));
-        }
-        const float up_p = power_for(most_p), up_t = power_for(most_t);
-        uint8_t *to = p.heads + ((uint64_t)chunk * a.v_heads + head) * kHeadBytes;
-        __half *out = reinterpret_cast<__half *>(to);
-#pragma unroll
-        for (int t = 0; t < kChunk; ++t) {
-            const float x = tt[t] * up_t, y = pp[t] * up_p;
-            const __half xh = __float2half_rn(x), yh = __float2half_rn(y);
-            constexpr uint32_t kRow = kTriStride / 2;
-            out[t * kRow + lane] = xh;
-            out[(kChunk + t) * kRow + lane] = __float2half_rn(x - __half2float(xh));
-            out[(2 * kChunk + t) * kRow + lane] = yh;
-            out[(3 * kChunk + t) * kRow + lane] = __float2half_rn(y - __half2float(yh));
-        }
+        const float of_t = put_matrix(to, tt, most_t, lane);
         float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
         const float fade = exp2f(high + low) * poison;
         numbers[kOfK + lane] = fade * scales[0][lane];
         numbers[kOfQ + lane] = a.scale * fade * scales[1][lane];
         numbers[kOfU + lane] = exp2f((last_high - high) + (last_low - low)) * scales[0][lane];
-        if (lane < 4) {
-            const float x = lane == 0 ? exp2f(last_high + last_low) * spoilt : lane == 1 ? inverse_power(up_t) : lane == 2 ? a.scale * inverse_power(up_p) : 0.f;
-            numbers[kLeft + lane] = x;
-        }
+        if (lane < 3) numbers[kLeft + lane] = lane == 0 ? exp2f(last_high + last_low) * spoilt : lane == 1 ? of_t : a.scale * of_p;
     }
 }
 
@@ -516,19 +514,20 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
         copies_arrive(bar);
         sent = j + 1;
     };
-    // No CTA ends with copies under way, not where a wait has run out either: a limit of its own, a millisecond, for them to land.
+    // No CTA ends with copies under way, not where a wait has run out either: at least a millisecond for them to land.
     constexpr long long kLanding = 2000000;
     auto drain = [&]() {
-        for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, kLanding);
+        for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, max(p.wait_limit, kLanding));
     };
-    constexpr bool kSender = chunk_threads(kSteps) > 256;
-    if (kSender && warp == 8) {
+    // who copies: a ninth warp, or one whose pair has no columns, or the first beside its other work
+    const uint32_t sender = chunk_threads(kSteps) > 256 ? 8 : columns <= kColumns - 16 ? 7 : 0;
+    if (warp == sender && sender) {
         for (uint32_t j = 0; j < range.chunks && good; ++j) send(j);
         drain();
         return;
     }
     if (pair * 16 >= columns) return;      // whole pairs
-    if (!kSender && warp == 0)
+    if (warp == sender)
         for (uint32_t j = 0; j < min(kStages - 1, range.chunks); ++j) send(j);
     // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
     float s[2 * kSteps][4];
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
                     for (int n = 0; n < 8; ++n) mma(x[n], high, y[n / 2][n % 2 * 2], y[n / 2][n % 2 * 2 + 1]);
                 }
             }
-            if (!kSender && warp == 0 && j + kStages - 1 < range.chunks) send(j + kStages - 1);
+            if (warp == sender && j + kStages - 1 < range.chunks) send(j + kStages - 1);
             {
                 const float down0 = inverse_power(up0), down1 = inverse_power(up1);
 #pragma unroll
@@ -798,7 +797,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
         }
     }
     if (!good) {
-        if (!kSender && warp == 0) drain();
+        if (warp == sender) drain();
         return;
     }
 #pragma unroll
