@@ -266,7 +266,7 @@ __device__ __forceinline__ float put_matrix(uint8_t *to, const float (&x)[kChunk
 
 // A CTA for every chunk and key head. kTerms: binary16 terms of k and q, 1 where they have 16 bits themselves.
 template <int kTerms>
-__global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __grid_constant__ ChunkParams p) {
     extern __shared__ __align__(16) uint8_t smem[];     // K and Q in binary16, rows of p.wide + 8; then a triangle of each warp
     __shared__ float dots[2][kChunk][kChunk + 1], scales[2][kChunk];
     __shared__ float4 sums[kPrepareThreads / 32][kChunk];      // the log decays' sums in two floats, beta
@@ -294,41 +294,67 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     // 16 lanes a row where it has no more than 128 elements
     const uint32_t row_lanes = p.wide <= 128 ? 16 : 32, at_once = kPrepareThreads / row_lanes, e0 = tid % row_lanes * 8;
     const bool low_dim = e0 < k_dim, in_row = e0 < p.wide;
-#pragma unroll 4
-    for (uint32_t i = tid / row_lanes; i < 2 * kChunk; i += at_once) {
-        const uint32_t t = i % kChunk, q = i / kChunk;
-        float x[8] = {}, sum = 0.f, most = 0.f;
-        if ((int32_t)t < count && low_dim) {
-            const uint64_t token = first + t;
-            const uint64_t at = q ? token * a.q_token_stride + key_head * a.q_head_stride : token * a.k_token_stride + key_head * a.k_head_stride;
-            load8(q ? a.q : a.k, at + e0, a.dtype, x);
+    // each head's decays of this lane's token; the first ones before the rows, so that they are there when the triangles are made
+    const bool on = (int32_t)lane < count;
+    const uint32_t group = p.d.group.d;
+    const uint64_t decays_at = (first + (on ? lane : 0)) * a.decay_stride + key_head * group, betas_at = (first + (on ? lane : 0)) * a.beta_stride + key_head * group;
+    float g = 0.f, beta = 0.f;
+    if (on && warp < group) {
+        g = a.log_decay[decays_at + warp];
+        beta = a.beta[betas_at + warp];
+    }
+    constexpr uint32_t kBatch = 8 / kTerms;     // rows on their way at once
+    uint4 raw[kBatch][kTerms];
+    for (uint32_t i0 = tid / row_lanes; i0 < 2 * kChunk; i0 += kBatch * at_once) {
+#pragma unroll
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t i = i0 + j * at_once, t = i % kChunk, q = i / kChunk;
+#pragma unroll
+            for (int e = 0; e < kTerms; ++e) raw[j][e] = make_uint4(0, 0, 0, 0);
+            if ((int32_t)t < count && low_dim) {
+                const uint64_t token = first + t;
+                const uint64_t at = q ? token * a.q_token_stride + key_head * a.q_head_stride : token * a.k_token_stride + key_head * a.k_head_stride;
+                const uint4 *from = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(q ? a.q : a.k) + (at + e0) * kTerms);
+#pragma unroll
+                for (int e = 0; e < kTerms; ++e) raw[j][e] = __ldg(from + e);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            sum = fmaf(x[e], x[e], sum);
-            most = fmaxf(most, fabsf(x[e]));
-        }
-        if (row_lanes == 32) {
-            sum += __shfl_xor_sync(~0u, sum, 16);
-            most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
-        }
+        for (uint32_t j = 0; j < kBatch; ++j) {
+            const uint32_t i = i0 + j * at_once, t = i % kChunk, q = i / kChunk;
+            float x[8], sum = 0.f, most = 0.f;
 #pragma unroll
-        for (int e = 8; e; e /= 2) {
-            sum += __shfl_xor_sync(~0u, sum, e);
-            most = fmaxf(most, __shfl_xor_sync(~0u, most, e));
-        }
-        const float up = power_for(most);
-        if (e0 == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
-        uint32_t high[4], low[4];
+            for (int e = 0; e < 8; ++e) {
+                const uint4 &r = raw[j][kTerms == 2 ? e / 4 : 0];
+                const uint32_t words[4] = {r.x, r.y, r.z, r.w}, word = words[kTerms == 2 ? e % 4 : e / 2];
+                if (kTerms == 2) x[e] = __uint_as_float(word);
+                else if (a.dtype == NINFER_BF16) x[e] = __uint_as_float(e % 2 ? word & 0xffff0000u : word << 16);
+                else x[e] = __half2float(__ushort_as_half((unsigned short)(e % 2 ? word >> 16 : word & 0xffffu)));
+                sum = fmaf(x[e], x[e], sum);
+                most = fmaxf(most, fabsf(x[e]));
+            }
+            if (row_lanes == 32) {
+                sum += __shfl_xor_sync(~0u, sum, 16);
+                most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
+            }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split(x[2 * e] * up, x[2 * e + 1] * up, high[e], low[e]);
-        if (in_row) {
-            const uint4 h = make_uint4(high[0], high[1], high[2], high[3]), l = make_uint4(low[0], low[1], low[2], low[3]);
-            *reinterpret_cast<uint4 *>(smem + i * stride + e0 * 2) = h;
-            *reinterpret_cast<uint4 *>(rows + i * stride + e0 * 2) = h;
-            if (kTerms == 2) {
-                *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + e0 * 2) = l;
-                *reinterpret_cast<uint4 *>(rows + term_bytes + i * stride + e0 * 2) = l;
+            for (int e = 8; e; e /= 2) {
+                sum += __shfl_xor_sync(~0u, sum, e);
+                most = fmaxf(most, __shfl_xor_sync(~0u, most, e));
+            }
+            const float up = power_for(most);
+            if (e0 == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
+            uint32_t high[4], low[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split(x[2 * e] * up, x[2 * e + 1] * up, high[e], low[e]);
+            if (in_row) {
+                const uint4 h = make_uint4(high[0], high[1], high[2], high[3]), l = make_uint4(low[0], low[1], low[2], low[3]);
+                *reinterpret_cast<uint4 *>(smem + i * stride + e0 * 2) = h;
+                *reinterpret_cast<uint4 *>(rows + i * stride + e0 * 2) = h;
+                if (kTerms == 2) {
+                    *reinterpret_cast<uint4 *>(smem + term_bytes + i * stride + e0 * 2) = l;
+                    *reinterpret_cast<uint4 *>(rows + term_bytes + i * stride + e0 * 2) = l;
+                }
             }
         }
     }
@@ -374,12 +400,12 @@ __global__ void __launch_bounds__(kPrepareThreads) prepare_kernel(const __grid_c
     // A warp a value head: lane s has column s of both triangles. Log decays are added up in units of ln 2 and in two floats, so that
     // differences of far sums are as exact as those of near ones; 2^(+-2^15) is all the same.
     float(*tri)[kChunk][kTriRow] = reinterpret_cast<float(*)[kChunk][kTriRow]>(smem);
-    const uint32_t group = p.d.group.d;
     for (uint32_t i = warp; i < group; i += kPrepareThreads / 32) {
         const uint32_t head = key_head * group + i;
-        const bool on = (int32_t)lane < count;
-        const uint64_t token = first + (on ? lane : 0);
-        const float g = on ? a.log_decay[token * a.decay_stride + head] : 0.f, beta = on ? a.beta[token * a.beta_stride + head] : 0.f;
+        if (on && i != warp) {
+            g = a.log_decay[decays_at + i];
+            beta = a.beta[betas_at + i];
+        }
         const float bound = fminf(fmaxf(g, -32768.f), 32768.f);
         float high = bound * 1.44269504f, low = fmaf(bound, 1.44269504f, -high) + bound * 1.92596299e-8f;
 #pragma unroll
