@@ -11,7 +11,7 @@
 // request's first token to its last. The chain of dependent products bounds it (the tensor cores are busy for a third of it).
 //
 // Measured: 64 requests of one token, 48 states of 128 x 128 each, 405 MB, 69 us (5.9 TB/s; with 128 columns a CTA, one CTA an SM, 104).
-// A prompt of 8001 tokens with 48 heads: 90 us of preparation and 590 of chunks, 2.35 us each; token by token in fp32, four
+// A prompt of 8001 tokens with 48 heads: 89 us of preparation and 515 of chunks, 2.05 us each; token by token in fp32, four
 // lanes a column, 7390.
 #include <cmath>
 
@@ -460,27 +460,114 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
     }
 }
 
-// Eight warps that compute, and one that copies where it leaves them registers enough (128 columns of k in 224 of them: 777 us for 681).
+// A ninth warp copies where it leaves the others registers enough: 168 a thread instead of 255.
 __host__ __device__ constexpr int chunk_threads(int steps) { return steps < 4 ? 288 : 256; }
 
 // Chunks in shared memory at once, and buffers for the sums: what fits an SM.
 __host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
 __host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 1 : 2; }
 
+// With 48 columns a CTA (3 pairs) the two warps without any take from the pairs' chain what is not of it: the results (P U and Q S), made
+// by one of them (the other copies) or, with a ninth warp, by both; 8001 tokens with 48 heads 603 us, by the pairs themselves 681. What a
+// pair hands over: U and Q S of 16 columns by 32 tokens, two buffers.
+constexpr uint32_t kResultWarp = 6, kHandedBytes = 8 * 32 * 16;
+__host__ __device__ constexpr uint32_t pairs_of(bool results) { return results ? 3 : 4; }
+
+// Shared memory: the stages, the results' turning (16 tokens by 16 columns a warp), the pairs' sums, what is handed over.
+__host__ __device__ constexpr uint32_t stage_bytes_of(uint32_t wide, int terms) {
+    return terms * 2 * kChunk * (wide * 2 + 16) + kHeadBytes + kChunk * (kColumns * (terms == 2 ? 4 : 2) + 16);
+}
+__host__ __device__ constexpr uint32_t sums_at_of(uint32_t wide, int terms, bool results) {
+    return stages_of(wide, terms) * stage_bytes_of(wide, terms) + (results ? 2 : 8) * (kChunk / 2 * 80);
+}
+__host__ __device__ constexpr uint32_t handed_at_of(uint32_t wide, int terms, bool results) {
+    return sums_at_of(wide, terms, results) + sums_of(wide, terms) * pairs_of(results) * 2 * 6 * 32 * 16;
+}
+__host__ __device__ constexpr uint32_t chunk_smem_of(uint32_t wide, int terms, bool results) {
+    return handed_at_of(wide, terms, results) + (results ? pairs_of(results) * 2 * kHandedBytes : 0);
+}
+
+// 16 columns by 32 tokens as the A operand, each column times its power of two.
+__device__ __forceinline__ void halves(const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            split(y[2 * k + h][0] * p0, y[2 * k + h][1] * p0, high[k][2 * h], low[k][2 * h]);
+            split(y[2 * k + h][2] * p1, y[2 * k + h][3] * p1, high[k][2 * h + 1], low[k][2 * h + 1]);
+        }
+}
+// 16 tokens of a matrix's rows as the B operand, of both of its terms.
+__device__ __forceinline__ void load_terms(uint32_t (&b)[2][4], uint32_t from) {
+    load_matrices(b[0], from);
+    load_matrices(b[1], from + kChunk * kTriStride);
+}
+__device__ __forceinline__ void times(float (&y)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], const uint32_t (&b)[2][4], int i, int term) {
+    mma(y, term == 2 ? low : high, b[term == 1][2 * i], b[term == 1][2 * i + 1]);
+}
+// u += A times a lower triangle whose first term lies at `from` (this lane's row and column of the first 16 by 16).
+__device__ __forceinline__ void times_triangle(float (&u)[4][4], const uint32_t (&high)[2][4], const uint32_t (&low)[2][4], uint32_t from) {
+    uint32_t t00[2][4], t01[2][4], t11[2][4];
+    load_terms(t00, from);
+    load_terms(t01, from + 16 * kTriStride);
+    load_terms(t11, from + 16 * kTriStride + 32);
+#pragma unroll
+    for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            times(u[i], high[0], low[0], t00, i, term);
+            times(u[2 + i], high[0], low[0], t01, i, term);
+        }
+#pragma unroll
+    for (int term = 0; term < 3; ++term)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) times(u[2 + i], high[1], low[1], t11, i, term);
+}
+// 16 tokens by 16 columns to where this lane's first 16 bytes go, turned in shared memory at `at`; `left` tokens there are.
+struct Results {
+    uint32_t es, row;       // bytes an element, this lane's token
+    uint64_t step;          // bytes a token
+    bool on;
+};
+__device__ __forceinline__ void put_results(const Results &r, int dtype, uint8_t *smem, uint32_t at, uint8_t *to, const float (&o)[2][4], int32_t left, uint32_t lane) {
+    if (dtype == NINFER_F32) {
+        uint8_t *turned = smem + at + lane % 4 * 160 + lane / 4 * 4;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(turned + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 32) = o[i / 4][i % 4];
+    } else {
+        uint32_t x[4];          // pairs of tokens, turned as they are stored
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
+            const __half2 h = __floats2half2_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
+            x[i] = dtype == NINFER_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
+        }
+        store_matrices_turned(smem_u32(smem) + at + (lane % 8 + lane / 16 * 8) * 80 + lane / 8 % 2 * 16, x);
+    }
+    __syncwarp();
+    const uint8_t *from = smem + at + r.row * 80 + lane % r.es * 16;
+    if (r.on && (int32_t)r.row < left) *reinterpret_cast<uint4 *>(to) = *reinterpret_cast<const uint4 *>(from);
+    if (r.es == 4 && r.on && (int32_t)r.row + 8 < left) *reinterpret_cast<uint4 *>(to + 8 * r.step) = *reinterpret_cast<const uint4 *>(from + 8 * 80);
+    __syncwarp();
+}
+
 // 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
 // products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
 // as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
-// outputs by tokens. A warp without columns keeps the next chunks coming (bulk copies, mbarriers); nothing else holds pairs together, so
+// outputs by tokens where no other warp makes them. One warp keeps the next chunks coming (bulk copies, mbarriers); nothing else holds pairs together, so
 // that of two pairs on a scheduler one multiplies while the other splits and scales.
-// kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q.
-template <int kSteps, int kTerms>
-__global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __grid_constant__ ChunkParams p) {
+// kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q; kResults: 48 columns. One CTA an SM is said where ptxas otherwise
+// takes fewer registers and loads later (173 for 207: 662 us for 603).
+template <int kSteps, int kTerms, bool kResults>
+__global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4 ? 1 : 0) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride;
     constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + kTrianglesBytes, kV = kTri + kHeadBytes;
     constexpr uint32_t kSums = sums_of(kSteps * 32, kTerms), es = kTerms == 2 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
+    static_assert(stage_bytes == stage_bytes_of(kSteps * 32, kTerms));
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
+    constexpr bool kNinth = chunk_threads(kSteps) > 256;       // a warp that copies
+    __shared__ __align__(8) uint64_t full[kStages], empty[kStages], handed[3][2], taken[3][2];
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_gated_delta_args &a = p.d.a;
@@ -493,14 +580,19 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
     if (tid == 0) {
         for (uint32_t i = 0; i < kStages; ++i) {
             mbar_init(smem_u32(&full[i]), 1 + 32);          // the bulk copies, and each lane's of the values
-            mbar_init(smem_u32(&empty[i]), (columns + 15) / 16 * 2);
+            mbar_init(smem_u32(&empty[i]), (columns + 15) / 16 * 2 + kResults);
+        }
+        for (uint32_t i = 0; kResults && i < 6; ++i) {
+            mbar_init(smem_u32(&handed[i / 2][i % 2]), 2);       // a pair's warps
+            mbar_init(smem_u32(&taken[i / 2][i % 2]), 1);
         }
         fence_mbar_init();
     }
     __syncthreads();
     const uint32_t pair = warp / 2, half = warp % 2;
     const bool bf16 = a.dtype == NINFER_BF16;
-    const uint32_t out_at = kStages * stage_bytes + warp * (kChunk / 2 * 80), sums_at = kStages * stage_bytes + 8 * (kChunk / 2 * 80);
+    constexpr uint32_t kSumsAt = sums_at_of(kSteps * 32, kTerms, kResults), kHandedAt = handed_at_of(kSteps * 32, kTerms, kResults);
+    const uint32_t out_at = kStages * stage_bytes + (kResults ? warp % 2 : warp) * (kChunk / 2 * 80);
     const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
     const uint32_t t_row = lane % 16, t_col = lane / 16 * 16, half_col = half * kSteps * 32;
@@ -545,16 +637,72 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
     auto drain = [&]() {
         for (uint32_t j = sent > kStages ? sent - kStages : 0; j < sent; ++j) mbar_wait(smem_u32(&full[j % kStages]), j / kStages & 1, p.error, max(p.wait_limit, kLanding));
     };
-    // who copies: a ninth warp, or one whose pair has no columns, or the first beside its other work
-    const uint32_t sender = chunk_threads(kSteps) > 256 ? 8 : columns <= kColumns - 16 ? 7 : 0;
-    if (warp == sender && sender) {
+    // a lane's first 16 bytes of results: of 16 tokens by 16 columns, two (f32: four) a token
+    const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2, out_col = lane % out_es * 16 / out_es;
+    const uint64_t out_step = a.v_heads * v_dim * out_es;
+    Results results = {out_es, lane / out_es, out_step, mine + out_col < v_dim};
+    uint8_t *to_out = static_cast<uint8_t *>(a.out) + (uint64_t)(range.begin + results.row) * out_step + ((uint64_t)part.head * v_dim + part.column + out_col) * out_es;
+    uint32_t slot = 0, parity = 0;
+    // who copies: a ninth warp, or one without columns, or the first beside its other work
+    const uint32_t sender = kNinth ? 8 : kResults ? kResultWarp + 1 : 0;
+    if ((kNinth || kResults) && warp == sender) {
         for (uint32_t j = 0; j < range.chunks && good; ++j) send(j);
         drain();
+        return;
+    }
+    constexpr uint32_t kResultWarps = kNinth ? 2 : 1;       // each has its chunks
+    if (kResults && warp >= kResultWarp && warp < kResultWarp + kResultWarps) {
+        to_out += (warp - kResultWarp) * kChunk * out_step;
+        for (uint32_t j = warp - kResultWarp; j < range.chunks; j += kResultWarps) {
+            slot = j % kStages;
+            parity = j / kStages & 1;
+            good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[slot]), parity, p.error, p.wait_limit)));
+            const uint32_t stage = base + slot * stage_bytes;
+            const float *numbers = reinterpret_cast<const float *>(smem + slot * stage_bytes + kNumbersAt);
+            const int32_t count = min(range.end - range.begin - (int32_t)j * kChunk, kChunk);
+            for (uint32_t g = 0; g * 16 < columns; ++g) {
+                good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&handed[g][j % 2]), j / 2 & 1, p.error, p.wait_limit)));
+                const float4 *from = reinterpret_cast<const float4 *>(smem + kHandedAt + (g * 2 + j % 2) * kHandedBytes) + lane;
+                float u[4][4], qs[4][4], o[4][4] = {}, m0 = 0.f, m1 = 0.f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    const float4 x = from[n * 32], y = from[(4 + n) * 32];
+                    u[n][0] = x.x; u[n][1] = x.y; u[n][2] = x.z; u[n][3] = x.w;
+                    qs[n][0] = y.x; qs[n][1] = y.y; qs[n][2] = y.z; qs[n][3] = y.w;
+                    m0 = fmaxf(m0, fmaxf(fabsf(x.x), fabsf(x.y)));
+                    m1 = fmaxf(m1, fmaxf(fabsf(x.z), fabsf(x.w)));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&taken[g][j % 2]));
+                const float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
+                uint32_t high[2][4], low[2][4];
+                halves(u, p0, p1, high, low);
+                times_triangle(o, high, low, stage + kTri + (2 * kChunk + b_row) * kTriStride + b_col);
+                const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
+                if (!good) continue;
+                results.on = part.column + g * 16 + out_col < v_dim;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float y[2][4];
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        const float2 of_q = *reinterpret_cast<const float2 *>(numbers + kOfQ + (h * 2 + n) * 8 + lane % 4 * 2);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) y[n][e] = (e % 2 ? of_q.y : of_q.x) * qs[2 * h + n][e] + o[2 * h + n][e] * (e / 2 ? g1 : g0);
+                    }
+                    put_results(results, a.out_dtype, smem, out_at, to_out + (uint64_t)h * 16 * out_step + g * 16 * out_es, y, count - h * 16, lane);
+                }
+            }
+            to_out += kResultWarps * kChunk * out_step;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
+        }
         return;
     }
     if (pair * 16 >= columns) return;      // whole pairs
     if (warp == sender)
         for (uint32_t j = 0; j < min(kStages - 1, range.chunks); ++j) send(j);
+    to_out += (uint64_t)half * 16 * out_step + pair * 16 * out_es;
     // s[n][e]: k = 16 kSteps half + 8 n + 2 (lane % 4) + e % 2 of column (e / 2: + 8)
     float s[2 * kSteps][4];
     float *state = a.state + part.state;
@@ -566,12 +714,6 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
             const uint32_t k = k_first + n * 8 + e % 2, c = column + e / 2 * 8;
             s[n][e] = k < k_dim && c < v_dim && !part.fresh ? state[k * v_dim + c] : 0.f;
         }
-    // this lane's first 16 bytes of a chunk's results: of 16 tokens by 16 columns, two (f32: four) a token
-    const uint32_t out_es = a.out_dtype == NINFER_F32 ? 4 : 2, out_row = lane / out_es, out_col = lane % out_es * 16 / out_es;
-    const bool out_on = mine + out_col < v_dim;
-    const uint64_t out_step = a.v_heads * v_dim * out_es;
-    uint8_t *to_out = static_cast<uint8_t *>(a.out) + (uint64_t)(range.begin + half * 16 + out_row) * out_step + ((uint64_t)part.head * v_dim + mine + out_col) * out_es;
-    uint32_t slot = 0, parity = 0;
     for (uint32_t j = 0; j < range.chunks; ++j) {
         good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&full[slot]), parity, p.error, p.wait_limit)));
         const uint32_t stage = base + slot * stage_bytes;
@@ -624,8 +766,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
             }
             // the pair's halves: all of K S to both, of Q S the first 16 tokens to the first. Two buffers: who writes one again has
             // passed the barrier between, and with it the other's reads.
-            float4 *sums = reinterpret_cast<float4 *>(smem + sums_at) + (j % kSums * 8 + warp) * 6 * 32 + lane;
-            const float4 *others = reinterpret_cast<const float4 *>(smem + sums_at) + (j % kSums * 8 + (warp ^ 1)) * 6 * 32 + lane;
+            float4 *sums = reinterpret_cast<float4 *>(smem + kSumsAt) + (j % kSums * (2 * pairs_of(kResults)) + warp) * 6 * 32 + lane;
+            const float4 *others = reinterpret_cast<const float4 *>(smem + kSumsAt) + (j % kSums * (2 * pairs_of(kResults)) + (warp ^ 1)) * 6 * 32 + lane;
 #pragma unroll
             for (int n = 0; n < 4; ++n) sums[n * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
 #pragma unroll
@@ -680,43 +822,11 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
                 for (int e = 0; e < 4; ++e) qs[n][e] = (half ? x[6 + n][e] : x[4 + n][e]) + oe[e];
             }
             if (kSums == 1) named_barrier(1 + pair, 64);
-            auto halves = [&](const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
-#pragma unroll
-                for (int k = 0; k < 2; ++k)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        split(y[2 * k + h][0] * p0, y[2 * k + h][1] * p0, high[k][2 * h], low[k][2 * h]);
-                        split(y[2 * k + h][2] * p1, y[2 * k + h][3] * p1, high[k][2 * h + 1], low[k][2 * h + 1]);
-                    }
-            };
-            // 16 tokens t = 16 n .. of a triangle, given by its first of two terms, as the B operand: columns s = 16 k ..
-            auto triangle = [&](uint32_t (&b)[2][4], uint32_t which, int k, uint32_t n) {
-                const uint32_t from = stage + kTri + (which * kChunk + n * 16 + b_row) * kTriStride + k * 32 + b_col;
-                load_matrices(b[0], from);
-                load_matrices(b[1], from + kChunk * kTriStride);
-            };
-            auto times = [&](float (&y)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], const uint32_t (&b)[2][4], int i, int term) {
-                mma(y, term == 2 ? low : high, b[term == 1][2 * i], b[term == 1][2 * i + 1]);
-            };
             uint32_t high[2][4], low[2][4];
             float u[4][4] = {};
             float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
             halves(w, p0, p1, high, low);
-            uint32_t t00[2][4], t01[2][4], t11[2][4];
-            triangle(t00, 0, 0, 0);
-            triangle(t01, 0, 0, 1);
-            triangle(t11, 0, 1, 1);
-#pragma unroll
-            for (int term = 0; term < 3; ++term)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    times(u[i], high[0], low[0], t00, i, term);
-                    times(u[2 + i], high[0], low[0], t01, i, term);
-                }
-#pragma unroll
-            for (int term = 0; term < 3; ++term)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) times(u[2 + i], high[1], low[1], t11, i, term);
+            times_triangle(u, high, low, stage + kTri + b_row * kTriStride + b_col);
             const float of_t = numbers[kOfT], f0 = of_t * inverse_power(p0), f1 = of_t * inverse_power(p1);
             m0 = m1 = 0.f;
             float n0 = 0.f, n1 = 0.f;
@@ -733,24 +843,39 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
                 n0 = fmaxf(n0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
                 n1 = fmaxf(n1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
             }
-            // P U for this warp's 16 tokens
-            p0 = power_for(quad_max(m0));
-            p1 = power_for(quad_max(m1));
-            halves(u, p0, p1, high, low);
-            float o[2][4] = {};
-            triangle(t00, 2, 0, half);
-            triangle(t11, 2, 1, 1);
+            float o[2][4] = {}, g0 = 0.f, g1 = 0.f;
+            if constexpr (kResults) {       // handed over
+                if (j >= 2) good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&taken[pair][j % 2]), (j / 2 - 1) & 1, p.error, p.wait_limit)));
+                float4 *to = reinterpret_cast<float4 *>(smem + kHandedAt + (pair * 2 + j % 2) * kHandedBytes) + half * 64 + lane;
 #pragma unroll
-            for (int term = 0; term < 3; ++term)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) times(o[i], high[0], low[0], t00, i, term);
-            if (half) {
+                for (int n = 0; n < 2; ++n) {
+                    to[n * 32] = half ? make_float4(u[2 + n][0], u[2 + n][1], u[2 + n][2], u[2 + n][3]) : make_float4(u[n][0], u[n][1], u[n][2], u[n][3]);
+                    to[(4 + n) * 32] = make_float4(qs[n][0], qs[n][1], qs[n][2], qs[n][3]);
+                }
+                __syncwarp();
+                if (lane == 0 && good) mbar_arrive(smem_u32(&handed[pair][j % 2]));      // else there are no results
+            } else {        // P U for this warp's 16 tokens
+                p0 = power_for(quad_max(m0));
+                p1 = power_for(quad_max(m1));
+                halves(u, p0, p1, high, low);
+                uint32_t t0[2][4], t1[2][4];
+                const uint32_t from = stage + kTri + (2 * kChunk + b_row) * kTriStride + b_col;
+                load_terms(t0, from + half * 16 * kTriStride);
+                load_terms(t1, from + 16 * kTriStride + 32);
 #pragma unroll
                 for (int term = 0; term < 3; ++term)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) times(o[i], high[1], low[1], t11, i, term);
+                    for (int i = 0; i < 2; ++i) times(o[i], high[0], low[0], t0, i, term);
+                if (half) {
+#pragma unroll
+                    for (int term = 0; term < 3; ++term)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) times(o[i], high[1], low[1], t1, i, term);
+                }
+                const float of_p = numbers[kOfP];
+                g0 = of_p * inverse_power(p0);
+                g1 = of_p * inverse_power(p1);
             }
-            const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
             // S^T = e^G_last S^T + (e^(G_last - G) U)^T K; the products begin at zero and are added rounded to nearest
             p0 = power_for(quad_max(n0));
             p1 = power_for(quad_max(n1));
@@ -791,34 +916,13 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
                 slot = 0;
                 parity ^= 1;
             }
-            // out, through shared memory: 16 columns of this warp's 16 tokens
-            if (good) {
+            if (!kResults && good) {
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
+                for (int n = 0; n < 2; ++n)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) o[n][e] = (e % 2 ? of_q[n].y : of_q[n].x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0);
-                }
-                if (a.out_dtype == NINFER_F32) {
-                    uint8_t *to = smem + out_at + lane % 4 * 160 + lane / 4 * 4;
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(to + (i / 4 * 8 + i % 2) * 80 + i / 2 % 2 * 32) = o[i / 4][i % 4];
-                } else {
-                    uint32_t r[4];          // pairs of tokens, turned as they are stored
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
-                        const __half2 h = __floats2half2_rn(o[i / 2][i % 2 * 2], o[i / 2][i % 2 * 2 + 1]);
-                        r[i] = a.out_dtype == NINFER_BF16 ? *reinterpret_cast<const uint32_t *>(&b) : *reinterpret_cast<const uint32_t *>(&h);
-                    }
-                    store_matrices_turned(base + out_at + b_row * 80 + b_col, r);
-                }
-                __syncwarp();
-                const uint8_t *from = smem + out_at + out_row * 80 + lane % out_es * 16;
-                if (out_on && (int32_t)(half * 16 + out_row) < count) *reinterpret_cast<uint4 *>(to_out) = *reinterpret_cast<const uint4 *>(from);
-                if (out_es == 4 && out_on && (int32_t)(half * 16 + out_row + 8) < count)
-                    *reinterpret_cast<uint4 *>(to_out + 8 * out_step) = *reinterpret_cast<const uint4 *>(from + 8 * 80);
+                put_results(results, a.out_dtype, smem, out_at, to_out, o, count - (int32_t)half * 16, lane);
                 to_out += kChunk * out_step;
-                __syncwarp();
             }
         }
     }
@@ -835,9 +939,12 @@ __global__ void __launch_bounds__(chunk_threads(kSteps)) chunk_kernel(const __gr
         }
 }
 
-template <int kTerms>
+template <int kTerms, bool kResults>
 auto chunk_kernel_of(uint32_t wide) {
-    return wide == 64 ? chunk_kernel<2, kTerms> : wide == 96 ? chunk_kernel<3, kTerms> : wide == 128 ? chunk_kernel<4, kTerms> : chunk_kernel<8, kTerms>;
+    return wide == 64   ? chunk_kernel<2, kTerms, kResults>
+           : wide == 96 ? chunk_kernel<3, kTerms, kResults>
+           : wide == 128 ? chunk_kernel<4, kTerms, kResults>
+                         : chunk_kernel<8, kTerms, kResults>;
 }
 
 // k_dim rounded up to what the kernel has instances for
@@ -962,10 +1069,11 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     if (st) return st;
     c.wait_limit = wait_limit_cycles();
     const uint32_t prepare_smem = std::max((uint32_t)c.rows_bytes, kTriSmem);
-    const uint32_t chunk_smem = stages_of(c.wide, terms) * ((uint32_t)c.rows_bytes + kHeadBytes + kChunk * (kColumns * (uint32_t)dtype_size(a.dtype) + 16)) +
-                                8 * (kChunk / 2 * 80 + sums_of(c.wide, terms) * 6 * 32 * 16);
+    const bool results = slab < kColumns;
+    const uint32_t chunk_smem = chunk_smem_of(c.wide, terms, results);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
-    const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide) : chunk_kernel_of<1>(c.wide);
+    const auto chunk = terms == 2 ? (results ? chunk_kernel_of<2, true>(c.wide) : chunk_kernel_of<2, false>(c.wide))
+                                  : (results ? chunk_kernel_of<1, true>(c.wide) : chunk_kernel_of<1, false>(c.wide));
     st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
     if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(chunk), (int)chunk_smem);
     if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kPrepareThreads), prepare_smem, s, c);

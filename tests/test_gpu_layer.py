@@ -221,6 +221,25 @@ def test_gated_delta_ragged(k_heads, v_heads, dk, dv, dtype, out):
     run_delta(case, out, offsets=offsets, slots=[3, 5, 9, -1, 0, 2, 1], lengths=[5, 0, 0, 7, 1, 0, 9])
 
 
+@pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
+@pytest.mark.parametrize("dk", [64, 96, 128, 256])
+def test_gated_delta_ragged_many_heads(dk, dtype, out):
+    """More states than SMs: 64 columns a CTA, the last of them with eight."""
+    rng = np.random.default_rng(dk)
+    counts = [70, 1, 0, 33, 128, 6]
+    offsets = np.concatenate([[0], np.cumsum(counts)])
+    case = delta_case(rng, offsets[-1], 6, 4, 28, dk, 72, dtype, 7)
+    run_delta(case, out, offsets=offsets, slots=[6, 3, 1, 0, 2, 5], lengths=[0, 3, 1, 0, 5, 0])
+
+
+@pytest.mark.parametrize("dv", [8, 16, 40, 48, 104, 152, 248])
+@pytest.mark.parametrize("dk,dtype", [(128, "bf16"), (128, "f32"), (96, "bf16"), (256, "f16"), (256, "f32")])
+def test_gated_delta_columns_of_a_prompt(dk, dv, dtype):
+    """48 columns a CTA, and what is left of them for the last: one to three pairs of warps."""
+    rng = np.random.default_rng(dk + dv)
+    run_delta(delta_case(rng, 230, 1, 1, 2, dk, dv, dtype), "f32" if dv % 16 else dtype, offsets=[0, 227])
+
+
 def test_gated_delta_offsets_of_any_value():
     rng = np.random.default_rng(7)
     for offsets in ([-5, 3, 3, 9, 40], [0, 2 ** 31 - 1, 7, 7, -2 ** 31], [30, 30, 0, 5, 5], [9, 12, 4, 4, 9]):
