@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 //   O = scale (diag(e^G) Q S + P U),          P_ts = e^(G_t - G_s) q_t . k_s for s <= t, else 0
 //   S <- e^(G_last) S + K^T diag(e^(G_last - G)) U
 // T diag(beta) and P need no state: prepare_kernel makes them for all chunks at once, chunk_kernel goes through them.
-constexpr int kChunk = 32, kPrepareThreads = 128, kColumns = 64;      // columns of a state a CTA
+constexpr int kChunk = 32, kPrepareThreads = 128;
 constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
 enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
 constexpr uint32_t kTriStride = kChunk * 2 + 16, kTrianglesBytes = 4 * kChunk * kTriStride;     // T high and low, P high and low
@@ -460,32 +460,38 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
     }
 }
 
-// A ninth warp copies where it leaves the others registers enough: 168 a thread instead of 255.
-__host__ __device__ constexpr int chunk_threads(int steps) { return steps < 4 ? 288 : 256; }
-
-// Chunks in shared memory at once, and buffers for the sums: what fits an SM.
-__host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 2 : 3; }
-__host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms) { return wide * terms >= 512 ? 1 : 2; }
-
-// With 48 columns a CTA (3 pairs) the two warps without any take from the pairs' chain what is not of it: the results (P U and Q S), made
-// by one of them (the other copies) or, with a ninth warp, by both; 8001 tokens with 48 heads 603 us, by the pairs themselves 681. What a
-// pair hands over: U and Q S of 16 columns by 32 tokens, two buffers.
+// Columns of a state a CTA: 48 where few heads leave no more than a CTA for every SM, else 32, two CTAs an SM of which one begins or ends
+// while the other computes (64 prompts of 33 tokens with 48 heads 320 us, of 128 tokens 558; with 64 columns 349 and 582), or 64 where
+// shared memory has no room for two.
+// With 48 (3 pairs of warps) the two warps without columns take from the pairs' chain what is not of it: the results (P U and Q S), made
+// by one of them (the other copies) or, with a ninth warp that copies, by both; 8001 tokens with 48 heads 603 us, by the pairs themselves 681.
+// What a pair hands over: U and Q S of 16 columns by 32 tokens, two buffers.
 constexpr uint32_t kResultWarp = 6, kHandedBytes = 8 * 32 * 16;
-__host__ __device__ constexpr uint32_t pairs_of(bool results) { return results ? 3 : 4; }
+// The ninth warp is there where it leaves the others registers enough: 168 a thread instead of 255.
+__host__ __device__ constexpr int chunk_threads(int steps, int columns) { return columns == 32 ? 128 : columns == 48 && steps < 4 ? 288 : 256; }
 
-// Shared memory: the stages, the results' turning (16 tokens by 16 columns a warp), the pairs' sums, what is handed over.
-__host__ __device__ constexpr uint32_t stage_bytes_of(uint32_t wide, int terms) {
-    return terms * 2 * kChunk * (wide * 2 + 16) + kHeadBytes + kChunk * (kColumns * (terms == 2 ? 4 : 2) + 16);
+// Shared memory: the stages (chunks at once), the results' turning (16 tokens by 16 columns a warp), the pairs' sums (one buffer or two),
+// what is handed over.
+__host__ __device__ constexpr uint32_t values_of(int columns) { return columns == 32 ? 32 : 64; }      // columns of V that are copied
+__host__ __device__ constexpr uint32_t stage_bytes_of(uint32_t wide, int terms, int columns) {
+    return terms * 2 * kChunk * (wide * 2 + 16) + kHeadBytes + kChunk * (values_of(columns) * (terms == 2 ? 4 : 2) + 16);
 }
-__host__ __device__ constexpr uint32_t sums_at_of(uint32_t wide, int terms, bool results) {
-    return stages_of(wide, terms) * stage_bytes_of(wide, terms) + (results ? 2 : 8) * (kChunk / 2 * 80);
+__host__ __device__ constexpr uint32_t turning_of(int columns) { return (columns == 48 ? 2 : columns / 8) * (kChunk / 2 * 80); }
+__host__ __device__ constexpr uint32_t sums_bytes_of(int columns) { return columns / 8 * 6 * 32 * 16; }
+__host__ __device__ constexpr uint32_t smem_of(uint32_t wide, int terms, int columns, uint32_t stages, uint32_t sums) {
+    return stages * stage_bytes_of(wide, terms, columns) + turning_of(columns) + sums * sums_bytes_of(columns) + (columns == 48 ? 6 * kHandedBytes : 0);
 }
-__host__ __device__ constexpr uint32_t handed_at_of(uint32_t wide, int terms, bool results) {
-    return sums_at_of(wide, terms, results) + sums_of(wide, terms) * pairs_of(results) * 2 * 6 * 32 * 16;
+__host__ __device__ constexpr uint32_t room_of(int columns) { return columns == 32 ? 113 * 1024 - 256 : 227 * 1024 - 256; }
+__host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms, int columns) { return smem_of(wide, terms, columns, 2, 2) <= room_of(columns) ? 2 : 1; }
+__host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms, int columns) {
+    return smem_of(wide, terms, columns, 3, sums_of(wide, terms, columns)) <= room_of(columns) ? 3 : 2;
 }
-__host__ __device__ constexpr uint32_t chunk_smem_of(uint32_t wide, int terms, bool results) {
-    return handed_at_of(wide, terms, results) + (results ? pairs_of(results) * 2 * kHandedBytes : 0);
+__host__ __device__ constexpr uint32_t chunk_smem_of(uint32_t wide, int terms, int columns) {
+    return smem_of(wide, terms, columns, stages_of(wide, terms, columns), sums_of(wide, terms, columns));
 }
+
+// Columns where there are more states than SMs.
+__host__ __device__ constexpr int many_columns(uint32_t wide, int terms) { return smem_of(wide, terms, 32, 2, 1) <= room_of(32) ? 32 : 64; }
 
 // 16 columns by 32 tokens as the A operand, each column times its power of two.
 __device__ __forceinline__ void halves(const float (&y)[4][4], float p0, float p1, uint32_t (&high)[2][4], uint32_t (&low)[2][4]) {
@@ -551,22 +557,23 @@ __device__ __forceinline__ void put_results(const Results &r, int dtype, uint8_t
     __syncwarp();
 }
 
-// 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
+// 32 to 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
 // products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
 // as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
 // outputs by tokens where no other warp makes them. One warp keeps the next chunks coming (bulk copies, mbarriers); nothing else holds pairs together, so
 // that of two pairs on a scheduler one multiplies while the other splits and scales.
-// kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q; kResults: 48 columns. One CTA an SM is said where ptxas otherwise
+// kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q. The CTAs an SM are said to ptxas, which otherwise
 // takes fewer registers and loads later (173 for 207: 662 us for 603).
-template <int kSteps, int kTerms, bool kResults>
-__global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4 ? 1 : 0) chunk_kernel(const __grid_constant__ ChunkParams p) {
+template <int kSteps, int kTerms, int kColumns>
+__global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 32 ? 2 : 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride;
-    constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms), kTri = kTerms * kTermBytes, kNumbersAt = kTri + kTrianglesBytes, kV = kTri + kHeadBytes;
-    constexpr uint32_t kSums = sums_of(kSteps * 32, kTerms), es = kTerms == 2 ? 4 : 2, v_stride = kColumns * es + 16, stage_bytes = kV + kChunk * v_stride;
-    static_assert(stage_bytes == stage_bytes_of(kSteps * 32, kTerms));
+    constexpr bool kResults = kColumns == 48, kNinth = chunk_threads(kSteps, kColumns) > 256;       // a warp that copies
+    constexpr uint32_t kStages = stages_of(kSteps * 32, kTerms, kColumns), kTri = kTerms * kTermBytes, kNumbersAt = kTri + kTrianglesBytes, kV = kTri + kHeadBytes;
+    constexpr uint32_t kSums = sums_of(kSteps * 32, kTerms, kColumns), es = kTerms == 2 ? 4 : 2, v_stride = values_of(kColumns) * es + 16, stage_bytes = kV + kChunk * v_stride;
+    static_assert(stage_bytes == stage_bytes_of(kSteps * 32, kTerms, kColumns));
+    static_assert(chunk_smem_of(kSteps * 32, kTerms, kColumns) <= room_of(kColumns));
     extern __shared__ __align__(16) uint8_t smem[];
-    constexpr bool kNinth = chunk_threads(kSteps) > 256;       // a warp that copies
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], handed[3][2], taken[3][2];
     pdl_launch_dependents();
     pdl_wait();
@@ -591,7 +598,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4
     __syncthreads();
     const uint32_t pair = warp / 2, half = warp % 2;
     const bool bf16 = a.dtype == NINFER_BF16;
-    constexpr uint32_t kSumsAt = sums_at_of(kSteps * 32, kTerms, kResults), kHandedAt = handed_at_of(kSteps * 32, kTerms, kResults);
+    constexpr uint32_t kSumsAt = kStages * stage_bytes + turning_of(kColumns), kHandedAt = kSumsAt + kSums * sums_bytes_of(kColumns);
     const uint32_t out_at = kStages * stage_bytes + (kResults ? warp % 2 : warp) * (kChunk / 2 * 80);
     const uint32_t mine = part.column + pair * 16, column = mine + lane / 4;         // this thread's: column, column + 8
     const uint32_t b_row = lane % 8 + lane / 16 * 8, b_col = lane / 8 % 2 * 16;          // of the four matrices that a lane addresses
@@ -600,7 +607,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4
     bool good = true;       // once a wait has run out, none is made and nothing is stored
     // The copying warp's: chunk j into its stage, which all warps have left. Lanes whose 16 bytes of values lie past the last column copy
     // the last ones there are; what they get is part of no result.
-    constexpr uint32_t kUnits = kColumns * es / 16;
+    constexpr uint32_t kUnits = values_of(kColumns) * es / 16;
     constexpr int32_t kRowsAtOnce = 32 / kUnits;
     const uint8_t *next_rows = p.rows + ((uint64_t)range.chunk * a.k_heads + part.key_head) * p.rows_bytes;
     const uint8_t *next_head = p.heads + ((uint64_t)range.chunk * a.v_heads + part.head) * kHeadBytes;
@@ -766,8 +773,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4
             }
             // the pair's halves: all of K S to both, of Q S the first 16 tokens to the first. Two buffers: who writes one again has
             // passed the barrier between, and with it the other's reads.
-            float4 *sums = reinterpret_cast<float4 *>(smem + kSumsAt) + (j % kSums * (2 * pairs_of(kResults)) + warp) * 6 * 32 + lane;
-            const float4 *others = reinterpret_cast<const float4 *>(smem + kSumsAt) + (j % kSums * (2 * pairs_of(kResults)) + (warp ^ 1)) * 6 * 32 + lane;
+            float4 *sums = reinterpret_cast<float4 *>(smem + kSumsAt) + (j % kSums * (kColumns / 8) + warp) * 6 * 32 + lane;
+            const float4 *others = reinterpret_cast<const float4 *>(smem + kSumsAt) + (j % kSums * (kColumns / 8) + (warp ^ 1)) * 6 * 32 + lane;
 #pragma unroll
             for (int n = 0; n < 4; ++n) sums[n * 32] = make_float4(x[n][0], x[n][1], x[n][2], x[n][3]);
 #pragma unroll
@@ -939,12 +946,18 @@ __global__ void __launch_bounds__(chunk_threads(kSteps), kResults || kSteps == 4
         }
 }
 
-template <int kTerms, bool kResults>
-auto chunk_kernel_of(uint32_t wide) {
-    return wide == 64   ? chunk_kernel<2, kTerms, kResults>
-           : wide == 96 ? chunk_kernel<3, kTerms, kResults>
-           : wide == 128 ? chunk_kernel<4, kTerms, kResults>
-                         : chunk_kernel<8, kTerms, kResults>;
+using ChunkKernel = void (*)(ChunkParams);
+template <int kSteps, int kTerms>
+ChunkKernel chunk_kernel_at(int columns) {
+    if (columns == 48) return chunk_kernel<kSteps, kTerms, 48>;
+    return chunk_kernel<kSteps, kTerms, many_columns(kSteps * 32, kTerms)>;
+}
+template <int kTerms>
+ChunkKernel chunk_kernel_of(uint32_t wide, int columns) {
+    return wide == 64    ? chunk_kernel_at<2, kTerms>(columns)
+           : wide == 96  ? chunk_kernel_at<3, kTerms>(columns)
+           : wide == 128 ? chunk_kernel_at<4, kTerms>(columns)
+                         : chunk_kernel_at<8, kTerms>(columns);
 }
 
 // k_dim rounded up to what the kernel has instances for
@@ -1050,18 +1063,17 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
                                           : (small ? step_kernel<32, 8> : step_kernel<32, 16>);
         return launch_dependent("gated delta", kernel, dim3(blocks), dim3(kStepThreads), 0, s, p);
     }
-    // 64 columns a CTA, or 48 where that gives work to more of the SMs without a second round
     DeviceInfo d;
     st = device_info(&d);
     if (st) return st;
-    const uint64_t slab = rows * ((a.v_dim + 47) / 48) <= (uint64_t)d.sms ? 48 : kColumns;
-    grid(slab, &blocks);
     const int terms = a.dtype == NINFER_F32 ? 2 : 1;
+    const int columns = rows * ((a.v_dim + 47) / 48) <= (uint64_t)d.sms ? 48 : many_columns(wide_of(a.k_dim), terms);
+    grid((uint64_t)columns, &blocks);
     const uint64_t chunks = a.tokens / kChunk + a.requests;
     ChunkParams c;
     c.d = p;
     c.wide = wide_of(a.k_dim);
-    c.slab = (uint32_t)slab;
+    c.slab = (uint32_t)columns;
     c.rows_bytes = rows_bytes_of(terms, a.k_dim);
     c.rows = static_cast<uint8_t *>(workspace);
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
@@ -1069,14 +1081,12 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     if (st) return st;
     c.wait_limit = wait_limit_cycles();
     const uint32_t prepare_smem = std::max((uint32_t)c.rows_bytes, kTriSmem);
-    const bool results = slab < kColumns;
-    const uint32_t chunk_smem = chunk_smem_of(c.wide, terms, results);
+    const uint32_t chunk_smem = chunk_smem_of(c.wide, terms, columns);
     const auto prepare = terms == 2 ? prepare_kernel<2> : prepare_kernel<1>;
-    const auto chunk = terms == 2 ? (results ? chunk_kernel_of<2, true>(c.wide) : chunk_kernel_of<2, false>(c.wide))
-                                  : (results ? chunk_kernel_of<1, true>(c.wide) : chunk_kernel_of<1, false>(c.wide));
+    const auto chunk = terms == 2 ? chunk_kernel_of<2>(c.wide, columns) : chunk_kernel_of<1>(c.wide, columns);
     st = set_smem_attribute(reinterpret_cast<const void *>(prepare), (int)prepare_smem);
     if (!st) st = set_smem_attribute(reinterpret_cast<const void *>(chunk), (int)chunk_smem);
     if (!st) st = launch_dependent("gated delta", prepare, dim3((unsigned)(chunks * a.k_heads)), dim3(kPrepareThreads), prepare_smem, s, c);
-    if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3(chunk_threads((int)c.wide / 32)), chunk_smem, s, c);
+    if (!st) st = launch_dependent("gated delta", chunk, dim3(blocks), dim3((unsigned)chunk_threads((int)c.wide / 32, columns)), chunk_smem, s, c);
     return st;
 }

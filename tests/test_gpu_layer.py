@@ -224,7 +224,7 @@ def test_gated_delta_ragged(k_heads, v_heads, dk, dv, dtype, out):
 @pytest.mark.parametrize("dtype,out", [("f32", "f32"), ("bf16", "bf16"), ("f16", "f32")])
 @pytest.mark.parametrize("dk", [64, 96, 128, 256])
 def test_gated_delta_ragged_many_heads(dk, dtype, out):
-    """More states than SMs: 64 columns a CTA, the last of them with eight."""
+    """More states than SMs: 32 or 64 columns a CTA, the last of them with eight."""
     rng = np.random.default_rng(dk)
     counts = [70, 1, 0, 33, 128, 6]
     offsets = np.concatenate([[0], np.cumsum(counts)])
