@@ -460,10 +460,11 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
     }
 }
 
-// Columns of a state a CTA: 48 where few heads leave no more than a CTA for every SM, else 32, two CTAs an SM of which one begins or ends
+// Columns of a state a CTA: where that makes no more CTAs than SMs 16, 32 or up to 48 (8001 tokens with 16 heads of 128 columns by 16, 32 and
+// 48: 412, 468 and 576 us; 48 heads by 48 and by 32 columns, two CTAs an SM: 603 and 701), else 32, two CTAs an SM of which one begins or ends
 // while the other computes (64 prompts of 33 tokens with 48 heads 320 us, of 128 tokens 558; with 64 columns 349 and 582), or 64 where
 // shared memory has no room for two.
-// With 48 (3 pairs of warps) the two warps without columns take from the pairs' chain what is not of it: the results (P U and Q S), made
+// With up to 48 (3 pairs of warps) the two warps without columns take from the pairs' chain what is not of it: the results (P U and Q S), made
 // by one of them (the other copies) or, with a ninth warp that copies, by both; 8001 tokens with 48 heads 603 us, by the pairs themselves 681.
 // What a pair hands over: U and Q S of 16 columns by 32 tokens, two buffers.
 constexpr uint32_t kResultWarp = 6, kHandedBytes = 8 * 32 * 16;
@@ -1067,13 +1068,17 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     st = device_info(&d);
     if (st) return st;
     const int terms = a.dtype == NINFER_F32 ? 2 : 1;
-    const int columns = rows * ((a.v_dim + 47) / 48) <= (uint64_t)d.sms ? 48 : many_columns(wide_of(a.k_dim), terms);
-    grid((uint64_t)columns, &blocks);
+    int columns = many_columns(wide_of(a.k_dim), terms), slab = columns;
+    for (int most = 48; most >= 16 && rows * ((a.v_dim + most - 1) / most) <= (uint64_t)d.sms; most -= 16) {
+        columns = 48;
+        slab = most;
+    }
+    grid((uint64_t)slab, &blocks);
     const uint64_t chunks = a.tokens / kChunk + a.requests;
     ChunkParams c;
     c.d = p;
     c.wide = wide_of(a.k_dim);
-    c.slab = (uint32_t)columns;
+    c.slab = (uint32_t)slab;
     c.rows_bytes = rows_bytes_of(terms, a.k_dim);
     c.rows = static_cast<uint8_t *>(workspace);
     c.heads = c.rows + chunks * a.k_heads * c.rows_bytes;
