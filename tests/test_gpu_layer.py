@@ -235,9 +235,17 @@ def test_gated_delta_ragged_many_heads(dk, dtype, out):
 @pytest.mark.parametrize("dv", [8, 16, 40, 48, 104, 152, 248])
 @pytest.mark.parametrize("dk,dtype", [(128, "bf16"), (128, "f32"), (96, "bf16"), (256, "f16"), (256, "f32")])
 def test_gated_delta_columns_of_a_prompt(dk, dv, dtype):
-    """48 columns a CTA, and what is left of them for the last: one to three pairs of warps."""
+    """16 columns a CTA, and what is left of them for the last."""
     rng = np.random.default_rng(dk + dv)
     run_delta(delta_case(rng, 230, 1, 1, 2, dk, dv, dtype), "f32" if dv % 16 else dtype, offsets=[0, 227])
+
+
+@pytest.mark.parametrize("v_heads,dv", [(36, 128), (36, 104), (48, 128), (48, 104), (48, 72), (152, 48), (152, 24), (150, 40)])
+@pytest.mark.parametrize("dk,dtype", [(128, "bf16"), (128, "f32"), (64, "f16"), (96, "f32"), (256, "bf16"), (256, "f32")])
+def test_gated_delta_columns_of_many_heads(dk, v_heads, dv, dtype):
+    """32 and 48 columns a CTA where those fill the SMs, one to three pairs of warps in the last."""
+    rng = np.random.default_rng(dk + dv + v_heads)
+    run_delta(delta_case(rng, 140, 1, 2, v_heads, dk, dv, dtype), dtype, offsets=[0, 139])
 
 
 def test_gated_delta_offsets_of_any_value():
