@@ -612,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
         s.listed = s.taken = 0;
     }
     __syncthreads();
+    cluster_arrive();
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_sample_args &a = p.a;
@@ -661,6 +662,8 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
             for (int j = 0; j < 4; ++j) larger(v[j], i + j);
         });
     uint32_t lowest = most == -INFINITY ? ~0u : key_of(most);       // of the threads' largest, which top-k looks at
+    __syncwarp();
+    cluster_wait();         // every CTA of the row has begun: what follows is stored into the others' shared memory
     const uint64_t best = row.cluster_max((uint64_t)key_of(most) << 32 | (uint32_t)~place, lowest);
     const float top = logit_of((uint32_t)(best >> 32));
     const bool lead = tid == 0 && row.rank == 0, none = top == -INFINITY;
