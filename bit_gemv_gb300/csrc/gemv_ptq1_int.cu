@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_ptq1_int_kernel(const __grid
     const uint32_t ring_to = min(p.nslots, c.nbatch);
     const uint32_t pre = min(p.pre_issue, ring_to);
 
-    if (csize == 2) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    if (csize > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     if (tid == 0) {
         for (uint32_t s = 0; s < p.nslots; ++s) {
             mbar_init(bar0 + 8 * s, 1);

@@ -10,7 +10,8 @@ CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))),
 ARRIVE = re.compile(r"cluster_arrive\(\)|barrier\.cluster\.arrive(?:\.relaxed|\.release)?\.aligned;\" |cluster_sync\(\)|join\(\)")
 WAIT = re.compile(r"cluster_wait\(\)|barrier\.cluster\.wait(?:\.acquire)?\.aligned;\" |cluster_sync\(\)|join\(\)")
 # file, kernel, its calls that reach another CTA's shared memory
-KERNELS = [("sample.cu", "sample_kernel", r"row\.(?:cluster_max|exchange|merge|template merge|list|adopt|locate)")]
+KERNELS = [("sample.cu", "sample_kernel", r"row\.(?:cluster_max|exchange|merge|template merge|list|adopt|locate)"),
+           ("gemv_ptq1_int.cu", "gemv_ptq1_int_kernel", r"mapa_shared|st_cluster")]
 
 
 def body(name, kernel):
@@ -24,15 +25,22 @@ def body(name, kernel):
     return text[at:end]
 
 
+def condition(text, at):
+    """The condition of the statement at a place: on its line, or that of the block that it begins."""
+    return re.findall(r"if \(([^{}]*?)\)\s*(?:\{[^{}]*)?$", text[max(at - 200, 0):at].replace("asm volatile(\"", "").rstrip())
+
+
 @pytest.mark.parametrize("name,kernel,remote", KERNELS)
 def test_no_access_before_every_cta_has_begun(name, kernel, remote):
     text = body(name, kernel)
     arrive, wait, first = ARRIVE.search(text), WAIT.search(text), re.search(remote, text)
     assert arrive and wait and first
     assert arrive.start() <= wait.start() < first.start()
+    # a wait without an arrival before it, or the reverse, has no meaning
+    assert condition(text, arrive.start()) == condition(text, wait.start())
 
 
 def test_every_file_with_such_accesses_is_listed():
     found = {f for f in os.listdir(CSRC) if f.endswith((".cu", ".cuh")) and f != "async.cuh" and "mapa_shared(" in open(os.path.join(CSRC, f)).read()}
     # attention's kernel joins through cluster_sync alone
-    assert found == {n for n, _, _ in KERNELS} | {"kv_attention.cuh", "gemv_pq2_int.cu", "gemv_ptq1_int.cu"}
+    assert found == {n for n, _, _ in KERNELS} | {"kv_attention.cuh", "gemv_pq2_int.cu"}
