@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_pq2_int_kernel(const __grid_
     // (two CTAs sharing the rotations), where requesting it at once measured faster
     const bool ring_after_x = csize == 1;
 
+    if (csize == 2) cluster_arrive();
     if (tid == producer * 32) {
         prefetch_tmap(last_cta ? &p.wmap_last : &p.wmap_main);
         prefetch_tmap(last_cta ? &p.smap_last : &p.smap_main);
@@ -223,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_pq2_int_kernel(const __grid_
         // queue the rest of the ring behind it
         *reinterpret_cast<volatile float *>(scr + 1080 + (t >> 5)) = v[0] + v[15];
         if (ring_after_x) named_barrier_arrive(kBarX, nwait);
+        __syncwarp();
+        if (csize == 2) cluster_wait();      // the other CTA has begun: its table is written too
         rotate_pack2(p.signs != nullptr, v, d, b, p.groups, act_s + (task / p.nblk) * p.act_bytes,
                      act_remote0 ? act_remote0 + (task / p.nblk) * p.act_bytes : 0u, scr, t, kBarPair0 + pr);
     } else {
@@ -238,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) gemv_pq2_int_kernel(const __grid_
             }
             __syncwarp();
         }
+        if (csize == 2) cluster_wait();
     }
     // more rotations than rotating pairs: further rounds
 #pragma unroll 1
