@@ -748,9 +748,8 @@ def ninfer_gated_delta(q, k, v, log_decay, beta, state, offsets=None, slots=None
     if out is None:
         out = _torch().empty(v_shape, dtype=out_dtype or v.dtype, device=v.device)
     w_at = w_bytes = 0
-    need = ninfer_gated_delta_workspace(tokens, requests, k_heads, v_heads, k_dim, v_dim) if workspace is None else 0
-    if need:
-        workspace = _torch().empty(need, dtype=_torch().uint8, device=q.device)
+    if workspace is None and offsets is not None:       # single tokens need none
+        workspace = _torch().empty(ninfer_gated_delta_workspace(tokens, requests, k_heads, v_heads, k_dim, v_dim), dtype=_torch().uint8, device=q.device)
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous tensor on cuda:{device}")

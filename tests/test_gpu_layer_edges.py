@@ -31,3 +31,18 @@ def test_sample_ctas_of_a_row_that_begin_late(rows, vocab, dtype):
             first = tokens
             assert torch.equal(x.float()[::3].gather(1, tokens[::3, None].long())[:, 0], largest)
         assert torch.equal(tokens, first)
+
+
+# ------------------------------------------------------------ gated delta ---
+def test_gated_delta_single_tokens_take_no_workspace():
+    """Without offsets nothing is allocated beside the result, and a size that no workspace could have is no matter."""
+    case = delta_case(np.random.default_rng(1), 40, 40, 2, 6, 64, 64, "bf16")
+    out = nt.ninfer_gated_delta(**case)
+    count = lambda: torch.cuda.memory_stats()["allocation.all.allocated"]  # noqa: E731
+    before = count()
+    nt.ninfer_gated_delta(**case, out=out)
+    assert count() == before
+    nt.ninfer_gated_delta(**case)
+    assert count() == before + 1
+    nt.ninfer_gated_delta(**case, offsets=i32([0, 40]), out=out)
+    assert count() >= before + 2        # a prompt's, and the offsets
