@@ -171,9 +171,11 @@ __global__ void __launch_bounds__(kStepThreads) step_kernel(const __grid_constan
 //   O = scale (diag(e^G) Q S + P U),          P_ts = e^(G_t - G_s) q_t . k_s for s <= t, else 0
 //   S <- e^(G_last) S + K^T diag(e^(G_last - G)) U
 // T diag(beta) and P need no state: prepare_kernel makes them for all chunks at once, chunk_kernel goes through them.
+// Every row of K and Q is a row of binary16 times its own scale. T's rows take their keys' scales, so that U comes out as what it adds to the
+// state, of one size with it, and P is made of the rows without their scales: a small key or query beside large ones keeps its bits.
 constexpr int kChunk = 32, kPrepareThreads = 128;
-constexpr int kNumbers = 128;                                       // floats of a chunk and head: below
-enum { kOfK = 0, kOfQ = 32, kOfU = 64, kLeft = 96, kOfT, kOfP };     // e^G k's scale, scale e^G q's, e^(G_last - G) k's; e^G_last, T's, scale P's
+constexpr int kNumbers = 132;                                       // floats of a chunk and head: below
+enum { kOfK = 0, kOfQ = 32, kOfU = 64, kOfP = 96, kLeft = 128, kOfT };   // e^G k's scale, scale e^G q's, e^(G_last - G), scale q's and P's; e^G_last, T's
 constexpr uint32_t kTriStride = kChunk * 2 + 16, kTrianglesBytes = 4 * kChunk * kTriStride;     // T high and low, P high and low
 constexpr uint32_t kHeadBytes = kTrianglesBytes + kNumbers * 4;
 
@@ -393,7 +395,8 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const uint32_t t = warp % 2 * 16 + lane / 4 + e / 2 * 8, u = n * 8 + lane % 4 * 2 + e % 2;
-                dots[warp / 2][t][u] = (d[n][e] + odd[n][e] + (kTerms == 2 ? lower[kTerms == 2 ? n : 0][e] : 0.f)) * scales[warp / 2][t] * scales[0][u];
+                const float dot = d[n][e] + odd[n][e] + (kTerms == 2 ? lower[kTerms == 2 ? n : 0][e] : 0.f);
+                dots[warp / 2][t][u] = warp / 2 ? dot : dot * scales[0][t] * scales[0][u];       // of Q: without the scales
             }
     }
     __syncthreads();
@@ -448,15 +451,16 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
             tt[t] = (sum4[0] + sum4[1]) + (sum4[2] + sum4[3]);
         }
 #pragma unroll
-        for (int t = 0; t < kChunk; ++t) most_t = fmaxf(most_t, fabsf(tt[t] *= beta));
+        for (int t = 0; t < kChunk; ++t) most_t = fmaxf(most_t, fabsf(tt[t] *= beta * scales[0][t]));
         __syncwarp();
         const float of_t = put_matrix(to, tt, most_t, lane);
         float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
         const float fade = exp2f(high + low) * poison;
         numbers[kOfK + lane] = fade * scales[0][lane];
         numbers[kOfQ + lane] = a.scale * fade * scales[1][lane];
-        numbers[kOfU + lane] = exp2f((last_high - high) + (last_low - low)) * scales[0][lane];
-        if (lane < 3) numbers[kLeft + lane] = lane == 0 ? exp2f(last_high + last_low) * spoilt : lane == 1 ? of_t : a.scale * of_p;
+        numbers[kOfU + lane] = exp2f((last_high - high) + (last_low - low));
+        numbers[kOfP + lane] = a.scale * scales[1][lane] * of_p;
+        if (lane < 2) numbers[kLeft + lane] = lane == 0 ? exp2f(last_high + last_low) * spoilt : of_t;
     }
 }
 
@@ -686,7 +690,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                 uint32_t high[2][4], low[2][4];
                 halves(u, p0, p1, high, low);
                 times_triangle(o, high, low, stage + kTri + (2 * kChunk + b_row) * kTriStride + b_col);
-                const float of_p = numbers[kOfP], g0 = of_p * inverse_power(p0), g1 = of_p * inverse_power(p1);
+                const float g0 = inverse_power(p0), g1 = inverse_power(p1);
                 if (!good) continue;
                 results.on = part.column + g * 16 + out_col < v_dim;
 #pragma unroll
@@ -695,8 +699,10 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
                         const float2 of_q = *reinterpret_cast<const float2 *>(numbers + kOfQ + (h * 2 + n) * 8 + lane % 4 * 2);
+                        const float2 of_p = *reinterpret_cast<const float2 *>(numbers + kOfP + (h * 2 + n) * 8 + lane % 4 * 2);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) y[n][e] = (e % 2 ? of_q.y : of_q.x) * qs[2 * h + n][e] + o[2 * h + n][e] * (e / 2 ? g1 : g0);
+                        for (int e = 0; e < 4; ++e)
+                            y[n][e] = fmaf(e % 2 ? of_q.y : of_q.x, qs[2 * h + n][e], o[2 * h + n][e] * (e / 2 ? g1 : g0) * (e % 2 ? of_p.y : of_p.x));
                     }
                     put_results(results, a.out_dtype, smem, out_at, to_out + (uint64_t)h * 16 * out_step + g * 16 * out_es, y, count - h * 16, lane);
                 }
@@ -810,7 +816,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                         if (n * 8 + (int32_t)(lane % 4) * 2 + e % 2 >= count) w[n][e] = 0.f;
             }
             named_barrier(1 + pair, 64);
-            // W = V - e^G K S, then U = T diag(beta) W
+            // W = V - e^G K S, then U = T diag(beta) W, times the keys' scales
             float m0 = 0.f, m1 = 0.f, qs[2][4];
 #pragma unroll
             for (int n = 0; n < 4; ++n) {
@@ -880,9 +886,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                         for (int i = 0; i < 2; ++i) times(o[i], high[1], low[1], t1, i, term);
                 }
-                const float of_p = numbers[kOfP];
-                g0 = of_p * inverse_power(p0);
-                g1 = of_p * inverse_power(p1);
+                g0 = inverse_power(p0);
+                g1 = inverse_power(p1);
             }
             // S^T = e^G_last S^T + (e^(G_last - G) U)^T K; the products begin at zero and are added rounded to nearest
             p0 = power_for(quad_max(n0));
@@ -915,9 +920,12 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s[2 * n0_ + m][e] = fmaf(y[m][e], e / 2 ? d1 : d0, left * s[2 * n0_ + m][e]);
             }
-            float2 of_q[2];
+            float2 of_q[2], of_p[2];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) of_q[n] = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
+            for (int n = 0; n < 2; ++n) {
+                of_q[n] = *reinterpret_cast<const float2 *>(numbers + kOfQ + (half * 2 + n) * 8 + lane % 4 * 2);
+                of_p[n] = *reinterpret_cast<const float2 *>(numbers + kOfP + (half * 2 + n) * 8 + lane % 4 * 2);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&empty[slot]));
             if (++slot == kStages) {
@@ -928,7 +936,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                 for (int n = 0; n < 2; ++n)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) o[n][e] = (e % 2 ? of_q[n].y : of_q[n].x) * qs[n][e] + o[n][e] * (e / 2 ? g1 : g0);
+                    for (int e = 0; e < 4; ++e)
+                        o[n][e] = fmaf(e % 2 ? of_q[n].y : of_q[n].x, qs[n][e], o[n][e] * (e / 2 ? g1 : g0) * (e % 2 ? of_p[n].y : of_p[n].x));
                 put_results(results, a.out_dtype, smem, out_at, to_out, o, count - (int32_t)half * 16, lane);
                 to_out += kChunk * out_step;
             }

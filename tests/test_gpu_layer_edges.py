@@ -46,3 +46,41 @@ def test_gated_delta_single_tokens_take_no_workspace():
     assert count() == before + 1
     nt.ninfer_gated_delta(**case, offsets=i32([0, 40]), out=out)
     assert count() >= before + 2        # a prompt's, and the offsets
+
+
+# few states (results by warps of their own, with a ninth warp and without) and more than SMs (32 and 64 columns a CTA)
+INSTANCES = [(1, 2, 64, 48, "bf16"), (1, 2, 128, 40, "bf16"), (1, 2, 96, 32, "f32"), (2, 4, 256, 16, "f16"), (8, 160, 128, 24, "bf16"),
+             (4, 160, 96, 24, "f32"), (2, 160, 256, 16, "bf16"), (1, 160, 256, 8, "f32")]
+
+
+@pytest.mark.parametrize("k_heads,v_heads,dk,dv,dtype", INSTANCES)
+@pytest.mark.parametrize("widest", [0, 20, 40, 60])
+def test_gated_delta_prompts_of_unequal_sizes(k_heads, v_heads, dk, dv, dtype, widest):
+    """Without norms: queries, and keys with the betas that suit them, whose sizes differ by up to 2^widest among the tokens of a chunk. A
+    token's result is as exact as its own query and the state allow."""
+    if dtype == "f16" and widest > 20:
+        widest = 20             # its exponents
+    rng = np.random.default_rng(dk + widest)
+    case = delta_case(rng, 90, 2, k_heads, v_heads, dk, dv, dtype, 2)
+    sizes = lambda: f32(2.0 ** -rng.integers(0, widest + 1, (90, 1, 1)))  # noqa: E731
+    for n, most in (("q", 1.0), ("k", 4.0)):
+        size = sizes()
+        case[n] = (case[n].float() * dk ** -0.5 * size * (most if dtype != "f16" else 1)).to(TORCH[dtype])
+    norm = case["k"].float().square().sum(-1).repeat_interleave(v_heads // k_heads, 1)
+    case["beta"] = torch.minimum(case["beta"], 1 / norm)
+    run_delta(case, "f32", offsets=[0, 58, 90], norm_eps=None)
+
+
+@pytest.mark.parametrize("dk,dtype", [(128, "bf16"), (96, "f32"), (256, "f32")])
+@pytest.mark.parametrize("v_heads", [2, 160])
+def test_gated_delta_prompts_with_small_queries(dk, v_heads, dtype):
+    """A query's size has no part in the bits of its result: queries times powers of two give results times those, bit by bit."""
+    rng = np.random.default_rng(dk)
+    case = delta_case(rng, 100, 1, 1, v_heads, dk, 16, dtype, 1)
+    case["k"] = case["k"] * dk ** -0.5
+    size = torch.exp2(-f32(rng.integers(0, 50, 100))).float()
+    state = case["state"].clone()
+    out = nt.ninfer_gated_delta(**case, offsets=i32([0, 100]), out_dtype=torch.float32)
+    case["state"], case["q"] = state, (case["q"].float() * size[:, None, None]).to(TORCH[dtype])
+    small = nt.ninfer_gated_delta(**case, offsets=i32([0, 100]), out_dtype=torch.float32)
+    assert torch.equal(small, out * size[:, None, None])
