@@ -232,6 +232,38 @@ __device__ __forceinline__ float quad_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
     return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
 }
+// The larger magnitude; NaN where one is.
+__device__ __forceinline__ float most_of(float m, float v) {
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v)));
+    return m;
+}
+
+// What is not finite goes into no product with other tokens' values: zeros times it would make NaN of earlier ones, and the power of two
+// that fits it zeros. Of two columns by 32 tokens (y[n][e]: token 8 n + 2 (lane % 4) + e % 2 of column e / 2, the same two of a quad of lanes) the
+// first tokens that are not finite, in a byte each.
+constexpr uint32_t kAllFinite = kChunk | kChunk << 8;
+__device__ __forceinline__ uint32_t first_spoilt(const float (&y)[4][4]) {
+    uint32_t first[2] = {kChunk, kChunk};
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (!(fabsf(y[n][e]) < INFINITY)) first[e / 2] = min(first[e / 2], n * 8 + threadIdx.x % 4 * 2 + e % 2);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int k = 1; k < 4; k *= 2) first[i] = min(first[i], __shfl_xor_sync(~0u, first[i], k));
+    return first[0] | first[1] << 8;
+}
+// `value` instead of the values from there on, of kCount times 8 tokens from 8 n0 on.
+template <int kCount>
+__device__ __forceinline__ void from_spoilt(uint32_t first, float (&y)[kCount][4], float value, uint32_t n0 = 0) {
+#pragma unroll
+    for (int n = 0; n < kCount; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if ((n0 + n) * 8 + threadIdx.x % 4 * 2 + e % 2 >= (first >> e / 2 * 8 & 255)) y[n][e] = value;
+}
 
 // A request's tokens, and the chunks that are its own: distinct ones for requests whose tokens are.
 struct Range {
@@ -333,19 +365,25 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
                 else if (a.dtype == NINFER_BF16) x[e] = __uint_as_float(e % 2 ? word & 0xffff0000u : word << 16);
                 else x[e] = __half2float(__ushort_as_half((unsigned short)(e % 2 ? word >> 16 : word & 0xffffu)));
                 sum = fmaf(x[e], x[e], sum);
-                most = fmaxf(most, fabsf(x[e]));
+                most = most_of(most, x[e]);
             }
             if (row_lanes == 32) {
                 sum += __shfl_xor_sync(~0u, sum, 16);
-                most = fmaxf(most, __shfl_xor_sync(~0u, most, 16));
+                most = most_of(most, __shfl_xor_sync(~0u, most, 16));
             }
 #pragma unroll
             for (int e = 8; e; e /= 2) {
                 sum += __shfl_xor_sync(~0u, sum, e);
-                most = fmaxf(most, __shfl_xor_sync(~0u, most, e));
+                most = most_of(most, __shfl_xor_sync(~0u, most, e));
+            }
+            if (!(most < INFINITY)) {       // a row that is not finite: zeros
+                most = 0.f;
+                sum = NAN;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
             }
             const float up = power_for(most);
-            if (e0 == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? 1.f : 1.f / sqrtf(sum + a.norm_eps));
+            if (e0 == 0) scales[q][t] = (int32_t)t >= count ? 0.f : inverse_power(up) * (a.norm_eps < 0.f ? (sum == sum ? 1.f : NAN) : 1.f / sqrtf(sum + a.norm_eps));
             uint32_t high[4], low[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) split(x[2 * e] * up, x[2 * e + 1] * up, high[e], low[e]);
@@ -360,6 +398,11 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
             }
         }
     }
+    __syncthreads();
+    // a query's scale spoils its own result alone; a key's all that follows (below), and enters no product
+    const bool bad_key = !(scales[0][lane] < INFINITY);
+    __syncthreads();
+    if (warp == 0 && bad_key) scales[0][lane] = 0.f;
     __syncthreads();
     // (K, Q) K^T: 16 rows a warp
     {
@@ -409,6 +452,11 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
             g = a.log_decay[decays_at + i];
             beta = a.beta[betas_at + i];
         }
+        // A decay, beta or key that is not finite makes all of the state NaN (a decay of -infinity zeros): the chunks' kernel does that from the first
+        // such token on, and here they count as zeros.
+        const bool spoils = !(g < INFINITY) || !(fabsf(beta) < INFINITY) || bad_key;
+        const uint32_t bad = __ballot_sync(~0u, spoils);
+        if (spoils) g = beta = 0.f;
         const float bound = fminf(fmaxf(g, -32768.f), 32768.f);
         float high = bound * 1.44269504f, low = fmaf(bound, 1.44269504f, -high) + bound * 1.92596299e-8f;
 #pragma unroll
@@ -421,8 +469,6 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
             }
         }
         const float last_high = __shfl_sync(~0u, high, 31), last_low = __shfl_sync(~0u, low, 31);
-        const uint32_t bad = __ballot_sync(~0u, g != g);
-        const float poison = bad & (~0u >> (31 - lane)) ? NAN : 1.f, spoilt = bad ? NAN : 1.f;
         sums[warp][lane] = make_float4(high, low, beta, 0.f);
         __syncwarp();
         uint8_t *to = p.heads + ((uint64_t)chunk * a.v_heads + head) * kHeadBytes;       // T high and low, P high and low, the numbers
@@ -455,12 +501,12 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
         __syncwarp();
         const float of_t = put_matrix(to, tt, most_t, lane);
         float *numbers = reinterpret_cast<float *>(to + kTrianglesBytes);
-        const float fade = exp2f(high + low) * poison;
-        numbers[kOfK + lane] = fade * scales[0][lane];
+        const float fade = exp2f(high + low);
+        numbers[kOfK + lane] = bad & (~0u >> (31 - lane)) ? NAN : fade * scales[0][lane];
         numbers[kOfQ + lane] = a.scale * fade * scales[1][lane];
         numbers[kOfU + lane] = exp2f((last_high - high) + (last_low - low));
         numbers[kOfP + lane] = a.scale * scales[1][lane] * of_p;
-        if (lane < 2) numbers[kLeft + lane] = lane == 0 ? exp2f(last_high + last_low) * spoilt : of_t;
+        if (lane < 2) numbers[kLeft + lane] = lane == 0 ? exp2f(last_high + last_low) : of_t;
     }
 }
 
@@ -486,7 +532,7 @@ __host__ __device__ constexpr uint32_t sums_bytes_of(int columns) { return colum
 __host__ __device__ constexpr uint32_t smem_of(uint32_t wide, int terms, int columns, uint32_t stages, uint32_t sums) {
     return stages * stage_bytes_of(wide, terms, columns) + turning_of(columns) + sums * sums_bytes_of(columns) + (columns == 48 ? 6 * kHandedBytes : 0);
 }
-__host__ __device__ constexpr uint32_t room_of(int columns) { return columns == 32 ? 113 * 1024 - 256 : 227 * 1024 - 256; }
+__host__ __device__ constexpr uint32_t room_of(int columns) { return (columns == 32 ? 113 : 227) * 1024 - 384; }       // less what has its place at compile time
 __host__ __device__ constexpr uint32_t sums_of(uint32_t wide, int terms, int columns) { return smem_of(wide, terms, columns, 2, 2) <= room_of(columns) ? 2 : 1; }
 __host__ __device__ constexpr uint32_t stages_of(uint32_t wide, int terms, int columns) {
     return smem_of(wide, terms, columns, 3, sums_of(wide, terms, columns)) <= room_of(columns) ? 3 : 2;
@@ -516,12 +562,14 @@ __device__ __forceinline__ void load_terms(uint32_t (&b)[2][4], uint32_t from) {
 __device__ __forceinline__ void times(float (&y)[4], const uint32_t (&high)[4], const uint32_t (&low)[4], const uint32_t (&b)[2][4], int i, int term) {
     mma(y, term == 2 ? low : high, b[term == 1][2 * i], b[term == 1][2 * i + 1]);
 }
-// u += A times a lower triangle whose first term lies at `from` (this lane's row and column of the first 16 by 16).
-__device__ __forceinline__ void times_triangle(float (&u)[4][4], const uint32_t (&high)[2][4], const uint32_t (&low)[2][4], uint32_t from) {
-    uint32_t t00[2][4], t01[2][4], t11[2][4];
+// A lower triangle whose first term lies at `from` (this lane's row and column of the first 16 by 16); u += A times it.
+__device__ __forceinline__ void load_triangle(uint32_t (&t00)[2][4], uint32_t (&t01)[2][4], uint32_t (&t11)[2][4], uint32_t from) {
     load_terms(t00, from);
     load_terms(t01, from + 16 * kTriStride);
     load_terms(t11, from + 16 * kTriStride + 32);
+}
+__device__ __forceinline__ void times_triangle(float (&u)[4][4], const uint32_t (&high)[2][4], const uint32_t (&low)[2][4], const uint32_t (&t00)[2][4],
+                                               const uint32_t (&t01)[2][4], const uint32_t (&t11)[2][4]) {
 #pragma unroll
     for (int term = 0; term < 3; ++term)
 #pragma unroll
@@ -580,6 +628,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
     static_assert(chunk_smem_of(kSteps * 32, kTerms, kColumns) <= room_of(kColumns));
     extern __shared__ __align__(16) uint8_t smem[];
     __shared__ __align__(8) uint64_t full[kStages], empty[kStages], handed[3][2], taken[3][2];
+    __shared__ uint32_t spoilt[kResults ? 3 : 1][2][8];      // handed over too
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_gated_delta_args &a = p.d.a;
@@ -684,13 +733,17 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                     m0 = fmaxf(m0, fmaxf(fabsf(x.x), fabsf(x.y)));
                     m1 = fmaxf(m1, fmaxf(fabsf(x.z), fabsf(x.w)));
                 }
+                const uint32_t first = spoilt[g][j % 2][lane / 4];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&taken[g][j % 2]));
                 const float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
                 uint32_t high[2][4], low[2][4];
                 halves(u, p0, p1, high, low);
-                times_triangle(o, high, low, stage + kTri + (2 * kChunk + b_row) * kTriStride + b_col);
+                uint32_t t00[2][4], t01[2][4], t11[2][4];
+                load_triangle(t00, t01, t11, stage + kTri + (2 * kChunk + b_row) * kTriStride + b_col);
+                times_triangle(o, high, low, t00, t01, t11);
                 const float g0 = inverse_power(p0), g1 = inverse_power(p1);
+                if (first != kAllFinite) from_spoilt(first, o, NAN);
                 if (!good) continue;
                 results.on = part.column + g * 16 + out_col < v_dim;
 #pragma unroll
@@ -825,8 +878,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                 const float oe[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[n][e] -= (e % 2 ? f.y : f.x) * (x[n][e] + oe[e]);
-                m0 = fmaxf(m0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
-                m1 = fmaxf(m1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
+                m0 = most_of(most_of(m0, w[n][0]), w[n][1]);
+                m1 = most_of(most_of(m1, w[n][2]), w[n][3]);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -836,11 +889,30 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                 for (int e = 0; e < 4; ++e) qs[n][e] = (half ? x[6 + n][e] : x[4 + n][e]) + oe[e];
             }
             if (kSums == 1) named_barrier(1 + pair, 64);
-            uint32_t high[2][4], low[2][4];
+            uint32_t high[2][4], low[2][4], t00[2][4], t01[2][4], t11[2][4];
+            load_triangle(t00, t01, t11, stage + kTri + b_row * kTriStride + b_col);        // ahead of the branch
             float u[4][4] = {};
-            float p0 = power_for(quad_max(m0)), p1 = power_for(quad_max(m1));
+            // W of a column is zero from its first token on that is not finite; that token's result and later ones are NaN, and so is the state
+            // (520 us for the prompt of 8001 tokens, 514 without the test; values tested before the pair's barrier, which waits for it: 541)
+            const bool odd = !(most_of(m0, m1) < INFINITY);
+            m0 = quad_max(m0);
+            m1 = quad_max(m1);
+            uint32_t first = kAllFinite;
+            if (__any_sync(~0u, odd)) {
+                first = first_spoilt(w);
+                from_spoilt(first, w, 0.f);
+                m0 = m1 = 0.f;
+#pragma unroll
+                for (int n = 0; n < 4; ++n) {
+                    m0 = fmaxf(m0, fmaxf(fabsf(w[n][0]), fabsf(w[n][1])));
+                    m1 = fmaxf(m1, fmaxf(fabsf(w[n][2]), fabsf(w[n][3])));
+                }
+                m0 = quad_max(m0);
+                m1 = quad_max(m1);
+            }
+            float p0 = power_for(m0), p1 = power_for(m1);
             halves(w, p0, p1, high, low);
-            times_triangle(u, high, low, stage + kTri + b_row * kTriStride + b_col);
+            times_triangle(u, high, low, t00, t01, t11);
             const float of_t = numbers[kOfT], f0 = of_t * inverse_power(p0), f1 = of_t * inverse_power(p1);
             m0 = m1 = 0.f;
             float n0 = 0.f, n1 = 0.f;
@@ -866,6 +938,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                     to[n * 32] = half ? make_float4(u[2 + n][0], u[2 + n][1], u[2 + n][2], u[2 + n][3]) : make_float4(u[n][0], u[n][1], u[n][2], u[n][3]);
                     to[(4 + n) * 32] = make_float4(qs[n][0], qs[n][1], qs[n][2], qs[n][3]);
                 }
+                if (!half && lane % 4 == 0) spoilt[pair][j % 2][lane / 4] = first;
                 __syncwarp();
                 if (lane == 0 && good) mbar_arrive(smem_u32(&handed[pair][j % 2]));      // else there are no results
             } else {        // P U for this warp's 16 tokens
@@ -894,6 +967,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
             p1 = power_for(quad_max(n1));
             halves(w, p0, p1, high, low);
             const float left = numbers[kLeft], d0 = inverse_power(p0), d1 = inverse_power(p1);
+            const float left0 = (first & 255) < kChunk ? NAN : left, left1 = first >> 8 < kChunk ? NAN : left;
             constexpr int kAtOnce = kSteps % 2 ? 1 : 2;
 #pragma unroll
             for (int n0_ = 0; n0_ < kSteps; n0_ += kAtOnce) {
@@ -918,7 +992,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                 for (int m = 0; m < 2 * kAtOnce; ++m)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[2 * n0_ + m][e] = fmaf(y[m][e], e / 2 ? d1 : d0, left * s[2 * n0_ + m][e]);
+                    for (int e = 0; e < 4; ++e) s[2 * n0_ + m][e] = fmaf(y[m][e], e / 2 ? d1 : d0, (e / 2 ? left1 : left0) * s[2 * n0_ + m][e]);
             }
             float2 of_q[2], of_p[2];
 #pragma unroll
@@ -938,6 +1012,7 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         o[n][e] = fmaf(e % 2 ? of_q[n].y : of_q[n].x, qs[n][e], o[n][e] * (e / 2 ? g1 : g0) * (e % 2 ? of_p[n].y : of_p[n].x));
+                if (first != kAllFinite) from_spoilt(first, o, NAN, half * 2);
                 put_results(results, a.out_dtype, smem, out_at, to_out, o, count - (int32_t)half * 16, lane);
                 to_out += kChunk * out_step;
             }

@@ -84,3 +84,60 @@ def test_gated_delta_prompts_with_small_queries(dk, v_heads, dtype):
     case["state"], case["q"] = state, (case["q"].float() * size[:, None, None]).to(TORCH[dtype])
     small = nt.ninfer_gated_delta(**case, offsets=i32([0, 100]), out_dtype=torch.float32)
     assert torch.equal(small, out * size[:, None, None])
+
+
+def check_finite_parts(case, offsets, norm_eps=1e-6, out_dtype="f32", **kw):
+    """What is finite by the definition is right, and nothing else is finite."""
+    tokens, v_heads, dv = case["v"].shape
+    args = [f64(case[n]) for n in ("q", "k", "v", "log_decay", "beta", "state")]
+    with np.errstate(all="ignore"):
+        want, state, out_bound, bound = ol.gated_delta(*args, offsets, range(len(offsets) - 1), None, case["q"].shape[2] ** -0.5, norm_eps,
+                                                       2.0 ** -23, 2.0 ** -39)
+    out = nt.ninfer_gated_delta(**case, offsets=i32(offsets), norm_eps=norm_eps, out_dtype=TORCH[out_dtype], **kw)
+    for got, want, bound, half in ((f64(out), want, out_bound, HALF[out_dtype]), (f64(case["state"]), state, bound, HALF["f32"])):
+        live = np.isfinite(want)
+        assert np.array_equal(np.isfinite(got), live), (np.argwhere(np.isfinite(got) != live)[:5], live.mean())
+        assert (np.abs(got - want)[live] <= bound[live] + half * np.abs(want[live]) + 1e-40).all()
+    return out
+
+
+@pytest.mark.parametrize("k_heads,v_heads,dk,dv,dtype", INSTANCES)
+@pytest.mark.parametrize("norm_eps", [1e-6, None])
+def test_gated_delta_non_finite_values_reach_no_earlier_token(k_heads, v_heads, dk, dv, dtype, norm_eps):
+    """An infinity or NaN at a token of a prompt changes that token and the later ones of its columns, heads and request, and nothing before
+    or beside them, wherever it lies among the 32 tokens of a chunk."""
+    rng = np.random.default_rng(dk + v_heads)
+    offsets = [0, 67, 75, 110]
+    clean = delta_case(rng, 110, 3, k_heads, v_heads, dk, dv, dtype, 3)
+    for n in ("q", "k"):
+        clean[n] = (clean[n] * dk ** -0.5).contiguous()
+    for i, n in enumerate(("q", "k", "v", "log_decay", "beta", "state")):
+        for value in (float("nan"), float("inf"), -float("inf"))[i % 3 if v_heads > 99 else 0:i % 3 + 1 if v_heads > 99 else 3]:
+            case = {m: t.clone() for m, t in clean.items()}
+            if n == "state":
+                case[n][1, v_heads - 1, dk // 2, dv - 3] = value
+            else:
+                for t in (rng.integers(0, 16), 16 + rng.integers(0, 16), 32 + rng.integers(0, 35), 67, 109)[rng.integers(0, 2)::2]:
+                    at = case[n][int(t), int(rng.integers(0, case[n].shape[1]))]
+                    if n in ("q", "k", "v"):
+                        at[int(rng.integers(0, at.shape[0]))] = value
+                    else:
+                        at.fill_(value)
+            check_finite_parts(case, offsets, norm_eps)
+
+
+def test_gated_delta_non_finite_values_of_many_tokens():
+    """Whole columns of values, all decays, a prompt's first and last tokens."""
+    rng = np.random.default_rng(3)
+    nan, inf = float("nan"), float("inf")
+    for dk, dtype in ((128, "bf16"), (256, "f32")):
+        for v_heads in (2, 160):
+            case = delta_case(rng, 70, 1, 1, v_heads, dk, 24, dtype, 1)
+            case["v"][:, 0, 3], case["v"][69, 1, 5], case["v"][0, 1, 6] = inf, nan, -inf
+            case["v"][40, 1, 7], case["v"][33, 1, 7] = nan, inf
+            case["beta"][64:, 1] = nan
+            check_finite_parts(case, [0, 70])
+            case = delta_case(rng, 70, 1, 1, v_heads, dk, 24, dtype, 1)
+            case["q"][::2, 0, 1] = nan
+            case["log_decay"].fill_(-inf)
+            check_finite_parts(case, [0, 70])
