@@ -7,8 +7,8 @@
 // than 32768 elements are read twice (norm_long_kernel).
 //
 // Measured: 8192 rows of 5120 with a residual, all bfloat16, 336 MB, 49.2 to 50.0 us (6.7 to 6.8 TB/s, the rate of a copy); 4001 rows of 48
-// heads of 128 with gates, 147 MB, 25.1 us (5.9 TB/s, at 74 % of the issue slots). Reciprocal square roots, exponentials and
-// quotients are the fast ones, within 2 units (2^-24 z for an exponent z): with the exact ones' sequences 55 and 39 us.
+// heads of 128 with gates, 147 MB, 26.3 us (5.6 TB/s, at 73 % of the issue slots). Reciprocal square roots, powers and reciprocals
+// are the fast ones, within 4 2^-24: with the exact ones' sequences 55 and 39 us. (A gate's exponent in one float, 2^-24 z off, 25.2.)
 #include <cmath>
 
 #include "decode.cuh"
@@ -62,7 +62,18 @@ __device__ __forceinline__ void widen(const Raw8 &r, int dtype, float (&o)[8]) {
     }
 }
 
-__device__ __forceinline__ float gated(float y, float z) { return y * __fdividef(z, 1.f + __expf(-z)); }
+// y z / (1 + e^-z) as y z E / (1 + E) with E = e^z (from 44 on the quotient is 1): no sum overflows, and nothing is lost down to the least number.
+// E = 2^2t e^d with t = z log2(e) / 2 rounded, whose power is a normal number, and d = z - 2 t ln 2 what that left out; within 14 2^-24
+// (2^t 4, twice; ln 2's own rounding 5 at z = -104; the sum 1).
+__device__ __forceinline__ float gated(float y, float z) {
+    const float a = fminf(z, 44.f), t = a * 0.72134752f;
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+    e *= e;
+    e = fmaf(e, fmaf(t, -1.38629436f, a), e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+    return e * r * (y * z);
+}
 
 // Where element `at` of group `group` lies in the row's tensors.
 struct Place {

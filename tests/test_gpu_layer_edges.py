@@ -141,3 +141,25 @@ def test_gated_delta_non_finite_values_of_many_tokens():
             case["q"][::2, 0, 1] = nan
             case["log_decay"].fill_(-inf)
             check_finite_parts(case, [0, 70])
+
+
+# ------------------------------------------------------------------- norm ---
+@pytest.mark.parametrize("group", [128, 24, 512, 5, 33000])
+def test_norm_gates_of_any_size(group):
+    """z / (1 + e^-z) however far from 0, infinities and NaN as the formula has them. In units of 2^-24 the root of the squares' sum is off by 23
+    (test_gpu_layer.py), the reciprocal root by 4, the exponential by 14, the reciprocal by 2, a sum and four products by one each: 48."""
+    rng = np.random.default_rng(group)
+    cols = group * max(1, 2048 // group)
+    x = randn(rng, (8, cols))
+    gate = f32(rng.uniform(-104, 104, (8, cols)))
+    gate[1] = f32(rng.uniform(-89, -86, cols))
+    gate[2] = f32(rng.standard_normal(cols) * 1e-3)
+    gate[3, :5] = f32([1e30, -1e30, 0.0, -0.0, 3e38])
+    for dtype in ("f32", "bf16"):
+        xd, gd = x.to(TORCH[dtype]), gate.to(TORCH[dtype])
+        _, want = ol.norm(f64(xd), None, f64(gd), None, group, 1e-5)
+        near(f64(nt.ninfer_norm(xd, None, 1e-5, gate=gd, group=group, out_dtype=torch.float32)), want, 48 * 2.0 ** -24 * np.abs(want), "f32")
+    gate[0, 0], gate[0, 1], gate[0, 2] = float("inf"), -float("inf"), float("nan")
+    x[0, 0] = 1.0
+    y = nt.ninfer_norm(x, None, 1e-5, gate=gate, group=group)
+    assert y[0, 0] == float("inf") and y[0, 1:3].isnan().all() and y[0, 3:].isfinite().all()
