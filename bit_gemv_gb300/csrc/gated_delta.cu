@@ -18,6 +18,7 @@
 #include "decode.cuh"
 #include "gemv.h"
 #include "ninfer_layer.h"
+#include "overlap.h"
 
 namespace ninfer {
 namespace {
@@ -1127,6 +1128,20 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     p.group = FastDiv((uint32_t)(a.v_heads / a.k_heads));
     const uint64_t rows = a.requests * a.v_heads;       // below 2^47; of at most eight slabs each
     if (rows * ((a.v_dim + 31) / 32) > 0x7fffffffull) return fail(NINFER_ERR_OVERFLOW, "gated delta: too many requests and heads");
+    const uint64_t es = dtype_size(a.dtype);
+    const auto heads = [&](const void *p, uint64_t dim, uint64_t token, uint64_t n, uint64_t head) { return Span(p, dim * es, a.tokens, token * es, n, head * es); };
+    const Span out(a.out, a.tokens * a.v_heads * a.v_dim * dtype_size(a.out_dtype)), v = heads(a.v, a.v_dim, a.v_token_stride, a.v_heads, a.v_head_stride);
+    const Span written[] = {out, Span(a.state, whole * 4, a.slots, a.slot_stride * 4), Span(a.status, 4), Span(workspace, need)};
+    const Span inputs[] = {heads(a.q, a.k_dim, a.q_token_stride, a.k_heads, a.q_head_stride), heads(a.k, a.k_dim, a.k_token_stride, a.k_heads, a.k_head_stride),
+                           out.same(v) && a.out_dtype == a.dtype ? Span() : v, Span(a.log_decay, a.v_heads * 4, a.tokens, a.decay_stride * 4),
+                           Span(a.beta, a.v_heads * 4, a.tokens, a.beta_stride * 4), Span(a.state_slots, a.requests * 4), Span(a.offsets, (a.requests + 1) * 4),
+                           Span(a.lengths, a.requests * 4)};
+    bool shared = false;
+    for (const Span &o : written) {
+        for (const Span &i : inputs) shared = shared || o.meets(i);
+        for (const Span &w : written) shared = shared || (&w != &o && o.meets(w));
+    }
+    if (shared) return fail(NINFER_ERR_INVALID_ARGUMENT, "gated delta: out may be v without gaps, of one dtype; no other of out, state, status and workspace overlaps anything");
     const auto grid = [&](uint64_t slab, unsigned *blocks) {
         const uint64_t slabs = (a.v_dim + slab - 1) / slab;
         p.slabs = FastDiv((uint32_t)slabs);

@@ -14,6 +14,7 @@
 #include "decode.cuh"
 #include "gemv.h"
 #include "ninfer_layer.h"
+#include "overlap.h"
 
 namespace ninfer {
 namespace {
@@ -311,15 +312,18 @@ extern "C" int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream) {
         if (a.rows > 1 && t.stride >= (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "norm: %s stride of 2^40 or more", t.name);
         vec = vec && aligned(t.p, 16) && (a.rows == 1 || t.p == a.weight || t.stride * es % 16 == 0);
     }
-    // in place only where every element is written where it was read
-    const bool moved = a.rows > 1 && (a.out == a.x ? a.out_stride != a.x_stride : a.out == a.gate && a.out_stride != a.gate_stride);
-    if ((a.sum && a.sum == a.residual && a.rows > 1 && a.sum_stride != a.residual_stride) || moved || (a.out == a.x && a.out_dtype != a.x_dtype) ||
-        (a.out == a.gate && a.out_dtype != a.gate_dtype) || a.out == a.residual || a.out == a.sum || a.sum == a.x || (a.sum && a.sum == a.gate))
-        return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: out may be x or gate, sum the residual, with the same stride and dtype; no other outputs overlap");
     const uint64_t groups = a.cols / a.group;
     uint64_t total;
     if (!mul_ok(a.rows, groups, &total) || total > 0x7fffffffull)
         return fail(NINFER_ERR_OVERFLOW, "norm: rows * groups over 2^31 - 1");
+    // in place only where every element is written where it was read
+    const auto span = [&](const void *p, uint64_t stride, int dtype) { return Span(p, a.cols * dtype_size(dtype), a.rows, stride * dtype_size(dtype)); };
+    const Span x = span(a.x, a.x_stride, a.x_dtype), gate = a.gate ? span(a.gate, a.gate_stride, a.gate_dtype) : Span(), out = span(a.out, a.out_stride, a.out_dtype);
+    const Span residual = a.residual ? span(a.residual, a.residual_stride, a.residual_dtype) : Span(), sum = a.sum ? span(a.sum, a.sum_stride, a.residual_dtype) : Span();
+    const Span weight = a.weight ? Span(a.weight, a.group * dtype_size(a.weight_dtype)) : Span();
+    if ((out.meets(x) && !(out.same(x) && a.out_dtype == a.x_dtype)) || (out.meets(gate) && !(out.same(gate) && a.out_dtype == a.gate_dtype)) ||
+        (sum.meets(residual) && !sum.same(residual)) || out.meets(residual) || out.meets(sum) || out.meets(weight) || sum.meets(x) || sum.meets(gate) || sum.meets(weight))
+        return fail(NINFER_ERR_INVALID_ARGUMENT, "norm: out may be x or gate, sum the residual, with the same stride and dtype; no other outputs overlap");
     NormParams p;
     p.a = a;
     p.groups = FastDiv((uint32_t)groups);

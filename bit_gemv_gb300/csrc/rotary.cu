@@ -15,6 +15,7 @@
 #include "decode.cuh"
 #include "gemv.h"
 #include "ninfer_layer.h"
+#include "overlap.h"
 
 namespace ninfer {
 namespace {
@@ -255,15 +256,18 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
             return fail(NINFER_ERR_ALIGNMENT, "rotary: q, k and their outputs must have bases and strides of 16 bytes' multiples");
         if (token >= (1ull << 40) || head >= (1ull << 40)) return fail(NINFER_ERR_OVERFLOW, "rotary: a stride of 2^40 or more");
     }
-    const auto moved = [&](uint64_t token, uint64_t to_token, uint64_t head, uint64_t to_head, uint64_t heads) {
-        return (a.tokens > 1 && token != to_token) || (heads > 1 && head != to_head);
-    };
-    if ((a.q == a.q_out && moved(a.q_token_stride, a.q_out_token_stride, a.q_head_stride, a.q_out_head_stride, a.q_heads)) ||
-        (a.k && a.k == a.k_out && moved(a.k_token_stride, a.k_out_token_stride, a.k_head_stride, a.k_out_head_stride, a.kv_heads)) ||
-        a.q_out == a.k || (a.k && (a.q_out == a.k_out || a.q == a.k_out)))
-        return fail(NINFER_ERR_INVALID_ARGUMENT, "rotary: an output may be its own input with the same strides, and overlaps nothing else");
     if (!aligned(a.positions, 4) || !aligned(a.frequencies, 8) || !aligned(a.q_weight, 16) || !aligned(a.k_weight, 16))
         return fail(NINFER_ERR_ALIGNMENT, "rotary: positions must be 4-byte, frequencies 8-byte, weights 16-byte aligned");
+    const auto span = [&](const void *p, uint64_t token, uint64_t heads, uint64_t head) { return p ? Span(p, a.head_dim * es, a.tokens, token * es, heads, head * es) : Span(); };
+    const Span q = span(a.q, a.q_token_stride, a.q_heads, a.q_head_stride), q_out = span(a.q_out, a.q_out_token_stride, a.q_heads, a.q_out_head_stride);
+    const Span k = span(a.k, a.k_token_stride, a.kv_heads, a.k_head_stride), k_out = span(a.k_out, a.k_out_token_stride, a.kv_heads, a.k_out_head_stride);
+    const bool q_here = q_out.same(q), k_here = k_out.same(k);
+    bool shared = (!q_here && q_out.meets(q)) || (!k_here && k_out.meets(k)) || !q_out.simple() || !k_out.simple() || q_out.meets(k_out) ||
+                  (!k_here && q_out.meets(k)) || (!q_here && k_out.meets(q));
+    const uint64_t weight_bytes = a.q_weight || a.k_weight ? a.head_dim * dtype_size(a.weight_dtype) : 0;
+    for (const Span &in : {Span(a.positions, a.tokens * 4), Span(a.frequencies, a.rotary_dim * 4), Span(a.q_weight, weight_bytes), Span(a.k_weight, weight_bytes)})
+        shared = shared || q_out.meets(in) || k_out.meets(in);
+    if (shared) return fail(NINFER_ERR_INVALID_ARGUMENT, "rotary: an output may be its own input with the same strides, and overlaps nothing else");
     RotaryParams p;
     p.a = a;
     p.half = (uint32_t)(a.rotary_dim / 2);

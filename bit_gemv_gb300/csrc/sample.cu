@@ -31,6 +31,7 @@
 #include "decode.cuh"
 #include "gemv.h"
 #include "ninfer_layer.h"
+#include "overlap.h"
 
 namespace ninfer {
 namespace {
@@ -988,6 +989,15 @@ extern "C" int ninfer_sample(const ninfer_sample_args *args, ninfer_stream strea
     for (const void *q : {(const void *)a.temperature, (const void *)a.top_p, (const void *)a.min_p, (const void *)a.top_k,
                           (const void *)a.random, (const void *)a.tokens, (const void *)a.logprobs})
         if (!aligned(q, 4)) return fail(NINFER_ERR_ALIGNMENT, "sample: controls and outputs must be 4-byte aligned");
+    // a row's controls have been read when its results are written
+    const Span logits(a.logits, a.vocab * dtype_size(a.dtype), a.rows, a.stride * dtype_size(a.dtype));
+    const Span chosen(a.tokens, a.rows * 4), logprobs(a.logprobs, a.rows * 4);
+    bool shared = chosen.meets(logprobs) || chosen.meets(logits) || logprobs.meets(logits);
+    for (const void *q : {(const void *)a.temperature, (const void *)a.top_p, (const void *)a.min_p, (const void *)a.top_k, (const void *)a.random}) {
+        const Span in(q, a.rows * 4);
+        shared = shared || (chosen.meets(in) && !chosen.same(in)) || (logprobs.meets(in) && !logprobs.same(in));
+    }
+    if (shared) return fail(NINFER_ERR_INVALID_ARGUMENT, "sample: tokens and logprobs may not overlap logits, each other or parts of the controls");
     DeviceInfo d;
     int st = device_info(&d);
     if (st) return st;

@@ -64,7 +64,7 @@ int ninfer_norm(const ninfer_norm_args *args, ninfer_stream stream);
  * The fraction of a turn is exact (products of whole numbers modulo 2^64), so that far positions lose nothing.
  *   q, k, q_out, k_out: device, one dtype (f32, bf16, f16), element e of head h of token t at
  *     t * token_stride + h * head_stride + e, each with strides of its own, multiples of 16 bytes; an output may be its
- *     input (same strides). k NULL: queries alone.
+ *     input (same strides), and overlaps nothing else that the call reads or writes. k NULL: queries alone.
  *   positions: device int32[tokens]; a token with a negative one is left out: nothing of it is written.
  *   frequencies: device uint64[rotary_dim / 2], turns a position times 2^64.
  *   q_weight, k_weight: device, head_dim elements of weight_dtype; NULL: no norm. magnitude, weight_offset
@@ -126,6 +126,7 @@ int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream stream);
  *     requests without tokens.
  *   workspace: with offsets, device, 256-byte aligned, at least ninfer_gated_delta_workspace() bytes; its contents need no
  *     initial value and are not preserved, and no other call may use it at the same time. Without offsets it is not used (NULL will do).
+ *   out may be v itself (of one dtype, v without gaps). Beside that out, state, status and workspace overlap nothing that the call reads or writes.
  *   k_dim, v_dim: multiples of 8 up to 256; v_heads a multiple of k_heads; scale finite.
  * States and sums are fp32. With offsets, a request's tokens go 32 at a time through the tensor cores: operands hold 22 bits of each
  * value (q and k of 16-bit types all of theirs). Each token's q and k has a scale of its own, for each column of a state the state, the values
@@ -167,7 +168,7 @@ int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *workspace, uin
  *   logits: device, dtype f32, bf16 or f16, row b at b * stride.
  *   temperature, top_p, min_p: device float[rows], NULL: 1, 1, 0; top_k: device int32[rows], NULL: 0.
  *   random: device float[rows], in [0, 1) (cut to it).
- *   tokens: device int32[rows]; logprobs: device float[rows] or NULL.
+ *   tokens: device int32[rows]; logprobs: device float[rows] or NULL. Each may be one of the controls' arrays; else they overlap nothing.
  * Weights are whole multiples of 2^(vocab's bits - 62) of the largest one, each off by less than 2^-29 and the rounding of x - m (2^-24 of
  * the exponent) of itself; their sums are exact and do not depend on an order: equal rows give equal tokens, however they are divided.
  * Errors: INVALID_ARGUMENT, SHAPE (rows or vocab 0, vocab over 2^30, stride below vocab), ALIGNMENT, OVERFLOW, CUDA.

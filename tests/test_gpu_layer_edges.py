@@ -163,3 +163,71 @@ def test_norm_gates_of_any_size(group):
     x[0, 0] = 1.0
     y = nt.ninfer_norm(x, None, 1e-5, gate=gate, group=group)
     assert y[0, 0] == float("inf") and y[0, 1:3].isnan().all() and y[0, 3:].isfinite().all()
+
+
+# ------------------------------------------------------------------ views ---
+def test_views_between_each_others_rows_are_taken():
+    """Parts of one buffer that share no element, whatever their strides, and outputs that the documentation allows over inputs."""
+    rng = np.random.default_rng(31)
+    # norm: x, residual, gate, sum and out as columns of one buffer; rows of two strides between each other
+    wide = randn(rng, (6, 5 * 64))
+    x, r, g, s, o = (wide[:, i * 64:(i + 1) * 64] for i in range(5))
+    want_s, want = ol.norm(f64(x), f64(r), f64(g))
+    nt.ninfer_norm(x, residual=r, gate=g, sum=s, out=o)
+    near(f64(o), want, 48 * 2.0 ** -24 * np.abs(want), "f32")
+    near(f64(s), want_s, 2.0 ** -24 * np.abs(want_s), "f32")
+    rows = randn(rng, (12, 64))
+    even, third = rows[0:9:2], rows[1:12:4]                 # x at 0, 2, 4; out at 1, 5, 9
+    before = rows.clone()
+    nt.ninfer_norm(even[:3], out=third)
+    assert torch.equal(third, nt.ninfer_norm(before[0:5:2]))
+    third.copy_(before[1:12:4])
+    assert torch.equal(rows, before)
+    # rotary: queries and gates by turns in rows that end with keys, in place; heads before tokens
+    q_heads, kv, dim = 4, 2, 64
+    width = (2 * q_heads + kv) * dim
+    buffer = randn(rng, (5, width))
+    q, k = buffer[:, :2 * q_heads * dim].unflatten(1, (q_heads, 2 * dim))[:, :, :dim], buffer[:, 2 * q_heads * dim:].unflatten(1, (kv, dim))
+    freq, positions = torch.from_numpy(nt.ninfer_rotary_frequencies(dim)[0]).to(DEV), i32(np.arange(5) * 7)
+    gates = buffer[:, :2 * q_heads * dim].unflatten(1, (q_heads, 2 * dim))[:, :, dim:]
+    kept, apart = gates.clone(), nt.ninfer_rotary(q.clone(), k.clone(), positions, freq)
+    nt.ninfer_rotary(q, k, positions, freq, q_out=gates)     # the gates' places
+    assert torch.equal(gates, apart[0]) and torch.equal(k, apart[1])
+    gates.copy_(kept)
+    turned = randn(rng, (q_heads + kv, 5, dim))
+    qt, kt = turned[:q_heads].transpose(0, 1), turned[q_heads:].transpose(0, 1)
+    apart = nt.ninfer_rotary(qt.clone(), kt.clone(), positions, freq)
+    nt.ninfer_rotary(qt, kt, positions, freq)
+    assert torch.equal(qt, apart[0]) and torch.equal(kt, apart[1])
+    # gated delta: states between which the results lie, and results in the values' place
+    for tokens, offsets in ((3, None), (70, i32([0, 40, 65, 70]))):
+        case = delta_case(rng, tokens, 3, 1, 2, 64, 32, "f32", 3)
+        state = case["state"].clone()
+        want = nt.ninfer_gated_delta(**{**case, "state": state}, offsets=offsets)
+        pool = torch.zeros(3, 2 * 64 * 32 + tokens * 64, device=DEV)
+        pool[:, :4096] = case["state"].flatten(1)
+        got = nt.ninfer_gated_delta(**{**case, "state": pool[:, :4096].unflatten(1, (2, 64, 32))}, offsets=offsets, out=pool[1, 4096:].view(tokens, 2, 32))
+        assert torch.equal(got, want) and torch.equal(pool[:, :4096], state.flatten(1)) and not pool[0, 4096:].any() and not pool[2, 4096:].any()
+        values = case["v"].contiguous()
+        state = case["state"].clone()
+        assert nt.ninfer_gated_delta(**{**case, "state": state, "v": values}, offsets=offsets, out=values) is values
+        assert torch.equal(values, want)
+    # sampling: results in the controls' place
+    x, random, k = randn(rng, (9, 60000)), f32(rng.random(9)), i32([0, 3, 50, 0, 7, 0, 0, 1, 2000])
+    logprobs = torch.empty(9, device=DEV)
+    tokens = nt.ninfer_sample(x, random, top_k=k, logprobs=logprobs)
+    nt.ninfer_sample(x, random, top_k=k, out=k, logprobs=random)
+    assert torch.equal(k, tokens) and torch.equal(random, logprobs)
+
+
+@pytest.mark.parametrize("dk,dv,v_heads,dtype", [(128, 128, 4, "bf16"), (64, 40, 4, "f16"), (128, 72, 160, "bf16"), (256, 24, 160, "f32"), (96, 48, 6, "f32")])
+def test_gated_delta_results_in_the_values_place(dk, dv, v_heads, dtype):
+    rng = np.random.default_rng(dk + dv)
+    for tokens, offsets in ((3, None), (400, i32([0, 340, 341, 400]))):
+        case = delta_case(rng, tokens, 3, 2, v_heads, dk, dv, dtype, 3)
+        state, values = case["state"].clone(), case["v"].contiguous()
+        want = nt.ninfer_gated_delta(**{**case, "state": state}, offsets=offsets)
+        nt.ninfer_gated_delta(**{**case, "v": values}, offsets=offsets, out=values)
+        # bit by bit: without norms the states grow beyond all numbers, and NaN is no NaN's equal
+        same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))  # noqa: E731
+        assert same(values, want) and same(case["state"], state)
