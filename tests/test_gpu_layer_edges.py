@@ -143,6 +143,26 @@ def test_gated_delta_non_finite_values_of_many_tokens():
             check_finite_parts(case, [0, 70])
 
 
+@pytest.mark.parametrize("k_heads,v_heads,dk,dv,dtype", [(4, 8, 128, 128, "bf16"), (2, 4, 64, 64, "f16"), (2, 4, 96, 80, "f32"), (1, 6, 256, 48, "bf16"),
+                                                         (1, 6, 256, 72, "f32")])
+def test_gated_delta_a_request_alone_and_among_others(k_heads, v_heads, dk, dv, dtype):
+    """The number of requests picks the columns of a CTA and who makes the results; no bit of a request's results depends on it."""
+    rng = np.random.default_rng(dk + dv)
+    lengths = rng.integers(1, 140, 90)
+    offsets = np.concatenate([[0], np.cumsum(lengths)])
+    case = delta_case(rng, offsets[-1], 90, k_heads, v_heads, dk, dv, dtype, 90)
+    for norm_eps in (1e-6, None):
+        if norm_eps is None:
+            case["k"] = case["k"] * dk ** -0.5
+        state = case["state"].clone()
+        out = nt.ninfer_gated_delta(**{**case, "state": state}, offsets=i32(offsets), norm_eps=norm_eps)
+        for some in ([0], [17], [89], [3, 50], list(range(12, 24)), list(range(40, 70))):
+            part = {n: torch.cat([case[n][offsets[r]:offsets[r + 1]] for r in some]) for n in ("q", "k", "v", "log_decay", "beta")}
+            s, o = case["state"][some].clone(), np.concatenate([[0], np.cumsum(lengths[some])])
+            got = nt.ninfer_gated_delta(**part, state=s, offsets=i32(o), norm_eps=norm_eps)
+            assert torch.equal(got, torch.cat([out[offsets[r]:offsets[r + 1]] for r in some])) and torch.equal(s, state[some])
+
+
 # ------------------------------------------------------------------- norm ---
 @pytest.mark.parametrize("group", [128, 24, 512, 5, 33000])
 def test_norm_gates_of_any_size(group):
