@@ -69,6 +69,40 @@ __device__ __forceinline__ void load8(const void *base, uint64_t idx, int dtype,
     }
 }
 
+// 8 neighbouring elements as they lie in memory: all loads of a thread are under way before the first conversion
+struct Raw8 {
+    uint4 lo, hi;
+};
+
+__device__ __forceinline__ Raw8 raw8(const void *base, uint64_t at, int dtype) {
+    Raw8 r;
+    const uint8_t *p = static_cast<const uint8_t *>(base) + at * (dtype == NINFER_F32 ? 4 : 2);
+    r.lo = *reinterpret_cast<const uint4 *>(p);
+    if (dtype == NINFER_F32) r.hi = *reinterpret_cast<const uint4 *>(p + 16);
+    return r;
+}
+
+__device__ __forceinline__ void widen(const Raw8 &r, int dtype, float (&o)[8]) {
+    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
+    if (dtype == NINFER_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = __uint_as_float(w[i]);
+    } else if (dtype == NINFER_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            o[2 * i] = f.x;
+            o[2 * i + 1] = f.y;
+        }
+    }
+}
+
 __device__ __forceinline__ void store8(void *base, uint64_t idx, int dtype, const float (&o)[8]) {
     if (dtype == NINFER_F32) {
         float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(base) + idx);

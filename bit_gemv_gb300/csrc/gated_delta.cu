@@ -611,7 +611,7 @@ __device__ __forceinline__ void put_results(const Results &r, int dtype, uint8_t
     __syncwarp();
 }
 
-// 32 to 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
+// 16 to 64 columns of one state a CTA, 16 a pair of warps, of which each has half of the columns' k; the state stays in the
 // accumulators' layout of mma, transposed (rows are columns of S, columns k), which is the layout of the A operand of the
 // products with K and Q, and U, made the same way, that of the products with P and K. Every factor that is not exact in binary16 enters
 // as two terms, scaled row by row. The pair adds up its halves of K S and Q S through shared memory, has U twice, and shares out the
@@ -1150,7 +1150,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
     unsigned blocks;
     const cudaStream_t s = (cudaStream_t)stream;
     if (!a.offsets) {
-        // whole rows of a state where there are enough of them for the SMs, else narrow slabs
+        // 64 columns a CTA where heads and requests make enough of them for the SMs, else 32
         DeviceInfo d;
         st = device_info(&d);
         if (st) return st;
@@ -1158,9 +1158,7 @@ extern "C" int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *wor
         const int lanes = narrow || a.v_dim <= 32 ? 8 : 16;
         grid(lanes * 4, &blocks);
         const bool small = a.k_dim <= (uint64_t)(8 * kStepThreads / lanes);
-        const auto kernel = lanes == 8    ? step_kernel<8, 8>
-                            : lanes == 16 ? (small ? step_kernel<16, 8> : step_kernel<16, 16>)
-                                          : (small ? step_kernel<32, 8> : step_kernel<32, 16>);
+        const auto kernel = lanes == 8 ? step_kernel<8, 8> : small ? step_kernel<16, 8> : step_kernel<16, 16>;
         return launch_dependent("gated delta", kernel, dim3(blocks), dim3(kStepThreads), 0, s, p);
     }
     DeviceInfo d;

@@ -25,36 +25,8 @@ constexpr int kThreads = 256;
 struct RotaryParams {
     ninfer_rotary_args a;
     uint32_t heads, q_heads, half;      // heads: q_heads + kv_heads; half: rotary_dim / 2
-    uint32_t first, tokens;     // of this launch
     float inverse;              // 1 / head_dim
 };
-
-// 8 neighbouring elements as they lie in memory
-struct Raw8 {
-    uint4 lo, hi;
-};
-
-template <int kDtype>
-__device__ __forceinline__ Raw8 raw8(const void *base, uint64_t at) {
-    Raw8 r;
-    if (kDtype == NINFER_F32) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(base) + at);
-        r.lo = p[0];
-        r.hi = p[1];
-    } else
-        r.lo = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(base) + at);
-    return r;
-}
-
-template <int kDtype>
-__device__ __forceinline__ void widen(const Raw8 &r, float (&o)[8]) {
-    const uint32_t w[8] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w, r.hi.x, r.hi.y, r.hi.z, r.hi.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-        o[i] = kDtype == NINFER_F32    ? __uint_as_float(w[i])
-               : kDtype == NINFER_BF16 ? __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16)
-                                       : __half2float(__ushort_as_half((uint16_t)(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xffff)));
-}
 
 // Heads of a team under way at once.
 __host__ __device__ constexpr uint32_t ahead_of(int dtype) { return dtype == NINFER_F32 ? 2 : 4; }
@@ -68,7 +40,7 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
     pdl_launch_dependents();
     pdl_wait();
     const ninfer_rotary_args &a = p.a;
-    const uint32_t token = p.first + blockIdx.x, tid = threadIdx.x;
+    const uint32_t token = blockIdx.x, tid = threadIdx.x;
     const int32_t position = a.positions[token];
     if (position < 0) return;
     const uint32_t lane = tid % kLanes, team = tid / kLanes, e = lane * 8;
@@ -85,7 +57,7 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
             const uint32_t h = h0 + j * teams + team;
             const bool key = h >= p.q_heads;
             const uint32_t head = key ? h - p.q_heads : h;
-            if (inside && h < p.heads) raw[j] = raw8<kDtype>(key ? a.k : a.q, (key ? k_in : q_in) + head * (key ? a.k_head_stride : a.q_head_stride));
+            if (inside && h < p.heads) raw[j] = raw8(key ? a.k : a.q, (key ? k_in : q_in) + head * (key ? a.k_head_stride : a.q_head_stride), kDtype);
         }
     };
     fetch(0);
@@ -105,7 +77,7 @@ __global__ void __launch_bounds__(kThreads, 5) rotary_kernel(const __grid_consta
         const bool on = inside && h < p.heads, key = h >= p.q_heads;
         const uint32_t head = key ? h - p.q_heads : h;
         float x[8] = {};
-        if (on) widen<kDtype>(raw[j], x);
+        if (on) widen(raw[j], kDtype, x);
         const void *weight = key ? a.k_weight : a.q_weight;
         if (a.q_weight || a.k_weight) {
             float sum = 0.f;
@@ -273,8 +245,6 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
     p.half = (uint32_t)(a.rotary_dim / 2);
     p.q_heads = (uint32_t)a.q_heads;
     p.heads = (uint32_t)(a.q_heads + (a.k ? a.kv_heads : 0));
-    p.first = 0;
-    p.tokens = (uint32_t)a.tokens;
     p.inverse = 1.f / (float)a.head_dim;
     const unsigned lanes = a.head_dim <= 64 ? 8 : a.head_dim <= 128 ? 16 : 32;
     const int pairs = a.interleaved ? 0 : p.half % 8 == 0 ? 1 : 2;
@@ -284,5 +254,5 @@ extern "C" int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream strea
     // as many teams as take the heads in the fewest rounds
     const unsigned ahead = ahead_of(a.dtype), rounds = (p.heads * lanes + ahead * kThreads - 1) / (ahead * kThreads);
     const unsigned teams = (p.heads + ahead * rounds - 1) / (ahead * rounds), threads = (teams * lanes + 31) / 32 * 32;
-    return launch_dependent("rotary", kernel, dim3(p.tokens), dim3(threads), 0, (cudaStream_t)stream, p);
+    return launch_dependent("rotary", kernel, dim3((unsigned)a.tokens), dim3(threads), 0, (cudaStream_t)stream, p);
 }

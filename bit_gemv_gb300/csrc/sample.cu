@@ -113,7 +113,6 @@ struct alignas(16) Shared {
     struct {
         uint64_t above, inside;
         uint32_t bin, bin2, border, last;
-        bool over;
     } cut;
     uint64_t target, all;
 };
