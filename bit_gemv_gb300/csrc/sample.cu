@@ -60,6 +60,7 @@ struct SampleParams {
     uint32_t vectors;       // 16-byte vectors of a row a CTA
     int scale;              // weights are whole multiples of 2^-scale
     bool held;              // in shared memory
+    uint32_t few_k;         // top_k up to which the tokens that may be kept are listed
     float unit, slack;      // of the histogram's weights: a bin's largest is `unit`; sums are too small by less than `slack` of themselves
 };
 
@@ -718,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     float limit = INFINITY, scale = row.c_hi * 64.f;
     uint64_t all_weights = 0;
     if (by_k) {
-        if ((uint32_t)top_k <= kFew && (uint32_t)top_k * 5 < ranks * kThreads * 4) {
+        if ((uint32_t)top_k <= p.few_k) {
             scale = (float)(kBins - 1) / (row.m - logit_of(lowest));
             if (!(fabsf(scale) < FLT_MAX)) scale = 0.f;            // one logit only; otherwise what lies off by rounding goes to the last bin
             row.clear();
@@ -1017,6 +1018,12 @@ extern "C" int ninfer_sample(const ninfer_sample_args *args, ninfer_stream strea
     p.unit = (float)std::min<uint64_t>(65535, 0xfffffff0ull / tokens);
     p.slack = 0x1p-12f + 1.02f / p.unit;
     p.held = p.vectors * 16ull <= kMostSliceBytes;
+    // Listing costs by top_k, a border's histogram by the tokens of a thread, so that the one ends where top_k is 12 times these (us, listed and
+    // by histogram: a row of 248320 with top_k 200 14.5 and 17.8, 400 21.0 and 18.1; 64 rows of 4099, 50 12.2 and 13.0, 200 16.4 and 13.4). Where
+    // clusters have to wait for others, listing frees most of their CTAs sooner (64 rows of 248320, 800 92 and 117, 1024 119 and 119). Fewer threads than
+    // top_k or hardly more have no maxima that bound it (256 rows of 32003 in a CTA each, 380 42.7 and 45.5, 800 54.9 and 48.0).
+    const uint64_t each = (a.vocab + ranks * kThreads - 1) / (ranks * kThreads), most = ranks * kThreads * 4 / 5;
+    p.few_k = (uint32_t)std::min<uint64_t>(most, a.rows * ranks > (uint64_t)d.sms * kResident ? kFew : std::min<uint64_t>(kFew, 12 * each));
     const auto kernel = a.dtype == NINFER_F32    ? sample_kernel<NINFER_F32>
                         : a.dtype == NINFER_BF16 ? sample_kernel<NINFER_BF16>
                                                  : sample_kernel<NINFER_F16>;
