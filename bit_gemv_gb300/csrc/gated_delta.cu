@@ -233,11 +233,12 @@ __device__ __forceinline__ float quad_max(float v) {
     v = fmaxf(v, __shfl_xor_sync(~0u, v, 1));
     return fmaxf(v, __shfl_xor_sync(~0u, v, 2));
 }
-// The larger magnitude; NaN where one is.
-__device__ __forceinline__ float most_of(float m, float v) {
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(fabsf(v)));
+// The largest magnitude; NaN where one is.
+__device__ __forceinline__ float most_of(float m, float v, float w) {
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v), "f"(w));
     return m;
 }
+__device__ __forceinline__ float most_of(float m, float v) { return most_of(m, v, v); }
 
 // What is not finite goes into no product with other tokens' values: zeros times it would make NaN of earlier ones, and the power of two
 // that fits it zeros. Of two columns by 32 tokens (y[n][e]: token 8 n + 2 (lane % 4) + e % 2 of column e / 2, the same two of a quad of lanes) the
@@ -266,18 +267,22 @@ __device__ __forceinline__ void from_spoilt(uint32_t first, float (&y)[kCount][4
             if ((n0 + n) * 8 + threadIdx.x % 4 * 2 + e % 2 >= (first >> e / 2 * 8 & 255)) y[n][e] = value;
 }
 
-// A request's tokens, and the chunks that are its own: distinct ones for requests whose tokens are.
+// A request's tokens, and the chunks that are its own: distinct ones for requests whose tokens are, in whatever order they lie. A chunk of 32 tokens
+// holds one with 31 over a multiple of 32, whose 32nd is its number; a request's last chunk, if it has fewer, comes behind all those.
 struct Range {
     int32_t begin, end;
-    uint32_t chunk, chunks;
+    uint32_t first, whole, last, chunks;        // number of the first whole chunk, how many, number of one with fewer tokens, chunks in all
 };
 __device__ __forceinline__ Range range_of(const ninfer_gated_delta_args &a, uint32_t request) {
     const int32_t most = (int32_t)a.tokens;
     Range r;
     r.begin = min(max(a.offsets[request], 0), most);
     r.end = min(max(a.offsets[request + 1], 0), most);
-    r.chunks = r.end > r.begin ? (uint32_t)(r.end - r.begin + kChunk - 1) / kChunk : 0;
-    r.chunk = (uint32_t)r.begin / kChunk + request;
+    const uint32_t count = r.end > r.begin ? r.end - r.begin : 0;
+    r.first = (uint32_t)r.begin / kChunk;
+    r.whole = count / kChunk;
+    r.last = (uint32_t)most / kChunk + request;
+    r.chunks = (count + kChunk - 1) / kChunk;
     return r;
 }
 
@@ -312,17 +317,21 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
     const uint32_t tid = threadIdx.x, lane = tid % 32, warp = tid / 32, k_dim = (uint32_t)a.k_dim;
     const uint32_t chunk = blockIdx.x / (uint32_t)a.k_heads, key_head = blockIdx.x % (uint32_t)a.k_heads;
     // the request that this chunk belongs to
+    const uint32_t whole = (uint32_t)a.tokens / kChunk;
     if (tid == 0) found = ~0u;
     __syncthreads();
-    for (uint32_t r = tid; r < (uint32_t)a.requests; r += kPrepareThreads) {
-        const Range c = range_of(a, r);
-        if (chunk - c.chunk < c.chunks) found = r;
-    }
+    if (chunk < whole)
+        for (uint32_t r = tid; r < (uint32_t)a.requests; r += kPrepareThreads) {
+            const Range c = range_of(a, r);
+            if (chunk - c.first < c.whole) found = r;
+        }
     __syncthreads();
-    const uint32_t request = found;
+    const uint32_t request = chunk < whole ? found : chunk - whole;
     if (request == ~0u) return;
     const Range range = range_of(a, request);
-    const int32_t first = range.begin + (int32_t)(chunk - range.chunk) * kChunk, count = min(range.end - first, kChunk);
+    const uint32_t place = chunk < whole ? chunk - range.first : range.whole;        // among the request's
+    if (place >= range.chunks) return;
+    const int32_t first = range.begin + (int32_t)place * kChunk, count = min(range.end - first, kChunk);
     // rows of K, then of Q: their norms, and their elements times a power of two
     const uint32_t stride = p.wide * 2 + 16, term_bytes = 2 * kChunk * stride;
     uint8_t *rows = p.rows + (uint64_t)blockIdx.x * p.rows_bytes;
@@ -366,7 +375,7 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
                 else if (a.dtype == NINFER_BF16) x[e] = __uint_as_float(e % 2 ? word & 0xffff0000u : word << 16);
                 else x[e] = __half2float(__ushort_as_half((unsigned short)(e % 2 ? word >> 16 : word & 0xffffu)));
                 sum = fmaf(x[e], x[e], sum);
-                most = most_of(most, x[e]);
+                if (e % 2) most = most_of(most, x[e - 1], x[e]);
             }
             if (row_lanes == 32) {
                 sum += __shfl_xor_sync(~0u, sum, 16);
@@ -664,11 +673,9 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
     // the last ones there are; what they get is part of no result.
     constexpr uint32_t kUnits = values_of(kColumns) * es / 16;
     constexpr int32_t kRowsAtOnce = 32 / kUnits;
-    const uint8_t *next_rows = p.rows + ((uint64_t)range.chunk * a.k_heads + part.key_head) * p.rows_bytes;
-    const uint8_t *next_head = p.heads + ((uint64_t)range.chunk * a.v_heads + part.head) * kHeadBytes;
     const uint8_t *next_v = static_cast<const uint8_t *>(a.v) +
                             ((uint64_t)(range.begin + lane / kUnits) * a.v_token_stride + part.head * a.v_head_stride + part.column) * es + min(lane % kUnits, columns * es / 16 - 1) * 16;
-    const uint64_t rows_step = a.k_heads * p.rows_bytes, head_step = a.v_heads * kHeadBytes, v_step = kRowsAtOnce * a.v_token_stride * es;
+    const uint64_t v_step = kRowsAtOnce * a.v_token_stride * es;
     auto send = [&](uint32_t j) {
         if (j >= kStages) good = !__any_sync(~0u, !(good && mbar_wait(smem_u32(&empty[j % kStages]), (j / kStages - 1) & 1, p.error, p.wait_limit)));
         if (!good) return;
@@ -676,11 +683,10 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
         const int32_t left = range.end - range.begin - (int32_t)j * kChunk - (int32_t)(lane / kUnits);      // tokens from this lane's first on
         if (lane == 0) {
             mbar_arrive_expect_tx(bar, kTri + kHeadBytes);
-            bulk_g2s(stage, next_rows, kTri, bar);
-            bulk_g2s(stage + kTri, next_head, kHeadBytes, bar);
+            const uint32_t chunk = j < range.whole ? range.first + j : range.last;
+            bulk_g2s(stage, p.rows + (uint64_t)(chunk * (uint32_t)a.k_heads + part.key_head) * p.rows_bytes, kTri, bar);
+            bulk_g2s(stage + kTri, p.heads + ((uint64_t)chunk * a.v_heads + part.head) * kHeadBytes, kHeadBytes, bar);
         }
-        next_rows += rows_step;
-        next_head += head_step;
         // the values, 16 bytes at a time (a bulk copy a row took 80 cycles to issue, each)
         const uint32_t to = stage + kV + lane / kUnits * v_stride + lane % kUnits * 16;
         const uint8_t *from = next_v;
@@ -879,8 +885,8 @@ __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 3
                 const float oe[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[n][e] -= (e % 2 ? f.y : f.x) * (x[n][e] + oe[e]);
-                m0 = most_of(most_of(m0, w[n][0]), w[n][1]);
-                m1 = most_of(most_of(m1, w[n][2]), w[n][3]);
+                m0 = most_of(m0, w[n][0], w[n][1]);
+                m1 = most_of(m1, w[n][2], w[n][3]);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {

@@ -119,7 +119,7 @@ int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream stream);
  *     `slots` does so and sets NINFER_DELTA_BAD_SLOT. Slots of one call differ from each other (the results of requests that
  *     share one are undefined).
  *   offsets: device int32[requests + 1], tokens offsets[i] .. offsets[i + 1] - 1 belong to request i (cut to
- *     [0, tokens]); NULL: one token each, token i of request i (tokens = requests).
+ *     [0, tokens]) and to no other (the results of requests that share some are undefined); NULL: one token each, token i of request i (tokens = requests).
  *   lengths: device int32[requests], tokens that the request's state has seen; one that has seen none (0 and less) begins
  *     with zeros, whatever its slot holds. NULL: every state is read.
  *   out: device [tokens][v_heads][v_dim] of out_dtype; rows of no request are left as they were, and so are the states of

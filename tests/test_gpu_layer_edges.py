@@ -163,6 +163,15 @@ def test_gated_delta_a_request_alone_and_among_others(k_heads, v_heads, dk, dv, 
             assert torch.equal(got, torch.cat([out[offsets[r]:offsets[r + 1]] for r in some])) and torch.equal(s, state[some])
 
 
+@pytest.mark.parametrize("dk,dtype", [(64, "bf16"), (128, "f32"), (256, "f16")])
+def test_gated_delta_requests_in_any_order_of_their_tokens(dk, dtype):
+    """Offsets that fall begin again further ahead; requests without tokens lie between."""
+    rng = np.random.default_rng(dk)
+    for offsets in ([64, 100, 0, 64], [128, 256, 0, 128], [200, 231, 100, 200, 33, 100, 0, 33], [161, 162, 96, 161, 0, 32, 32, 64, 64, 96], [70, 5000, -3, 70]):
+        case = delta_case(rng, max(min(max(offsets), 300), 1), len(offsets) - 1, 1, 2, dk, 24, dtype)
+        run_delta(case, offsets=offsets)
+
+
 # ------------------------------------------------------------------- norm ---
 @pytest.mark.parametrize("group", [128, 24, 512, 5, 33000])
 def test_norm_gates_of_any_size(group):
