@@ -678,9 +678,10 @@ __global__ void __launch_bounds__(kThreads, kResident) sample_kernel(const __gri
     row.infinite = top == INFINITY;
     row.m = row.infinite ? 0.f : top;
     if (row.infinite) most = most == INFINITY ? 0.f : -INFINITY;
-    // log2(e) / temperature
-    row.c_hi = fminf(__fdiv_rn(1.44269504f, temperature), 1e36f);
-    row.c_lo = __fdiv_rn(fmaf(-row.c_hi, temperature, 1.44269504f) + 1.92596299e-8f, temperature);
+    // log2(e) / temperature, of which 64 times (bins) are a float too
+    const float warm = fmaxf(temperature, 0x1p-119f);
+    row.c_hi = __fdiv_rn(1.44269504f, warm);
+    row.c_lo = __fdiv_rn(fmaf(-row.c_hi, warm, 1.44269504f) + 1.92596299e-8f, warm);
     if (!isfinite(row.c_lo)) row.c_lo = 0.f;
     if (min_p > 0.f) row.least = times(fminf(min_p, 1.f), 1ull << p.scale, true);
     const bool by_k = top_k > 0 && (uint32_t)top_k < vocab, by_p = top_p < 1.f, by_m = min_p > 0.f;

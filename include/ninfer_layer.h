@@ -164,14 +164,14 @@ int ninfer_gated_delta(const ninfer_gated_delta_args *args, void *workspace, uin
  *   C = those of B with w_v >= min_p (NaN: all; at most 1 counts);
  *   token = the first v of C, in rising order of v, for which the w of C up to and with v add up to more than random * (C's sum);
  *   logprob = ln(w_token / C's sum).
- * temperature <= 0 (or NaN): the largest logit, the lowest of equal ones, logprob 0. A row without a logit above
+ * temperature <= 0 (or NaN): the largest logit, the lowest of equal ones, logprob 0; one below 2^-119 counts as that. A row without a logit above
  * -infinity: token -1, logprob -infinity. If m is +infinity, w is 1 where x is and 0 elsewhere.
  *   logits: device, dtype f32, bf16 or f16, row b at b * stride.
  *   temperature, top_p, min_p: device float[rows], NULL: 1, 1, 0; top_k: device int32[rows], NULL: 0.
  *   random: device float[rows], in [0, 1) (cut to it).
  *   tokens: device int32[rows]; logprobs: device float[rows] or NULL. Each may be one of the controls' arrays; else they overlap nothing.
  * Weights are whole multiples of 2^(vocab's bits - 62) of the largest one, each off by less than 2^-29 and the rounding of x - m (2^-24 of
- * the exponent) of itself; their sums are exact and do not depend on an order: equal rows give equal tokens, however they are divided.
+ * the exponent; 0 where x - m overflows) of itself; their sums are exact and do not depend on an order: equal rows give equal tokens, however they are divided.
  * Errors: INVALID_ARGUMENT, SHAPE (rows or vocab 0, vocab over 2^30, stride below vocab), ALIGNMENT, OVERFLOW, CUDA.
  */
 typedef struct {

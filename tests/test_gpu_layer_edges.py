@@ -6,7 +6,7 @@ import torch
 
 import bit_gemv_gb300 as nt
 from oracle import layer as ol
-from test_gpu_layer import DEV, HALF, TORCH, delta_case, f32, f64, i32, near, randn, run_delta
+from test_gpu_layer import DEV, HALF, TORCH, check_sample, delta_case, f32, f64, i32, near, randn, run_delta
 
 pytestmark = pytest.mark.gpu
 
@@ -31,6 +31,19 @@ def test_sample_ctas_of_a_row_that_begin_late(rows, vocab, dtype):
             first = tokens
             assert torch.equal(x.float()[::3].gather(1, tokens[::3, None].long())[:, 0], largest)
         assert torch.equal(tokens, first)
+
+
+def test_sample_least_temperatures():
+    """Logits as small as their temperature, down to the least numbers: 2^-119 and all temperatures below it give the same, by the definition."""
+    rng = np.random.default_rng(41)
+    x = randn(rng, (6, 3000), "f32", 2.0 ** -118)
+    random = rng.random(6).tolist()
+    for controls in ({}, dict(top_p=[0.8] * 6), dict(top_k=[9] * 6), dict(min_p=[0.05] * 6)):
+        tokens = check_sample(x, random, temperature=[2.0 ** -119] * 6, **controls)
+        for t in (1e-36, 2e-38, 1e-45):
+            args = {n: (i32 if n == "top_k" else f32)(c) for n, c in controls.items()}
+            assert nt.ninfer_sample(x, f32(random), temperature=f32([t] * 6), **args).tolist() == tokens
+    assert len(set(tokens)) > 1
 
 
 # ------------------------------------------------------------ gated delta ---
