@@ -185,6 +185,19 @@ def test_gated_delta_requests_in_any_order_of_their_tokens(dk, dtype):
         run_delta(case, offsets=offsets)
 
 
+@pytest.mark.parametrize("dk,dtype,v_heads", [(128, "bf16", 4), (96, "f32", 4), (256, "f16", 160), (128, "f32", 160)])
+def test_gated_delta_prompts_cut_at_chunks(dk, dtype, v_heads):
+    """A prompt in several calls, cut at multiples of 32 tokens, gives the bits of one call, whose workspace grows with it."""
+    rng = np.random.default_rng(dk)
+    case = delta_case(rng, 203, 1, 2, v_heads, dk, 40, dtype, 1)
+    state, parts = case["state"].clone(), []
+    for a, b in ((0, 32), (32, 128), (128, 203)):
+        part = {n: case[n][a:b] for n in ("q", "k", "v", "log_decay", "beta")}
+        parts.append(nt.ninfer_gated_delta(**part, state=state, offsets=i32([0, b - a]), lengths=i32([a]), norm_eps=1e-6))
+    whole = nt.ninfer_gated_delta(**case, offsets=i32([0, 203]), lengths=i32([0]), norm_eps=1e-6)
+    assert torch.equal(torch.cat(parts), whole) and torch.equal(state, case["state"])
+
+
 # ------------------------------------------------------------------- norm ---
 @pytest.mark.parametrize("group", [128, 24, 512, 5, 33000])
 def test_norm_gates_of_any_size(group):
