@@ -11,7 +11,7 @@
 // request's first token to its last. The chain of dependent products bounds it (the tensor cores are busy for a third of it).
 //
 // Measured: 64 requests of one token, 48 states of 128 x 128 each, 405 MB, 69 us (5.9 TB/s; with 128 columns a CTA, one CTA an SM, 104).
-// A prompt of 8001 tokens with 48 heads: 89 us of preparation and 515 of chunks, 2.05 us each; token by token in fp32, four
+// A prompt of 8001 tokens with 48 heads: 93 us of preparation and 522 of chunks, 2.07 us each, 620 in all; token by token in fp32, four
 // lanes a column, 7390.
 #include <cmath>
 
@@ -521,11 +521,11 @@ __global__ void __launch_bounds__(kPrepareThreads, 6) prepare_kernel(const __gri
 }
 
 // Columns of a state a CTA: where that makes no more CTAs than SMs 16, 32 or up to 48 (8001 tokens with 16 heads of 128 columns by 16, 32 and
-// 48: 412, 468 and 576 us; 48 heads by 48 and by 32 columns, two CTAs an SM: 603 and 701), else 32, two CTAs an SM of which one begins or ends
-// while the other computes (64 prompts of 33 tokens with 48 heads 320 us, of 128 tokens 558; with 64 columns 349 and 582), or 64 where
+// 48: 420, 475 and 592 us; 48 heads by 48 and by 32 columns, two CTAs an SM: 620 and 716), else 32, two CTAs an SM of which one begins or ends
+// while the other computes (64 prompts of 33 tokens with 48 heads 322 us, of 128 tokens 567; with 48 columns 440 and 721), or 64 where
 // shared memory has no room for two.
 // With up to 48 (3 pairs of warps) the two warps without columns take from the pairs' chain what is not of it: the results (P U and Q S), made
-// by one of them (the other copies) or, with a ninth warp that copies, by both; 8001 tokens with 48 heads 603 us, by the pairs themselves 681.
+// by one of them (the other copies) or, with a ninth warp that copies, by both; for 8001 tokens with 48 heads 78 us less than by the pairs themselves.
 // What a pair hands over: U and Q S of 16 columns by 32 tokens, two buffers.
 constexpr uint32_t kResultWarp = 6, kHandedBytes = 8 * 32 * 16;
 // The ninth warp is there where it leaves the others registers enough: 168 a thread instead of 255.
@@ -627,7 +627,7 @@ __device__ __forceinline__ void put_results(const Results &r, int dtype, uint8_t
 // outputs by tokens where no other warp makes them. One warp keeps the next chunks coming (bulk copies, mbarriers); nothing else holds pairs together, so
 // that of two pairs on a scheduler one multiplies while the other splits and scales.
 // kSteps: steps of 16 of k_dim of a warp; kTerms: terms of k and q. The CTAs an SM are said to ptxas, which otherwise
-// takes fewer registers and loads later (173 for 207: 662 us for 603).
+// takes fewer registers and loads later (173 for 207, 59 us more for the same prompt).
 template <int kSteps, int kTerms, int kColumns>
 __global__ void __launch_bounds__(chunk_threads(kSteps, kColumns), kColumns == 32 ? 2 : 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
     constexpr uint32_t kRowStride = kSteps * 64 + 16, kTermBytes = 2 * kChunk * kRowStride;

@@ -8,8 +8,9 @@
 // token, asks for its first heads, puts the sines and cosines into shared memory and then turns its heads,
 // a few lanes each, 8 elements a lane, with as many threads as take them in the fewest rounds.
 //
-// Measured: 30011 tokens of 40 heads of 128 in bfloat16, 615 MB, 102 us (6.0 TB/s). Heads asked for only after the sines and
-// cosines: 140; 256 threads for every token: 125; 64 registers a thread instead of 48: 109.
+// Measured: 30011 tokens of 40 heads of 128 in bfloat16, neighbouring pairs, 615 MB, 102 us (6.0 TB/s). Heads asked for only after the sines and
+// cosines: 140; 256 threads for every token: 125; 64 registers a thread instead of 48: 109. Halves, whose partners are eight shuffles of a lane
+// away, 168 us, with norms (a weight, a root and a quotient a head) 209; 28 heads of 256 with 64 elements turned, halves, 861 MB, 161 and with norms 214.
 #include <cmath>
 
 #include "decode.cuh"

@@ -21,9 +21,9 @@
 // to the exact sum of what lies above. Where more than 2048 tokens lie there (equal logits without end), the border comes from the
 // key's bits, eight at a time.
 //
-// What bounds it: HBM for nothing but greedy rows (64 of 248320 fp32 logits, 64 MB, 21 us); about 40 instructions for each exact weight
-// (temperature alone: 80 us; large nuclei, which need them twice: 140), and the chain of a cluster's exchanges (top-k 57, min-p 39; one row 9 to
-// 13 us, 40 with a nucleus of most of the row).
+// What bounds it: not HBM (greedy rows, 64 of 248320 fp32 logits, 64 MB, 26 us, held like others); about 40 instructions for each exact weight (normal
+// logits of deviation 2.5, temperature alone: 87 us; large nuclei, which need them twice: 240 to 300), and the chain of a cluster's exchanges (top-k 62,
+// min-p 52; one row 11 to 13 us, 49 with a nucleus of most of the row).
 #include <cfloat>
 #include <cmath>
 #include <cstddef>

@@ -4,7 +4,7 @@ a batch of requests: whole prompts first, then a token of each request at a time
   python examples/serve_step.py [--steps N] [--requests R] [--page P]
 
 Weights are random, so the answers mean nothing; the calls are those of a real
-serving loop, all of them the library's:
+serving loop. The library's (what is left to torch: decays, betas and random numbers, and the gathers of rows):
 
   ninfer_kv_tables       where this step's tokens go, their positions and offsets
   ninfer_ternary_embed   token ids -> rows
