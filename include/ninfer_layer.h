@@ -133,7 +133,7 @@ int ninfer_rotary(const ninfer_rotary_args *args, ninfer_stream stream);
  * States and sums are fp32. With offsets, a request's tokens go 32 at a time through the tensor cores: operands hold 22 bits of each
  * value (q and k of 16-bit types all of theirs). Each token's q and k has a scale of its own, for each column of a state the state, the values
  * and what the tokens add to it have one: nothing counts that is under 2^-38 of the largest state, value or addition of its column among those 32
- * tokens, before it or behind it. (Without offsets there is no such limit.) Infinities and NaN reach what the formulas give them and no earlier
+ * tokens, before it or behind it. (Without offsets there is no such limit.) Infinities and NaN make NaN of what the formulas give them to, and reach no earlier
  * token, other column, head or request, as long as finite operands' products are within fp32's range. No bit of a request's results
  * depends on the others of the call. (Without offsets the order of sums goes by the number of states.)
  * If a kernel's bounded wait runs out (ninfer_set_wait_limit), the device error word is set and the results are incomplete.

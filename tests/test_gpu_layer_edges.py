@@ -198,6 +198,30 @@ def test_gated_delta_prompts_cut_at_chunks(dk, dtype, v_heads):
     assert torch.equal(torch.cat(parts), whole) and torch.equal(state, case["state"])
 
 
+@pytest.mark.parametrize("dk,dv,dtype,requests", [(128, 128, "bf16", 6), (64, 40, "f32", 6), (256, 72, "f16", 60), (96, 64, "bf16", 200)])
+def test_gated_delta_single_tokens_of_non_finite_values(dk, dv, dtype, requests):
+    """Infinities and NaN of a request's token stay with its heads and columns."""
+    rng = np.random.default_rng(dk)
+    clean = delta_case(rng, requests, requests, 2, 4, dk, dv, dtype, requests)
+    for n in ("q", "k", "v", "log_decay", "beta", "state"):
+        for value in (float("nan"), float("inf"), -float("inf")):
+            case = {m: t.clone() for m, t in clean.items()}
+            r, h = int(rng.integers(0, requests)), int(rng.integers(0, case[n].shape[1]))
+            if n == "state":
+                case[n][r, h, dk - 1, dv // 2] = value
+            elif n in ("q", "k", "v"):
+                case[n][r, h, 3] = value
+            else:
+                case[n][r, h] = value
+            with np.errstate(all="ignore"):
+                want, state, out_bound, bound = ol.gated_delta(*(f64(case[m]) for m in ("q", "k", "v", "log_decay", "beta", "state")), range(requests + 1),
+                                                               range(requests), None, dk ** -0.5, 1e-6, 2.0 ** -23)
+            out = nt.ninfer_gated_delta(**case, norm_eps=1e-6, out_dtype=torch.float32)
+            for got, want, bound in ((f64(out), want, out_bound), (f64(case["state"]), state, bound)):
+                live = np.isfinite(want)
+                assert np.array_equal(np.isfinite(got), live) and (np.abs(got - want)[live] <= bound[live] + HALF["f32"] * np.abs(want[live]) + 1e-40).all()
+
+
 # ------------------------------------------------------------------- norm ---
 @pytest.mark.parametrize("group", [128, 24, 512, 5, 33000])
 def test_norm_gates_of_any_size(group):
